@@ -23,7 +23,8 @@
  *    one layer.  Call once per layer for a multi-layer cache.
  *  - Element type: PA_F32 or PA_BF16; K, V, Q and the output share it,
  *    except for the e4m3 pool calls (pa_reshape_and_cache_fp8,
- *    pa_decode_fp8), whose pools hold PA_FP8_E4M3 codes with fp32 scales.
+ *    pa_decode_fp8 and the block-scaled cache's), whose pools hold
+ *    PA_FP8_E4M3 codes with fp32 scales.
  *    Accumulation is fp32 whatever the storage type (the tensor-core forms
  *    round their product operands as each call's description states); bf16
  *    results are rounded to nearest even.
@@ -61,8 +62,9 @@ extern "C" {
 
 /* PA_FP8_E4M3 is a storage type for K/V pools only: 8-bit e4m3 codes (4
  * exponent bits with bias 7, 3 mantissa bits, largest finite value 448)
- * with one fp32 scale per token for its K vector and one for its V vector.
- * See pa_reshape_and_cache_fp8 and pa_decode_fp8. */
+ * with one fp32 scale per token for its K vector and one for its V vector
+ * (pa_reshape_and_cache_fp8, pa_decode_fp8), or one per (block, KV head)
+ * (pa_append_fp8_blocks and the calls after it). */
 typedef enum { PA_F32 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2 } pa_dtype;
 
 /* host-detected errors (negative return values) */
@@ -292,6 +294,194 @@ int pa_decode_fp8(void* out, const void* query,
                   int block_size, int num_blocks, float scale, int partition_size,
                   void* workspace, size_t workspace_bytes,
                   pa_dtype dtype, void* stream);
+
+/*
+ * The block-scaled e4m3 cache: an e4m3 pool with one fp32 scale per (block,
+ * KV head) for K and one for V.
+ *
+ *   k_cache, v_cache  codes [num_blocks, block_size, num_kv_heads, head_dim]
+ *   k_scale, v_scale  [num_blocks, PA_SCALE_ROW(num_kv_heads)] fp32, 16-byte
+ *                     aligned: entry h of a block's row belongs to KV head h
+ *                     (a row is padded to whole 16-byte chunks; the padding
+ *                     is read, never used and never written)
+ *
+ * A dequantised element is e4m3_value(code) * scale.  The calls below write
+ * powers of two; pa_decode_fp8_blocks, pa_decode_weights and
+ * pa_prefill_fp8_blocks read any finite scale >= 0.  Blocks are copied and
+ * swapped with pa_copy_blocks / pa_swap_blocks on the codes and again, with
+ * the same pairs, on (k_scale, v_scale) as fp32 pools of block_size 4,
+ * num_kv_heads = PA_SCALE_ROW(num_kv_heads) / 4 and head_dim 1.
+ */
+#define PA_SCALE_ROW(num_kv_heads) (((num_kv_heads) + 3) / 4 * 4)
+
+/*
+ * Quantising append into a block-scaled e4m3 cache.  Sequence b's new tokens
+ * are rows query_start[b] .. query_start[b+1]-1 of key and value: the last
+ * n_b tokens of its context (context_lens counts them).  For every block they
+ * touch and every head, K and V each on their own:
+ *
+ *   a     = max |x| over the block's new finite elements of the head
+ *   need  = the smallest power of two with a <= 448 * need, at least 2^-100
+ *           (0 when a is 0)
+ *   s     = max(need, the block's scale), the latter only if the block holds
+ *           earlier tokens of the sequence; a block begun by this call starts
+ *           from need
+ *   codes = e4m3(x / s), nearest even, saturating; codes of the earlier tokens
+ *           become e4m3(value(code) * old_scale / s)
+ *
+ * Powers of two make x / s exact and a raised scale exact for every code whose
+ * value stays a normal one, so the tokens' split into calls hardly shows.
+ * A NaN gives a NaN code; an infinity gives +-448 codes, or NaN codes where the
+ * block's head holds nothing that is finite and not zero.
+ *
+ *   key, value     [total_tokens, num_kv_heads, head_dim], src_dtype PA_F32 or
+ *                  PA_BF16
+ *   query_start    [num_seqs + 1] int32, non-decreasing from 0 to total_tokens
+ *                  (a sequence may add none)
+ *
+ * Blocks that receive tokens must belong to one sequence only (copy shared
+ * ones first), named once in its table row.  A sequence whose rows or lengths
+ * are inconsistent (rows outside [0, total_tokens], more rows than tokens, a
+ * context longer than its table row) writes nothing and sets PA_DEV_BAD_LEN;
+ * a block id outside the pool is skipped and sets PA_DEV_BAD_BLOCK.
+ */
+int pa_append_fp8_blocks(const void* key, const void* value,
+                         const int32_t* query_start, int total_tokens,
+                         const int32_t* block_tables, int max_blocks_per_seq,
+                         const int32_t* context_lens, int num_seqs,
+                         void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                         int num_blocks, int block_size, int num_kv_heads, int head_dim,
+                         pa_dtype src_dtype, void* stream);
+
+/*
+ * Paged decode attention over a block-scaled e4m3 cache: the result of
+ * pa_decode over the dequantised pool.  The K scale multiplies the scores of a
+ * block's tokens, the V scale their softmax weights (the normaliser uses the
+ * unscaled weights), both in fp32.
+ *
+ *   query, out      PA_BF16
+ *   partition_size, workspace: as for pa_decode_fp8
+ *   other arguments as for pa_decode
+ */
+int pa_decode_fp8_blocks(void* out, const void* query,
+                         const void* k_cache, const void* v_cache,
+                         const float* k_scale, const float* v_scale,
+                         const int32_t* block_tables, int max_blocks_per_seq,
+                         const int32_t* context_lens, int num_seqs,
+                         int num_heads, int num_kv_heads, int head_dim,
+                         int block_size, int num_blocks, float scale, int partition_size,
+                         void* workspace, size_t workspace_bytes,
+                         pa_dtype dtype, void* stream);
+
+/*
+ * Causal attention of each sequence's newest tokens over a block-scaled e4m3
+ * cache: pa_prefill_varlen's rows and positions, for every head_dim,
+ * block_size and query group that pa_decode takes (num_seqs unlimited).  The
+ * tokens' K/V are already appended.  Rows at negative positions are zeros.
+ *
+ *   out, query     [total_queries, num_heads, head_dim], PA_BF16
+ *   query_start    [num_seqs + 1] int32, non-decreasing from 0 to total_queries
+ *                  (a bad pair sets PA_DEV_BAD_LEN, and that sequence writes
+ *                  nothing)
+ *   scale          > 0
+ */
+int pa_prefill_fp8_blocks(void* out, const void* query, const int32_t* query_start, int total_queries,
+                          const void* k_cache, const void* v_cache,
+                          const float* k_scale, const float* v_scale,
+                          const int32_t* block_tables, int max_blocks_per_seq,
+                          const int32_t* context_lens, int num_seqs,
+                          int num_heads, int num_kv_heads, int head_dim,
+                          int block_size, int num_blocks, float scale,
+                          pa_dtype dtype, void* stream);
+
+/*
+ * Decode that keeps account of what attention looks at.  out is pa_decode's
+ * (or pa_decode_fp8_blocks') result; besides, with w[b,h,t] the softmax weight
+ * of token t for query head h of sequence b,
+ *
+ *   weights[b, g, t] += sum over the query heads h of KV head g of w[b,h,t]
+ *
+ * for t < L_b (the rest of a row is untouched), in fp32 and in head order: the
+ * same call gives the same totals.  A token's total starts from what the
+ * caller put there: 0 for a new token (pa_evict leaves zeros behind).
+ *
+ *   weights         [num_seqs, num_kv_heads] rows of weights_stride floats,
+ *                   weights_stride >= max_blocks_per_seq * block_size
+ *   dtype           of query and out
+ *   kv_dtype        of the pools: dtype itself, or PA_FP8_E4M3 (block-scaled,
+ *                   dtype PA_BF16); k_scale, v_scale are used only then
+ *   workspace       at least pa_decode_weights_workspace_bytes(): the split-K
+ *                   partials and an fp32 score per (query head, table slot)
+ *   other arguments as for pa_decode; num_heads / num_kv_heads <= 1024
+ */
+int pa_decode_weights(void* out, float* weights, long long weights_stride,
+                      const void* query, const void* k_cache, const void* v_cache,
+                      const float* k_scale, const float* v_scale,
+                      const int32_t* block_tables, int max_blocks_per_seq,
+                      const int32_t* context_lens, int num_seqs,
+                      int num_heads, int num_kv_heads, int head_dim,
+                      int block_size, int num_blocks, float scale, int partition_size,
+                      void* workspace, size_t workspace_bytes,
+                      pa_dtype dtype, pa_dtype kv_dtype, void* stream);
+
+/* Bytes of workspace pa_decode_weights needs for these sizes.  Pure host
+ * arithmetic; no CUDA call. */
+size_t pa_decode_weights_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                         int max_blocks_per_seq, int block_size, int partition_size,
+                                         pa_dtype kv_dtype);
+
+/*
+ * Evict: cut the cache of every (sequence, KV head) to `budget` tokens.  Each
+ * KV head keeps tokens of its own choice; all heads of a sequence keep the
+ * same number, so its new length is min(L_b, budget).
+ *
+ * Slot t < L_b of (b, g) holds the token at position
+ *   pos(t) = token_pos[b,g,t]        for t < kept_lens[b]
+ *            seen_lens[b] - L_b + t  for the tokens appended since.
+ * Protected are pos < sinks and pos >= seen_lens[b] - recent.  Where
+ * L_b > budget, the `budget` tokens stay that come first by: protected, then
+ * larger weights[b,g,t] (NaN last), then lower t.  Kept tokens in slots below
+ * the budget keep their slot; the i-th kept token (by slot) at or above the
+ * budget moves into the i-th slot below it whose token was dropped.  K/V rows,
+ * weights and positions move together; attention over the cache does not
+ * depend on the order of its rows.  Rows of a PA_FP8_E4M3 (block-scaled) pool
+ * are requantised: a block that receives rows takes the largest of its scale
+ * and theirs, and its own remaining rows follow it.
+ *
+ *   kept_lens    [num_seqs] int32: tokens whose token_pos entry is valid, i.e.
+ *                new_lens of the sequence's last eviction (0 before the first)
+ *   seen_lens    [num_seqs] int32: tokens the sequence has had in all, the
+ *                dropped ones included (L_b before its first eviction)
+ *   weights, token_pos  [num_seqs, num_kv_heads] rows of row_stride floats /
+ *                int32, row_stride >= max_blocks_per_seq * block_size
+ *   budget, recent, sinks   >= 1, >= 0, >= 0; recent + sinks <= budget
+ *   new_lens     [num_seqs] int32 (written); may be context_lens or kept_lens
+ *   weights_out, token_pos_out  rows like weights and token_pos (written: the
+ *                kept tokens' entries, then 0 and -1 up to max_blocks_per_seq *
+ *                block_size); may be weights and token_pos themselves, with no
+ *                other overlap
+ *   workspace    at least pa_evict_workspace_bytes(), 16-byte aligned; calls
+ *                that share one must be ordered
+ *
+ * The blocks of a sequence must be its own (copy shared ones first).  Blocks
+ * wholly past the new length are the caller's to free.  A context length
+ * outside its table row, or a kept length outside the context, is clamped and
+ * sets PA_DEV_BAD_LEN; a move from or to a block id outside the pool is skipped
+ * and sets PA_DEV_BAD_BLOCK.  A pool with per-token scales
+ * (pa_reshape_and_cache_fp8) cannot be evicted by head: one scale there serves
+ * all heads of a token.
+ */
+int pa_evict(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+             const int32_t* block_tables, int max_blocks_per_seq,
+             const int32_t* context_lens, const int32_t* kept_lens, const int32_t* seen_lens, int num_seqs,
+             const float* weights, const int32_t* token_pos,
+             int budget, int recent, int sinks,
+             int32_t* new_lens, float* weights_out, int32_t* token_pos_out, long long row_stride,
+             int num_blocks, int block_size, int num_kv_heads, int head_dim,
+             void* workspace, size_t workspace_bytes, pa_dtype kv_dtype, void* stream);
+
+/* Bytes of workspace pa_evict needs for these sizes.  Pure host arithmetic. */
+size_t pa_evict_workspace_bytes(int num_seqs, int num_kv_heads, int max_blocks_per_seq, int block_size, int budget);
 
 /*
  * Swap blocks between two pools (preemption by swapping).  [KVS] §19.2.6:

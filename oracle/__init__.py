@@ -54,4 +54,11 @@ from .quant import (  # noqa: F401
     reshape_and_cache_fp8,
     paged_decode_fp8,
 )
+from .bounded import (  # noqa: F401
+    pow2_scale,
+    dequantize_blocks,
+    append_fp8_blocks,
+    attention_weights,
+    evict,
+)
 from .block_manager import BlockPool, BlockTable, BlockExhausted  # noqa: F401

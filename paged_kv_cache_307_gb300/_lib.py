@@ -57,6 +57,23 @@ lib.pa_prefill_varlen.argtypes = [_p, _p, _i32p, _i, _p, _p, _i32p, _i, _i32p, _
 lib.pa_prefill_varlen.restype = _i
 lib.pa_swap_blocks.argtypes = [_p, _p, _i, _p, _p, _i, _i64p, _i, _i, _i, _i, _i, _p]
 lib.pa_swap_blocks.restype = _i
+lib.pa_append_fp8_blocks.argtypes = [_p, _p, _i32p, _i, _i32p, _i, _i32p, _i, _p, _p, _p, _p, _i, _i, _i, _i, _i, _p]
+lib.pa_append_fp8_blocks.restype = _i
+lib.pa_decode_fp8_blocks.argtypes = lib.pa_decode_fp8.argtypes
+lib.pa_decode_fp8_blocks.restype = _i
+lib.pa_prefill_fp8_blocks.argtypes = [_p, _p, _i32p, _i, _p, _p, _p, _p, _i32p, _i, _i32p, _i, _i, _i, _i, _i, _i, _f,
+                                      _i, _p]
+lib.pa_prefill_fp8_blocks.restype = _i
+lib.pa_decode_weights.argtypes = [_p, _p, ctypes.c_longlong, _p, _p, _p, _p, _p, _i32p, _i, _i32p, _i, _i, _i, _i, _i,
+                                  _i, _f, _i, _p, _sz, _i, _i, _p]
+lib.pa_decode_weights.restype = _i
+lib.pa_decode_weights_workspace_bytes.argtypes = [_i, _i, _i, _i, _i, _i, _i, _i]
+lib.pa_decode_weights_workspace_bytes.restype = _sz
+lib.pa_evict.argtypes = [_p, _p, _p, _p, _i32p, _i, _i32p, _i32p, _i32p, _i, _p, _i32p, _i, _i, _i, _i32p, _p, _i32p,
+                         ctypes.c_longlong, _i, _i, _i, _i, _p, _sz, _i, _p]
+lib.pa_evict.restype = _i
+lib.pa_evict_workspace_bytes.argtypes = [_i, _i, _i, _i, _i]
+lib.pa_evict_workspace_bytes.restype = _sz
 lib.pa_last_error.argtypes = []
 lib.pa_last_error.restype = _i
 lib.pa_strerror.argtypes = [_i]
@@ -275,6 +292,217 @@ def swap_blocks(dst_k, dst_v, src_k, src_v, pairs, stream=None):
     _check(lib.pa_swap_blocks(_ptr(dst_k), _ptr(dst_v), dst_k.shape[0], _ptr(src_k), _ptr(src_v), src_k.shape[0],
                               _ptr(pairs), pairs.shape[0], bs, H, D, _dtype(dst_k), _stream(stream)),
            "pa_swap_blocks")
+
+
+def scale_row(num_kv_heads):
+    """Floats in one block's row of a block-scaled e4m3 cache's scales."""
+    return (num_kv_heads + 3) // 4 * 4
+
+
+def _same_device(*ts):
+    """Every tensor on one device, the current one (the one the library launches on)."""
+    for t in ts:
+        if t is not None and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
+            raise ValueError("tensors must be on the current CUDA device")
+
+
+def _int32(*ts):
+    for t in ts:
+        if t.dtype != torch.int32:
+            raise TypeError("lengths, tables and starts are int32")
+
+
+def _table(block_tables, context_lens):
+    _int32(block_tables, context_lens)
+    if block_tables.dim() != 2 or context_lens.shape != block_tables.shape[:1]:
+        raise ValueError("block_tables is [num_seqs, max_blocks], context_lens [num_seqs]")
+
+
+def _pools(k_cache, v_cache):
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache are [num_blocks, block_size, num_kv_heads, head_dim] of one type")
+
+
+def _block_scales(k_cache, v_cache, k_scale, v_scale):
+    _pools(k_cache, v_cache)
+    if k_cache.dtype != torch.uint8:
+        raise TypeError("a block-scaled cache holds e4m3 codes in uint8 pools")
+    if k_scale is None or v_scale is None:
+        raise ValueError("a block-scaled cache needs k_scale and v_scale")
+    want = (k_cache.shape[0], scale_row(k_cache.shape[2]))
+    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+        raise TypeError("scales are float32")
+    if tuple(k_scale.shape) != want or tuple(v_scale.shape) != want:
+        raise ValueError("scales are [num_blocks, num_kv_heads rounded up to a multiple of 4]")
+
+
+def append_fp8_blocks(key, value, query_start, block_tables, context_lens, k_cache, v_cache, k_scale, v_scale,
+                      stream=None):
+    """Quantise key/value [T, Hkv, D] (bf16 or fp32), the last tokens of each
+    context (sequence b's rows are query_start[b]..query_start[b+1]-1), into an
+    e4m3 pool with one power-of-two scale per (block, KV head)."""
+    _contig(key, value, query_start, block_tables, context_lens, k_cache, v_cache, k_scale, v_scale)
+    _block_scales(k_cache, v_cache, k_scale, v_scale)
+    _table(block_tables, context_lens)
+    _int32(query_start)
+    NB, bs, H, D = k_cache.shape
+    B = context_lens.shape[0]
+    if tuple(query_start.shape) != (B + 1,):
+        raise ValueError("query_start is [num_seqs + 1]")
+    if key.shape != value.shape or key.dtype != value.dtype or tuple(key.shape[1:]) != (H, D):
+        raise ValueError("key and value are [tokens, num_kv_heads, head_dim] of one type")
+    _same_device(key, value, query_start, block_tables, context_lens, k_cache, v_cache, k_scale, v_scale)
+    _check(lib.pa_append_fp8_blocks(_ptr(key), _ptr(value), _ptr(query_start), key.shape[0], _ptr(block_tables),
+                                    block_tables.shape[1], _ptr(context_lens), B, _ptr(k_cache), _ptr(v_cache),
+                                    _ptr(k_scale), _ptr(v_scale), NB, bs, H, D, _dtype(key), _stream(stream)),
+           "pa_append_fp8_blocks")
+
+
+def copy_blocks_fp8_blocks(k_cache, v_cache, k_scale, v_scale, pairs, stream=None):
+    """Copy-on-write for a block-scaled e4m3 cache: the codes, then the scale rows."""
+    _block_scales(k_cache, v_cache, k_scale, v_scale)
+    copy_blocks(k_cache, v_cache, pairs, stream)
+    NB, n = k_scale.shape
+    copy_blocks(k_scale.view(NB, 4, n // 4, 1), v_scale.view(NB, 4, n // 4, 1), pairs, stream)
+
+
+def _query(q, out, k_cache):
+    if out.shape != q.shape or out.dtype != q.dtype or q.dim() != 3 or q.shape[2] != k_cache.shape[3]:
+        raise ValueError("q and out are [rows, num_heads, head_dim] of one type")
+
+
+def alloc_fp8_blocks_workspace(q, k_cache, block_tables, partition_size=0):
+    """Workspace for decode_fp8_blocks with these sizes."""
+    return alloc_workspace(q, k_cache, block_tables, partition_size)
+
+
+def decode_fp8_blocks(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
+                      partition_size=0, workspace=None, stream=None):
+    """out[B,Hq,D] (bf16) = paged decode attention of q over a block-scaled e4m3 cache."""
+    _contig(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
+    _block_scales(k_cache, v_cache, k_scale, v_scale)
+    _table(block_tables, context_lens)
+    _query(q, out, k_cache)
+    B, Hq, D = q.shape
+    if B != context_lens.shape[0]:
+        raise ValueError("one query row per sequence")
+    NB, bs, Hkv, _ = k_cache.shape
+    if workspace is None:
+        workspace = alloc_fp8_blocks_workspace(q, k_cache, block_tables, partition_size)
+    _same_device(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, workspace)
+    _check(lib.pa_decode_fp8_blocks(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                    _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), B, Hq, Hkv, D, bs,
+                                    NB, ctypes.c_float(scale), partition_size, _ptr(workspace), workspace.numel(),
+                                    _dtype(q), _stream(stream)), "pa_decode_fp8_blocks")
+    return out
+
+
+def prefill_fp8_blocks(out, q, query_start, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
+                       stream=None):
+    """Mixed round over a block-scaled e4m3 cache: q/out [rows, Hq, D] (bf16), sequence b's rows are
+    query_start[b]..query_start[b+1]-1, the last tokens of its context, causal."""
+    _contig(out, q, query_start, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
+    _block_scales(k_cache, v_cache, k_scale, v_scale)
+    _table(block_tables, context_lens)
+    _int32(query_start)
+    _query(q, out, k_cache)
+    rows, Hq, D = q.shape
+    NB, bs, Hkv, _ = k_cache.shape
+    B = context_lens.shape[0]
+    if tuple(query_start.shape) != (B + 1,):
+        raise ValueError("query_start is [num_seqs + 1]")
+    _same_device(out, q, query_start, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
+    _check(lib.pa_prefill_fp8_blocks(_ptr(out), _ptr(q), _ptr(query_start), rows, _ptr(k_cache), _ptr(v_cache),
+                                     _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1],
+                                     _ptr(context_lens), B, Hq, Hkv, D, bs, NB, ctypes.c_float(scale), _dtype(q),
+                                     _stream(stream)), "pa_prefill_fp8_blocks")
+    return out
+
+
+def alloc_weights_workspace(q, k_cache, block_tables, partition_size=0):
+    """Workspace for decode_weights with these sizes."""
+    B, Hq, D = q.shape
+    n = lib.pa_decode_weights_workspace_bytes(B, Hq, k_cache.shape[2], D, block_tables.shape[1], k_cache.shape[1],
+                                              partition_size, _dtype(k_cache))
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+
+
+def decode_weights(out, weights, q, k_cache, v_cache, block_tables, context_lens, scale, k_scale=None, v_scale=None,
+                   partition_size=0, workspace=None, stream=None):
+    """out[B,Hq,D] = paged decode attention of q, and weights[b,g,t] (fp32 [B, Hkv, >= max_blocks * bs]) grows by
+    the softmax weights of KV head g's query heads for token t.  The pools are q's type, or a block-scaled e4m3
+    cache with its scales."""
+    _contig(out, weights, q, k_cache, v_cache, block_tables, context_lens)
+    _table(block_tables, context_lens)
+    _query(q, out, k_cache)
+    fp8 = k_cache.dtype == torch.uint8
+    if fp8:
+        _block_scales(k_cache, v_cache, k_scale, v_scale)
+        _contig(k_scale, v_scale)
+    else:
+        _pools(k_cache, v_cache)
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("scales belong to e4m3 pools")
+    B, Hq, D = q.shape
+    NB, bs, Hkv, _ = k_cache.shape
+    if B != context_lens.shape[0]:
+        raise ValueError("one query row per sequence")
+    if weights.dtype != torch.float32 or weights.dim() != 3 or tuple(weights.shape[:2]) != (B, Hkv):
+        raise ValueError("weights is float32 [num_seqs, num_kv_heads, slots]")
+    if workspace is None:
+        workspace = alloc_weights_workspace(q, k_cache, block_tables, partition_size)
+    _same_device(out, weights, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, workspace)
+    _check(lib.pa_decode_weights(_ptr(out), _ptr(weights), weights.shape[2], _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                 _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1],
+                                 _ptr(context_lens), B, Hq, Hkv, D, bs, NB, ctypes.c_float(scale), partition_size,
+                                 _ptr(workspace), workspace.numel(), _dtype(q), _dtype(k_cache), _stream(stream)),
+           "pa_decode_weights")
+    return out
+
+
+def alloc_evict_workspace(k_cache, block_tables, budget):
+    """Workspace for evict with these sizes."""
+    n = lib.pa_evict_workspace_bytes(block_tables.shape[0], k_cache.shape[2], block_tables.shape[1],
+                                     k_cache.shape[1], budget)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=k_cache.device)
+
+
+def evict(k_cache, v_cache, block_tables, context_lens, kept_lens, seen_lens, weights, token_pos, budget, new_lens,
+          weights_out, token_pos_out, recent=0, sinks=0, k_scale=None, v_scale=None, workspace=None, stream=None):
+    """Cut every (sequence, KV head) to its `budget` tokens of largest weight (protected: the first `sinks` and the
+    last `recent` positions).  weights/token_pos [B, Hkv, slots] name each slot's total and position; the outputs
+    may be the inputs themselves.  new_lens[b] = min(L_b, budget)."""
+    _contig(k_cache, v_cache, block_tables, context_lens, kept_lens, seen_lens, weights, token_pos, new_lens,
+            weights_out, token_pos_out)
+    _table(block_tables, context_lens)
+    _int32(kept_lens, seen_lens, token_pos, new_lens, token_pos_out)
+    fp8 = k_cache.dtype == torch.uint8
+    if fp8:
+        _block_scales(k_cache, v_cache, k_scale, v_scale)
+        _contig(k_scale, v_scale)
+    else:
+        _pools(k_cache, v_cache)
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("scales belong to e4m3 pools")
+    B = context_lens.shape[0]
+    NB, bs, Hkv, D = k_cache.shape
+    if kept_lens.shape != (B,) or seen_lens.shape != (B,) or new_lens.shape != (B,):
+        raise ValueError("kept_lens, seen_lens and new_lens are [num_seqs]")
+    if weights.dtype != torch.float32 or weights_out.dtype != torch.float32:
+        raise TypeError("weights are float32")
+    if weights.dim() != 3 or tuple(weights.shape[:2]) != (B, Hkv) or not (
+            weights.shape == token_pos.shape == weights_out.shape == token_pos_out.shape):
+        raise ValueError("weights and token_pos are [num_seqs, num_kv_heads, slots], in and out alike")
+    if workspace is None:
+        workspace = alloc_evict_workspace(k_cache, block_tables, budget)
+    _same_device(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, kept_lens, seen_lens, weights,
+                 token_pos, new_lens, weights_out, token_pos_out, workspace)
+    _check(lib.pa_evict(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
+                        block_tables.shape[1], _ptr(context_lens), _ptr(kept_lens), _ptr(seen_lens), B, _ptr(weights),
+                        _ptr(token_pos), budget, recent, sinks, _ptr(new_lens), _ptr(weights_out),
+                        _ptr(token_pos_out), weights.shape[2], NB, bs, Hkv, D, _ptr(workspace), workspace.numel(),
+                        _dtype(k_cache), _stream(stream)), "pa_evict")
+    return new_lens
 
 
 def selftest_bounded_wait(limit_ns, stream=None):

@@ -115,7 +115,17 @@ extern "C" int pa_last_error(void) {
   const unsigned c = pa::fetch_status_prefill();
   const unsigned d = pa::fetch_status_selftest();
   if (a == 0xffffffffu || b == 0xffffffffu || c == 0xffffffffu || d == 0xffffffffu) return PA_ERR_CUDA;
-  return (int)(a | b | c | d);
+  unsigned all = a | b | c | d;
+  // the block-scaled e4m3 cache and the eviction units
+  unsigned (*const more[])() = {pa::fetch_status_fp8_blocks, pa::fetch_status_decode_fp8_blocks,
+                                pa::fetch_status_decode_weights, pa::fetch_status_decode_weights_fp8,
+                                pa::fetch_status_prefill_fp8_blocks, pa::fetch_status_evict};
+  for (auto fetch : more) {
+    const unsigned v = fetch();
+    if (v == 0xffffffffu) return PA_ERR_CUDA;
+    all |= v;
+  }
+  return (int)all;
 }
 
 extern "C" const char* pa_strerror(int code) {
@@ -136,6 +146,6 @@ extern "C" const char* pa_strerror(int code) {
   }
 }
 
-extern "C" int pa_version(void) { return 100; }
+extern "C" int pa_version(void) { return 101; }
 
 extern "C" const char* pa_last_host_error(void) { return pa::g_host_msg; }

@@ -226,6 +226,16 @@ template <> struct Elem<fp8e4m3> {
   }
 };
 
+// Tag type for e4m3 codes in a pool with one scale per (block, KV head).
+struct fp8e4m3b {
+  uint8_t bits;
+};
+template <> struct Elem<fp8e4m3b> : Elem<fp8e4m3> {};
+
+// Floats in one block's row of such a pool's scales: the KV heads rounded up
+// to whole 16-byte chunks, so that a row can be moved by bulk copies.
+__host__ __device__ __forceinline__ constexpr int scale_row(int num_kv_heads) { return (num_kv_heads + 3) & ~3; }
+
 inline int elem_bytes(pa_dtype dt) { return dt == PA_F32 ? 4 : dt == PA_FP8_E4M3 ? 1 : 2; }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -264,6 +274,12 @@ cudaError_t launch_after(const void* kernel, dim3 grid, dim3 block, void** args,
 unsigned fetch_status_cache_ops();
 unsigned fetch_status_decode();
 unsigned fetch_status_decode_fp8();
+unsigned fetch_status_decode_fp8_blocks();
+unsigned fetch_status_decode_weights();
+unsigned fetch_status_decode_weights_fp8();
+unsigned fetch_status_fp8_blocks();
+unsigned fetch_status_prefill_fp8_blocks();
+unsigned fetch_status_evict();
 unsigned fetch_status_shared();
 unsigned fetch_status_prefill();
 unsigned fetch_status_selftest();

@@ -263,14 +263,31 @@ extern "C" size_t pa_decode_workspace_bytes(int num_seqs, int num_heads, int num
   return (size_t)(ml + rows * head_dim * 4 + 256);     // + the work-item counter
 }
 
-// Shared by pa_decode and pa_decode_fp8: dtype is the query/output type,
-// kv the pool's (dtype itself, or PA_FP8_E4M3 with per-token scales).
+// What pa_decode_weights adds to a decode: the running totals and their row
+// stride (floats), and how many workspace bytes the scores take.
+struct WeightsArgs {
+  float* weights;
+  long long stride;
+};
+
+// Workspace of a weights-mode decode: (m, l) of every partition, the partial
+// outputs (none when no sequence can span two partitions), the item counter,
+// then the scores.
+static size_t weights_partials_bytes(long long rows, int max_parts, int head_dim) {
+  const long long ml = ((rows * max_parts * 8) + 255) / 256 * 256;
+  return (size_t)(ml + (max_parts > 1 ? rows * max_parts * head_dim * 4 : 0) + 256);
+}
+
+// Shared by pa_decode, pa_decode_fp8, pa_decode_fp8_blocks and
+// pa_decode_weights (wa not null): dtype is the query/output type, kv the
+// pool's (dtype itself, or PA_FP8_E4M3 with per-token scales, or with one scale
+// per (block, KV head) when `blk`).
 static int decode_impl(void* out, const void* query, const void* k_cache, const void* v_cache,
                        const float* k_scale, const float* v_scale, const int32_t* block_tables,
                        int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int num_heads,
                        int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
                        int partition_size, void* workspace, size_t workspace_bytes, pa_dtype dtype, pa_dtype kv,
-                       void* stream) {
+                       void* stream, bool blk = false, const WeightsArgs* wa = nullptr) {
   if (dtype != PA_F32 && dtype != PA_BF16) return PA_ERR_DTYPE;
   if (kv != dtype && !(kv == PA_FP8_E4M3 && dtype == PA_BF16)) return PA_ERR_DTYPE;
   const bool fp8 = kv == PA_FP8_E4M3;
@@ -279,8 +296,16 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
       max_blocks_per_seq <= 0)
     return PA_ERR_SHAPE;
   if (partition_size > 0 && partition_size % block_size) return PA_ERR_SHAPE;
+  if (wa) {
+    // one second-kernel CTA per (sequence, KV head, kWeightTokens tokens), and the merge's
+    const long long max_ctx = (long long)max_blocks_per_seq * block_size;
+    const long long ctas = (long long)num_seqs * num_kv_heads * ((max_ctx + kWeightTokens - 1) / kWeightTokens) +
+                           (long long)num_seqs * num_heads;
+    if (wa->stride < max_ctx || num_heads / num_kv_heads > 1024 || ctas > 0x7fffffffll) return PA_ERR_SHAPE;
+  }
   if (num_seqs == 0) return PA_OK;
-  if (!out || !query || !k_cache || !v_cache || !block_tables || !context_lens) return PA_ERR_NULL;
+  if (!out || !query || !k_cache || !v_cache || !block_tables || !context_lens || (wa && !wa->weights))
+    return PA_ERR_NULL;
   if (fp8 && (!k_scale || !v_scale)) return PA_ERR_NULL;
   if (!aligned16(out) || !aligned16(query) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_ALIGN;
   if (fp8 && (!aligned16(k_scale) || !aligned16(v_scale))) return PA_ERR_ALIGN;
@@ -289,8 +314,10 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
                                   kv == PA_FP8_E4M3, num_seqs, num_kv_heads);
   const long long max_ctx = (long long)max_blocks_per_seq * block_size;
   const int max_parts = (int)((max_ctx + P - 1) / P);
-  const size_t need = pa_decode_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim,
-                                                max_blocks_per_seq, block_size, partition_size);
+  const size_t partials = wa ? weights_partials_bytes((long long)num_seqs * num_heads, max_parts, head_dim) : 0;
+  const size_t need = wa ? partials + (size_t)num_seqs * num_heads * max_ctx * 4
+                         : pa_decode_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim,
+                                                     max_blocks_per_seq, block_size, partition_size);
   if (need && (!workspace || workspace_bytes < need)) return PA_ERR_WORKSPACE;
 
   int dev = 0;
@@ -333,7 +360,10 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
   prm.ws_o = need ? reinterpret_cast<float*>(static_cast<char*>(workspace) + ((rows * 8) + 255) / 256 * 256)
                   : nullptr;
   // the work-item counter: the workspace's last 256 bytes
-  prm.ws_next = need ? reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + need - 256) : nullptr;
+  // (weights mode: before the scores)
+  prm.ws_next = need ? reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + (wa ? partials : need) - 256)
+                     : nullptr;
+  prm.ws_s = wa ? reinterpret_cast<float*>(static_cast<char*>(workspace) + partials) : nullptr;
   prm.B = num_seqs;
   prm.Hq = num_heads;
   prm.Hkv = num_kv_heads;
@@ -357,6 +387,7 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
   prm.qscale = scale * kLog2e;
   prm.k_scale = fp8 ? k_scale : nullptr;
   prm.v_scale = fp8 ? v_scale : nullptr;
+  prm.scale_row = scale_row(num_kv_heads);
   prm.tile_bytes = (uint32_t)(block_size * head_dim * elem_bytes(kv));
   // K/V stages per CTA: ~96 KB on the tensor-core path (one ring shared by
   // the four head warps), ~64 KB on the CUDA-core path (a ring per warp);
@@ -379,11 +410,14 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
   prm.spg_shift = (spg & (spg - 1)) ? -1 : (spg == 1 ? 0 : spg == 2 ? 1 : spg == 4 ? 2 : 3);
   const int S = spg * prm.WPH;
 
-  const Launch L = fp8               ? pick_decode_fp8(head_dim, GT, prm.HG, use_mma)
+  const Launch L = wa && fp8         ? pick_decode_weights_fp8(head_dim, GT, prm.HG, use_mma)
+                   : wa              ? pick_decode_weights(dtype == PA_F32, head_dim, GT, prm.HG, use_mma)
+                   : blk             ? pick_decode_fp8_blocks(head_dim, GT, prm.HG, use_mma)
+                   : fp8             ? pick_decode_fp8(head_dim, GT, prm.HG, use_mma)
                    : use_mma         ? (head_dim == 64 ? pick_mma<64>(GT, prm.HG) : pick_mma<128>(GT, prm.HG))
                    : dtype == PA_F32 ? pick1<float, float>(head_dim, GT, prm.HG)
                                      : pick1<__nv_bfloat16, __nv_bfloat16>(head_dim, GT, prm.HG);
-  const size_t smem = 2 * (size_t)S * prm.HG * prm.tile_bytes + (fp8 ? 2 * (size_t)S * block_size * 4 : 0) +
+  const size_t smem = 2 * (size_t)S * prm.HG * prm.tile_bytes + (fp8 ? 2 * (size_t)S * (blk ? 4 : block_size) * 4 : 0) +
                       (size_t)kConsumerWarps * GT * (head_dim + 2) * sizeof(float) +
                       2 * (size_t)S * sizeof(uint64_t) + 2 * kItemQ * sizeof(uint64_t) + 16 +
                       (kItemQ + 4) * sizeof(int) +
@@ -409,7 +443,20 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
                  "cudaLaunchKernel(decode_kernel)")) {
     return PA_ERR_CUDA;
   }
-  if (max_parts > 1) {
+  if (wa) {
+    const unsigned merge_blocks =
+        max_parts > 1 ? (unsigned)(((long long)num_seqs * num_heads * 32 + kWeightTokens - 1) / kWeightTokens) : 0u;
+    const long long blocks =
+        merge_blocks + (long long)num_seqs * num_kv_heads * ((max_ctx + kWeightTokens - 1) / kWeightTokens);
+    float* w = wa->weights;
+    long long stride = wa->stride;
+    unsigned mb = merge_blocks;
+    void* wargs[] = {&prm, &w, &stride, &mb};
+    if (!ck(launch_dependent(L.merge, dim3((unsigned)blocks), dim3(kWeightTokens), wargs, 2 * (size_t)G * 4,
+                             (cudaStream_t)stream),
+            "cudaLaunchKernel(weights_kernel)"))
+      return PA_ERR_CUDA;
+  } else if (max_parts > 1) {
     const long long warps = (long long)num_seqs * num_heads;
     const unsigned blocks = (unsigned)((warps * 32 + 255) / 256);
     void* margs[] = {&prm};
@@ -441,6 +488,42 @@ extern "C" int pa_decode_fp8(void* out, const void* query, const void* k_cache, 
   return decode_impl(out, query, k_cache, v_cache, k_scale, v_scale, block_tables, max_blocks_per_seq,
                      context_lens, num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
                      partition_size, workspace, workspace_bytes, dtype, PA_FP8_E4M3, stream);
+}
+
+extern "C" int pa_decode_fp8_blocks(void* out, const void* query, const void* k_cache, const void* v_cache,
+                                    const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                                    int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
+                                    int num_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                    float scale, int partition_size, void* workspace, size_t workspace_bytes,
+                                    pa_dtype dtype, void* stream) {
+  return decode_impl(out, query, k_cache, v_cache, k_scale, v_scale, block_tables, max_blocks_per_seq,
+                     context_lens, num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                     partition_size, workspace, workspace_bytes, dtype, PA_FP8_E4M3, stream, true);
+}
+
+extern "C" size_t pa_decode_weights_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                                    int max_blocks_per_seq, int block_size, int partition_size,
+                                                    pa_dtype kv_dtype) {
+  const int P = partition_size_impl(kv_dtype == PA_FP8_E4M3, num_seqs, num_heads, num_kv_heads, head_dim,
+                                    max_blocks_per_seq, block_size, partition_size);
+  if (P <= 0 || num_seqs <= 0) return 0;
+  const long long max_ctx = (long long)max_blocks_per_seq * block_size;
+  const long long rows = (long long)num_seqs * num_heads;
+  return weights_partials_bytes(rows, (int)((max_ctx + P - 1) / P), head_dim) + (size_t)(rows * max_ctx * 4);
+}
+
+extern "C" int pa_decode_weights(void* out, float* weights, long long weights_stride, const void* query,
+                                 const void* k_cache, const void* v_cache, const float* k_scale,
+                                 const float* v_scale, const int32_t* block_tables, int max_blocks_per_seq,
+                                 const int32_t* context_lens, int num_seqs, int num_heads, int num_kv_heads,
+                                 int head_dim, int block_size, int num_blocks, float scale, int partition_size,
+                                 void* workspace, size_t workspace_bytes, pa_dtype dtype, pa_dtype kv_dtype,
+                                 void* stream) {
+  const WeightsArgs wa{weights, weights_stride};
+  return decode_impl(out, query, k_cache, v_cache, k_scale, v_scale, block_tables, max_blocks_per_seq,
+                     context_lens, num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                     partition_size, workspace, workspace_bytes, dtype, kv_dtype, stream, kv_dtype == PA_FP8_E4M3,
+                     &wa);
 }
 
 // ---------------------------------------------------------------------------

@@ -59,6 +59,8 @@
 //    issued before the CTA exits.
 #pragma once
 
+#include <type_traits>
+
 #include "pa_common.cuh"
 #include "pa_mma.cuh"
 
@@ -85,8 +87,10 @@ struct DecodeParams {
   long long n_virtual;
   int dense;          // 1: enumerate only real items through a per-CTA prefix table (B <= kDenseMaxSeqs)
   float qscale;       // scale * log2(e)
-  const float* k_scale;  // e4m3 pools: per-token K scales [num_blocks * bs]; else null
-  const float* v_scale;  // e4m3 pools: per-token V scales
+  const float* k_scale;  // e4m3 pools: per-token K scales [num_blocks * bs], or per-block scales
+  const float* v_scale;  // [num_blocks][scale_row]; the same for V; else null
+  int scale_row;         // per-block scales: floats per block
+  float* ws_s;           // weights mode: scores [B*Hq][max_blocks*bs] in log2 units
   int HG;             // KV heads per work item (one consumer warp each when HG = 4)
   int n_hg;           // Hkv / HG
   int WPH;            // warp groups: kConsumerWarps / HG (warps sharing one head)
@@ -186,7 +190,10 @@ __device__ __forceinline__ bool decode_item(const DecodeParams& p, long long v, 
 }
 
 // T: query/output element type; KT: K/V pool element type (T itself, or
-// e4m3 codes with a per-token scale for K and for V).
+// e4m3 codes with a per-token scale for K and for V, or e4m3 codes with one
+// scale per (block, KV head)).  W: weights mode: every valid token's scores
+// (log2 units, fp32) go to ws_s and every item's (m, l) to ws_ml, split or not,
+// for weights_kernel to turn into softmax weights.
 // e4m3 tensor-core instances are held to three CTAs per SM (at most 136
 // registers): their per-block conversion work needs the extra warps to hide
 // latency (20 % faster on the grouped-query workload than two CTAs per SM).
@@ -195,13 +202,14 @@ __device__ __forceinline__ bool decode_item(const DecodeParams& p, long long v, 
 #ifndef PA_FP8_MMA_MIN_BLOCKS
 #define PA_FP8_MMA_MIN_BLOCKS 3
 #endif
-template <typename T, typename KT, int D, int GT, bool MMA, int HG>
+template <typename T, typename KT, int D, int GT, bool MMA, int HG, bool W = false>
 __global__ void __launch_bounds__(kThreads, (MMA && sizeof(KT) == 1) ? (GT <= 8 ? PA_FP8_MMA_MIN_BLOCKS : 2) : 1)
 decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
               const DecodeParams p) {
   using E = Elem<T>;                           // queries and output
   using EK = Elem<KT>;                         // K/V pool
-  constexpr bool SCALED = EK::kBytes == 1;     // e4m3 codes with per-token scales
+  constexpr bool SCALED = EK::kBytes == 1;     // e4m3 codes with scales
+  constexpr bool BLK = std::is_same<KT, fp8e4m3b>::value;   // one scale per (block, KV head), else per token
   constexpr int CHUNKS = D * EK::kBytes / 16;  // 16-byte chunks per token row
   // chunks per lane: two, except for e4m3 with several query heads, where
   // two chunks (32 dims) per lane would need 2*GT*32 registers for q and o
@@ -230,9 +238,11 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
   unsigned char* tilesK = smem;
   unsigned char* tilesV = smem + (size_t)S * stage_bytes;
   // e4m3 pools: each stage also holds the block's bs K scales and bs V scales
+  // (per-block scales: the 16-byte chunk of the scale row with the item's heads)
+  const int scl_n = BLK ? 4 : p.bs;
   float* sclK = reinterpret_cast<float*>(tilesV + (size_t)S * stage_bytes);
-  float* sclV = sclK + (SCALED ? S * p.bs : 0);
-  float* mbuf = sclV + (SCALED ? S * p.bs : 0);
+  float* sclV = sclK + (SCALED ? S * scl_n : 0);
+  float* mbuf = sclV + (SCALED ? S * scl_n : 0);
   uint64_t* full = reinterpret_cast<uint64_t*>(mbuf + NCW * GT * (D + 2));
   uint64_t* empty = full + S;
   uint64_t* qfull = empty + S;                  // [kItemQ] item queue: index written
@@ -455,7 +465,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
               atomicOr(&g_status_decode, PA_DEV_TIMEOUT);
               *abort_flag = 1;
             } else {
-              mbar_arrive_expect_tx(&full[st], 2u * stage_bytes + (SCALED ? 8u * (uint32_t)p.bs : 0u));
+              mbar_arrive_expect_tx(&full[st], 2u * stage_bytes + (SCALED ? 8u * (uint32_t)scl_n : 0u));
               go = 1;
             }
           }
@@ -472,8 +482,10 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
                             0, item.kvh0, 0, bi, pol);
               if constexpr (SCALED) {
                 if (lane == 2 || lane == 3)
-                  bulk_load((lane == 2 ? sclK : sclV) + st * p.bs,
-                            (lane == 2 ? p.k_scale : p.v_scale) + (size_t)bi * p.bs, 4u * p.bs, &full[st], pol);
+                  bulk_load((lane == 2 ? sclK : sclV) + st * scl_n,
+                            (lane == 2 ? p.k_scale : p.v_scale) +
+                                (BLK ? (size_t)bi * p.scale_row + (item.kvh0 & ~3) : (size_t)bi * p.bs),
+                            4u * scl_n, &full[st], pol);
               }
             } else if (lane < NOPS) {
               // tensor-core path: many 128-byte-swizzled column spans per
@@ -487,8 +499,10 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
                           bi, pol);
             } else if (SCALED && (lane == NOPS || lane == NOPS + 1)) {
               const bool vs = lane == NOPS + 1;
-              bulk_load((vs ? sclV : sclK) + st * p.bs, (vs ? p.v_scale : p.k_scale) + (size_t)bi * p.bs, 4u * p.bs,
-                        &full[st], pol);
+              bulk_load((vs ? sclV : sclK) + st * scl_n,
+                        (vs ? p.v_scale : p.k_scale) +
+                            (BLK ? (size_t)bi * p.scale_row + (item.kvh0 & ~3) : (size_t)bi * p.bs),
+                        4u * scl_n, &full[st], pol);
             }
           }
           if (lane == 0 && go) {
@@ -566,6 +580,10 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
       if (L < 0 || L > p.max_blocks * p.bs) atomicOr(&g_status_decode, PA_DEV_BAD_LEN);
     }
     const int h0 = (item.kvh0 + hl) * p.G + item.sg * GT;
+    // weights mode: the score of the warp's h-th query head for token t
+    auto put_score = [&](bool ok, int h, int t, float s) {
+      if (ok && h < GT) p.ws_s[((size_t)item.b * p.Hq + h0 + h) * ((size_t)p.max_blocks * p.bs) + t] = s;
+    };
 
     if constexpr (MMA && SCALED && GT <= 8) {
       // e4m3 pool, query group of at most 8 heads: tokens in the M rows.
@@ -637,8 +655,10 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
           unsigned char* vt_ptr = tilesV + (size_t)st * stage_bytes + (size_t)hl * p.tile_bytes;
           const uint32_t kt = smem_u32(tilesK + (size_t)st * stage_bytes + (size_t)hl * p.tile_bytes);
           const uint32_t vt = smem_u32(vt_ptr);
-          const float* sk = sclK + st * p.bs;
-          const float* sv = sclV + st * p.bs;
+          // (token t's scale is sk[t * SS]: per-block scales are one value)
+          const float* sk = sclK + st * scl_n + (BLK ? (item.kvh0 + hl) & 3 : 0);
+          const float* sv = sclV + st * scl_n + (BLK ? (item.kvh0 + hl) & 3 : 0);
+          constexpr int SS = BLK ? 0 : 1;
           if (valid < p.bs) {
             for (int idx = lane; idx < (p.bs - valid) * 8; idx += 32)
               *reinterpret_cast<uint4*>(vt_ptr + (valid + idx / 8) * 128 + (idx % 8) * 16) =
@@ -647,9 +667,13 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
             __syncwarp();
           }
           float vmax = 0.f;
-          for (int t = lane; t < valid; t += 32) vmax = fmaxf(vmax, sv[t]);
+          if constexpr (BLK) {
+            vmax = sv[0];
+          } else {
+            for (int t = lane; t < valid; t += 32) vmax = fmaxf(vmax, sv[t]);
 #pragma unroll
-          for (int off = 16; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
+            for (int off = 16; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
+          }
           if (vmax > 0.f) {
             const int ve = ilogbf(vmax) + 1;
             if (ve > rexp) {
@@ -690,11 +714,18 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
             }
             const int t0 = tb + g, t1 = tb + g + 8;
             const bool ok0 = t0 < valid, ok1 = t1 < valid;
-            const float f0 = ok0 ? sfac * sk[t0] : 0.f, f1 = ok1 ? sfac * sk[t1] : 0.f;
+            const float f0 = ok0 ? sfac * sk[t0 * SS] : 0.f, f1 = ok1 ? sfac * sk[t1 * SS] : 0.f;
             St[0] = ok0 ? St[0] * f0 : -INFINITY;
             St[1] = ok0 ? St[1] * f0 : -INFINITY;
             St[2] = ok1 ? St[2] * f1 : -INFINITY;
             St[3] = ok1 ? St[3] * f1 : -INFINITY;
+            if constexpr (W) {
+              const int tk = (item.jb + i) * p.bs;
+              put_score(ok0, 2 * tq, tk + t0, St[0]);
+              put_score(ok0, 2 * tq + 1, tk + t0, St[1]);
+              put_score(ok1, 2 * tq, tk + t1, St[2]);
+              put_score(ok1, 2 * tq + 1, tk + t1, St[3]);
+            }
             float alpha[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -716,7 +747,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
                 OT[c][3] *= alpha[1];
               }
             }
-            const float vs0 = ok0 ? sv[t0] * vdown : 0.f, vs1 = ok1 ? sv[t1] * vdown : 0.f;
+            const float vs0 = ok0 ? sv[t0 * SS] * vdown : 0.f, vs1 = ok1 ? sv[t1 * SS] * vdown : 0.f;
             float pw[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -858,8 +889,10 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
           unsigned char* vt_ptr = tilesV + (size_t)st * stage_bytes + (size_t)hl * p.tile_bytes;
           const uint32_t kt = smem_u32(tilesK + (size_t)st * stage_bytes + (size_t)hl * p.tile_bytes);
           const uint32_t vt = smem_u32(vt_ptr);
-          const float* sk = sclK + st * p.bs;
-          const float* sv = sclV + st * p.bs;
+          // (token t's scale is sk[t * SS]: per-block scales are one value)
+          const float* sk = sclK + st * scl_n + (BLK ? (item.kvh0 + hl) & 3 : 0);
+          const float* sv = sclV + st * scl_n + (BLK ? (item.kvh0 + hl) & 3 : 0);
+          constexpr int SS = BLK ? 0 : 1;
           if (valid < p.bs) {
             // slots past the context may hold anything (NaN codes): clear
             // those V rows (P is 0 there, but 0 * NaN would be NaN)
@@ -871,9 +904,13 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
           }
           // V-scale reference for this block (valid tokens only)
           float vmax = 0.f;
-          for (int t = lane; t < valid; t += 32) vmax = fmaxf(vmax, sv[t]);
+          if constexpr (BLK) {
+            vmax = sv[0];
+          } else {
+            for (int t = lane; t < valid; t += 32) vmax = fmaxf(vmax, sv[t]);
 #pragma unroll
-          for (int off = 16; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
+            for (int off = 16; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
+          }
           if (vmax > 0.f) {
             const int ve = ilogbf(vmax) + 1;          // 2^ve > vmax
             if (ve > rexp) {
@@ -921,8 +958,9 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
               for (int e = 0; e < 4; ++e) {
                 const int t = tb + n * 8 + 2 * tq + (e & 1);
                 const bool ok = t < valid;
-                S[n][e] = ok ? S[n][e] * (sfac * sk[t]) : -INFINITY;
-                if (e < 2) vsc[n][e] = ok ? sv[t] * vdown : 0.f;
+                S[n][e] = ok ? S[n][e] * (sfac * sk[t * SS]) : -INFINITY;
+                if (e < 2) vsc[n][e] = ok ? sv[t * SS] * vdown : 0.f;
+                if constexpr (W) put_score(ok, g + 8 * (e >> 1), (item.jb + i) * p.bs + t, S[n][e]);
                 mx[e >> 1] = fmaxf(mx[e >> 1], S[n][e]);
               }
             float alpha[2];
@@ -1081,6 +1119,13 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
             St[1] = ok0 ? St[1] * p.qscale : -INFINITY;
             St[2] = ok1 ? St[2] * p.qscale : -INFINITY;
             St[3] = ok1 ? St[3] * p.qscale : -INFINITY;
+            if constexpr (W) {
+              const int tk = (item.jb + i) * p.bs;
+              put_score(ok0, 2 * tq, tk + t0, St[0]);
+              put_score(ok0, 2 * tq + 1, tk + t0, St[1]);
+              put_score(ok1, 2 * tq, tk + t1, St[2]);
+              put_score(ok1, 2 * tq + 1, tk + t1, St[3]);
+            }
             float alpha[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -1229,6 +1274,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
               for (int e = 0; e < 4; ++e) {
                 const int t = tb + n * 8 + 2 * tq + (e & 1);
                 S[n][e] = t < valid ? S[n][e] * p.qscale : -INFINITY;
+                if constexpr (W) put_score(t < valid, g + 8 * (e >> 1), (item.jb + i) * p.bs + t, S[n][e]);
                 mx[e >> 1] = fmaxf(mx[e >> 1], S[n][e]);
               }
             float alpha[2];
@@ -1383,13 +1429,14 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
               }
               // e4m3: the token's K scale multiplies its whole score
               float ksc = 1.f;
-              if constexpr (SCALED) ksc = ok ? sclK[st * p.bs + t] : 0.f;
+              if constexpr (SCALED) ksc = ok ? sclK[st * scl_n + (BLK ? (item.kvh0 + hl) & 3 : t)] : 0.f;
   #pragma unroll
               for (int h = 0; h < GT; ++h) {
   #pragma unroll
                 for (int off = LPT / 2; off > 0; off >>= 1)
                   part[h] += __shfl_xor_sync(0xffffffffu, part[h], off);
                 s[k][h] = ok ? part[h] * ksc : -INFINITY;
+                if constexpr (W) put_score(ok && li == 0, h, (item.jb + i) * p.bs + t, s[k][h]);
               }
             }
   #pragma unroll
@@ -1423,7 +1470,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
                              vf + hf * EPC);
                 // e4m3: the token's V scale rides on its softmax weight
                 float vsc = 1.f;
-                if constexpr (SCALED) vsc = sclV[st * p.bs + t];
+                if constexpr (SCALED) vsc = sclV[st * scl_n + (BLK ? (item.kvh0 + hl) & 3 : t)];
   #pragma unroll
                 for (int h = 0; h < GT; ++h) {
                   const float pk = exp2f(s[k][h] - m[h]);
@@ -1505,6 +1552,12 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
       const size_t bh = (size_t)item.b * p.Hq + (size_t)(item.kvh0 + hh) * p.G + item.sg * GT + h;
       if (!item.split) {
         E::store1(static_cast<T*>(p.out) + bh * D + d, den > 0.f ? num / den : 0.f);
+        if constexpr (W) {
+          if (d == 0) {
+            p.ws_ml[bh * p.max_parts * 2] = M;
+            p.ws_ml[bh * p.max_parts * 2 + 1] = den;
+          }
+        }
       } else {
         const size_t slot = bh * p.max_parts + item.part;
         p.ws_o[slot * D + d] = num;
@@ -1523,11 +1576,9 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
 // Lane i < 32 computes partition i's weight (broadcast by shuffle); each
 // partition's row of o is read as one vector of D/32 floats per lane.
 template <typename T, int D>
-__global__ void __launch_bounds__(256)
-merge_kernel(const DecodeParams p) {
+__device__ __forceinline__ void merge_row(const DecodeParams& p, long long gw) {
   using E = Elem<T>;
   constexpr int VPL = D / 32;                 // dims per lane: 4, 2 or 1
-  const long long gw = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (gw >= (long long)p.B * p.Hq) return;
   const int b = (int)(gw / p.Hq);
@@ -1585,6 +1636,66 @@ merge_kernel(const DecodeParams p) {
   for (int k = 0; k < VPL; ++k) E::store1(out + k, acc[k] * inv);
 }
 
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+merge_kernel(const DecodeParams p) {
+  merge_row<T, D>(p, ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5);
+}
+
+// Weights mode's second kernel: the first `merge_blocks` CTAs merge the
+// partitions as merge_kernel does; each of the others takes one (sequence, KV
+// head, 256 tokens) and adds the softmax weights to their running totals:
+//   weights[b, g, t] += sum over the group's heads h of 2^(s[b,h,t] - M_h) / l_h
+// with (M_h, l_h) the log-sum-exp of the partitions' states.  One thread per
+// token reads its G scores (a coalesced row of each head) and adds them in
+// head order: no atomics, the same sum on every run.
+constexpr int kWeightTokens = 256;
+template <typename T, int D>
+__global__ void __launch_bounds__(kWeightTokens)
+weights_kernel(const DecodeParams p, float* weights, long long wstride, unsigned merge_blocks) {
+  extern __shared__ float hm[];               // [G] M_h, then [G] 1 / l_h
+  if (blockIdx.x < merge_blocks) {
+    merge_row<T, D>(p, ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5);
+    return;
+  }
+  const int Lmax = p.max_blocks * p.bs;
+  const int nt = (Lmax + kWeightTokens - 1) / kWeightTokens;
+  long long u = (long long)blockIdx.x - merge_blocks;
+  const int t0 = (int)(u % nt) * kWeightTokens;
+  u /= nt;
+  const int g = (int)(u % p.Hkv), b = (int)(u / p.Hkv);
+  int L = __ldg(&p.context_lens[b]);
+  if (L < 0 || L > Lmax) L = L < 0 ? 0 : Lmax;
+  if (t0 >= L) return;
+  const int t = t0 + (int)threadIdx.x;
+  const int nparts = (L + p.part_tokens - 1) / p.part_tokens;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const size_t row0 = (size_t)b * p.Hq + (size_t)g * p.G;
+  for (int h = warp; h < p.G; h += kWeightTokens / 32) {
+    const float* ml = p.ws_ml + (row0 + h) * p.max_parts * 2;
+    float M = -INFINITY, den = 0.f;
+    for (int i = lane; i < nparts; i += 32) M = fmaxf(M, ml[2 * i]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    for (int i = lane; i < nparts; i += 32)
+      den += ml[2 * i] == -INFINITY ? 0.f : exp2f(ml[2 * i] - M) * ml[2 * i + 1];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
+    if (lane == 0) {
+      hm[h] = M == -INFINITY ? 0.f : M;
+      hm[p.G + h] = den > 0.f ? 1.f / den : 0.f;
+    }
+  }
+  __syncthreads();
+  if (t >= L) return;
+  float sum = 0.f;
+  for (int h = 0; h < p.G; ++h)
+    sum = fmaf(exp2f(p.ws_s[(row0 + h) * Lmax + t] - hm[h]), hm[p.G + h], sum);
+  float* w = weights + ((size_t)b * p.Hkv + g) * wstride + t;
+  *w += sum;
+}
+
 }  // namespace
 
 // A decode kernel and the merge kernel that goes with it.
@@ -1596,5 +1707,11 @@ struct Launch {
 // e4m3-pool instances (pa_decode_fp8.cu): bf16 queries, hg KV heads per
 // work item, tensor cores (head_dim 128, gt a power of two >= 2) or CUDA cores.
 Launch pick_decode_fp8(int head_dim, int gt, int hg, bool mma);
+// The same for pools with one scale per (block, KV head) (pa_decode_fp8_blocks.cu).
+Launch pick_decode_fp8_blocks(int head_dim, int gt, int hg, bool mma);
+// Weights-mode instances: pools of the query's type (pa_decode_weights.cu) and
+// block-scaled e4m3 pools (pa_decode_weights_fp8.cu).
+Launch pick_decode_weights(bool f32, int head_dim, int gt, int hg, bool mma);
+Launch pick_decode_weights_fp8(int head_dim, int gt, int hg, bool mma);
 
 }  // namespace pa

@@ -1,0 +1,216 @@
+// pa_fp8_blocks.cu — quantising append into an e4m3 pool with one power-of-two
+// scale per (block, KV head).
+//
+// For every block that a sequence's new tokens touch and every head, K and V
+// apart:
+//   a    = max |x| over the block's new finite elements of the head
+//   need = the smallest power of two with a <= 448 * need (at least 2^-100; 0 when a is 0)
+//   s    = max(need, the block's scale if it holds earlier tokens of the sequence)
+//   new codes = e4m3(x / s), saturating; earlier codes c become e4m3(value(c) * old / s)
+// A power of two costs a floating-point code nothing: its relative precision
+// is the same at every exponent, x / s is exact, and raising the scale of codes
+// written before shifts their exponents, which is exact but for values that
+// fall below the smallest normal code.  So a block filled token by token holds
+// what one filled at once holds, up to those.
+//
+// One warp per (touched block, head, K|V): the block's new rows of the head
+// are read once for the maximum and once (from L1) for the codes, 16 bytes per
+// lane, D elements of a head being 4 to 32 lanes' worth.  Blocks are owned by
+// one warp each, so nothing is atomic.  Which block a warp works on needs no
+// scan over the sequences: sequence b's units start at
+//   U_b = floor(query_start[b] / bs) + 2 b,
+// and n tokens touch at most floor((n - 1) / bs) + 2 blocks, which never passes
+// U_{b+1}; a binary search over query_start finds b, and surplus units leave.
+// Bound by HBM: reads elem and writes 1 byte per element.
+#include "pa_common.cuh"
+
+namespace pa {
+namespace {
+
+__device__ unsigned g_status_fp8_blocks;
+
+constexpr int kWarps = 4;
+constexpr float kMinScale = 7.888609052210118e-31f;   // 2^-100
+constexpr float kE4m3Max = 448.f;
+
+// The smallest power of two s with a <= 448 s, not below 2^-100; 0 for 0.
+// (448 = 1.75 * 2^8: a = m * 2^e with m in [1, 2) needs 2^(e-8), or 2^(e-7) when m > 1.75.)
+__device__ __forceinline__ float pow2_scale(float a) {
+  if (!(a > 0.f)) return 0.f;
+  const uint32_t u = __float_as_uint(a);
+  const int e = (int)(u >> 23) - 127;                 // a subnormal counts as 2^-127: the floor applies
+  const int k = e - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return k < -100 ? kMinScale : __uint_as_float((uint32_t)(k + 127) << 23);
+}
+
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+  return (uint32_t)__nv_cvt_float_to_fp8(a, __NV_SATFINITE, __NV_E4M3) |
+         (uint32_t)__nv_cvt_float_to_fp8(b, __NV_SATFINITE, __NV_E4M3) << 8 |
+         (uint32_t)__nv_cvt_float_to_fp8(c, __NV_SATFINITE, __NV_E4M3) << 16 |
+         (uint32_t)__nv_cvt_float_to_fp8(d, __NV_SATFINITE, __NV_E4M3) << 24;
+}
+
+struct AppendParams {
+  const void* src[2];            // key, value [T, Hkv, D]
+  uint8_t* pool[2];
+  float* scale[2];
+  const int32_t* query_start;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  int B, T, Hkv, D, bs, max_blocks, num_blocks, scale_row;
+};
+
+// Whether sequence b's rows lie in [0, T] and its new tokens in its context, and
+// the context in its table row.
+__device__ __forceinline__ bool good_seq(const AppendParams& p, int b) {
+  const int s0 = __ldg(&p.query_start[b]), s1 = __ldg(&p.query_start[b + 1]);
+  const int L = __ldg(&p.context_lens[b]);
+  return s0 >= 0 && s1 >= s0 && s1 <= p.T && L >= 0 && L <= p.max_blocks * p.bs && s1 - s0 <= L;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendParams p) {
+  using E = Elem<T>;
+  constexpr int EPC = E::kPerChunk;
+  const int lane = threadIdx.x & 31;
+  const int hx = (int)blockIdx.y * kWarps + (int)(threadIdx.x >> 5);   // (K|V, head)
+  const int u = (int)blockIdx.x;
+  if (u == 0 && blockIdx.y == 0) {
+    // every sequence's arguments are looked at once, whatever units it has
+    for (int i = (int)threadIdx.x; i < p.B; i += kWarps * 32)
+      if (!good_seq(p, i)) atomicOr(&g_status_fp8_blocks, PA_DEV_BAD_LEN);
+  }
+  // the last sequence whose first unit is not above u
+  int lo = 0, hi = p.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(&p.query_start[mid]) / p.bs + 2 * mid <= u) lo = mid;
+    else hi = mid - 1;
+  }
+  const int b = lo;
+  const int s0 = __ldg(&p.query_start[b]), s1 = __ldg(&p.query_start[b + 1]);
+  const int L = __ldg(&p.context_lens[b]);
+  const int i = u - (s0 / p.bs + 2 * b);        // the sequence's i-th touched block
+  const int n = s1 - s0;
+  if (!good_seq(p, b)) return;
+  if (n == 0 || i < 0 || hx >= 2 * p.Hkv) return;
+  const int j = (L - n) / p.bs + i;             // logical block
+  if (j * p.bs >= L) return;
+  const int blk = __ldg(&p.block_tables[(size_t)b * p.max_blocks + j]);
+  if ((unsigned)blk >= (unsigned)p.num_blocks) {
+    if (hx == 0 && lane == 0) atomicOr(&g_status_fp8_blocks, PA_DEV_BAD_BLOCK);
+    return;
+  }
+  const int kv = hx >= p.Hkv ? 1 : 0;
+  const int h = hx - kv * p.Hkv;
+  const int first = max(L - n - j * p.bs, 0);   // the block's first new slot; earlier ones hold tokens
+  const int cnt = min(L - j * p.bs, p.bs) - first;
+  const size_t row = (size_t)p.Hkv * p.D;       // elements from token to token, in the source and in the pool
+  const unsigned char* src = static_cast<const unsigned char*>(p.src[kv]) +
+                             ((size_t)(s0 + j * p.bs + first - (L - n)) * row + (size_t)h * p.D) * sizeof(T);
+  uint8_t* dst = p.pool[kv] + (size_t)blk * p.bs * row + (size_t)h * p.D;
+  const int cpr = p.D / EPC;                    // 16-byte source chunks per row: 4, 8, 16 or 32
+  float amax = 0.f;
+  for (int c = lane; c < cnt * cpr; c += 32) {
+    float f[EPC];
+    E::unpack(ld_nc_v4(src + ((size_t)(c / cpr) * row + (size_t)(c % cpr) * EPC) * sizeof(T)), f);
+#pragma unroll
+    for (int e = 0; e < EPC; ++e) amax = fabsf(f[e]) <= 3.402823466e38f ? fmaxf(amax, fabsf(f[e])) : amax;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  float* sp = p.scale[kv] + (size_t)blk * p.scale_row + h;
+  const float old = first > 0 ? *sp : 0.f;
+  const float s = fmaxf(old, pow2_scale(amax));
+  const float inv = s > 0.f ? 1.f / s : 0.f;    // exact: s is a power of two
+  __syncwarp();
+  if (lane == 0 && (first == 0 || s != old)) *sp = s;
+  if (first > 0 && s > old) {
+    // the earlier tokens' codes under the raised scale, 16 codes per lane
+    const float f = old * inv;
+    const int c16 = p.D / 16;
+    for (int c = lane; c < first * c16; c += 32) {
+      uint8_t* at = dst + (size_t)(c / c16) * row + (size_t)(c % c16) * 16;
+      float v[16];
+      Elem<fp8e4m3>::unpack(*reinterpret_cast<const uint4*>(at), v);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] *= f;
+      st_v4(at, make_uint4(encode4(v[0], v[1], v[2], v[3]), encode4(v[4], v[5], v[6], v[7]),
+                           encode4(v[8], v[9], v[10], v[11]), encode4(v[12], v[13], v[14], v[15])));
+    }
+  }
+  dst += (size_t)first * row;
+  for (int c = lane; c < cnt * cpr; c += 32) {
+    const int t = c / cpr, d = (c % cpr) * EPC;
+    float f[EPC];
+    E::unpack(ld_nc_v4(src + ((size_t)t * row + d) * sizeof(T)), f);
+    uint32_t w[EPC / 4];
+#pragma unroll
+    for (int k = 0; k < EPC / 4; ++k)
+      w[k] = encode4(f[4 * k] * inv, f[4 * k + 1] * inv, f[4 * k + 2] * inv, f[4 * k + 3] * inv);
+    if constexpr (EPC == 8) {
+      *reinterpret_cast<uint2*>(dst + (size_t)t * row + d) = make_uint2(w[0], w[1]);
+    } else {
+      *reinterpret_cast<uint32_t*>(dst + (size_t)t * row + d) = w[0];
+    }
+  }
+}
+
+}  // namespace
+
+unsigned fetch_status_fp8_blocks() {
+  unsigned v = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_status_fp8_blocks, sizeof(v)) != cudaSuccess) return 0xffffffffu;
+  if (v && cudaMemcpyToSymbol(g_status_fp8_blocks, &zero, sizeof(zero)) != cudaSuccess) return 0xffffffffu;
+  return v;
+}
+
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" int pa_append_fp8_blocks(const void* key, const void* value, const int32_t* query_start,
+                                    int total_tokens, const int32_t* block_tables, int max_blocks_per_seq,
+                                    const int32_t* context_lens, int num_seqs, void* k_cache, void* v_cache,
+                                    float* k_scale, float* v_scale, int num_blocks, int block_size,
+                                    int num_kv_heads, int head_dim, pa_dtype src_dtype, void* stream) {
+  if (src_dtype != PA_F32 && src_dtype != PA_BF16) return PA_ERR_DTYPE;
+  if (total_tokens < 0 || num_seqs < 0 || num_blocks <= 0 || num_kv_heads <= 0 || max_blocks_per_seq <= 0 ||
+      !supported_head_dim(head_dim) || !supported_block_size(block_size))
+    return PA_ERR_SHAPE;
+  if ((long long)max_blocks_per_seq * block_size > 0x7fffffffll ||
+      (long long)total_tokens / block_size + 2ll * num_seqs > 0x7fffffffll)
+    return PA_ERR_SHAPE;
+  const long long groups = (2ll * num_kv_heads + kWarps - 1) / kWarps;
+  if (groups > 65535) return PA_ERR_SHAPE;
+  if (total_tokens == 0 || num_seqs == 0) return PA_OK;
+  if (!key || !value || !query_start || !block_tables || !context_lens || !k_cache || !v_cache || !k_scale || !v_scale)
+    return PA_ERR_NULL;
+  if (!aligned16(key) || !aligned16(value) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) ||
+      !aligned16(v_scale))
+    return PA_ERR_ALIGN;
+  AppendParams p;
+  p.src[0] = key;
+  p.src[1] = value;
+  p.pool[0] = static_cast<uint8_t*>(k_cache);
+  p.pool[1] = static_cast<uint8_t*>(v_cache);
+  p.scale[0] = k_scale;
+  p.scale[1] = v_scale;
+  p.query_start = query_start;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.B = num_seqs;
+  p.T = total_tokens;
+  p.Hkv = num_kv_heads;
+  p.D = head_dim;
+  p.bs = block_size;
+  p.max_blocks = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.scale_row = scale_row(num_kv_heads);
+  const dim3 grid((unsigned)(total_tokens / block_size + 2 * num_seqs), (unsigned)groups);
+  if (src_dtype == PA_BF16)
+    append_kernel<__nv_bfloat16><<<grid, kWarps * 32, 0, (cudaStream_t)stream>>>(p);
+  else
+    append_kernel<float><<<grid, kWarps * 32, 0, (cudaStream_t)stream>>>(p);
+  return ck(cudaGetLastError(), "launch append_kernel") ? PA_OK : PA_ERR_CUDA;
+}
