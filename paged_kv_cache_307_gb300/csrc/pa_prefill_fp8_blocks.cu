@@ -5,12 +5,36 @@
 // position p = L_b - n_b + i and attends to the keys at 0..p:
 //   out = sum_t softmax_t(scale * <q, K_t>) V_t,  K = value(code) * k_scale[block, head], V likewise.
 //
-// rows_kernel: one warp per (row, query head), any sizes.  Lane t of a step of
+// tile_kernel (head_dim 128): 5th-generation tensor cores.  One CTA per (query
+// tile, KV head): 128 rows = QP = 128 / G positions x G query heads, keys in
+// tiles of 64, scores and output in tensor memory.
+//  * No K or V tile goes through TMA: warps 4 (K) and 5-6 (V) read the rows
+//    of codes from the pool into registers, a tile ahead, and write them as
+//    16-bit values into the 128-byte-swizzled tiles the MMAs read.  K becomes
+//    f16 (cvt.rn.f16x2.e4m3x2, exact: every code is an f16 value) and its scale
+//    stays apart; V becomes bf16 with its scale multiplied in (exact for a power
+//    of two; bf16 has the exponents for it, so a row that attends only to
+//    blocks of small scale keeps its precision beside blocks of large scale).
+//  * Q (TMA, bf16) is turned into f16 in place by the softmax warps, each row
+//    scaled by its own power of two so that its largest value is in
+//    [2^14, 2^15): exact but for values 2^-28 below that.
+//  * S = Q K^T in f16, one thread per row: x = s * (K scale of the key's block)
+//    * (row factor), running maximum and sum, P = 2^(x - m) in bf16 over the S
+//    columns, O += P V in bf16.  The reference only moves when the maximum
+//    has grown by 2^8.
+//  * Warp 7 issues S_{j+1} before P_j V_j.  Two CTAs per SM (98 KB, 256 threads: the softmax
+//    needs 128 registers, which two CTAs of eight warps have).
+//  * Keys at or past the context length are zeros in both tiles, whatever the
+//    pool holds there.  Every wait is bounded (2 s).
+//
+// rows_kernel: one warp per (row, query head), for the other sizes.  Lane t of a step of
 // 32 keys computes one key's whole score from its row of codes; the warp takes
 // the running maximum and sum, then every lane accumulates its D / 32 head
 // dims over the 32 keys.  The block's K scale multiplies the score, its V scale
 // the softmax weight; the sum of the softmax is over the unscaled weights.
-#include "pa_common.cuh"
+#include <stddef.h>
+
+#include "pa_tc.cuh"
 
 namespace pa {
 namespace {
@@ -131,6 +155,463 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const Params p) {
   for (int d = 0; d < DPL; ++d) orow[d] = __float2bfloat16_rn(o[d] * inv);
 }
 
+
+// ------------------------------------------------------------------ tile_kernel
+
+constexpr int kTileThreads = 256;      // 4 softmax, 1 K, 2 V, 1 MMA warps
+constexpr int kRows = 128;
+constexpr int kKT = 64;                // keys per tile
+constexpr uint32_t kQHalf = 16384;     // 128 rows x 64 columns of 16 bits
+constexpr uint32_t kKVHalf = 8192;     // 64 keys x 64 columns of 16 bits
+constexpr uint32_t kOffQ = 0;
+constexpr uint32_t kOffK = 32768;      // 2 stages x 2 halves
+constexpr uint32_t kOffV = 65536;
+constexpr uint32_t kOffBar = 98304;
+constexpr uint32_t kTileSmem = kOffBar + 512 + 1024;   // + alignment slack
+constexpr float kRescaleThreshold = 8.0f;              // log2 units
+constexpr uint32_t kTmemCols = 256;    // S (and P) at columns 0 and 64, O at 128
+constexpr uint32_t kColO = 128;
+
+struct Bars {
+  uint64_t q, qf, full_k[2], full_v[2], empty_k[2], empty_v[2], s[2], p[2], pv[2], drain;
+  // K scale of every 4 keys (block sizes are multiples of 4) of tile t in slot
+  // t & 3: K of tile t+2 and t+3 may be written while the softmax reads t's
+  // (their stages free up with S_t and S_{t+1}), t+4's only after P_t
+  alignas(16) float kscl[4][kKT / 4];
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(Bars) <= 512 && offsetof(Bars, kscl) % 16 == 0, "barrier block");
+
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (*abort_flag) return false;
+  if (mbar_wait(bar, parity)) return true;
+  atomicOr(&g_status_prefill_fp8, PA_DEV_TIMEOUT);
+  *abort_flag = 1;
+  return false;
+}
+__device__ __forceinline__ float ex2_f32(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// K (one warp) or V (two warps): the codes of each key tile, read a tile ahead
+// into registers, written as 16-bit rows.  Thread x holds the 16-code chunk
+// x % 8 of rows x / 8 + (threads / 8) i.
+template <bool K>
+__device__ __forceinline__ void convert_tiles(const Params& p, Bars* bars, unsigned char* smem, int b, int kvh, int kend,
+                                              int nt, int x) {
+  constexpr int N = K ? 16 : 8, RS = kKT / N;     // rows a thread holds, and their distance
+  volatile int* abort_flag = &bars->abort;
+  const int ch = x & 7, r0 = x >> 3;
+  const float* scales = (K ? p.k_scale : p.v_scale) + kvh;
+  const int32_t* tab = p.block_tables + (size_t)b * p.max_blocks;
+  const size_t tok = (size_t)p.Hkv * 128;
+  const uint8_t* base = (K ? p.k : p.v) + (size_t)kvh * 128 + ch * 16;
+  uint64_t* full = K ? bars->full_k : bars->full_v;
+  uint64_t* empty = K ? bars->empty_k : bars->empty_v;
+  // codes 16 ch .. 16 ch + 15 are columns of half ch / 4, 16-byte chunks 2 (ch % 4) and the next
+  unsigned char* tile = smem + (K ? kOffK : kOffV) + (ch >> 2) * kKVHalf;
+  const int c0 = (ch & 3) * 2;
+  const int bsh = 31 - __clz(p.bs);
+  const int lane = (int)(threadIdx.x & 31), nbt = kKT >> bsh;   // blocks per tile, a lane each: at most 16
+  // lane l: the block id and scale of the tile's block l (0 where the tile has none that counts)
+  auto block_of = [&](int t) -> int {
+    const int key = t * kKT + (lane << bsh);
+    return lane < nbt && key < kend ? __ldg(&tab[key >> bsh]) : 0;
+  };
+  auto checked = [&](int blk) -> int {
+    if ((unsigned)blk < (unsigned)p.num_blocks) return blk;
+    if (K) atomicOr(&g_status_prefill_fp8, PA_DEV_BAD_BLOCK);
+    return 0;
+  };
+  auto scale_of = [&](int blk) -> float { return lane < nbt ? __ldg(&scales[(size_t)blk * p.scale_row]) : 0.f; };
+  // (keys past the context read block 0: no branch, and their codes are not used)
+  auto load = [&](int r, int blk) -> uint4 {
+    return ld_nc_v4(base + (((size_t)blk << bsh) + (r & (p.bs - 1))) * tok);
+  };
+  uint4 c[N];
+  // blk, scl: of the tile after the one in c; cur: scales of the one in c
+  int blk = 0;
+  float cur = 0.f, scl = 0.f;
+  if (nt > 0) {
+    blk = checked(block_of(0));
+    cur = scale_of(blk);
+#pragma unroll
+    for (int i = 0; i < N; ++i) c[i] = load(r0 + RS * i, __shfl_sync(0xffffffffu, blk, (r0 + RS * i) >> bsh));
+    blk = checked(block_of(1));
+    scl = scale_of(blk);
+  }
+  for (int t = 0; t < nt; ++t) {
+    const int st = t & 1;
+    const bool ok = wait_or_abort(&empty[st], ((uint32_t)(t >> 1) & 1u) ^ 1u, abort_flag);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    unsigned char* dst = tile + st * 2 * kKVHalf;
+    const int after = block_of(t + 2);             // (its answer is not needed before the tile is written)
+    // Half of the rows are converted, then that half's rows of the next tile are
+    // requested in one go, and so for the other half: a wait for one half's
+    // data never covers loads issued since for the other.
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = r0 + RS * i;
+      const float si = __shfl_sync(0xffffffffu, cur, r >> bsh);
+      const float sc = t * kKT + r < kend ? si : 0.f;
+      const bool none = sc == 0.f;
+      const uint32_t w[4] = {none ? 0u : c[i].x, none ? 0u : c[i].y, none ? 0u : c[i].z, none ? 0u : c[i].w};
+      uint32_t o[8];
+      if constexpr (K) {
+        // scale 0: a row of zeros, and the score takes scale 1
+#pragma unroll
+        for (int k = 0; k < 4; ++k) e4m3x4_to_f16x2x2(w[k], o[2 * k], o[2 * k + 1]);
+        if (ch == 0 && (r & 3) == 0) bars->kscl[t & 3][r >> 2] = none ? 1.f : sc;
+      } else {
+        const uint64_t s2 = f2pack(sc, sc);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t h[2];
+          e4m3x4_to_f16x2x2(w[k], h[0], h[1]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float a, d;
+            f16x2_to_float2(h[e], a, d);
+            f2unpack(fmul2(f2pack(a, d), s2), a, d);
+            const __nv_bfloat162 pk = __floats2bfloat162_rn(a, d);
+            o[2 * k + e] = *reinterpret_cast<const uint32_t*>(&pk);
+          }
+        }
+      }
+      *reinterpret_cast<uint4*>(dst + r * 128 + ((c0 ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(dst + r * 128 + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+      if (i == N / 2 - 1 || i == N - 1) {
+        uint32_t at[N / 2];
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k)
+          at[k] = (uint32_t)__shfl_sync(0xffffffffu, blk, (r0 + RS * (i - (N / 2 - 1) + k)) >> bsh);
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k)
+          c[i - (N / 2 - 1) + k] = load(r0 + RS * (i - (N / 2 - 1) + k), (int)at[k]);
+      }
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(&full[st]);
+    cur = scl;
+    blk = checked(after);
+    scl = scale_of(blk);
+  }
+}
+
+__global__ void __launch_bounds__(kTileThreads, 2)
+tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapO, const Params p,
+            const int QP) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  Bars* bars = reinterpret_cast<Bars*>(smem + kOffBar);
+  volatile int* abort_flag = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- work item: sequence b's tiles are units U_b = floor(query_start[b] / QP) + b
+  // and on; n rows make at most floor(n / QP) + 1 tiles, which never passes U_{b+1}
+  const int kvh = (int)(blockIdx.x % p.Hkv);
+  const int u = (int)(blockIdx.x / p.Hkv);
+  if (blockIdx.x == 0) {
+    for (int i = (int)threadIdx.x; i < p.B; i += kTileThreads) {
+      const int Li = __ldg(&p.context_lens[i]);
+      if (!good_rows(p, i) || Li < 0 || Li > p.max_blocks * p.bs) atomicOr(&g_status_prefill_fp8, PA_DEV_BAD_LEN);
+    }
+  }
+  int lo = 0, hi = p.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(&p.query_start[mid]) / QP + mid <= u) lo = mid;
+    else hi = mid - 1;
+  }
+  const int b = lo;
+  if (!good_rows(p, b)) return;
+  const int qrow0 = __ldg(&p.query_start[b]);
+  const int nq = __ldg(&p.query_start[b + 1]) - qrow0;
+  const int ti = u - (qrow0 / QP + b);
+  const int ntiles = (nq + QP - 1) / QP;
+  if (ti < 0 || ti >= ntiles) return;              // nothing allocated yet
+  const int q0 = (ntiles - 1 - ti) * QP;           // the longest tile first
+  int L = __ldg(&p.context_lens[b]);
+  L = L < 0 ? 0 : min(L, p.max_blocks * p.bs);
+  const int pos0 = L - nq + q0;
+  const int kend = min(L, pos0 + QP);
+  const int nt = kend > 0 ? (kend + kKT - 1) / kKT : 0;
+
+  if (threadIdx.x == 224) {
+    mbar_init(&bars->q, 1);
+    mbar_init(&bars->qf, 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->full_k[i], 32);
+      mbar_init(&bars->full_v[i], 64);
+      mbar_init(&bars->empty_k[i], 1);
+      mbar_init(&bars->empty_v[i], 1);
+      mbar_init(&bars->s[i], 1);
+      mbar_init(&bars->p[i], 128);
+      mbar_init(&bars->pv[i], 1);
+    }
+    mbar_init(&bars->drain, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+    if (nt > 0) {
+      prefetch_tensormap(&mapQ);
+      mbar_arrive_expect_tx(&bars->q, 2u * 128u * (uint32_t)(p.G * QP));
+      const uint64_t pol = policy_evict_first();
+      tma_load_4d(smem + kOffQ, &mapQ, &bars->q, 0, kvh * p.G, qrow0 + q0, 0, pol);
+      tma_load_4d(smem + kOffQ + kQHalf, &mapQ, &bars->q, 64, kvh * p.G, qrow0 + q0, 0, pol);
+    }
+  }
+  __syncwarp();
+  if (warp == 7) {
+    tmem_alloc(&bars->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  const uint32_t tO = tmem + kColO;
+
+  if (warp == 4) {
+    convert_tiles<true>(p, bars, smem, b, kvh, kend, nt, lane);
+  } else if (warp == 5 || warp == 6) {
+    convert_tiles<false>(p, bars, smem, b, kvh, kend, nt, (int)threadIdx.x - 160);
+  } else if (warp == 7) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0 && nt > 0) {
+      // S: f16 x f16; P V: bf16 x bf16 (V MN-major)
+      constexpr uint32_t idS = idesc_f16_f32(kRows, kKT);
+      constexpr uint32_t idO = idesc_bf16_f32(kRows, 128, false, true);
+      auto issue_s = [&](int j) {
+        const uint32_t kb = sbase + kOffK + (j & 1) * 2 * kKVHalf;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          umma_bf16(tmem + (j & 1) * kKT,
+                    sdesc_sw128(sbase + kOffQ + (uint32_t)(kk >> 2) * kQHalf + (uint32_t)(kk & 3) * 32u, 16, 1024),
+                    sdesc_sw128(kb + (uint32_t)(kk >> 2) * kKVHalf + (uint32_t)(kk & 3) * 32u, 16, 1024), idS,
+                    kk > 0 ? 1u : 0u);
+        }
+        umma_commit(&bars->s[j & 1]);
+        umma_commit(&bars->empty_k[j & 1]);
+      };
+      if (wait_or_abort(&bars->qf, 0, abort_flag) && wait_or_abort(&bars->full_k[0], 0, abort_flag)) {
+        tc_fence_after();
+        issue_s(0);
+        for (int j = 0; j < nt; ++j) {
+          const int st = j & 1;
+          const uint32_t ph = (uint32_t)(j >> 1) & 1u;
+          if (j + 1 < nt) {
+            if (!wait_or_abort(&bars->full_k[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u, abort_flag)) break;
+            tc_fence_after();
+            issue_s(j + 1);
+          }
+          if (!wait_or_abort(&bars->p[st], ph, abort_flag)) break;
+          if (!wait_or_abort(&bars->full_v[st], ph, abort_flag)) break;
+          tc_fence_after();
+          const uint32_t vb = sbase + kOffV + st * 2 * kKVHalf;
+#pragma unroll
+          for (int kk = 0; kk < kKT / 16; ++kk)
+            umma_bf16_ts(tO, tmem + st * kKT + kk * 8, sdesc_sw128(vb + (uint32_t)kk * 2048u, kKVHalf, 1024), idO,
+                         (j > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&bars->pv[st]);
+          umma_commit(&bars->empty_v[st]);
+        }
+      }
+      // every MMA issued so far has completed before TMEM is freed, and Q has landed
+      umma_commit(&bars->drain);
+      mbar_wait(&bars->drain, 0);
+      mbar_wait(&bars->q, 0);
+    }
+  } else {
+    // ---------------------------------------------------------- softmax + epilogue
+    const int r = warp * 32 + lane;                // tile row and TMEM lane
+    const int qi = r / p.G, hh = r % p.G;
+    const int pos = pos0 + qi;
+    const bool row_out = qi < QP && (q0 + qi) < nq;
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    float rowf = 0.f;                              // scale * log2(e) / the row's power of two
+    bool live = true;
+    if (nt > 0) {
+      // this thread's row of Q: bf16 -> f16 in place, zeros for rows that are not the sequence's
+      live = __all_sync(0xffffffffu, wait_or_abort(&bars->q, 0, abort_flag));
+      uint4 qv[16];
+      float mx = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        qv[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (live && row_out)
+          qv[i] = *reinterpret_cast<const uint4*>(smem + kOffQ + (i >> 3) * kQHalf + r * 128 + (((i & 7) ^ (r & 7)) << 4));
+        float f[8];
+        Elem<__nv_bfloat16>::unpack(qv[i], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(f[e]));
+      }
+      // 2^qe >= max / 2^15
+      const int qe = mx > 0.f && mx < INFINITY ? max(-110, min(110, ilogbf(mx) - 14)) : 0;
+      const float down = __uint_as_float((uint32_t)(127 - qe) << 23);
+      rowf = p.qscale * __uint_as_float((uint32_t)(127 + qe) << 23);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float f[8];
+        Elem<__nv_bfloat16>::unpack(qv[i], f);
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __half2 h2 = __floats2half2_rn(f[2 * e] * down, f[2 * e + 1] * down);
+          w[e] = *reinterpret_cast<const uint32_t*>(&h2);
+        }
+        if (live)
+          *reinterpret_cast<uint4*>(smem + kOffQ + (i >> 3) * kQHalf + r * 128 + (((i & 7) ^ (r & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      fence_proxy_async_smem();
+      if (live) mbar_arrive(&bars->qf);
+    }
+    float m_ref = -INFINITY, lsum = 0.f;
+    for (int j = 0; j < nt && live; ++j) {
+      const int st = j & 1;
+      const uint32_t ph = (uint32_t)(j >> 1) & 1u;
+      const int k0 = j * kKT;
+      bool ok = wait_or_abort(&bars->s[st], ph, abort_flag);   // (K's scales were there before S was issued)
+      if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
+      tc_fence_after();
+      uint32_t v[2][32];
+      tmem_ld32(tmem + st * kKT + lane_off, v[0]);
+      tmem_ld32(tmem + st * kKT + 32 + lane_off, v[1]);
+      const float4* ks4 = reinterpret_cast<const float4*>(bars->kscl[j & 3]);   // 16 keys' scales each
+      tmem_ld_wait();
+      if (k0 + kKT - 1 > pos) {
+#pragma unroll
+        for (int c = 0; c < kKT; ++c)
+          if (k0 + c > pos) v[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {                // 16 keys a step
+        const float4 k4 = ks4[i];
+        const float f[4] = {k4.x, k4.y, k4.z, k4.w};
+        float a[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const uint32_t* x = &v[i >> 1][(i & 1) * 16 + 4 * g];
+          a[g] = f[g] * fmax3(fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])), __uint_as_float(x[2]),
+                              __uint_as_float(x[3]));
+        }
+        mx = fmax3(fmax3(mx, a[0], a[1]), a[2], a[3]);
+      }
+      mx *= rowf;
+      const bool need = mx > m_ref + kRescaleThreshold;
+      const float alpha = need ? exp2f(m_ref - mx) : 1.f;
+      if (need) m_ref = mx;
+      if (j > 0 && __any_sync(0xffffffffu, need)) {
+        ok = wait_or_abort(&bars->pv[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t w[16];
+          tmem_ld16(tO + lane_off + c * 16, w);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+          tmem_st16(tO + lane_off + c * 16, w);
+        }
+        tmem_st_wait();
+      }
+      lsum *= alpha;
+      const float negm = m_ref == -INFINITY ? 0.f : -m_ref;
+      const uint64_t nm2 = f2pack(negm, negm);
+      uint64_t ls2[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ls2[i] = f2pack(0.f, 0.f);
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t pw[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float4 k4 = ks4[hf * 2 + (c >> 3)];
+          const int g = (c >> 1) & 3;
+          const float f = rowf * (g == 0 ? k4.x : g == 1 ? k4.y : g == 2 ? k4.z : k4.w);
+          float x0, x1;
+          f2unpack(ffma2(f2pack(__uint_as_float(v[hf][2 * c]), __uint_as_float(v[hf][2 * c + 1])), f2pack(f, f), nm2),
+                   x0, x1);
+          const float p0 = ex2_f32(x0), p1 = ex2_f32(x1);
+          const __nv_bfloat162 pk = __floats2bfloat162_rn(p0, p1);
+          ls2[c & 3] = fadd2(ls2[c & 3], f2pack(p0, p1));
+          pw[c] = *reinterpret_cast<const uint32_t*>(&pk);
+        }
+        tmem_st16(tmem + st * kKT + hf * 16 + lane_off, pw);
+      }
+      float ls8[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f2unpack(ls2[i], ls8[2 * i], ls8[2 * i + 1]);
+      lsum += ((ls8[0] + ls8[1]) + (ls8[2] + ls8[3])) + ((ls8[4] + ls8[5]) + (ls8[6] + ls8[7]));
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&bars->p[st]);
+    }
+
+    bool have = nt > 0 && live;
+    if (have) {
+      const bool ok = wait_or_abort(&bars->pv[(nt - 1) & 1], (uint32_t)((nt - 1) >> 1) & 1u, abort_flag);
+      have = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    }
+    const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+    const bool full = nt > 0 && q0 + QP <= nq;
+    unsigned char* orow = static_cast<unsigned char*>(p.out) +
+                          (((size_t)qrow0 + q0 + qi) * p.Hq + (size_t)kvh * p.G + hh) * 256;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t v[32];
+      if (have) {
+        tmem_ld32(tO + lane_off + c * 32, v);
+        tmem_ld_wait();
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float a0 = have ? __uint_as_float(v[g * 8 + 2 * e]) * inv : 0.f;
+          const float a1 = have ? __uint_as_float(v[g * 8 + 2 * e + 1]) * inv : 0.f;
+          const __nv_bfloat162 pk = __floats2bfloat162_rn(a0, a1);
+          w[e] = *reinterpret_cast<const uint32_t*>(&pk);
+        }
+        const int ch = c * 4 + g;
+        if (full) {
+          // staged in the Q buffer (free: S_{nt-1} completed before P_{nt-1} V_{nt-1}) for two TMA stores
+          *reinterpret_cast<uint4*>(smem + kOffQ + (ch >> 3) * kQHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        } else if (row_out) {
+          st_v4(orow + ch * 16, make_uint4(w[0], w[1], w[2], w[3]));
+        }
+      }
+    }
+    if (full) {
+      fence_proxy_async_smem();
+      named_sync(1, 128);
+      if (warp == 0 && lane == 0) {
+        tma_store_4d(&mapO, smem + kOffQ, 0, kvh * p.G, qrow0 + q0, 0);
+        tma_store_4d(&mapO, smem + kOffQ + kQHalf, 64, kvh * p.G, qrow0 + q0, 0);
+        bulk_commit();
+        bulk_wait_all();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 7) tmem_dealloc(tmem, kTmemCols);
+}
+
 }  // namespace
 
 unsigned fetch_status_prefill_fp8_blocks() {
@@ -185,6 +666,30 @@ extern "C" int pa_prefill_fp8_blocks(void* out, const void* query, const int32_t
   p.num_blocks = num_blocks;
   p.scale_row = scale_row(num_kv_heads);
   p.qscale = scale * kLog2e;
+  if (head_dim == 128 && p.G <= kRows) {
+    const int QP = kRows / p.G;
+    const long long ctas = ((long long)total_queries / QP + num_seqs) * num_kv_heads;
+    if (ctas > 0x7fffffffll) return PA_ERR_SHAPE;
+    CUtensorMap mapQ, mapO;
+    const uint64_t dims[4] = {128, (uint64_t)num_heads, (uint64_t)total_queries, 1};
+    const uint64_t str[3] = {256, (uint64_t)num_heads * 256, (uint64_t)total_queries * num_heads * 256};
+    const uint32_t box[4] = {64, (uint32_t)p.G, (uint32_t)QP, 1};
+    if (!encode_map(&mapQ, query, PA_BF16, 4, dims, str, box, true) ||
+        !encode_map(&mapO, out, PA_BF16, 4, dims, str, box, true)) {
+      note_host_error("cuTensorMapEncodeTiled failed for the query tile");
+      return PA_ERR_CUDA;
+    }
+    int dev = 0;
+    if (!ck(cudaGetDevice(&dev), "cudaGetDevice")) return PA_ERR_CUDA;
+    if (!raise_smem_limit(reinterpret_cast<const void*>(&tile_kernel), dev)) return PA_ERR_CUDA;
+    int qp = QP;
+    void* args[] = {&mapQ, &mapO, &p, &qp};
+    if (!ck(cudaLaunchKernel(reinterpret_cast<const void*>(&tile_kernel), dim3((unsigned)ctas), dim3(kTileThreads),
+                             args, kTileSmem, (cudaStream_t)stream),
+            "cudaLaunchKernel(tile_kernel)"))
+      return PA_ERR_CUDA;
+    return PA_OK;
+  }
   const dim3 grid((unsigned)total_queries, (unsigned)groups);
   if (head_dim == 128)
     rows_kernel<128><<<grid, kRowWarps * 32, 0, (cudaStream_t)stream>>>(p);
