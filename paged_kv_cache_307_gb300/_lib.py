@@ -299,41 +299,90 @@ def scale_row(num_kv_heads):
     return (num_kv_heads + 3) // 4 * 4
 
 
-def _same_device(*ts):
-    """Every tensor on one device, the current one (the one the library launches on)."""
+_KIND = {torch.float32: PA_F32, torch.bfloat16: PA_BF16, torch.uint8: PA_FP8_E4M3}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _kind(t):
+    k = _KIND.get(t.dtype)
+    if k is None:
+        raise TypeError("unsupported dtype %s" % t.dtype)
+    return k
+
+
+def _on(stream, device):
+    """The raw handle of `stream`, or of the device's current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+
+
+def _ready(*ts):
+    """The current device, which every tensor has to be on (the library launches there), contiguous."""
     for t in ts:
-        if t is not None and (not t.is_cuda or t.device.index != torch.cuda.current_device()):
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+    if not ts[0].is_cuda:
+        raise ValueError("tensors must be on the current CUDA device")
+    d = torch.cuda.current_device()
+    for t in ts:
+        if t.get_device() != d:
             raise ValueError("tensors must be on the current CUDA device")
+    return d
 
 
 def _int32(*ts):
     for t in ts:
-        if t.dtype != torch.int32:
+        if t.dtype is not torch.int32:
             raise TypeError("lengths, tables and starts are int32")
 
 
 def _table(block_tables, context_lens):
+    """(num_seqs, max_blocks)"""
     _int32(block_tables, context_lens)
-    if block_tables.dim() != 2 or context_lens.shape != block_tables.shape[:1]:
+    if block_tables.dim() != 2 or context_lens.dim() != 1 or context_lens.size(0) != block_tables.size(0):
         raise ValueError("block_tables is [num_seqs, max_blocks], context_lens [num_seqs]")
+    return block_tables.size(0), block_tables.size(1)
 
 
-def _pools(k_cache, v_cache):
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+def _pools(k_cache, v_cache, k_scale=None, v_scale=None):
+    """(num_blocks, block_size, num_kv_heads, head_dim, kind); an e4m3 pool comes with its block scales."""
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not k_cache.dtype:
         raise ValueError("k_cache and v_cache are [num_blocks, block_size, num_kv_heads, head_dim] of one type")
+    kind = _kind(k_cache)
+    if kind != PA_FP8_E4M3:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("scales belong to e4m3 pools")
+    else:
+        if k_scale is None or v_scale is None:
+            raise ValueError("a block-scaled cache needs k_scale and v_scale")
+        if k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32:
+            raise TypeError("scales are float32")
+        if k_scale.shape != (shape[0], scale_row(shape[2])) or v_scale.shape != k_scale.shape:
+            raise ValueError("scales are [num_blocks, num_kv_heads rounded up to a multiple of 4]")
+    return shape[0], shape[1], shape[2], shape[3], kind
 
 
-def _block_scales(k_cache, v_cache, k_scale, v_scale):
-    _pools(k_cache, v_cache)
-    if k_cache.dtype != torch.uint8:
+def _block_scaled(k_cache, v_cache, k_scale, v_scale):
+    sizes = _pools(k_cache, v_cache, k_scale, v_scale)
+    if sizes[4] != PA_FP8_E4M3:
         raise TypeError("a block-scaled cache holds e4m3 codes in uint8 pools")
-    if k_scale is None or v_scale is None:
-        raise ValueError("a block-scaled cache needs k_scale and v_scale")
-    want = (k_cache.shape[0], scale_row(k_cache.shape[2]))
-    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
-        raise TypeError("scales are float32")
-    if tuple(k_scale.shape) != want or tuple(v_scale.shape) != want:
-        raise ValueError("scales are [num_blocks, num_kv_heads rounded up to a multiple of 4]")
+    return sizes[:4]
+
+
+def _starts(query_start, num_seqs):
+    _int32(query_start)
+    if query_start.dim() != 1 or query_start.size(0) != num_seqs + 1:
+        raise ValueError("query_start is [num_seqs + 1]")
+
+
+def _query(q, out, head_dim):
+    """(rows, num_heads)"""
+    shape = q.shape
+    if out.shape != shape or out.dtype is not q.dtype or len(shape) != 3 or shape[2] != head_dim:
+        raise ValueError("q and out are [rows, num_heads, head_dim] of one type")
+    return shape[0], shape[1]
 
 
 def append_fp8_blocks(key, value, query_start, block_tables, context_lens, k_cache, v_cache, k_scale, v_scale,
@@ -341,34 +390,27 @@ def append_fp8_blocks(key, value, query_start, block_tables, context_lens, k_cac
     """Quantise key/value [T, Hkv, D] (bf16 or fp32), the last tokens of each
     context (sequence b's rows are query_start[b]..query_start[b+1]-1), into an
     e4m3 pool with one power-of-two scale per (block, KV head)."""
-    _contig(key, value, query_start, block_tables, context_lens, k_cache, v_cache, k_scale, v_scale)
-    _block_scales(k_cache, v_cache, k_scale, v_scale)
-    _table(block_tables, context_lens)
-    _int32(query_start)
-    NB, bs, H, D = k_cache.shape
-    B = context_lens.shape[0]
-    if tuple(query_start.shape) != (B + 1,):
-        raise ValueError("query_start is [num_seqs + 1]")
-    if key.shape != value.shape or key.dtype != value.dtype or tuple(key.shape[1:]) != (H, D):
+    NB, bs, H, D = _block_scaled(k_cache, v_cache, k_scale, v_scale)
+    B, cols = _table(block_tables, context_lens)
+    _starts(query_start, B)
+    shape = key.shape
+    if value.shape != shape or value.dtype is not key.dtype or len(shape) != 3 or shape[1] != H or shape[2] != D:
         raise ValueError("key and value are [tokens, num_kv_heads, head_dim] of one type")
-    _same_device(key, value, query_start, block_tables, context_lens, k_cache, v_cache, k_scale, v_scale)
-    _check(lib.pa_append_fp8_blocks(_ptr(key), _ptr(value), _ptr(query_start), key.shape[0], _ptr(block_tables),
-                                    block_tables.shape[1], _ptr(context_lens), B, _ptr(k_cache), _ptr(v_cache),
-                                    _ptr(k_scale), _ptr(v_scale), NB, bs, H, D, _dtype(key), _stream(stream)),
-           "pa_append_fp8_blocks")
+    kind = _kind(key)
+    dev = _ready(key, value, query_start, block_tables, context_lens, k_cache, v_cache, k_scale, v_scale)
+    _check(lib.pa_append_fp8_blocks(key.data_ptr(), value.data_ptr(), query_start.data_ptr(), shape[0],
+                                    block_tables.data_ptr(), cols, context_lens.data_ptr(), B, k_cache.data_ptr(),
+                                    v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), NB, bs, H, D, kind,
+                                    _on(stream, dev)), "pa_append_fp8_blocks")
 
 
 def copy_blocks_fp8_blocks(k_cache, v_cache, k_scale, v_scale, pairs, stream=None):
     """Copy-on-write for a block-scaled e4m3 cache: the codes, then the scale rows."""
-    _block_scales(k_cache, v_cache, k_scale, v_scale)
+    _block_scaled(k_cache, v_cache, k_scale, v_scale)
+    _ready(k_cache, v_cache, k_scale, v_scale, pairs)
     copy_blocks(k_cache, v_cache, pairs, stream)
     NB, n = k_scale.shape
     copy_blocks(k_scale.view(NB, 4, n // 4, 1), v_scale.view(NB, 4, n // 4, 1), pairs, stream)
-
-
-def _query(q, out, k_cache):
-    if out.shape != q.shape or out.dtype != q.dtype or q.dim() != 3 or q.shape[2] != k_cache.shape[3]:
-        raise ValueError("q and out are [rows, num_heads, head_dim] of one type")
 
 
 def alloc_fp8_blocks_workspace(q, k_cache, block_tables, partition_size=0):
@@ -379,21 +421,20 @@ def alloc_fp8_blocks_workspace(q, k_cache, block_tables, partition_size=0):
 def decode_fp8_blocks(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
                       partition_size=0, workspace=None, stream=None):
     """out[B,Hq,D] (bf16) = paged decode attention of q over a block-scaled e4m3 cache."""
-    _contig(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
-    _block_scales(k_cache, v_cache, k_scale, v_scale)
-    _table(block_tables, context_lens)
-    _query(q, out, k_cache)
-    B, Hq, D = q.shape
-    if B != context_lens.shape[0]:
+    NB, bs, Hkv, D = _block_scaled(k_cache, v_cache, k_scale, v_scale)
+    B, cols = _table(block_tables, context_lens)
+    rows, Hq = _query(q, out, D)
+    if rows != B:
         raise ValueError("one query row per sequence")
-    NB, bs, Hkv, _ = k_cache.shape
+    kind = _kind(q)
     if workspace is None:
         workspace = alloc_fp8_blocks_workspace(q, k_cache, block_tables, partition_size)
-    _same_device(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, workspace)
-    _check(lib.pa_decode_fp8_blocks(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                                    _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), B, Hq, Hkv, D, bs,
-                                    NB, ctypes.c_float(scale), partition_size, _ptr(workspace), workspace.numel(),
-                                    _dtype(q), _stream(stream)), "pa_decode_fp8_blocks")
+    dev = _ready(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, workspace)
+    _check(lib.pa_decode_fp8_blocks(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                    k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(), cols,
+                                    context_lens.data_ptr(), B, Hq, Hkv, D, bs, NB, scale, partition_size,
+                                    workspace.data_ptr(), workspace.nbytes, kind, _on(stream, dev)),
+           "pa_decode_fp8_blocks")
     return out
 
 
@@ -401,21 +442,16 @@ def prefill_fp8_blocks(out, q, query_start, k_cache, v_cache, k_scale, v_scale, 
                        stream=None):
     """Mixed round over a block-scaled e4m3 cache: q/out [rows, Hq, D] (bf16), sequence b's rows are
     query_start[b]..query_start[b+1]-1, the last tokens of its context, causal."""
-    _contig(out, q, query_start, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
-    _block_scales(k_cache, v_cache, k_scale, v_scale)
-    _table(block_tables, context_lens)
-    _int32(query_start)
-    _query(q, out, k_cache)
-    rows, Hq, D = q.shape
-    NB, bs, Hkv, _ = k_cache.shape
-    B = context_lens.shape[0]
-    if tuple(query_start.shape) != (B + 1,):
-        raise ValueError("query_start is [num_seqs + 1]")
-    _same_device(out, q, query_start, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
-    _check(lib.pa_prefill_fp8_blocks(_ptr(out), _ptr(q), _ptr(query_start), rows, _ptr(k_cache), _ptr(v_cache),
-                                     _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1],
-                                     _ptr(context_lens), B, Hq, Hkv, D, bs, NB, ctypes.c_float(scale), _dtype(q),
-                                     _stream(stream)), "pa_prefill_fp8_blocks")
+    NB, bs, Hkv, D = _block_scaled(k_cache, v_cache, k_scale, v_scale)
+    B, cols = _table(block_tables, context_lens)
+    _starts(query_start, B)
+    rows, Hq = _query(q, out, D)
+    kind = _kind(q)
+    dev = _ready(out, q, query_start, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens)
+    _check(lib.pa_prefill_fp8_blocks(out.data_ptr(), q.data_ptr(), query_start.data_ptr(), rows, k_cache.data_ptr(),
+                                     v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                     block_tables.data_ptr(), cols, context_lens.data_ptr(), B, Hq, Hkv, D, bs, NB,
+                                     scale, kind, _on(stream, dev)), "pa_prefill_fp8_blocks")
     return out
 
 
@@ -423,7 +459,7 @@ def alloc_weights_workspace(q, k_cache, block_tables, partition_size=0):
     """Workspace for decode_weights with these sizes."""
     B, Hq, D = q.shape
     n = lib.pa_decode_weights_workspace_bytes(B, Hq, k_cache.shape[2], D, block_tables.shape[1], k_cache.shape[1],
-                                              partition_size, _dtype(k_cache))
+                                              partition_size, _kind(k_cache))
     return torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
 
 
@@ -432,31 +468,26 @@ def decode_weights(out, weights, q, k_cache, v_cache, block_tables, context_lens
     """out[B,Hq,D] = paged decode attention of q, and weights[b,g,t] (fp32 [B, Hkv, >= max_blocks * bs]) grows by
     the softmax weights of KV head g's query heads for token t.  The pools are q's type, or a block-scaled e4m3
     cache with its scales."""
-    _contig(out, weights, q, k_cache, v_cache, block_tables, context_lens)
-    _table(block_tables, context_lens)
-    _query(q, out, k_cache)
-    fp8 = k_cache.dtype == torch.uint8
-    if fp8:
-        _block_scales(k_cache, v_cache, k_scale, v_scale)
-        _contig(k_scale, v_scale)
-    else:
-        _pools(k_cache, v_cache)
-        if k_scale is not None or v_scale is not None:
-            raise ValueError("scales belong to e4m3 pools")
-    B, Hq, D = q.shape
-    NB, bs, Hkv, _ = k_cache.shape
-    if B != context_lens.shape[0]:
+    NB, bs, Hkv, D, kv = _pools(k_cache, v_cache, k_scale, v_scale)
+    B, cols = _table(block_tables, context_lens)
+    rows, Hq = _query(q, out, D)
+    if rows != B:
         raise ValueError("one query row per sequence")
-    if weights.dtype != torch.float32 or weights.dim() != 3 or tuple(weights.shape[:2]) != (B, Hkv):
+    kind = _kind(q)
+    wshape = weights.shape
+    if weights.dtype is not torch.float32 or len(wshape) != 3 or wshape[0] != B or wshape[1] != Hkv:
         raise ValueError("weights is float32 [num_seqs, num_kv_heads, slots]")
     if workspace is None:
         workspace = alloc_weights_workspace(q, k_cache, block_tables, partition_size)
-    _same_device(out, weights, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, workspace)
-    _check(lib.pa_decode_weights(_ptr(out), _ptr(weights), weights.shape[2], _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                 _ptr(k_scale), _ptr(v_scale), _ptr(block_tables), block_tables.shape[1],
-                                 _ptr(context_lens), B, Hq, Hkv, D, bs, NB, ctypes.c_float(scale), partition_size,
-                                 _ptr(workspace), workspace.numel(), _dtype(q), _dtype(k_cache), _stream(stream)),
-           "pa_decode_weights")
+    ks = vs = None
+    if kv == PA_FP8_E4M3:
+        _ready(k_scale, v_scale)
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    dev = _ready(out, weights, q, k_cache, v_cache, block_tables, context_lens, workspace)
+    _check(lib.pa_decode_weights(out.data_ptr(), weights.data_ptr(), wshape[2], q.data_ptr(), k_cache.data_ptr(),
+                                 v_cache.data_ptr(), ks, vs, block_tables.data_ptr(), cols, context_lens.data_ptr(),
+                                 B, Hq, Hkv, D, bs, NB, scale, partition_size, workspace.data_ptr(),
+                                 workspace.nbytes, kind, kv, _on(stream, dev)), "pa_decode_weights")
     return out
 
 
@@ -472,36 +503,31 @@ def evict(k_cache, v_cache, block_tables, context_lens, kept_lens, seen_lens, we
     """Cut every (sequence, KV head) to its `budget` tokens of largest weight (protected: the first `sinks` and the
     last `recent` positions).  weights/token_pos [B, Hkv, slots] name each slot's total and position; the outputs
     may be the inputs themselves.  new_lens[b] = min(L_b, budget)."""
-    _contig(k_cache, v_cache, block_tables, context_lens, kept_lens, seen_lens, weights, token_pos, new_lens,
-            weights_out, token_pos_out)
-    _table(block_tables, context_lens)
+    NB, bs, Hkv, D, kv = _pools(k_cache, v_cache, k_scale, v_scale)
+    B, cols = _table(block_tables, context_lens)
     _int32(kept_lens, seen_lens, token_pos, new_lens, token_pos_out)
-    fp8 = k_cache.dtype == torch.uint8
-    if fp8:
-        _block_scales(k_cache, v_cache, k_scale, v_scale)
-        _contig(k_scale, v_scale)
-    else:
-        _pools(k_cache, v_cache)
-        if k_scale is not None or v_scale is not None:
-            raise ValueError("scales belong to e4m3 pools")
-    B = context_lens.shape[0]
-    NB, bs, Hkv, D = k_cache.shape
-    if kept_lens.shape != (B,) or seen_lens.shape != (B,) or new_lens.shape != (B,):
-        raise ValueError("kept_lens, seen_lens and new_lens are [num_seqs]")
-    if weights.dtype != torch.float32 or weights_out.dtype != torch.float32:
+    for t in (kept_lens, seen_lens, new_lens):
+        if t.dim() != 1 or t.size(0) != B:
+            raise ValueError("kept_lens, seen_lens and new_lens are [num_seqs]")
+    if weights.dtype is not torch.float32 or weights_out.dtype is not torch.float32:
         raise TypeError("weights are float32")
-    if weights.dim() != 3 or tuple(weights.shape[:2]) != (B, Hkv) or not (
-            weights.shape == token_pos.shape == weights_out.shape == token_pos_out.shape):
+    shape = weights.shape
+    if len(shape) != 3 or shape[0] != B or shape[1] != Hkv or not (
+            token_pos.shape == shape and weights_out.shape == shape and token_pos_out.shape == shape):
         raise ValueError("weights and token_pos are [num_seqs, num_kv_heads, slots], in and out alike")
     if workspace is None:
         workspace = alloc_evict_workspace(k_cache, block_tables, budget)
-    _same_device(k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, kept_lens, seen_lens, weights,
-                 token_pos, new_lens, weights_out, token_pos_out, workspace)
-    _check(lib.pa_evict(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
-                        block_tables.shape[1], _ptr(context_lens), _ptr(kept_lens), _ptr(seen_lens), B, _ptr(weights),
-                        _ptr(token_pos), budget, recent, sinks, _ptr(new_lens), _ptr(weights_out),
-                        _ptr(token_pos_out), weights.shape[2], NB, bs, Hkv, D, _ptr(workspace), workspace.numel(),
-                        _dtype(k_cache), _stream(stream)), "pa_evict")
+    ks = vs = None
+    if kv == PA_FP8_E4M3:
+        _ready(k_scale, v_scale)
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    dev = _ready(k_cache, v_cache, block_tables, context_lens, kept_lens, seen_lens, weights, token_pos, new_lens,
+                 weights_out, token_pos_out, workspace)
+    _check(lib.pa_evict(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, block_tables.data_ptr(), cols,
+                        context_lens.data_ptr(), kept_lens.data_ptr(), seen_lens.data_ptr(), B, weights.data_ptr(),
+                        token_pos.data_ptr(), budget, recent, sinks, new_lens.data_ptr(), weights_out.data_ptr(),
+                        token_pos_out.data_ptr(), shape[2], NB, bs, Hkv, D, workspace.data_ptr(), workspace.nbytes,
+                        kv, _on(stream, dev)), "pa_evict")
     return new_lens
 
 

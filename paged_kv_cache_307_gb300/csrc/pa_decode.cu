@@ -324,8 +324,12 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
   if (!ck(cudaGetDevice(&dev), "cudaGetDevice")) return PA_ERR_CUDA;
   CUtensorMap mapK, mapV;
   const int G = num_heads / num_kv_heads;
+  // Block-scaled pools of head_dim 128: the tcgen05 kernel, for every group size
+  // (its TMA boxes are whole 8-row swizzle atoms, so blocks of 4 stay out).
+  const bool use_tc = blk && head_dim == 128 && block_size >= 8;
   // Tensor cores over the query group when it is a real contraction (G >= 2).
-  const bool use_mma = ((kv == PA_BF16 && (head_dim == 64 || head_dim == 128)) ||
+  const bool use_mma = !blk &&
+                       ((kv == PA_BF16 && (head_dim == 64 || head_dim == 128)) ||
                         (kv == PA_FP8_E4M3 && head_dim == 128)) &&
                        G >= 2 && (G & (G - 1)) == 0 && block_size >= 8;
   // KV heads per work item: 4 on the tensor-core path (one warp per head,
@@ -342,8 +346,9 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
                  : fp8    ? fp8_heads_per_item(num_kv_heads)
                  : mha_hg ? PA_MHA_HEADS_PER_ITEM
                           : 1;
-  if (!get_map(&mapK, k_cache, kv, num_blocks, block_size, num_kv_heads, head_dim, dev, use_mma, HG) ||
-      !get_map(&mapV, v_cache, kv, num_blocks, block_size, num_kv_heads, head_dim, dev, use_mma, HG)) {
+  const bool swz = use_mma || use_tc;
+  if (!get_map(&mapK, k_cache, kv, num_blocks, block_size, num_kv_heads, head_dim, dev, swz, HG) ||
+      !get_map(&mapV, v_cache, kv, num_blocks, block_size, num_kv_heads, head_dim, dev, swz, HG)) {
     note_host_error("cuTensorMapEncodeTiled failed for the K/V pool");
     return PA_ERR_CUDA;
   }
@@ -410,9 +415,24 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
   prm.spg_shift = (spg & (spg - 1)) ? -1 : (spg == 1 ? 0 : spg == 2 ? 1 : spg == 4 ? 2 : 3);
   const int S = spg * prm.WPH;
 
-  const Launch L = wa && fp8         ? pick_decode_weights_fp8(head_dim, GT, prm.HG, use_mma)
+  void* args[] = {&mapK, &mapV, &prm};
+  Launch L;
+  if (use_tc) {
+    // one CTA per (partition, sequence, up to 16 query heads of a KV head)
+    prm.nsub = (G + 15) / 16;
+    const long long ctas = (long long)max_parts * num_seqs * prm.nsub * num_kv_heads;
+    if (ctas > 0x7fffffffll) return PA_ERR_SHAPE;
+    const int gt = (G + prm.nsub - 1) / prm.nsub;
+    size_t tc_smem = 0;
+    L = wa ? pick_decode_weights_fp8_tc(gt, &tc_smem) : pick_decode_fp8_blocks_tc(gt, &tc_smem);
+    if (!raise_smem_limit(L.kernel, dev)) return PA_ERR_CUDA;
+    if (!ck(cudaLaunchKernel(L.kernel, dim3((unsigned)ctas), dim3(192), args, tc_smem, (cudaStream_t)stream),
+            "cudaLaunchKernel(tc_decode_kernel)"))
+      return PA_ERR_CUDA;
+  } else {
+  L = wa && fp8         ? pick_decode_weights_fp8(head_dim, GT, prm.HG)
                    : wa              ? pick_decode_weights(dtype == PA_F32, head_dim, GT, prm.HG, use_mma)
-                   : blk             ? pick_decode_fp8_blocks(head_dim, GT, prm.HG, use_mma)
+                   : blk             ? pick_decode_fp8_blocks(head_dim, GT, prm.HG)
                    : fp8             ? pick_decode_fp8(head_dim, GT, prm.HG, use_mma)
                    : use_mma         ? (head_dim == 64 ? pick_mma<64>(GT, prm.HG) : pick_mma<128>(GT, prm.HG))
                    : dtype == PA_F32 ? pick1<float, float>(head_dim, GT, prm.HG)
@@ -427,7 +447,6 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
   long long grid = (long long)occ * device_sm_count();
   if (grid > prm.n_virtual) grid = prm.n_virtual;
 
-  void* args[] = {&mapK, &mapV, &prm};
   if (prm.ws_next && prm.dense) {
     // items handed out at run time from the counter in the workspace
     void* rargs[] = {&prm.ws_next};
@@ -442,6 +461,7 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
                                   (cudaStream_t)stream),
                  "cudaLaunchKernel(decode_kernel)")) {
     return PA_ERR_CUDA;
+  }
   }
   if (wa) {
     const unsigned merge_blocks =

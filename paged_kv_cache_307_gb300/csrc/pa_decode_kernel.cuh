@@ -1707,11 +1707,15 @@ struct Launch {
 // e4m3-pool instances (pa_decode_fp8.cu): bf16 queries, hg KV heads per
 // work item, tensor cores (head_dim 128, gt a power of two >= 2) or CUDA cores.
 Launch pick_decode_fp8(int head_dim, int gt, int hg, bool mma);
-// The same for pools with one scale per (block, KV head) (pa_decode_fp8_blocks.cu).
-Launch pick_decode_fp8_blocks(int head_dim, int gt, int hg, bool mma);
+// The same for pools with one scale per (block, KV head): CUDA cores, and the
+// tcgen05 kernel for gt query heads per CTA (<= 16) with its shared memory
+// (pa_decode_fp8_blocks.cu).
+Launch pick_decode_fp8_blocks(int head_dim, int gt, int hg);
+Launch pick_decode_fp8_blocks_tc(int gt, size_t* smem);
 // Weights-mode instances: pools of the query's type (pa_decode_weights.cu) and
 // block-scaled e4m3 pools (pa_decode_weights_fp8.cu).
 Launch pick_decode_weights(bool f32, int head_dim, int gt, int hg, bool mma);
-Launch pick_decode_weights_fp8(int head_dim, int gt, int hg, bool mma);
+Launch pick_decode_weights_fp8(int head_dim, int gt, int hg);
+Launch pick_decode_weights_fp8_tc(int gt, size_t* smem);
 
 }  // namespace pa

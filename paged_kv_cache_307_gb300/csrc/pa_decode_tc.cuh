@@ -1,0 +1,531 @@
+// pa_decode_tc.cuh — paged decode attention over an e4m3 pool with one scale
+// per (block, KV head) on the 5th-generation tensor cores (tcgen05.mma
+// kind::f8f6f4): the codes go from HBM to shared memory by TMA and from there
+// into the products as they are.  Shared by the translation units that
+// instantiate it (pa_decode_fp8_blocks.cu, pa_decode_weights_fp8.cu).
+//
+// What bounds decode over 8-bit pools is not the bytes but the instructions
+// that widen every code for 16-bit products (about 36 per token and KV head on
+// the mma.sync path, two instructions per cycle and SM, 60 % of the copy
+// bandwidth).  Here a tile of 128 tokens of one KV head costs eight MMAs, and
+// per token only its scores are touched by threads.
+//
+// One CTA = (sequence, partition of P tokens, KV head, up to 16 query heads):
+//   S^T[128 tokens x N] = K[128 x 128] Q^T      A = K tile (K-major), B = Q rows
+//   O^T[128 dims x N]  += V^T[128 x 128] P^T    A = V tile (MN-major), B = P rows
+// N = 2 x (8 or 16) columns: every query head has two rows, because bf16 Q (8
+// significant bits) and P do not fit one e4m3 value (4 bits):
+//   q 2^-e = hi + lo / 16, hi = e4m3(q 2^-e), lo = e4m3(16 (q 2^-e - hi)),
+// with 2^e per head so that max |q 2^-e| is in [128, 256).  The residual of hi
+// has at most 4 significant bits left, so the split is exact while
+// |q 2^-e| >= 2^-6, and off by at most 2^-14 (2^-21 of the largest) below.  P
+// likewise, 32 p (v / vref) in place of q 2^-e: 8 bits for weights down to
+// 2^-11 of the largest, an absolute 2^-19 of it below.  p is in [0, 8] relative
+// to the running reference, v / vref <= 1 is the V scale of the token's block
+// against the largest so far.  The K scale multiplies the score in fp32.
+//
+//  * warp 4 (TMA): block-table entries and scales by parallel lanes, K and V
+//    boxes {128 B, 1 head, bs rows} into 2-stage rings of 16 KB tiles; K's
+//    stage frees with its S, V's with its O.
+//  * warp 5: TMEM, and the MMAs: S_{j+1} before O += V_j P_j.
+//  * warps 0-3: one thread per token: scores from TMEM, scale, mask, p = 2^(s-m),
+//    the sum, P's two terms as bytes into the B tile.  The references (m per
+//    head, vref) are common to the 128 threads and move only when a score
+//    exceeds m by 3 (a factor 8) or a V scale exceeds vref: one barrier with a
+//    vote per tile; then O is rescaled in TMEM.
+//  * 74 KB of shared memory for up to 8 heads: three CTAs per SM, so one CTA's
+//    softmax and its start and end overlap the others' copies.
+//  * V rows past the context are zeroed in shared memory (0 * NaN).  Waits are
+//    bounded (2 s); after a timeout the softmax warps keep walking the tiles
+//    without waiting, so that their barriers stay matched.
+#pragma once
+
+#include <stddef.h>
+
+#include "pa_decode_kernel.cuh"
+#include "pa_tc.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kTcThreads = 192;
+constexpr int kTcTile = 128;               // tokens per tile
+constexpr uint32_t kTcStage = 16384;       // 128 tokens x 128 codes
+constexpr float kTcSlack = 3.f;            // log2 units a score may exceed the reference by
+constexpr float kTcPScale = 32.f;          // p in [0, 8] -> [0, 256]
+
+struct TcShared {
+  uint64_t full_k[2], full_v[2], empty_k[2], empty_v[2], s[2], p[2], pv[2], scl_full[4], qf, drain;
+  // scales of the 128 / bs blocks of tile j in slot j & 3: tile j+2's and j+3's
+  // may be written while the softmax works on j, j+4's only after P_j
+  alignas(16) float scl[4][2][16];
+  alignas(16) float mx[4][16];             // per warp: tile maximum of every head; at the end, sums
+  float vmx[4];
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int NH>
+constexpr uint32_t tc_smem_bytes() {
+  return 4 * kTcStage + 3u * (2u * NH * 128u) + (uint32_t)sizeof(TcShared) + 1024u;
+}
+
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+// kind::f8f6f4, e4m3 operands (format 0), fp32 accumulation.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn_major) {
+  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// Two floats as e4m3 codes (a in the low byte), saturating, and back.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ void from_e4m3x2(uint32_t c, float& a, float& b) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 x;\n\tcvt.u16.u32 x, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(h) : "r"(c));
+  f16x2_to_float2(h, a, b);
+}
+__device__ __forceinline__ void sts_u8(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// Barrier 2 of the 128 softmax threads, true for all if true for any.
+__device__ __forceinline__ bool vote128(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r) : "r"(x ? 1u : 0u) : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+  return x;
+}
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (*abort_flag) return false;
+  if (mbar_wait(bar, parity)) return true;
+  atomicOr(&g_status_decode, PA_DEV_TIMEOUT);
+  *abort_flag = 1;
+  return false;
+}
+// Byte x of row n of a 128-byte-swizzled tile.
+__device__ __forceinline__ uint32_t swz_byte(int n, int x) {
+  return (uint32_t)(n * 128 + (((x >> 4) ^ (n & 7)) << 4) + (x & 15));
+}
+
+// GT: query heads of the CTA, rounded up (1, 2, 4, 8, 16); W: weights mode.
+// p.nsub CTAs share a KV head's G query heads, hs = ceil(G / nsub) each.
+template <int GT, bool W>
+__global__ void __launch_bounds__(kTcThreads, GT <= 8 ? 3 : 2)
+tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                 const DecodeParams p) {
+  constexpr int D = 128;
+  constexpr int NH = GT <= 8 ? 8 : 16;          // heads' rows of one term
+  constexpr int N = 2 * NH;
+  constexpr uint32_t kTmem = N == 16 ? 64u : 128u;   // S_0, S_1, O: N columns each
+  constexpr uint32_t kOffV = 2 * kTcStage, kOffQ = 4 * kTcStage, kOffP = kOffQ + N * 128;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  TcShared* sh = reinterpret_cast<TcShared*>(smem + kOffP + 2 * N * 128);
+  volatile int* abort_flag = &sh->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  // ---- item: KV heads innermost (neighbouring CTAs read neighbouring rows of the same blocks),
+  // partitions outermost (the CTAs without work, past the shorter contexts, come last)
+  int u = (int)blockIdx.x;
+  const int kvh = u % p.Hkv;
+  u /= p.Hkv;
+  const int sub = u % p.nsub;
+  u /= p.nsub;
+  const int b = u % p.B, part = u / p.B;
+  const int Lmax = p.max_blocks * p.bs;
+  const int L0 = __ldg(&p.context_lens[b]);
+  const int L = L0 < 0 ? 0 : min(L0, Lmax);
+  if (part == 0 && kvh == 0 && sub == 0 && threadIdx.x == 0 && L != L0) atomicOr(&g_status_decode, PA_DEV_BAD_LEN);
+  const int nparts = L > 0 ? (L + p.part_tokens - 1) / p.part_tokens : 1;
+  if (part >= nparts) return;                   // nothing allocated yet
+  const int hs = (p.G + p.nsub - 1) / p.nsub;
+  const int h0 = kvh * p.G + sub * hs;          // first query head
+  const int gh = min(hs, p.G - sub * hs);       // query heads of this CTA, <= GT
+  const int t0 = part * p.part_tokens, t1 = min(L, t0 + p.part_tokens);
+  const int nt = (t1 - t0 + kTcTile - 1) / kTcTile;
+  const int bsh = 31 - __clz(p.bs);
+
+  if (threadIdx.x == 160) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->full_k[i], 1);
+      mbar_init(&sh->full_v[i], 1);
+      mbar_init(&sh->empty_k[i], 1);
+      mbar_init(&sh->empty_v[i], 1);
+      mbar_init(&sh->s[i], 1);
+      mbar_init(&sh->p[i], 128);
+      mbar_init(&sh->pv[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&sh->scl_full[i], 1);
+    mbar_init(&sh->qf, 128);
+    mbar_init(&sh->drain, 1);
+    sh->abort = 0;
+    fence_mbar_init();
+  }
+  __syncwarp();
+  if (warp == 5) {
+    tmem_alloc(&sh->tmem_base, kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+  const uint32_t tO = tmem + 2 * N;
+
+  if (warp == 4) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      prefetch_tensormap(&mapK);
+      prefetch_tensormap(&mapV);
+    }
+    const uint64_t pol = policy_evict_first();
+    const int32_t* row = p.block_tables + (size_t)b * p.max_blocks;
+    const uint32_t box = (uint32_t)p.bs * 128u;
+    // lane i: block i of a tile (at most 16), its id and scales
+    auto fetch = [&](int j, int& blk, float& ks, float& vs) {
+      const int t = t0 + j * kTcTile + (lane << bsh);
+      blk = 0;
+      ks = vs = 0.f;
+      if (j < nt && lane < (kTcTile >> bsh) && t < t1) {
+        blk = __ldg(&row[t >> bsh]);
+        if ((unsigned)blk >= (unsigned)p.num_blocks) {
+          atomicOr(&g_status_decode, PA_DEV_BAD_BLOCK);
+          blk = 0;                              // keep every copy inside the pool
+        }
+        ks = __ldg(&p.k_scale[(size_t)blk * p.scale_row + kvh]);
+        vs = __ldg(&p.v_scale[(size_t)blk * p.scale_row + kvh]);
+      }
+    };
+    int blk;
+    float ks, vs;
+    fetch(0, blk, ks, vs);
+    int issued_k = 0, issued_v = 0;
+    for (int j = 0; j < nt; ++j) {
+      const int st = j & 1;
+      const uint32_t ph = ((uint32_t)(j >> 1) & 1u) ^ 1u;
+      const int nb = (min(kTcTile, t1 - t0 - j * kTcTile) + p.bs - 1) >> bsh;
+      bool ok = true;
+      if (lane == 0) ok = tc_wait(&sh->empty_k[st], ph, abort_flag);
+      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
+      if (lane < 16) {
+        sh->scl[j & 3][0][lane] = ks;
+        sh->scl[j & 3][1][lane] = vs;
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sh->scl_full[j & 3]);
+        mbar_arrive_expect_tx(&sh->full_k[st], (uint32_t)nb * box);
+      }
+      __syncwarp();
+      if (lane < nb)
+        tma_load_4d(smem + st * kTcStage + lane * box, &mapK, &sh->full_k[st], 0, kvh, 0, blk, pol);
+      issued_k = j + 1;
+      if (lane == 0) ok = tc_wait(&sh->empty_v[st], ph, abort_flag);
+      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
+      if (lane == 0) mbar_arrive_expect_tx(&sh->full_v[st], (uint32_t)nb * box);
+      __syncwarp();
+      if (lane < nb)
+        tma_load_4d(smem + kOffV + st * kTcStage + lane * box, &mapV, &sh->full_v[st], 0, kvh, 0, blk, pol);
+      issued_v = j + 1;
+      fetch(j + 1, blk, ks, vs);
+    }
+    // no TMA write may land after the CTA has left
+    if (lane == 0) {
+      for (int j = max(0, issued_k - 2); j < issued_k; ++j) mbar_wait(&sh->full_k[j & 1], (uint32_t)(j >> 1) & 1u);
+      for (int j = max(0, issued_v - 2); j < issued_v; ++j) mbar_wait(&sh->full_v[j & 1], (uint32_t)(j >> 1) & 1u);
+    }
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && nt > 0) {
+      constexpr uint32_t idS = idesc_e4m3_f32(kTcTile, N, false);
+      constexpr uint32_t idO = idesc_e4m3_f32(D, N, true);
+      auto issue_s = [&](int j) {
+        const uint32_t kb = sbase + (uint32_t)(j & 1) * kTcStage;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)           // 32 head dims each
+          umma_f8(tmem + (j & 1) * N, sdesc_sw128(kb + kk * 32u, 16, 1024),
+                  sdesc_sw128(sbase + kOffQ + kk * 32u, 16, 1024), idS, kk > 0 ? 1u : 0u);
+        umma_commit(&sh->s[j & 1]);
+        umma_commit(&sh->empty_k[j & 1]);
+      };
+      if (tc_wait(&sh->qf, 0, abort_flag) && tc_wait(&sh->full_k[0], 0, abort_flag)) {
+        tc_fence_after();
+        issue_s(0);
+        for (int j = 0; j < nt; ++j) {
+          const int st = j & 1;
+          const uint32_t ph = (uint32_t)(j >> 1) & 1u;
+          if (j + 1 < nt) {
+            if (!tc_wait(&sh->full_k[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u, abort_flag)) break;
+            tc_fence_after();
+            issue_s(j + 1);
+          }
+          if (!tc_wait(&sh->p[st], ph, abort_flag)) break;
+          if (!tc_wait(&sh->full_v[st], ph, abort_flag)) break;
+          tc_fence_after();
+          const uint32_t vb = sbase + kOffV + (uint32_t)st * kTcStage;
+          const uint32_t pb = sbase + kOffP + (uint32_t)st * (N * 128);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)         // 32 tokens each: four 8-token groups of 1024 bytes
+            umma_f8(tO, sdesc_sw128(vb + kk * 4096u, kTcStage, 1024), sdesc_sw128(pb + kk * 32u, 16, 1024), idO,
+                    (j > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&sh->pv[st]);
+          umma_commit(&sh->empty_v[st]);
+        }
+      }
+      umma_commit(&sh->drain);                   // every MMA has completed before TMEM is freed
+      mbar_wait(&sh->drain, 0);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int r = (int)threadIdx.x;              // token of the tile, head dim at either end; TMEM lane
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    float qf[GT];                                // scale * log2(e) * 2^e of every head
+    {
+      float q[GT];
+      const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q) + ((size_t)b * p.Hq + h0) * D + r;
+#pragma unroll
+      for (int h = 0; h < GT; ++h) {
+        q[h] = __bfloat162float(qp[(size_t)min(h, gh - 1) * D]);
+        const float m = warp_max(fabsf(q[h]));
+        if (lane == 0) sh->mx[warp][h] = m;
+      }
+      named_sync(1, 128);
+#pragma unroll
+      for (int h = 0; h < GT; ++h) {
+        const float m = fmaxf(fmaxf(sh->mx[0][h], sh->mx[1][h]), fmaxf(sh->mx[2][h], sh->mx[3][h]));
+        const int e = m > 0.f && m < INFINITY ? max(-110, min(110, ilogbf(m) - 7)) : 0;
+        // (an infinite query has no answer: NaN, as its scores would be)
+        const float x = m < INFINITY ? q[h] * __uint_as_float((uint32_t)(127 - e) << 23) : NAN;
+        qf[h] = p.qscale * __uint_as_float((uint32_t)(127 + e) << 23);
+        const uint32_t hi = e4m3x2(x, 0.f);
+        float back, none;
+        from_e4m3x2(hi, back, none);
+        const uint32_t lo = e4m3x2((x - back) * 16.f, 0.f);
+        sts_u8(sbase + kOffQ + swz_byte(h, r), hi);
+        sts_u8(sbase + kOffQ + swz_byte(NH + h, r), lo);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&sh->qf);
+      named_sync(1, 128);                        // mx is written again below
+    }
+    float m[GT], l[GT];
+#pragma unroll
+    for (int h = 0; h < GT; ++h) {
+      m[h] = -INFINITY;
+      l[h] = 0.f;
+    }
+    float vref = 0.f;                            // 0: none yet
+
+    for (int j = 0; j < nt; ++j) {
+      const int st = j & 1;
+      const uint32_t ph = (uint32_t)(j >> 1) & 1u;
+      const int t = t0 + j * kTcTile + r;
+      const bool ok = t < t1;
+      tc_wait(&sh->scl_full[j & 3], (uint32_t)(j >> 2) & 1u, abort_flag);
+      const float ks = sh->scl[j & 3][0][r >> bsh], vs = ok ? sh->scl[j & 3][1][r >> bsh] : 0.f;
+      __syncwarp();
+      tc_wait(&sh->s[st], ph, abort_flag);
+      __syncwarp();
+      tc_fence_after();
+      float s[GT];
+      {
+        uint32_t hi[NH], lo[NH];
+        if constexpr (NH == 8) {
+          uint32_t v[16];
+          tmem_ld16(tmem + st * N + lane_off, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int h = 0; h < 8; ++h) {
+            hi[h] = v[h];
+            lo[h] = v[8 + h];
+          }
+        } else {
+          uint32_t v[32];
+          tmem_ld32(tmem + st * N + lane_off, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int h = 0; h < 16; ++h) {
+            hi[h] = v[h];
+            lo[h] = v[16 + h];
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < GT; ++h)
+          s[h] = ok ? fmaf(__uint_as_float(lo[h]), 0.0625f, __uint_as_float(hi[h])) * (qf[h] * ks) : -INFINITY;
+      }
+      if constexpr (W) {
+        if (ok) {
+          float* sp = p.ws_s + ((size_t)b * p.Hq + h0) * (size_t)Lmax + t;
+#pragma unroll
+          for (int h = 0; h < GT; ++h)
+            if (h < gh) sp[(size_t)h * Lmax] = s[h];
+        }
+      }
+      bool need = vs > vref;
+#pragma unroll
+      for (int h = 0; h < GT; ++h) need = need || s[h] > m[h] + kTcSlack;
+      __syncwarp();
+      if (vote128(need)) {
+        // new references: the tile's maxima where they are above
+#pragma unroll
+        for (int h = 0; h < GT; ++h) {
+          const float x = warp_max(s[h]);
+          if (lane == 0) sh->mx[warp][h] = x;
+        }
+        const float xv = warp_max(vs);
+        if (lane == 0) sh->vmx[warp] = xv;
+        named_sync(1, 128);
+        const float vnew = fmaxf(vref, fmaxf(fmaxf(sh->vmx[0], sh->vmx[1]), fmaxf(sh->vmx[2], sh->vmx[3])));
+        const float fv = vref > 0.f ? vref / vnew : 0.f;
+        vref = vnew;
+        float f[GT];
+#pragma unroll
+        for (int h = 0; h < GT; ++h) {
+          const float x = fmaxf(fmaxf(sh->mx[0][h], sh->mx[1][h]), fmaxf(sh->mx[2][h], sh->mx[3][h]));
+          const float mn = fmaxf(m[h], x);
+          const float a = m[h] == -INFINITY ? 0.f : exp2f(m[h] - mn);
+          m[h] = mn;
+          l[h] *= a;
+          f[h] = a * fv;
+        }
+        if (j > 0) {
+          // O holds V_{j-1} P_{j-1}: this thread's head dim, every head's two columns
+          tc_wait(&sh->pv[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u, abort_flag);
+          __syncwarp();
+          tc_fence_after();
+          if constexpr (NH == 8) {
+            uint32_t v[16];
+            tmem_ld16(tO + lane_off, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int h = 0; h < GT; ++h) {
+              v[h] = __float_as_uint(__uint_as_float(v[h]) * f[h]);
+              v[8 + h] = __float_as_uint(__uint_as_float(v[8 + h]) * f[h]);
+            }
+            tmem_st16(tO + lane_off, v);
+          } else {
+            uint32_t v[32];
+            tmem_ld32(tO + lane_off, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int h = 0; h < GT; ++h) {
+              v[h] = __float_as_uint(__uint_as_float(v[h]) * f[h]);
+              v[16 + h] = __float_as_uint(__uint_as_float(v[16 + h]) * f[h]);
+            }
+            tmem_st32(tO + lane_off, v);
+          }
+          tmem_st_wait();
+        }
+        named_sync(1, 128);                      // mx is free again
+      }
+      // P: 32 p v / vref as two e4m3 terms, byte r of rows h and NH + h
+      const float vf = vref > 0.f ? kTcPScale * (vs / vref) : 0.f;
+      const uint32_t pb = sbase + kOffP + (uint32_t)st * (N * 128);
+#pragma unroll
+      for (int h = 0; h < GT; h += 2) {
+        const bool two = GT > 1;
+        const float p0 = s[h] == -INFINITY ? 0.f : exp2f(s[h] - m[h]);
+        l[h] += p0;
+        float p1 = 0.f;
+        if constexpr (GT > 1) {
+          p1 = s[h + 1] == -INFINITY ? 0.f : exp2f(s[h + 1] - m[h + 1]);
+          l[h + 1] += p1;
+        }
+        const float x0 = p0 * vf, x1 = p1 * vf;
+        const uint32_t hi = e4m3x2(x0, x1);
+        float y0, y1;
+        from_e4m3x2(hi, y0, y1);
+        const uint32_t lo = e4m3x2((x0 - y0) * 16.f, (x1 - y1) * 16.f);
+        sts_u8(pb + swz_byte(h, r), hi);
+        sts_u8(pb + swz_byte(NH + h, r), lo);
+        if (two) {
+          sts_u8(pb + swz_byte(h + 1, r), hi >> 8);
+          sts_u8(pb + swz_byte(NH + h + 1, r), lo >> 8);
+        }
+      }
+      if (!ok) {
+        // the slot may hold anything (NaN codes, an older tile): 0 * NaN would reach O
+        tc_wait(&sh->full_v[st], ph, abort_flag);
+        unsigned char* vrow = smem + kOffV + st * kTcStage + r * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vrow + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(&sh->p[st]);
+    }
+
+    // ------------------------------------------------------------ output
+    __syncwarp();
+    named_sync(1, 128);
+#pragma unroll
+    for (int h = 0; h < GT; ++h) {
+      float x = l[h];
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+      if (lane == 0) sh->mx[warp][h] = x;
+    }
+    named_sync(1, 128);
+    float o[GT];
+#pragma unroll
+    for (int h = 0; h < GT; ++h) o[h] = 0.f;
+    if (nt > 0) {
+      tc_wait(&sh->pv[(nt - 1) & 1], (uint32_t)((nt - 1) >> 1) & 1u, abort_flag);
+      __syncwarp();
+      tc_fence_after();
+      const float up = vref * (1.f / kTcPScale);
+      if constexpr (NH == 8) {
+        uint32_t v[16];
+        tmem_ld16(tO + lane_off, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < GT; ++h) o[h] = fmaf(__uint_as_float(v[8 + h]), 0.0625f, __uint_as_float(v[h])) * up;
+      } else {
+        uint32_t v[32];
+        tmem_ld32(tO + lane_off, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < GT; ++h) o[h] = fmaf(__uint_as_float(v[16 + h]), 0.0625f, __uint_as_float(v[h])) * up;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < GT; ++h) {
+      if (h >= gh) break;
+      const float den = (sh->mx[0][h] + sh->mx[1][h]) + (sh->mx[2][h] + sh->mx[3][h]);
+      const size_t bh = (size_t)b * p.Hq + h0 + h;
+      const size_t slot = bh * p.max_parts + part;
+      if (nparts > 1)
+        p.ws_o[slot * D + r] = o[h];
+      else
+        static_cast<__nv_bfloat16*>(p.out)[bh * D + r] = __float2bfloat16_rn(den > 0.f ? o[h] / den : 0.f);
+      if (r == 0 && (W || nparts > 1)) {
+        p.ws_ml[slot * 2] = m[h];
+        p.ws_ml[slot * 2 + 1] = den;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 5) tmem_dealloc(tmem, kTmem);
+}
+
+}  // namespace
+}  // namespace pa

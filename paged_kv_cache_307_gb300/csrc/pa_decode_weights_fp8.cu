@@ -1,7 +1,7 @@
 // pa_decode_weights_fp8.cu — weights-mode decode instances (scores kept for
 // weights_kernel) for e4m3 K/V pools with one scale per (block, KV head).
 // Compiled on its own so the instances build in parallel with the others.
-#include "pa_decode_kernel.cuh"
+#include "pa_decode_tc.cuh"
 
 namespace pa {
 namespace {
@@ -23,26 +23,27 @@ Launch pick_gt(int gt, int hg) {
   return pick_hg<D, 1>(hg);
 }
 
-// Tensor-core instances (head_dim 128): GT query heads per KV head, 1 or 2 KV heads per item.
+// tcgen05 instances (head_dim 128): gt query heads of a KV head per CTA.
 template <int GT>
-Launch pick_mma_hg(int hg) {
-  const void* fin = reinterpret_cast<const void*>(&weights_kernel<B16, 128>);
-  if (hg == 2) return {reinterpret_cast<const void*>(&decode_kernel<B16, fp8e4m3b, 128, GT, true, 2, true>), fin};
-  return {reinterpret_cast<const void*>(&decode_kernel<B16, fp8e4m3b, 128, GT, true, 1, true>), fin};
+Launch pick_tc(size_t* smem) {
+  *smem = tc_smem_bytes<(GT <= 8 ? 8 : 16)>();
+  return {reinterpret_cast<const void*>(&tc_decode_kernel<GT, true>), reinterpret_cast<const void*>(&weights_kernel<B16, 128>)};
 }
 
 }  // namespace
 
-Launch pick_decode_weights_fp8(int head_dim, int gt, int hg, bool mma) {
-  if (mma) {
-    if (gt == 16) return pick_mma_hg<16>(hg);
-    if (gt == 8) return pick_mma_hg<8>(hg);
-    if (gt == 4) return pick_mma_hg<4>(hg);
-    return pick_mma_hg<2>(hg);
-  }
+Launch pick_decode_weights_fp8(int head_dim, int gt, int hg) {
   if (head_dim == 32) return pick_gt<32>(gt, hg);
   if (head_dim == 64) return pick_gt<64>(gt, hg);
   return pick_gt<128>(gt, hg);
+}
+
+Launch pick_decode_weights_fp8_tc(int gt, size_t* smem) {
+  if (gt > 8) return pick_tc<16>(smem);
+  if (gt > 4) return pick_tc<8>(smem);
+  if (gt > 2) return pick_tc<4>(smem);
+  if (gt > 1) return pick_tc<2>(smem);
+  return pick_tc<1>(smem);
 }
 
 unsigned fetch_status_decode_weights_fp8() {
