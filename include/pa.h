@@ -360,8 +360,16 @@ int pa_append_fp8_blocks(const void* key, const void* value,
  * unscaled weights), both in fp32.
  *
  *   query, out      PA_BF16
- *   partition_size, workspace: as for pa_decode_fp8
+ *   partition_size  as for pa_decode, but for the automatic choice:
+ *                   pa_decode_fp8_blocks_partition_size returns the size used
+ *   workspace       at least pa_decode_fp8_blocks_workspace_bytes() with the
+ *                   same sizes, 16-byte aligned (may be NULL when that is 0)
  *   other arguments as for pa_decode
+ *
+ * head_dim 128 with block_size 8 to 32 runs on the tcgen05 tensor cores, the
+ * codes as they are (e4m3 products, fp32 accumulation): Q and the softmax weights
+ * enter as two e4m3 terms each, which carry bf16's 8 significant bits.  Everything
+ * else runs on CUDA cores in fp32.
  */
 int pa_decode_fp8_blocks(void* out, const void* query,
                          const void* k_cache, const void* v_cache,
@@ -372,6 +380,13 @@ int pa_decode_fp8_blocks(void* out, const void* query,
                          int block_size, int num_blocks, float scale, int partition_size,
                          void* workspace, size_t workspace_bytes,
                          pa_dtype dtype, void* stream);
+
+/* Bytes of workspace pa_decode_fp8_blocks needs for these sizes, and the
+ * partition size (tokens) it uses.  Pure host arithmetic; no CUDA call. */
+size_t pa_decode_fp8_blocks_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                            int max_blocks_per_seq, int block_size, int partition_size);
+int pa_decode_fp8_blocks_partition_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                        int max_blocks_per_seq, int block_size, int partition_size);
 
 /*
  * Causal attention of each sequence's newest tokens over a block-scaled e4m3
@@ -410,8 +425,9 @@ int pa_prefill_fp8_blocks(void* out, const void* query, const int32_t* query_sta
  *   dtype           of query and out
  *   kv_dtype        of the pools: dtype itself, or PA_FP8_E4M3 (block-scaled,
  *                   dtype PA_BF16); k_scale, v_scale are used only then
- *   workspace       at least pa_decode_weights_workspace_bytes(): the split-K
- *                   partials and an fp32 score per (query head, table slot)
+ *   workspace       at least pa_decode_weights_workspace_bytes(), 16-byte
+ *                   aligned: the split-K partials and an fp32 score per (query
+ *                   head, table slot)
  *   other arguments as for pa_decode; num_heads / num_kv_heads <= 1024
  */
 int pa_decode_weights(void* out, float* weights, long long weights_stride,

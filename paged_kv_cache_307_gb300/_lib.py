@@ -61,6 +61,10 @@ lib.pa_append_fp8_blocks.argtypes = [_p, _p, _i32p, _i, _i32p, _i, _i32p, _i, _p
 lib.pa_append_fp8_blocks.restype = _i
 lib.pa_decode_fp8_blocks.argtypes = lib.pa_decode_fp8.argtypes
 lib.pa_decode_fp8_blocks.restype = _i
+lib.pa_decode_fp8_blocks_workspace_bytes.argtypes = [_i, _i, _i, _i, _i, _i, _i]
+lib.pa_decode_fp8_blocks_workspace_bytes.restype = _sz
+lib.pa_decode_fp8_blocks_partition_size.argtypes = [_i, _i, _i, _i, _i, _i, _i]
+lib.pa_decode_fp8_blocks_partition_size.restype = _i
 lib.pa_prefill_fp8_blocks.argtypes = [_p, _p, _i32p, _i, _p, _p, _p, _p, _i32p, _i, _i32p, _i, _i, _i, _i, _i, _i, _f,
                                       _i, _p]
 lib.pa_prefill_fp8_blocks.restype = _i
@@ -415,7 +419,10 @@ def copy_blocks_fp8_blocks(k_cache, v_cache, k_scale, v_scale, pairs, stream=Non
 
 def alloc_fp8_blocks_workspace(q, k_cache, block_tables, partition_size=0):
     """Workspace for decode_fp8_blocks with these sizes."""
-    return alloc_workspace(q, k_cache, block_tables, partition_size)
+    B, Hq, D = q.shape
+    n = lib.pa_decode_fp8_blocks_workspace_bytes(B, Hq, k_cache.shape[2], D, block_tables.shape[1], k_cache.shape[1],
+                                                 partition_size)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
 
 
 def decode_fp8_blocks(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,

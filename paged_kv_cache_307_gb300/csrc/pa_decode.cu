@@ -183,6 +183,29 @@ int resolve_partition(int max_blocks, int bs, int partition_size, int G, bool fp
   return P;
 }
 
+// Block-scaled pools that the tcgen05 kernel takes: head_dim 128, and blocks of 8
+// and more (its TMA boxes are whole 8-row swizzle atoms).
+bool tc_shape(int head_dim, int block_size) { return head_dim == 128 && block_size >= 8; }
+
+// Automatic split of the tcgen05 kernel, one CTA per (partition, sequence, KV
+// head): the largest of 2048, 1024 and 512 tokens that gives two CTAs per SM at
+// the table's capacity.  A CTA's start and end weigh about as much as three of
+// its 128-token tiles, so long partitions pay while there are CTAs enough: 64
+// requests x 8 KV heads over U[1024, 16384] take 374, 251, 204 and 194 us at 256,
+// 512, 1024 and 2048 tokens; one request x 8 heads at 32768 tokens 27.1, 25.1,
+// 21.8 and 29.0, eight at up to 8192 tokens 32.2, 26.8, 23.8 and 29.8.
+int resolve_partition_tc(int max_blocks, int bs, int partition_size, int G, int num_seqs, int num_kv_heads) {
+  const int max_ctx = max_blocks * bs;
+  if (partition_size < 0) return max_ctx;
+  int P = partition_size;
+  if (P <= 0) {
+    const long long items = (long long)num_seqs * num_kv_heads * ((G + 15) / 16);
+    P = 2048;
+    while (P > 512 && items * max_ctx < 2ll * 152 * P) P /= 2;
+  }
+  return P >= max_ctx ? max_ctx : P;
+}
+
 // Clears the decode kernel's item counter.  The decode kernel is its
 // programmatic dependent on eager calls: its CTAs become resident and build
 // their tables while this runs, and wait for it on the device before their
@@ -264,18 +287,28 @@ extern "C" size_t pa_decode_workspace_bytes(int num_seqs, int num_heads, int num
 }
 
 // What pa_decode_weights adds to a decode: the running totals and their row
-// stride (floats), and how many workspace bytes the scores take.
+// stride (floats).
 struct WeightsArgs {
   float* weights;
   long long stride;
 };
 
-// Workspace of a weights-mode decode: (m, l) of every partition, the partial
-// outputs (none when no sequence can span two partitions), the item counter,
-// then the scores.
-static size_t weights_partials_bytes(long long rows, int max_parts, int head_dim) {
+// (m, l) of every partition, the partial outputs (none when no sequence can span
+// two partitions) and the item counter: the workspace of a block-scaled decode,
+// and what a weights-mode decode has before its scores.
+static size_t partials_bytes(long long rows, int max_parts, int head_dim) {
   const long long ml = ((rows * max_parts * 8) + 255) / 256 * 256;
   return (size_t)(ml + (max_parts > 1 ? rows * max_parts * head_dim * 4 : 0) + 256);
+}
+
+// The partition a block-scaled decode uses.
+static int partition_blocks(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int max_blocks_per_seq,
+                            int block_size, int partition_size) {
+  const int P = partition_size_impl(true, num_seqs, num_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size,
+                                    partition_size);
+  if (P <= 0 || !tc_shape(head_dim, block_size)) return P;
+  return resolve_partition_tc(max_blocks_per_seq, block_size, partition_size, num_heads / num_kv_heads, num_seqs,
+                              num_kv_heads);
 }
 
 // Shared by pa_decode, pa_decode_fp8, pa_decode_fp8_blocks and
@@ -296,6 +329,7 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
       max_blocks_per_seq <= 0)
     return PA_ERR_SHAPE;
   if (partition_size > 0 && partition_size % block_size) return PA_ERR_SHAPE;
+  if (blk && (long long)num_seqs * num_heads > 0x7fffffffll) return PA_ERR_SHAPE;
   if (wa) {
     // one second-kernel CTA per (sequence, KV head, kWeightTokens tokens), and the merge's
     const long long max_ctx = (long long)max_blocks_per_seq * block_size;
@@ -310,23 +344,26 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
   if (!aligned16(out) || !aligned16(query) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_ALIGN;
   if (fp8 && (!aligned16(k_scale) || !aligned16(v_scale))) return PA_ERR_ALIGN;
 
-  const int P = resolve_partition(max_blocks_per_seq, block_size, partition_size, num_heads / num_kv_heads,
-                                  kv == PA_FP8_E4M3, num_seqs, num_kv_heads);
+  const int P = blk ? partition_blocks(num_seqs, num_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size,
+                                       partition_size)
+                    : resolve_partition(max_blocks_per_seq, block_size, partition_size, num_heads / num_kv_heads,
+                                        kv == PA_FP8_E4M3, num_seqs, num_kv_heads);
   const long long max_ctx = (long long)max_blocks_per_seq * block_size;
   const int max_parts = (int)((max_ctx + P - 1) / P);
-  const size_t partials = wa ? weights_partials_bytes((long long)num_seqs * num_heads, max_parts, head_dim) : 0;
+  const size_t partials = wa ? partials_bytes((long long)num_seqs * num_heads, max_parts, head_dim) : 0;
   const size_t need = wa ? partials + (size_t)num_seqs * num_heads * max_ctx * 4
+                   : blk ? pa_decode_fp8_blocks_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim,
+                                                                max_blocks_per_seq, block_size, partition_size)
                          : pa_decode_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim,
                                                      max_blocks_per_seq, block_size, partition_size);
+  if ((wa || blk) && need && !aligned16(workspace)) return PA_ERR_ALIGN;
   if (need && (!workspace || workspace_bytes < need)) return PA_ERR_WORKSPACE;
 
   int dev = 0;
   if (!ck(cudaGetDevice(&dev), "cudaGetDevice")) return PA_ERR_CUDA;
   CUtensorMap mapK, mapV;
   const int G = num_heads / num_kv_heads;
-  // Block-scaled pools of head_dim 128: the tcgen05 kernel, for every group size
-  // (its TMA boxes are whole 8-row swizzle atoms, so blocks of 4 stay out).
-  const bool use_tc = blk && head_dim == 128 && block_size >= 8;
+  const bool use_tc = blk && tc_shape(head_dim, block_size);   // for every group size
   // Tensor cores over the query group when it is a real contraction (G >= 2).
   const bool use_mma = !blk &&
                        ((kv == PA_BF16 && (head_dim == 64 || head_dim == 128)) ||
@@ -464,17 +501,21 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
   }
   }
   if (wa) {
-    const unsigned merge_blocks =
-        max_parts > 1 ? (unsigned)(((long long)num_seqs * num_heads * 32 + kWeightTokens - 1) / kWeightTokens) : 0u;
-    const long long blocks =
-        merge_blocks + (long long)num_seqs * num_kv_heads * ((max_ctx + kWeightTokens - 1) / kWeightTokens);
+    unsigned merge_ctas = max_parts > 1 ? (unsigned)(num_seqs * num_heads) : 0u;
+    const long long ctas =
+        merge_ctas + (long long)num_seqs * num_kv_heads * ((max_ctx + kWeightTokens - 1) / kWeightTokens);
     float* w = wa->weights;
     long long stride = wa->stride;
-    unsigned mb = merge_blocks;
-    void* wargs[] = {&prm, &w, &stride, &mb};
-    if (!ck(launch_dependent(L.merge, dim3((unsigned)blocks), dim3(kWeightTokens), wargs, 2 * (size_t)G * 4,
+    void* wargs[] = {&prm, &w, &stride, &merge_ctas};
+    if (!ck(launch_dependent(L.merge, dim3((unsigned)ctas), dim3(kFinishThreads), wargs, 2 * (size_t)G * 4,
                              (cudaStream_t)stream),
             "cudaLaunchKernel(weights_kernel)"))
+      return PA_ERR_CUDA;
+  } else if (max_parts > 1 && blk) {
+    void* margs[] = {&prm};
+    if (!ck(launch_after(L.merge, dim3((unsigned)(num_seqs * num_heads)), dim3(kFinishThreads), margs,
+                         (cudaStream_t)stream),
+            "cudaLaunchKernel(merge_wide_kernel)"))
       return PA_ERR_CUDA;
   } else if (max_parts > 1) {
     const long long warps = (long long)num_seqs * num_heads;
@@ -521,15 +562,34 @@ extern "C" int pa_decode_fp8_blocks(void* out, const void* query, const void* k_
                      partition_size, workspace, workspace_bytes, dtype, PA_FP8_E4M3, stream, true);
 }
 
+extern "C" int pa_decode_fp8_blocks_partition_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                                   int max_blocks_per_seq, int block_size, int partition_size) {
+  return partition_blocks(num_seqs, num_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size,
+                          partition_size);
+}
+
+extern "C" size_t pa_decode_fp8_blocks_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                                       int max_blocks_per_seq, int block_size, int partition_size) {
+  const int P = partition_blocks(num_seqs, num_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size,
+                                 partition_size);
+  if (P <= 0 || num_seqs <= 0) return 0;
+  const long long max_ctx = (long long)max_blocks_per_seq * block_size;
+  const int max_parts = (int)((max_ctx + P - 1) / P);
+  return max_parts > 1 ? partials_bytes((long long)num_seqs * num_heads, max_parts, head_dim) : 0;
+}
+
 extern "C" size_t pa_decode_weights_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                                                     int max_blocks_per_seq, int block_size, int partition_size,
                                                     pa_dtype kv_dtype) {
-  const int P = partition_size_impl(kv_dtype == PA_FP8_E4M3, num_seqs, num_heads, num_kv_heads, head_dim,
-                                    max_blocks_per_seq, block_size, partition_size);
+  const int P = kv_dtype == PA_FP8_E4M3
+                    ? partition_blocks(num_seqs, num_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size,
+                                       partition_size)
+                    : partition_size_impl(false, num_seqs, num_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                                          block_size, partition_size);
   if (P <= 0 || num_seqs <= 0) return 0;
   const long long max_ctx = (long long)max_blocks_per_seq * block_size;
   const long long rows = (long long)num_seqs * num_heads;
-  return weights_partials_bytes(rows, (int)((max_ctx + P - 1) / P), head_dim) + (size_t)(rows * max_ctx * 4);
+  return partials_bytes(rows, (int)((max_ctx + P - 1) / P), head_dim) + (size_t)(rows * max_ctx * 4);
 }
 
 extern "C" int pa_decode_weights(void* out, float* weights, long long weights_stride, const void* query,

@@ -17,7 +17,7 @@ using B16 = __nv_bfloat16;
 // CUDA-core instances: 1 or 2 KV heads per item.
 template <int D, int GT>
 Launch pick_hg(int hg) {
-  const void* merge = reinterpret_cast<const void*>(&merge_kernel<B16, D>);
+  const void* merge = reinterpret_cast<const void*>(&merge_wide_kernel<B16, D>);
   if (hg == 2) return {reinterpret_cast<const void*>(&decode_kernel<B16, fp8e4m3b, D, GT, false, 2>), merge};
   return {reinterpret_cast<const void*>(&decode_kernel<B16, fp8e4m3b, D, GT, false, 1>), merge};
 }
@@ -33,7 +33,8 @@ Launch pick_gt(int gt, int hg) {
 template <int GT>
 Launch pick_tc(size_t* smem) {
   *smem = tc_smem_bytes<(GT <= 8 ? 8 : 16)>();
-  return {reinterpret_cast<const void*>(&tc_decode_kernel<GT, false>), reinterpret_cast<const void*>(&merge_kernel<B16, 128>)};
+  return {reinterpret_cast<const void*>(&tc_decode_kernel<GT, false>),
+          reinterpret_cast<const void*>(&merge_wide_kernel<B16, 128>)};
 }
 
 }  // namespace

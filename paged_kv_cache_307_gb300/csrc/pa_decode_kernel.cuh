@@ -1576,9 +1576,11 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
 // Lane i < 32 computes partition i's weight (broadcast by shuffle); each
 // partition's row of o is read as one vector of D/32 floats per lane.
 template <typename T, int D>
-__device__ __forceinline__ void merge_row(const DecodeParams& p, long long gw) {
+__global__ void __launch_bounds__(256)
+merge_kernel(const DecodeParams p) {
   using E = Elem<T>;
   constexpr int VPL = D / 32;                 // dims per lane: 4, 2 or 1
+  const long long gw = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (gw >= (long long)p.B * p.Hq) return;
   const int b = (int)(gw / p.Hq);
@@ -1636,43 +1638,126 @@ __device__ __forceinline__ void merge_row(const DecodeParams& p, long long gw) {
   for (int k = 0; k < VPL; ++k) E::store1(out + k, acc[k] * inv);
 }
 
+// One CTA per (sequence, query head): the merge of merge_kernel with the
+// partitions spread over the CTA's eight warps.  A warp reads its partials four
+// in flight; a long context of few sequences has few rows and many partials,
+// and one warp walking 128 of them took 20 us of a 47 us call.
+constexpr int kFinishThreads = 256;
 template <typename T, int D>
-__global__ void __launch_bounds__(256)
-merge_kernel(const DecodeParams p) {
-  merge_row<T, D>(p, ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5);
+__device__ __forceinline__ void merge_row_wide(const DecodeParams& p, int bh) {
+  using E = Elem<T>;
+  constexpr int NW = kFinishThreads / 32, VPL = D / 32;
+  __shared__ float so[NW][D], sm[NW], sl[NW];
+  const int b = bh / p.Hq;
+  int L = __ldg(&p.context_lens[b]);
+  const int Lmax = p.max_blocks * p.bs;
+  L = L < 0 ? 0 : min(L, Lmax);
+  const int nparts = L > 0 ? (L + p.part_tokens - 1) / p.part_tokens : 1;
+  if (nparts <= 1) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float* ml = p.ws_ml + (size_t)bh * p.max_parts * 2;
+  const float* po = p.ws_o + (size_t)bh * p.max_parts * D + lane * VPL;
+  float M = -INFINITY, den = 0.f, acc[VPL];
+#pragma unroll
+  for (int k = 0; k < VPL; ++k) acc[k] = 0.f;
+  // this warp's partials, four at a time, with a running reference
+  for (int i0 = warp; i0 < nparts; i0 += 4 * NW) {
+    float m[4], l[4], v[4][VPL];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k * NW;
+      m[k] = i < nparts ? ml[2 * i] : -INFINITY;
+      l[k] = i < nparts ? ml[2 * i + 1] : 0.f;
+#pragma unroll
+      for (int d = 0; d < VPL; ++d) v[k][d] = i < nparts ? po[(size_t)i * D + d] : 0.f;
+    }
+    const float Mn = fmaxf(M, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+    const float a = M == -INFINITY ? 0.f : exp2f(M - Mn);
+    M = Mn;
+    den *= a;
+#pragma unroll
+    for (int d = 0; d < VPL; ++d) acc[d] *= a;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float w = m[k] == -INFINITY ? 0.f : exp2f(m[k] - M);
+      den = fmaf(w, l[k], den);
+#pragma unroll
+      for (int d = 0; d < VPL; ++d) acc[d] = fmaf(w, v[k][d], acc[d]);
+    }
+  }
+#pragma unroll
+  for (int d = 0; d < VPL; ++d) so[warp][lane * VPL + d] = acc[d];
+  if (lane == 0) {
+    sm[warp] = M;
+    sl[warp] = den;
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < D) {
+    float Mx = sm[0];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) Mx = fmaxf(Mx, sm[w]);
+    float num = 0.f, dsum = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float f = sm[w] == -INFINITY ? 0.f : exp2f(sm[w] - Mx);
+      num = fmaf(f, so[w][threadIdx.x], num);
+      dsum = fmaf(f, sl[w], dsum);
+    }
+    E::store1(static_cast<T*>(p.out) + (size_t)bh * D + threadIdx.x, dsum > 0.f ? num / dsum : 0.f);
+  }
 }
 
-// Weights mode's second kernel: the first `merge_blocks` CTAs merge the
-// partitions as merge_kernel does; each of the others takes one (sequence, KV
-// head, 256 tokens) and adds the softmax weights to their running totals:
-//   weights[b, g, t] += sum over the group's heads h of 2^(s[b,h,t] - M_h) / l_h
-// with (M_h, l_h) the log-sum-exp of the partitions' states.  One thread per
-// token reads its G scores (a coalesced row of each head) and adds them in
-// head order: no atomics, the same sum on every run.
-constexpr int kWeightTokens = 256;
 template <typename T, int D>
-__global__ void __launch_bounds__(kWeightTokens)
-weights_kernel(const DecodeParams p, float* weights, long long wstride, unsigned merge_blocks) {
+__global__ void __launch_bounds__(kFinishThreads) merge_wide_kernel(const DecodeParams p) {
+  merge_row_wide<T, D>(p, (int)blockIdx.x);
+}
+
+// Weights mode's second kernel: the first `merge_ctas` CTAs merge a row's
+// partitions; each of the others takes one (sequence, KV head, 1024 tokens) and
+// adds the softmax weights to their running totals:
+//   weights[b, g, t] += sum over the group's heads h of 2^(s[b,h,t] - M_h) / l_h
+// with (M_h, l_h) the log-sum-exp of the partitions' states.  A thread has four
+// tokens, 256 apart, whose scores of four heads are on their way while the
+// states are merged; heads are added in order: no atomics, the same sum on every
+// run.
+constexpr int kWeightTokens = 4 * kFinishThreads;
+template <typename T, int D>
+__global__ void __launch_bounds__(kFinishThreads)
+weights_kernel(const DecodeParams p, float* weights, long long wstride, unsigned merge_ctas) {
   extern __shared__ float hm[];               // [G] M_h, then [G] 1 / l_h
-  if (blockIdx.x < merge_blocks) {
-    merge_row<T, D>(p, ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5);
+  if (blockIdx.x < merge_ctas) {
+    merge_row_wide<T, D>(p, (int)blockIdx.x);
     return;
   }
   const int Lmax = p.max_blocks * p.bs;
   const int nt = (Lmax + kWeightTokens - 1) / kWeightTokens;
-  long long u = (long long)blockIdx.x - merge_blocks;
+  long long u = (long long)blockIdx.x - merge_ctas;
   const int t0 = (int)(u % nt) * kWeightTokens;
   u /= nt;
   const int g = (int)(u % p.Hkv), b = (int)(u / p.Hkv);
   int L = __ldg(&p.context_lens[b]);
-  if (L < 0 || L > Lmax) L = L < 0 ? 0 : Lmax;
+  L = L < 0 ? 0 : min(L, Lmax);
   if (t0 >= L) return;
   const int t = t0 + (int)threadIdx.x;
   const int nparts = (L + p.part_tokens - 1) / p.part_tokens;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const size_t row0 = (size_t)b * p.Hq + (size_t)g * p.G;
-  for (int h = warp; h < p.G; h += kWeightTokens / 32) {
+  const float* sp = p.ws_s + row0 * Lmax + t;
+  float* wp = weights + ((size_t)b * p.Hkv + g) * wstride + t;
+  float s[4][4], was[4], sum[4] = {0.f, 0.f, 0.f, 0.f};
+  auto load = [&](int h) {                    // the scores of heads h .. h + 3
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        s[i][k] = h + i < p.G && t + k * kFinishThreads < L ? sp[(size_t)(h + i) * Lmax + k * kFinishThreads] : 0.f;
+  };
+  load(0);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) was[k] = t + k * kFinishThreads < L ? wp[k * kFinishThreads] : 0.f;
+  for (int h = warp; h < p.G; h += kFinishThreads / 32) {
     const float* ml = p.ws_ml + (row0 + h) * p.max_parts * 2;
     float M = -INFINITY, den = 0.f;
     for (int i = lane; i < nparts; i += 32) M = fmaxf(M, ml[2 * i]);
@@ -1688,12 +1773,19 @@ weights_kernel(const DecodeParams p, float* weights, long long wstride, unsigned
     }
   }
   __syncthreads();
-  if (t >= L) return;
-  float sum = 0.f;
-  for (int h = 0; h < p.G; ++h)
-    sum = fmaf(exp2f(p.ws_s[(row0 + h) * Lmax + t] - hm[h]), hm[p.G + h], sum);
-  float* w = weights + ((size_t)b * p.Hkv + g) * wstride + t;
-  *w += sum;
+  for (int h = 0; h < p.G; h += 4) {
+    if (h > 0) load(h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (h + i < p.G) {
+        const float M = hm[h + i], inv = hm[p.G + h + i];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum[k] = fmaf(exp2f(s[i][k] - M), inv, sum[k]);
+      }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (t + k * kFinishThreads < L) wp[k * kFinishThreads] = was[k] + sum[k];
 }
 
 }  // namespace

@@ -150,17 +150,34 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
   u /= p.nsub;
   const int b = u % p.B, part = u / p.B;
   const int Lmax = p.max_blocks * p.bs;
+  const int hs = (p.G + p.nsub - 1) / p.nsub;
+  const int h0 = kvh * p.G + sub * hs;          // first query head
+  const int gh = min(hs, p.G - sub * hs);       // query heads of this CTA, <= GT
+  const int t0 = part * p.part_tokens;
+  const int bsh = 31 - __clz(p.bs);
+  // What does not depend on the context's length is requested with it: the
+  // queries, and the first three tiles' block-table entries (a lane each, inside
+  // the row whatever the length is).
+  __nv_bfloat16 qraw[GT];
+  int id[3] = {0, 0, 0};
+  if (warp < 4) {
+    const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q) + ((size_t)b * p.Hq + h0) * D + threadIdx.x;
+#pragma unroll
+    for (int h = 0; h < GT; ++h) qraw[h] = qp[(size_t)min(h, gh - 1) * D];
+  } else if (warp == 4) {
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      const int i = ((t0 + j * kTcTile) >> bsh) + lane;
+      if (lane < (kTcTile >> bsh) && i < p.max_blocks) id[j] = __ldg(&p.block_tables[(size_t)b * p.max_blocks + i]);
+    }
+  }
   const int L0 = __ldg(&p.context_lens[b]);
   const int L = L0 < 0 ? 0 : min(L0, Lmax);
   if (part == 0 && kvh == 0 && sub == 0 && threadIdx.x == 0 && L != L0) atomicOr(&g_status_decode, PA_DEV_BAD_LEN);
   const int nparts = L > 0 ? (L + p.part_tokens - 1) / p.part_tokens : 1;
   if (part >= nparts) return;                   // nothing allocated yet
-  const int hs = (p.G + p.nsub - 1) / p.nsub;
-  const int h0 = kvh * p.G + sub * hs;          // first query head
-  const int gh = min(hs, p.G - sub * hs);       // query heads of this CTA, <= GT
-  const int t0 = part * p.part_tokens, t1 = min(L, t0 + p.part_tokens);
+  const int t1 = min(L, t0 + p.part_tokens);
   const int nt = (t1 - t0 + kTcTile - 1) / kTcTile;
-  const int bsh = 31 - __clz(p.bs);
 
   if (threadIdx.x == 160) {
     for (int i = 0; i < 2; ++i) {
@@ -198,24 +215,24 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
     const uint64_t pol = policy_evict_first();
     const int32_t* row = p.block_tables + (size_t)b * p.max_blocks;
     const uint32_t box = (uint32_t)p.bs * 128u;
-    // lane i: block i of a tile (at most 16), its id and scales
-    auto fetch = [&](int j, int& blk, float& ks, float& vs) {
-      const int t = t0 + j * kTcTile + (lane << bsh);
-      blk = 0;
-      ks = vs = 0.f;
-      if (j < nt && lane < (kTcTile >> bsh) && t < t1) {
-        blk = __ldg(&row[t >> bsh]);
-        if ((unsigned)blk >= (unsigned)p.num_blocks) {
-          atomicOr(&g_status_decode, PA_DEV_BAD_BLOCK);
-          blk = 0;                              // keep every copy inside the pool
-        }
-        ks = __ldg(&p.k_scale[(size_t)blk * p.scale_row + kvh]);
-        vs = __ldg(&p.v_scale[(size_t)blk * p.scale_row + kvh]);
-      }
+    // Lane i: block i of a tile (at most 16), its id and scales.  The scales hang
+    // on the id and both come from memory: ids are read three tiles ahead and
+    // scales two, so that neither latency is waited for (one tile ahead for
+    // both held every tile up by two memory latencies, about 4000 clocks).
+    auto in_use = [&](int j) -> bool {
+      return j < nt && lane < (kTcTile >> bsh) && t0 + j * kTcTile + (lane << bsh) < t1;
     };
-    int blk;
-    float ks, vs;
-    fetch(0, blk, ks, vs);
+    auto checked = [&](int id) -> int {
+      if ((unsigned)id < (unsigned)p.num_blocks) return id;
+      atomicOr(&g_status_decode, PA_DEV_BAD_BLOCK);
+      return 0;                                 // keep every copy inside the pool
+    };
+    auto scale_of = [&](const float* s, int id) -> float { return __ldg(&s[(size_t)id * p.scale_row + kvh]); };
+    int blk = in_use(0) ? checked(id[0]) : 0;
+    float ks = scale_of(p.k_scale, blk), vs = scale_of(p.v_scale, blk);
+    int blk1 = in_use(1) ? checked(id[1]) : 0;
+    float ks1 = scale_of(p.k_scale, blk1), vs1 = scale_of(p.v_scale, blk1);
+    int blk2 = id[2];
     int issued_k = 0, issued_v = 0;
     for (int j = 0; j < nt; ++j) {
       const int st = j & 1;
@@ -224,15 +241,7 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       bool ok = true;
       if (lane == 0) ok = tc_wait(&sh->empty_k[st], ph, abort_flag);
       if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
-      if (lane < 16) {
-        sh->scl[j & 3][0][lane] = ks;
-        sh->scl[j & 3][1][lane] = vs;
-      }
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sh->scl_full[j & 3]);
-        mbar_arrive_expect_tx(&sh->full_k[st], (uint32_t)nb * box);
-      }
+      if (lane == 0) mbar_arrive_expect_tx(&sh->full_k[st], (uint32_t)nb * box);
       __syncwarp();
       if (lane < nb)
         tma_load_4d(smem + st * kTcStage + lane * box, &mapK, &sh->full_k[st], 0, kvh, 0, blk, pol);
@@ -244,7 +253,19 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       if (lane < nb)
         tma_load_4d(smem + kOffV + st * kTcStage + lane * box, &mapV, &sh->full_v[st], 0, kvh, 0, blk, pol);
       issued_v = j + 1;
-      fetch(j + 1, blk, ks, vs);
+      if (lane < 16) {
+        sh->scl[j & 3][0][lane] = ks;
+        sh->scl[j & 3][1][lane] = vs;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->scl_full[j & 3]);
+      blk = blk1;
+      ks = ks1;
+      vs = vs1;
+      blk1 = in_use(j + 2) ? checked(blk2) : 0;
+      ks1 = scale_of(p.k_scale, blk1);
+      vs1 = scale_of(p.v_scale, blk1);
+      blk2 = in_use(j + 3) ? __ldg(&row[((t0 + (j + 3) * kTcTile) >> bsh) + lane]) : 0;
     }
     // no TMA write may land after the CTA has left
     if (lane == 0) {
@@ -299,10 +320,9 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
     float qf[GT];                                // scale * log2(e) * 2^e of every head
     {
       float q[GT];
-      const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q) + ((size_t)b * p.Hq + h0) * D + r;
 #pragma unroll
       for (int h = 0; h < GT; ++h) {
-        q[h] = __bfloat162float(qp[(size_t)min(h, gh - 1) * D]);
+        q[h] = __bfloat162float(qraw[h]);
         const float m = warp_max(fabsf(q[h]));
         if (lane == 0) sh->mx[warp][h] = m;
       }

@@ -27,7 +27,8 @@ Launch pick_gt(int gt, int hg) {
 template <int GT>
 Launch pick_tc(size_t* smem) {
   *smem = tc_smem_bytes<(GT <= 8 ? 8 : 16)>();
-  return {reinterpret_cast<const void*>(&tc_decode_kernel<GT, true>), reinterpret_cast<const void*>(&weights_kernel<B16, 128>)};
+  return {reinterpret_cast<const void*>(&tc_decode_kernel<GT, true>),
+          reinterpret_cast<const void*>(&weights_kernel<B16, 128>)};
 }
 
 }  // namespace

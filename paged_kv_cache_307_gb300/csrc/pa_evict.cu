@@ -10,17 +10,20 @@
 // sequence.)  A token's position in the text then no longer follows from its
 // slot, so it is carried in token_pos.
 //
-// select_kernel, one CTA per (sequence, KV head): the budget-th largest key by
-// radix selection, 8 bits a pass over an order-preserving integer image of the
-// weights (protected tokens above all others); then one pass in slot order
-// that marks what is kept, breaking ties by the lower slot, and numbers the
-// holes and the movers by a block-wide scan; weights, positions and the list
-// of moves come out of it.
-// move_kernel, one warp per (sequence, KV head, destination block): its rows
-// are copied in; over an e4m3 pool the block's scale becomes the largest of
-// its own and the incoming rows' and the rows are requantised (the scales are
-// powers of two: exact but for underflow).  One warp owns a destination
-// block's head, so nothing is atomic.
+// select_kernel, one CTA per (sequence, KV head): the keys (an order-preserving
+// integer image of the weights, protected tokens above all others) are read
+// once into shared memory; the budget-th largest comes out by radix selection,
+// 8 bits a pass.  Each warp then owns a run of consecutive slots and walks it 32
+// at a time: a sweep that counts ties, one that decides what stays (ties by the
+// lower slot), one that numbers the holes and the movers; between sweeps one scan
+// over the warps.  Weights, positions and the list of moves come out of it.
+// Counts: a digit's 256 bins exist eight times, a lane adding to copy lane % 8:
+// weights share their leading bits, and 32 lanes adding to one word take 32 turns.
+// move_kernel, one warp per destination block: the block's moves, a lane each,
+// then their rows with eight 16-byte loads in flight per lane; over an e4m3 pool
+// the block's scale becomes the largest of its own and the incoming rows' and the
+// rows are requantised (the scales are powers of two: exact but for underflow).
+// One warp owns a destination block's head, so nothing is atomic.
 // Bound by latency and HBM: 8 bytes read per token and head, 8 written per slot,
 // and the moved rows.
 #include "pa_common.cuh"
@@ -30,9 +33,9 @@ namespace {
 
 __device__ unsigned g_status_evict;
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kMoveWarps = 4;
+constexpr int kHistCopies = 8;
+constexpr int kMaxSmemKeys = 48 * 1024;   // tokens whose keys fit in shared memory beside the bins
+constexpr int kMoveWarps = 8;
 
 struct Move {
   int32_t src;          // slot the row comes from
@@ -70,54 +73,92 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 
 __device__ __forceinline__ int clamp_len(int L, int Lmax) { return L < 0 ? 0 : min(L, Lmax); }
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p) {
-  __shared__ int hist[256];
-  __shared__ int wsum[2][kSelWarps];
+// Exclusive sum over the warps of x (the same in every lane of a warp), and the total.
+template <int NW>
+__device__ __forceinline__ int scan_warps(int x, int* buf, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();                       // (buf's last readers are done)
+  if (lane == 0) buf[warp] = x;
+  __syncthreads();
+  int v = lane < NW ? buf[lane] : 0;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, v, off);
+    if (lane >= off) v += y;
+  }
+  total = __shfl_sync(0xffffffffu, v, NW - 1);
+  return warp ? __shfl_sync(0xffffffffu, v, warp - 1) : (__shfl_sync(0xffffffffu, v, 0), 0);
+}
+
+// SMEM: the keys are kept in shared memory (else recomputed from the inputs).
+template <int NT, bool SMEM>
+__global__ void __launch_bounds__(NT) select_kernel(const EvictParams p) {
+  constexpr int NW = NT / 32;
+  __shared__ int hist[256 * kHistCopies];
+  __shared__ int wbuf[NW];
   __shared__ int sh_digit, sh_left;
+  extern __shared__ uint32_t keys[];
+  asm volatile("griddepcontrol.launch_dependents;");
   const int bh = (int)blockIdx.x, b = bh / p.Hkv, h = bh % p.Hkv;
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int Lmax = p.max_blocks * p.bs;
   const int L0 = __ldg(&p.context_lens[b]);
-  const int L = clamp_len(L0, Lmax);
   const int K0 = __ldg(&p.kept_lens[b]);
-  const int kept = clamp_len(K0, L);
   const int seen = __ldg(&p.seen_lens[b]);
+  const int L = clamp_len(L0, Lmax);
+  const int kept = clamp_len(K0, L);
+  const int newL = min(L, p.budget);
   if (h == 0 && tid == 0) {
     if (L0 != L || K0 != kept) atomicOr(&g_status_evict, PA_DEV_BAD_LEN);
-    p.ws_len[b] = min(L, p.budget);
+    p.ws_len[b] = newL;
   }
   const size_t row = (size_t)bh * p.stride;
   const float* w = p.weights + row;
   const int32_t* tp = p.token_pos + row;
   float* wo = p.weights_out + row;
   int32_t* po = p.pos_out + row;
-  const int newL = min(L, p.budget);
   auto pos_of = [&](int t) { return t < kept ? tp[t] : seen - L + t; };
-  auto key_of = [&](int t) -> uint32_t {
-    const int pos = pos_of(t);
-    return pos < p.sinks || pos >= seen - p.recent ? 0xffffffffu : order_key(w[t]);
-  };
   int32_t* first = p.first + (size_t)bh * (p.nb + 1);
   if (L <= p.budget) {
     // nothing leaves (in and out may be the same rows: each thread reads its entry before writing it)
-    for (int t = tid; t < Lmax; t += kSelThreads) {
+    for (int t = tid; t < Lmax; t += NT) {
       const float wt = t < L ? w[t] : 0.f;
       const int pt = t < L ? pos_of(t) : -1;
       wo[t] = wt;
       po[t] = pt;
     }
-    for (int j = tid; j <= p.nb; j += kSelThreads) first[j] = 0;
+    for (int j = tid; j <= p.nb; j += NT) first[j] = 0;
     return;
   }
+  auto make_key = [&](int t) -> uint32_t {
+    const float wt = w[t];
+    const int pos = pos_of(t);
+    return pos < p.sinks || pos >= seen - p.recent ? 0xffffffffu : order_key(wt);
+  };
+  if constexpr (SMEM) {
+#pragma unroll 4
+    for (int t = tid; t < L; t += NT) keys[t] = make_key(t);
+  }
+  auto key_of = [&](int t) -> uint32_t {
+    if constexpr (SMEM) return keys[t];
+    else return make_key(t);
+  };
   // ---- the budget-th largest key: 8 bits a pass from the top
   uint32_t prefix = 0, mask = 0;
   int left = p.budget;                    // how many of the keys that match the prefix are kept
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
+    for (int i = tid; i < 256 * kHistCopies; i += NT) hist[i] = 0;
     __syncthreads();
-    for (int t = tid; t < L; t += kSelThreads) {
+    for (int t = tid; t < L; t += NT) {
       const uint32_t k = key_of(t);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
+      if ((k & mask) == prefix) atomicAdd(&hist[((k >> shift) & 255u) * kHistCopies + (lane & (kHistCopies - 1))], 1);
+    }
+    __syncthreads();
+    if (tid < 256) {
+      int c = 0;
+#pragma unroll
+      for (int i = 0; i < kHistCopies; ++i) c += hist[tid * kHistCopies + ((i + tid) & (kHistCopies - 1))];
+      hist[tid * kHistCopies] = c;        // (a thread's own eight words)
     }
     __syncthreads();
     if (warp == 0) {
@@ -125,7 +166,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
       int c[8], sum = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        c[i] = hist[255 - 8 * lane - i];
+        c[i] = hist[(255 - 8 * lane - i) * kHistCopies];
         sum += c[i];
       }
       int incl = sum;
@@ -154,67 +195,66 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
   }
   // keys above `prefix` are kept, and the first `left` of those equal to it
 
-  // ---- one pass in slot order: kept, holes below the budget, movers at or above it
+  // ---- each warp's run of slots, 32 at a time
+  const int run = ((L + NT - 1) / NT) * 32;
+  const int r0 = min(L, warp * run), r1 = min(L, r0 + run);
+  const unsigned lt = (1u << lane) - 1u;
+  int eq = 0, total;
+  for (int t0 = r0; t0 < r1; t0 += 32) {
+    const int t = t0 + lane;
+    eq += __popc(__ballot_sync(0xffffffffu, t < r1 && key_of(t) == prefix));
+  }
+  const int tie0 = scan_warps<NW>(eq, wbuf, total);
+  auto stays = [&](int t, int& ties) -> unsigned {     // the 32 slots' answer, ties counted on
+    const uint32_t k = t < r1 ? key_of(t) : 0u;
+    const unsigned me = __ballot_sync(0xffffffffu, t < r1 && k == prefix);
+    const bool s = t < r1 && (k > prefix || (k == prefix && ties + __popc(me & lt) < left));
+    ties += __popc(me);
+    return __ballot_sync(0xffffffffu, s);
+  };
+  int ties = tie0, holes = 0, movers = 0;
+  for (int t0 = r0; t0 < r1; t0 += 32) {
+    const unsigned s = stays(t0 + lane, ties);
+    const unsigned in = r1 - t0 >= 32 ? 0xffffffffu : (1u << (r1 - t0)) - 1u;          // slots of the run
+    const unsigned low = t0 + 32 <= p.budget ? 0xffffffffu : t0 < p.budget ? (1u << (p.budget - t0)) - 1u : 0u;
+    holes += __popc(in & low & ~s);
+    movers += __popc(s & ~low);
+  }
+  int hole0 = scan_warps<NW>(holes, wbuf, total);
+  const int nmove = total;                             // as many movers as holes
+  int mover0 = scan_warps<NW>(movers, wbuf, total);
   Move* mv = p.moves + (size_t)bh * p.cap;
   int32_t* dst = p.dst + (size_t)bh * p.cap;
-  int ties = 0, holes = 0, movers = 0;    // running counts over the slots before this tile
-  for (int t0 = 0; t0 < L; t0 += kSelThreads) {
-    const int t = t0 + tid;
-    const uint32_t k = t < L ? key_of(t) : 0u;
-    const bool eq = t < L && k == prefix;
-    const unsigned lt = (1u << lane) - 1u;
-    const unsigned me = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) wsum[0][warp] = __popc(me);
-    __syncthreads();
-    int eb = ties, et = 0;
-    for (int i = 0; i < kSelWarps; ++i) {
-      if (i < warp) eb += wsum[0][i];
-      et += wsum[0][i];
-    }
-    const bool stay = t < L && (k > prefix || (eq && eb + __popc(me & lt) < left));
-    const bool hole = t < p.budget && !stay, come = t >= p.budget && stay;
-    const unsigned mh = __ballot_sync(0xffffffffu, hole || come);
-    // a tile may hold both kinds: holes below the budget, movers from it on
-    const unsigned mhole = __ballot_sync(0xffffffffu, hole);
-    if (lane == 0) wsum[1][warp] = __popc(mhole) | (__popc(mh & ~mhole) << 16);
-    __syncthreads();
-    int hb = holes, cb = movers, ht = 0, ct = 0;
-    for (int i = 0; i < kSelWarps; ++i) {
-      const int v = wsum[1][i];
-      if (i < warp) {
-        hb += v & 0xffff;
-        cb += v >> 16;
-      }
-      ht += v & 0xffff;
-      ct += v >> 16;
-    }
-    hb += __popc(mhole & lt);
-    cb += __popc(mh & ~mhole & lt);
-    if (t < p.budget) {
-      if ((t % p.bs) == 0) first[t / p.bs] = hb;
-      if (hole) dst[hb] = t;
-      else {
+  ties = tie0;
+  for (int t0 = r0; t0 < r1; t0 += 32) {
+    const int t = t0 + lane;
+    const unsigned s = stays(t, ties);
+    const unsigned in = r1 - t0 >= 32 ? 0xffffffffu : (1u << (r1 - t0)) - 1u;
+    const unsigned low = t0 + 32 <= p.budget ? 0xffffffffu : t0 < p.budget ? (1u << (p.budget - t0)) - 1u : 0u;
+    const unsigned hm = in & low & ~s, cm = s & ~low;
+    const unsigned bit = 1u << lane;
+    if (in & low & bit) {
+      const int at = hole0 + __popc(hm & lt);
+      if ((t & (p.bs - 1)) == 0) first[t / p.bs] = at;
+      if (hm & bit) {
+        dst[at] = t;
+      } else {
         // (in and out may be the same row)
         const float wt = w[t];
         const int pt = pos_of(t);
         wo[t] = wt;
         po[t] = pt;
       }
-    } else if (come) {
-      Move m;
-      m.src = t;
-      m.k_scale = m.v_scale = 0.f;
-      mv[cb] = m;
+    } else if (cm & bit) {
+      mv[mover0 + __popc(cm & lt)].src = t;
     }
-    ties += et;
-    holes += ht;
-    movers += ct;
-    __syncthreads();
+    hole0 += __popc(hm);
+    mover0 += __popc(cm);
   }
-  if (tid == 0) first[p.nb] = holes;
+  if (tid == 0) first[p.nb] = nmove;
   __syncthreads();
   // ---- the movers' weights, positions and scales, then the rest of the rows
-  for (int i = tid; i < holes; i += kSelThreads) {
+  for (int i = tid; i < nmove; i += NT) {
     const int s = mv[i].src;
     wo[dst[i]] = w[s];
     po[dst[i]] = pos_of(s);
@@ -227,7 +267,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
     }
   }
   __syncthreads();
-  for (int t = newL + tid; t < Lmax; t += kSelThreads) {
+  for (int t = newL + tid; t < Lmax; t += NT) {
     wo[t] = 0.f;
     po[t] = -1;
   }
@@ -249,70 +289,104 @@ __device__ __forceinline__ uint4 rescale16(uint4 x, float f) {
                     encode4(v[8], v[9], v[10], v[11]), encode4(v[12], v[13], v[14], v[15]));
 }
 
-__global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const EvictParams p) {
-  const int lane = threadIdx.x & 31;
-  const long long u = (long long)blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
-  if (u >= (long long)p.B * p.Hkv * p.nb) return;
-  const int j = (int)(u % p.nb);
-  const int bh = (int)(u / p.nb), b = bh / p.Hkv, h = bh % p.Hkv;
+// One CTA per (sequence, KV head) and `per` destination blocks.
+__global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const EvictParams p, int per) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = (p.nb + per - 1) / per;
+  const int bh = (int)(blockIdx.x / groups), g0 = (int)(blockIdx.x % groups) * per;
+  const int b = bh / p.Hkv, h = bh % p.Hkv;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int newL = p.ws_len[b];
-  if (j == 0 && h == 0 && lane == 0) p.new_lens[b] = newL;
-  const int32_t* first = p.first + (size_t)bh * (p.nb + 1) + j;
-  const int m0 = first[0], m1 = first[1];
-  if (m0 >= m1) return;
+  if (g0 == 0 && h == 0 && threadIdx.x == 0) p.new_lens[b] = newL;
   const int32_t* tab = p.block_tables + (size_t)b * p.max_blocks;
-  const int dblk = __ldg(&tab[j]);
-  if ((unsigned)dblk >= (unsigned)p.num_blocks) {
-    if (lane == 0) atomicOr(&g_status_evict, PA_DEV_BAD_BLOCK);
-    return;
-  }
   const Move* mv = p.moves + (size_t)bh * p.cap;
   const int32_t* dst = p.dst + (size_t)bh * p.cap;
-  const int rb = p.D * p.elem, cpr = rb / 16;             // one head's row, in 16-byte chunks
+  const int rb = p.D * p.elem;                            // one head's row in bytes: 32 to 512
+  const int csh = 31 - __clz(rb / 16), cpr = 1 << csh;    // its 16-byte chunks, a power of two
   const size_t tok = (size_t)p.Hkv * rb;                  // from token to token
-#pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    unsigned char* pool = static_cast<unsigned char*>(p.pool[kv]);
-    unsigned char* dbase = pool + ((size_t)dblk * p.bs) * tok + (size_t)h * rb;
-    float s = 0.f, old = 0.f;
+  for (int j = g0 + warp; j < min(p.nb, g0 + per); j += kMoveWarps) {
+    const int32_t* first = p.first + (size_t)bh * (p.nb + 1) + j;
+    const int m0 = first[0], n = first[1] - m0;           // at most bs moves
+    if (n <= 0) continue;
+    const int dblk = __ldg(&tab[j]);
+    if ((unsigned)dblk >= (unsigned)p.num_blocks) {
+      if (lane == 0) atomicOr(&g_status_evict, PA_DEV_BAD_BLOCK);
+      continue;
+    }
+    // lane i: move i
+    long long srow = -1;                                  // source row in the pool, -1: its block is not one
+    int drow = 0;
+    float sc[2] = {0.f, 0.f};
+    if (lane < n) {
+      const Move m = mv[m0 + lane];
+      const int sblk = __ldg(&tab[m.src / p.bs]);
+      drow = dst[m0 + lane] - j * p.bs;
+      sc[0] = m.k_scale;
+      sc[1] = m.v_scale;
+      if ((unsigned)sblk < (unsigned)p.num_blocks) srow = (long long)sblk * p.bs + m.src % p.bs;
+      else atomicOr(&g_status_evict, PA_DEV_BAD_BLOCK);
+    }
+    float s[2] = {0.f, 0.f};
     if (p.elem == 1) {
-      float* sp = p.scale[kv] + (size_t)dblk * p.scale_row + h;
-      old = *sp;
-      s = old;
-      for (int i = m0 + lane; i < m1; i += 32) s = fmaxf(s, kv ? mv[i].v_scale : mv[i].k_scale);
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, off));
-      __syncwarp();
-      if (s > old) {
-        if (lane == 0) *sp = s;
-        // the rows that stay in the block (the holes are overwritten below)
-        const float f = old / s;
-        const int rows = min(p.bs, newL - j * p.bs);
-        for (int c = lane; c < rows * cpr; c += 32) {
-          unsigned char* at = dbase + (size_t)(c / cpr) * tok + (size_t)(c % cpr) * 16;
-          *reinterpret_cast<uint4*>(at) = rescale16(*reinterpret_cast<const uint4*>(at), f);
-        }
+      for (int kv = 0; kv < 2; ++kv) {
+        float* sp = p.scale[kv] + (size_t)dblk * p.scale_row + h;
+        const float old = *sp;
+        float x = srow >= 0 ? sc[kv] : 0.f;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+        s[kv] = fmaxf(old, x);
         __syncwarp();
+        if (s[kv] > old) {
+          if (lane == 0) *sp = s[kv];
+          // the rows that stay in the block (the holes are overwritten below)
+          unsigned char* dbase =
+              static_cast<unsigned char*>(p.pool[kv]) + ((size_t)dblk * p.bs) * tok + (size_t)h * rb;
+          const float f = old / s[kv];
+          const int rows = min(p.bs, newL - j * p.bs);
+          for (int c = lane; c < rows << csh; c += 32) {
+            unsigned char* at = dbase + (size_t)(c >> csh) * tok + (size_t)(c & (cpr - 1)) * 16;
+            *reinterpret_cast<uint4*>(at) = rescale16(*reinterpret_cast<const uint4*>(at), f);
+          }
+          __syncwarp();
+        }
       }
     }
-    for (int c = lane; c < (m1 - m0) * cpr; c += 32) {
-      const int i = m0 + c / cpr;
-      const Move m = mv[i];
-      const int sblk = __ldg(&tab[m.src / p.bs]);
-      if ((unsigned)sblk >= (unsigned)p.num_blocks) {
-        atomicOr(&g_status_evict, PA_DEV_BAD_BLOCK);
-        continue;
+    // rows of K and V, four 16-byte chunks of each in flight per lane
+    const unsigned char* kp = static_cast<const unsigned char*>(p.pool[0]) + (size_t)h * rb;
+    const unsigned char* vp = static_cast<const unsigned char*>(p.pool[1]) + (size_t)h * rb;
+    const size_t dbase = (size_t)dblk * p.bs;
+    for (int c0 = 0; c0 < n << csh; c0 += 128) {
+      uint4 x[4], y[4];
+      long long sr[4];
+      int dr[4];
+      float sk[4], sv[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = c0 + 32 * k + lane, i = min(c >> csh, 31);
+        sr[k] = __shfl_sync(0xffffffffu, srow, i);
+        dr[k] = __shfl_sync(0xffffffffu, drow, i);
+        sk[k] = __shfl_sync(0xffffffffu, sc[0], i);
+        sv[k] = __shfl_sync(0xffffffffu, sc[1], i);
+        if (c >= n << csh) sr[k] = -1;
+        if (sr[k] >= 0) {
+          const size_t at = (size_t)sr[k] * tok + (size_t)(c & (cpr - 1)) * 16;
+          x[k] = *reinterpret_cast<const uint4*>(kp + at);
+          y[k] = *reinterpret_cast<const uint4*>(vp + at);
+        }
       }
-      const unsigned char* from =
-          pool + ((size_t)sblk * p.bs + m.src % p.bs) * tok + (size_t)h * rb + (size_t)(c % cpr) * 16;
-      unsigned char* to = dbase + (size_t)(dst[i] - j * p.bs) * tok + (size_t)(c % cpr) * 16;
-      uint4 x = *reinterpret_cast<const uint4*>(from);
-      if (p.elem == 1) {
-        const float ss = kv ? m.v_scale : m.k_scale;
-        if (ss != s) x = rescale16(x, s > 0.f ? ss / s : 0.f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (sr[k] < 0) continue;
+        const int c = c0 + 32 * k + lane;
+        const size_t at = (dbase + dr[k]) * tok + (size_t)h * rb + (size_t)(c & (cpr - 1)) * 16;
+        if (p.elem == 1) {
+          if (sk[k] != s[0]) x[k] = rescale16(x[k], s[0] > 0.f ? sk[k] / s[0] : 0.f);
+          if (sv[k] != s[1]) y[k] = rescale16(y[k], s[1] > 0.f ? sv[k] / s[1] : 0.f);
+        }
+        st_v4(static_cast<unsigned char*>(p.pool[0]) + at, x[k]);
+        st_v4(static_cast<unsigned char*>(p.pool[1]) + at, y[k]);
       }
-      st_v4(to, x);
     }
   }
 }
@@ -382,8 +456,11 @@ extern "C" int pa_evict(void* k_cache, void* v_cache, float* k_scale, float* v_s
   if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(workspace)) return PA_ERR_ALIGN;
   const Layout l = layout(num_seqs, num_kv_heads, max_blocks_per_seq, block_size, budget);
   if (!workspace || workspace_bytes < l.total) return PA_ERR_WORKSPACE;
-  const long long units = (long long)num_seqs * num_kv_heads * l.nb;
-  const long long blocks = (units + kMoveWarps - 1) / kMoveWarps;
+  // destination blocks per CTA of the second kernel: a warp has one while the
+  // (sequence, head) rows alone do not fill the SMs, four otherwise
+  const int rows = num_seqs * num_kv_heads;
+  const int per = rows >= 2 * 152 ? 4 * kMoveWarps : kMoveWarps;
+  const long long blocks = (long long)rows * ((l.nb + per - 1) / per);
   if (blocks > 0x7fffffffll) return PA_ERR_SHAPE;
   EvictParams p;
   p.pool[0] = k_cache;
@@ -418,13 +495,26 @@ extern "C" int pa_evict(void* k_cache, void* v_cache, float* k_scale, float* v_s
   p.dst = reinterpret_cast<int32_t*>(ws + l.dst);
   p.first = reinterpret_cast<int32_t*>(ws + l.first);
   p.ws_len = reinterpret_cast<int32_t*>(ws + l.len);
+  // Few slots: 256 threads, several (sequence, head) rows per SM; many: 1024.
+  const bool in_smem = max_ctx <= kMaxSmemKeys;
+  const size_t smem = in_smem ? (size_t)max_ctx * 4 : 0;
+  const bool wide = max_ctx > 4096;
+  const void* select = !in_smem ? reinterpret_cast<const void*>(&select_kernel<1024, false>)
+                       : wide   ? reinterpret_cast<const void*>(&select_kernel<1024, true>)
+                                : reinterpret_cast<const void*>(&select_kernel<256, true>);
+  if (smem > 32 * 1024) {
+    if (!ck(cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemKeys * 4),
+            "cudaFuncSetAttribute(select_kernel)"))
+      return PA_ERR_CUDA;
+  }
   void* args[] = {&p};
-  if (!ck(cudaLaunchKernel(reinterpret_cast<const void*>(&select_kernel), dim3((unsigned)(num_seqs * num_kv_heads)),
-                           dim3(kSelThreads), args, 0, (cudaStream_t)stream),
+  if (!ck(cudaLaunchKernel(select, dim3((unsigned)rows), dim3(wide ? 1024u : 256u), args, smem, (cudaStream_t)stream),
           "cudaLaunchKernel(select_kernel)"))
     return PA_ERR_CUDA;
+  int per_arg = per;
+  void* margs[] = {&p, &per_arg};
   if (!ck(launch_after(reinterpret_cast<const void*>(&move_kernel), dim3((unsigned)blocks), dim3(kMoveWarps * 32),
-                       args, (cudaStream_t)stream),
+                       margs, (cudaStream_t)stream),
           "cudaLaunchKernel(move_kernel)"))
     return PA_ERR_CUDA;
   return PA_OK;

@@ -58,7 +58,8 @@ def test_append(pa, kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(dt=0), -3), (dict(dt=2), -3), (dict(D=96), -2), (dict(Hq=7), -2), (dict(bs=64), -2), (dict(ps=24), -2),
     (dict(ks=NULL), -1), (dict(q=NULL), -1), (dict(ks=ODD), -4), (dict(q=ODD), -4),
-    (dict(mb=64, ps=512), -5), (dict(mb=64, ps=512, ws=FAKE, n=16), -5), (dict(B=0), 0)])
+    (dict(mb=64, ps=512), -5), (dict(mb=64, ps=512, ws=FAKE, n=16), -5), (dict(mb=64, ps=512, ws=ODD, n=1 << 30), -4),
+    (dict(B=0), 0)])
 def test_decode(pa, kw, code):
     assert _decode(pa, **kw) == code
 
@@ -73,7 +74,7 @@ def test_prefill(pa, kw, code):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(stride=63), -2), (dict(Hq=2050), -2), (dict(D=40), -2), (dict(dt=0, kv=1), -3), (dict(dt=0, kv=2), -3),
-    (dict(kv=5), -3), (dict(w=NULL), -1), (dict(kv=2, ks=NULL), -1), (dict(kv=2, ks=ODD), -4), (dict(ws=NULL), -5),
+    (dict(kv=5), -3), (dict(w=NULL), -1), (dict(kv=2, ks=NULL), -1), (dict(kv=2, ks=ODD), -4), (dict(ws=ODD), -4), (dict(ws=NULL), -5),
     (dict(n=100), -5), (dict(B=0), 0)])
 def test_weights(pa, kw, code):
     assert _weights(pa, **kw) == code
@@ -95,6 +96,14 @@ def test_workspace_arithmetic(pa):
     # two partitions of 32 tokens: partial outputs too
     assert L.pa_decode_weights_workspace_bytes(2, 8, 2, 128, 4, 16, 32, 1) == 256 + 32 * 128 * 4 + 256 + 2 * 8 * 64 * 4
     assert L.pa_decode_weights_workspace_bytes(0, 8, 2, 128, 4, 16, 0, 1) == 0
+    part, ws = L.pa_decode_fp8_blocks_partition_size, L.pa_decode_fp8_blocks_workspace_bytes
+    assert part(64, 32, 8, 128, 1024, 16, 0) == 2048              # 512 CTAs x 8 partitions at capacity
+    assert part(1, 32, 8, 128, 2048, 16, 0) == 512                # 8 x 64 >= 2 x 152 > 8 x 32
+    assert part(1, 8, 8, 128, 8, 16, 0) == 128                    # never longer than the table
+    assert part(1, 32, 8, 64, 2048, 16, 0) == 256   # CUDA cores: pa_decode_fp8's
+    assert part(1, 32, 8, 128, 2048, 16, 24) == -2 and part(1, 32, 8, 128, 2048, 16, -1) == 32768
+    assert ws(1, 32, 8, 128, 2048, 16, 512) == 32 * 64 * 8 + 32 * 64 * 512 + 256
+    assert ws(1, 32, 8, 128, 2048, 16, -1) == 0
     assert L.pa_evict_workspace_bytes(0, 2, 4, 16, 32) == 0
     assert L.pa_evict_workspace_bytes(2, 2, 4, 16, 0) == 0
     assert L.pa_evict_workspace_bytes(2, 2, 4, 16, 32) > 4 * 32 * 4
