@@ -366,8 +366,8 @@ int pa_append_fp8_blocks(const void* key, const void* value,
  *                   same sizes, 16-byte aligned (may be NULL when that is 0)
  *   other arguments as for pa_decode
  *
- * head_dim 128 with block_size 8 to 32 runs on the tcgen05 tensor cores, the
- * codes as they are (e4m3 products, fp32 accumulation): Q and the softmax weights
+ * With block_size 8 to 32 and num_kv_heads * head_dim a multiple of 128 it runs
+ * on the tcgen05 tensor cores, the codes as they are (e4m3 products, fp32 accumulation): Q and the softmax weights
  * enter as two e4m3 terms each, which carry bf16's 8 significant bits.  Everything
  * else runs on CUDA cores in fp32.
  */

@@ -183,23 +183,29 @@ int resolve_partition(int max_blocks, int bs, int partition_size, int G, bool fp
   return P;
 }
 
-// Block-scaled pools that the tcgen05 kernel takes: head_dim 128, and blocks of 8
-// and more (its TMA boxes are whole 8-row swizzle atoms).
-bool tc_shape(int head_dim, int block_size) { return head_dim == 128 && block_size >= 8; }
+// Block-scaled pools that the tcgen05 kernel takes: blocks of 8 and more (its TMA
+// boxes are whole 8-row swizzle atoms), and KV heads that fill whole rows of 128
+// codes.
+bool tc_shape(int num_kv_heads, int head_dim, int block_size) {
+  return block_size >= 8 && num_kv_heads % (128 / head_dim) == 0;
+}
+// CTAs that share such a row's query heads, 16 at most each.
+int tc_subs(int G, int head_dim) { return (G * (128 / head_dim) + 15) / 16; }
 
-// Automatic split of the tcgen05 kernel, one CTA per (partition, sequence, KV
-// head): the largest of 2048, 1024 and 512 tokens that gives two CTAs per SM at
+// Automatic split of the tcgen05 kernel, one CTA per (partition, sequence, row of
+// 128 codes): the largest of 2048, 1024 and 512 tokens that gives two CTAs per SM at
 // the table's capacity.  A CTA's start and end weigh about as much as three of
 // its 128-token tiles, so long partitions pay while there are CTAs enough: 64
 // requests x 8 KV heads over U[1024, 16384] take 374, 251, 204 and 194 us at 256,
 // 512, 1024 and 2048 tokens; one request x 8 heads at 32768 tokens 27.1, 25.1,
 // 21.8 and 29.0, eight at up to 8192 tokens 32.2, 26.8, 23.8 and 29.8.
-int resolve_partition_tc(int max_blocks, int bs, int partition_size, int G, int num_seqs, int num_kv_heads) {
+int resolve_partition_tc(int max_blocks, int bs, int partition_size, int G, int head_dim, int num_seqs,
+                         int num_kv_heads) {
   const int max_ctx = max_blocks * bs;
   if (partition_size < 0) return max_ctx;
   int P = partition_size;
   if (P <= 0) {
-    const long long items = (long long)num_seqs * num_kv_heads * ((G + 15) / 16);
+    const long long items = (long long)num_seqs * (num_kv_heads / (128 / head_dim)) * tc_subs(G, head_dim);
     P = 2048;
     while (P > 512 && items * max_ctx < 2ll * 152 * P) P /= 2;
   }
@@ -306,9 +312,9 @@ static int partition_blocks(int num_seqs, int num_heads, int num_kv_heads, int h
                             int block_size, int partition_size) {
   const int P = partition_size_impl(true, num_seqs, num_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size,
                                     partition_size);
-  if (P <= 0 || !tc_shape(head_dim, block_size)) return P;
-  return resolve_partition_tc(max_blocks_per_seq, block_size, partition_size, num_heads / num_kv_heads, num_seqs,
-                              num_kv_heads);
+  if (P <= 0 || !supported_head_dim(head_dim) || !tc_shape(num_kv_heads, head_dim, block_size)) return P;
+  return resolve_partition_tc(max_blocks_per_seq, block_size, partition_size, num_heads / num_kv_heads, head_dim,
+                              num_seqs, num_kv_heads);
 }
 
 // Shared by pa_decode, pa_decode_fp8, pa_decode_fp8_blocks and
@@ -363,7 +369,7 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
   if (!ck(cudaGetDevice(&dev), "cudaGetDevice")) return PA_ERR_CUDA;
   CUtensorMap mapK, mapV;
   const int G = num_heads / num_kv_heads;
-  const bool use_tc = blk && tc_shape(head_dim, block_size);   // for every group size
+  const bool use_tc = blk && tc_shape(num_kv_heads, head_dim, block_size);   // for every group size
   // Tensor cores over the query group when it is a real contraction (G >= 2).
   const bool use_mma = !blk &&
                        ((kv == PA_BF16 && (head_dim == 64 || head_dim == 128)) ||
@@ -384,8 +390,9 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
                  : mha_hg ? PA_MHA_HEADS_PER_ITEM
                           : 1;
   const bool swz = use_mma || use_tc;
-  if (!get_map(&mapK, k_cache, kv, num_blocks, block_size, num_kv_heads, head_dim, dev, swz, HG) ||
-      !get_map(&mapV, v_cache, kv, num_blocks, block_size, num_kv_heads, head_dim, dev, swz, HG)) {
+  const int map_h = use_tc ? num_kv_heads / (128 / head_dim) : num_kv_heads, map_d = use_tc ? 128 : head_dim;
+  if (!get_map(&mapK, k_cache, kv, num_blocks, block_size, map_h, map_d, dev, swz, HG) ||
+      !get_map(&mapV, v_cache, kv, num_blocks, block_size, map_h, map_d, dev, swz, HG)) {
     note_host_error("cuTensorMapEncodeTiled failed for the K/V pool");
     return PA_ERR_CUDA;
   }
@@ -430,6 +437,7 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
   prm.k_scale = fp8 ? k_scale : nullptr;
   prm.v_scale = fp8 ? v_scale : nullptr;
   prm.scale_row = scale_row(num_kv_heads);
+  prm.k_codes = blk ? static_cast<const uint8_t*>(k_cache) : nullptr;
   prm.tile_bytes = (uint32_t)(block_size * head_dim * elem_bytes(kv));
   // K/V stages per CTA: ~96 KB on the tensor-core path (one ring shared by
   // the four head warps), ~64 KB on the CUDA-core path (a ring per warp);
@@ -455,13 +463,14 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
   void* args[] = {&mapK, &mapV, &prm};
   Launch L;
   if (use_tc) {
-    // one CTA per (partition, sequence, up to 16 query heads of a KV head)
-    prm.nsub = (G + 15) / 16;
-    const long long ctas = (long long)max_parts * num_seqs * prm.nsub * num_kv_heads;
+    // one CTA per (partition, sequence, up to 16 query heads of a row of 128 codes)
+    const int hp = 128 / head_dim;
+    prm.nsub = tc_subs(G, head_dim);
+    const long long ctas = (long long)max_parts * num_seqs * prm.nsub * (num_kv_heads / hp);
     if (ctas > 0x7fffffffll) return PA_ERR_SHAPE;
-    const int gt = (G + prm.nsub - 1) / prm.nsub;
+    const int gt = (hp * G + prm.nsub - 1) / prm.nsub;
     size_t tc_smem = 0;
-    L = wa ? pick_decode_weights_fp8_tc(gt, &tc_smem) : pick_decode_fp8_blocks_tc(gt, &tc_smem);
+    L = wa ? pick_decode_weights_fp8_tc(head_dim, gt, &tc_smem) : pick_decode_fp8_blocks_tc(head_dim, gt, &tc_smem);
     if (!raise_smem_limit(L.kernel, dev)) return PA_ERR_CUDA;
     if (!ck(cudaLaunchKernel(L.kernel, dim3((unsigned)ctas), dim3(192), args, tc_smem, (cudaStream_t)stream),
             "cudaLaunchKernel(tc_decode_kernel)"))

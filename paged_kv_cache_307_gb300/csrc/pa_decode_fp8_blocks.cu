@@ -1,8 +1,8 @@
 // pa_decode_fp8_blocks.cu — decode kernel instances for e4m3 K/V pools with one
 // scale per (block, KV head).
 //
-// head_dim 128 with block_size 8 to 32 runs tc_decode_kernel (pa_decode_tc.cuh);
-// the rest runs the CUDA-core form of pa_decode_kernel.cuh with KT = fp8e4m3b:
+// Blocks of 8 to 32 whose KV heads fill whole rows of 128 codes run
+// tc_decode_kernel (pa_decode_tc.cuh); the rest runs the CUDA-core form of pa_decode_kernel.cuh with KT = fp8e4m3b:
 // with each stage the producer moves the 16-byte chunk of the block's scale row
 // that holds the item's heads, and a consumer warp reads its head's one value
 // for all of the block's tokens.  Queries and output are bf16.  Compiled on its
@@ -29,12 +29,23 @@ Launch pick_gt(int gt, int hg) {
   return pick_hg<D, 1>(hg);
 }
 
-// tcgen05 instances (head_dim 128): gt query heads of a KV head per CTA.
-template <int GT>
+// tcgen05 instances: gt query heads per CTA, 128 / head_dim KV heads per row of codes.
+template <int GT, int HP>
 Launch pick_tc(size_t* smem) {
   *smem = tc_smem_bytes<(GT <= 8 ? 8 : 16)>();
-  return {reinterpret_cast<const void*>(&tc_decode_kernel<GT, false>),
-          reinterpret_cast<const void*>(&merge_wide_kernel<B16, 128>)};
+  return {reinterpret_cast<const void*>(&tc_decode_kernel<GT, HP, false>),
+          reinterpret_cast<const void*>(&merge_wide_kernel<B16, 128 / HP>)};
+}
+
+template <int HP>
+Launch pick_tc_gt(int gt, size_t* smem) {
+  if (gt > 8) return pick_tc<16, HP>(smem);
+  if (gt > 4) return pick_tc<8, HP>(smem);
+  if constexpr (HP == 1)
+    if (gt == 1) return pick_tc<1, HP>(smem);
+  if constexpr (HP <= 2)
+    if (gt <= 2) return pick_tc<2, HP>(smem);
+  return pick_tc<4, HP>(smem);
 }
 
 }  // namespace
@@ -45,12 +56,10 @@ Launch pick_decode_fp8_blocks(int head_dim, int gt, int hg) {
   return pick_gt<128>(gt, hg);
 }
 
-Launch pick_decode_fp8_blocks_tc(int gt, size_t* smem) {
-  if (gt > 8) return pick_tc<16>(smem);
-  if (gt > 4) return pick_tc<8>(smem);
-  if (gt > 2) return pick_tc<4>(smem);
-  if (gt > 1) return pick_tc<2>(smem);
-  return pick_tc<1>(smem);
+Launch pick_decode_fp8_blocks_tc(int head_dim, int gt, size_t* smem) {
+  if (head_dim == 32) return pick_tc_gt<4>(gt, smem);
+  if (head_dim == 64) return pick_tc_gt<2>(gt, smem);
+  return pick_tc_gt<1>(gt, smem);
 }
 
 unsigned fetch_status_decode_fp8_blocks() {

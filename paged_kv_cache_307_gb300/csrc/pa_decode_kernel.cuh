@@ -90,6 +90,7 @@ struct DecodeParams {
   const float* k_scale;  // e4m3 pools: per-token K scales [num_blocks * bs], or per-block scales
   const float* v_scale;  // [num_blocks][scale_row]; the same for V; else null
   int scale_row;         // per-block scales: floats per block
+  const uint8_t* k_codes;  // per-block scales: the K pool
   float* ws_s;           // weights mode: scores [B*Hq][max_blocks*bs] in log2 units
   int HG;             // KV heads per work item (one consumer warp each when HG = 4)
   int n_hg;           // Hkv / HG
@@ -1540,7 +1541,9 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
 #pragma unroll
       for (int g = 0; g < WPH; ++g) M = fmaxf(M, mbuf[((g * HG + hh) * GT + h) * (D + 2) + D]);
       float num = 0.f, den = 0.f;
-      if (M != -INFINITY) {
+      // (block-scaled pools and weights mode let a NaN sum through)
+      constexpr bool kNan = BLK || W;
+      if (kNan || M != -INFINITY) {
 #pragma unroll
         for (int g = 0; g < WPH; ++g) {
           const float* src = mbuf + ((g * HG + hh) * GT + h) * (D + 2);
@@ -1551,7 +1554,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
       }
       const size_t bh = (size_t)item.b * p.Hq + (size_t)(item.kvh0 + hh) * p.G + item.sg * GT + h;
       if (!item.split) {
-        E::store1(static_cast<T*>(p.out) + bh * D + d, den > 0.f ? num / den : 0.f);
+        E::store1(static_cast<T*>(p.out) + bh * D + d, (kNan ? den != 0.f : den > 0.f) ? num / den : 0.f);
         if constexpr (W) {
           if (d == 0) {
             p.ws_ml[bh * p.max_parts * 2] = M;
@@ -1704,7 +1707,7 @@ __device__ __forceinline__ void merge_row_wide(const DecodeParams& p, int bh) {
       num = fmaf(f, so[w][threadIdx.x], num);
       dsum = fmaf(f, sl[w], dsum);
     }
-    E::store1(static_cast<T*>(p.out) + (size_t)bh * D + threadIdx.x, dsum > 0.f ? num / dsum : 0.f);
+    E::store1(static_cast<T*>(p.out) + (size_t)bh * D + threadIdx.x, dsum != 0.f ? num / dsum : 0.f);
   }
 }
 
@@ -1769,7 +1772,7 @@ weights_kernel(const DecodeParams p, float* weights, long long wstride, unsigned
     for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
     if (lane == 0) {
       hm[h] = M == -INFINITY ? 0.f : M;
-      hm[p.G + h] = den > 0.f ? 1.f / den : 0.f;
+      hm[p.G + h] = den != 0.f ? 1.f / den : 0.f;
     }
   }
   __syncthreads();
@@ -1803,11 +1806,11 @@ Launch pick_decode_fp8(int head_dim, int gt, int hg, bool mma);
 // tcgen05 kernel for gt query heads per CTA (<= 16) with its shared memory
 // (pa_decode_fp8_blocks.cu).
 Launch pick_decode_fp8_blocks(int head_dim, int gt, int hg);
-Launch pick_decode_fp8_blocks_tc(int gt, size_t* smem);
+Launch pick_decode_fp8_blocks_tc(int head_dim, int gt, size_t* smem);
 // Weights-mode instances: pools of the query's type (pa_decode_weights.cu) and
 // block-scaled e4m3 pools (pa_decode_weights_fp8.cu).
 Launch pick_decode_weights(bool f32, int head_dim, int gt, int hg, bool mma);
 Launch pick_decode_weights_fp8(int head_dim, int gt, int hg);
-Launch pick_decode_weights_fp8_tc(int gt, size_t* smem);
+Launch pick_decode_weights_fp8_tc(int head_dim, int gt, size_t* smem);
 
 }  // namespace pa

@@ -24,6 +24,12 @@
 // to the running reference, v / vref <= 1 is the V scale of the token's block
 // against the largest so far.  The K scale multiplies the score in fp32.
 //
+// head_dim 64 and 32 (HP = 2 and 4): HP neighbouring KV heads make one row of 128
+// codes, so the pool is read as one of Hkv / HP heads of 128.  The query heads of
+// all of them share the CTA; a query row is zero outside its own KV head's
+// columns, and of its output row only those are kept.  The products are HP times
+// what they need be, and the tensor cores are idle enough for it.
+//
 //  * warp 4 (TMA): block-table entries and scales by parallel lanes, K and V
 //    boxes {128 B, 1 head, bs rows} into 2-stage rings of 16 KB tiles; K's
 //    stage frees with its S, V's with its O.
@@ -56,11 +62,12 @@ constexpr float kTcPScale = 32.f;          // p in [0, 8] -> [0, 256]
 
 struct TcShared {
   uint64_t full_k[2], full_v[2], empty_k[2], empty_v[2], s[2], p[2], pv[2], scl_full[4], qf, drain;
-  // scales of the 128 / bs blocks of tile j in slot j & 3: tile j+2's and j+3's
-  // may be written while the softmax works on j, j+4's only after P_j
-  alignas(16) float scl[4][2][16];
+  // scales (K, V) of the 128 / bs blocks of tile j, HP heads each, in slot j & 3:
+  // tile j+2's and j+3's may be written while the softmax works on j, j+4's only
+  // after P_j
+  alignas(16) float scl[4][2][64];
   alignas(16) float mx[4][16];             // per warp: tile maximum of every head; at the end, sums
-  float vmx[4];
+  float vmx[4][4];
   uint32_t tmem_base;
   int abort;
 };
@@ -122,13 +129,30 @@ __device__ __forceinline__ uint32_t swz_byte(int n, int x) {
   return (uint32_t)(n * 128 + (((x >> 4) ^ (n & 7)) << 4) + (x & 15));
 }
 
-// GT: query heads of the CTA, rounded up (1, 2, 4, 8, 16); W: weights mode.
-// p.nsub CTAs share a KV head's G query heads, hs = ceil(G / nsub) each.
-template <int GT, bool W>
+// The score (log2 units) of query head hq for sequence b's token t, by itself.
+template <int D>
+__device__ __noinline__ float plain_score(const DecodeParams& p, int b, int t, int hq, int kvh) {
+  int id = p.block_tables[(size_t)b * p.max_blocks + t / p.bs];
+  if ((unsigned)id >= (unsigned)p.num_blocks) id = 0;
+  const uint8_t* k = p.k_codes + (((size_t)id * p.bs + t % p.bs) * p.Hkv + kvh) * D;
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + ((size_t)b * p.Hq + hq) * D;
+  float acc = 0.f;
+  for (int d = 0; d < D; ++d) {
+    __nv_fp8_e4m3 c;
+    c.__x = k[d];
+    acc = fmaf(__bfloat162float(q[d]), static_cast<float>(c), acc);
+  }
+  return acc * (p.qscale * p.k_scale[(size_t)id * p.scale_row + kvh]);
+}
+
+// GT: query heads of the CTA, rounded up (1, 2, 4, 8, 16); HP: KV heads per row
+// of 128 codes; W: weights mode.  p.nsub CTAs share the HP * G query heads of a
+// row's KV heads, hs = ceil(HP * G / nsub) each.
+template <int GT, int HP, bool W>
 __global__ void __launch_bounds__(kTcThreads, GT <= 8 ? 3 : 2)
 tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                  const DecodeParams p) {
-  constexpr int D = 128;
+  constexpr int D = 128 / HP;
   constexpr int NH = GT <= 8 ? 8 : 16;          // heads' rows of one term
   constexpr int N = 2 * NH;
   constexpr uint32_t kTmem = N == 16 ? 64u : 128u;   // S_0, S_1, O: N columns each
@@ -144,15 +168,17 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
   // ---- item: KV heads innermost (neighbouring CTAs read neighbouring rows of the same blocks),
   // partitions outermost (the CTAs without work, past the shorter contexts, come last)
   int u = (int)blockIdx.x;
-  const int kvh = u % p.Hkv;
-  u /= p.Hkv;
+  const int rowh = u % (p.Hkv / HP);            // row of 128 codes: KV heads rowh * HP and on
+  u /= p.Hkv / HP;
   const int sub = u % p.nsub;
   u /= p.nsub;
   const int b = u % p.B, part = u / p.B;
   const int Lmax = p.max_blocks * p.bs;
-  const int hs = (p.G + p.nsub - 1) / p.nsub;
-  const int h0 = kvh * p.G + sub * hs;          // first query head
-  const int gh = min(hs, p.G - sub * hs);       // query heads of this CTA, <= GT
+  const int hs = (HP * p.G + p.nsub - 1) / p.nsub;
+  const int h0 = rowh * HP * p.G + sub * hs;    // first query head
+  const int gh = min(hs, HP * p.G - sub * hs);  // query heads of this CTA, <= GT (0: the last one is short)
+  // which of the row's KV heads query head h reads
+  auto kv_of = [&](int h) -> int { return HP == 1 ? 0 : (sub * hs + min(h, gh - 1)) / p.G; };
   const int t0 = part * p.part_tokens;
   const int bsh = 31 - __clz(p.bs);
   // What does not depend on the context's length is requested with it: the
@@ -161,9 +187,12 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
   __nv_bfloat16 qraw[GT];
   int id[3] = {0, 0, 0};
   if (warp < 4) {
-    const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q) + ((size_t)b * p.Hq + h0) * D + threadIdx.x;
+    const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q) + ((size_t)b * p.Hq + h0) * D;
 #pragma unroll
-    for (int h = 0; h < GT; ++h) qraw[h] = qp[(size_t)min(h, gh - 1) * D];
+    for (int h = 0; h < GT; ++h) {
+      const int d = (int)threadIdx.x - kv_of(h) * D;       // the thread's column within the head, if it has one
+      qraw[h] = gh > 0 && (HP == 1 || (d >= 0 && d < D)) ? qp[min(h, gh - 1) * D + d] : __float2bfloat16_rn(0.f);
+    }
   } else if (warp == 4) {
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
@@ -173,9 +202,9 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
   }
   const int L0 = __ldg(&p.context_lens[b]);
   const int L = L0 < 0 ? 0 : min(L0, Lmax);
-  if (part == 0 && kvh == 0 && sub == 0 && threadIdx.x == 0 && L != L0) atomicOr(&g_status_decode, PA_DEV_BAD_LEN);
+  if (part == 0 && rowh == 0 && sub == 0 && threadIdx.x == 0 && L != L0) atomicOr(&g_status_decode, PA_DEV_BAD_LEN);
   const int nparts = L > 0 ? (L + p.part_tokens - 1) / p.part_tokens : 1;
-  if (part >= nparts) return;                   // nothing allocated yet
+  if (part >= nparts || gh <= 0) return;        // nothing allocated yet
   const int t1 = min(L, t0 + p.part_tokens);
   const int nt = (t1 - t0 + kTcTile - 1) / kTcTile;
 
@@ -227,11 +256,22 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       atomicOr(&g_status_decode, PA_DEV_BAD_BLOCK);
       return 0;                                 // keep every copy inside the pool
     };
-    auto scale_of = [&](const float* s, int id) -> float { return __ldg(&s[(size_t)id * p.scale_row + kvh]); };
+    struct Scales {
+      float k[HP], v[HP];
+    };
+    auto scales_of = [&](int id) -> Scales {
+      Scales x;
+#pragma unroll
+      for (int i = 0; i < HP; ++i) {
+        x.k[i] = __ldg(&p.k_scale[(size_t)id * p.scale_row + rowh * HP + i]);
+        x.v[i] = __ldg(&p.v_scale[(size_t)id * p.scale_row + rowh * HP + i]);
+      }
+      return x;
+    };
     int blk = in_use(0) ? checked(id[0]) : 0;
-    float ks = scale_of(p.k_scale, blk), vs = scale_of(p.v_scale, blk);
+    Scales sc = scales_of(blk);
     int blk1 = in_use(1) ? checked(id[1]) : 0;
-    float ks1 = scale_of(p.k_scale, blk1), vs1 = scale_of(p.v_scale, blk1);
+    Scales sc1 = scales_of(blk1);
     int blk2 = id[2];
     int issued_k = 0, issued_v = 0;
     for (int j = 0; j < nt; ++j) {
@@ -244,27 +284,28 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       if (lane == 0) mbar_arrive_expect_tx(&sh->full_k[st], (uint32_t)nb * box);
       __syncwarp();
       if (lane < nb)
-        tma_load_4d(smem + st * kTcStage + lane * box, &mapK, &sh->full_k[st], 0, kvh, 0, blk, pol);
+        tma_load_4d(smem + st * kTcStage + lane * box, &mapK, &sh->full_k[st], 0, rowh, 0, blk, pol);
       issued_k = j + 1;
       if (lane == 0) ok = tc_wait(&sh->empty_v[st], ph, abort_flag);
       if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
       if (lane == 0) mbar_arrive_expect_tx(&sh->full_v[st], (uint32_t)nb * box);
       __syncwarp();
       if (lane < nb)
-        tma_load_4d(smem + kOffV + st * kTcStage + lane * box, &mapV, &sh->full_v[st], 0, kvh, 0, blk, pol);
+        tma_load_4d(smem + kOffV + st * kTcStage + lane * box, &mapV, &sh->full_v[st], 0, rowh, 0, blk, pol);
       issued_v = j + 1;
       if (lane < 16) {
-        sh->scl[j & 3][0][lane] = ks;
-        sh->scl[j & 3][1][lane] = vs;
+#pragma unroll
+        for (int i = 0; i < HP; ++i) {
+          sh->scl[j & 3][0][lane * HP + i] = sc.k[i];
+          sh->scl[j & 3][1][lane * HP + i] = sc.v[i];
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->scl_full[j & 3]);
       blk = blk1;
-      ks = ks1;
-      vs = vs1;
+      sc = sc1;
       blk1 = in_use(j + 2) ? checked(blk2) : 0;
-      ks1 = scale_of(p.k_scale, blk1);
-      vs1 = scale_of(p.v_scale, blk1);
+      sc1 = scales_of(blk1);
       blk2 = in_use(j + 3) ? __ldg(&row[((t0 + (j + 3) * kTcTile) >> bsh) + lane]) : 0;
     }
     // no TMA write may land after the CTA has left
@@ -276,7 +317,7 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0 && nt > 0) {
       constexpr uint32_t idS = idesc_e4m3_f32(kTcTile, N, false);
-      constexpr uint32_t idO = idesc_e4m3_f32(D, N, true);
+      constexpr uint32_t idO = idesc_e4m3_f32(128, N, true);
       auto issue_s = [&](int j) {
         const uint32_t kb = sbase + (uint32_t)(j & 1) * kTcStage;
 #pragma unroll
@@ -351,7 +392,19 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       m[h] = -INFINITY;
       l[h] = 0.f;
     }
-    float vref = 0.f;                            // 0: none yet
+    float vref[HP];                              // 0: none yet
+    int kvi[GT];
+#pragma unroll
+    for (int i = 0; i < HP; ++i) vref[i] = 0.f;
+#pragma unroll
+    for (int h = 0; h < GT; ++h) kvi[h] = kv_of(h);
+    // x[kv] for a head's kv without indexing registers
+    auto pick = [&](const float (&x)[HP], int kv) -> float {
+      float y = x[0];
+#pragma unroll
+      for (int i = 1; i < HP; ++i) y = kv == i ? x[i] : y;
+      return y;
+    };
 
     for (int j = 0; j < nt; ++j) {
       const int st = j & 1;
@@ -359,7 +412,12 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       const int t = t0 + j * kTcTile + r;
       const bool ok = t < t1;
       tc_wait(&sh->scl_full[j & 3], (uint32_t)(j >> 2) & 1u, abort_flag);
-      const float ks = sh->scl[j & 3][0][r >> bsh], vs = ok ? sh->scl[j & 3][1][r >> bsh] : 0.f;
+      float ks[HP], vs[HP];
+#pragma unroll
+      for (int i = 0; i < HP; ++i) {
+        ks[i] = sh->scl[j & 3][0][(r >> bsh) * HP + i];
+        vs[i] = ok ? sh->scl[j & 3][1][(r >> bsh) * HP + i] : 0.f;
+      }
       __syncwarp();
       tc_wait(&sh->s[st], ph, abort_flag);
       __syncwarp();
@@ -388,7 +446,14 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
         }
 #pragma unroll
         for (int h = 0; h < GT; ++h)
-          s[h] = ok ? fmaf(__uint_as_float(lo[h]), 0.0625f, __uint_as_float(hi[h])) * (qf[h] * ks) : -INFINITY;
+          s[h] = ok ? fmaf(__uint_as_float(lo[h]), 0.0625f, __uint_as_float(hi[h])) * (qf[h] * pick(ks, kvi[h])) : -INFINITY;
+      }
+      if constexpr (HP > 1) {
+        // a NaN code of another KV head in the row times this head's zeros is NaN:
+        // such a token's scores are taken from its own codes
+#pragma unroll
+        for (int h = 0; h < GT; ++h)
+          if (s[h] != s[h]) s[h] = plain_score<D>(p, b, t, h0 + min(h, gh - 1), rowh * HP + kvi[h]);
       }
       if constexpr (W) {
         if (ok) {
@@ -398,7 +463,9 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
             if (h < gh) sp[(size_t)h * Lmax] = s[h];
         }
       }
-      bool need = vs > vref;
+      bool need = false;
+#pragma unroll
+      for (int i = 0; i < HP; ++i) need = need || vs[i] > vref[i];
 #pragma unroll
       for (int h = 0; h < GT; ++h) need = need || s[h] > m[h] + kTcSlack;
       __syncwarp();
@@ -409,12 +476,19 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           const float x = warp_max(s[h]);
           if (lane == 0) sh->mx[warp][h] = x;
         }
-        const float xv = warp_max(vs);
-        if (lane == 0) sh->vmx[warp] = xv;
+#pragma unroll
+        for (int i = 0; i < HP; ++i) {
+          const float x = warp_max(vs[i]);
+          if (lane == 0) sh->vmx[warp][i] = x;
+        }
         named_sync(1, 128);
-        const float vnew = fmaxf(vref, fmaxf(fmaxf(sh->vmx[0], sh->vmx[1]), fmaxf(sh->vmx[2], sh->vmx[3])));
-        const float fv = vref > 0.f ? vref / vnew : 0.f;
-        vref = vnew;
+        float fv[HP];
+#pragma unroll
+        for (int i = 0; i < HP; ++i) {
+          const float vnew = fmaxf(vref[i], fmaxf(fmaxf(sh->vmx[0][i], sh->vmx[1][i]), fmaxf(sh->vmx[2][i], sh->vmx[3][i])));
+          fv[i] = vref[i] > 0.f ? vref[i] / vnew : 0.f;
+          vref[i] = vnew;
+        }
         float f[GT];
 #pragma unroll
         for (int h = 0; h < GT; ++h) {
@@ -423,7 +497,7 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           const float a = m[h] == -INFINITY ? 0.f : exp2f(m[h] - mn);
           m[h] = mn;
           l[h] *= a;
-          f[h] = a * fv;
+          f[h] = a * pick(fv, kvi[h]);
         }
         if (j > 0) {
           // O holds V_{j-1} P_{j-1}: this thread's head dim, every head's two columns
@@ -456,7 +530,9 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
         named_sync(1, 128);                      // mx is free again
       }
       // P: 32 p v / vref as two e4m3 terms, byte r of rows h and NH + h
-      const float vf = vref > 0.f ? kTcPScale * (vs / vref) : 0.f;
+      float vf[HP];
+#pragma unroll
+      for (int i = 0; i < HP; ++i) vf[i] = vref[i] > 0.f ? kTcPScale * (vs[i] / vref[i]) : 0.f;
       const uint32_t pb = sbase + kOffP + (uint32_t)st * (N * 128);
 #pragma unroll
       for (int h = 0; h < GT; h += 2) {
@@ -468,7 +544,7 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           p1 = s[h + 1] == -INFINITY ? 0.f : exp2f(s[h + 1] - m[h + 1]);
           l[h + 1] += p1;
         }
-        const float x0 = p0 * vf, x1 = p1 * vf;
+        const float x0 = p0 * pick(vf, kvi[h]), x1 = GT > 1 ? p1 * pick(vf, kvi[h + (GT > 1)]) : 0.f;
         const uint32_t hi = e4m3x2(x0, x1);
         float y0, y1;
         from_e4m3x2(hi, y0, y1);
@@ -510,19 +586,21 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       tc_wait(&sh->pv[(nt - 1) & 1], (uint32_t)((nt - 1) >> 1) & 1u, abort_flag);
       __syncwarp();
       tc_fence_after();
-      const float up = vref * (1.f / kTcPScale);
+      float up[HP];
+#pragma unroll
+      for (int i = 0; i < HP; ++i) up[i] = vref[i] * (1.f / kTcPScale);
       if constexpr (NH == 8) {
         uint32_t v[16];
         tmem_ld16(tO + lane_off, v);
         tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < GT; ++h) o[h] = fmaf(__uint_as_float(v[8 + h]), 0.0625f, __uint_as_float(v[h])) * up;
+        for (int h = 0; h < GT; ++h) o[h] = fmaf(__uint_as_float(v[8 + h]), 0.0625f, __uint_as_float(v[h])) * pick(up, kvi[h]);
       } else {
         uint32_t v[32];
         tmem_ld32(tO + lane_off, v);
         tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < GT; ++h) o[h] = fmaf(__uint_as_float(v[16 + h]), 0.0625f, __uint_as_float(v[h])) * up;
+        for (int h = 0; h < GT; ++h) o[h] = fmaf(__uint_as_float(v[16 + h]), 0.0625f, __uint_as_float(v[h])) * pick(up, kvi[h]);
       }
     }
 #pragma unroll
@@ -531,10 +609,13 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       const float den = (sh->mx[0][h] + sh->mx[1][h]) + (sh->mx[2][h] + sh->mx[3][h]);
       const size_t bh = (size_t)b * p.Hq + h0 + h;
       const size_t slot = bh * p.max_parts + part;
-      if (nparts > 1)
-        p.ws_o[slot * D + r] = o[h];
-      else
-        static_cast<__nv_bfloat16*>(p.out)[bh * D + r] = __float2bfloat16_rn(den > 0.f ? o[h] / den : 0.f);
+      const int d = r - kvi[h] * D;              // the row's columns of the head's own KV head
+      if (HP == 1 || (d >= 0 && d < D)) {
+        if (nparts > 1)
+          p.ws_o[slot * D + d] = o[h];
+        else
+          static_cast<__nv_bfloat16*>(p.out)[bh * D + d] = __float2bfloat16_rn(den != 0.f ? o[h] / den : 0.f);
+      }
       if (r == 0 && (W || nparts > 1)) {
         p.ws_ml[slot * 2] = m[h];
         p.ws_ml[slot * 2 + 1] = den;

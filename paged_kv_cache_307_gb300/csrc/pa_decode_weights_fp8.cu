@@ -23,12 +23,23 @@ Launch pick_gt(int gt, int hg) {
   return pick_hg<D, 1>(hg);
 }
 
-// tcgen05 instances (head_dim 128): gt query heads of a KV head per CTA.
-template <int GT>
+// tcgen05 instances: gt query heads per CTA, 128 / head_dim KV heads per row of codes.
+template <int GT, int HP>
 Launch pick_tc(size_t* smem) {
   *smem = tc_smem_bytes<(GT <= 8 ? 8 : 16)>();
-  return {reinterpret_cast<const void*>(&tc_decode_kernel<GT, true>),
-          reinterpret_cast<const void*>(&weights_kernel<B16, 128>)};
+  return {reinterpret_cast<const void*>(&tc_decode_kernel<GT, HP, true>),
+          reinterpret_cast<const void*>(&weights_kernel<B16, 128 / HP>)};
+}
+
+template <int HP>
+Launch pick_tc_gt(int gt, size_t* smem) {
+  if (gt > 8) return pick_tc<16, HP>(smem);
+  if (gt > 4) return pick_tc<8, HP>(smem);
+  if constexpr (HP == 1)
+    if (gt == 1) return pick_tc<1, HP>(smem);
+  if constexpr (HP <= 2)
+    if (gt <= 2) return pick_tc<2, HP>(smem);
+  return pick_tc<4, HP>(smem);
 }
 
 }  // namespace
@@ -39,12 +50,10 @@ Launch pick_decode_weights_fp8(int head_dim, int gt, int hg) {
   return pick_gt<128>(gt, hg);
 }
 
-Launch pick_decode_weights_fp8_tc(int gt, size_t* smem) {
-  if (gt > 8) return pick_tc<16>(smem);
-  if (gt > 4) return pick_tc<8>(smem);
-  if (gt > 2) return pick_tc<4>(smem);
-  if (gt > 1) return pick_tc<2>(smem);
-  return pick_tc<1>(smem);
+Launch pick_decode_weights_fp8_tc(int head_dim, int gt, size_t* smem) {
+  if (head_dim == 32) return pick_tc_gt<4>(gt, smem);
+  if (head_dim == 64) return pick_tc_gt<2>(gt, smem);
+  return pick_tc_gt<1>(gt, smem);
 }
 
 unsigned fetch_status_decode_weights_fp8() {

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const Params p) {
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l != 0.f ? 1.f / l : 0.f;
   __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + ((size_t)row * p.Hq + hq) * D + lane * DPL;
 #pragma unroll
   for (int d = 0; d < DPL; ++d) orow[d] = __float2bfloat16_rn(o[d] * inv);
@@ -564,7 +564,7 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
       have = __all_sync(0xffffffffu, ok);
       tc_fence_after();
     }
-    const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+    const float inv = lsum != 0.f ? 1.f / lsum : 0.f;
     const bool full = nt > 0 && q0 + QP <= nq;
     unsigned char* orow = static_cast<unsigned char*>(p.out) +
                           (((size_t)qrow0 + q0 + qi) * p.Hq + (size_t)kvh * p.G + hh) * 256;

@@ -90,6 +90,26 @@ def test_weights_sharp_softmax(pa):
         check(w, wref, wtol)
 
 
+@pytest.mark.parametrize("pool,Hq,Hkv,D", [("f32", 4, 2, 32), ("bf16", 4, 4, 128), ("bf16", 8, 2, 128), ("e4m3", 4, 4, 64)])
+def test_weights_nan_key_makes_nan_of_its_head(pa, pool, Hq, Hkv, D):
+    c = Case(pool, [150, 1], Hq, Hkv, D, 16, seed=6)
+    c.k[c.tab[0, 1].long(), 3, 1, 5] = 0x7F if pool == "e4m3" else float("nan")
+    c.k[c.tab[1, 0].long(), 0, 0, 5] = 0x7F if pool == "e4m3" else float("nan")
+    c.cuda()
+    out, w = torch.empty_like(c.q), torch.zeros(2, Hkv, c.tab.shape[1] * 16, device="cuda")
+    pa.decode_weights(out, w, c.q, c.k, c.v, c.tab, c.lens, c.scale, k_scale=c.ks, v_scale=c.vs)
+    assert pa.last_error() == 0
+    G = Hq // Hkv
+    nan = torch.zeros(out.shape, dtype=torch.bool)
+    nan[0, G:2 * G] = True
+    nan[1, :G] = True
+    assert torch.equal(out.isnan().cpu(), nan)
+    wn = torch.zeros(w.shape, dtype=torch.bool)
+    wn[0, 1, :150] = True
+    wn[1, 0, :1] = True
+    assert torch.equal(w.isnan().cpu(), wn)
+
+
 def test_weights_many_sequences(pa):
     rng = np.random.default_rng(0)
     c = Case("bf16", rng.integers(0, 40, 1100), 4, 2, 64, 16, seed=1)

@@ -139,7 +139,9 @@ LENS = [1, 0, 15, 16, 17, 300, 700, 129, 128]
 
 @pytest.mark.parametrize("Hq,Hkv,D,bs", [(8, 8, 128, 16), (8, 2, 128, 16), (32, 8, 128, 16), (16, 4, 64, 8), (12, 4, 128, 16),
                                          (4, 4, 32, 4), (14, 2, 128, 32), (16, 1, 128, 8), (6, 3, 128, 8), (5, 5, 64, 32),
-                                         (64, 2, 128, 16), (8, 1, 128, 4), (7, 1, 128, 16), (24, 3, 64, 16), (18, 2, 128, 16)])
+                                         (64, 2, 128, 16), (8, 1, 128, 4), (7, 1, 128, 16), (24, 3, 64, 16), (18, 2, 128, 16),
+                                         (8, 8, 64, 16), (4, 2, 64, 32), (12, 12, 32, 8), (20, 4, 32, 16), (40, 4, 64, 16),
+                                         (4, 4, 32, 16), (6, 2, 64, 16)])
 @pytest.mark.parametrize("partition", [0, 64, -1])
 def test_decode(pa, Hq, Hkv, D, bs, partition):
     c = Case("e4m3", LENS, Hq, Hkv, D, bs, seed=Hq + bs)
@@ -175,6 +177,25 @@ def test_decode_bad_block_and_length(pa):
     out = torch.empty_like(c.q)
     pa.decode_fp8_blocks(out, c.q, c.k, c.v, c.ks, c.vs, c.tab, c.lens, c.scale)
     assert pa.last_error() == pa.DEV_BAD_BLOCK | pa.DEV_BAD_LEN
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (4, 4, 64), (8, 4, 32), (3, 3, 64)])
+def test_decode_nan_stays_in_its_head(pa, Hq, Hkv, D):
+    """A NaN key makes NaN of its own KV head's query heads, a NaN value of its own dim, and of nothing else."""
+    c = Case("e4m3", [150, 40], Hq, Hkv, D, 16, seed=6)
+    ref, tol = reference(c)
+    c.k[c.tab[0, 1].long(), 3, 1, 5] = 0x7F
+    c.v[c.tab[1, 0].long(), 2, 0, 7] = 0xFF
+    c.cuda()
+    out = torch.empty_like(c.q)
+    pa.decode_fp8_blocks(out, c.q, c.k, c.v, c.ks, c.vs, c.tab, c.lens, c.scale)
+    assert pa.last_error() == 0
+    G = Hq // Hkv
+    nan = torch.zeros(out.shape, dtype=torch.bool)
+    nan[0, G:2 * G] = True
+    nan[1, :G, 7] = True
+    assert torch.equal(out.isnan().cpu(), nan)
+    check(torch.where(nan.cuda(), torch.zeros_like(out), out), np.where(nan.numpy(), 0, ref), tol)
 
 
 def test_decode_many_sequences(pa):
