@@ -236,6 +236,26 @@ template <> struct Elem<fp8e4m3b> : Elem<fp8e4m3> {};
 // to whole 16-byte chunks, so that a row can be moved by bulk copies.
 __host__ __device__ __forceinline__ constexpr int scale_row(int num_kv_heads) { return (num_kv_heads + 3) & ~3; }
 
+// Warp-collective: the last sequence i < n whose first unit
+//   floor(start[i] / per) + mul * i
+// is not above u, 0 if there is none (start non-decreasing; any other array still
+// gives an index in range).  32 candidates a step, so that a batch of up to 1024
+// costs two memory latencies and not ten.
+__device__ __forceinline__ int find_unit(const int32_t* start, int n, int per, int mul, int u) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0;
+  while (n > 1) {
+    const int step = (n + 31) >> 5;
+    const int i = lane * step;
+    const bool le = i < n && __ldg(&start[lo + i]) / per + mul * (lo + i) <= u;
+    const int c = __popc(__ballot_sync(0xffffffffu, le));
+    const int at = c > 0 ? (c - 1) * step : 0;
+    lo += at;
+    n = min(step, n - at);
+  }
+  return lo;
+}
+
 inline int elem_bytes(pa_dtype dt) { return dt == PA_F32 ? 4 : dt == PA_FP8_E4M3 ? 1 : 2; }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

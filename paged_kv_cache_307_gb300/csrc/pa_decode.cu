@@ -89,37 +89,6 @@ struct MapKey {
 };
 std::map<MapKey, CUtensorMap> g_maps;
 
-// swz = false: box {D, boxh heads, bs, 1 block}, no swizzle (CUDA-core path).
-// swz = true: box {64, 1 head, bs, 1 block}, 128-byte swizzle (tensor-core path).
-bool get_map(CUtensorMap* out, const void* base, pa_dtype dt, int nb, int bs, int h, int d, int dev, bool swz,
-             int boxh) {
-  MapKey key{base, (int)dt, nb, bs, h, d, dev, swz ? 1 : 0, swz ? 1 : boxh};
-  std::lock_guard<std::mutex> lk(g_mu);
-  auto f = g_maps.find(key);
-  if (f != g_maps.end()) {
-    *out = f->second;
-    return true;
-  }
-  bool ok;
-  if (swz) {
-    const uint64_t e = (uint64_t)elem_bytes(dt);
-    const uint64_t dims[4] = {(uint64_t)d, (uint64_t)h, (uint64_t)bs, (uint64_t)nb};
-    const uint64_t str[3] = {d * e, (uint64_t)h * d * e, (uint64_t)bs * h * d * e};
-    const uint32_t box[4] = {(uint32_t)(128 / e), 1, (uint32_t)bs, 1};   // one 128-byte row span
-    ok = encode_map(out, base, dt, 4, dims, str, box, true);
-  } else {
-    const uint64_t e = (uint64_t)elem_bytes(dt);
-    const uint64_t dims[4] = {(uint64_t)d, (uint64_t)h, (uint64_t)bs, (uint64_t)nb};
-    const uint64_t str[3] = {d * e, (uint64_t)h * d * e, (uint64_t)bs * h * d * e};
-    const uint32_t box[4] = {(uint32_t)d, (uint32_t)boxh, (uint32_t)bs, 1};
-    ok = encode_map(out, base, dt, 4, dims, str, box, false);
-  }
-  if (!ok) return false;
-  if (g_maps.size() > 64) g_maps.clear();
-  g_maps[key] = *out;
-  return true;
-}
-
 int occupancy_for(const void* kernel, size_t smem, int dev) {
   std::lock_guard<std::mutex> lk(g_mu);
   auto key = std::make_tuple(kernel, dev, smem);
@@ -183,35 +152,6 @@ int resolve_partition(int max_blocks, int bs, int partition_size, int G, bool fp
   return P;
 }
 
-// Block-scaled pools that the tcgen05 kernel takes: blocks of 8 and more (its TMA
-// boxes are whole 8-row swizzle atoms), and KV heads that fill whole rows of 128
-// codes.
-bool tc_shape(int num_kv_heads, int head_dim, int block_size) {
-  return block_size >= 8 && num_kv_heads % (128 / head_dim) == 0;
-}
-// CTAs that share such a row's query heads, 16 at most each.
-int tc_subs(int G, int head_dim) { return (G * (128 / head_dim) + 15) / 16; }
-
-// Automatic split of the tcgen05 kernel, one CTA per (partition, sequence, row of
-// 128 codes): the largest of 2048, 1024 and 512 tokens that gives two CTAs per SM at
-// the table's capacity.  A CTA's start and end weigh about as much as three of
-// its 128-token tiles, so long partitions pay while there are CTAs enough: 64
-// requests x 8 KV heads over U[1024, 16384] take 374, 251, 204 and 194 us at 256,
-// 512, 1024 and 2048 tokens; one request x 8 heads at 32768 tokens 27.1, 25.1,
-// 21.8 and 29.0, eight at up to 8192 tokens 32.2, 26.8, 23.8 and 29.8.
-int resolve_partition_tc(int max_blocks, int bs, int partition_size, int G, int head_dim, int num_seqs,
-                         int num_kv_heads) {
-  const int max_ctx = max_blocks * bs;
-  if (partition_size < 0) return max_ctx;
-  int P = partition_size;
-  if (P <= 0) {
-    const long long items = (long long)num_seqs * (num_kv_heads / (128 / head_dim)) * tc_subs(G, head_dim);
-    P = 2048;
-    while (P > 512 && items * max_ctx < 2ll * 152 * P) P /= 2;
-  }
-  return P >= max_ctx ? max_ctx : P;
-}
-
 // Clears the decode kernel's item counter.  The decode kernel is its
 // programmatic dependent on eager calls: its CTAs become resident and build
 // their tables while this runs, and wait for it on the device before their
@@ -219,6 +159,39 @@ int resolve_partition_tc(int max_blocks, int bs, int partition_size, int G, int 
 __global__ void __launch_bounds__(32) decode_reset_kernel(int32_t* next) {
   asm volatile("griddepcontrol.launch_dependents;");
   if (threadIdx.x == 0) *next = 0;
+}
+
+}  // namespace
+
+// swz = false: box {D, boxh heads, bs, 1 block}, no swizzle (CUDA-core path).
+// swz = true: box {64, 1 head, bs, 1 block}, 128-byte swizzle (tensor-core path).
+bool pool_map(CUtensorMap* out, const void* base, pa_dtype dt, int nb, int bs, int h, int d, int dev, bool swz,
+             int boxh) {
+  MapKey key{base, (int)dt, nb, bs, h, d, dev, swz ? 1 : 0, swz ? 1 : boxh};
+  std::lock_guard<std::mutex> lk(g_mu);
+  auto f = g_maps.find(key);
+  if (f != g_maps.end()) {
+    *out = f->second;
+    return true;
+  }
+  bool ok;
+  if (swz) {
+    const uint64_t e = (uint64_t)elem_bytes(dt);
+    const uint64_t dims[4] = {(uint64_t)d, (uint64_t)h, (uint64_t)bs, (uint64_t)nb};
+    const uint64_t str[3] = {d * e, (uint64_t)h * d * e, (uint64_t)bs * h * d * e};
+    const uint32_t box[4] = {(uint32_t)(128 / e), 1, (uint32_t)bs, 1};   // one 128-byte row span
+    ok = encode_map(out, base, dt, 4, dims, str, box, true);
+  } else {
+    const uint64_t e = (uint64_t)elem_bytes(dt);
+    const uint64_t dims[4] = {(uint64_t)d, (uint64_t)h, (uint64_t)bs, (uint64_t)nb};
+    const uint64_t str[3] = {d * e, (uint64_t)h * d * e, (uint64_t)bs * h * d * e};
+    const uint32_t box[4] = {(uint32_t)d, (uint32_t)boxh, (uint32_t)bs, 1};
+    ok = encode_map(out, base, dt, 4, dims, str, box, false);
+  }
+  if (!ok) return false;
+  if (g_maps.size() > 64) g_maps.clear();
+  g_maps[key] = *out;
+  return true;
 }
 
 // A launch that may begin before the previous kernel on the stream has
@@ -243,8 +216,6 @@ cudaError_t launch_dependent(const void* kernel, dim3 grid, dim3 block, void** a
   }
   return cudaLaunchKernel(kernel, grid, block, args, smem, stream);
 }
-
-}  // namespace
 
 unsigned fetch_status_decode() {
   unsigned v = 0, zero = 0;
@@ -292,41 +263,16 @@ extern "C" size_t pa_decode_workspace_bytes(int num_seqs, int num_heads, int num
   return (size_t)(ml + rows * head_dim * 4 + 256);     // + the work-item counter
 }
 
-// What pa_decode_weights adds to a decode: the running totals and their row
-// stride (floats).
-struct WeightsArgs {
-  float* weights;
-  long long stride;
-};
-
-// (m, l) of every partition, the partial outputs (none when no sequence can span
-// two partitions) and the item counter: the workspace of a block-scaled decode,
-// and what a weights-mode decode has before its scores.
-static size_t partials_bytes(long long rows, int max_parts, int head_dim) {
-  const long long ml = ((rows * max_parts * 8) + 255) / 256 * 256;
-  return (size_t)(ml + (max_parts > 1 ? rows * max_parts * head_dim * 4 : 0) + 256);
-}
-
-// The partition a block-scaled decode uses.
-static int partition_blocks(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int max_blocks_per_seq,
-                            int block_size, int partition_size) {
-  const int P = partition_size_impl(true, num_seqs, num_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size,
-                                    partition_size);
-  if (P <= 0 || !supported_head_dim(head_dim) || !tc_shape(num_kv_heads, head_dim, block_size)) return P;
-  return resolve_partition_tc(max_blocks_per_seq, block_size, partition_size, num_heads / num_kv_heads, head_dim,
-                              num_seqs, num_kv_heads);
-}
-
-// Shared by pa_decode, pa_decode_fp8, pa_decode_fp8_blocks and
-// pa_decode_weights (wa not null): dtype is the query/output type, kv the
-// pool's (dtype itself, or PA_FP8_E4M3 with per-token scales, or with one scale
-// per (block, KV head) when `blk`).
+// Shared by pa_decode, pa_decode_fp8 and, for bf16 query groups on tensor cores,
+// pa_decode_weights (wa not null: its partials, counter and scores are in the
+// workspace, which holds them): dtype is the query/output type, kv the pool's
+// (dtype itself, or PA_FP8_E4M3 with per-token scales).
 static int decode_impl(void* out, const void* query, const void* k_cache, const void* v_cache,
                        const float* k_scale, const float* v_scale, const int32_t* block_tables,
                        int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int num_heads,
                        int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
                        int partition_size, void* workspace, size_t workspace_bytes, pa_dtype dtype, pa_dtype kv,
-                       void* stream, bool blk = false, const WeightsArgs* wa = nullptr) {
+                       void* stream, const WeightsArgs* wa = nullptr) {
   if (dtype != PA_F32 && dtype != PA_BF16) return PA_ERR_DTYPE;
   if (kv != dtype && !(kv == PA_FP8_E4M3 && dtype == PA_BF16)) return PA_ERR_DTYPE;
   const bool fp8 = kv == PA_FP8_E4M3;
@@ -335,46 +281,28 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
       max_blocks_per_seq <= 0)
     return PA_ERR_SHAPE;
   if (partition_size > 0 && partition_size % block_size) return PA_ERR_SHAPE;
-  if (blk && (long long)num_seqs * num_heads > 0x7fffffffll) return PA_ERR_SHAPE;
-  if (wa) {
-    // one second-kernel CTA per (sequence, KV head, kWeightTokens tokens), and the merge's
-    const long long max_ctx = (long long)max_blocks_per_seq * block_size;
-    const long long ctas = (long long)num_seqs * num_kv_heads * ((max_ctx + kWeightTokens - 1) / kWeightTokens) +
-                           (long long)num_seqs * num_heads;
-    if (wa->stride < max_ctx || num_heads / num_kv_heads > 1024 || ctas > 0x7fffffffll) return PA_ERR_SHAPE;
-  }
   if (num_seqs == 0) return PA_OK;
-  if (!out || !query || !k_cache || !v_cache || !block_tables || !context_lens || (wa && !wa->weights))
-    return PA_ERR_NULL;
+  if (!out || !query || !k_cache || !v_cache || !block_tables || !context_lens) return PA_ERR_NULL;
   if (fp8 && (!k_scale || !v_scale)) return PA_ERR_NULL;
   if (!aligned16(out) || !aligned16(query) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_ALIGN;
   if (fp8 && (!aligned16(k_scale) || !aligned16(v_scale))) return PA_ERR_ALIGN;
 
-  const int P = blk ? partition_blocks(num_seqs, num_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size,
-                                       partition_size)
-                    : resolve_partition(max_blocks_per_seq, block_size, partition_size, num_heads / num_kv_heads,
-                                        kv == PA_FP8_E4M3, num_seqs, num_kv_heads);
+  const int P = resolve_partition(max_blocks_per_seq, block_size, partition_size, num_heads / num_kv_heads,
+                                  kv == PA_FP8_E4M3, num_seqs, num_kv_heads);
   const long long max_ctx = (long long)max_blocks_per_seq * block_size;
   const int max_parts = (int)((max_ctx + P - 1) / P);
-  const size_t partials = wa ? partials_bytes((long long)num_seqs * num_heads, max_parts, head_dim) : 0;
-  const size_t need = wa ? partials + (size_t)num_seqs * num_heads * max_ctx * 4
-                   : blk ? pa_decode_fp8_blocks_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim,
-                                                                max_blocks_per_seq, block_size, partition_size)
+  const size_t need = wa ? partials_bytes((long long)num_seqs * num_heads, max_parts, head_dim)
                          : pa_decode_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim,
                                                      max_blocks_per_seq, block_size, partition_size);
-  if ((wa || blk) && need && !aligned16(workspace)) return PA_ERR_ALIGN;
   if (need && (!workspace || workspace_bytes < need)) return PA_ERR_WORKSPACE;
 
   int dev = 0;
   if (!ck(cudaGetDevice(&dev), "cudaGetDevice")) return PA_ERR_CUDA;
   CUtensorMap mapK, mapV;
   const int G = num_heads / num_kv_heads;
-  const bool use_tc = blk && tc_shape(num_kv_heads, head_dim, block_size);   // for every group size
   // Tensor cores over the query group when it is a real contraction (G >= 2).
-  const bool use_mma = !blk &&
-                       ((kv == PA_BF16 && (head_dim == 64 || head_dim == 128)) ||
-                        (kv == PA_FP8_E4M3 && head_dim == 128)) &&
-                       G >= 2 && (G & (G - 1)) == 0 && block_size >= 8;
+  const bool use_mma = (kv == PA_BF16 && bf16_mma_shape(G, head_dim, block_size)) ||
+                       (kv == PA_FP8_E4M3 && head_dim == 128 && G >= 2 && (G & (G - 1)) == 0 && block_size >= 8);
   // KV heads per work item: 4 on the tensor-core path (one warp per head,
   // the four heads' tiles loaded back to back); 1 on the CUDA-core path,
   // where a warp ring per head measured faster for MHA.
@@ -389,10 +317,8 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
                  : fp8    ? fp8_heads_per_item(num_kv_heads)
                  : mha_hg ? PA_MHA_HEADS_PER_ITEM
                           : 1;
-  const bool swz = use_mma || use_tc;
-  const int map_h = use_tc ? num_kv_heads / (128 / head_dim) : num_kv_heads, map_d = use_tc ? 128 : head_dim;
-  if (!get_map(&mapK, k_cache, kv, num_blocks, block_size, map_h, map_d, dev, swz, HG) ||
-      !get_map(&mapV, v_cache, kv, num_blocks, block_size, map_h, map_d, dev, swz, HG)) {
+  if (!pool_map(&mapK, k_cache, kv, num_blocks, block_size, num_kv_heads, head_dim, dev, use_mma, HG) ||
+      !pool_map(&mapV, v_cache, kv, num_blocks, block_size, num_kv_heads, head_dim, dev, use_mma, HG)) {
     note_host_error("cuTensorMapEncodeTiled failed for the K/V pool");
     return PA_ERR_CUDA;
   }
@@ -409,10 +335,8 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
   prm.ws_o = need ? reinterpret_cast<float*>(static_cast<char*>(workspace) + ((rows * 8) + 255) / 256 * 256)
                   : nullptr;
   // the work-item counter: the workspace's last 256 bytes
-  // (weights mode: before the scores)
-  prm.ws_next = need ? reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + (wa ? partials : need) - 256)
-                     : nullptr;
-  prm.ws_s = wa ? reinterpret_cast<float*>(static_cast<char*>(workspace) + partials) : nullptr;
+  prm.ws_next = need ? reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + need - 256) : nullptr;
+  prm.ws_s = wa ? wa->scores : nullptr;
   prm.B = num_seqs;
   prm.Hq = num_heads;
   prm.Hkv = num_kv_heads;
@@ -436,8 +360,6 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
   prm.qscale = scale * kLog2e;
   prm.k_scale = fp8 ? k_scale : nullptr;
   prm.v_scale = fp8 ? v_scale : nullptr;
-  prm.scale_row = scale_row(num_kv_heads);
-  prm.k_codes = blk ? static_cast<const uint8_t*>(k_cache) : nullptr;
   prm.tile_bytes = (uint32_t)(block_size * head_dim * elem_bytes(kv));
   // K/V stages per CTA: ~96 KB on the tensor-core path (one ring shared by
   // the four head warps), ~64 KB on the CUDA-core path (a ring per warp);
@@ -460,30 +382,12 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
   prm.spg_shift = (spg & (spg - 1)) ? -1 : (spg == 1 ? 0 : spg == 2 ? 1 : spg == 4 ? 2 : 3);
   const int S = spg * prm.WPH;
 
-  void* args[] = {&mapK, &mapV, &prm};
-  Launch L;
-  if (use_tc) {
-    // one CTA per (partition, sequence, up to 16 query heads of a row of 128 codes)
-    const int hp = 128 / head_dim;
-    prm.nsub = tc_subs(G, head_dim);
-    const long long ctas = (long long)max_parts * num_seqs * prm.nsub * (num_kv_heads / hp);
-    if (ctas > 0x7fffffffll) return PA_ERR_SHAPE;
-    const int gt = (hp * G + prm.nsub - 1) / prm.nsub;
-    size_t tc_smem = 0;
-    L = wa ? pick_decode_weights_fp8_tc(head_dim, gt, &tc_smem) : pick_decode_fp8_blocks_tc(head_dim, gt, &tc_smem);
-    if (!raise_smem_limit(L.kernel, dev)) return PA_ERR_CUDA;
-    if (!ck(cudaLaunchKernel(L.kernel, dim3((unsigned)ctas), dim3(192), args, tc_smem, (cudaStream_t)stream),
-            "cudaLaunchKernel(tc_decode_kernel)"))
-      return PA_ERR_CUDA;
-  } else {
-  L = wa && fp8         ? pick_decode_weights_fp8(head_dim, GT, prm.HG)
-                   : wa              ? pick_decode_weights(dtype == PA_F32, head_dim, GT, prm.HG, use_mma)
-                   : blk             ? pick_decode_fp8_blocks(head_dim, GT, prm.HG)
+  const Launch L = wa                ? pick_decode_weights_mma(head_dim, GT, prm.HG)
                    : fp8             ? pick_decode_fp8(head_dim, GT, prm.HG, use_mma)
                    : use_mma         ? (head_dim == 64 ? pick_mma<64>(GT, prm.HG) : pick_mma<128>(GT, prm.HG))
                    : dtype == PA_F32 ? pick1<float, float>(head_dim, GT, prm.HG)
                                      : pick1<__nv_bfloat16, __nv_bfloat16>(head_dim, GT, prm.HG);
-  const size_t smem = 2 * (size_t)S * prm.HG * prm.tile_bytes + (fp8 ? 2 * (size_t)S * (blk ? 4 : block_size) * 4 : 0) +
+  const size_t smem = 2 * (size_t)S * prm.HG * prm.tile_bytes + (fp8 ? 2 * (size_t)S * block_size * 4 : 0) +
                       (size_t)kConsumerWarps * GT * (head_dim + 2) * sizeof(float) +
                       2 * (size_t)S * sizeof(uint64_t) + 2 * kItemQ * sizeof(uint64_t) + 16 +
                       (kItemQ + 4) * sizeof(int) +
@@ -493,6 +397,7 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
   long long grid = (long long)occ * device_sm_count();
   if (grid > prm.n_virtual) grid = prm.n_virtual;
 
+  void* args[] = {&mapK, &mapV, &prm};
   if (prm.ws_next && prm.dense) {
     // items handed out at run time from the counter in the workspace
     void* rargs[] = {&prm.ws_next};
@@ -508,25 +413,8 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
                  "cudaLaunchKernel(decode_kernel)")) {
     return PA_ERR_CUDA;
   }
-  }
-  if (wa) {
-    unsigned merge_ctas = max_parts > 1 ? (unsigned)(num_seqs * num_heads) : 0u;
-    const long long ctas =
-        merge_ctas + (long long)num_seqs * num_kv_heads * ((max_ctx + kWeightTokens - 1) / kWeightTokens);
-    float* w = wa->weights;
-    long long stride = wa->stride;
-    void* wargs[] = {&prm, &w, &stride, &merge_ctas};
-    if (!ck(launch_dependent(L.merge, dim3((unsigned)ctas), dim3(kFinishThreads), wargs, 2 * (size_t)G * 4,
-                             (cudaStream_t)stream),
-            "cudaLaunchKernel(weights_kernel)"))
-      return PA_ERR_CUDA;
-  } else if (max_parts > 1 && blk) {
-    void* margs[] = {&prm};
-    if (!ck(launch_after(L.merge, dim3((unsigned)(num_seqs * num_heads)), dim3(kFinishThreads), margs,
-                         (cudaStream_t)stream),
-            "cudaLaunchKernel(merge_wide_kernel)"))
-      return PA_ERR_CUDA;
-  } else if (max_parts > 1) {
+  if (wa) return launch_weights(L, prm, *wa, stream);
+  if (max_parts > 1) {
     const long long warps = (long long)num_seqs * num_heads;
     const unsigned blocks = (unsigned)((warps * 32 + 255) / 256);
     void* margs[] = {&prm};
@@ -538,6 +426,18 @@ static int decode_impl(void* out, const void* query, const void* k_cache, const 
   }
   return PA_OK;
 }
+
+namespace pa {
+int decode_weights_mma(void* out, const void* query, const void* k_cache, const void* v_cache,
+                       const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
+                       int num_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+                       int partition_size, void* workspace, size_t workspace_bytes, const WeightsArgs& wa,
+                       void* stream) {
+  return decode_impl(out, query, k_cache, v_cache, nullptr, nullptr, block_tables, max_blocks_per_seq, context_lens,
+                     num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, partition_size,
+                     workspace, workspace_bytes, PA_BF16, PA_BF16, stream, &wa);
+}
+}  // namespace pa
 
 extern "C" int pa_decode(void* out, const void* query, const void* k_cache, const void* v_cache,
                          const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
@@ -558,61 +458,6 @@ extern "C" int pa_decode_fp8(void* out, const void* query, const void* k_cache, 
   return decode_impl(out, query, k_cache, v_cache, k_scale, v_scale, block_tables, max_blocks_per_seq,
                      context_lens, num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
                      partition_size, workspace, workspace_bytes, dtype, PA_FP8_E4M3, stream);
-}
-
-extern "C" int pa_decode_fp8_blocks(void* out, const void* query, const void* k_cache, const void* v_cache,
-                                    const float* k_scale, const float* v_scale, const int32_t* block_tables,
-                                    int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
-                                    int num_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
-                                    float scale, int partition_size, void* workspace, size_t workspace_bytes,
-                                    pa_dtype dtype, void* stream) {
-  return decode_impl(out, query, k_cache, v_cache, k_scale, v_scale, block_tables, max_blocks_per_seq,
-                     context_lens, num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
-                     partition_size, workspace, workspace_bytes, dtype, PA_FP8_E4M3, stream, true);
-}
-
-extern "C" int pa_decode_fp8_blocks_partition_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
-                                                   int max_blocks_per_seq, int block_size, int partition_size) {
-  return partition_blocks(num_seqs, num_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size,
-                          partition_size);
-}
-
-extern "C" size_t pa_decode_fp8_blocks_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
-                                                       int max_blocks_per_seq, int block_size, int partition_size) {
-  const int P = partition_blocks(num_seqs, num_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size,
-                                 partition_size);
-  if (P <= 0 || num_seqs <= 0) return 0;
-  const long long max_ctx = (long long)max_blocks_per_seq * block_size;
-  const int max_parts = (int)((max_ctx + P - 1) / P);
-  return max_parts > 1 ? partials_bytes((long long)num_seqs * num_heads, max_parts, head_dim) : 0;
-}
-
-extern "C" size_t pa_decode_weights_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
-                                                    int max_blocks_per_seq, int block_size, int partition_size,
-                                                    pa_dtype kv_dtype) {
-  const int P = kv_dtype == PA_FP8_E4M3
-                    ? partition_blocks(num_seqs, num_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size,
-                                       partition_size)
-                    : partition_size_impl(false, num_seqs, num_heads, num_kv_heads, head_dim, max_blocks_per_seq,
-                                          block_size, partition_size);
-  if (P <= 0 || num_seqs <= 0) return 0;
-  const long long max_ctx = (long long)max_blocks_per_seq * block_size;
-  const long long rows = (long long)num_seqs * num_heads;
-  return partials_bytes(rows, (int)((max_ctx + P - 1) / P), head_dim) + (size_t)(rows * max_ctx * 4);
-}
-
-extern "C" int pa_decode_weights(void* out, float* weights, long long weights_stride, const void* query,
-                                 const void* k_cache, const void* v_cache, const float* k_scale,
-                                 const float* v_scale, const int32_t* block_tables, int max_blocks_per_seq,
-                                 const int32_t* context_lens, int num_seqs, int num_heads, int num_kv_heads,
-                                 int head_dim, int block_size, int num_blocks, float scale, int partition_size,
-                                 void* workspace, size_t workspace_bytes, pa_dtype dtype, pa_dtype kv_dtype,
-                                 void* stream) {
-  const WeightsArgs wa{weights, weights_stride};
-  return decode_impl(out, query, k_cache, v_cache, k_scale, v_scale, block_tables, max_blocks_per_seq,
-                     context_lens, num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
-                     partition_size, workspace, workspace_bytes, dtype, kv_dtype, stream, kv_dtype == PA_FP8_E4M3,
-                     &wa);
 }
 
 // ---------------------------------------------------------------------------

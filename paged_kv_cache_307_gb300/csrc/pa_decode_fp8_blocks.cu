@@ -2,11 +2,10 @@
 // scale per (block, KV head).
 //
 // Blocks of 8 to 32 whose KV heads fill whole rows of 128 codes run
-// tc_decode_kernel (pa_decode_tc.cuh); the rest runs the CUDA-core form of pa_decode_kernel.cuh with KT = fp8e4m3b:
-// with each stage the producer moves the 16-byte chunk of the block's scale row
-// that holds the item's heads, and a consumer warp reads its head's one value
-// for all of the block's tokens.  Queries and output are bf16.  Compiled on its
-// own so the instances build in parallel with the others.
+// tc_decode_kernel (pa_decode_tc.cuh), the rest direct_decode_kernel
+// (pa_decode_direct.cuh).  Queries and output are bf16.  Compiled on its own so
+// the instances build in parallel with the others.
+#include "pa_decode_direct.cuh"
 #include "pa_decode_tc.cuh"
 
 namespace pa {
@@ -14,19 +13,12 @@ namespace {
 
 using B16 = __nv_bfloat16;
 
-// CUDA-core instances: 1 or 2 KV heads per item.
-template <int D, int GT>
-Launch pick_hg(int hg) {
-  const void* merge = reinterpret_cast<const void*>(&merge_wide_kernel<B16, D>);
-  if (hg == 2) return {reinterpret_cast<const void*>(&decode_kernel<B16, fp8e4m3b, D, GT, false, 2>), merge};
-  return {reinterpret_cast<const void*>(&decode_kernel<B16, fp8e4m3b, D, GT, false, 1>), merge};
-}
-
 template <int D>
-Launch pick_gt(int gt, int hg) {
-  if (gt == 4) return pick_hg<D, 4>(hg);
-  if (gt == 2) return pick_hg<D, 2>(hg);
-  return pick_hg<D, 1>(hg);
+Launch pick_direct(int gt) {
+  const void* fin = reinterpret_cast<const void*>(&merge_wide_kernel<B16, D>);
+  if (gt > 2) return {reinterpret_cast<const void*>(&direct_decode_kernel<B16, fp8e4m3b, D, 4, false>), fin};
+  if (gt > 1) return {reinterpret_cast<const void*>(&direct_decode_kernel<B16, fp8e4m3b, D, 2, false>), fin};
+  return {reinterpret_cast<const void*>(&direct_decode_kernel<B16, fp8e4m3b, D, 1, false>), fin};
 }
 
 // tcgen05 instances: gt query heads per CTA, 128 / head_dim KV heads per row of codes.
@@ -50,10 +42,10 @@ Launch pick_tc_gt(int gt, size_t* smem) {
 
 }  // namespace
 
-Launch pick_decode_fp8_blocks(int head_dim, int gt, int hg) {
-  if (head_dim == 32) return pick_gt<32>(gt, hg);
-  if (head_dim == 64) return pick_gt<64>(gt, hg);
-  return pick_gt<128>(gt, hg);
+Launch pick_decode_fp8_blocks(int head_dim, int gt) {
+  if (head_dim == 32) return pick_direct<32>(gt);
+  if (head_dim == 64) return pick_direct<64>(gt);
+  return pick_direct<128>(gt);
 }
 
 Launch pick_decode_fp8_blocks_tc(int head_dim, int gt, size_t* smem) {

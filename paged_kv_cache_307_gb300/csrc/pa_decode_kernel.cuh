@@ -59,20 +59,10 @@
 //    issued before the CTA exits.
 #pragma once
 
-#include <type_traits>
-
 #include "pa_common.cuh"
 #include "pa_mma.cuh"
 
 namespace pa {
-namespace {
-
-__device__ unsigned g_status_decode;
-
-constexpr int kConsumerWarps = 4;
-constexpr int kThreads = (kConsumerWarps + 1) * 32;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr uint32_t kSmemAlign = 1024;
 
 struct DecodeParams {
   void* out;
@@ -101,6 +91,17 @@ struct DecodeParams {
   int32_t* ws_next;     // item counter in the workspace, zero at launch; null: items by static striding
   int lpt;              // dense order: partial last partitions after all full ones, largest first
 };
+
+namespace {
+
+__device__ unsigned g_status_decode;
+
+constexpr int kConsumerWarps = 4;
+constexpr int kThreads = (kConsumerWarps + 1) * 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kTcThreads = 192;        // tc_decode_kernel (pa_decode_tc.cuh)
+constexpr int kDirectThreads = 128;    // direct_decode_kernel (pa_decode_direct.cuh)
+constexpr uint32_t kSmemAlign = 1024;
 
 struct Item {
   int b, kvh0, sg, part, t1, jb, je;
@@ -191,10 +192,10 @@ __device__ __forceinline__ bool decode_item(const DecodeParams& p, long long v, 
 }
 
 // T: query/output element type; KT: K/V pool element type (T itself, or
-// e4m3 codes with a per-token scale for K and for V, or e4m3 codes with one
-// scale per (block, KV head)).  W: weights mode: every valid token's scores
-// (log2 units, fp32) go to ws_s and every item's (m, l) to ws_ml, split or not,
-// for weights_kernel to turn into softmax weights.
+// e4m3 codes with a per-token scale for K and for V).  W (bf16 tensor-core
+// instances): weights mode: every valid token's scores (log2 units, fp32) go to
+// ws_s and every item's (m, l) to ws_ml, split or not, for weights_kernel to turn
+// into softmax weights.
 // e4m3 tensor-core instances are held to three CTAs per SM (at most 136
 // registers): their per-block conversion work needs the extra warps to hide
 // latency (20 % faster on the grouped-query workload than two CTAs per SM).
@@ -209,8 +210,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
               const DecodeParams p) {
   using E = Elem<T>;                           // queries and output
   using EK = Elem<KT>;                         // K/V pool
-  constexpr bool SCALED = EK::kBytes == 1;     // e4m3 codes with scales
-  constexpr bool BLK = std::is_same<KT, fp8e4m3b>::value;   // one scale per (block, KV head), else per token
+  constexpr bool SCALED = EK::kBytes == 1;     // e4m3 codes with per-token scales
   constexpr int CHUNKS = D * EK::kBytes / 16;  // 16-byte chunks per token row
   // chunks per lane: two, except for e4m3 with several query heads, where
   // two chunks (32 dims) per lane would need 2*GT*32 registers for q and o
@@ -227,6 +227,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
   static_assert(LPT >= 1 && LPT <= 32 && (32 % LPT) == 0, "lane split");
   static_assert(QPC >= 1 && EPC % E::kPerChunk == 0, "query chunking");
   static_assert(!(SCALED && MMA) || D == 128, "e4m3 tensor-core path: head_dim 128");
+  static_assert(!W || (MMA && !SCALED), "weights mode: bf16 on tensor cores");
 
   constexpr int WPH = kConsumerWarps / HG;               // warp groups (warps sharing a head)
   static_assert(HG == 1 || HG == 2 || HG == 4, "KV heads per item");
@@ -239,11 +240,9 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
   unsigned char* tilesK = smem;
   unsigned char* tilesV = smem + (size_t)S * stage_bytes;
   // e4m3 pools: each stage also holds the block's bs K scales and bs V scales
-  // (per-block scales: the 16-byte chunk of the scale row with the item's heads)
-  const int scl_n = BLK ? 4 : p.bs;
   float* sclK = reinterpret_cast<float*>(tilesV + (size_t)S * stage_bytes);
-  float* sclV = sclK + (SCALED ? S * scl_n : 0);
-  float* mbuf = sclV + (SCALED ? S * scl_n : 0);
+  float* sclV = sclK + (SCALED ? S * p.bs : 0);
+  float* mbuf = sclV + (SCALED ? S * p.bs : 0);
   uint64_t* full = reinterpret_cast<uint64_t*>(mbuf + NCW * GT * (D + 2));
   uint64_t* empty = full + S;
   uint64_t* qfull = empty + S;                  // [kItemQ] item queue: index written
@@ -466,7 +465,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
               atomicOr(&g_status_decode, PA_DEV_TIMEOUT);
               *abort_flag = 1;
             } else {
-              mbar_arrive_expect_tx(&full[st], 2u * stage_bytes + (SCALED ? 8u * (uint32_t)scl_n : 0u));
+              mbar_arrive_expect_tx(&full[st], 2u * stage_bytes + (SCALED ? 8u * (uint32_t)p.bs : 0u));
               go = 1;
             }
           }
@@ -483,10 +482,8 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
                             0, item.kvh0, 0, bi, pol);
               if constexpr (SCALED) {
                 if (lane == 2 || lane == 3)
-                  bulk_load((lane == 2 ? sclK : sclV) + st * scl_n,
-                            (lane == 2 ? p.k_scale : p.v_scale) +
-                                (BLK ? (size_t)bi * p.scale_row + (item.kvh0 & ~3) : (size_t)bi * p.bs),
-                            4u * scl_n, &full[st], pol);
+                  bulk_load((lane == 2 ? sclK : sclV) + st * p.bs,
+                            (lane == 2 ? p.k_scale : p.v_scale) + (size_t)bi * p.bs, 4u * p.bs, &full[st], pol);
               }
             } else if (lane < NOPS) {
               // tensor-core path: many 128-byte-swizzled column spans per
@@ -500,10 +497,8 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
                           bi, pol);
             } else if (SCALED && (lane == NOPS || lane == NOPS + 1)) {
               const bool vs = lane == NOPS + 1;
-              bulk_load((vs ? sclV : sclK) + st * scl_n,
-                        (vs ? p.v_scale : p.k_scale) +
-                            (BLK ? (size_t)bi * p.scale_row + (item.kvh0 & ~3) : (size_t)bi * p.bs),
-                        4u * scl_n, &full[st], pol);
+              bulk_load((vs ? sclV : sclK) + st * p.bs, (vs ? p.v_scale : p.k_scale) + (size_t)bi * p.bs, 4u * p.bs,
+                        &full[st], pol);
             }
           }
           if (lane == 0 && go) {
@@ -656,10 +651,8 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
           unsigned char* vt_ptr = tilesV + (size_t)st * stage_bytes + (size_t)hl * p.tile_bytes;
           const uint32_t kt = smem_u32(tilesK + (size_t)st * stage_bytes + (size_t)hl * p.tile_bytes);
           const uint32_t vt = smem_u32(vt_ptr);
-          // (token t's scale is sk[t * SS]: per-block scales are one value)
-          const float* sk = sclK + st * scl_n + (BLK ? (item.kvh0 + hl) & 3 : 0);
-          const float* sv = sclV + st * scl_n + (BLK ? (item.kvh0 + hl) & 3 : 0);
-          constexpr int SS = BLK ? 0 : 1;
+          const float* sk = sclK + st * p.bs;
+          const float* sv = sclV + st * p.bs;
           if (valid < p.bs) {
             for (int idx = lane; idx < (p.bs - valid) * 8; idx += 32)
               *reinterpret_cast<uint4*>(vt_ptr + (valid + idx / 8) * 128 + (idx % 8) * 16) =
@@ -668,13 +661,9 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
             __syncwarp();
           }
           float vmax = 0.f;
-          if constexpr (BLK) {
-            vmax = sv[0];
-          } else {
-            for (int t = lane; t < valid; t += 32) vmax = fmaxf(vmax, sv[t]);
+          for (int t = lane; t < valid; t += 32) vmax = fmaxf(vmax, sv[t]);
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
-          }
+          for (int off = 16; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
           if (vmax > 0.f) {
             const int ve = ilogbf(vmax) + 1;
             if (ve > rexp) {
@@ -715,18 +704,11 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
             }
             const int t0 = tb + g, t1 = tb + g + 8;
             const bool ok0 = t0 < valid, ok1 = t1 < valid;
-            const float f0 = ok0 ? sfac * sk[t0 * SS] : 0.f, f1 = ok1 ? sfac * sk[t1 * SS] : 0.f;
+            const float f0 = ok0 ? sfac * sk[t0] : 0.f, f1 = ok1 ? sfac * sk[t1] : 0.f;
             St[0] = ok0 ? St[0] * f0 : -INFINITY;
             St[1] = ok0 ? St[1] * f0 : -INFINITY;
             St[2] = ok1 ? St[2] * f1 : -INFINITY;
             St[3] = ok1 ? St[3] * f1 : -INFINITY;
-            if constexpr (W) {
-              const int tk = (item.jb + i) * p.bs;
-              put_score(ok0, 2 * tq, tk + t0, St[0]);
-              put_score(ok0, 2 * tq + 1, tk + t0, St[1]);
-              put_score(ok1, 2 * tq, tk + t1, St[2]);
-              put_score(ok1, 2 * tq + 1, tk + t1, St[3]);
-            }
             float alpha[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -748,7 +730,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
                 OT[c][3] *= alpha[1];
               }
             }
-            const float vs0 = ok0 ? sv[t0 * SS] * vdown : 0.f, vs1 = ok1 ? sv[t1 * SS] * vdown : 0.f;
+            const float vs0 = ok0 ? sv[t0] * vdown : 0.f, vs1 = ok1 ? sv[t1] * vdown : 0.f;
             float pw[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -890,10 +872,8 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
           unsigned char* vt_ptr = tilesV + (size_t)st * stage_bytes + (size_t)hl * p.tile_bytes;
           const uint32_t kt = smem_u32(tilesK + (size_t)st * stage_bytes + (size_t)hl * p.tile_bytes);
           const uint32_t vt = smem_u32(vt_ptr);
-          // (token t's scale is sk[t * SS]: per-block scales are one value)
-          const float* sk = sclK + st * scl_n + (BLK ? (item.kvh0 + hl) & 3 : 0);
-          const float* sv = sclV + st * scl_n + (BLK ? (item.kvh0 + hl) & 3 : 0);
-          constexpr int SS = BLK ? 0 : 1;
+          const float* sk = sclK + st * p.bs;
+          const float* sv = sclV + st * p.bs;
           if (valid < p.bs) {
             // slots past the context may hold anything (NaN codes): clear
             // those V rows (P is 0 there, but 0 * NaN would be NaN)
@@ -905,13 +885,9 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
           }
           // V-scale reference for this block (valid tokens only)
           float vmax = 0.f;
-          if constexpr (BLK) {
-            vmax = sv[0];
-          } else {
-            for (int t = lane; t < valid; t += 32) vmax = fmaxf(vmax, sv[t]);
+          for (int t = lane; t < valid; t += 32) vmax = fmaxf(vmax, sv[t]);
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
-          }
+          for (int off = 16; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
           if (vmax > 0.f) {
             const int ve = ilogbf(vmax) + 1;          // 2^ve > vmax
             if (ve > rexp) {
@@ -959,9 +935,8 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
               for (int e = 0; e < 4; ++e) {
                 const int t = tb + n * 8 + 2 * tq + (e & 1);
                 const bool ok = t < valid;
-                S[n][e] = ok ? S[n][e] * (sfac * sk[t * SS]) : -INFINITY;
-                if (e < 2) vsc[n][e] = ok ? sv[t * SS] * vdown : 0.f;
-                if constexpr (W) put_score(ok, g + 8 * (e >> 1), (item.jb + i) * p.bs + t, S[n][e]);
+                S[n][e] = ok ? S[n][e] * (sfac * sk[t]) : -INFINITY;
+                if (e < 2) vsc[n][e] = ok ? sv[t] * vdown : 0.f;
                 mx[e >> 1] = fmaxf(mx[e >> 1], S[n][e]);
               }
             float alpha[2];
@@ -1430,14 +1405,13 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
               }
               // e4m3: the token's K scale multiplies its whole score
               float ksc = 1.f;
-              if constexpr (SCALED) ksc = ok ? sclK[st * scl_n + (BLK ? (item.kvh0 + hl) & 3 : t)] : 0.f;
+              if constexpr (SCALED) ksc = ok ? sclK[st * p.bs + t] : 0.f;
   #pragma unroll
               for (int h = 0; h < GT; ++h) {
   #pragma unroll
                 for (int off = LPT / 2; off > 0; off >>= 1)
                   part[h] += __shfl_xor_sync(0xffffffffu, part[h], off);
                 s[k][h] = ok ? part[h] * ksc : -INFINITY;
-                if constexpr (W) put_score(ok && li == 0, h, (item.jb + i) * p.bs + t, s[k][h]);
               }
             }
   #pragma unroll
@@ -1471,7 +1445,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
                              vf + hf * EPC);
                 // e4m3: the token's V scale rides on its softmax weight
                 float vsc = 1.f;
-                if constexpr (SCALED) vsc = sclV[st * scl_n + (BLK ? (item.kvh0 + hl) & 3 : t)];
+                if constexpr (SCALED) vsc = sclV[st * p.bs + t];
   #pragma unroll
                 for (int h = 0; h < GT; ++h) {
                   const float pk = exp2f(s[k][h] - m[h]);
@@ -1541,9 +1515,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
 #pragma unroll
       for (int g = 0; g < WPH; ++g) M = fmaxf(M, mbuf[((g * HG + hh) * GT + h) * (D + 2) + D]);
       float num = 0.f, den = 0.f;
-      // (block-scaled pools and weights mode let a NaN sum through)
-      constexpr bool kNan = BLK || W;
-      if (kNan || M != -INFINITY) {
+      if (W || M != -INFINITY) {           // (weights mode lets a NaN sum through)
 #pragma unroll
         for (int g = 0; g < WPH; ++g) {
           const float* src = mbuf + ((g * HG + hh) * GT + h) * (D + 2);
@@ -1554,7 +1526,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
       }
       const size_t bh = (size_t)item.b * p.Hq + (size_t)(item.kvh0 + hh) * p.G + item.sg * GT + h;
       if (!item.split) {
-        E::store1(static_cast<T*>(p.out) + bh * D + d, (kNan ? den != 0.f : den > 0.f) ? num / den : 0.f);
+        E::store1(static_cast<T*>(p.out) + bh * D + d, (W ? den != 0.f : den > 0.f) ? num / den : 0.f);
         if constexpr (W) {
           if (d == 0) {
             p.ws_ml[bh * p.max_parts * 2] = M;
@@ -1799,18 +1771,57 @@ struct Launch {
   const void* merge;
 };
 
+// bf16 pools: whether decode runs on tensor cores (mma.sync).
+inline bool bf16_mma_shape(int G, int head_dim, int block_size) {
+  return (head_dim == 64 || head_dim == 128) && G >= 2 && (G & (G - 1)) == 0 && block_size >= 8;
+}
+
+// pa_decode.cu: the tensor map of a K/V pool, cached per pool (box {D, boxh heads,
+// bs, 1 block}, or with swz one 128-byte swizzled row span), and a launch that may
+// begin before the previous kernel on the stream has completed (a plain one under
+// stream capture).
+bool pool_map(CUtensorMap* out, const void* base, pa_dtype dt, int nb, int bs, int h, int d, int dev, bool swz,
+              int boxh);
+cudaError_t launch_dependent(const void* kernel, dim3 grid, dim3 block, void** args, size_t smem,
+                             cudaStream_t stream);
+
+// What pa_decode_weights adds to a decode: the running totals, their row stride
+// (floats), and the scores in the workspace.
+struct WeightsArgs {
+  float* weights;
+  long long stride;
+  float* scores;
+};
+// (m, l) of every partition, the partial outputs (none when no sequence can span
+// two partitions) and the item counter: the workspace of a block-scaled decode,
+// and what a weights-mode decode has before its scores.  rows = sequences x heads.
+inline size_t partials_bytes(long long rows, int max_parts, int head_dim) {
+  const long long ml = ((rows * max_parts * 8) + 255) / 256 * 256;
+  return (size_t)(ml + (max_parts > 1 ? rows * max_parts * head_dim * 4 : 0) + 256);
+}
+// The second kernel of a weights-mode decode (pa_decode_blocks.cu); PA_OK or PA_ERR_CUDA.
+int launch_weights(const Launch& L, const DecodeParams& prm, const WeightsArgs& wa, void* stream);
+// Weights mode over bf16 pools on tensor cores (pa_decode.cu).
+int decode_weights_mma(void* out, const void* query, const void* k_cache, const void* v_cache,
+                       const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
+                       int num_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+                       int partition_size, void* workspace, size_t workspace_bytes, const WeightsArgs& wa,
+                       void* stream);
+
 // e4m3-pool instances (pa_decode_fp8.cu): bf16 queries, hg KV heads per
 // work item, tensor cores (head_dim 128, gt a power of two >= 2) or CUDA cores.
 Launch pick_decode_fp8(int head_dim, int gt, int hg, bool mma);
-// The same for pools with one scale per (block, KV head): CUDA cores, and the
-// tcgen05 kernel for gt query heads per CTA (<= 16) with its shared memory
+// The same for pools with one scale per (block, KV head): the direct kernel, and
+// the tcgen05 kernel for gt query heads per CTA (<= 16) with its shared memory
 // (pa_decode_fp8_blocks.cu).
-Launch pick_decode_fp8_blocks(int head_dim, int gt, int hg);
+Launch pick_decode_fp8_blocks(int head_dim, int gt);
 Launch pick_decode_fp8_blocks_tc(int head_dim, int gt, size_t* smem);
-// Weights-mode instances: pools of the query's type (pa_decode_weights.cu) and
-// block-scaled e4m3 pools (pa_decode_weights_fp8.cu).
-Launch pick_decode_weights(bool f32, int head_dim, int gt, int hg, bool mma);
-Launch pick_decode_weights_fp8(int head_dim, int gt, int hg);
+// Weights-mode instances: pools of the query's type (pa_decode_weights.cu:
+// decode_kernel on tensor cores, or the direct kernel) and block-scaled e4m3 pools
+// (pa_decode_weights_fp8.cu).
+Launch pick_decode_weights_mma(int head_dim, int gt, int hg);
+Launch pick_decode_weights(bool f32, int head_dim, int gt);
+Launch pick_decode_weights_fp8(int head_dim, int gt);
 Launch pick_decode_weights_fp8_tc(int head_dim, int gt, size_t* smem);
 
 }  // namespace pa

@@ -54,7 +54,6 @@
 namespace pa {
 namespace {
 
-constexpr int kTcThreads = 192;
 constexpr int kTcTile = 128;               // tokens per tile
 constexpr uint32_t kTcStage = 16384;       // 128 tokens x 128 codes
 constexpr float kTcSlack = 3.f;            // log2 units a score may exceed the reference by

@@ -1,7 +1,7 @@
 // pa_decode_weights.cu — weights-mode decode instances (scores kept for
 // weights_kernel) for f32 and bf16 K/V pools.  Compiled on its own so the
 // instances build in parallel with the others.
-#include "pa_decode_kernel.cuh"
+#include "pa_decode_direct.cuh"
 
 namespace pa {
 namespace {
@@ -9,18 +9,18 @@ namespace {
 using B16 = __nv_bfloat16;
 
 template <typename T, int D>
-Launch pick_gt(int gt) {
+Launch pick_direct(int gt) {
   const void* fin = reinterpret_cast<const void*>(&weights_kernel<T, D>);
-  if (gt == 4) return {reinterpret_cast<const void*>(&decode_kernel<T, T, D, 4, false, 1, true>), fin};
-  if (gt == 2) return {reinterpret_cast<const void*>(&decode_kernel<T, T, D, 2, false, 1, true>), fin};
-  return {reinterpret_cast<const void*>(&decode_kernel<T, T, D, 1, false, 1, true>), fin};
+  if (gt > 2) return {reinterpret_cast<const void*>(&direct_decode_kernel<T, T, D, 4, true>), fin};
+  if (gt > 1) return {reinterpret_cast<const void*>(&direct_decode_kernel<T, T, D, 2, true>), fin};
+  return {reinterpret_cast<const void*>(&direct_decode_kernel<T, T, D, 1, true>), fin};
 }
 
 template <typename T>
 Launch pick_d(int d, int gt) {
-  if (d == 32) return pick_gt<T, 32>(gt);
-  if (d == 64) return pick_gt<T, 64>(gt);
-  return pick_gt<T, 128>(gt);
+  if (d == 32) return pick_direct<T, 32>(gt);
+  if (d == 64) return pick_direct<T, 64>(gt);
+  return pick_direct<T, 128>(gt);
 }
 
 // Tensor-core instances: bf16, head_dim 64 or 128, GT query heads per KV head.
@@ -42,8 +42,11 @@ Launch pick_mma(int gt, int hg) {
 
 }  // namespace
 
-Launch pick_decode_weights(bool f32, int head_dim, int gt, int hg, bool mma) {
-  if (mma) return head_dim == 64 ? pick_mma<64>(gt, hg) : pick_mma<128>(gt, hg);
+Launch pick_decode_weights_mma(int head_dim, int gt, int hg) {
+  return head_dim == 64 ? pick_mma<64>(gt, hg) : pick_mma<128>(gt, hg);
+}
+
+Launch pick_decode_weights(bool f32, int head_dim, int gt) {
   return f32 ? pick_d<float>(head_dim, gt) : pick_d<B16>(head_dim, gt);
 }
 

@@ -1,6 +1,7 @@
 // pa_decode_weights_fp8.cu — weights-mode decode instances (scores kept for
 // weights_kernel) for e4m3 K/V pools with one scale per (block, KV head).
 // Compiled on its own so the instances build in parallel with the others.
+#include "pa_decode_direct.cuh"
 #include "pa_decode_tc.cuh"
 
 namespace pa {
@@ -8,19 +9,12 @@ namespace {
 
 using B16 = __nv_bfloat16;
 
-// CUDA-core instances: 1 or 2 KV heads per item.
-template <int D, int GT>
-Launch pick_hg(int hg) {
-  const void* fin = reinterpret_cast<const void*>(&weights_kernel<B16, D>);
-  if (hg == 2) return {reinterpret_cast<const void*>(&decode_kernel<B16, fp8e4m3b, D, GT, false, 2, true>), fin};
-  return {reinterpret_cast<const void*>(&decode_kernel<B16, fp8e4m3b, D, GT, false, 1, true>), fin};
-}
-
 template <int D>
-Launch pick_gt(int gt, int hg) {
-  if (gt == 4) return pick_hg<D, 4>(hg);
-  if (gt == 2) return pick_hg<D, 2>(hg);
-  return pick_hg<D, 1>(hg);
+Launch pick_direct(int gt) {
+  const void* fin = reinterpret_cast<const void*>(&weights_kernel<B16, D>);
+  if (gt > 2) return {reinterpret_cast<const void*>(&direct_decode_kernel<B16, fp8e4m3b, D, 4, true>), fin};
+  if (gt > 1) return {reinterpret_cast<const void*>(&direct_decode_kernel<B16, fp8e4m3b, D, 2, true>), fin};
+  return {reinterpret_cast<const void*>(&direct_decode_kernel<B16, fp8e4m3b, D, 1, true>), fin};
 }
 
 // tcgen05 instances: gt query heads per CTA, 128 / head_dim KV heads per row of codes.
@@ -44,10 +38,10 @@ Launch pick_tc_gt(int gt, size_t* smem) {
 
 }  // namespace
 
-Launch pick_decode_weights_fp8(int head_dim, int gt, int hg) {
-  if (head_dim == 32) return pick_gt<32>(gt, hg);
-  if (head_dim == 64) return pick_gt<64>(gt, hg);
-  return pick_gt<128>(gt, hg);
+Launch pick_decode_weights_fp8(int head_dim, int gt) {
+  if (head_dim == 32) return pick_direct<32>(gt);
+  if (head_dim == 64) return pick_direct<64>(gt);
+  return pick_direct<128>(gt);
 }
 
 Launch pick_decode_weights_fp8_tc(int head_dim, int gt, size_t* smem) {

@@ -273,11 +273,13 @@ __global__ void __launch_bounds__(NT) select_kernel(const EvictParams p) {
   }
 }
 
+// Two conversions of two values each, the first value in the low byte.
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
-  return (uint32_t)__nv_cvt_float_to_fp8(a, __NV_SATFINITE, __NV_E4M3) |
-         (uint32_t)__nv_cvt_float_to_fp8(b, __NV_SATFINITE, __NV_E4M3) << 8 |
-         (uint32_t)__nv_cvt_float_to_fp8(c, __NV_SATFINITE, __NV_E4M3) << 16 |
-         (uint32_t)__nv_cvt_float_to_fp8(d, __NV_SATFINITE, __NV_E4M3) << 24;
+  uint32_t r;
+  asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\tmov.b32 %0, {x, y};\n\t}"
+      : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
 }
 // Sixteen codes times f.
 __device__ __forceinline__ uint4 rescale16(uint4 x, float f) {

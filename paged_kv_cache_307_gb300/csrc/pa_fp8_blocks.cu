@@ -13,14 +13,14 @@
 // fall below the smallest normal code.  So a block filled token by token holds
 // what one filled at once holds, up to those.
 //
-// One warp per (touched block, head, K|V): the block's new rows of the head
-// are read once for the maximum and once (from L1) for the codes, 16 bytes per
-// lane, D elements of a head being 4 to 32 lanes' worth.  Blocks are owned by
-// one warp each, so nothing is atomic.  Which block a warp works on needs no
-// scan over the sequences: sequence b's units start at
+// One warp per (touched block, head, K|V): the block's new rows of the head,
+// 16 bytes per lane, are read once and stay in registers from the maximum to the
+// codes (eight loads in flight per lane).  Blocks are owned by one warp each, so
+// nothing is atomic.  Which block a warp works on needs no scan over the
+// sequences: sequence b's units start at
 //   U_b = floor(query_start[b] / bs) + 2 b,
 // and n tokens touch at most floor((n - 1) / bs) + 2 blocks, which never passes
-// U_{b+1}; a binary search over query_start finds b, and surplus units leave.
+// U_{b+1}; a search over query_start finds b, and surplus units leave.
 // Bound by HBM: reads elem and writes 1 byte per element.
 #include "pa_common.cuh"
 
@@ -30,6 +30,7 @@ namespace {
 __device__ unsigned g_status_fp8_blocks;
 
 constexpr int kWarps = 4;
+constexpr int kHeld = 8;               // 16-byte chunks a lane keeps
 constexpr float kMinScale = 7.888609052210118e-31f;   // 2^-100
 constexpr float kE4m3Max = 448.f;
 
@@ -43,11 +44,13 @@ __device__ __forceinline__ float pow2_scale(float a) {
   return k < -100 ? kMinScale : __uint_as_float((uint32_t)(k + 127) << 23);
 }
 
+// Two conversions of two values each, the first value in the low byte.
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
-  return (uint32_t)__nv_cvt_float_to_fp8(a, __NV_SATFINITE, __NV_E4M3) |
-         (uint32_t)__nv_cvt_float_to_fp8(b, __NV_SATFINITE, __NV_E4M3) << 8 |
-         (uint32_t)__nv_cvt_float_to_fp8(c, __NV_SATFINITE, __NV_E4M3) << 16 |
-         (uint32_t)__nv_cvt_float_to_fp8(d, __NV_SATFINITE, __NV_E4M3) << 24;
+  uint32_t r;
+  asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\tmov.b32 %0, {x, y};\n\t}"
+      : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
 }
 
 struct AppendParams {
@@ -80,14 +83,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendParams 
     for (int i = (int)threadIdx.x; i < p.B; i += kWarps * 32)
       if (!good_seq(p, i)) atomicOr(&g_status_fp8_blocks, PA_DEV_BAD_LEN);
   }
-  // the last sequence whose first unit is not above u
-  int lo = 0, hi = p.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(&p.query_start[mid]) / p.bs + 2 * mid <= u) lo = mid;
-    else hi = mid - 1;
-  }
-  const int b = lo;
+  const int b = find_unit(p.query_start, p.B, p.bs, 2, u);
   const int s0 = __ldg(&p.query_start[b]), s1 = __ldg(&p.query_start[b + 1]);
   const int L = __ldg(&p.context_lens[b]);
   const int i = u - (s0 / p.bs + 2 * b);        // the sequence's i-th touched block
@@ -106,20 +102,34 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendParams 
   const int first = max(L - n - j * p.bs, 0);   // the block's first new slot; earlier ones hold tokens
   const int cnt = min(L - j * p.bs, p.bs) - first;
   const size_t row = (size_t)p.Hkv * p.D;       // elements from token to token, in the source and in the pool
-  const unsigned char* src = static_cast<const unsigned char*>(p.src[kv]) +
+  const unsigned char* src = static_cast<const unsigned char*>((kv ? p.src[1] : p.src[0])) +
                              ((size_t)(s0 + j * p.bs + first - (L - n)) * row + (size_t)h * p.D) * sizeof(T);
-  uint8_t* dst = p.pool[kv] + (size_t)blk * p.bs * row + (size_t)h * p.D;
-  const int cpr = p.D / EPC;                    // 16-byte source chunks per row: 4, 8, 16 or 32
+  uint8_t* dst = (kv ? p.pool[1] : p.pool[0]) + (size_t)blk * p.bs * row + (size_t)h * p.D;
+  const int csh = 31 - __clz(p.D / EPC), cpr = 1 << csh;   // 16-byte source chunks per row: 4, 8, 16 or 32
+  const int chunks = cnt << csh;
+  auto fetch = [&](int c) {
+    return ld_nc_v4(src + ((size_t)(c >> csh) * row + (size_t)(c & (cpr - 1)) * EPC) * sizeof(T));
+  };
+  // the first kHeld chunks per lane stay in registers from the maximum to the
+  // codes (all of a bf16 block of 16 x 128), the rest is read again
+  uint4 held[kHeld];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    held[k] = lane + 32 * k < chunks ? fetch(lane + 32 * k) : make_uint4(0u, 0u, 0u, 0u);
   float amax = 0.f;
-  for (int c = lane; c < cnt * cpr; c += 32) {
+  auto top = [&](const uint4& x) {
     float f[EPC];
-    E::unpack(ld_nc_v4(src + ((size_t)(c / cpr) * row + (size_t)(c % cpr) * EPC) * sizeof(T)), f);
+    E::unpack(x, f);
 #pragma unroll
     for (int e = 0; e < EPC; ++e) amax = fabsf(f[e]) <= 3.402823466e38f ? fmaxf(amax, fabsf(f[e])) : amax;
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) top(held[k]);
+#pragma unroll 4
+  for (int c = lane + 32 * kHeld; c < chunks; c += 32) top(fetch(c));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-  float* sp = p.scale[kv] + (size_t)blk * p.scale_row + h;
+  float* sp = (kv ? p.scale[1] : p.scale[0]) + (size_t)blk * p.scale_row + h;
   const float old = first > 0 ? *sp : 0.f;
   const float s = fmaxf(old, pow2_scale(amax));
   const float inv = s > 0.f ? 1.f / s : 0.f;    // exact: s is a power of two
@@ -140,20 +150,25 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendParams 
     }
   }
   dst += (size_t)first * row;
-  for (int c = lane; c < cnt * cpr; c += 32) {
-    const int t = c / cpr, d = (c % cpr) * EPC;
+  auto put = [&](int c, const uint4& x) {
     float f[EPC];
-    E::unpack(ld_nc_v4(src + ((size_t)t * row + d) * sizeof(T)), f);
+    E::unpack(x, f);
     uint32_t w[EPC / 4];
 #pragma unroll
     for (int k = 0; k < EPC / 4; ++k)
       w[k] = encode4(f[4 * k] * inv, f[4 * k + 1] * inv, f[4 * k + 2] * inv, f[4 * k + 3] * inv);
+    uint8_t* at = dst + (size_t)(c >> csh) * row + (size_t)(c & (cpr - 1)) * EPC;
     if constexpr (EPC == 8) {
-      *reinterpret_cast<uint2*>(dst + (size_t)t * row + d) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
     } else {
-      *reinterpret_cast<uint32_t*>(dst + (size_t)t * row + d) = w[0];
+      *reinterpret_cast<uint32_t*>(at) = w[0];
     }
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    if (lane + 32 * k < chunks) put(lane + 32 * k, held[k]);
+#pragma unroll 4
+  for (int c = lane + 32 * kHeld; c < chunks; c += 32) put(c, fetch(c));
 }
 
 }  // namespace

@@ -78,13 +78,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const Params p) {
     }
   }
   if (hq >= p.Hq) return;
-  int lo = 0, hi = p.B - 1;                    // the last sequence that starts at or before the row
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(&p.query_start[mid]) <= row) lo = mid;
-    else hi = mid - 1;
-  }
-  const int b = lo;
+  const int b = find_unit(p.query_start, p.B, 1, 0, row);   // the last sequence that starts at or before the row
   if (!good_rows(p, b)) return;
   const int r0 = __ldg(&p.query_start[b]), r1 = __ldg(&p.query_start[b + 1]);
   if (row < r0 || row >= r1) return;
@@ -325,13 +319,7 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
       if (!good_rows(p, i) || Li < 0 || Li > p.max_blocks * p.bs) atomicOr(&g_status_prefill_fp8, PA_DEV_BAD_LEN);
     }
   }
-  int lo = 0, hi = p.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(&p.query_start[mid]) / QP + mid <= u) lo = mid;
-    else hi = mid - 1;
-  }
-  const int b = lo;
+  const int b = find_unit(p.query_start, p.B, QP, 1, u);
   if (!good_rows(p, b)) return;
   const int qrow0 = __ldg(&p.query_start[b]);
   const int nq = __ldg(&p.query_start[b + 1]) - qrow0;

@@ -101,7 +101,7 @@ def test_workspace_arithmetic(pa):
     assert part(1, 32, 8, 128, 2048, 16, 0) == 512                # 8 x 64 >= 2 x 152 > 8 x 32
     assert part(1, 8, 8, 128, 8, 16, 0) == 128                    # never longer than the table
     assert part(1, 32, 8, 64, 2048, 16, 0) == 512                 # two heads a row of codes
-    assert part(1, 20, 5, 64, 2048, 16, 0) == 256                 # no whole rows: CUDA cores, pa_decode_fp8's
+    assert part(1, 20, 5, 64, 2048, 16, 0) == 256                 # no whole rows: CUDA cores, 5 x 128 >= 4 x 152
     assert part(1, 32, 8, 128, 2048, 16, 24) == -2 and part(1, 32, 8, 128, 2048, 16, -1) == 32768
     assert ws(1, 32, 8, 128, 2048, 16, 512) == 32 * 64 * 8 + 32 * 64 * 512 + 256
     assert ws(1, 32, 8, 128, 2048, 16, -1) == 0
