@@ -273,6 +273,11 @@ int device_sm_count();
 bool encode_map(CUtensorMap* map, const void* base, pa_dtype dt, int rank, const uint64_t* dims,
                 const uint64_t* strides, const uint32_t* box, bool swizzle128);
 
+// Host: the tensor map of a K/V pool, cached per pool (box {D, boxh heads, bs, 1
+// block}, or with swz one 128-byte swizzled row span) (pa_decode.cu).
+bool pool_map(CUtensorMap* out, const void* base, pa_dtype dt, int nb, int bs, int h, int d, int dev, bool swz,
+              int boxh);
+
 // Host: record the text of the last host-side failure (per thread); read
 // back through pa_last_host_error().
 void note_host_error(const char* what);

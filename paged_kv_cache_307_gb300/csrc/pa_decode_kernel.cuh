@@ -1776,12 +1776,8 @@ inline bool bf16_mma_shape(int G, int head_dim, int block_size) {
   return (head_dim == 64 || head_dim == 128) && G >= 2 && (G & (G - 1)) == 0 && block_size >= 8;
 }
 
-// pa_decode.cu: the tensor map of a K/V pool, cached per pool (box {D, boxh heads,
-// bs, 1 block}, or with swz one 128-byte swizzled row span), and a launch that may
-// begin before the previous kernel on the stream has completed (a plain one under
-// stream capture).
-bool pool_map(CUtensorMap* out, const void* base, pa_dtype dt, int nb, int bs, int h, int d, int dev, bool swz,
-              int boxh);
+// A launch that may begin before the previous kernel on the stream has completed (a
+// plain one under stream capture) (pa_decode.cu).
 cudaError_t launch_dependent(const void* kernel, dim3 grid, dim3 block, void** args, size_t smem,
                              cudaStream_t stream);
 

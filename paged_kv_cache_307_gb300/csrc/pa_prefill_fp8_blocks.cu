@@ -8,13 +8,13 @@
 // tile_kernel (head_dim 128): 5th-generation tensor cores.  One CTA per (query
 // tile, KV head): 128 rows = QP = 128 / G positions x G query heads, keys in
 // tiles of 64, scores and output in tensor memory.
-//  * No K or V tile goes through TMA: warps 4 (K) and 5-6 (V) read the rows
-//    of codes from the pool into registers, a tile ahead, and write them as
-//    16-bit values into the 128-byte-swizzled tiles the MMAs read.  K becomes
-//    f16 (cvt.rn.f16x2.e4m3x2, exact: every code is an f16 value) and its scale
-//    stays apart; V becomes bf16 with its scale multiplied in (exact for a power
-//    of two; bf16 has the exponents for it, so a row that attends only to
-//    blocks of small scale keeps its precision beside blocks of large scale).
+//  * The codes of K and V come by TMA into two 8 KB stages each; warp 4 (K) and
+//    warps 5-6 (V) turn a stage into the 16-bit, 128-byte-swizzled tile that the
+//    MMAs read.  K becomes f16 (cvt.rn.f16x2.e4m3x2, exact: every code is an f16 value)
+//    and its scale stays apart; V becomes bf16 with its scale multiplied in (exact
+//    for a power of two; bf16 has the exponents for it, so a row that attends only to
+//    blocks of small scale keeps its precision beside blocks of large scale).  A
+//    16-bit K tile is needed from one S to the next only, so there is one; V has two.
 //  * Q (TMA, bf16) is turned into f16 in place by the softmax warps, each row
 //    scaled by its own power of two so that its largest value is in
 //    [2^14, 2^15): exact but for values 2^-28 below that.
@@ -22,7 +22,9 @@
 //    * (row factor), running maximum and sum, P = 2^(x - m) in bf16 over the S
 //    columns, O += P V in bf16.  The reference only moves when the maximum
 //    has grown by 2^8.
-//  * Warp 7 issues S_{j+1} before P_j V_j.  Two CTAs per SM (98 KB, 256 threads: the softmax
+//  * Warp 7 issues S_{j+1} before P_j V_j, and with each the request for the codes two
+//    tiles on (a converted tile means that its stage has been read; requested by the
+//    converting warps, the copies cost each of them a third of its time).  Two CTAs per SM (98 KB, 256 threads: the softmax
 //    needs 128 registers, which two CTAs of eight warps have).
 //  * Keys at or past the context length are zeros in both tiles, whatever the
 //    pool holds there.  Every wait is bounded (2 s).
@@ -157,25 +159,30 @@ constexpr int kRows = 128;
 constexpr int kKT = 64;                // keys per tile
 constexpr uint32_t kQHalf = 16384;     // 128 rows x 64 columns of 16 bits
 constexpr uint32_t kKVHalf = 8192;     // 64 keys x 64 columns of 16 bits
+constexpr uint32_t kRaw = 8192;        // 64 keys x 128 codes
 constexpr uint32_t kOffQ = 0;
-constexpr uint32_t kOffK = 32768;      // 2 stages x 2 halves
-constexpr uint32_t kOffV = 65536;
-constexpr uint32_t kOffBar = 98304;
-constexpr uint32_t kTileSmem = kOffBar + 512 + 1024;   // + alignment slack
+constexpr uint32_t kOffK = 32768;      // one 16-bit tile: 2 halves
+constexpr uint32_t kOffV = 49152;      // two
+constexpr uint32_t kOffRawK = 81920;   // 2 stages of codes
+constexpr uint32_t kOffRawV = 98304;
+constexpr uint32_t kOffBar = 114688;
+// Two CTAs per SM have 113 KB each: no room for alignment slack.  Without static
+// shared memory the dynamic part begins on a 1024-byte boundary (checked).
+constexpr uint32_t kTileSmem = kOffBar + 1024;
 constexpr float kRescaleThreshold = 8.0f;              // log2 units
 constexpr uint32_t kTmemCols = 256;    // S (and P) at columns 0 and 64, O at 128
 constexpr uint32_t kColO = 128;
 
 struct Bars {
-  uint64_t q, qf, full_k[2], full_v[2], empty_k[2], empty_v[2], s[2], p[2], pv[2], drain;
+  uint64_t q, qf, raw_k[2], raw_v[2], full_k, full_v[2], empty_k, empty_v[2], s[2], p[2], pv[2], drain;
   // K scale of every 4 keys (block sizes are multiples of 4) of tile t in slot
-  // t & 3: K of tile t+2 and t+3 may be written while the softmax reads t's
-  // (their stages free up with S_t and S_{t+1}), t+4's only after P_t
+  // t & 3: those of t+1 and t+2 may be written while the softmax reads t's, t+3's
+  // only after P_t (its K tile waits for S_{t+2}, which is issued after P_t)
   alignas(16) float kscl[4][kKT / 4];
   uint32_t tmem_base;
   int abort;
 };
-static_assert(sizeof(Bars) <= 512 && offsetof(Bars, kscl) % 16 == 0, "barrier block");
+static_assert(sizeof(Bars) <= 1024 && offsetof(Bars, kscl) % 16 == 0, "barrier block");
 
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   if (*abort_flag) return false;
@@ -194,117 +201,111 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// K (one warp) or V (two warps): the codes of each key tile, read a tile ahead
-// into registers, written as 16-bit rows.  Thread x holds the 16-code chunk
-// x % 8 of rows x / 8 + (threads / 8) i.
+// K (one warp) or V (two warps): the codes of each key tile as 16-bit rows.  Thread x takes the 16-code chunk x % 8 of every
+// (threads / 8)-th row.
 template <bool K>
 __device__ __forceinline__ void convert_tiles(const Params& p, Bars* bars, unsigned char* smem, int b, int kvh, int kend,
                                               int nt, int x) {
-  constexpr int N = K ? 16 : 8, RS = kKT / N;     // rows a thread holds, and their distance
+  constexpr int kThr = K ? 32 : 64, RS = kThr / 8;       // threads, and the distance of a thread's rows
   volatile int* abort_flag = &bars->abort;
+  const int lane = (int)(threadIdx.x & 31);
   const int ch = x & 7, r0 = x >> 3;
   const float* scales = (K ? p.k_scale : p.v_scale) + kvh;
   const int32_t* tab = p.block_tables + (size_t)b * p.max_blocks;
-  const size_t tok = (size_t)p.Hkv * 128;
-  const uint8_t* base = (K ? p.k : p.v) + (size_t)kvh * 128 + ch * 16;
-  uint64_t* full = K ? bars->full_k : bars->full_v;
-  uint64_t* empty = K ? bars->empty_k : bars->empty_v;
+  const int bsh = 31 - __clz(p.bs), nbt = kKT >> bsh;    // blocks per tile, a lane each: at most 16
+  uint64_t* raw_full = K ? bars->raw_k : bars->raw_v;
+  const unsigned char* raw = smem + (K ? kOffRawK : kOffRawV);
   // codes 16 ch .. 16 ch + 15 are columns of half ch / 4, 16-byte chunks 2 (ch % 4) and the next
   unsigned char* tile = smem + (K ? kOffK : kOffV) + (ch >> 2) * kKVHalf;
   const int c0 = (ch & 3) * 2;
-  const int bsh = 31 - __clz(p.bs);
-  const int lane = (int)(threadIdx.x & 31), nbt = kKT >> bsh;   // blocks per tile, a lane each: at most 16
-  // lane l: the block id and scale of the tile's block l (0 where the tile has none that counts)
-  auto block_of = [&](int t) -> int {
-    const int key = t * kKT + (lane << bsh);
-    return lane < nbt && key < kend ? __ldg(&tab[key >> bsh]) : 0;
-  };
-  auto checked = [&](int blk) -> int {
-    if ((unsigned)blk < (unsigned)p.num_blocks) return blk;
+  auto in_use = [&](int t) -> bool { return t < nt && lane < nbt && t * kKT + (lane << bsh) < kend; };
+  auto id_of = [&](int t) -> int { return in_use(t) ? __ldg(&tab[((t * kKT) >> bsh) + lane]) : 0; };
+  auto checked = [&](int id) -> int {
+    if ((unsigned)id < (unsigned)p.num_blocks) return id;
     if (K) atomicOr(&g_status_prefill_fp8, PA_DEV_BAD_BLOCK);
     return 0;
   };
-  auto scale_of = [&](int blk) -> float { return lane < nbt ? __ldg(&scales[(size_t)blk * p.scale_row]) : 0.f; };
-  // (keys past the context read block 0: no branch, and their codes are not used)
-  auto load = [&](int r, int blk) -> uint4 {
-    return ld_nc_v4(base + (((size_t)blk << bsh) + (r & (p.bs - 1))) * tok);
-  };
-  uint4 c[N];
-  // blk, scl: of the tile after the one in c; cur: scales of the one in c
-  int blk = 0;
-  float cur = 0.f, scl = 0.f;
+  auto scale_of = [&](int id) -> float { return __ldg(&scales[(size_t)id * p.scale_row]); };
+  // scales (a lane each) of the tile at hand and of the next, block ids of the one after
+  int id2 = 0;
+  float sc0 = 0.f, sc1 = 0.f;
   if (nt > 0) {
-    blk = checked(block_of(0));
-    cur = scale_of(blk);
-#pragma unroll
-    for (int i = 0; i < N; ++i) c[i] = load(r0 + RS * i, __shfl_sync(0xffffffffu, blk, (r0 + RS * i) >> bsh));
-    blk = checked(block_of(1));
-    scl = scale_of(blk);
+    const int id0 = checked(id_of(0)), id1 = checked(id_of(1));
+    id2 = id_of(2);
+    sc0 = scale_of(id0);
+    sc1 = scale_of(id1);
   }
   for (int t = 0; t < nt; ++t) {
     const int st = t & 1;
-    const bool ok = wait_or_abort(&empty[st], ((uint32_t)(t >> 1) & 1u) ^ 1u, abort_flag);
+    const uint32_t ph = (uint32_t)(t >> 1) & 1u;
+    bool ok = K ? wait_or_abort(&bars->empty_k, ((uint32_t)t & 1u) ^ 1u, abort_flag)
+                : wait_or_abort(&bars->empty_v[st], ph ^ 1u, abort_flag);
+    ok = ok && wait_or_abort(&raw_full[st], ph, abort_flag);
     if (!__all_sync(0xffffffffu, ok)) break;
-    unsigned char* dst = tile + st * 2 * kKVHalf;
-    const int after = block_of(t + 2);             // (its answer is not needed before the tile is written)
-    // Half of the rows are converted, then that half's rows of the next tile are
-    // requested in one go, and so for the other half: a wait for one half's
-    // data never covers loads issued since for the other.
+    const unsigned char* from = raw + st * kRaw + ch * 16;
+    unsigned char* dst = tile + (K ? 0 : st * 2 * kKVHalf);
+    if constexpr (K) {
+      // a scale of 0 as a tiny one: the scores are 0 all the same, and a masked -inf stays one
+      const float g = __shfl_sync(0xffffffffu, sc0, (4 * (lane & 15)) >> bsh);
+      if (lane < 16) bars->kscl[t & 3][lane] = fmaxf(g, 1e-37f);
+    }
+    // four rows at a time, read before the first is written (the compiler keeps
+    // shared-memory reads behind writes: one by one a row took a latency each)
+#pragma unroll 1
+    for (int rr = r0; rr < kKT; rr += 4 * RS) {
+      uint4 c[4];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int r = r0 + RS * i;
-      const float si = __shfl_sync(0xffffffffu, cur, r >> bsh);
-      const float sc = t * kKT + r < kend ? si : 0.f;
-      const bool none = sc == 0.f;
-      const uint32_t w[4] = {none ? 0u : c[i].x, none ? 0u : c[i].y, none ? 0u : c[i].z, none ? 0u : c[i].w};
-      uint32_t o[8];
-      if constexpr (K) {
-        // scale 0: a row of zeros, and the score takes scale 1
+      for (int i = 0; i < 4; ++i) c[i] = *reinterpret_cast<const uint4*>(from + (rr + i * RS) * 128);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) e4m3x4_to_f16x2x2(w[k], o[2 * k], o[2 * k + 1]);
-        if (ch == 0 && (r & 3) == 0) bars->kscl[t & 3][r >> 2] = none ? 1.f : sc;
-      } else {
-        const uint64_t s2 = f2pack(sc, sc);
+      for (int i = 0; i < 4; ++i) {
+        const int r = rr + i * RS;
+        const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+        uint32_t o[8];
+        if constexpr (K) {
+          // (rows past the context hold anything: their scores are masked)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t h[2];
-          e4m3x4_to_f16x2x2(w[k], h[0], h[1]);
+          for (int k = 0; k < 4; ++k) e4m3x4_to_f16x2x2(w[k], o[2 * k], o[2 * k + 1]);
+        } else {
+          const float s = __shfl_sync(0xffffffffu, sc0, r >> bsh);
+          const uint64_t s2 = f2pack(s, s);
+          const bool live = t * kKT + r < kend;          // (P is 0 past it, and 0 * NaN is not)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float a, d;
-            f16x2_to_float2(h[e], a, d);
-            f2unpack(fmul2(f2pack(a, d), s2), a, d);
-            const __nv_bfloat162 pk = __floats2bfloat162_rn(a, d);
-            o[2 * k + e] = *reinterpret_cast<const uint32_t*>(&pk);
+          for (int k = 0; k < 4; ++k) {
+            uint32_t h[2];
+            e4m3x4_to_f16x2x2(w[k], h[0], h[1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float a, d;
+              f16x2_to_float2(h[e], a, d);
+              f2unpack(fmul2(f2pack(a, d), s2), a, d);
+              const __nv_bfloat162 pk = __floats2bfloat162_rn(a, d);
+              o[2 * k + e] = live ? *reinterpret_cast<const uint32_t*>(&pk) : 0u;
+            }
           }
         }
-      }
-      *reinterpret_cast<uint4*>(dst + r * 128 + ((c0 ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4*>(dst + r * 128 + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-      if (i == N / 2 - 1 || i == N - 1) {
-        uint32_t at[N / 2];
-#pragma unroll
-        for (int k = 0; k < N / 2; ++k)
-          at[k] = (uint32_t)__shfl_sync(0xffffffffu, blk, (r0 + RS * (i - (N / 2 - 1) + k)) >> bsh);
-#pragma unroll
-        for (int k = 0; k < N / 2; ++k)
-          c[i - (N / 2 - 1) + k] = load(r0 + RS * (i - (N / 2 - 1) + k), (int)at[k]);
+        *reinterpret_cast<uint4*>(dst + r * 128 + ((c0 ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + r * 128 + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
       }
     }
     fence_proxy_async_smem();
-    mbar_arrive(&full[st]);
-    cur = scl;
-    blk = checked(after);
-    scl = scale_of(blk);
+    mbar_arrive(K ? &bars->full_k : &bars->full_v[st]);
+    id2 = in_use(t + 2) ? checked(id2) : 0;
+    sc0 = sc1;
+    sc1 = scale_of(id2);
+    id2 = id_of(t + 3);
   }
 }
 
 __global__ void __launch_bounds__(kTileThreads, 2)
-tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapO, const Params p,
+tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapO,
+            const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV, const Params p,
             const int QP) {
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023u) {                             // (see kTileSmem)
+    if (threadIdx.x == 0) atomicOr(&g_status_prefill_fp8, PA_DEV_TIMEOUT);
+    return;
+  }
   Bars* bars = reinterpret_cast<Bars*>(smem + kOffBar);
   volatile int* abort_flag = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -336,10 +337,12 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
   if (threadIdx.x == 224) {
     mbar_init(&bars->q, 1);
     mbar_init(&bars->qf, 128);
+    mbar_init(&bars->full_k, 32);
+    mbar_init(&bars->empty_k, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->full_k[i], 32);
+      mbar_init(&bars->raw_k[i], 1);
+      mbar_init(&bars->raw_v[i], 1);
       mbar_init(&bars->full_v[i], 64);
-      mbar_init(&bars->empty_k[i], 1);
       mbar_init(&bars->empty_v[i], 1);
       mbar_init(&bars->s[i], 1);
       mbar_init(&bars->p[i], 128);
@@ -372,50 +375,101 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
   } else if (warp == 5 || warp == 6) {
     convert_tiles<false>(p, bars, smem, b, kvh, kend, nt, (int)threadIdx.x - 160);
   } else if (warp == 7) {
-    // ---------------------------------------------------------- MMA issuer
-    if (lane == 0 && nt > 0) {
+    // ---------------------------------------------------------- code requests, MMA issuer
+    // The whole warp walks the tiles; lane 0 issues the MMAs and commits, parallel
+    // lanes a tile's copies, one block each.
+    if (nt > 0) {
       // S: f16 x f16; P V: bf16 x bf16 (V MN-major)
       constexpr uint32_t idS = idesc_f16_f32(kRows, kKT);
       constexpr uint32_t idO = idesc_bf16_f32(kRows, 128, false, true);
-      auto issue_s = [&](int j) {
-        const uint32_t kb = sbase + kOffK + (j & 1) * 2 * kKVHalf;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          umma_bf16(tmem + (j & 1) * kKT,
-                    sdesc_sw128(sbase + kOffQ + (uint32_t)(kk >> 2) * kQHalf + (uint32_t)(kk & 3) * 32u, 16, 1024),
-                    sdesc_sw128(kb + (uint32_t)(kk >> 2) * kKVHalf + (uint32_t)(kk & 3) * 32u, 16, 1024), idS,
-                    kk > 0 ? 1u : 0u);
-        }
-        umma_commit(&bars->s[j & 1]);
-        umma_commit(&bars->empty_k[j & 1]);
+      const int32_t* tab = p.block_tables + (size_t)b * p.max_blocks;
+      const int bsh = 31 - __clz(p.bs), nbt = kKT >> bsh;
+      const uint64_t pol = policy_evict_last();            // other query tiles read the same codes
+      auto id_of = [&](int t) -> int {
+        int id = 0;
+        if (t < nt && lane < nbt && t * kKT + (lane << bsh) < kend) id = __ldg(&tab[((t * kKT) >> bsh) + lane]);
+        return (unsigned)id < (unsigned)p.num_blocks ? id : 0;   // (flagged by the K warp)
       };
-      if (wait_or_abort(&bars->qf, 0, abort_flag) && wait_or_abort(&bars->full_k[0], 0, abort_flag)) {
+      int issued_k = 0, issued_v = 0;
+      auto request = [&](bool k, int t, int id) {          // tile t's codes into stage t & 1
+        if (t >= nt) return;
+        const uint32_t box = (uint32_t)p.bs * 128u;
+        const int nb = (min(kKT, kend - t * kKT) + p.bs - 1) >> bsh;
+        uint64_t* bar = k ? &bars->raw_k[t & 1] : &bars->raw_v[t & 1];
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)nb * box);
+        __syncwarp();
+        if (lane < nb)
+          tma_load_4d(smem + (k ? kOffRawK : kOffRawV) + (t & 1) * kRaw + lane * box, k ? &mapK : &mapV, bar, 0, kvh, 0,
+                      id, pol);
+        __syncwarp();
+        (k ? issued_k : issued_v) = t + 1;
+      };
+      // wait for all lanes alike
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag));
+      };
+      auto issue_s = [&](int j) {
+        if (lane == 0) {
+          const uint32_t kb = sbase + kOffK;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            umma_bf16(tmem + (j & 1) * kKT,
+                      sdesc_sw128(sbase + kOffQ + (uint32_t)(kk >> 2) * kQHalf + (uint32_t)(kk & 3) * 32u, 16, 1024),
+                      sdesc_sw128(kb + (uint32_t)(kk >> 2) * kKVHalf + (uint32_t)(kk & 3) * 32u, 16, 1024), idS,
+                      kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&bars->s[j & 1]);
+          umma_commit(&bars->empty_k);
+        }
+        __syncwarp();
+      };
+      int ida = id_of(0), idb = id_of(1);
+      int idv = id_of(2), idk = idv;                       // tile j+2's ids (V), tile j+3's (K)
+      request(true, 0, ida);
+      request(false, 0, ida);
+      request(true, 1, idb);
+      request(false, 1, idb);
+      if (wait(&bars->qf, 0) && wait(&bars->full_k, 0)) {
         tc_fence_after();
         issue_s(0);
+        request(true, 2, idk);
+        idk = id_of(3);
         for (int j = 0; j < nt; ++j) {
           const int st = j & 1;
           const uint32_t ph = (uint32_t)(j >> 1) & 1u;
           if (j + 1 < nt) {
-            if (!wait_or_abort(&bars->full_k[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u, abort_flag)) break;
+            if (!wait(&bars->full_k, (uint32_t)(j + 1) & 1u)) break;
             tc_fence_after();
             issue_s(j + 1);
+            request(true, j + 3, idk);
           }
-          if (!wait_or_abort(&bars->p[st], ph, abort_flag)) break;
-          if (!wait_or_abort(&bars->full_v[st], ph, abort_flag)) break;
+          if (!wait(&bars->p[st], ph)) break;
+          if (!wait(&bars->full_v[st], ph)) break;
           tc_fence_after();
-          const uint32_t vb = sbase + kOffV + st * 2 * kKVHalf;
+          if (lane == 0) {
+            const uint32_t vb = sbase + kOffV + st * 2 * kKVHalf;
 #pragma unroll
-          for (int kk = 0; kk < kKT / 16; ++kk)
-            umma_bf16_ts(tO, tmem + st * kKT + kk * 8, sdesc_sw128(vb + (uint32_t)kk * 2048u, kKVHalf, 1024), idO,
-                         (j > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(&bars->pv[st]);
-          umma_commit(&bars->empty_v[st]);
+            for (int kk = 0; kk < kKT / 16; ++kk)
+              umma_bf16_ts(tO, tmem + st * kKT + kk * 8, sdesc_sw128(vb + (uint32_t)kk * 2048u, kKVHalf, 1024), idO,
+                           (j > 0 || kk > 0) ? 1u : 0u);
+            umma_commit(&bars->pv[st]);
+            umma_commit(&bars->empty_v[st]);
+          }
+          __syncwarp();
+          request(false, j + 2, idv);
+          idv = idk;
+          idk = id_of(j + 4);
         }
       }
-      // every MMA issued so far has completed before TMEM is freed, and Q has landed
-      umma_commit(&bars->drain);
-      mbar_wait(&bars->drain, 0);
-      mbar_wait(&bars->q, 0);
+      // every MMA issued so far has completed before TMEM is freed; Q and the codes have landed
+      if (lane == 0) {
+        umma_commit(&bars->drain);
+        mbar_wait(&bars->drain, 0);
+        mbar_wait(&bars->q, 0);
+        for (int t = max(0, issued_k - 2); t < issued_k; ++t) mbar_wait(&bars->raw_k[t & 1], (uint32_t)(t >> 1) & 1u);
+        for (int t = max(0, issued_v - 2); t < issued_v; ++t) mbar_wait(&bars->raw_v[t & 1], (uint32_t)(t >> 1) & 1u);
+      }
+      __syncwarp();
     }
   } else {
     // ---------------------------------------------------------- softmax + epilogue
@@ -658,7 +712,7 @@ extern "C" int pa_prefill_fp8_blocks(void* out, const void* query, const int32_t
     const int QP = kRows / p.G;
     const long long ctas = ((long long)total_queries / QP + num_seqs) * num_kv_heads;
     if (ctas > 0x7fffffffll) return PA_ERR_SHAPE;
-    CUtensorMap mapQ, mapO;
+    CUtensorMap mapQ, mapO, mapK, mapV;
     const uint64_t dims[4] = {128, (uint64_t)num_heads, (uint64_t)total_queries, 1};
     const uint64_t str[3] = {256, (uint64_t)num_heads * 256, (uint64_t)total_queries * num_heads * 256};
     const uint32_t box[4] = {64, (uint32_t)p.G, (uint32_t)QP, 1};
@@ -669,9 +723,14 @@ extern "C" int pa_prefill_fp8_blocks(void* out, const void* query, const int32_t
     }
     int dev = 0;
     if (!ck(cudaGetDevice(&dev), "cudaGetDevice")) return PA_ERR_CUDA;
+    if (!pool_map(&mapK, k_cache, PA_FP8_E4M3, num_blocks, block_size, num_kv_heads, 128, dev, false, 1) ||
+        !pool_map(&mapV, v_cache, PA_FP8_E4M3, num_blocks, block_size, num_kv_heads, 128, dev, false, 1)) {
+      note_host_error("cuTensorMapEncodeTiled failed for the K/V pool");
+      return PA_ERR_CUDA;
+    }
     if (!raise_smem_limit(reinterpret_cast<const void*>(&tile_kernel), dev)) return PA_ERR_CUDA;
     int qp = QP;
-    void* args[] = {&mapQ, &mapO, &p, &qp};
+    void* args[] = {&mapQ, &mapO, &mapK, &mapV, &p, &qp};
     if (!ck(cudaLaunchKernel(reinterpret_cast<const void*>(&tile_kernel), dim3((unsigned)ctas), dim3(kTileThreads),
                              args, kTileSmem, (cudaStream_t)stream),
             "cudaLaunchKernel(tile_kernel)"))
