@@ -317,12 +317,13 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
     if (lane == 0 && nt > 0) {
       constexpr uint32_t idS = idesc_e4m3_f32(kTcTile, N, false);
       constexpr uint32_t idO = idesc_e4m3_f32(128, N, true);
+      const uint64_t dk = sdesc_sw128(sbase, 16, 1024), dq = sdesc_sw128(sbase + kOffQ, 16, 1024);
+      const uint64_t dv = sdesc_sw128(sbase + kOffV, kTcStage, 1024), dp = sdesc_sw128(sbase + kOffP, 16, 1024);
       auto issue_s = [&](int j) {
-        const uint32_t kb = sbase + (uint32_t)(j & 1) * kTcStage;
+        const uint64_t dkj = sdesc_at(dk, (uint32_t)(j & 1) * kTcStage);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)           // 32 head dims each
-          umma_f8(tmem + (j & 1) * N, sdesc_sw128(kb + kk * 32u, 16, 1024),
-                  sdesc_sw128(sbase + kOffQ + kk * 32u, 16, 1024), idS, kk > 0 ? 1u : 0u);
+          umma_f8(tmem + (j & 1) * N, sdesc_at(dkj, kk * 32u), sdesc_at(dq, kk * 32u), idS, kk > 0 ? 1u : 0u);
         umma_commit(&sh->s[j & 1]);
         umma_commit(&sh->empty_k[j & 1]);
       };
@@ -340,12 +341,10 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           if (!tc_wait(&sh->p[st], ph, abort_flag)) break;
           if (!tc_wait(&sh->full_v[st], ph, abort_flag)) break;
           tc_fence_after();
-          const uint32_t vb = sbase + kOffV + (uint32_t)st * kTcStage;
-          const uint32_t pb = sbase + kOffP + (uint32_t)st * (N * 128);
+          const uint64_t dvj = sdesc_at(dv, (uint32_t)st * kTcStage), dpj = sdesc_at(dp, (uint32_t)st * (N * 128));
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)         // 32 tokens each: four 8-token groups of 1024 bytes
-            umma_f8(tO, sdesc_sw128(vb + kk * 4096u, kTcStage, 1024), sdesc_sw128(pb + kk * 32u, 16, 1024), idO,
-                    (j > 0 || kk > 0) ? 1u : 0u);
+            umma_f8(tO, sdesc_at(dvj, kk * 4096u), sdesc_at(dpj, kk * 32u), idO, (j > 0 || kk > 0) ? 1u : 0u);
           umma_commit(&sh->pv[st]);
           umma_commit(&sh->empty_v[st]);
         }

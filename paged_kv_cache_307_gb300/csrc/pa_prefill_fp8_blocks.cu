@@ -5,29 +5,28 @@
 // position p = L_b - n_b + i and attends to the keys at 0..p:
 //   out = sum_t softmax_t(scale * <q, K_t>) V_t,  K = value(code) * k_scale[block, head], V likewise.
 //
-// tile_kernel (head_dim 128): 5th-generation tensor cores.  One CTA per (query
-// tile, KV head): 128 rows = QP = 128 / G positions x G query heads, keys in
-// tiles of 64, scores and output in tensor memory.
-//  * The codes of K and V come by TMA into two 8 KB stages each; warp 4 (K) and
-//    warps 5-6 (V) turn a stage into the 16-bit, 128-byte-swizzled tile that the
-//    MMAs read.  K becomes f16 (cvt.rn.f16x2.e4m3x2, exact: every code is an f16 value)
-//    and its scale stays apart; V becomes bf16 with its scale multiplied in (exact
-//    for a power of two; bf16 has the exponents for it, so a row that attends only to
-//    blocks of small scale keeps its precision beside blocks of large scale).  A
-//    16-bit K tile is needed from one S to the next only, so there is one; V has two.
+// tile_kernel (head_dim 128): 5th-generation tensor cores.  One CTA per (pair of
+// query tiles, KV head), one CTA per SM: a tile is 128 rows = QP = 128 / G positions
+// x G query heads, keys in tiles of 64, scores and output in tensor memory.
+//  * The codes of K and V come by TMA (warp 15) into four 8 KB stages each; warps 8-9
+//    (K) and 10-13 (V) turn a stage into the 16-bit, 128-byte-swizzled tile that the
+//    MMAs of both query tiles read: widening the codes is as many instructions as a
+//    tile's softmax, and the pair shares them.  K becomes f16
+//    (cvt.rn.f16x2.e4m3x2, exact: every code is an f16 value) and its scale stays
+//    apart; V becomes bf16 with its scale multiplied in (exact for a power of two;
+//    bf16 has the exponents for it, so a row that attends only to blocks of small
+//    scale keeps its precision beside blocks of large scale).
 //  * Q (TMA, bf16) is turned into f16 in place by the softmax warps, each row
 //    scaled by its own power of two so that its largest value is in
 //    [2^14, 2^15): exact but for values 2^-28 below that.
-//  * S = Q K^T in f16, one thread per row: x = s * (K scale of the key's block)
-//    * (row factor), running maximum and sum, P = 2^(x - m) in bf16 over the S
-//    columns, O += P V in bf16.  The reference only moves when the maximum
-//    has grown by 2^8.
-//  * Warp 7 issues S_{j+1} before P_j V_j, and with each the request for the codes two
-//    tiles on (a converted tile means that its stage has been read; requested by the
-//    converting warps, the copies cost each of them a third of its time).  Two CTAs per SM (98 KB, 256 threads: the softmax
-//    needs 128 registers, which two CTAs of eight warps have).
-//  * Keys at or past the context length are zeros in both tiles, whatever the
-//    pool holds there.  Every wait is bounded (2 s).
+//  * S = Q K^T in f16, one thread per row (warps 0-3 and 4-7, a query tile each):
+//    x = s * (K scale of the key's block) * (row factor), running maximum and sum,
+//    P = 2^(x - m) in bf16 over the S columns, O += P V in bf16.  The reference only
+//    moves when the maximum has grown by 2^8.
+//  * Warp 14 issues both tiles' S_{j+1} before their P_j V_j.  Tensor memory is full:
+//    two S buffers and an O for each tile, 512 columns.
+//  * Keys at or past the context length are zeros in the V tile, whatever the pool
+//    holds there.  Every wait is bounded (2 s).
 //
 // rows_kernel: one warp per (row, query head), for the other sizes.  Lane t of a step of
 // 32 keys computes one key's whole score from its row of codes; the warp takes
@@ -154,29 +153,28 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const Params p) {
 
 // ------------------------------------------------------------------ tile_kernel
 
-constexpr int kTileThreads = 256;      // 4 softmax, 1 K, 2 V, 1 MMA warps
+constexpr int kTileThreads = 512;      // 2 x 4 softmax, 2 K, 4 V, MMA and TMA warps
 constexpr int kRows = 128;
 constexpr int kKT = 64;                // keys per tile
+constexpr int kRawStages = 4;
 constexpr uint32_t kQHalf = 16384;     // 128 rows x 64 columns of 16 bits
 constexpr uint32_t kKVHalf = 8192;     // 64 keys x 64 columns of 16 bits
 constexpr uint32_t kRaw = 8192;        // 64 keys x 128 codes
-constexpr uint32_t kOffQ = 0;
-constexpr uint32_t kOffK = 32768;      // one 16-bit tile: 2 halves
-constexpr uint32_t kOffV = 49152;      // two
-constexpr uint32_t kOffRawK = 81920;   // 2 stages of codes
-constexpr uint32_t kOffRawV = 98304;
-constexpr uint32_t kOffBar = 114688;
-// Two CTAs per SM have 113 KB each: no room for alignment slack.  Without static
-// shared memory the dynamic part begins on a 1024-byte boundary (checked).
-constexpr uint32_t kTileSmem = kOffBar + 1024;
-constexpr float kRescaleThreshold = 8.0f;              // log2 units
-constexpr uint32_t kTmemCols = 256;    // S (and P) at columns 0 and 64, O at 128
-constexpr uint32_t kColO = 128;
+constexpr uint32_t kOffQ = 0;          // 2 query tiles x 2 halves
+constexpr uint32_t kOffK = 65536;      // 2 stages x 2 halves
+constexpr uint32_t kOffV = 98304;
+constexpr uint32_t kOffRawK = 131072;  // 4 stages of codes
+constexpr uint32_t kOffRawV = 163840;
+constexpr uint32_t kOffBar = 196608;
+constexpr uint32_t kTileSmem = kOffBar + 1024 + 1024;   // + alignment slack
+constexpr float kRescaleThreshold = 8.0f;               // log2 units
+constexpr uint32_t kTmemCols = 512;    // query tile h: S (and P) at columns 128 h and 128 h + 64, O at 256 + 128 h
 
 struct Bars {
-  uint64_t q, qf, raw_k[2], raw_v[2], full_k, full_v[2], empty_k, empty_v[2], s[2], p[2], pv[2], drain;
+  uint64_t q[2], qf[2], raw_k[kRawStages], raw_v[kRawStages], raw_ek[kRawStages], raw_ev[kRawStages];
+  uint64_t full_k[2], full_v[2], empty_k[2], empty_v[2], s[2][2], p[2][2], pv[2][2], drain;
   // K scale of every 4 keys (block sizes are multiples of 4) of tile t in slot
-  // t & 3: those of t+1 and t+2 may be written while the softmax reads t's, t+3's
+  // t & 3: those of t+1 to t+3 may be written while the softmax reads t's, t+4's
   // only after P_t (its K tile waits for S_{t+2}, which is issued after P_t)
   alignas(16) float kscl[4][kKT / 4];
   uint32_t tmem_base;
@@ -201,20 +199,18 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// K (one warp) or V (two warps): the codes of each key tile as 16-bit rows.  Thread x takes the 16-code chunk x % 8 of every
-// (threads / 8)-th row.
+// K (two warps) or V (four): the codes of each key tile as 16-bit rows.  Thread x
+// takes the 16-code chunk x % 8 of every (threads / 8)-th row.
 template <bool K>
 __device__ __forceinline__ void convert_tiles(const Params& p, Bars* bars, unsigned char* smem, int b, int kvh, int kend,
                                               int nt, int x) {
-  constexpr int kThr = K ? 32 : 64, RS = kThr / 8;       // threads, and the distance of a thread's rows
+  constexpr int kThr = K ? 64 : 128, RS = kThr / 8;      // threads, and the distance of a thread's rows
   volatile int* abort_flag = &bars->abort;
   const int lane = (int)(threadIdx.x & 31);
   const int ch = x & 7, r0 = x >> 3;
   const float* scales = (K ? p.k_scale : p.v_scale) + kvh;
   const int32_t* tab = p.block_tables + (size_t)b * p.max_blocks;
   const int bsh = 31 - __clz(p.bs), nbt = kKT >> bsh;    // blocks per tile, a lane each: at most 16
-  uint64_t* raw_full = K ? bars->raw_k : bars->raw_v;
-  const unsigned char* raw = smem + (K ? kOffRawK : kOffRawV);
   // codes 16 ch .. 16 ch + 15 are columns of half ch / 4, 16-byte chunks 2 (ch % 4) and the next
   unsigned char* tile = smem + (K ? kOffK : kOffV) + (ch >> 2) * kKVHalf;
   const int c0 = (ch & 3) * 2;
@@ -236,18 +232,16 @@ __device__ __forceinline__ void convert_tiles(const Params& p, Bars* bars, unsig
     sc1 = scale_of(id1);
   }
   for (int t = 0; t < nt; ++t) {
-    const int st = t & 1;
-    const uint32_t ph = (uint32_t)(t >> 1) & 1u;
-    bool ok = K ? wait_or_abort(&bars->empty_k, ((uint32_t)t & 1u) ^ 1u, abort_flag)
-                : wait_or_abort(&bars->empty_v[st], ph ^ 1u, abort_flag);
-    ok = ok && wait_or_abort(&raw_full[st], ph, abort_flag);
+    const int st = t & 1, rs = t & (kRawStages - 1);
+    bool ok = wait_or_abort(K ? &bars->empty_k[st] : &bars->empty_v[st], ((uint32_t)(t >> 1) & 1u) ^ 1u, abort_flag);
+    ok = ok && wait_or_abort(K ? &bars->raw_k[rs] : &bars->raw_v[rs], (uint32_t)(t / kRawStages) & 1u, abort_flag);
     if (!__all_sync(0xffffffffu, ok)) break;
-    const unsigned char* from = raw + st * kRaw + ch * 16;
-    unsigned char* dst = tile + (K ? 0 : st * 2 * kKVHalf);
+    const unsigned char* from = smem + (K ? kOffRawK : kOffRawV) + rs * kRaw + ch * 16;
+    unsigned char* dst = tile + st * 2 * kKVHalf;
     if constexpr (K) {
       // a scale of 0 as a tiny one: the scores are 0 all the same, and a masked -inf stays one
       const float g = __shfl_sync(0xffffffffu, sc0, (4 * (lane & 15)) >> bsh);
-      if (lane < 16) bars->kscl[t & 3][lane] = fmaxf(g, 1e-37f);
+      if (x < 16) bars->kscl[t & 3][x] = fmaxf(g, 1e-37f);
     }
     // four rows at a time, read before the first is written (the compiler keeps
     // shared-memory reads behind writes: one by one a row took a latency each)
@@ -288,7 +282,8 @@ __device__ __forceinline__ void convert_tiles(const Params& p, Bars* bars, unsig
       }
     }
     fence_proxy_async_smem();
-    mbar_arrive(K ? &bars->full_k : &bars->full_v[st]);
+    mbar_arrive(K ? &bars->full_k[st] : &bars->full_v[st]);
+    mbar_arrive(K ? &bars->raw_ek[rs] : &bars->raw_ev[rs]);
     id2 = in_use(t + 2) ? checked(id2) : 0;
     sc0 = sc1;
     sc1 = scale_of(id2);
@@ -296,22 +291,19 @@ __device__ __forceinline__ void convert_tiles(const Params& p, Bars* bars, unsig
   }
 }
 
-__global__ void __launch_bounds__(kTileThreads, 2)
+__global__ void __launch_bounds__(kTileThreads, 1)
 tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapO,
             const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV, const Params p,
             const int QP) {
-  extern __shared__ __align__(1024) unsigned char smem[];
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
-  if (sbase & 1023u) {                             // (see kTileSmem)
-    if (threadIdx.x == 0) atomicOr(&g_status_prefill_fp8, PA_DEV_TIMEOUT);
-    return;
-  }
   Bars* bars = reinterpret_cast<Bars*>(smem + kOffBar);
   volatile int* abort_flag = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // ---- work item: sequence b's tiles are units U_b = floor(query_start[b] / QP) + b
-  // and on; n rows make at most floor(n / QP) + 1 tiles, which never passes U_{b+1}
+  // ---- work item: sequence b's pairs are units U_b = floor(query_start[b] / (2 QP)) + b
+  // and on; n rows make at most floor(n / (2 QP)) + 1 pairs, which never passes U_{b+1}
   const int kvh = (int)(blockIdx.x % p.Hkv);
   const int u = (int)(blockIdx.x / p.Hkv);
   if (blockIdx.x == 0) {
@@ -320,47 +312,60 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
       if (!good_rows(p, i) || Li < 0 || Li > p.max_blocks * p.bs) atomicOr(&g_status_prefill_fp8, PA_DEV_BAD_LEN);
     }
   }
-  const int b = find_unit(p.query_start, p.B, QP, 1, u);
+  const int b = find_unit(p.query_start, p.B, 2 * QP, 1, u);
   if (!good_rows(p, b)) return;
   const int qrow0 = __ldg(&p.query_start[b]);
   const int nq = __ldg(&p.query_start[b + 1]) - qrow0;
-  const int ti = u - (qrow0 / QP + b);
-  const int ntiles = (nq + QP - 1) / QP;
-  if (ti < 0 || ti >= ntiles) return;              // nothing allocated yet
-  const int q0 = (ntiles - 1 - ti) * QP;           // the longest tile first
+  const int pi = u - (qrow0 / (2 * QP) + b);
+  const int npairs = (nq + 2 * QP - 1) / (2 * QP);
+  if (pi < 0 || pi >= npairs) return;              // nothing allocated yet
   int L = __ldg(&p.context_lens[b]);
   L = L < 0 ? 0 : min(L, p.max_blocks * p.bs);
-  const int pos0 = L - nq + q0;
-  const int kend = min(L, pos0 + QP);
-  const int nt = kend > 0 ? (kend + kKT - 1) / kKT : 0;
+  // query tile h: rows q0 + h QP and on; its keys [0, kend_h), none if it has no rows
+  const int q0 = (npairs - 1 - pi) * 2 * QP;       // the longest pair first
+  auto kend_of = [&](int h) -> int {
+    const int first = q0 + h * QP;
+    return first < nq ? max(0, min(L, L - nq + min(first + QP, nq))) : 0;
+  };
+  const int kend = max(kend_of(0), kend_of(1));
+  const int nt0 = (kend_of(0) + kKT - 1) / kKT, nt1 = (kend_of(1) + kKT - 1) / kKT;
+  const int nt = max(nt0, nt1);
 
-  if (threadIdx.x == 224) {
-    mbar_init(&bars->q, 1);
-    mbar_init(&bars->qf, 128);
-    mbar_init(&bars->full_k, 32);
-    mbar_init(&bars->empty_k, 1);
-    for (int i = 0; i < 2; ++i) {
+  if (threadIdx.x == 480) {
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&bars->q[h], 1);
+      mbar_init(&bars->qf[h], 128);
+      mbar_init(&bars->full_k[h], 64);
+      mbar_init(&bars->full_v[h], 128);
+      mbar_init(&bars->empty_k[h], 1);
+      mbar_init(&bars->empty_v[h], 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&bars->s[h][i], 1);
+        mbar_init(&bars->p[h][i], 128);
+        mbar_init(&bars->pv[h][i], 1);
+      }
+    }
+    for (int i = 0; i < kRawStages; ++i) {
       mbar_init(&bars->raw_k[i], 1);
       mbar_init(&bars->raw_v[i], 1);
-      mbar_init(&bars->full_v[i], 64);
-      mbar_init(&bars->empty_v[i], 1);
-      mbar_init(&bars->s[i], 1);
-      mbar_init(&bars->p[i], 128);
-      mbar_init(&bars->pv[i], 1);
+      mbar_init(&bars->raw_ek[i], 64);
+      mbar_init(&bars->raw_ev[i], 128);
     }
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
     fence_mbar_init();
-    if (nt > 0) {
-      prefetch_tensormap(&mapQ);
-      mbar_arrive_expect_tx(&bars->q, 2u * 128u * (uint32_t)(p.G * QP));
-      const uint64_t pol = policy_evict_first();
-      tma_load_4d(smem + kOffQ, &mapQ, &bars->q, 0, kvh * p.G, qrow0 + q0, 0, pol);
-      tma_load_4d(smem + kOffQ + kQHalf, &mapQ, &bars->q, 64, kvh * p.G, qrow0 + q0, 0, pol);
+    prefetch_tensormap(&mapQ);
+    const uint64_t pol = policy_evict_first();
+    for (int h = 0; h < 2; ++h) {
+      if ((h ? nt1 : nt0) == 0) continue;
+      unsigned char* dst = smem + kOffQ + h * 2 * kQHalf;
+      mbar_arrive_expect_tx(&bars->q[h], 2u * 128u * (uint32_t)(p.G * QP));
+      tma_load_4d(dst, &mapQ, &bars->q[h], 0, kvh * p.G, qrow0 + q0 + h * QP, 0, pol);
+      tma_load_4d(dst + kQHalf, &mapQ, &bars->q[h], 64, kvh * p.G, qrow0 + q0 + h * QP, 0, pol);
     }
   }
   __syncwarp();
-  if (warp == 7) {
+  if (warp == 14) {
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
   }
@@ -368,128 +373,145 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
-  const uint32_t tO = tmem + kColO;
 
-  if (warp == 4) {
-    convert_tiles<true>(p, bars, smem, b, kvh, kend, nt, lane);
-  } else if (warp == 5 || warp == 6) {
-    convert_tiles<false>(p, bars, smem, b, kvh, kend, nt, (int)threadIdx.x - 160);
-  } else if (warp == 7) {
-    // ---------------------------------------------------------- code requests, MMA issuer
-    // The whole warp walks the tiles; lane 0 issues the MMAs and commits, parallel
-    // lanes a tile's copies, one block each.
-    if (nt > 0) {
+  if (warp == 8 || warp == 9) {
+    convert_tiles<true>(p, bars, smem, b, kvh, kend, nt, (int)threadIdx.x - 256);
+  } else if (warp >= 10 && warp < 14) {
+    convert_tiles<false>(p, bars, smem, b, kvh, kend, nt, (int)threadIdx.x - 320);
+  } else if (warp == 15) {
+    // ---------------------------------------------------------- code requests
+    const int32_t* tab = p.block_tables + (size_t)b * p.max_blocks;
+    const int bsh = 31 - __clz(p.bs), nbt = kKT >> bsh;
+    const uint32_t box = (uint32_t)p.bs * 128u;
+    const uint64_t pol = policy_evict_last();              // other query tiles read the same codes
+    if (lane == 0) {
+      prefetch_tensormap(&mapK);
+      prefetch_tensormap(&mapV);
+    }
+    auto id_of = [&](int t) -> int {
+      int id = 0;
+      if (t < nt && lane < nbt && t * kKT + (lane << bsh) < kend) id = __ldg(&tab[((t * kKT) >> bsh) + lane]);
+      return (unsigned)id < (unsigned)p.num_blocks ? id : 0;   // (flagged by the K warps)
+    };
+    int issued = 0;
+    int id = id_of(0), id1 = id_of(1);
+    for (int t = 0; t < nt; ++t) {
+      const int rs = t & (kRawStages - 1);
+      const uint32_t ph = ((uint32_t)(t / kRawStages) & 1u) ^ 1u;
+      const int nb = (min(kKT, kend - t * kKT) + p.bs - 1) >> bsh;
+      bool ok = true;
+      if (lane == 0) ok = wait_or_abort(&bars->raw_ek[rs], ph, abort_flag) && wait_or_abort(&bars->raw_ev[rs], ph, abort_flag);
+      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars->raw_k[rs], (uint32_t)nb * box);
+        mbar_arrive_expect_tx(&bars->raw_v[rs], (uint32_t)nb * box);
+      }
+      __syncwarp();
+      // lanes 0-15: K's blocks, 16-31: V's
+      const int bl = lane & 15;
+      const int bid = __shfl_sync(0xffffffffu, id, bl);
+      if (bl < nb) {
+        const bool k = lane < 16;
+        tma_load_4d(smem + (k ? kOffRawK : kOffRawV) + rs * kRaw + bl * box, k ? &mapK : &mapV,
+                    k ? &bars->raw_k[rs] : &bars->raw_v[rs], 0, kvh, 0, bid, pol);
+      }
+      issued = t + 1;
+      id = id1;
+      id1 = id_of(t + 2);
+    }
+    // no TMA write may land after the CTA has left
+    if (lane == 0) {
+      for (int t = max(0, issued - kRawStages); t < issued; ++t) {
+        mbar_wait(&bars->raw_k[t & (kRawStages - 1)], (uint32_t)(t / kRawStages) & 1u);
+        mbar_wait(&bars->raw_v[t & (kRawStages - 1)], (uint32_t)(t / kRawStages) & 1u);
+      }
+      if (nt0 > 0) mbar_wait(&bars->q[0], 0);
+      if (nt1 > 0) mbar_wait(&bars->q[1], 0);
+    }
+  } else if (warp == 14) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0 && nt > 0) {
       // S: f16 x f16; P V: bf16 x bf16 (V MN-major)
       constexpr uint32_t idS = idesc_f16_f32(kRows, kKT);
       constexpr uint32_t idO = idesc_bf16_f32(kRows, 128, false, true);
-      const int32_t* tab = p.block_tables + (size_t)b * p.max_blocks;
-      const int bsh = 31 - __clz(p.bs), nbt = kKT >> bsh;
-      const uint64_t pol = policy_evict_last();            // other query tiles read the same codes
-      auto id_of = [&](int t) -> int {
-        int id = 0;
-        if (t < nt && lane < nbt && t * kKT + (lane << bsh) < kend) id = __ldg(&tab[((t * kKT) >> bsh) + lane]);
-        return (unsigned)id < (unsigned)p.num_blocks ? id : 0;   // (flagged by the K warp)
-      };
-      int issued_k = 0, issued_v = 0;
-      auto request = [&](bool k, int t, int id) {          // tile t's codes into stage t & 1
-        if (t >= nt) return;
-        const uint32_t box = (uint32_t)p.bs * 128u;
-        const int nb = (min(kKT, kend - t * kKT) + p.bs - 1) >> bsh;
-        uint64_t* bar = k ? &bars->raw_k[t & 1] : &bars->raw_v[t & 1];
-        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)nb * box);
-        __syncwarp();
-        if (lane < nb)
-          tma_load_4d(smem + (k ? kOffRawK : kOffRawV) + (t & 1) * kRaw + lane * box, k ? &mapK : &mapV, bar, 0, kvh, 0,
-                      id, pol);
-        __syncwarp();
-        (k ? issued_k : issued_v) = t + 1;
-      };
-      // wait for all lanes alike
-      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag));
-      };
+      const uint64_t dq = sdesc_sw128(sbase + kOffQ, 16, 1024), dk = sdesc_sw128(sbase + kOffK, 16, 1024);
+      const uint64_t dv = sdesc_sw128(sbase + kOffV, kKVHalf, 1024);
+      // both query tiles' scores of key tile j, as far as they have it
       auto issue_s = [&](int j) {
-        if (lane == 0) {
-          const uint32_t kb = sbase + kOffK;
+        const uint64_t dkj = sdesc_at(dk, (uint32_t)(j & 1) * 2 * kKVHalf);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            umma_bf16(tmem + (j & 1) * kKT,
-                      sdesc_sw128(sbase + kOffQ + (uint32_t)(kk >> 2) * kQHalf + (uint32_t)(kk & 3) * 32u, 16, 1024),
-                      sdesc_sw128(kb + (uint32_t)(kk >> 2) * kKVHalf + (uint32_t)(kk & 3) * 32u, 16, 1024), idS,
-                      kk > 0 ? 1u : 0u);
-          }
-          umma_commit(&bars->s[j & 1]);
-          umma_commit(&bars->empty_k);
+        for (int h = 0; h < 2; ++h) {
+          if (j >= (h ? nt1 : nt0)) continue;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_bf16(tmem + h * 128 + (j & 1) * kKT,
+                      sdesc_at(dq, (uint32_t)(2 * h + (kk >> 2)) * kQHalf + (uint32_t)(kk & 3) * 32u),
+                      sdesc_at(dkj, (uint32_t)(kk >> 2) * kKVHalf + (uint32_t)(kk & 3) * 32u), idS, kk > 0 ? 1u : 0u);
+          umma_commit(&bars->s[h][j & 1]);
         }
-        __syncwarp();
+        umma_commit(&bars->empty_k[j & 1]);
       };
-      int ida = id_of(0), idb = id_of(1);
-      int idv = id_of(2), idk = idv;                       // tile j+2's ids (V), tile j+3's (K)
-      request(true, 0, ida);
-      request(false, 0, ida);
-      request(true, 1, idb);
-      request(false, 1, idb);
-      if (wait(&bars->qf, 0) && wait(&bars->full_k, 0)) {
+      bool ok = (nt0 == 0 || wait_or_abort(&bars->qf[0], 0, abort_flag)) &&
+                (nt1 == 0 || wait_or_abort(&bars->qf[1], 0, abort_flag)) &&
+                wait_or_abort(&bars->full_k[0], 0, abort_flag);
+      if (ok) {
         tc_fence_after();
         issue_s(0);
-        request(true, 2, idk);
-        idk = id_of(3);
-        for (int j = 0; j < nt; ++j) {
+        for (int j = 0; j < nt && ok; ++j) {
           const int st = j & 1;
           const uint32_t ph = (uint32_t)(j >> 1) & 1u;
           if (j + 1 < nt) {
-            if (!wait(&bars->full_k, (uint32_t)(j + 1) & 1u)) break;
+            ok = wait_or_abort(&bars->full_k[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u, abort_flag);
+            if (!ok) break;
             tc_fence_after();
             issue_s(j + 1);
-            request(true, j + 3, idk);
           }
-          if (!wait(&bars->p[st], ph)) break;
-          if (!wait(&bars->full_v[st], ph)) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t vb = sbase + kOffV + st * 2 * kKVHalf;
+          ok = wait_or_abort(&bars->full_v[st], ph, abort_flag);
+          const uint64_t dvj = sdesc_at(dv, (uint32_t)st * 2 * kKVHalf);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (j >= (h ? nt1 : nt0)) continue;
+            ok = ok && wait_or_abort(&bars->p[h][st], ph, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < kKT / 16; ++kk)
-              umma_bf16_ts(tO, tmem + st * kKT + kk * 8, sdesc_sw128(vb + (uint32_t)kk * 2048u, kKVHalf, 1024), idO,
-                           (j > 0 || kk > 0) ? 1u : 0u);
-            umma_commit(&bars->pv[st]);
-            umma_commit(&bars->empty_v[st]);
+              umma_bf16_ts(tmem + 256 + h * 128, tmem + h * 128 + st * kKT + kk * 8,
+                           sdesc_at(dvj, (uint32_t)kk * 2048u), idO, (j > 0 || kk > 0) ? 1u : 0u);
+            umma_commit(&bars->pv[h][st]);
           }
-          __syncwarp();
-          request(false, j + 2, idv);
-          idv = idk;
-          idk = id_of(j + 4);
+          if (!ok) break;
+          umma_commit(&bars->empty_v[st]);
         }
       }
-      // every MMA issued so far has completed before TMEM is freed; Q and the codes have landed
-      if (lane == 0) {
-        umma_commit(&bars->drain);
-        mbar_wait(&bars->drain, 0);
-        mbar_wait(&bars->q, 0);
-        for (int t = max(0, issued_k - 2); t < issued_k; ++t) mbar_wait(&bars->raw_k[t & 1], (uint32_t)(t >> 1) & 1u);
-        for (int t = max(0, issued_v - 2); t < issued_v; ++t) mbar_wait(&bars->raw_v[t & 1], (uint32_t)(t >> 1) & 1u);
-      }
-      __syncwarp();
+      // every MMA issued so far has completed before TMEM is freed
+      umma_commit(&bars->drain);
+      mbar_wait(&bars->drain, 0);
     }
   } else {
     // ---------------------------------------------------------- softmax + epilogue
-    const int r = warp * 32 + lane;                // tile row and TMEM lane
+    const int h = warp >> 2;                       // query tile of the pair
+    const int r = (warp & 3) * 32 + lane;          // tile row and TMEM lane
     const int qi = r / p.G, hh = r % p.G;
-    const int pos = pos0 + qi;
-    const bool row_out = qi < QP && (q0 + qi) < nq;
-    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-    float rowf = 0.f;                              // scale * log2(e) / the row's power of two
+    const int qt = q0 + h * QP;                    // the tile's first row in the sequence
+    const int pos = L - nq + qt + qi;
+    const int ntt = h ? nt1 : nt0;
+    const bool row_out = qi < QP && (qt + qi) < nq;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + h * 128 + lane_off, tO = tmem + 256 + h * 128 + lane_off;
+    unsigned char* qs = smem + kOffQ + h * 2 * kQHalf + r * 128;   // the row's two halves
+    float rowf = 0.f;                              // scale * log2(e) * the row's power of two
     bool live = true;
-    if (nt > 0) {
+    if (ntt > 0) {
       // this thread's row of Q: bf16 -> f16 in place, zeros for rows that are not the sequence's
-      live = __all_sync(0xffffffffu, wait_or_abort(&bars->q, 0, abort_flag));
+      live = __all_sync(0xffffffffu, wait_or_abort(&bars->q[h], 0, abort_flag));
       uint4 qv[16];
       float mx = 0.f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         qv[i] = make_uint4(0u, 0u, 0u, 0u);
         if (live && row_out)
-          qv[i] = *reinterpret_cast<const uint4*>(smem + kOffQ + (i >> 3) * kQHalf + r * 128 + (((i & 7) ^ (r & 7)) << 4));
+          qv[i] = *reinterpret_cast<const uint4*>(qs + (i >> 3) * kQHalf + (((i & 7) ^ (r & 7)) << 4));
         float f[8];
         Elem<__nv_bfloat16>::unpack(qv[i], f);
 #pragma unroll
@@ -510,23 +532,23 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
           w[e] = *reinterpret_cast<const uint32_t*>(&h2);
         }
         if (live)
-          *reinterpret_cast<uint4*>(smem + kOffQ + (i >> 3) * kQHalf + r * 128 + (((i & 7) ^ (r & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(qs + (i >> 3) * kQHalf + (((i & 7) ^ (r & 7)) << 4)) =
               make_uint4(w[0], w[1], w[2], w[3]);
       }
       fence_proxy_async_smem();
-      if (live) mbar_arrive(&bars->qf);
+      if (live) mbar_arrive(&bars->qf[h]);
     }
     float m_ref = -INFINITY, lsum = 0.f;
-    for (int j = 0; j < nt && live; ++j) {
+    for (int j = 0; j < ntt && live; ++j) {
       const int st = j & 1;
       const uint32_t ph = (uint32_t)(j >> 1) & 1u;
       const int k0 = j * kKT;
-      bool ok = wait_or_abort(&bars->s[st], ph, abort_flag);   // (K's scales were there before S was issued)
+      bool ok = wait_or_abort(&bars->s[h][st], ph, abort_flag);   // (K's scales were there before S was issued)
       if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
       tc_fence_after();
       uint32_t v[2][32];
-      tmem_ld32(tmem + st * kKT + lane_off, v[0]);
-      tmem_ld32(tmem + st * kKT + 32 + lane_off, v[1]);
+      tmem_ld32(tS + st * kKT, v[0]);
+      tmem_ld32(tS + st * kKT + 32, v[1]);
       const float4* ks4 = reinterpret_cast<const float4*>(bars->kscl[j & 3]);   // 16 keys' scales each
       tmem_ld_wait();
       if (k0 + kKT - 1 > pos) {
@@ -553,17 +575,17 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
       const float alpha = need ? exp2f(m_ref - mx) : 1.f;
       if (need) m_ref = mx;
       if (j > 0 && __any_sync(0xffffffffu, need)) {
-        ok = wait_or_abort(&bars->pv[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u, abort_flag);
+        ok = wait_or_abort(&bars->pv[h][(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < 8; ++c) {
           uint32_t w[16];
-          tmem_ld16(tO + lane_off + c * 16, w);
+          tmem_ld16(tO + c * 16, w);
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
-          tmem_st16(tO + lane_off + c * 16, w);
+          tmem_st16(tO + c * 16, w);
         }
         tmem_st_wait();
       }
@@ -589,7 +611,7 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
           ls2[c & 3] = fadd2(ls2[c & 3], f2pack(p0, p1));
           pw[c] = *reinterpret_cast<const uint32_t*>(&pk);
         }
-        tmem_st16(tmem + st * kKT + hf * 16 + lane_off, pw);
+        tmem_st16(tS + st * kKT + hf * 16, pw);
       }
       float ls8[8];
 #pragma unroll
@@ -597,24 +619,24 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
       lsum += ((ls8[0] + ls8[1]) + (ls8[2] + ls8[3])) + ((ls8[4] + ls8[5]) + (ls8[6] + ls8[7]));
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&bars->p[st]);
+      mbar_arrive(&bars->p[h][st]);
     }
 
-    bool have = nt > 0 && live;
+    bool have = ntt > 0 && live;
     if (have) {
-      const bool ok = wait_or_abort(&bars->pv[(nt - 1) & 1], (uint32_t)((nt - 1) >> 1) & 1u, abort_flag);
+      const bool ok = wait_or_abort(&bars->pv[h][(ntt - 1) & 1], (uint32_t)((ntt - 1) >> 1) & 1u, abort_flag);
       have = __all_sync(0xffffffffu, ok);
       tc_fence_after();
     }
     const float inv = lsum != 0.f ? 1.f / lsum : 0.f;
-    const bool full = nt > 0 && q0 + QP <= nq;
+    const bool full = ntt > 0 && qt + QP <= nq;
     unsigned char* orow = static_cast<unsigned char*>(p.out) +
-                          (((size_t)qrow0 + q0 + qi) * p.Hq + (size_t)kvh * p.G + hh) * 256;
+                          (((size_t)qrow0 + qt + qi) * p.Hq + (size_t)kvh * p.G + hh) * 256;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       uint32_t v[32];
       if (have) {
-        tmem_ld32(tO + lane_off + c * 32, v);
+        tmem_ld32(tO + c * 32, v);
         tmem_ld_wait();
       }
 #pragma unroll
@@ -629,8 +651,8 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
         }
         const int ch = c * 4 + g;
         if (full) {
-          // staged in the Q buffer (free: S_{nt-1} completed before P_{nt-1} V_{nt-1}) for two TMA stores
-          *reinterpret_cast<uint4*>(smem + kOffQ + (ch >> 3) * kQHalf + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
+          // staged in the tile's Q buffer (free: its last S completed before its last P V) for two TMA stores
+          *reinterpret_cast<uint4*>(qs + (ch >> 3) * kQHalf + (((ch & 7) ^ (r & 7)) << 4)) =
               make_uint4(w[0], w[1], w[2], w[3]);
         } else if (row_out) {
           st_v4(orow + ch * 16, make_uint4(w[0], w[1], w[2], w[3]));
@@ -639,10 +661,11 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
     }
     if (full) {
       fence_proxy_async_smem();
-      named_sync(1, 128);
-      if (warp == 0 && lane == 0) {
-        tma_store_4d(&mapO, smem + kOffQ, 0, kvh * p.G, qrow0 + q0, 0);
-        tma_store_4d(&mapO, smem + kOffQ + kQHalf, 64, kvh * p.G, qrow0 + q0, 0);
+      named_sync(1 + h, 128);
+      if ((warp & 3) == 0 && lane == 0) {
+        unsigned char* src = smem + kOffQ + h * 2 * kQHalf;
+        tma_store_4d(&mapO, src, 0, kvh * p.G, qrow0 + qt, 0);
+        tma_store_4d(&mapO, src + kQHalf, 64, kvh * p.G, qrow0 + qt, 0);
         bulk_commit();
         bulk_wait_all();
       }
@@ -651,7 +674,7 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 7) tmem_dealloc(tmem, kTmemCols);
+  if (warp == 14) tmem_dealloc(tmem, kTmemCols);
 }
 
 }  // namespace
@@ -710,7 +733,7 @@ extern "C" int pa_prefill_fp8_blocks(void* out, const void* query, const int32_t
   p.qscale = scale * kLog2e;
   if (head_dim == 128 && p.G <= kRows) {
     const int QP = kRows / p.G;
-    const long long ctas = ((long long)total_queries / QP + num_seqs) * num_kv_heads;
+    const long long ctas = ((long long)total_queries / (2 * QP) + num_seqs) * num_kv_heads;
     if (ctas > 0x7fffffffll) return PA_ERR_SHAPE;
     CUtensorMap mapQ, mapO, mapK, mapV;
     const uint64_t dims[4] = {128, (uint64_t)num_heads, (uint64_t)total_queries, 1};
