@@ -5,26 +5,27 @@
 // position p = L_b - n_b + i and attends to the keys at 0..p:
 //   out = sum_t softmax_t(scale * <q, K_t>) V_t,  K = value(code) * k_scale[block, head], V likewise.
 //
-// tile_kernel (head_dim 128): 5th-generation tensor cores.  One CTA per (pair of
+// tile_kernel (head_dim 128, blocks of 8 and more): 5th-generation tensor cores.  One CTA per (pair of
 // query tiles, KV head), one CTA per SM: a tile is 128 rows = QP = 128 / G positions
-// x G query heads, keys in tiles of 64, scores and output in tensor memory.
-//  * The codes of K and V come by TMA (warp 15) into four 8 KB stages each; warps 8-9
-//    (K) and 10-13 (V) turn a stage into the 16-bit, 128-byte-swizzled tile that the
-//    MMAs of both query tiles read: widening the codes is as many instructions as a
-//    tile's softmax, and the pair shares them.  K becomes f16
-//    (cvt.rn.f16x2.e4m3x2, exact: every code is an f16 value) and its scale stays
-//    apart; V becomes bf16 with its scale multiplied in (exact for a power of two;
-//    bf16 has the exponents for it, so a row that attends only to blocks of small
-//    scale keeps its precision beside blocks of large scale).
-//  * Q (TMA, bf16) is turned into f16 in place by the softmax warps, each row
-//    scaled by its own power of two so that its largest value is in
-//    [2^14, 2^15): exact but for values 2^-28 below that.
-//  * S = Q K^T in f16, one thread per row (warps 0-3 and 4-7, a query tile each):
-//    x = s * (K scale of the key's block) * (row factor), running maximum and sum,
-//    P = 2^(x - m) in bf16 over the S columns, O += P V in bf16.  The reference only
-//    moves when the maximum has grown by 2^8.
-//  * Warp 14 issues both tiles' S_{j+1} before their P_j V_j.  Tensor memory is full:
-//    two S buffers and an O for each tile, 512 columns.
+// x G query heads; keys in tiles of 128; scores and output in tensor memory.
+//  * S = Q K^T takes the codes of K as they are (kind::f8f6f4).  Q enters as two e4m3
+//    terms: q 2^-e = hi + lo with 2^e per row so that the row's largest value is in
+//    [128, 256); hi carries 4 significant bits, lo the other 4 of a bf16 value, exactly
+//    down to 2^-10 of the largest and within 2^-17 of it below.  K's scales stay apart,
+//    in the softmax.
+//  * P V runs in bf16.  V's codes come by TMA into a stage of their own; warps 8-11
+//    widen them (cvt.rn.f16x2.e4m3x2), multiply their scale in (exact for a power of
+//    two; bf16 has the exponents for it, so a row that attends only to blocks of
+//    small scale keeps its precision beside blocks of large scale) and write the
+//    128-byte-swizzled tile that both query tiles' MMAs read: widening a tile is
+//    as many instructions as its softmax, and the pair shares it.
+//  * One thread per row (warps 0-3 and 4-7, a query tile each): x = s * (K scale of
+//    the key's block) * (row factor), running maximum and sum, P = 2^(x - m) in bf16
+//    over the S columns.  The reference only moves when the maximum has grown by 2^8.
+//  * Tensor memory is full: an S (then P) of 128 columns and an O of 128 for each
+//    query tile.  Warp 13 alternates between the tiles, P V then the next S of one
+//    while the other's softmax runs.  128 keys an MMA: at 64 the tensor core waits for
+//    its A operand (48 clocks for half the work of 68).
 //  * Keys at or past the context length are zeros in the V tile, whatever the pool
 //    holds there.  Every wait is bounded (2 s).
 //
@@ -153,29 +154,28 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const Params p) {
 
 // ------------------------------------------------------------------ tile_kernel
 
-constexpr int kTileThreads = 512;      // 2 x 4 softmax, 2 K, 4 V, MMA and TMA warps
+constexpr int kTileThreads = 448;      // 2 x 4 softmax, 4 V, TMA and MMA warps
 constexpr int kRows = 128;
-constexpr int kKT = 64;                // keys per tile
-constexpr int kRawStages = 4;
-constexpr uint32_t kQHalf = 16384;     // 128 rows x 64 columns of 16 bits
-constexpr uint32_t kKVHalf = 8192;     // 64 keys x 64 columns of 16 bits
-constexpr uint32_t kRaw = 8192;        // 64 keys x 128 codes
-constexpr uint32_t kOffQ = 0;          // 2 query tiles x 2 halves
-constexpr uint32_t kOffK = 65536;      // 2 stages x 2 halves
-constexpr uint32_t kOffV = 98304;
-constexpr uint32_t kOffRawK = 131072;  // 4 stages of codes
-constexpr uint32_t kOffRawV = 163840;
-constexpr uint32_t kOffBar = 196608;
+constexpr int kKT = 128;               // keys per tile
+constexpr int kKStages = 3;
+constexpr uint32_t kQHalf = 16384;     // 128 rows x 128 bytes
+constexpr uint32_t kCodes = 16384;     // 128 keys x 128 codes
+constexpr uint32_t kVHalf = 16384;     // 128 keys x 64 columns of bf16
+constexpr uint32_t kOffQ = 0;          // 2 query tiles x (bf16 columns 0-63, 64-127; then hi, lo; at the end the output)
+constexpr uint32_t kOffK = 65536;      // 3 stages of codes
+constexpr uint32_t kOffV = 114688;     // 2 stages x 2 halves of bf16
+constexpr uint32_t kOffRawV = 180224;  // 2 stages of codes
+constexpr uint32_t kOffBar = 212992;
 constexpr uint32_t kTileSmem = kOffBar + 1024 + 1024;   // + alignment slack
 constexpr float kRescaleThreshold = 8.0f;               // log2 units
-constexpr uint32_t kTmemCols = 512;    // query tile h: S (and P) at columns 128 h and 128 h + 64, O at 256 + 128 h
+constexpr uint32_t kTmemCols = 512;    // query tile h: S (and P) at columns 128 h, O at 256 + 128 h
 
 struct Bars {
-  uint64_t q[2], qf[2], raw_k[kRawStages], raw_v[kRawStages], raw_ek[kRawStages], raw_ev[kRawStages];
-  uint64_t full_k[2], full_v[2], empty_k[2], empty_v[2], s[2][2], p[2][2], pv[2][2], drain;
+  uint64_t q[2], qf[2], full_k[kKStages], empty_k[kKStages], raw_v[2], raw_ev[2], full_v[2], empty_v[2];
+  uint64_t s[2], p[2][2], pv[2], scl_full[4], drain;
   // K scale of every 4 keys (block sizes are multiples of 4) of tile t in slot
   // t & 3: those of t+1 to t+3 may be written while the softmax reads t's, t+4's
-  // only after P_t (its K tile waits for S_{t+2}, which is issued after P_t)
+  // only after P_t (its K stage waits for S_{t+1}, which is issued after P_t)
   alignas(16) float kscl[4][kKT / 4];
   uint32_t tmem_base;
   int abort;
@@ -199,50 +199,67 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// K (two warps) or V (four): the codes of each key tile as 16-bit rows.  Thread x
-// takes the 16-code chunk x % 8 of every (threads / 8)-th row.
-template <bool K>
-__device__ __forceinline__ void convert_tiles(const Params& p, Bars* bars, unsigned char* smem, int b, int kvh, int kend,
-                                              int nt, int x) {
-  constexpr int kThr = K ? 64 : 128, RS = kThr / 8;      // threads, and the distance of a thread's rows
+// D[tmem] (+)= A[smem] * B[smem], e4m3 operands.
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+// Four floats as e4m3 codes (the first in the low byte), and back.
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\tmov.b32 %0, {x, y};\n\t}"
+      : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+__device__ __forceinline__ void from_e4m3x4(uint32_t c, float* f) {
+  uint32_t a, b;
+  e4m3x4_to_f16x2x2(c, a, b);
+  f16x2_to_float2(a, f[0], f[1]);
+  f16x2_to_float2(b, f[2], f[3]);
+}
+
+// V (four warps): the codes of each key tile as bf16 rows.  Thread x takes the
+// 16-code chunk x % 8 of rows x / 8, x / 8 + 16, ...
+__device__ __forceinline__ void convert_v(const Params& p, Bars* bars, unsigned char* smem, int b, int kvh, int kend,
+                                          int nt, int x) {
+  constexpr int RS = 16;
   volatile int* abort_flag = &bars->abort;
   const int lane = (int)(threadIdx.x & 31);
   const int ch = x & 7, r0 = x >> 3;
-  const float* scales = (K ? p.k_scale : p.v_scale) + kvh;
+  const float* scales = p.v_scale + kvh;
   const int32_t* tab = p.block_tables + (size_t)b * p.max_blocks;
-  const int bsh = 31 - __clz(p.bs), nbt = kKT >> bsh;    // blocks per tile, a lane each: at most 16
+  const int bsh = 31 - __clz(p.bs), nbt = kKT >> bsh;    // blocks per tile, a lane each: at most 32
   // codes 16 ch .. 16 ch + 15 are columns of half ch / 4, 16-byte chunks 2 (ch % 4) and the next
-  unsigned char* tile = smem + (K ? kOffK : kOffV) + (ch >> 2) * kKVHalf;
+  unsigned char* tile = smem + kOffV + (ch >> 2) * kVHalf;
   const int c0 = (ch & 3) * 2;
-  auto in_use = [&](int t) -> bool { return t < nt && lane < nbt && t * kKT + (lane << bsh) < kend; };
-  auto id_of = [&](int t) -> int { return in_use(t) ? __ldg(&tab[((t * kKT) >> bsh) + lane]) : 0; };
-  auto checked = [&](int id) -> int {
-    if ((unsigned)id < (unsigned)p.num_blocks) return id;
-    if (K) atomicOr(&g_status_prefill_fp8, PA_DEV_BAD_BLOCK);
-    return 0;
+  auto id_of = [&](int t) -> int {
+    int id = 0;
+    if (t < nt && lane < nbt && t * kKT + (lane << bsh) < kend) id = __ldg(&tab[((t * kKT) >> bsh) + lane]);
+    return (unsigned)id < (unsigned)p.num_blocks ? id : 0;   // (flagged by the TMA warp)
   };
   auto scale_of = [&](int id) -> float { return __ldg(&scales[(size_t)id * p.scale_row]); };
   // scales (a lane each) of the tile at hand and of the next, block ids of the one after
   int id2 = 0;
   float sc0 = 0.f, sc1 = 0.f;
   if (nt > 0) {
-    const int id0 = checked(id_of(0)), id1 = checked(id_of(1));
+    const int id0 = id_of(0), id1 = id_of(1);
     id2 = id_of(2);
     sc0 = scale_of(id0);
     sc1 = scale_of(id1);
   }
   for (int t = 0; t < nt; ++t) {
-    const int st = t & 1, rs = t & (kRawStages - 1);
-    bool ok = wait_or_abort(K ? &bars->empty_k[st] : &bars->empty_v[st], ((uint32_t)(t >> 1) & 1u) ^ 1u, abort_flag);
-    ok = ok && wait_or_abort(K ? &bars->raw_k[rs] : &bars->raw_v[rs], (uint32_t)(t / kRawStages) & 1u, abort_flag);
+    const int st = t & 1;
+    const uint32_t ph = (uint32_t)(t >> 1) & 1u;
+    bool ok = wait_or_abort(&bars->empty_v[st], ph ^ 1u, abort_flag);
+    ok = ok && wait_or_abort(&bars->raw_v[st], ph, abort_flag);
     if (!__all_sync(0xffffffffu, ok)) break;
-    const unsigned char* from = smem + (K ? kOffRawK : kOffRawV) + rs * kRaw + ch * 16;
-    unsigned char* dst = tile + st * 2 * kKVHalf;
-    if constexpr (K) {
-      // a scale of 0 as a tiny one: the scores are 0 all the same, and a masked -inf stays one
-      const float g = __shfl_sync(0xffffffffu, sc0, (4 * (lane & 15)) >> bsh);
-      if (x < 16) bars->kscl[t & 3][x] = fmaxf(g, 1e-37f);
-    }
+    const unsigned char* from = smem + kOffRawV + st * kCodes + ch * 16;
+    unsigned char* dst = tile + st * 2 * kVHalf;
     // four rows at a time, read before the first is written (the compiler keeps
     // shared-memory reads behind writes: one by one a row took a latency each)
 #pragma unroll 1
@@ -255,26 +272,20 @@ __device__ __forceinline__ void convert_tiles(const Params& p, Bars* bars, unsig
         const int r = rr + i * RS;
         const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
         uint32_t o[8];
-        if constexpr (K) {
-          // (rows past the context hold anything: their scores are masked)
+        const float s = __shfl_sync(0xffffffffu, sc0, r >> bsh);
+        const uint64_t s2 = f2pack(s, s);
+        const bool live = t * kKT + r < kend;            // (P is 0 past it, and 0 * NaN is not)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) e4m3x4_to_f16x2x2(w[k], o[2 * k], o[2 * k + 1]);
-        } else {
-          const float s = __shfl_sync(0xffffffffu, sc0, r >> bsh);
-          const uint64_t s2 = f2pack(s, s);
-          const bool live = t * kKT + r < kend;          // (P is 0 past it, and 0 * NaN is not)
+        for (int k = 0; k < 4; ++k) {
+          uint32_t h[2];
+          e4m3x4_to_f16x2x2(w[k], h[0], h[1]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t h[2];
-            e4m3x4_to_f16x2x2(w[k], h[0], h[1]);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float a, d;
-              f16x2_to_float2(h[e], a, d);
-              f2unpack(fmul2(f2pack(a, d), s2), a, d);
-              const __nv_bfloat162 pk = __floats2bfloat162_rn(a, d);
-              o[2 * k + e] = live ? *reinterpret_cast<const uint32_t*>(&pk) : 0u;
-            }
+          for (int e = 0; e < 2; ++e) {
+            float a, d;
+            f16x2_to_float2(h[e], a, d);
+            f2unpack(fmul2(f2pack(a, d), s2), a, d);
+            const __nv_bfloat162 pk = __floats2bfloat162_rn(a, d);
+            o[2 * k + e] = live ? *reinterpret_cast<const uint32_t*>(&pk) : 0u;
           }
         }
         *reinterpret_cast<uint4*>(dst + r * 128 + ((c0 ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -282,9 +293,8 @@ __device__ __forceinline__ void convert_tiles(const Params& p, Bars* bars, unsig
       }
     }
     fence_proxy_async_smem();
-    mbar_arrive(K ? &bars->full_k[st] : &bars->full_v[st]);
-    mbar_arrive(K ? &bars->raw_ek[rs] : &bars->raw_ev[rs]);
-    id2 = in_use(t + 2) ? checked(id2) : 0;
+    mbar_arrive(&bars->full_v[st]);
+    mbar_arrive(&bars->raw_ev[st]);
     sc0 = sc1;
     sc1 = scale_of(id2);
     id2 = id_of(t + 3);
@@ -331,26 +341,24 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
   const int nt0 = (kend_of(0) + kKT - 1) / kKT, nt1 = (kend_of(1) + kKT - 1) / kKT;
   const int nt = max(nt0, nt1);
 
-  if (threadIdx.x == 480) {
+  if (threadIdx.x == 384) {
     for (int h = 0; h < 2; ++h) {
       mbar_init(&bars->q[h], 1);
       mbar_init(&bars->qf[h], 128);
-      mbar_init(&bars->full_k[h], 64);
+      mbar_init(&bars->raw_v[h], 1);
+      mbar_init(&bars->raw_ev[h], 128);
       mbar_init(&bars->full_v[h], 128);
-      mbar_init(&bars->empty_k[h], 1);
       mbar_init(&bars->empty_v[h], 1);
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&bars->s[h][i], 1);
-        mbar_init(&bars->p[h][i], 128);
-        mbar_init(&bars->pv[h][i], 1);
-      }
+      mbar_init(&bars->s[h], 1);
+      mbar_init(&bars->p[h][0], 128);
+      mbar_init(&bars->p[h][1], 128);
+      mbar_init(&bars->pv[h], 1);
     }
-    for (int i = 0; i < kRawStages; ++i) {
-      mbar_init(&bars->raw_k[i], 1);
-      mbar_init(&bars->raw_v[i], 1);
-      mbar_init(&bars->raw_ek[i], 64);
-      mbar_init(&bars->raw_ev[i], 128);
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(&bars->full_k[i], 1);
+      mbar_init(&bars->empty_k[i], 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&bars->scl_full[i], 1);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
     fence_mbar_init();
@@ -365,7 +373,7 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
     }
   }
   __syncwarp();
-  if (warp == 14) {
+  if (warp == 13) {
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
   }
@@ -374,14 +382,12 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
-  if (warp == 8 || warp == 9) {
-    convert_tiles<true>(p, bars, smem, b, kvh, kend, nt, (int)threadIdx.x - 256);
-  } else if (warp >= 10 && warp < 14) {
-    convert_tiles<false>(p, bars, smem, b, kvh, kend, nt, (int)threadIdx.x - 320);
-  } else if (warp == 15) {
-    // ---------------------------------------------------------- code requests
+  if (warp >= 8 && warp < 12) {
+    convert_v(p, bars, smem, b, kvh, kend, nt, (int)threadIdx.x - 256);
+  } else if (warp == 12) {
+    // ---------------------------------------------------------- code requests, K's scales
     const int32_t* tab = p.block_tables + (size_t)b * p.max_blocks;
-    const int bsh = 31 - __clz(p.bs), nbt = kKT >> bsh;
+    const int bsh = 31 - __clz(p.bs), nbt = kKT >> bsh;    // blocks per tile, a lane each
     const uint32_t box = (uint32_t)p.bs * 128u;
     const uint64_t pol = policy_evict_last();              // other query tiles read the same codes
     if (lane == 0) {
@@ -389,99 +395,124 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
       prefetch_tensormap(&mapV);
     }
     auto id_of = [&](int t) -> int {
-      int id = 0;
-      if (t < nt && lane < nbt && t * kKT + (lane << bsh) < kend) id = __ldg(&tab[((t * kKT) >> bsh) + lane]);
-      return (unsigned)id < (unsigned)p.num_blocks ? id : 0;   // (flagged by the K warps)
+      const bool used = t < nt && lane < nbt && t * kKT + (lane << bsh) < kend;
+      return used ? __ldg(&tab[((t * kKT) >> bsh) + lane]) : 0;
     };
-    int issued = 0;
-    int id = id_of(0), id1 = id_of(1);
+    auto checked = [&](int id) -> int {
+      if ((unsigned)id < (unsigned)p.num_blocks) return id;
+      atomicOr(&g_status_prefill_fp8, PA_DEV_BAD_BLOCK);
+      return 0;
+    };
+    auto scale_of = [&](int id) -> float { return __ldg(&p.k_scale[(size_t)id * p.scale_row + kvh]); };
+    int issued_k = 0, issued_v = 0;
+    int id = checked(id_of(0)), id1 = checked(id_of(1)), id2 = id_of(2);
+    float sc = scale_of(id), sc1 = scale_of(id1);
+    int ks = 0;                                            // K stage, and its use count's parity
+    uint32_t kph = 1u;
     for (int t = 0; t < nt; ++t) {
-      const int rs = t & (kRawStages - 1);
-      const uint32_t ph = ((uint32_t)(t / kRawStages) & 1u) ^ 1u;
       const int nb = (min(kKT, kend - t * kKT) + p.bs - 1) >> bsh;
       bool ok = true;
-      if (lane == 0) ok = wait_or_abort(&bars->raw_ek[rs], ph, abort_flag) && wait_or_abort(&bars->raw_ev[rs], ph, abort_flag);
+      if (lane == 0) ok = wait_or_abort(&bars->empty_k[ks], kph, abort_flag);
       if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bars->raw_k[rs], (uint32_t)nb * box);
-        mbar_arrive_expect_tx(&bars->raw_v[rs], (uint32_t)nb * box);
-      }
+      if (lane == 0) mbar_arrive_expect_tx(&bars->full_k[ks], (uint32_t)nb * box);
       __syncwarp();
-      // lanes 0-15: K's blocks, 16-31: V's
-      const int bl = lane & 15;
-      const int bid = __shfl_sync(0xffffffffu, id, bl);
-      if (bl < nb) {
-        const bool k = lane < 16;
-        tma_load_4d(smem + (k ? kOffRawK : kOffRawV) + rs * kRaw + bl * box, k ? &mapK : &mapV,
-                    k ? &bars->raw_k[rs] : &bars->raw_v[rs], 0, kvh, 0, bid, pol);
+      if (lane < nb) tma_load_4d(smem + kOffK + ks * kCodes + lane * box, &mapK, &bars->full_k[ks], 0, kvh, 0, id, pol);
+      issued_k = t + 1;
+      // a scale of 0 as a tiny one: the scores are 0 all the same, and a masked -inf stays one
+      bars->kscl[t & 3][lane] = fmaxf(__shfl_sync(0xffffffffu, sc, (4 * lane) >> bsh), 1e-37f);
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bars->scl_full[t & 3]);
+        ok = wait_or_abort(&bars->raw_ev[t & 1], ((uint32_t)(t >> 1) & 1u) ^ 1u, abort_flag);
       }
-      issued = t + 1;
+      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
+      if (lane == 0) mbar_arrive_expect_tx(&bars->raw_v[t & 1], (uint32_t)nb * box);
+      __syncwarp();
+      if (lane < nb)
+        tma_load_4d(smem + kOffRawV + (t & 1) * kCodes + lane * box, &mapV, &bars->raw_v[t & 1], 0, kvh, 0, id, pol);
+      issued_v = t + 1;
       id = id1;
-      id1 = id_of(t + 2);
+      sc = sc1;
+      id1 = checked(id2);
+      sc1 = scale_of(id1);
+      id2 = id_of(t + 3);
+      if (++ks == kKStages) {
+        ks = 0;
+        kph ^= 1u;
+      }
     }
     // no TMA write may land after the CTA has left
     if (lane == 0) {
-      for (int t = max(0, issued - kRawStages); t < issued; ++t) {
-        mbar_wait(&bars->raw_k[t & (kRawStages - 1)], (uint32_t)(t / kRawStages) & 1u);
-        mbar_wait(&bars->raw_v[t & (kRawStages - 1)], (uint32_t)(t / kRawStages) & 1u);
-      }
+      for (int t = max(0, issued_k - kKStages); t < issued_k; ++t)
+        mbar_wait(&bars->full_k[t % kKStages], (uint32_t)(t / kKStages) & 1u);
+      for (int t = max(0, issued_v - 2); t < issued_v; ++t) mbar_wait(&bars->raw_v[t & 1], (uint32_t)(t >> 1) & 1u);
       if (nt0 > 0) mbar_wait(&bars->q[0], 0);
       if (nt1 > 0) mbar_wait(&bars->q[1], 0);
     }
-  } else if (warp == 14) {
+  } else if (warp == 13) {
     // ---------------------------------------------------------- MMA issuer
     if (lane == 0 && nt > 0) {
-      // S: f16 x f16; P V: bf16 x bf16 (V MN-major)
-      constexpr uint32_t idS = idesc_f16_f32(kRows, kKT);
-      constexpr uint32_t idO = idesc_bf16_f32(kRows, 128, false, true);
+      constexpr uint32_t idS = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);   // e4m3, fp32
+      constexpr uint32_t idO = idesc_bf16_f32(kRows, 128, false, true);   // V MN-major
       const uint64_t dq = sdesc_sw128(sbase + kOffQ, 16, 1024), dk = sdesc_sw128(sbase + kOffK, 16, 1024);
-      const uint64_t dv = sdesc_sw128(sbase + kOffV, kKVHalf, 1024);
-      // both query tiles' scores of key tile j, as far as they have it
-      auto issue_s = [&](int j) {
-        const uint64_t dkj = sdesc_at(dk, (uint32_t)(j & 1) * 2 * kKVHalf);
+      const uint64_t dv = sdesc_sw128(sbase + kOffV, kVHalf, 1024);
+      // scores of query tile h and the key tile in stage ks: hi, then lo, 32 head dims each
+      auto issue_s = [&](int h, int ks) {
+        const uint64_t dqh = sdesc_at(dq, (uint32_t)h * 2 * kQHalf), dkj = sdesc_at(dk, (uint32_t)ks * kCodes);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (j >= (h ? nt1 : nt0)) continue;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_bf16(tmem + h * 128 + (j & 1) * kKT,
-                      sdesc_at(dq, (uint32_t)(2 * h + (kk >> 2)) * kQHalf + (uint32_t)(kk & 3) * 32u),
-                      sdesc_at(dkj, (uint32_t)(kk >> 2) * kKVHalf + (uint32_t)(kk & 3) * 32u), idS, kk > 0 ? 1u : 0u);
-          umma_commit(&bars->s[h][j & 1]);
-        }
-        umma_commit(&bars->empty_k[j & 1]);
+        for (int kk = 0; kk < 8; ++kk)
+          umma_f8(tmem + h * 128, sdesc_at(dqh, (uint32_t)(kk >> 2) * kQHalf + (uint32_t)(kk & 3) * 32u),
+                  sdesc_at(dkj, (uint32_t)(kk & 3) * 32u), idS, kk > 0 ? 1u : 0u);
+        umma_commit(&bars->s[h]);
       };
+      const int ntt[2] = {nt0, nt1};
       bool ok = (nt0 == 0 || wait_or_abort(&bars->qf[0], 0, abort_flag)) &&
                 (nt1 == 0 || wait_or_abort(&bars->qf[1], 0, abort_flag)) &&
                 wait_or_abort(&bars->full_k[0], 0, abort_flag);
       if (ok) {
         tc_fence_after();
-        issue_s(0);
+        if (nt0 > 0) issue_s(0, 0);
+        if (nt1 > 0) issue_s(1, 0);
+        umma_commit(&bars->empty_k[0]);
+        int ks = 1;                                        // stage of key tile j + 1, and its parity
+        uint32_t kph = 0u;
         for (int j = 0; j < nt && ok; ++j) {
           const int st = j & 1;
-          const uint32_t ph = (uint32_t)(j >> 1) & 1u;
-          if (j + 1 < nt) {
-            ok = wait_or_abort(&bars->full_k[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            issue_s(j + 1);
-          }
-          ok = wait_or_abort(&bars->full_v[st], ph, abort_flag);
-          const uint64_t dvj = sdesc_at(dv, (uint32_t)st * 2 * kKVHalf);
+          const uint64_t dvj = sdesc_at(dv, (uint32_t)st * 2 * kVHalf);
+          ok = wait_or_abort(&bars->full_v[st], (uint32_t)(j >> 1) & 1u, abort_flag);
+          bool have_k = false;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (j >= (h ? nt1 : nt0)) continue;
-            ok = ok && wait_or_abort(&bars->p[h][st], ph, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
+            if (j >= ntt[h]) continue;
 #pragma unroll
-            for (int kk = 0; kk < kKT / 16; ++kk)
-              umma_bf16_ts(tmem + 256 + h * 128, tmem + h * 128 + st * kKT + kk * 8,
-                           sdesc_at(dvj, (uint32_t)kk * 2048u), idO, (j > 0 || kk > 0) ? 1u : 0u);
-            umma_commit(&bars->pv[h][st]);
+            for (int g = 0; g < 2; ++g) {                  // keys 64 g .. 64 g + 63: as soon as their P is there
+              ok = ok && wait_or_abort(&bars->p[h][g], (uint32_t)j & 1u, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 4 * g; kk < 4 * g + 4; ++kk)
+                umma_bf16_ts(tmem + 256 + h * 128, tmem + h * 128 + kk * 8, sdesc_at(dvj, (uint32_t)kk * 2048u), idO,
+                             (j > 0 || kk > 0) ? 1u : 0u);
+            }
+            if (!ok) break;
+            umma_commit(&bars->pv[h]);
+            if (j + 1 < ntt[h]) {
+              if (!have_k) {
+                ok = wait_or_abort(&bars->full_k[ks], kph, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                have_k = true;
+              }
+              issue_s(h, ks);
+            }
           }
           if (!ok) break;
           umma_commit(&bars->empty_v[st]);
+          if (j + 1 < nt) umma_commit(&bars->empty_k[ks]);
+          if (++ks == kKStages) {
+            ks = 0;
+            kph ^= 1u;
+          }
         }
       }
       // every MMA issued so far has completed before TMEM is freed
@@ -503,7 +534,7 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
     float rowf = 0.f;                              // scale * log2(e) * the row's power of two
     bool live = true;
     if (ntt > 0) {
-      // this thread's row of Q: bf16 -> f16 in place, zeros for rows that are not the sequence's
+      // this thread's row of Q, in place: bf16 halves -> hi and lo; zeros for rows that are not the sequence's
       live = __all_sync(0xffffffffu, wait_or_abort(&bars->q[h], 0, abort_flag));
       uint4 qv[16];
       float mx = 0.f;
@@ -517,65 +548,76 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
 #pragma unroll
         for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(f[e]));
       }
-      // 2^qe >= max / 2^15
-      const int qe = mx > 0.f && mx < INFINITY ? max(-110, min(110, ilogbf(mx) - 14)) : 0;
-      const float down = __uint_as_float((uint32_t)(127 - qe) << 23);
+      const int qe = mx > 0.f && mx < INFINITY ? max(-110, min(110, ilogbf(mx) - 7)) : 0;
+      // (an infinite query has no answer: NaN, as its scores would be)
+      const float down = mx < INFINITY ? __uint_as_float((uint32_t)(127 - qe) << 23) : NAN;
       rowf = p.qscale * __uint_as_float((uint32_t)(127 + qe) << 23);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float f[8];
-        Elem<__nv_bfloat16>::unpack(qv[i], f);
-        uint32_t w[4];
+      for (int i = 0; i < 8; ++i) {                // 16 head dims
+        float f[16];
+        Elem<__nv_bfloat16>::unpack(qv[2 * i], f);
+        Elem<__nv_bfloat16>::unpack(qv[2 * i + 1], f + 8);
+        uint32_t hi[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const __half2 h2 = __floats2half2_rn(f[2 * e] * down, f[2 * e + 1] * down);
-          w[e] = *reinterpret_cast<const uint32_t*>(&h2);
+          float* x = f + 4 * e;
+          float y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] *= down;
+          hi[e] = to_e4m3x4(x[0], x[1], x[2], x[3]);
+          from_e4m3x4(hi[e], y);
+          lo[e] = to_e4m3x4(x[0] - y[0], x[1] - y[1], x[2] - y[2], x[3] - y[3]);
         }
-        if (live)
-          *reinterpret_cast<uint4*>(qs + (i >> 3) * kQHalf + (((i & 7) ^ (r & 7)) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
+        if (live) {
+          *reinterpret_cast<uint4*>(qs + ((i ^ (r & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(qs + kQHalf + ((i ^ (r & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
       }
       fence_proxy_async_smem();
       if (live) mbar_arrive(&bars->qf[h]);
     }
     float m_ref = -INFINITY, lsum = 0.f;
     for (int j = 0; j < ntt && live; ++j) {
-      const int st = j & 1;
-      const uint32_t ph = (uint32_t)(j >> 1) & 1u;
+      const uint32_t ph = (uint32_t)j & 1u;
       const int k0 = j * kKT;
-      bool ok = wait_or_abort(&bars->s[h][st], ph, abort_flag);   // (K's scales were there before S was issued)
+      bool ok = wait_or_abort(&bars->scl_full[j & 3], (uint32_t)(j >> 2) & 1u, abort_flag);
+      ok = ok && wait_or_abort(&bars->s[h], ph, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
       tc_fence_after();
-      uint32_t v[2][32];
-      tmem_ld32(tS + st * kKT, v[0]);
-      tmem_ld32(tS + st * kKT + 32, v[1]);
       const float4* ks4 = reinterpret_cast<const float4*>(bars->kscl[j & 3]);   // 16 keys' scales each
-      tmem_ld_wait();
-      if (k0 + kKT - 1 > pos) {
-#pragma unroll
-        for (int c = 0; c < kKT; ++c)
-          if (k0 + c > pos) v[c >> 5][c & 31] = __float_as_uint(-INFINITY);
-      }
+      const bool partial = k0 + kKT - 1 > pos;
+      // maximum of the row's scaled scores, 32 keys at a time
       float mx = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {                // 16 keys a step
-        const float4 k4 = ks4[i];
-        const float f[4] = {k4.x, k4.y, k4.z, k4.w};
-        float a[4];
+      for (int c = 0; c < 4; ++c) {
+        uint32_t v[32];
+        tmem_ld32(tS + c * 32, v);
+        tmem_ld_wait();
+        if (partial) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const uint32_t* x = &v[i >> 1][(i & 1) * 16 + 4 * g];
-          a[g] = f[g] * fmax3(fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])), __uint_as_float(x[2]),
-                              __uint_as_float(x[3]));
+          for (int i = 0; i < 32; ++i)
+            if (k0 + c * 32 + i > pos) v[i] = __float_as_uint(-INFINITY);
         }
-        mx = fmax3(fmax3(mx, a[0], a[1]), a[2], a[3]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float4 k4 = ks4[2 * c + i];
+          const float f[4] = {k4.x, k4.y, k4.z, k4.w};
+          float a[4];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const uint32_t* x = &v[i * 16 + 4 * g];
+            a[g] = f[g] * fmax3(fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])), __uint_as_float(x[2]),
+                                __uint_as_float(x[3]));
+          }
+          mx = fmax3(fmax3(mx, a[0], a[1]), a[2], a[3]);
+        }
       }
       mx *= rowf;
       const bool need = mx > m_ref + kRescaleThreshold;
       const float alpha = need ? exp2f(m_ref - mx) : 1.f;
       if (need) m_ref = mx;
       if (j > 0 && __any_sync(0xffffffffu, need)) {
-        ok = wait_or_abort(&bars->pv[h][(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u, abort_flag);
+        ok = wait_or_abort(&bars->pv[h], (uint32_t)(j - 1) & 1u, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
         tc_fence_after();
 #pragma unroll 1
@@ -595,36 +637,45 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
       uint64_t ls2[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) ls2[i] = f2pack(0.f, 0.f);
+      // P of keys 32 c .. 32 c + 31 into columns 16 c .. 16 c + 15: scores that have been read
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t pw[16];
+      for (int c = 0; c < 4; ++c) {
+        uint32_t v[32], pw[16];
+        tmem_ld32(tS + c * 32, v);
+        tmem_ld_wait();
+        if (partial) {
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float4 k4 = ks4[hf * 2 + (c >> 3)];
-          const int g = (c >> 1) & 3;
+          for (int i = 0; i < 32; ++i)
+            if (k0 + c * 32 + i > pos) v[i] = __float_as_uint(-INFINITY);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float4 k4 = ks4[2 * c + (i >> 3)];
+          const int g = (i >> 1) & 3;
           const float f = rowf * (g == 0 ? k4.x : g == 1 ? k4.y : g == 2 ? k4.z : k4.w);
           float x0, x1;
-          f2unpack(ffma2(f2pack(__uint_as_float(v[hf][2 * c]), __uint_as_float(v[hf][2 * c + 1])), f2pack(f, f), nm2),
-                   x0, x1);
+          f2unpack(ffma2(f2pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2pack(f, f), nm2), x0, x1);
           const float p0 = ex2_f32(x0), p1 = ex2_f32(x1);
           const __nv_bfloat162 pk = __floats2bfloat162_rn(p0, p1);
-          ls2[c & 3] = fadd2(ls2[c & 3], f2pack(p0, p1));
-          pw[c] = *reinterpret_cast<const uint32_t*>(&pk);
+          ls2[i & 3] = fadd2(ls2[i & 3], f2pack(p0, p1));
+          pw[i] = *reinterpret_cast<const uint32_t*>(&pk);
         }
-        tmem_st16(tS + st * kKT + hf * 16, pw);
+        tmem_st16(tS + c * 16, pw);
+        if (c & 1) {
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&bars->p[h][c >> 1]);
+        }
       }
       float ls8[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) f2unpack(ls2[i], ls8[2 * i], ls8[2 * i + 1]);
       lsum += ((ls8[0] + ls8[1]) + (ls8[2] + ls8[3])) + ((ls8[4] + ls8[5]) + (ls8[6] + ls8[7]));
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&bars->p[h][st]);
     }
 
     bool have = ntt > 0 && live;
     if (have) {
-      const bool ok = wait_or_abort(&bars->pv[h][(ntt - 1) & 1], (uint32_t)((ntt - 1) >> 1) & 1u, abort_flag);
+      const bool ok = wait_or_abort(&bars->pv[h], (uint32_t)(ntt - 1) & 1u, abort_flag);
       have = __all_sync(0xffffffffu, ok);
       tc_fence_after();
     }
@@ -674,7 +725,7 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 14) tmem_dealloc(tmem, kTmemCols);
+  if (warp == 13) tmem_dealloc(tmem, kTmemCols);
 }
 
 }  // namespace
@@ -731,7 +782,7 @@ extern "C" int pa_prefill_fp8_blocks(void* out, const void* query, const int32_t
   p.num_blocks = num_blocks;
   p.scale_row = scale_row(num_kv_heads);
   p.qscale = scale * kLog2e;
-  if (head_dim == 128 && p.G <= kRows) {
+  if (head_dim == 128 && block_size >= 8 && p.G <= kRows) {   // (K's boxes are whole 8-row swizzle atoms)
     const int QP = kRows / p.G;
     const long long ctas = ((long long)total_queries / (2 * QP) + num_seqs) * num_kv_heads;
     if (ctas > 0x7fffffffll) return PA_ERR_SHAPE;
@@ -746,7 +797,8 @@ extern "C" int pa_prefill_fp8_blocks(void* out, const void* query, const int32_t
     }
     int dev = 0;
     if (!ck(cudaGetDevice(&dev), "cudaGetDevice")) return PA_ERR_CUDA;
-    if (!pool_map(&mapK, k_cache, PA_FP8_E4M3, num_blocks, block_size, num_kv_heads, 128, dev, false, 1) ||
+    // K's codes 128-byte-swizzled for the MMAs, V's plain
+    if (!pool_map(&mapK, k_cache, PA_FP8_E4M3, num_blocks, block_size, num_kv_heads, 128, dev, true, 1) ||
         !pool_map(&mapV, v_cache, PA_FP8_E4M3, num_blocks, block_size, num_kv_heads, 128, dev, false, 1)) {
       note_host_error("cuTensorMapEncodeTiled failed for the K/V pool");
       return PA_ERR_CUDA;
