@@ -469,7 +469,8 @@ size_t pa_decode_weights_workspace_bytes(int num_seqs, int num_heads, int num_kv
  *   seen_lens    [num_seqs] int32: tokens the sequence has had in all, the
  *                dropped ones included (L_b before its first eviction)
  *   weights, token_pos  [num_seqs, num_kv_heads] rows of row_stride floats /
- *                int32, row_stride >= max_blocks_per_seq * block_size
+ *                int32, row_stride >= max_blocks_per_seq * block_size (which is
+ *                at most 6291456 tokens)
  *   budget, recent, sinks   >= 1, >= 0, >= 0; recent + sinks <= budget
  *   new_lens     [num_seqs] int32 (written); may be context_lens or kept_lens
  *   weights_out, token_pos_out  rows like weights and token_pos (written: the

@@ -10,15 +10,18 @@
 // sequence.)  A token's position in the text then no longer follows from its
 // slot, so it is carried in token_pos.
 //
-// select_kernel, one CTA per (sequence, KV head): the keys (an order-preserving
-// integer image of the weights, protected tokens above all others) are read
-// once into shared memory; the budget-th largest comes out by radix selection,
-// 8 bits a pass.  Each warp then owns a run of consecutive slots and walks it 32
-// at a time: a sweep that counts ties, one that decides what stays (ties by the
-// lower slot), one that numbers the holes and the movers; between sweeps one scan
-// over the warps.  Weights, positions and the list of moves come out of it.
-// Counts: a digit's 256 bins exist eight times, a lane adding to copy lane % 8:
-// weights share their leading bits, and 32 lanes adding to one word take 32 turns.
+// select_kernel, one CTA or a cluster of four per (sequence, KV head): the keys (an
+// order-preserving integer image of the weights, protected tokens above all
+// others) are read once into shared memory, a quarter of the slots by each CTA of a
+// cluster; the budget-th largest comes out by radix selection, 8 bits a pass, each
+// pass with bins of its own, cleared at the start, the cluster's bins added up over
+// distributed shared memory.  Each warp then owns a run of consecutive slots and
+// walks it 32 at a time: a sweep that counts ties, one that decides what stays (ties
+// by the lower slot; a bit per slot is kept), one that numbers the holes and the
+// movers; between sweeps one scan over the warps and CTAs.  Weights, positions and
+// the list of moves come out of it.
+// Weights share their leading bits, and 32 lanes adding to one word take 32 turns: the
+// first pass adds once per digit and warp, and the bins exist twice.
 // move_kernel, one warp per destination block: the block's moves, a lane each,
 // then their rows with eight 16-byte loads in flight per lane; over an e4m3 pool
 // the block's scale becomes the largest of its own and the incoming rows' and the
@@ -33,8 +36,11 @@ namespace {
 
 __device__ unsigned g_status_evict;
 
-constexpr int kHistCopies = 8;
-constexpr int kMaxSmemKeys = 48 * 1024;   // tokens whose keys fit in shared memory beside the bins
+constexpr int kBins = 288;                // 256 digits, one word of padding after every 8
+constexpr int kCopies = 2;
+constexpr int kCluster = 4;
+constexpr int kMaxSmemKeys = 48 * 1024;   // slots of a CTA whose keys fit in shared memory
+constexpr int kMaxTokens = kCluster * 32 * kMaxSmemKeys;   // a bit for each slot in the room of the keys
 constexpr int kMoveWarps = 8;
 
 struct Move {
@@ -73,11 +79,32 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 
 __device__ __forceinline__ int clamp_len(int L, int Lmax) { return L < 0 ? 0 : min(L, Lmax); }
 
-// Exclusive sum over the warps of x (the same in every lane of a warp), and the total.
-template <int NW>
-__device__ __forceinline__ int scan_warps(int x, int* buf, int& total) {
+__device__ __forceinline__ int cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return (int)r;
+}
+__device__ __forceinline__ int ld_cluster(const int* p, int rank) {
+  uint32_t a;
+  int v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+// Every thread of the CTA, or of the cluster; what they wrote before is visible after.
+template <int CS>
+__device__ __forceinline__ void sync_all() {
+  if constexpr (CS == 1) {
+    __syncthreads();
+  } else {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  }
+}
+// Exclusive sum of x (the same in every lane of a warp) over the warps of the
+// cluster, and the total.  buf [NW + 1] is used once.
+template <int NW, int CS>
+__device__ __forceinline__ int scan_warps(int x, int* buf, int rank, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __syncthreads();                       // (buf's last readers are done)
   if (lane == 0) buf[warp] = x;
   __syncthreads();
   int v = lane < NW ? buf[lane] : 0;
@@ -86,29 +113,50 @@ __device__ __forceinline__ int scan_warps(int x, int* buf, int& total) {
     const int y = __shfl_up_sync(0xffffffffu, v, off);
     if (lane >= off) v += y;
   }
+  int before = __shfl_up_sync(0xffffffffu, v, 1);      // lane w: the warps before w
+  if (lane == 0) before = 0;
+  before = __shfl_sync(0xffffffffu, before, warp);
   total = __shfl_sync(0xffffffffu, v, NW - 1);
-  return warp ? __shfl_sync(0xffffffffu, v, warp - 1) : (__shfl_sync(0xffffffffu, v, 0), 0);
+  if constexpr (CS > 1) {
+    if (threadIdx.x == 0) buf[NW] = total;
+    sync_all<CS>();
+    int all = 0;
+#pragma unroll
+    for (int r = 0; r < CS; ++r) {
+      const int n = ld_cluster(&buf[NW], r);
+      if (r < rank) before += n;
+      all += n;
+    }
+    total = all;
+  }
+  return before;
 }
 
-// SMEM: the keys are kept in shared memory (else recomputed from the inputs).
-template <int NT, bool SMEM>
-__global__ void __launch_bounds__(NT) select_kernel(const EvictParams p) {
+// NT threads a CTA, CS CTAs a cluster.  SMEM: the keys are kept in shared memory
+// (else recomputed from the inputs).  words: shared words for a CTA's stay bits.
+template <int NT, int CS, bool SMEM>
+__global__ void __launch_bounds__(NT) select_kernel(const EvictParams p, int words) {
   constexpr int NW = NT / 32;
-  __shared__ int hist[256 * kHistCopies];
-  __shared__ int wbuf[NW];
+  __shared__ int hist[4][kCopies][kBins];
+  __shared__ int wbuf[3][NW + 1];
   __shared__ int sh_digit, sh_left;
-  extern __shared__ uint32_t keys[];
+  extern __shared__ uint32_t dyn[];
   asm volatile("griddepcontrol.launch_dependents;");
-  const int bh = (int)blockIdx.x, b = bh / p.Hkv, h = bh % p.Hkv;
+  const int rank = CS > 1 ? cluster_rank() : 0;
+  const int bh = (int)blockIdx.x / CS, b = bh / p.Hkv, h = bh % p.Hkv;
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gid = rank * NT + tid;                   // thread of the cluster
   const int Lmax = p.max_blocks * p.bs;
+  uint32_t* stay_bits = dyn;                         // this CTA's slots
+  uint32_t* keys = dyn + words;                      // (SMEM)
   const int L0 = __ldg(&p.context_lens[b]);
   const int K0 = __ldg(&p.kept_lens[b]);
   const int seen = __ldg(&p.seen_lens[b]);
+  for (int i = tid; i < 4 * kCopies * kBins; i += NT) (&hist[0][0][0])[i] = 0;
   const int L = clamp_len(L0, Lmax);
   const int kept = clamp_len(K0, L);
   const int newL = min(L, p.budget);
-  if (h == 0 && tid == 0) {
+  if (h == 0 && gid == 0) {
     if (L0 != L || K0 != kept) atomicOr(&g_status_evict, PA_DEV_BAD_LEN);
     p.ws_len[b] = newL;
   }
@@ -119,54 +167,84 @@ __global__ void __launch_bounds__(NT) select_kernel(const EvictParams p) {
   int32_t* po = p.pos_out + row;
   auto pos_of = [&](int t) { return t < kept ? tp[t] : seen - L + t; };
   int32_t* first = p.first + (size_t)bh * (p.nb + 1);
+  // the rest of the two rows: 0 and -1 from slot t on
+  auto clear_from = [&](int t) {
+#pragma unroll 4
+    for (int x = t + gid; x < Lmax; x += CS * NT) {
+      wo[x] = 0.f;
+      po[x] = -1;
+    }
+  };
   if (L <= p.budget) {
     // nothing leaves (in and out may be the same rows: each thread reads its entry before writing it)
-    for (int t = tid; t < Lmax; t += NT) {
-      const float wt = t < L ? w[t] : 0.f;
-      const int pt = t < L ? pos_of(t) : -1;
+#pragma unroll 4
+    for (int t = gid; t < L; t += CS * NT) {
+      const float wt = w[t];
+      const int pt = pos_of(t);
       wo[t] = wt;
       po[t] = pt;
     }
-    for (int j = tid; j <= p.nb; j += NT) first[j] = 0;
+    clear_from(L);
+    for (int j = gid; j <= p.nb; j += CS * NT) first[j] = 0;
     return;
   }
+  // this CTA's slots: [base, base + n), a multiple of 32 but for the end
+  const int per = CS > 1 ? (((L + CS - 1) / CS + 31) & ~31) : L;
+  const int base = min(L, rank * per), n = min(L - base, per);
   auto make_key = [&](int t) -> uint32_t {
     const float wt = w[t];
     const int pos = pos_of(t);
     return pos < p.sinks || pos >= seen - p.recent ? 0xffffffffu : order_key(wt);
   };
   if constexpr (SMEM) {
-#pragma unroll 4
-    for (int t = tid; t < L; t += NT) keys[t] = make_key(t);
+#pragma unroll 8
+    for (int i = tid; i < n; i += NT) keys[i] = make_key(base + i);
   }
-  auto key_of = [&](int t) -> uint32_t {
-    if constexpr (SMEM) return keys[t];
-    else return make_key(t);
+  auto key_of = [&](int i) -> uint32_t {             // slot base + i
+    if constexpr (SMEM) return keys[i];
+    else return make_key(base + i);
   };
+  __syncthreads();
   // ---- the budget-th largest key: 8 bits a pass from the top
   uint32_t prefix = 0, mask = 0;
   int left = p.budget;                    // how many of the keys that match the prefix are kept
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256 * kHistCopies; i += NT) hist[i] = 0;
-    __syncthreads();
-    for (int t = tid; t < L; t += NT) {
-      const uint32_t k = key_of(t);
-      if ((k & mask) == prefix) atomicAdd(&hist[((k >> shift) & 255u) * kHistCopies + (lane & (kHistCopies - 1))], 1);
+#pragma unroll 1
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    int* bins = hist[pass][lane & (kCopies - 1)];
+    if (pass == 0) {
+      // the leading bits of most weights are the same few: one addition per digit and warp
+      for (int i0 = tid - lane; i0 < n; i0 += NT) {
+        const bool in = i0 + lane < n;
+        const int d = in ? (int)(key_of(i0 + lane) >> 24) : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, d);
+        if (in && (same & ((1u << lane) - 1u)) == 0) atomicAdd(&bins[d + (d >> 3)], __popc(same));
+      }
+    } else {
+#pragma unroll 4
+      for (int i = tid; i < n; i += NT) {
+        const uint32_t k = key_of(i);
+        const int d = (int)(k >> shift) & 255;
+        if ((k & mask) == prefix) atomicAdd(&bins[d + (d >> 3)], 1);
+      }
     }
-    __syncthreads();
-    if (tid < 256) {
-      int c = 0;
-#pragma unroll
-      for (int i = 0; i < kHistCopies; ++i) c += hist[tid * kHistCopies + ((i + tid) & (kHistCopies - 1))];
-      hist[tid * kHistCopies] = c;        // (a thread's own eight words)
-    }
-    __syncthreads();
+    sync_all<CS>();
     if (warp == 0) {
-      // lane l holds digits 255-8l .. 248-8l, the largest first
+      // lane l holds digits 255-8l .. 248-8l, the largest first: 9 (31 - l) + 7 - i in the padded bins
       int c[8], sum = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        c[i] = hist[(255 - 8 * lane - i) * kHistCopies];
+        c[i] = 0;
+#pragma unroll
+        for (int k = 0; k < kCopies; ++k) {
+          const int* bin = &hist[pass][k][9 * (31 - lane) + 7 - i];
+          if constexpr (CS == 1) {
+            c[i] += *bin;
+          } else {
+#pragma unroll
+            for (int r = 0; r < CS; ++r) c[i] += ld_cluster(bin, r);
+          }
+        }
         sum += c[i];
       }
       int incl = sum;
@@ -176,88 +254,88 @@ __global__ void __launch_bounds__(NT) select_kernel(const EvictParams p) {
         if (lane >= off) incl += y;
       }
       int before = incl - sum;
-      if (before < left && left <= incl) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (before < left && left <= before + c[i]) {
-            sh_digit = 255 - 8 * lane - i;
-            sh_left = left - before;
-          }
-          before += c[i];
+      for (int i = 0; i < 8; ++i) {
+        if (before < left && left <= before + c[i]) {     // in exactly one lane
+          sh_digit = 255 - 8 * lane - i;
+          sh_left = left - before;
         }
+        before += c[i];
       }
     }
     __syncthreads();
     prefix |= (uint32_t)sh_digit << shift;
-    mask |= 0xffu << shift;
     left = sh_left;
-    __syncthreads();
+    mask |= 0xffu << shift;
+    // (the next write to the pair comes after a barrier)
   }
   // keys above `prefix` are kept, and the first `left` of those equal to it
 
   // ---- each warp's run of slots, 32 at a time
-  const int run = ((L + NT - 1) / NT) * 32;
-  const int r0 = min(L, warp * run), r1 = min(L, r0 + run);
+  const int run = ((n + NT - 1) / NT) * 32;
+  const int r0 = min(n, warp * run), r1 = min(n, r0 + run);
   const unsigned lt = (1u << lane) - 1u;
   int eq = 0, total;
-  for (int t0 = r0; t0 < r1; t0 += 32) {
-    const int t = t0 + lane;
-    eq += __popc(__ballot_sync(0xffffffffu, t < r1 && key_of(t) == prefix));
-  }
-  const int tie0 = scan_warps<NW>(eq, wbuf, total);
-  auto stays = [&](int t, int& ties) -> unsigned {     // the 32 slots' answer, ties counted on
-    const uint32_t k = t < r1 ? key_of(t) : 0u;
-    const unsigned me = __ballot_sync(0xffffffffu, t < r1 && k == prefix);
-    const bool s = t < r1 && (k > prefix || (k == prefix && ties + __popc(me & lt) < left));
-    ties += __popc(me);
-    return __ballot_sync(0xffffffffu, s);
+  for (int i0 = r0; i0 < r1; i0 += 32)
+    eq += __popc(__ballot_sync(0xffffffffu, i0 + lane < r1 && key_of(i0 + lane) == prefix));
+  int ties = scan_warps<NW, CS>(eq, wbuf[0], rank, total);
+  // slots of the 32 from base + i0 that are in the run, and those below the budget
+  auto in_run = [&](int i0) -> unsigned { return r1 - i0 >= 32 ? 0xffffffffu : (1u << (r1 - i0)) - 1u; };
+  auto below = [&](int i0) -> unsigned {
+    const int t0 = base + i0;
+    return t0 + 32 <= p.budget ? 0xffffffffu : t0 < p.budget ? (1u << (p.budget - t0)) - 1u : 0u;
   };
-  int ties = tie0, holes = 0, movers = 0;
-  for (int t0 = r0; t0 < r1; t0 += 32) {
-    const unsigned s = stays(t0 + lane, ties);
-    const unsigned in = r1 - t0 >= 32 ? 0xffffffffu : (1u << (r1 - t0)) - 1u;          // slots of the run
-    const unsigned low = t0 + 32 <= p.budget ? 0xffffffffu : t0 < p.budget ? (1u << (p.budget - t0)) - 1u : 0u;
-    holes += __popc(in & low & ~s);
-    movers += __popc(s & ~low);
+  int holes = 0, movers = 0;
+  for (int i0 = r0; i0 < r1; i0 += 32) {
+    const bool in = i0 + lane < r1;
+    const uint32_t k = in ? key_of(i0 + lane) : 0u;
+    const unsigned me = __ballot_sync(0xffffffffu, in && k == prefix);
+    const unsigned s =
+        __ballot_sync(0xffffffffu, in && (k > prefix || (k == prefix && ties + __popc(me & lt) < left)));
+    ties += __popc(me);
+    if (lane == 0) stay_bits[i0 >> 5] = s;
+    holes += __popc(in_run(i0) & below(i0) & ~s);
+    movers += __popc(s & ~below(i0));
   }
-  int hole0 = scan_warps<NW>(holes, wbuf, total);
+  int hole0 = scan_warps<NW, CS>(holes, wbuf[1], rank, total);
   const int nmove = total;                             // as many movers as holes
-  int mover0 = scan_warps<NW>(movers, wbuf, total);
+  int mover0 = scan_warps<NW, CS>(movers, wbuf[2], rank, total);
   Move* mv = p.moves + (size_t)bh * p.cap;
   int32_t* dst = p.dst + (size_t)bh * p.cap;
-  ties = tie0;
-  for (int t0 = r0; t0 < r1; t0 += 32) {
-    const int t = t0 + lane;
-    const unsigned s = stays(t, ties);
-    const unsigned in = r1 - t0 >= 32 ? 0xffffffffu : (1u << (r1 - t0)) - 1u;
-    const unsigned low = t0 + 32 <= p.budget ? 0xffffffffu : t0 < p.budget ? (1u << (p.budget - t0)) - 1u : 0u;
-    const unsigned hm = in & low & ~s, cm = s & ~low;
-    const unsigned bit = 1u << lane;
-    if (in & low & bit) {
+  for (int i0 = r0; i0 < r1; i0 += 32) {
+    const unsigned s = stay_bits[i0 >> 5], low = in_run(i0) & below(i0);
+    const unsigned hm = low & ~s, cm = s & ~below(i0), bit = 1u << lane;
+    const int t = base + i0 + lane;
+    if (low & bit) {
       const int at = hole0 + __popc(hm & lt);
       if ((t & (p.bs - 1)) == 0) first[t / p.bs] = at;
-      if (hm & bit) {
-        dst[at] = t;
-      } else {
-        // (in and out may be the same row)
-        const float wt = w[t];
-        const int pt = pos_of(t);
-        wo[t] = wt;
-        po[t] = pt;
-      }
+      if (hm & bit) dst[at] = t;
     } else if (cm & bit) {
       mv[mover0 + __popc(cm & lt)].src = t;
     }
     hole0 += __popc(hm);
     mover0 += __popc(cm);
   }
-  if (tid == 0) first[p.nb] = nmove;
-  __syncthreads();
-  // ---- the movers' weights, positions and scales, then the rest of the rows
-  for (int i = tid; i < nmove; i += NT) {
-    const int s = mv[i].src;
-    wo[dst[i]] = w[s];
-    po[dst[i]] = pos_of(s);
+  if (gid == 0) first[p.nb] = nmove;
+  sync_all<CS>();
+  // ---- what stays below the budget, the movers' weights, positions and scales, then the rest of the
+  // rows (in and out may be the same: a slot below the budget is read by its own thread only, and the
+  // movers' slots are cleared after they have been read)
+#pragma unroll 4
+  for (int i = tid; i < min(n, newL - base); i += NT) {
+    if ((stay_bits[i >> 5] >> (i & 31)) & 1u) {
+      const int t = base + i;
+      const float wt = w[t];
+      const int pt = pos_of(t);
+      wo[t] = wt;
+      po[t] = pt;
+    }
+  }
+#pragma unroll 2
+  for (int i = gid; i < nmove; i += CS * NT) {
+    const int s = mv[i].src, d = dst[i];
+    const float wt = w[s];
+    const int pt = pos_of(s);
     if (p.elem == 1) {
       const int blk = __ldg(&p.block_tables[(size_t)b * p.max_blocks + s / p.bs]);
       if ((unsigned)blk < (unsigned)p.num_blocks) {
@@ -265,12 +343,11 @@ __global__ void __launch_bounds__(NT) select_kernel(const EvictParams p) {
         mv[i].v_scale = p.scale[1][(size_t)blk * p.scale_row + h];
       }
     }
+    wo[d] = wt;
+    po[d] = pt;
   }
-  __syncthreads();
-  for (int t = newL + tid; t < Lmax; t += NT) {
-    wo[t] = 0.f;
-    po[t] = -1;
-  }
+  sync_all<CS>();
+  clear_from(newL);
 }
 
 // Two conversions of two values each, the first value in the low byte.
@@ -447,9 +524,9 @@ extern "C" int pa_evict(void* k_cache, void* v_cache, float* k_scale, float* v_s
   const bool fp8 = kv_dtype == PA_FP8_E4M3;
   const long long max_ctx = (long long)max_blocks_per_seq * block_size;
   if (num_seqs < 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || num_kv_heads <= 0 ||
-      !supported_head_dim(head_dim) || !supported_block_size(block_size) || max_ctx > 0x7fffffffll ||
+      !supported_head_dim(head_dim) || !supported_block_size(block_size) || max_ctx > kMaxTokens ||
       row_stride < max_ctx || budget <= 0 || recent < 0 || sinks < 0 || (long long)recent + sinks > budget ||
-      (long long)num_seqs * num_kv_heads > 0x7fffffffll)
+      (long long)num_seqs * num_kv_heads * kCluster > 0x7fffffffll)
     return PA_ERR_SHAPE;
   if (num_seqs == 0) return PA_OK;
   if (!k_cache || !v_cache || !block_tables || !context_lens || !kept_lens || !seen_lens || !weights || !token_pos ||
@@ -497,22 +574,37 @@ extern "C" int pa_evict(void* k_cache, void* v_cache, float* k_scale, float* v_s
   p.dst = reinterpret_cast<int32_t*>(ws + l.dst);
   p.first = reinterpret_cast<int32_t*>(ws + l.first);
   p.ws_len = reinterpret_cast<int32_t*>(ws + l.len);
-  // Few slots: 256 threads, several (sequence, head) rows per SM; many: 1024.
-  const bool in_smem = max_ctx <= kMaxSmemKeys;
-  const size_t smem = in_smem ? (size_t)max_ctx * 4 : 0;
+  // Up to 4096 slots: one CTA of 256 threads, several (sequence, head) rows per SM;
+  // above: a cluster of four of 512.
   const bool wide = max_ctx > 4096;
-  const void* select = !in_smem ? reinterpret_cast<const void*>(&select_kernel<1024, false>)
-                       : wide   ? reinterpret_cast<const void*>(&select_kernel<1024, true>)
-                                : reinterpret_cast<const void*>(&select_kernel<256, true>);
+  const int cs = wide ? kCluster : 1;
+  const long long slots = wide ? ((max_ctx + cs - 1) / cs + 31) / 32 * 32 : max_ctx;    // of a CTA
+  const bool in_smem = slots <= kMaxSmemKeys;
+  int words = (int)((slots + 31) / 32);
+  const size_t smem = (size_t)words * 4 + (in_smem ? (size_t)slots * 4 : 0);
+  const void* select = !wide     ? reinterpret_cast<const void*>(&select_kernel<256, 1, true>)
+                       : in_smem ? reinterpret_cast<const void*>(&select_kernel<512, kCluster, true>)
+                                 : reinterpret_cast<const void*>(&select_kernel<512, kCluster, false>);
   if (smem > 32 * 1024) {
-    if (!ck(cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemKeys * 4),
+    // (static bins of 9 KB come on top)
+    if (!ck(cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, 204 * 1024),
             "cudaFuncSetAttribute(select_kernel)"))
       return PA_ERR_CUDA;
   }
-  void* args[] = {&p};
-  if (!ck(cudaLaunchKernel(select, dim3((unsigned)rows), dim3(wide ? 1024u : 256u), args, smem, (cudaStream_t)stream),
-          "cudaLaunchKernel(select_kernel)"))
-    return PA_ERR_CUDA;
+  void* args[] = {&p, &words};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * cs));
+  cfg.blockDim = dim3(wide ? 512u : 256u);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = (cudaStream_t)stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)cs;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = wide ? 1 : 0;
+  if (!ck(cudaLaunchKernelExC(&cfg, select, args), "cudaLaunchKernelExC(select_kernel)")) return PA_ERR_CUDA;
   int per_arg = per;
   void* margs[] = {&p, &per_arg};
   if (!ck(launch_after(reinterpret_cast<const void*>(&move_kernel), dim3((unsigned)blocks), dim3(kMoveWarps * 32),

@@ -82,7 +82,7 @@ def test_weights(pa, kw, code):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(budget=0), -2), (dict(recent=-1), -2), (dict(sinks=-1), -2), (dict(recent=20, sinks=13), -2),
-    (dict(stride=63), -2), (dict(bs=5), -2), (dict(D=16), -2), (dict(kv=3), -3), (dict(k=NULL), -1),
+    (dict(stride=63), -2), (dict(mb=393217, stride=1 << 40), -2), (dict(bs=5), -2), (dict(D=16), -2), (dict(kv=3), -3), (dict(k=NULL), -1),
     (dict(new=NULL), -1), (dict(kv=2, ks=NULL), -1), (dict(k=ODD), -4), (dict(ws=ODD), -4), (dict(ws=NULL), -5),
     (dict(n=8), -5), (dict(B=0), 0)])
 def test_evict(pa, kw, code):

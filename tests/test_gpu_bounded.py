@@ -198,9 +198,11 @@ def test_evict_all_equal_negative_and_not_finite_weights(pa):
     assert _evict_both(pa, c, w, pos, kl, seen, 100, 0, 0, False) == 0
 
 
-def test_evict_long_context(pa):
-    args = _evict_inputs("bf16", [70001, 5], 1, 32, 32, 2048, seed=5)
-    assert _evict_both(pa, *args, 2048, 256, 4, False) == 0
+@pytest.mark.parametrize("L", [4097, 70001, 200003])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_long_context(pa, L, in_place):
+    args = _evict_inputs("bf16", [L, 5, 2500], 1, 32, 32, 2048, seed=5, ties=L < 5000)
+    assert _evict_both(pa, *args, 2048, 256, 4, in_place) == 0
 
 
 def test_evict_lengths_out_of_range_are_clamped_and_flagged(pa):
