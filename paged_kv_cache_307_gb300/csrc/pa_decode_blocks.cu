@@ -158,7 +158,7 @@ int run(void* out, const void* query, const void* k_cache, const void* v_cache, 
   if (keep) return launch_weights(L, prm, wa, stream);
   if (max_parts > 1) {
     void* args[] = {&prm};
-    if (!ck(launch_dependent(L.merge, dim3((unsigned)rows), dim3(kFinishThreads), args, 0, (cudaStream_t)stream),
+    if (!ck(launch_dependent(L.merge, dim3(merge_ctas_of(prm)), dim3(kFinishThreads), args, 0, (cudaStream_t)stream),
             "cudaLaunchKernel(merge_wide_kernel)"))
       return PA_ERR_CUDA;
   }
@@ -184,10 +184,15 @@ int launch_weights(const Launch& L, const DecodeParams& prm, const WeightsArgs& 
   DecodeParams p = prm;
   float* w = wa.weights;
   long long stride = wa.stride;
-  unsigned merge_ctas = p.max_parts > 1 ? (unsigned)(p.B * p.Hq) : 0u;
+  unsigned merge_ctas = merge_ctas_of(p);
   const long long max_ctx = (long long)p.max_blocks * p.bs;
-  const long long ctas = merge_ctas + (long long)p.B * p.Hkv * ((max_ctx + kWeightTokens - 1) / kWeightTokens);
-  void* args[] = {&p, &w, &stride, &merge_ctas};
+  // one wave of CTAs at the table's capacity (eight fit an SM) where the chunks allow it
+  const long long all = (long long)p.B * p.Hkv * ((max_ctx + kWeightTokens - 1) / kWeightTokens);
+  int chunks = (int)(all / (8 * 152));
+  chunks = chunks < 1 ? 1 : chunks > 8 ? 8 : chunks;
+  const long long span = (long long)chunks * kWeightTokens;
+  const long long ctas = merge_ctas + (long long)p.B * p.Hkv * ((max_ctx + span - 1) / span);
+  void* args[] = {&p, &w, &stride, &merge_ctas, &chunks};
   return ck(launch_dependent(L.merge, dim3((unsigned)ctas), dim3(kFinishThreads), args, 2 * (size_t)p.G * 4,
                              (cudaStream_t)stream),
             "cudaLaunchKernel(weights_kernel)")

@@ -1613,16 +1613,16 @@ merge_kernel(const DecodeParams p) {
   for (int k = 0; k < VPL; ++k) E::store1(out + k, acc[k] * inv);
 }
 
-// One CTA per (sequence, query head): the merge of merge_kernel with the
-// partitions spread over the CTA's eight warps.  A warp reads its partials four
-// in flight; a long context of few sequences has few rows and many partials,
-// and one warp walking 128 of them took 20 us of a 47 us call.
+// The merge of merge_kernel for one (sequence, query head) by NW warps of a CTA, the
+// partitions spread over them, four partials in flight per warp.  A long context of
+// few sequences has few rows and many partials: one warp walking 128 of them took
+// 20 us of a 47 us call.  A row of few partials takes one warp.
 constexpr int kFinishThreads = 256;
-template <typename T, int D>
+constexpr int kNarrowParts = 16;           // partials up to which a row has one warp
+template <typename T, int D, int NW>
 __device__ __forceinline__ void merge_row_wide(const DecodeParams& p, int bh) {
   using E = Elem<T>;
-  constexpr int NW = kFinishThreads / 32, VPL = D / 32;
-  __shared__ float so[NW][D], sm[NW], sl[NW];
+  constexpr int VPL = D / 32;
   const int b = bh / p.Hq;
   int L = __ldg(&p.context_lens[b]);
   const int Lmax = p.max_blocks * p.bs;
@@ -1630,7 +1630,7 @@ __device__ __forceinline__ void merge_row_wide(const DecodeParams& p, int bh) {
   const int nparts = L > 0 ? (L + p.part_tokens - 1) / p.part_tokens : 1;
   if (nparts <= 1) return;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = NW == 1 ? 0 : threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float* ml = p.ws_ml + (size_t)bh * p.max_parts * 2;
   const float* po = p.ws_o + (size_t)bh * p.max_parts * D + lane * VPL;
   float M = -INFINITY, den = 0.f, acc[VPL];
@@ -1661,77 +1661,105 @@ __device__ __forceinline__ void merge_row_wide(const DecodeParams& p, int bh) {
       for (int d = 0; d < VPL; ++d) acc[d] = fmaf(w, v[k][d], acc[d]);
     }
   }
+  T* out = static_cast<T*>(p.out) + (size_t)bh * D;
+  if constexpr (NW == 1) {
+    const float inv = den != 0.f ? 1.f / den : 0.f;
 #pragma unroll
-  for (int d = 0; d < VPL; ++d) so[warp][lane * VPL + d] = acc[d];
-  if (lane == 0) {
-    sm[warp] = M;
-    sl[warp] = den;
-  }
-  __syncthreads();
-  if ((int)threadIdx.x < D) {
-    float Mx = sm[0];
+    for (int d = 0; d < VPL; ++d) E::store1(out + lane * VPL + d, acc[d] * inv);
+  } else {
+    __shared__ float so[NW][D], sm[NW], sl[NW];
 #pragma unroll
-    for (int w = 1; w < NW; ++w) Mx = fmaxf(Mx, sm[w]);
-    float num = 0.f, dsum = 0.f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const float f = sm[w] == -INFINITY ? 0.f : exp2f(sm[w] - Mx);
-      num = fmaf(f, so[w][threadIdx.x], num);
-      dsum = fmaf(f, sl[w], dsum);
+    for (int d = 0; d < VPL; ++d) so[warp][lane * VPL + d] = acc[d];
+    if (lane == 0) {
+      sm[warp] = M;
+      sl[warp] = den;
     }
-    E::store1(static_cast<T*>(p.out) + (size_t)bh * D + threadIdx.x, dsum != 0.f ? num / dsum : 0.f);
+    __syncthreads();
+    if ((int)threadIdx.x < D) {
+      float Mx = sm[0];
+#pragma unroll
+      for (int w = 1; w < NW; ++w) Mx = fmaxf(Mx, sm[w]);
+      float num = 0.f, dsum = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float f = sm[w] == -INFINITY ? 0.f : exp2f(sm[w] - Mx);
+        num = fmaf(f, so[w][threadIdx.x], num);
+        dsum = fmaf(f, sl[w], dsum);
+      }
+      E::store1(out + threadIdx.x, dsum != 0.f ? num / dsum : 0.f);
+    }
   }
+}
+
+// CTA x of the merge: one row, or one for each of its warps.
+template <typename T, int D>
+__device__ __forceinline__ void merge_cta(const DecodeParams& p, int x) {
+  constexpr int W = kFinishThreads / 32;
+  if (p.max_parts > kNarrowParts) {
+    merge_row_wide<T, D, W>(p, x);
+  } else {
+    const int bh = x * W + (int)(threadIdx.x >> 5);
+    if (bh < p.B * p.Hq) merge_row_wide<T, D, 1>(p, bh);
+  }
+}
+inline unsigned merge_ctas_of(const DecodeParams& p) {
+  const int W = kFinishThreads / 32;
+  return p.max_parts <= 1 ? 0u : (unsigned)(p.max_parts > kNarrowParts ? p.B * p.Hq : (p.B * p.Hq + W - 1) / W);
 }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kFinishThreads) merge_wide_kernel(const DecodeParams p) {
-  merge_row_wide<T, D>(p, (int)blockIdx.x);
+  merge_cta<T, D>(p, (int)blockIdx.x);
 }
 
-// Weights mode's second kernel: the first `merge_ctas` CTAs merge a row's
-// partitions; each of the others takes one (sequence, KV head, 1024 tokens) and
-// adds the softmax weights to their running totals:
+// Weights mode's second kernel: the first `merge_ctas` CTAs merge the rows'
+// partitions; each of the others takes one (sequence, KV head, `chunks` times 1024
+// tokens) and adds the softmax weights to their running totals:
 //   weights[b, g, t] += sum over the group's heads h of 2^(s[b,h,t] - M_h) / l_h
 // with (M_h, l_h) the log-sum-exp of the partitions' states.  A thread has four
-// tokens, 256 apart, whose scores of four heads are on their way while the
-// states are merged; heads are added in order: no atomics, the same sum on every
-// run.
+// tokens of a chunk, 256 apart; the first chunk's scores of four heads are on their
+// way while the states are merged.  Heads are added in order: no atomics, the same
+// sum on every run.
 constexpr int kWeightTokens = 4 * kFinishThreads;
 template <typename T, int D>
 __global__ void __launch_bounds__(kFinishThreads)
-weights_kernel(const DecodeParams p, float* weights, long long wstride, unsigned merge_ctas) {
+weights_kernel(const DecodeParams p, float* weights, long long wstride, unsigned merge_ctas, int chunks) {
   extern __shared__ float hm[];               // [G] M_h, then [G] 1 / l_h
   if (blockIdx.x < merge_ctas) {
-    merge_row_wide<T, D>(p, (int)blockIdx.x);
+    merge_cta<T, D>(p, (int)blockIdx.x);
     return;
   }
   const int Lmax = p.max_blocks * p.bs;
-  const int nt = (Lmax + kWeightTokens - 1) / kWeightTokens;
+  const int span = chunks * kWeightTokens;
+  const int nt = (Lmax + span - 1) / span;
   long long u = (long long)blockIdx.x - merge_ctas;
-  const int t0 = (int)(u % nt) * kWeightTokens;
+  const int t0 = (int)(u % nt) * span;
   u /= nt;
   const int g = (int)(u % p.Hkv), b = (int)(u / p.Hkv);
   int L = __ldg(&p.context_lens[b]);
   L = L < 0 ? 0 : min(L, Lmax);
   if (t0 >= L) return;
-  const int t = t0 + (int)threadIdx.x;
   const int nparts = (L + p.part_tokens - 1) / p.part_tokens;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const size_t row0 = (size_t)b * p.Hq + (size_t)g * p.G;
-  const float* sp = p.ws_s + row0 * Lmax + t;
-  float* wp = weights + ((size_t)b * p.Hkv + g) * wstride + t;
-  float s[4][4], was[4], sum[4] = {0.f, 0.f, 0.f, 0.f};
+  const float* sp = p.ws_s + row0 * Lmax;
+  float* wp = weights + ((size_t)b * p.Hkv + g) * wstride;
+  int t = t0 + (int)threadIdx.x;
+  float s[4][4], was[4];
   auto load = [&](int h) {                    // the scores of heads h .. h + 3
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        s[i][k] = h + i < p.G && t + k * kFinishThreads < L ? sp[(size_t)(h + i) * Lmax + k * kFinishThreads] : 0.f;
+        s[i][k] = h + i < p.G && t + k * kFinishThreads < L ? sp[(size_t)(h + i) * Lmax + t + k * kFinishThreads] : 0.f;
+  };
+  auto load_totals = [&]() {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) was[k] = t + k * kFinishThreads < L ? wp[t + k * kFinishThreads] : 0.f;
   };
   load(0);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) was[k] = t + k * kFinishThreads < L ? wp[k * kFinishThreads] : 0.f;
+  load_totals();
   for (int h = warp; h < p.G; h += kFinishThreads / 32) {
     const float* ml = p.ws_ml + (row0 + h) * p.max_parts * 2;
     float M = -INFINITY, den = 0.f;
@@ -1739,7 +1767,7 @@ weights_kernel(const DecodeParams p, float* weights, long long wstride, unsigned
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     for (int i = lane; i < nparts; i += 32)
-      den += ml[2 * i] == -INFINITY ? 0.f : exp2f(ml[2 * i] - M) * ml[2 * i + 1];
+      den += ml[2 * i] == -INFINITY ? 0.f * ml[2 * i + 1] : exp2f(ml[2 * i] - M) * ml[2 * i + 1];
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
     if (lane == 0) {
@@ -1748,19 +1776,26 @@ weights_kernel(const DecodeParams p, float* weights, long long wstride, unsigned
     }
   }
   __syncthreads();
-  for (int h = 0; h < p.G; h += 4) {
-    if (h > 0) load(h);
+  for (int c = 0;; ) {
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int h = 0; h < p.G; h += 4) {
+      if (h > 0) load(h);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (h + i < p.G) {
-        const float M = hm[h + i], inv = hm[p.G + h + i];
+      for (int i = 0; i < 4; ++i)
+        if (h + i < p.G) {
+          const float M = hm[h + i], inv = hm[p.G + h + i];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sum[k] = fmaf(exp2f(s[i][k] - M), inv, sum[k]);
-      }
+          for (int k = 0; k < 4; ++k) sum[k] = fmaf(exp2f(s[i][k] - M), inv, sum[k]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (t + k * kFinishThreads < L) wp[t + k * kFinishThreads] = was[k] + sum[k];
+    if (++c == chunks || t0 + c * kWeightTokens >= L) break;
+    t += kWeightTokens;
+    load(0);
+    load_totals();
   }
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (t + k * kFinishThreads < L) wp[k * kFinishThreads] = was[k] + sum[k];
 }
 
 }  // namespace
