@@ -260,6 +260,10 @@ inline int elem_bytes(pa_dtype dt) { return dt == PA_F32 ? 4 : dt == PA_FP8_E4M3
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// The block-scaled cache's and the weight-keeping calls' longest table row, in tokens:
+// a tile's or a step's last token then fits 32 bits wherever it starts in a row.
+constexpr long long kMaxRowTokens = 1ll << 30;
+
 inline bool supported_head_dim(int d) { return d == 32 || d == 64 || d == 128; }
 inline bool supported_block_size(int bs) { return bs == 4 || bs == 8 || bs == 16 || bs == 32; }
 

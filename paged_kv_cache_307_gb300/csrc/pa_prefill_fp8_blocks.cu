@@ -14,26 +14,34 @@
 //    down to 2^-10 of the largest and within 2^-17 of it below.  K's scales stay apart,
 //    in the softmax.
 //  * P V runs in bf16.  V's codes come by TMA into a stage of their own; warps 8-11
-//    widen them (cvt.rn.f16x2.e4m3x2), multiply their scale in (exact for a power of
-//    two; bf16 has the exponents for it, so a row that attends only to blocks of
-//    small scale keeps its precision beside blocks of large scale) and write the
-//    128-byte-swizzled tile that both query tiles' MMAs read: widening a tile is
-//    as many instructions as its softmax, and the pair shares it.
+//    widen them (codes_to_bf16), multiply their scale in (exact for a power of two;
+//    bf16 has the exponents for it, so a row that attends only to blocks of small scale
+//    keeps its precision beside blocks of large scale) and write the 128-byte-swizzled
+//    tile that both query tiles' MMAs read: widening a tile is as many instructions as
+//    its softmax, and the pair shares it.
 //  * One thread per row (warps 0-3 and 4-7, a query tile each): x = s * (K scale of
 //    the key's block) * (row factor), running maximum and sum, P = 2^(x - m) in bf16
 //    over the S columns.  The reference only moves when the maximum has grown by 2^8.
-//  * Tensor memory is full: an S (then P) of 128 columns and an O of 128 for each
-//    query tile.  Warp 13 alternates between the tiles, P V then the next S of one
-//    while the other's softmax runs.  128 keys an MMA: at 64 the tensor core waits for
-//    its A operand (48 clocks for half the work of 68).
-//  * Keys at or past the context length are zeros in the V tile, whatever the pool
-//    holds there.  Every wait is bounded (2 s).
+//  * A query tile goes in steps of 64 keys.  Tensor memory is full: two buffers of 64
+//    columns for S (then P) and an O of 128 for each query tile.  Warps 13 and 14 issue
+//    a query tile's MMAs each: P V of a step, then the S of the next but one, so that
+//    the step's successor has its scores already.  (Steps of 128 keys in one buffer
+//    make less of the tensor core wait for its A operand, 68 clocks an MMA against 48
+//    for half the work, but chain softmax, P V and S: 8 chunks of 512 queries took
+//    218 us and not 191.  One issuing warp for both tiles: 235, its waits in a row.)
+//  * Keys at or past the context length have P = 0, and in the V tile they are finite
+//    whatever the pool holds: a NaN code comes out finite, a block past the context with
+//    a scale of 0.  A NaN of a key in the context has to reach the rows at and past it
+//    and no others of its tile: the first such key of each head dim is noted and makes
+//    NaN of that dim at the end.  Every wait is bounded (2 s).
 //
 // rows_kernel: one warp per (row, query head), for the other sizes.  Lane t of a step of
 // 32 keys computes one key's whole score from its row of codes; the warp takes
 // the running maximum and sum, then every lane accumulates its D / 32 head
 // dims over the 32 keys.  The block's K scale multiplies the score, its V scale
 // the softmax weight; the sum of the softmax is over the unscaled weights.
+#include <float.h>
+#include <limits.h>
 #include <stddef.h>
 
 #include "pa_tc.cuh"
@@ -154,9 +162,10 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const Params p) {
 
 // ------------------------------------------------------------------ tile_kernel
 
-constexpr int kTileThreads = 448;      // 2 x 4 softmax, 4 V, TMA and MMA warps
+constexpr int kTileThreads = 480;      // 2 x 4 softmax, 4 V, TMA and 2 MMA warps
 constexpr int kRows = 128;
 constexpr int kKT = 128;               // keys per tile
+constexpr int kStep = 64;              // keys per step of a query tile
 constexpr int kKStages = 3;
 constexpr uint32_t kQHalf = 16384;     // 128 rows x 128 bytes
 constexpr uint32_t kCodes = 16384;     // 128 keys x 128 codes
@@ -166,21 +175,24 @@ constexpr uint32_t kOffK = 65536;      // 3 stages of codes
 constexpr uint32_t kOffV = 114688;     // 2 stages x 2 halves of bf16
 constexpr uint32_t kOffRawV = 180224;  // 2 stages of codes
 constexpr uint32_t kOffBar = 212992;
-constexpr uint32_t kTileSmem = kOffBar + 1024 + 1024;   // + alignment slack
+constexpr uint32_t kTileSmem = kOffBar + 2048 + 1024;   // + alignment slack
 constexpr float kRescaleThreshold = 8.0f;               // log2 units
 constexpr uint32_t kTmemCols = 512;    // query tile h: S (and P) at columns 128 h, O at 256 + 128 h
 
 struct Bars {
   uint64_t q[2], qf[2], full_k[kKStages], empty_k[kKStages], raw_v[2], raw_ev[2], full_v[2], empty_v[2];
-  uint64_t s[2], p[2][2], pv[2], scl_full[4], drain;
+  uint64_t s[2][2], p[2][2], pv[2], scl_full[4], drain[2];
   // K scale of every 4 keys (block sizes are multiples of 4) of tile t in slot
   // t & 3: those of t+1 to t+3 may be written while the softmax reads t's, t+4's
   // only after P_t (its K stage waits for S_{t+1}, which is issued after P_t)
   alignas(16) float kscl[4][kKT / 4];
+  // first key whose V is NaN, of every head dim, and whether there is any
+  int nan_key[128];
+  int any_nan;
   uint32_t tmem_base;
   int abort;
 };
-static_assert(sizeof(Bars) <= 1024 && offsetof(Bars, kscl) % 16 == 0, "barrier block");
+static_assert(sizeof(Bars) <= 2048 && offsetof(Bars, kscl) % 16 == 0, "barrier block");
 
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   if (*abort_flag) return false;
@@ -223,6 +235,36 @@ __device__ __forceinline__ void from_e4m3x4(uint32_t c, float* f) {
   f16x2_to_float2(b, f[2], f[3]);
 }
 
+// Four codes' bits 7: set for a NaN (the other bits say nothing).
+__device__ __forceinline__ uint32_t nan_bits(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
+// The NaN among the sixteen codes of key t, head dims d and on.
+__device__ __noinline__ void note_nan(uint4 c, Bars* bars, int d, int t, int kend) {
+  if (t >= kend) return;
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    for (uint32_t m = nan_bits(w[k]) & 0x80808080u; m; m &= m - 1) {
+      atomicMin(&bars->nan_key[d + 4 * k + ((__ffs(m) - 1) >> 3)], t);
+      bars->any_nan = 1;
+    }
+  }
+}
+// Four codes times s (bf16 in both halves) as bf16 pairs.  A code's seven magnitude bits, taken for
+// the last four of a bf16's exponent and the first three of its digits, are its value times 2^-120,
+// the subnormal ones too; two products put that right and the scale in (one factor s 2^120 would
+// overflow for s >= 2^8).  A NaN code comes out as 480 s: finite, so that 0 times it is 0.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t s, uint32_t& a, uint32_t& b) {
+  const uint32_t hi = ((w >> 4) & 0x07070707u) | (w & 0x80808080u), lo = (w << 4) & 0xf0f0f0f0u;
+  constexpr uint32_t kUp = 0x7b807b80u;                  // 2^120
+  a = mul_bf16x2(mul_bf16x2(__byte_perm(lo, hi, 0x5140), kUp), s);
+  b = mul_bf16x2(mul_bf16x2(__byte_perm(lo, hi, 0x7362), kUp), s);
+}
+
 // V (four warps): the codes of each key tile as bf16 rows.  Thread x takes the
 // 16-code chunk x % 8 of rows x / 8, x / 8 + 16, ...
 __device__ __forceinline__ void convert_v(const Params& p, Bars* bars, unsigned char* smem, int b, int kvh, int kend,
@@ -237,15 +279,21 @@ __device__ __forceinline__ void convert_v(const Params& p, Bars* bars, unsigned 
   // codes 16 ch .. 16 ch + 15 are columns of half ch / 4, 16-byte chunks 2 (ch % 4) and the next
   unsigned char* tile = smem + kOffV + (ch >> 2) * kVHalf;
   const int c0 = (ch & 3) * 2;
-  auto id_of = [&](int t) -> int {
-    int id = 0;
-    if (t < nt && lane < nbt && t * kKT + (lane << bsh) < kend) id = __ldg(&tab[((t * kKT) >> bsh) + lane]);
-    return (unsigned)id < (unsigned)p.num_blocks ? id : 0;   // (flagged by the TMA warp)
+  auto id_of = [&](int t) -> int {                       // -1: no block of the context
+    if (t < nt && lane < nbt && t * kKT + (lane << bsh) < kend) {
+      const int id = __ldg(&tab[((t * kKT) >> bsh) + lane]);
+      return (unsigned)id < (unsigned)p.num_blocks ? id : 0;   // (flagged by the TMA warp)
+    }
+    return -1;
   };
-  auto scale_of = [&](int id) -> float { return __ldg(&scales[(size_t)id * p.scale_row]); };
+  // as a bf16 in both halves; 0 past the context, where codes may be anything and P is 0
+  auto scale_of = [&](int id) -> uint32_t {
+    const __nv_bfloat162 x = __float2bfloat162_rn(id >= 0 ? __ldg(&scales[(size_t)id * p.scale_row]) : 0.f);
+    return *reinterpret_cast<const uint32_t*>(&x);
+  };
   // scales (a lane each) of the tile at hand and of the next, block ids of the one after
-  int id2 = 0;
-  float sc0 = 0.f, sc1 = 0.f;
+  int id2 = -1;
+  uint32_t sc0 = 0u, sc1 = 0u;
   if (nt > 0) {
     const int id0 = id_of(0), id1 = id_of(1);
     id2 = id_of(2);
@@ -267,27 +315,23 @@ __device__ __forceinline__ void convert_v(const Params& p, Bars* bars, unsigned 
       uint4 c[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) c[i] = *reinterpret_cast<const uint4*>(from + (rr + i * RS) * 128);
+      // bit 7 of a byte's magnitude plus one: set for the NaN code (0x7f, 0xff) alone
+      uint32_t bad = 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        bad |= nan_bits(c[i].x) | nan_bits(c[i].y) | nan_bits(c[i].z) | nan_bits(c[i].w);
+      if (bad & 0x80808080u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) note_nan(c[i], bars, ch * 16, t * kKT + rr + i * RS, kend);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = rr + i * RS;
         const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
         uint32_t o[8];
-        const float s = __shfl_sync(0xffffffffu, sc0, r >> bsh);
-        const uint64_t s2 = f2pack(s, s);
-        const bool live = t * kKT + r < kend;            // (P is 0 past it, and 0 * NaN is not)
+        const uint32_t s2 = __shfl_sync(0xffffffffu, sc0, r >> bsh);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t h[2];
-          e4m3x4_to_f16x2x2(w[k], h[0], h[1]);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float a, d;
-            f16x2_to_float2(h[e], a, d);
-            f2unpack(fmul2(f2pack(a, d), s2), a, d);
-            const __nv_bfloat162 pk = __floats2bfloat162_rn(a, d);
-            o[2 * k + e] = live ? *reinterpret_cast<const uint32_t*>(&pk) : 0u;
-          }
-        }
+        for (int k = 0; k < 4; ++k) codes_to_bf16(w[k], s2, o[2 * k], o[2 * k + 1]);
         *reinterpret_cast<uint4*>(dst + r * 128 + ((c0 ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4*>(dst + r * 128 + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
       }
@@ -338,8 +382,9 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
     return first < nq ? max(0, min(L, L - nq + min(first + QP, nq))) : 0;
   };
   const int kend = max(kend_of(0), kend_of(1));
-  const int nt0 = (kend_of(0) + kKT - 1) / kKT, nt1 = (kend_of(1) + kKT - 1) / kKT;
-  const int nt = max(nt0, nt1);
+  // key tiles of the pair, and steps of 64 keys of each query tile
+  const int nt = (kend + kKT - 1) / kKT;
+  const int ns0 = (kend_of(0) + kStep - 1) / kStep, ns1 = (kend_of(1) + kStep - 1) / kStep;
 
   if (threadIdx.x == 384) {
     for (int h = 0; h < 2; ++h) {
@@ -348,24 +393,26 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
       mbar_init(&bars->raw_v[h], 1);
       mbar_init(&bars->raw_ev[h], 128);
       mbar_init(&bars->full_v[h], 128);
-      mbar_init(&bars->empty_v[h], 1);
-      mbar_init(&bars->s[h], 1);
+      mbar_init(&bars->empty_v[h], 2);
+      mbar_init(&bars->drain[h], 1);
+      mbar_init(&bars->s[h][0], 1);
+      mbar_init(&bars->s[h][1], 1);
       mbar_init(&bars->p[h][0], 128);
       mbar_init(&bars->p[h][1], 128);
       mbar_init(&bars->pv[h], 1);
     }
     for (int i = 0; i < kKStages; ++i) {
       mbar_init(&bars->full_k[i], 1);
-      mbar_init(&bars->empty_k[i], 1);
+      mbar_init(&bars->empty_k[i], 2);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&bars->scl_full[i], 1);
-    mbar_init(&bars->drain, 1);
     bars->abort = 0;
+    bars->any_nan = 0;
     fence_mbar_init();
     prefetch_tensormap(&mapQ);
     const uint64_t pol = policy_evict_first();
     for (int h = 0; h < 2; ++h) {
-      if ((h ? nt1 : nt0) == 0) continue;
+      if ((h ? ns1 : ns0) == 0) continue;
       unsigned char* dst = smem + kOffQ + h * 2 * kQHalf;
       mbar_arrive_expect_tx(&bars->q[h], 2u * 128u * (uint32_t)(p.G * QP));
       tma_load_4d(dst, &mapQ, &bars->q[h], 0, kvh * p.G, qrow0 + q0 + h * QP, 0, pol);
@@ -373,6 +420,7 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
     }
   }
   __syncwarp();
+  if (threadIdx.x < 128) bars->nan_key[threadIdx.x] = INT_MAX;
   if (warp == 13) {
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
@@ -446,78 +494,64 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
       for (int t = max(0, issued_k - kKStages); t < issued_k; ++t)
         mbar_wait(&bars->full_k[t % kKStages], (uint32_t)(t / kKStages) & 1u);
       for (int t = max(0, issued_v - 2); t < issued_v; ++t) mbar_wait(&bars->raw_v[t & 1], (uint32_t)(t >> 1) & 1u);
-      if (nt0 > 0) mbar_wait(&bars->q[0], 0);
-      if (nt1 > 0) mbar_wait(&bars->q[1], 0);
+      if (ns0 > 0) mbar_wait(&bars->q[0], 0);
+      if (ns1 > 0) mbar_wait(&bars->q[1], 0);
     }
-  } else if (warp == 13) {
-    // ---------------------------------------------------------- MMA issuer
+  } else if (warp >= 13) {
+    // ---------------------------------------------------------- MMA issuers, one per query tile
     if (lane == 0 && nt > 0) {
-      constexpr uint32_t idS = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);   // e4m3, fp32
+      constexpr uint32_t idS = (1u << 4) | ((uint32_t)(kStep >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);   // e4m3, fp32
       constexpr uint32_t idO = idesc_bf16_f32(kRows, 128, false, true);   // V MN-major
-      const uint64_t dq = sdesc_sw128(sbase + kOffQ, 16, 1024), dk = sdesc_sw128(sbase + kOffK, 16, 1024);
+      const int h = warp - 13, ns = h ? ns1 : ns0;
+      const uint64_t dq = sdesc_sw128(sbase + kOffQ + h * 2 * kQHalf, 16, 1024), dk = sdesc_sw128(sbase + kOffK, 16, 1024);
       const uint64_t dv = sdesc_sw128(sbase + kOffV, kVHalf, 1024);
-      // scores of query tile h and the key tile in stage ks: hi, then lo, 32 head dims each
-      auto issue_s = [&](int h, int ks) {
-        const uint64_t dqh = sdesc_at(dq, (uint32_t)h * 2 * kQHalf), dkj = sdesc_at(dk, (uint32_t)ks * kCodes);
+      const uint32_t tS = tmem + h * 128, tO = tmem + 256 + h * 128;
+      int ks = 0;                                          // stage of the next scores' key tile, and its parity
+      uint32_t kph = 0u;
+      // scores of step i: hi, then lo, 32 head dims each.  A query tile that has no more
+      // steps keeps giving back the stages.
+      auto scores = [&](int i) -> bool {
+        const int g = i & 1;
+        if (g == 0 && !wait_or_abort(&bars->full_k[ks], kph, abort_flag)) return false;
+        if (i < ns) {
+          tc_fence_after();
+          const uint64_t dkj = sdesc_at(dk, (uint32_t)ks * kCodes + (uint32_t)g * (kStep * 128u));
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_f8(tmem + h * 128, sdesc_at(dqh, (uint32_t)(kk >> 2) * kQHalf + (uint32_t)(kk & 3) * 32u),
-                  sdesc_at(dkj, (uint32_t)(kk & 3) * 32u), idS, kk > 0 ? 1u : 0u);
-        umma_commit(&bars->s[h]);
-      };
-      const int ntt[2] = {nt0, nt1};
-      bool ok = (nt0 == 0 || wait_or_abort(&bars->qf[0], 0, abort_flag)) &&
-                (nt1 == 0 || wait_or_abort(&bars->qf[1], 0, abort_flag)) &&
-                wait_or_abort(&bars->full_k[0], 0, abort_flag);
-      if (ok) {
-        tc_fence_after();
-        if (nt0 > 0) issue_s(0, 0);
-        if (nt1 > 0) issue_s(1, 0);
-        umma_commit(&bars->empty_k[0]);
-        int ks = 1;                                        // stage of key tile j + 1, and its parity
-        uint32_t kph = 0u;
-        for (int j = 0; j < nt && ok; ++j) {
-          const int st = j & 1;
-          const uint64_t dvj = sdesc_at(dv, (uint32_t)st * 2 * kVHalf);
-          ok = wait_or_abort(&bars->full_v[st], (uint32_t)(j >> 1) & 1u, abort_flag);
-          bool have_k = false;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (j >= ntt[h]) continue;
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {                  // keys 64 g .. 64 g + 63: as soon as their P is there
-              ok = ok && wait_or_abort(&bars->p[h][g], (uint32_t)j & 1u, abort_flag);
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll
-              for (int kk = 4 * g; kk < 4 * g + 4; ++kk)
-                umma_bf16_ts(tmem + 256 + h * 128, tmem + h * 128 + kk * 8, sdesc_at(dvj, (uint32_t)kk * 2048u), idO,
-                             (j > 0 || kk > 0) ? 1u : 0u);
-            }
-            if (!ok) break;
-            umma_commit(&bars->pv[h]);
-            if (j + 1 < ntt[h]) {
-              if (!have_k) {
-                ok = wait_or_abort(&bars->full_k[ks], kph, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-                have_k = true;
-              }
-              issue_s(h, ks);
-            }
-          }
-          if (!ok) break;
-          umma_commit(&bars->empty_v[st]);
-          if (j + 1 < nt) umma_commit(&bars->empty_k[ks]);
+          for (int kk = 0; kk < 8; ++kk)
+            umma_f8(tS + g * 64, sdesc_at(dq, (uint32_t)(kk >> 2) * kQHalf + (uint32_t)(kk & 3) * 32u),
+                    sdesc_at(dkj, (uint32_t)(kk & 3) * 32u), idS, kk > 0 ? 1u : 0u);
+          umma_commit(&bars->s[h][g]);
+        }
+        if (g == 1) {
+          umma_commit(&bars->empty_k[ks]);
           if (++ks == kKStages) {
             ks = 0;
             kph ^= 1u;
           }
         }
+        return true;
+      };
+      bool ok = (ns == 0 || wait_or_abort(&bars->qf[h], 0, abort_flag)) && scores(0) && scores(1);
+      for (int i = 0; i < 2 * nt && ok; ++i) {
+        const int t = i >> 1, g = i & 1;
+        if (g == 0) ok = wait_or_abort(&bars->full_v[t & 1], (uint32_t)(t >> 1) & 1u, abort_flag);
+        if (i < ns) {
+          ok = ok && wait_or_abort(&bars->p[h][g], (uint32_t)t & 1u, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dvj = sdesc_at(dv, (uint32_t)(t & 1) * 2 * kVHalf + (uint32_t)g * 8192u);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16_ts(tO, tS + g * 64 + kk * 8, sdesc_at(dvj, (uint32_t)kk * 2048u), idO, (i > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&bars->pv[h]);
+        }
+        if (!ok) break;
+        if (g == 1) umma_commit(&bars->empty_v[t & 1]);
+        if (i + 2 < 2 * nt) ok = scores(i + 2);
       }
       // every MMA issued so far has completed before TMEM is freed
-      umma_commit(&bars->drain);
-      mbar_wait(&bars->drain, 0);
+      umma_commit(&bars->drain[h]);
+      mbar_wait(&bars->drain[h], 0);
     }
   } else {
     // ---------------------------------------------------------- softmax + epilogue
@@ -526,14 +560,14 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
     const int qi = r / p.G, hh = r % p.G;
     const int qt = q0 + h * QP;                    // the tile's first row in the sequence
     const int pos = L - nq + qt + qi;
-    const int ntt = h ? nt1 : nt0;
+    const int ns = h ? ns1 : ns0;
     const bool row_out = qi < QP && (qt + qi) < nq;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + h * 128 + lane_off, tO = tmem + 256 + h * 128 + lane_off;
     unsigned char* qs = smem + kOffQ + h * 2 * kQHalf + r * 128;   // the row's two halves
     float rowf = 0.f;                              // scale * log2(e) * the row's power of two
     bool live = true;
-    if (ntt > 0) {
+    if (ns > 0) {
       // this thread's row of Q, in place: bf16 halves -> hi and lo; zeros for rows that are not the sequence's
       live = __all_sync(0xffffffffu, wait_or_abort(&bars->q[h], 0, abort_flag));
       uint4 qv[16];
@@ -551,7 +585,7 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
       const int qe = mx > 0.f && mx < INFINITY ? max(-110, min(110, ilogbf(mx) - 7)) : 0;
       // (an infinite query has no answer: NaN, as its scores would be)
       const float down = mx < INFINITY ? __uint_as_float((uint32_t)(127 - qe) << 23) : NAN;
-      rowf = p.qscale * __uint_as_float((uint32_t)(127 + qe) << 23);
+      rowf = fmaxf(p.qscale * __uint_as_float((uint32_t)(127 + qe) << 23), FLT_MIN);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {                // 16 head dims
         float f[16];
@@ -577,22 +611,25 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
       if (live) mbar_arrive(&bars->qf[h]);
     }
     float m_ref = -INFINITY, lsum = 0.f;
-    for (int j = 0; j < ntt && live; ++j) {
-      const uint32_t ph = (uint32_t)j & 1u;
-      const int k0 = j * kKT;
-      bool ok = wait_or_abort(&bars->scl_full[j & 3], (uint32_t)(j >> 2) & 1u, abort_flag);
-      ok = ok && wait_or_abort(&bars->s[h], ph, abort_flag);
+    for (int j = 0; j < ns && live; ++j) {
+      const int g = j & 1, t = j >> 1;             // step j: half g of key tile t
+      const int k0 = j * kStep;
+      const uint32_t tP = tS + g * 64;
+      bool ok = g == 1 || wait_or_abort(&bars->scl_full[t & 3], (uint32_t)(t >> 2) & 1u, abort_flag);
+      ok = ok && wait_or_abort(&bars->s[h][g], (uint32_t)t & 1u, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) { live = false; break; }
       tc_fence_after();
-      const float4* ks4 = reinterpret_cast<const float4*>(bars->kscl[j & 3]);   // 16 keys' scales each
-      const bool partial = k0 + kKT - 1 > pos;
+      const float4* ks4 = reinterpret_cast<const float4*>(bars->kscl[t & 3]) + 4 * g;   // 16 keys' scales each
+      const bool partial = k0 + kStep - 1 > pos;
       // maximum of the row's scaled scores, 32 keys at a time
       float mx = -INFINITY;
+      uint32_t buf[2][32];
+      tmem_ld32(tP, buf[0]);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t v[32];
-        tmem_ld32(tS + c * 32, v);
+      for (int c = 0; c < 2; ++c) {
+        uint32_t (&v)[32] = buf[c];
         tmem_ld_wait();
+        if (c < 1) tmem_ld32(tP + 32, buf[1]);
         if (partial) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
@@ -637,22 +674,17 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
       uint64_t ls2[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) ls2[i] = f2pack(0.f, 0.f);
-      // P of keys 32 c .. 32 c + 31 into columns 16 c .. 16 c + 15: scores that have been read
+      // P of keys 32 c .. 32 c + 31 into columns 16 c .. 16 c + 15
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t v[32], pw[16];
-        tmem_ld32(tS + c * 32, v);
-        tmem_ld_wait();
-        if (partial) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (k0 + c * 32 + i > pos) v[i] = __float_as_uint(-INFINITY);
-        }
+      for (int c = 0; c < 2; ++c) {
+        uint32_t (&v)[32] = buf[c];
+        uint32_t pw[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const float4 k4 = ks4[2 * c + (i >> 3)];
-          const int g = (i >> 1) & 3;
-          const float f = rowf * (g == 0 ? k4.x : g == 1 ? k4.y : g == 2 ? k4.z : k4.w);
+          const int q = (i >> 1) & 3;
+          // (above 0: a masked score is -inf, and -inf * 0 is NaN)
+          const float f = fmaxf(rowf * (q == 0 ? k4.x : q == 1 ? k4.y : q == 2 ? k4.z : k4.w), FLT_MIN);
           float x0, x1;
           f2unpack(ffma2(f2pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2pack(f, f), nm2), x0, x1);
           const float p0 = ex2_f32(x0), p1 = ex2_f32(x1);
@@ -660,27 +692,28 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
           ls2[i & 3] = fadd2(ls2[i & 3], f2pack(p0, p1));
           pw[i] = *reinterpret_cast<const uint32_t*>(&pk);
         }
-        tmem_st16(tS + c * 16, pw);
-        if (c & 1) {
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(&bars->p[h][c >> 1]);
-        }
+        tmem_st16(tP + c * 16, pw);
       }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&bars->p[h][g]);
       float ls8[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) f2unpack(ls2[i], ls8[2 * i], ls8[2 * i + 1]);
       lsum += ((ls8[0] + ls8[1]) + (ls8[2] + ls8[3])) + ((ls8[4] + ls8[5]) + (ls8[6] + ls8[7]));
     }
 
-    bool have = ntt > 0 && live;
+    bool have = ns > 0 && live;
     if (have) {
-      const bool ok = wait_or_abort(&bars->pv[h], (uint32_t)(ntt - 1) & 1u, abort_flag);
+      // (the last scores were there before the last but one P V: that phase has to pass first)
+      bool ok = ns < 2 || wait_or_abort(&bars->pv[h], (uint32_t)(ns - 2) & 1u, abort_flag);
+      ok = ok && wait_or_abort(&bars->pv[h], (uint32_t)(ns - 1) & 1u, abort_flag);
       have = __all_sync(0xffffffffu, ok);
       tc_fence_after();
     }
     const float inv = lsum != 0.f ? 1.f / lsum : 0.f;
-    const bool full = ntt > 0 && qt + QP <= nq;
+    const bool full = ns > 0 && qt + QP <= nq;
+    const bool nan_values = have && *static_cast<volatile int*>(&bars->any_nan);
     unsigned char* orow = static_cast<unsigned char*>(p.out) +
                           (((size_t)qrow0 + qt + qi) * p.Hq + (size_t)kvh * p.G + hh) * 256;
 #pragma unroll
@@ -689,6 +722,11 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
       if (have) {
         tmem_ld32(tO + c * 32, v);
         tmem_ld_wait();
+      }
+      if (nan_values) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (*static_cast<volatile int*>(&bars->nan_key[c * 32 + i]) <= pos) v[i] = 0x7fffffffu;
       }
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
@@ -751,7 +789,7 @@ extern "C" int pa_prefill_fp8_blocks(void* out, const void* query, const int32_t
   if (num_seqs < 0 || total_queries < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads ||
       num_blocks <= 0 || max_blocks_per_seq <= 0 || !supported_head_dim(head_dim) ||
       !supported_block_size(block_size) || !(scale > 0.f) ||
-      (long long)max_blocks_per_seq * block_size > 0x7fffffffll)
+      (long long)max_blocks_per_seq * block_size > kMaxRowTokens)
     return PA_ERR_SHAPE;
   const long long groups = ((long long)num_heads + kRowWarps - 1) / kRowWarps;
   if (groups > 65535) return PA_ERR_SHAPE;
