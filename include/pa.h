@@ -307,10 +307,13 @@ int pa_decode_fp8(void* out, const void* query,
  *
  * A dequantised element is e4m3_value(code) * scale.  The calls below write
  * powers of two; pa_decode_fp8_blocks, pa_decode_weights and
- * pa_prefill_fp8_blocks read any finite scale >= 0.  Blocks are copied and
+ * pa_prefill_fp8_blocks read any finite scale >= 0 (the last rounds a V scale
+ * to bf16, which a power of two survives).  Blocks are copied and
  * swapped with pa_copy_blocks / pa_swap_blocks on the codes and again, with
  * the same pairs, on (k_scale, v_scale) as fp32 pools of block_size 4,
  * num_kv_heads = PA_SCALE_ROW(num_kv_heads) / 4 and head_dim 1.
+ * A table row of these calls, and of pa_decode_weights over any pool, holds at
+ * most 2^30 tokens (PA_ERR_SHAPE above).
  */
 #define PA_SCALE_ROW(num_kv_heads) (((num_kv_heads) + 3) / 4 * 4)
 
@@ -367,9 +370,11 @@ int pa_append_fp8_blocks(const void* key, const void* value,
  *   other arguments as for pa_decode
  *
  * With block_size 8 to 32 and num_kv_heads * head_dim a multiple of 128 it runs
- * on the tcgen05 tensor cores, the codes as they are (e4m3 products, fp32 accumulation): Q and the softmax weights
- * enter as two e4m3 terms each, which carry bf16's 8 significant bits.  Everything
- * else runs on CUDA cores in fp32.
+ * on the tcgen05 tensor cores, the codes as they are (e4m3 products, fp32
+ * accumulation): Q, and the products of softmax weight and V scale, enter as two
+ * e4m3 terms each, which carry bf16's 8 significant bits for products down to
+ * 2^-11 of the head's largest and 2^-19 of that largest below.  Everything else
+ * runs on CUDA cores in fp32.
  */
 int pa_decode_fp8_blocks(void* out, const void* query,
                          const void* k_cache, const void* v_cache,
@@ -399,6 +404,9 @@ int pa_decode_fp8_blocks_partition_size(int num_seqs, int num_heads, int num_kv_
  *                  (a bad pair sets PA_DEV_BAD_LEN, and that sequence writes
  *                  nothing)
  *   scale          > 0
+ *
+ * A NaN value makes NaN of its head dim in the rows at and past its token, a NaN
+ * key of those rows whole; the rows before are not touched by either.
  */
 int pa_prefill_fp8_blocks(void* out, const void* query, const int32_t* query_start, int total_queries,
                           const void* k_cache, const void* v_cache,

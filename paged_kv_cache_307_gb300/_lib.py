@@ -321,6 +321,13 @@ def _on(stream, device):
     return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
 
 
+def _on_stream(workspace, stream):
+    """A workspace of the call's own, kept from other uses until `stream` is through with it."""
+    if stream is not None:
+        workspace.record_stream(stream)
+    return workspace
+
+
 def _ready(*ts):
     """The current device, which every tensor has to be on (the library launches there), contiguous."""
     for t in ts:
@@ -435,7 +442,7 @@ def decode_fp8_blocks(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, 
         raise ValueError("one query row per sequence")
     kind = _kind(q)
     if workspace is None:
-        workspace = alloc_fp8_blocks_workspace(q, k_cache, block_tables, partition_size)
+        workspace = _on_stream(alloc_fp8_blocks_workspace(q, k_cache, block_tables, partition_size), stream)
     dev = _ready(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, workspace)
     _check(lib.pa_decode_fp8_blocks(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                                     k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(), cols,
@@ -485,7 +492,7 @@ def decode_weights(out, weights, q, k_cache, v_cache, block_tables, context_lens
     if weights.dtype is not torch.float32 or len(wshape) != 3 or wshape[0] != B or wshape[1] != Hkv:
         raise ValueError("weights is float32 [num_seqs, num_kv_heads, slots]")
     if workspace is None:
-        workspace = alloc_weights_workspace(q, k_cache, block_tables, partition_size)
+        workspace = _on_stream(alloc_weights_workspace(q, k_cache, block_tables, partition_size), stream)
     ks = vs = None
     if kv == PA_FP8_E4M3:
         _ready(k_scale, v_scale)
@@ -523,7 +530,7 @@ def evict(k_cache, v_cache, block_tables, context_lens, kept_lens, seen_lens, we
             token_pos.shape == shape and weights_out.shape == shape and token_pos_out.shape == shape):
         raise ValueError("weights and token_pos are [num_seqs, num_kv_heads, slots], in and out alike")
     if workspace is None:
-        workspace = alloc_evict_workspace(k_cache, block_tables, budget)
+        workspace = _on_stream(alloc_evict_workspace(k_cache, block_tables, budget), stream)
     ks = vs = None
     if kv == PA_FP8_E4M3:
         _ready(k_scale, v_scale)

@@ -29,7 +29,7 @@ bool good_sizes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int
                 int partition_size) {
   return num_seqs >= 0 && num_heads > 0 && num_kv_heads > 0 && num_heads % num_kv_heads == 0 &&
          supported_head_dim(head_dim) && supported_block_size(block_size) && max_blocks > 0 &&
-         (long long)max_blocks * block_size <= 0x7fffffffll &&
+         (long long)max_blocks * block_size <= kMaxRowTokens &&
          !(partition_size > 0 && partition_size % block_size) && (long long)num_seqs * num_heads <= 0x7fffffffll;
 }
 

@@ -1628,8 +1628,9 @@ __device__ __forceinline__ void merge_row_wide(const DecodeParams& p, int bh) {
   const int Lmax = p.max_blocks * p.bs;
   L = L < 0 ? 0 : min(L, Lmax);
   const int nparts = L > 0 ? (L + p.part_tokens - 1) / p.part_tokens : 1;
-  if (nparts <= 1) return;
+  // every CTA waits, those without work too: this grid's end then is that of the one before it
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (nparts <= 1) return;
   const int warp = NW == 1 ? 0 : threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float* ml = p.ws_ml + (size_t)bh * p.max_parts * 2;
   const float* po = p.ws_o + (size_t)bh * p.max_parts * D + lane * VPL;
@@ -1738,10 +1739,10 @@ weights_kernel(const DecodeParams p, float* weights, long long wstride, unsigned
   const int g = (int)(u % p.Hkv), b = (int)(u / p.Hkv);
   int L = __ldg(&p.context_lens[b]);
   L = L < 0 ? 0 : min(L, Lmax);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (t0 >= L) return;
   const int nparts = (L + p.part_tokens - 1) / p.part_tokens;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const size_t row0 = (size_t)b * p.Hq + (size_t)g * p.G;
   const float* sp = p.ws_s + row0 * Lmax;
   float* wp = weights + ((size_t)b * p.Hkv + g) * wstride;

@@ -19,10 +19,11 @@
 // with 2^e per head so that max |q 2^-e| is in [128, 256).  The residual of hi
 // has at most 4 significant bits left, so the split is exact while
 // |q 2^-e| >= 2^-6, and off by at most 2^-14 (2^-21 of the largest) below.  P
-// likewise, 32 p (v / vref) in place of q 2^-e: 8 bits for weights down to
-// 2^-11 of the largest, an absolute 2^-19 of it below.  p is in [0, 8] relative
-// to the running reference, v / vref <= 1 is the V scale of the token's block
-// against the largest so far.  The K scale multiplies the score in fp32.
+// likewise: a token enters O with 32 2^(z - w), z = score + log2 of its block's V
+// scale, w the head's running reference for z; so 8 bits for products of weight
+// and V scale down to 2^-11 of the head's largest, an absolute 2^-19 of it below,
+// however far the blocks' scales are apart.  The sum of the softmax has a reference m
+// of its own (a block may have the scale 0); the K scale multiplies the score in fp32.
 //
 // head_dim 64 and 32 (HP = 2 and 4): HP neighbouring KV heads make one row of 128
 // codes, so the pool is read as one of Hkv / HP heads of 128.  The query heads of
@@ -35,10 +36,10 @@
 //    stage frees with its S, V's with its O.
 //  * warp 5: TMEM, and the MMAs: S_{j+1} before O += V_j P_j.
 //  * warps 0-3: one thread per token: scores from TMEM, scale, mask, p = 2^(s-m),
-//    the sum, P's two terms as bytes into the B tile.  The references (m per
-//    head, vref) are common to the 128 threads and move only when a score
-//    exceeds m by 3 (a factor 8) or a V scale exceeds vref: one barrier with a
-//    vote per tile; then O is rescaled in TMEM.
+//    the sum, P's two terms as bytes into the B tile.  The references (m and w of
+//    every head) are common to the 128 threads and move only when a score or a z
+//    exceeds its own by 3 (a factor 8): one barrier with a vote per tile; then O is
+//    rescaled in TMEM.
 //  * 74 KB of shared memory for up to 8 heads: three CTAs per SM, so one CTA's
 //    softmax and its start and end overlap the others' copies.
 //  * V rows past the context are zeroed in shared memory (0 * NaN).  Waits are
@@ -57,16 +58,16 @@ namespace {
 constexpr int kTcTile = 128;               // tokens per tile
 constexpr uint32_t kTcStage = 16384;       // 128 tokens x 128 codes
 constexpr float kTcSlack = 3.f;            // log2 units a score may exceed the reference by
-constexpr float kTcPScale = 32.f;          // p in [0, 8] -> [0, 256]
+constexpr float kTcPShift = 5.f;           // log2 of what P is scaled by: [0, 8] -> [0, 256]
 
 struct TcShared {
   uint64_t full_k[2], full_v[2], empty_k[2], empty_v[2], s[2], p[2], pv[2], scl_full[4], qf, drain;
-  // scales (K, V) of the 128 / bs blocks of tile j, HP heads each, in slot j & 3:
+  // scales (K's, log2 of V's) of the 128 / bs blocks of tile j, HP heads each, in slot j & 3:
   // tile j+2's and j+3's may be written while the softmax works on j, j+4's only
   // after P_j
   alignas(16) float scl[4][2][64];
   alignas(16) float mx[4][16];             // per warp: tile maximum of every head; at the end, sums
-  float vmx[4][4];
+  alignas(16) float wx[4][16];             // likewise of z
   uint32_t tmem_base;
   int abort;
 };
@@ -263,7 +264,7 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
 #pragma unroll
       for (int i = 0; i < HP; ++i) {
         x.k[i] = __ldg(&p.k_scale[(size_t)id * p.scale_row + rowh * HP + i]);
-        x.v[i] = __ldg(&p.v_scale[(size_t)id * p.scale_row + rowh * HP + i]);
+        x.v[i] = __ldg(&p.v_scale[(size_t)id * p.scale_row + rowh * HP + i]);   // (its log2 when it is used)
       }
       return x;
     };
@@ -296,7 +297,7 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
 #pragma unroll
         for (int i = 0; i < HP; ++i) {
           sh->scl[j & 3][0][lane * HP + i] = sc.k[i];
-          sh->scl[j & 3][1][lane * HP + i] = sc.v[i];
+          sh->scl[j & 3][1][lane * HP + i] = log2f(sc.v[i]);
         }
       }
       __syncwarp();
@@ -384,18 +385,14 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       mbar_arrive(&sh->qf);
       named_sync(1, 128);                        // mx is written again below
     }
-    float m[GT], l[GT];
-#pragma unroll
-    for (int h = 0; h < GT; ++h) {
-      m[h] = -INFINITY;
-      l[h] = 0.f;
-    }
-    float vref[HP];                              // 0: none yet
+    float m[GT], l[GT], w[GT];
     int kvi[GT];
 #pragma unroll
-    for (int i = 0; i < HP; ++i) vref[i] = 0.f;
-#pragma unroll
-    for (int h = 0; h < GT; ++h) kvi[h] = kv_of(h);
+    for (int h = 0; h < GT; ++h) {
+      m[h] = w[h] = -INFINITY;
+      l[h] = 0.f;
+      kvi[h] = kv_of(h);
+    }
     // x[kv] for a head's kv without indexing registers
     auto pick = [&](const float (&x)[HP], int kv) -> float {
       float y = x[0];
@@ -410,11 +407,11 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       const int t = t0 + j * kTcTile + r;
       const bool ok = t < t1;
       tc_wait(&sh->scl_full[j & 3], (uint32_t)(j >> 2) & 1u, abort_flag);
-      float ks[HP], vs[HP];
+      float ks[HP], lv[HP];
 #pragma unroll
       for (int i = 0; i < HP; ++i) {
         ks[i] = sh->scl[j & 3][0][(r >> bsh) * HP + i];
-        vs[i] = ok ? sh->scl[j & 3][1][(r >> bsh) * HP + i] : 0.f;
+        lv[i] = ok ? sh->scl[j & 3][1][(r >> bsh) * HP + i] : -INFINITY;
       }
       __syncwarp();
       tc_wait(&sh->s[st], ph, abort_flag);
@@ -463,39 +460,29 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       }
       bool need = false;
 #pragma unroll
-      for (int i = 0; i < HP; ++i) need = need || vs[i] > vref[i];
-#pragma unroll
-      for (int h = 0; h < GT; ++h) need = need || s[h] > m[h] + kTcSlack;
+      for (int h = 0; h < GT; ++h) need = need || s[h] > m[h] + kTcSlack || s[h] + pick(lv, kvi[h]) > w[h] + kTcSlack;
       __syncwarp();
       if (vote128(need)) {
         // new references: the tile's maxima where they are above
 #pragma unroll
         for (int h = 0; h < GT; ++h) {
-          const float x = warp_max(s[h]);
-          if (lane == 0) sh->mx[warp][h] = x;
-        }
-#pragma unroll
-        for (int i = 0; i < HP; ++i) {
-          const float x = warp_max(vs[i]);
-          if (lane == 0) sh->vmx[warp][i] = x;
+          const float x = warp_max(s[h]), y = warp_max(s[h] + pick(lv, kvi[h]));
+          if (lane == 0) {
+            sh->mx[warp][h] = x;
+            sh->wx[warp][h] = y;
+          }
         }
         named_sync(1, 128);
-        float fv[HP];
-#pragma unroll
-        for (int i = 0; i < HP; ++i) {
-          const float vnew = fmaxf(vref[i], fmaxf(fmaxf(sh->vmx[0][i], sh->vmx[1][i]), fmaxf(sh->vmx[2][i], sh->vmx[3][i])));
-          fv[i] = vref[i] > 0.f ? vref[i] / vnew : 0.f;
-          vref[i] = vnew;
-        }
         float f[GT];
 #pragma unroll
         for (int h = 0; h < GT; ++h) {
           const float x = fmaxf(fmaxf(sh->mx[0][h], sh->mx[1][h]), fmaxf(sh->mx[2][h], sh->mx[3][h]));
-          const float mn = fmaxf(m[h], x);
-          const float a = m[h] == -INFINITY ? 0.f : exp2f(m[h] - mn);
+          const float y = fmaxf(fmaxf(sh->wx[0][h], sh->wx[1][h]), fmaxf(sh->wx[2][h], sh->wx[3][h]));
+          const float mn = fmaxf(m[h], x), wn = fmaxf(w[h], y);
+          l[h] *= m[h] == -INFINITY ? 0.f : exp2f(m[h] - mn);
+          f[h] = w[h] == -INFINITY ? 0.f : exp2f(w[h] - wn);
           m[h] = mn;
-          l[h] *= a;
-          f[h] = a * pick(fv, kvi[h]);
+          w[h] = wn;
         }
         if (j > 0) {
           // O holds V_{j-1} P_{j-1}: this thread's head dim, every head's two columns
@@ -527,22 +514,18 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
         }
         named_sync(1, 128);                      // mx is free again
       }
-      // P: 32 p v / vref as two e4m3 terms, byte r of rows h and NH + h
-      float vf[HP];
-#pragma unroll
-      for (int i = 0; i < HP; ++i) vf[i] = vref[i] > 0.f ? kTcPScale * (vs[i] / vref[i]) : 0.f;
+      // P: 32 2^(z - w) as two e4m3 terms, byte r of rows h and NH + h
       const uint32_t pb = sbase + kOffP + (uint32_t)st * (N * 128);
+      auto weight = [&](int h) -> float {
+        const float z = s[h] + pick(lv, kvi[h]);
+        return z == -INFINITY ? 0.f : exp2f(z - w[h] + kTcPShift);
+      };
 #pragma unroll
       for (int h = 0; h < GT; h += 2) {
         const bool two = GT > 1;
-        const float p0 = s[h] == -INFINITY ? 0.f : exp2f(s[h] - m[h]);
-        l[h] += p0;
-        float p1 = 0.f;
-        if constexpr (GT > 1) {
-          p1 = s[h + 1] == -INFINITY ? 0.f : exp2f(s[h + 1] - m[h + 1]);
-          l[h + 1] += p1;
-        }
-        const float x0 = p0 * pick(vf, kvi[h]), x1 = GT > 1 ? p1 * pick(vf, kvi[h + (GT > 1)]) : 0.f;
+        l[h] += s[h] == -INFINITY ? 0.f : exp2f(s[h] - m[h]);
+        if constexpr (GT > 1) l[h + 1] += s[h + 1] == -INFINITY ? 0.f : exp2f(s[h + 1] - m[h + 1]);
+        const float x0 = weight(h), x1 = GT > 1 ? weight(h + (GT > 1)) : 0.f;
         const uint32_t hi = e4m3x2(x0, x1);
         float y0, y1;
         from_e4m3x2(hi, y0, y1);
@@ -584,21 +567,19 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       tc_wait(&sh->pv[(nt - 1) & 1], (uint32_t)((nt - 1) >> 1) & 1u, abort_flag);
       __syncwarp();
       tc_fence_after();
-      float up[HP];
-#pragma unroll
-      for (int i = 0; i < HP; ++i) up[i] = vref[i] * (1.f / kTcPScale);
+      auto up = [&](int h) -> float { return w[h] == -INFINITY ? 0.f : exp2f(w[h] - m[h] - kTcPShift); };
       if constexpr (NH == 8) {
         uint32_t v[16];
         tmem_ld16(tO + lane_off, v);
         tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < GT; ++h) o[h] = fmaf(__uint_as_float(v[8 + h]), 0.0625f, __uint_as_float(v[h])) * pick(up, kvi[h]);
+        for (int h = 0; h < GT; ++h) o[h] = fmaf(__uint_as_float(v[8 + h]), 0.0625f, __uint_as_float(v[h])) * up(h);
       } else {
         uint32_t v[32];
         tmem_ld32(tO + lane_off, v);
         tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < GT; ++h) o[h] = fmaf(__uint_as_float(v[16 + h]), 0.0625f, __uint_as_float(v[h])) * pick(up, kvi[h]);
+        for (int h = 0; h < GT; ++h) o[h] = fmaf(__uint_as_float(v[16 + h]), 0.0625f, __uint_as_float(v[h])) * up(h);
       }
     }
 #pragma unroll

@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendParams 
   if (!good_seq(p, b)) return;
   if (n == 0 || i < 0 || hx >= 2 * p.Hkv) return;
   const int j = (L - n) / p.bs + i;             // logical block
-  if (j * p.bs >= L) return;
+  if (j >= (L + p.bs - 1) / p.bs) return;
   const int blk = __ldg(&p.block_tables[(size_t)b * p.max_blocks + j]);
   if ((unsigned)blk >= (unsigned)p.num_blocks) {
     if (hx == 0 && lane == 0) atomicOr(&g_status_fp8_blocks, PA_DEV_BAD_BLOCK);
@@ -193,8 +193,8 @@ extern "C" int pa_append_fp8_blocks(const void* key, const void* value, const in
   if (total_tokens < 0 || num_seqs < 0 || num_blocks <= 0 || num_kv_heads <= 0 || max_blocks_per_seq <= 0 ||
       !supported_head_dim(head_dim) || !supported_block_size(block_size))
     return PA_ERR_SHAPE;
-  if ((long long)max_blocks_per_seq * block_size > 0x7fffffffll ||
-      (long long)total_tokens / block_size + 2ll * num_seqs > 0x7fffffffll)
+  if ((long long)max_blocks_per_seq * block_size > kMaxRowTokens ||
+      (long long)total_tokens / block_size + 2ll * num_seqs > 0x3fffffffll)
     return PA_ERR_SHAPE;
   const long long groups = (2ll * num_kv_heads + kWarps - 1) / kWarps;
   if (groups > 65535) return PA_ERR_SHAPE;

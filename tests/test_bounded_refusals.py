@@ -30,8 +30,8 @@ def _decode(pa, q=FAKE, ks=FAKE, mb=4, B=2, Hq=8, H=2, D=128, bs=16, ps=0, ws=NU
                                        n, dt, NULL)
 
 
-def _prefill(pa, q=FAKE, start=FAKE, T=4, ks=FAKE, B=2, Hq=8, H=2, D=128, bs=16, scale=1.0, dt=1):
-    return pa.lib.pa_prefill_fp8_blocks(FAKE, q, start, T, FAKE, FAKE, ks, FAKE, FAKE, 4, FAKE, B, Hq, H, D, bs, 10,
+def _prefill(pa, q=FAKE, start=FAKE, T=4, ks=FAKE, mb=4, B=2, Hq=8, H=2, D=128, bs=16, scale=1.0, dt=1):
+    return pa.lib.pa_prefill_fp8_blocks(FAKE, q, start, T, FAKE, FAKE, ks, FAKE, FAKE, mb, FAKE, B, Hq, H, D, bs, 10,
                                         scale, dt, NULL)
 
 
@@ -48,7 +48,7 @@ def _evict(pa, k=FAKE, ks=FAKE, mb=4, B=2, budget=32, recent=8, sinks=2, stride=
 
 @pytest.mark.parametrize("kw,code", [
     (dict(D=48), -2), (dict(bs=12), -2), (dict(H=0), -2), (dict(T=-1), -2), (dict(B=-1), -2), (dict(NB=0), -2),
-    (dict(mb=0), -2), (dict(mb=1 << 28, bs=32), -2), (dict(H=1 << 20), -2), (dict(dt=2), -3), (dict(dt=9), -3),
+    (dict(mb=0), -2), (dict(mb=1 << 28, bs=32), -2), (dict(mb=(1 << 25) + 1, bs=32), -2), (dict(H=1 << 20), -2), (dict(dt=2), -3), (dict(dt=9), -3),
     (dict(k_scale=NULL), -1), (dict(key=NULL), -1), (dict(key=ODD), -4), (dict(k_scale=ODD), -4),
     (dict(T=0, key=NULL), 0), (dict(B=0), 0)])
 def test_append(pa, kw, code):
@@ -56,7 +56,7 @@ def test_append(pa, kw, code):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(dt=0), -3), (dict(dt=2), -3), (dict(D=96), -2), (dict(Hq=7), -2), (dict(bs=64), -2), (dict(ps=24), -2),
+    (dict(dt=0), -3), (dict(dt=2), -3), (dict(D=96), -2), (dict(Hq=7), -2), (dict(bs=64), -2), (dict(ps=24), -2), (dict(mb=(1 << 25) + 1, bs=32), -2),
     (dict(ks=NULL), -1), (dict(q=NULL), -1), (dict(ks=ODD), -4), (dict(q=ODD), -4),
     (dict(mb=64, ps=512), -5), (dict(mb=64, ps=512, ws=FAKE, n=16), -5), (dict(mb=64, ps=512, ws=ODD, n=1 << 30), -4),
     (dict(B=0), 0)])
@@ -65,7 +65,7 @@ def test_decode(pa, kw, code):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(dt=0), -3), (dict(D=96), -2), (dict(Hq=7), -2), (dict(bs=2), -2), (dict(scale=0.0), -2),
+    (dict(dt=0), -3), (dict(D=96), -2), (dict(Hq=7), -2), (dict(bs=2), -2), (dict(scale=0.0), -2), (dict(mb=(1 << 25) + 1, bs=32), -2),
     (dict(scale=float("nan")), -2), (dict(T=-1), -2), (dict(start=NULL), -1), (dict(ks=NULL), -1), (dict(q=ODD), -4),
     (dict(T=0, q=NULL), 0), (dict(B=0), 0)])
 def test_prefill(pa, kw, code):
@@ -73,7 +73,7 @@ def test_prefill(pa, kw, code):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(stride=63), -2), (dict(Hq=2050), -2), (dict(D=40), -2), (dict(dt=0, kv=1), -3), (dict(dt=0, kv=2), -3),
+    (dict(stride=63), -2), (dict(mb=(1 << 25) + 1, bs=32, stride=1 << 40), -2), (dict(Hq=2050), -2), (dict(D=40), -2), (dict(dt=0, kv=1), -3), (dict(dt=0, kv=2), -3),
     (dict(kv=5), -3), (dict(w=NULL), -1), (dict(kv=2, ks=NULL), -1), (dict(kv=2, ks=ODD), -4), (dict(ws=ODD), -4), (dict(ws=NULL), -5),
     (dict(n=100), -5), (dict(B=0), 0)])
 def test_weights(pa, kw, code):

@@ -398,3 +398,16 @@ def test_two_streams_two_workspaces(pa):
     for L, w in ((a, want[0]), (b, want[1])):
         assert all(torch.equal(x, y) for x, y in zip(L.state(), w))
     assert pa.last_error() == 0
+
+
+@pytest.mark.parametrize("pool", ["f32", "bf16", "e4m3"])
+def test_empty_contexts_in_a_long_table(pa, pool):
+    """Nothing to look at: zeros come out and the running totals stay, whatever the partitions."""
+    c = Case(pool, [0, 0, 0], 8, 2, 128, 16, spare_cols=400).cuda()
+    w = torch.full((3, 2, c.tab.shape[1] * 16), 3.0, device="cuda")
+    for partition in (0, 64, -1):
+        out = torch.full_like(c.q, float("nan"))
+        sc = dict(k_scale=c.ks, v_scale=c.vs) if pool == "e4m3" else {}
+        pa.decode_weights(out, w, c.q, c.k, c.v, c.tab, c.lens, c.scale, partition_size=partition, **sc)
+        assert (out == 0).all() and (w == 3.0).all()
+    assert pa.last_error() == 0

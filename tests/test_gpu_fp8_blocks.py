@@ -170,6 +170,46 @@ def test_decode_scales_far_apart_and_zero(pa, Hq, Hkv, D):
     check(out, ref, tol)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,bs", [(8, 2, 128, 16), (16, 1, 128, 8), (4, 2, 64, 16), (8, 4, 32, 32), (4, 2, 128, 4)])
+@pytest.mark.parametrize("first", [True, False])
+def test_decode_looks_at_values_of_small_scale(pa, Hq, Hkv, D, bs, first):
+    """The softmax sits on blocks whose V scale is 2^-24 of the others': their digits are kept.  A token's
+    product of weight and V scale is off by 2^-8 of itself, or by 2^-19 of the head's largest."""
+    L = 420
+    c = Case("e4m3", [L], Hq, Hkv, D, bs, seed=bs, spare_cols=0)
+    mine = np.zeros(L, dtype=bool)
+    mine[:64] = first
+    mine[320:384] = not first
+    blocks = c.tab[0, [j for j in range(-(-L // bs)) if mine[j * bs]]].long()
+    c.vs[blocks] *= 2.0 ** -24
+    G = Hq // Hkv
+    for h in range(Hkv):                             # the group's queries agree, and those blocks' keys with them
+        c.q[0, h * G:(h + 1) * G] = c.q[0, h * G]
+        c.k[blocks, :, h] = (c.q[0, h * G] * 64).clamp(-448, 448).float().to(torch.float8_e4m3fn).view(torch.uint8)
+    c.ks[:] = 2.0 ** -2
+    K, V = c.f64_pools()
+    q = c.q.double().numpy()
+    at = [(int(c.tab[0, t // bs]), t % bs) for t in range(L)]
+    ref, tol = np.zeros(c.q.shape), np.zeros(c.q.shape)
+    for h in range(Hq):
+        k, v = (np.stack([x[b, i, h // G] for b, i in at]) for x in (K, V))
+        vs = np.array([float(c.vs[b, h // G]) for b, _ in at])
+        s = k @ q[0, h] * c.scale
+        p = np.exp(s - s.max())
+        p /= p.sum()
+        assert p[~mine].max() < 2.0 ** -34           # (with their scales they are still the smaller products)
+        ref[0, h] = p @ v
+        ds = np.abs(k * q[0, h]).sum(1).max() * c.scale * ((D + 4) * 2.0 ** -24 + 2.0 ** -20)
+        A = p @ np.abs(v)
+        tol[0, h] = (2.0 ** -9 * np.abs(ref[0, h]) + (2.0 ** -8 + np.expm1(2 * ds) + (L + 64) * 2.0 ** -23) * A +
+                     2.0 ** -19 * (p * vs).max() * np.abs(v / vs[:, None]).sum(0))
+    c.cuda()
+    out = torch.empty_like(c.q)
+    pa.decode_fp8_blocks(out, c.q, c.k, c.v, c.ks, c.vs, c.tab, c.lens, c.scale)
+    assert pa.last_error() == 0
+    check(out, ref, tol)
+
+
 def test_decode_bad_block_and_length(pa):
     c = Case("e4m3", [100, 100, 100], 8, 2, 128, 16).cuda()
     c.lens[1] = 10 ** 6
@@ -251,3 +291,64 @@ def test_prefill_bad_rows(pa, start):
         lo, hi = max(0, start[b]), min(12, start[b + 1])
         owned = set(range(lo, hi)) - {r for g in range(3) if g not in bad for r in range(start[g], start[g + 1])}
         assert all((out[r] == 7.0).all() for r in owned)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,bs", [(8, 2, 128, 16), (4, 4, 128, 8), (8, 4, 64, 16), (4, 2, 128, 4)])
+def test_prefill_nan_reaches_the_rows_that_see_it(pa, Hq, Hkv, D, bs):
+    """A NaN value makes NaN of its dim in the rows at and past it, a NaN key of those rows' whole heads; rows
+    before them, in the same tile of keys or of queries, keep their numbers."""
+    lens, n = [300, 90], [300, 40]
+    c = Case("e4m3", lens, Hq, Hkv, D, bs, seed=5, rows=sum(n))
+    start = _start(n)
+    ref, tol = reference(c, start.numpy())
+    nan = np.zeros(c.q.shape, dtype=bool)
+    G = Hq // Hkv
+    for x, b, t, h, d in ((c.v, 0, 77, 1, 3), (c.v, 0, 200, 1, 3), (c.v, 0, 70, 1, 9), (c.v, 0, 299, 0, D - 1),
+                          (c.v, 1, 60, 0, 0), (c.k, 0, 130, 0, 5), (c.k, 1, 89, 1, 1)):
+        x[int(c.tab[b, t // bs]), t % bs, h, d] = 0xFF if t & 1 else 0x7F
+        row = int(start[b]) + max(0, t - (lens[b] - n[b]))
+        nan[row:int(start[b + 1]), h * G:(h + 1) * G, d if x is c.v else slice(None)] = True
+    c.cuda()
+    out = torch.empty_like(c.q)
+    pa.prefill_fp8_blocks(out, c.q, start.cuda(), c.k, c.v, c.ks, c.vs, c.tab, c.lens, c.scale)
+    assert pa.last_error() == 0
+    assert np.array_equal(out.isnan().cpu().numpy(), nan)
+    check(torch.where(torch.from_numpy(nan).cuda(), torch.zeros_like(out), out), np.where(nan, 0, ref), tol)
+
+
+@pytest.mark.parametrize("power", [-20, -60, -120])
+def test_prefill_small_queries_and_blocks_of_zeros(pa, power):
+    """Scores far below 1 next to masked ones: the causal mask stays a mask."""
+    lens, n = [200, 70], [200, 3]
+    c = Case("e4m3", lens, 8, 2, 128, 16, seed=8, rows=sum(n))
+    c.q *= 2.0 ** power
+    for j in (0, 3, 12):
+        c.ks[c.tab[0, j].long()] = 0.0
+        c.k[c.tab[0, j].long()] = 0
+    c.ks[c.tab[1, :4].long()] = 2.0 ** -100
+    start = _start(n)
+    ref, tol = reference(c, start.numpy())
+    c.cuda()
+    out = torch.empty_like(c.q)
+    pa.prefill_fp8_blocks(out, c.q, start.cuda(), c.k, c.v, c.ks, c.vs, c.tab, c.lens, c.scale)
+    assert pa.last_error() == 0
+    check(out, ref, tol)
+
+
+def test_decode_on_another_stream_keeps_its_own_workspace(pa):
+    """A call that makes its workspace and runs on a stream that is not the current one: what the current stream
+    allocates and writes next is other memory."""
+    c = Case("e4m3", [9000] * 8, 8, 2, 128, 16, seed=2)
+    ref, tol = reference(c)
+    c.cuda()
+    out = torch.empty_like(c.q)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    n = pa.alloc_fp8_blocks_workspace(c.q, c.k, c.tab).numel()
+    assert n > 16
+    for _ in range(20):
+        pa.decode_fp8_blocks(out, c.q, c.k, c.v, c.ks, c.vs, c.tab, c.lens, c.scale, stream=side)
+        torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert pa.last_error() == 0
+    check(out, ref, tol)
