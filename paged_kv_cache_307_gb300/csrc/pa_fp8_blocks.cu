@@ -13,15 +13,21 @@
 // fall below the smallest normal code.  So a block filled token by token holds
 // what one filled at once holds, up to those.
 //
-// One warp per (touched block, head, K|V): the block's new rows of the head,
+// One warp per (touched block, head): the block's new rows of the head, K's and V's,
 // 16 bytes per lane, are read once and stay in registers from the maximum to the
-// codes (eight loads in flight per lane).  Blocks are owned by one warp each, so
+// codes (sixteen loads in flight per lane).  Blocks are owned by one warp each, so
 // nothing is atomic.  Which block a warp works on needs no scan over the
 // sequences: sequence b's units start at
 //   U_b = floor(query_start[b] / bs) + 2 b,
 // and n tokens touch at most floor((n - 1) / bs) + 2 blocks, which never passes
 // U_{b+1}; a search over query_start finds b, and surplus units leave.
-// Bound by HBM: reads elem and writes 1 byte per element.
+// Bound by HBM: reads elem and writes 1 byte per element.  A warp's life is a chain of
+// five latencies (starts, length, block id, rows, and the writes), so what counts is the
+// bytes that an SM's warps have in flight: 8 prompts of 4096 tokens x 8 heads x 128 in
+// bf16 (201 MB in all) take 37.0 us (4.7 TB/s) with K and V in one warp at four CTAs of
+// 128 registers per SM, 41 at three (no bound on registers), 44 at five; with a warp
+// for K and one for V 43, 38 and 45 at three, six and eight.  One token for 64
+// sequences x 32 heads takes 8 us, launch and latencies.
 #include "pa_common.cuh"
 
 namespace pa {
@@ -72,11 +78,11 @@ __device__ __forceinline__ bool good_seq(const AppendParams& p, int b) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(const AppendParams p) {
   using E = Elem<T>;
   constexpr int EPC = E::kPerChunk;
   const int lane = threadIdx.x & 31;
-  const int hx = (int)blockIdx.y * kWarps + (int)(threadIdx.x >> 5);   // (K|V, head)
+  const int h = (int)blockIdx.y * kWarps + (int)(threadIdx.x >> 5);
   const int u = (int)blockIdx.x;
   if (u == 0 && blockIdx.y == 0) {
     // every sequence's arguments are looked at once, whatever units it has
@@ -89,86 +95,93 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendParams 
   const int i = u - (s0 / p.bs + 2 * b);        // the sequence's i-th touched block
   const int n = s1 - s0;
   if (!good_seq(p, b)) return;
-  if (n == 0 || i < 0 || hx >= 2 * p.Hkv) return;
+  if (n == 0 || i < 0 || h >= p.Hkv) return;
   const int j = (L - n) / p.bs + i;             // logical block
   if (j >= (L + p.bs - 1) / p.bs) return;
   const int blk = __ldg(&p.block_tables[(size_t)b * p.max_blocks + j]);
   if ((unsigned)blk >= (unsigned)p.num_blocks) {
-    if (hx == 0 && lane == 0) atomicOr(&g_status_fp8_blocks, PA_DEV_BAD_BLOCK);
+    if (h == 0 && lane == 0) atomicOr(&g_status_fp8_blocks, PA_DEV_BAD_BLOCK);
     return;
   }
-  const int kv = hx >= p.Hkv ? 1 : 0;
-  const int h = hx - kv * p.Hkv;
   const int first = max(L - n - j * p.bs, 0);   // the block's first new slot; earlier ones hold tokens
   const int cnt = min(L - j * p.bs, p.bs) - first;
   const size_t row = (size_t)p.Hkv * p.D;       // elements from token to token, in the source and in the pool
-  const unsigned char* src = static_cast<const unsigned char*>((kv ? p.src[1] : p.src[0])) +
-                             ((size_t)(s0 + j * p.bs + first - (L - n)) * row + (size_t)h * p.D) * sizeof(T);
-  uint8_t* dst = (kv ? p.pool[1] : p.pool[0]) + (size_t)blk * p.bs * row + (size_t)h * p.D;
+  const size_t from = ((size_t)(s0 + j * p.bs + first - (L - n)) * row + (size_t)h * p.D) * sizeof(T);
+  const size_t to = (size_t)blk * p.bs * row + (size_t)h * p.D;
+  const size_t sat = (size_t)blk * p.scale_row + h;
   const int csh = 31 - __clz(p.D / EPC), cpr = 1 << csh;   // 16-byte source chunks per row: 4, 8, 16 or 32
   const int chunks = cnt << csh;
-  auto fetch = [&](int c) {
-    return ld_nc_v4(src + ((size_t)(c >> csh) * row + (size_t)(c & (cpr - 1)) * EPC) * sizeof(T));
+  auto fetch = [&](int kv, int c) {
+    return ld_nc_v4(static_cast<const unsigned char*>(p.src[kv]) + from +
+                    ((size_t)(c >> csh) * row + (size_t)(c & (cpr - 1)) * EPC) * sizeof(T));
   };
-  // the first kHeld chunks per lane stay in registers from the maximum to the
+  // K's and V's first kHeld chunks per lane stay in registers from the maximum to the
   // codes (all of a bf16 block of 16 x 128), the rest is read again
-  uint4 held[kHeld];
+  uint4 held[2][kHeld];
+  float olds[2];
 #pragma unroll
-  for (int k = 0; k < kHeld; ++k)
-    held[k] = lane + 32 * k < chunks ? fetch(lane + 32 * k) : make_uint4(0u, 0u, 0u, 0u);
-  float amax = 0.f;
-  auto top = [&](const uint4& x) {
-    float f[EPC];
-    E::unpack(x, f);
+  for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
-    for (int e = 0; e < EPC; ++e) amax = fabsf(f[e]) <= 3.402823466e38f ? fmaxf(amax, fabsf(f[e])) : amax;
-  };
+    for (int k = 0; k < kHeld; ++k)
+      held[kv][k] = lane + 32 * k < chunks ? fetch(kv, lane + 32 * k) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-  for (int k = 0; k < kHeld; ++k) top(held[k]);
+  for (int kv = 0; kv < 2; ++kv) olds[kv] = first > 0 ? p.scale[kv][sat] : 0.f;
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    float amax = 0.f;
+    auto top = [&](const uint4& x) {
+      float f[EPC];
+      E::unpack(x, f);
+#pragma unroll
+      for (int e = 0; e < EPC; ++e) amax = fabsf(f[e]) <= 3.402823466e38f ? fmaxf(amax, fabsf(f[e])) : amax;
+    };
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) top(held[kv][k]);
 #pragma unroll 4
-  for (int c = lane + 32 * kHeld; c < chunks; c += 32) top(fetch(c));
+    for (int c = lane + 32 * kHeld; c < chunks; c += 32) top(fetch(kv, c));
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-  float* sp = (kv ? p.scale[1] : p.scale[0]) + (size_t)blk * p.scale_row + h;
-  const float old = first > 0 ? *sp : 0.f;
-  const float s = fmaxf(old, pow2_scale(amax));
-  const float inv = s > 0.f ? 1.f / s : 0.f;    // exact: s is a power of two
-  __syncwarp();
-  if (lane == 0 && (first == 0 || s != old)) *sp = s;
-  if (first > 0 && s > old) {
-    // the earlier tokens' codes under the raised scale, 16 codes per lane
-    const float f = old * inv;
-    const int c16 = p.D / 16;
-    for (int c = lane; c < first * c16; c += 32) {
-      uint8_t* at = dst + (size_t)(c / c16) * row + (size_t)(c % c16) * 16;
-      float v[16];
-      Elem<fp8e4m3>::unpack(*reinterpret_cast<const uint4*>(at), v);
+    for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    const float old = olds[kv];
+    const float s = fmaxf(old, pow2_scale(amax));
+    const float inv = s > 0.f ? 1.f / s : 0.f;    // exact: s is a power of two
+    __syncwarp();
+    if (lane == 0 && (first == 0 || s != old)) p.scale[kv][sat] = s;
+    uint8_t* dst = p.pool[kv] + to;
+    if (first > 0 && s > old) {
+      // the earlier tokens' codes under the raised scale, 16 codes per lane
+      const float f = old * inv;
+      const int c16 = p.D / 16;
+      for (int c = lane; c < first * c16; c += 32) {
+        uint8_t* at = dst + (size_t)(c / c16) * row + (size_t)(c % c16) * 16;
+        float v[16];
+        Elem<fp8e4m3>::unpack(*reinterpret_cast<const uint4*>(at), v);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] *= f;
-      st_v4(at, make_uint4(encode4(v[0], v[1], v[2], v[3]), encode4(v[4], v[5], v[6], v[7]),
-                           encode4(v[8], v[9], v[10], v[11]), encode4(v[12], v[13], v[14], v[15])));
+        for (int e = 0; e < 16; ++e) v[e] *= f;
+        st_v4(at, make_uint4(encode4(v[0], v[1], v[2], v[3]), encode4(v[4], v[5], v[6], v[7]),
+                             encode4(v[8], v[9], v[10], v[11]), encode4(v[12], v[13], v[14], v[15])));
+      }
     }
+    dst += (size_t)first * row;
+    auto put = [&](int c, const uint4& x) {
+      float f[EPC];
+      E::unpack(x, f);
+      uint32_t w[EPC / 4];
+#pragma unroll
+      for (int k = 0; k < EPC / 4; ++k)
+        w[k] = encode4(f[4 * k] * inv, f[4 * k + 1] * inv, f[4 * k + 2] * inv, f[4 * k + 3] * inv);
+      uint8_t* at = dst + (size_t)(c >> csh) * row + (size_t)(c & (cpr - 1)) * EPC;
+      if constexpr (EPC == 8) {
+        *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+      } else {
+        *reinterpret_cast<uint32_t*>(at) = w[0];
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (lane + 32 * k < chunks) put(lane + 32 * k, held[kv][k]);
+#pragma unroll 4
+    for (int c = lane + 32 * kHeld; c < chunks; c += 32) put(c, fetch(kv, c));
   }
-  dst += (size_t)first * row;
-  auto put = [&](int c, const uint4& x) {
-    float f[EPC];
-    E::unpack(x, f);
-    uint32_t w[EPC / 4];
-#pragma unroll
-    for (int k = 0; k < EPC / 4; ++k)
-      w[k] = encode4(f[4 * k] * inv, f[4 * k + 1] * inv, f[4 * k + 2] * inv, f[4 * k + 3] * inv);
-    uint8_t* at = dst + (size_t)(c >> csh) * row + (size_t)(c & (cpr - 1)) * EPC;
-    if constexpr (EPC == 8) {
-      *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
-    } else {
-      *reinterpret_cast<uint32_t*>(at) = w[0];
-    }
-  };
-#pragma unroll
-  for (int k = 0; k < kHeld; ++k)
-    if (lane + 32 * k < chunks) put(lane + 32 * k, held[k]);
-#pragma unroll 4
-  for (int c = lane + 32 * kHeld; c < chunks; c += 32) put(c, fetch(c));
 }
 
 }  // namespace
@@ -196,7 +209,7 @@ extern "C" int pa_append_fp8_blocks(const void* key, const void* value, const in
   if ((long long)max_blocks_per_seq * block_size > kMaxRowTokens ||
       (long long)total_tokens / block_size + 2ll * num_seqs > 0x3fffffffll)
     return PA_ERR_SHAPE;
-  const long long groups = (2ll * num_kv_heads + kWarps - 1) / kWarps;
+  const long long groups = ((long long)num_kv_heads + kWarps - 1) / kWarps;
   if (groups > 65535) return PA_ERR_SHAPE;
   if (total_tokens == 0 || num_seqs == 0) return PA_OK;
   if (!key || !value || !query_start || !block_tables || !context_lens || !k_cache || !v_cache || !k_scale || !v_scale)
