@@ -13,6 +13,11 @@
 // rows) and no pipeline's fill: with few and short requests that chain is the call.
 // Lane groups and warps are merged by log-sum-exp at the end.
 // Arithmetic is fp32 throughout.
+// 5 requests x 4 KV heads of head_dim 64 (f32, groups of 3) of up to 700 tokens take
+// 10 us on the GPU with their weights, 41 through the TMA ring of decode_kernel, whose
+// fill such contexts never repay; 32 x 8 heads of 128 over U[128, 4096]: bf16 in
+// groups of 7 163 us against 140, so at large batches the ring is 15 % ahead: what is
+// bound there is the issue of the CUDA-core products.
 #pragma once
 
 #include "pa_decode_kernel.cuh"

@@ -23,11 +23,13 @@
 // U_{b+1}; a search over query_start finds b, and surplus units leave.
 // Bound by HBM: reads elem and writes 1 byte per element.  A warp's life is a chain of
 // five latencies (starts, length, block id, rows, and the writes), so what counts is the
-// bytes that an SM's warps have in flight: 8 prompts of 4096 tokens x 8 heads x 128 in
-// bf16 (201 MB in all) take 37.0 us (4.7 TB/s) with K and V in one warp at four CTAs of
-// 128 registers per SM, 41 at three (no bound on registers), 44 at five; with a warp
-// for K and one for V 43, 38 and 45 at three, six and eight.  One token for 64
-// sequences x 32 heads takes 8 us, launch and latencies.
+// bytes that an SM's warps have in flight, then the instructions per element: 8 prompts
+// of 3000 to 4096 tokens x 8 heads x 128 in bf16 (174 MB in all) take 34.8 us (5.0 TB/s,
+// 74 % of the copy rate) with K and V in one warp at four CTAs of 128 registers per SM
+// and 41 at five; 37.0 with the maximum taken over floats and not over their bits, and
+// so 41 and 44 at three and five CTAs, and with a warp for K and one for V 43, 38 and 45
+// at three, six and eight.  One token for 64 sequences x 32 heads takes 7 us on the GPU,
+// launch and latencies.
 #include "pa_common.cuh"
 
 namespace pa {
@@ -49,6 +51,49 @@ __device__ __forceinline__ float pow2_scale(float a) {
   const int k = e - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
   return k < -100 ? kMinScale : __uint_as_float((uint32_t)(k + 127) << 23);
 }
+
+// Magnitudes of 16 bytes of elements as integers, ordered like the values.
+template <typename T> struct Magnitude;
+template <> struct Magnitude<__nv_bfloat16> {
+  static constexpr uint32_t kInf = 0x7f80u;
+  __device__ __forceinline__ static uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  // the running maxima of the even and the odd elements, with those of x
+  __device__ __forceinline__ static uint32_t top(const uint4& x, uint32_t m) {
+    constexpr uint32_t kAbs = 0x7fff7fffu;
+    return max2(max2(max2(m, x.x & kAbs), max2(x.y & kAbs, x.z & kAbs)), x.w & kAbs);
+  }
+  __device__ __forceinline__ static uint32_t one(uint32_t m) { return max(m & 0xffffu, m >> 16); }
+  __device__ __forceinline__ static uint32_t finite_top(const uint4& x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t m = 0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t a = w[k] & 0x7fffu, b = (w[k] >> 16) & 0x7fffu;
+      m = max(m, max(a < kInf ? a : 0u, b < kInf ? b : 0u));
+    }
+    return m;
+  }
+  __device__ __forceinline__ static float value(uint32_t m) { return __uint_as_float(m << 16); }
+};
+template <> struct Magnitude<float> {
+  static constexpr uint32_t kInf = 0x7f800000u, kAbs = 0x7fffffffu;
+  __device__ __forceinline__ static uint32_t top(const uint4& x, uint32_t m) {
+    return max(max(max(m, x.x & kAbs), max(x.y & kAbs, x.z & kAbs)), x.w & kAbs);
+  }
+  __device__ __forceinline__ static uint32_t one(uint32_t m) { return m; }
+  __device__ __forceinline__ static uint32_t finite_top(const uint4& x) {
+    const uint32_t w[4] = {x.x & kAbs, x.y & kAbs, x.z & kAbs, x.w & kAbs};
+    uint32_t m = 0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m = max(m, w[k] < kInf ? w[k] : 0u);
+    return m;
+  }
+  __device__ __forceinline__ static float value(uint32_t m) { return __uint_as_float(m); }
+};
 
 // Two conversions of two values each, the first value in the low byte.
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
@@ -80,6 +125,7 @@ __device__ __forceinline__ bool good_seq(const AppendParams& p, int b) {
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(const AppendParams p) {
   using E = Elem<T>;
+  using M = Magnitude<T>;
   constexpr int EPC = E::kPerChunk;
   const int lane = threadIdx.x & 31;
   const int h = (int)blockIdx.y * kWarps + (int)(threadIdx.x >> 5);
@@ -128,19 +174,20 @@ __global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(const AppendPara
   for (int kv = 0; kv < 2; ++kv) olds[kv] = first > 0 ? p.scale[kv][sat] : 0.f;
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
-    float amax = 0.f;
-    auto top = [&](const uint4& x) {
-      float f[EPC];
-      E::unpack(x, f);
+    // the largest magnitude, by its bits; elements that are not finite are above all others
+    // and leave the maximum to a second look at the finite ones
+    uint32_t top = 0u;
 #pragma unroll
-      for (int e = 0; e < EPC; ++e) amax = fabsf(f[e]) <= 3.402823466e38f ? fmaxf(amax, fabsf(f[e])) : amax;
-    };
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) top(held[kv][k]);
+    for (int k = 0; k < kHeld; ++k) top = M::top(held[kv][k], top);
 #pragma unroll 4
-    for (int c = lane + 32 * kHeld; c < chunks; c += 32) top(fetch(kv, c));
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    for (int c = lane + 32 * kHeld; c < chunks; c += 32) top = M::top(fetch(kv, c), top);
+    top = __reduce_max_sync(0xffffffffu, M::one(top));
+    if (top >= M::kInf) {
+      top = 0u;
+      for (int c = lane; c < chunks; c += 32) top = max(top, M::finite_top(fetch(kv, c)));
+      top = __reduce_max_sync(0xffffffffu, top);
+    }
+    const float amax = M::value(top);
     const float old = olds[kv];
     const float s = fmaxf(old, pow2_scale(amax));
     const float inv = s > 0.f ? 1.f / s : 0.f;    // exact: s is a power of two
