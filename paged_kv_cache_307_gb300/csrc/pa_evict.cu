@@ -29,6 +29,8 @@
 // One warp owns a destination block's head, so nothing is atomic.
 // Bound by latency and HBM: 8 bytes read per token and head, 8 written per slot,
 // and the moved rows.
+#include <limits.h>
+
 #include "pa_common.cuh"
 
 namespace pa {
@@ -100,36 +102,48 @@ __device__ __forceinline__ void sync_all() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
   }
 }
-// Exclusive sum of x (the same in every lane of a warp) over the warps of the
-// cluster, and the total.  buf [NW + 1] is used once.
+// Exclusive sums of x and y (the same in every lane of a warp) over the warps of the
+// cluster, and x's total.  buf [2][NW + 1] is used once.
 template <int NW, int CS>
-__device__ __forceinline__ int scan_warps(int x, int* buf, int rank, int& total) {
+__device__ __forceinline__ void scan_warps(int& x, int& y, int (*buf)[NW + 1], int rank, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (lane == 0) buf[warp] = x;
-  __syncthreads();
-  int v = lane < NW ? buf[lane] : 0;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, v, off);
-    if (lane >= off) v += y;
+  if (lane == 0) {
+    buf[0][warp] = x;
+    buf[1][warp] = y;
   }
-  int before = __shfl_up_sync(0xffffffffu, v, 1);      // lane w: the warps before w
-  if (lane == 0) before = 0;
-  before = __shfl_sync(0xffffffffu, before, warp);
-  total = __shfl_sync(0xffffffffu, v, NW - 1);
+  __syncthreads();
+  int sum[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    int v = lane < NW ? buf[k][lane] : 0;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, off);
+      if (lane >= off) v += u;
+    }
+    int before = __shfl_up_sync(0xffffffffu, v, 1);    // lane w: the warps before w
+    if (lane == 0) before = 0;
+    (k == 0 ? x : y) = __shfl_sync(0xffffffffu, before, warp);
+    sum[k] = __shfl_sync(0xffffffffu, v, NW - 1);
+  }
+  total = sum[0];
   if constexpr (CS > 1) {
-    if (threadIdx.x == 0) buf[NW] = total;
+    if (threadIdx.x == 0) {
+      buf[0][NW] = sum[0];
+      buf[1][NW] = sum[1];
+    }
     sync_all<CS>();
-    int all = 0;
+    total = 0;
 #pragma unroll
     for (int r = 0; r < CS; ++r) {
-      const int n = ld_cluster(&buf[NW], r);
-      if (r < rank) before += n;
-      all += n;
+      const int n0 = ld_cluster(&buf[0][NW], r), n1 = ld_cluster(&buf[1][NW], r);
+      if (r < rank) {
+        x += n0;
+        y += n1;
+      }
+      total += n0;
     }
-    total = all;
   }
-  return before;
 }
 
 // NT threads a CTA, CS CTAs a cluster.  SMEM: the keys are kept in shared memory
@@ -138,8 +152,9 @@ template <int NT, int CS, bool SMEM>
 __global__ void __launch_bounds__(NT) select_kernel(const EvictParams p, int words) {
   constexpr int NW = NT / 32;
   __shared__ int hist[4][kCopies][kBins];
-  __shared__ int wbuf[3][NW + 1];
-  __shared__ int sh_digit, sh_left;
+  __shared__ int all[CS > 1 ? kBins : 1];
+  __shared__ int wbuf[2][2][NW + 1];
+  __shared__ int sh_digit, sh_left, sh_here;
   extern __shared__ uint32_t dyn[];
   asm volatile("griddepcontrol.launch_dependents;");
   const int rank = CS > 1 ? cluster_rank() : 0;
@@ -207,7 +222,8 @@ __global__ void __launch_bounds__(NT) select_kernel(const EvictParams p, int wor
   __syncthreads();
   // ---- the budget-th largest key: 8 bits a pass from the top
   uint32_t prefix = 0, mask = 0;
-  int left = p.budget;                    // how many of the keys that match the prefix are kept
+  int left = p.budget;                    // how many of the keys that match the prefix are kept,
+  int here = 0;                           // and how many match it
 #pragma unroll 1
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
@@ -229,21 +245,30 @@ __global__ void __launch_bounds__(NT) select_kernel(const EvictParams p, int wor
       }
     }
     sync_all<CS>();
+    if constexpr (CS > 1) {
+      // the cluster's bins, a digit per thread
+      if (tid < 256) {
+        int n = 0;
+#pragma unroll
+        for (int r = 0; r < CS; ++r)
+#pragma unroll
+          for (int k = 0; k < kCopies; ++k) n += ld_cluster(&hist[pass][k][tid + (tid >> 3)], r);
+        all[tid + (tid >> 3)] = n;
+      }
+      __syncthreads();
+    }
     if (warp == 0) {
       // lane l holds digits 255-8l .. 248-8l, the largest first: 9 (31 - l) + 7 - i in the padded bins
       int c[8], sum = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        c[i] = 0;
+        const int at = 9 * (31 - lane) + 7 - i;
+        if constexpr (CS > 1) {
+          c[i] = all[at];
+        } else {
+          c[i] = 0;
 #pragma unroll
-        for (int k = 0; k < kCopies; ++k) {
-          const int* bin = &hist[pass][k][9 * (31 - lane) + 7 - i];
-          if constexpr (CS == 1) {
-            c[i] += *bin;
-          } else {
-#pragma unroll
-            for (int r = 0; r < CS; ++r) c[i] += ld_cluster(bin, r);
-          }
+          for (int k = 0; k < kCopies; ++k) c[i] += hist[pass][k][at];
         }
         sum += c[i];
       }
@@ -259,6 +284,7 @@ __global__ void __launch_bounds__(NT) select_kernel(const EvictParams p, int wor
         if (before < left && left <= before + c[i]) {     // in exactly one lane
           sh_digit = 255 - 8 * lane - i;
           sh_left = left - before;
+          sh_here = c[i];
         }
         before += c[i];
       }
@@ -266,6 +292,7 @@ __global__ void __launch_bounds__(NT) select_kernel(const EvictParams p, int wor
     __syncthreads();
     prefix |= (uint32_t)sh_digit << shift;
     left = sh_left;
+    here = sh_here;
     mask |= 0xffu << shift;
     // (the next write to the pair comes after a barrier)
   }
@@ -275,10 +302,16 @@ __global__ void __launch_bounds__(NT) select_kernel(const EvictParams p, int wor
   const int run = ((n + NT - 1) / NT) * 32;
   const int r0 = min(n, warp * run), r1 = min(n, r0 + run);
   const unsigned lt = (1u << lane) - 1u;
-  int eq = 0, total;
-  for (int i0 = r0; i0 < r1; i0 += 32)
-    eq += __popc(__ballot_sync(0xffffffffu, i0 + lane < r1 && key_of(i0 + lane) == prefix));
-  int ties = scan_warps<NW, CS>(eq, wbuf[0], rank, total);
+  // ties before the run (where all that tie are kept, their order is no matter)
+  int ties = 0, total;
+  if (here != left) {
+    for (int i0 = r0; i0 < r1; i0 += 32)
+      ties += __popc(__ballot_sync(0xffffffffu, i0 + lane < r1 && key_of(i0 + lane) == prefix));
+    int none = 0;
+    scan_warps<NW, CS>(ties, none, wbuf[0], rank, total);
+  } else {
+    left = INT_MAX;
+  }
   // slots of the 32 from base + i0 that are in the run, and those below the budget
   auto in_run = [&](int i0) -> unsigned { return r1 - i0 >= 32 ? 0xffffffffu : (1u << (r1 - i0)) - 1u; };
   auto below = [&](int i0) -> unsigned {
@@ -297,9 +330,9 @@ __global__ void __launch_bounds__(NT) select_kernel(const EvictParams p, int wor
     holes += __popc(in_run(i0) & below(i0) & ~s);
     movers += __popc(s & ~below(i0));
   }
-  int hole0 = scan_warps<NW, CS>(holes, wbuf[1], rank, total);
+  int hole0 = holes, mover0 = movers;
+  scan_warps<NW, CS>(hole0, mover0, wbuf[1], rank, total);
   const int nmove = total;                             // as many movers as holes
-  int mover0 = scan_warps<NW, CS>(movers, wbuf[2], rank, total);
   Move* mv = p.moves + (size_t)bh * p.cap;
   int32_t* dst = p.dst + (size_t)bh * p.cap;
   for (int i0 = r0; i0 < r1; i0 += 32) {
