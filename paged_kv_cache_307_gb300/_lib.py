@@ -303,6 +303,7 @@ def scale_row(num_kv_heads):
     return (num_kv_heads + 3) // 4 * 4
 
 
+_I32, _F32 = torch.int32, torch.float32
 _KIND = {torch.float32: PA_F32, torch.bfloat16: PA_BF16, torch.uint8: PA_FP8_E4M3}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -330,30 +331,28 @@ def _on_stream(workspace, stream):
 
 def _ready(*ts):
     """The current device, which every tensor has to be on (the library launches there), contiguous."""
+    d = torch.cuda.current_device() if ts[0].is_cuda else -2
     for t in ts:
-        if not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
-    if not ts[0].is_cuda:
-        raise ValueError("tensors must be on the current CUDA device")
-    d = torch.cuda.current_device()
-    for t in ts:
-        if t.get_device() != d:
+        if t.get_device() != d or not t.is_contiguous():
+            if not t.is_contiguous():
+                raise ValueError("tensors must be contiguous")
             raise ValueError("tensors must be on the current CUDA device")
     return d
 
 
 def _int32(*ts):
     for t in ts:
-        if t.dtype is not torch.int32:
+        if t.dtype is not _I32:
             raise TypeError("lengths, tables and starts are int32")
 
 
 def _table(block_tables, context_lens):
     """(num_seqs, max_blocks)"""
     _int32(block_tables, context_lens)
-    if block_tables.dim() != 2 or context_lens.dim() != 1 or context_lens.size(0) != block_tables.size(0):
+    shape, lens = block_tables.shape, context_lens.shape
+    if len(shape) != 2 or len(lens) != 1 or lens[0] != shape[0]:
         raise ValueError("block_tables is [num_seqs, max_blocks], context_lens [num_seqs]")
-    return block_tables.size(0), block_tables.size(1)
+    return shape
 
 
 def _pools(k_cache, v_cache, k_scale=None, v_scale=None):
@@ -368,11 +367,11 @@ def _pools(k_cache, v_cache, k_scale=None, v_scale=None):
     else:
         if k_scale is None or v_scale is None:
             raise ValueError("a block-scaled cache needs k_scale and v_scale")
-        if k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32:
+        if k_scale.dtype is not _F32 or v_scale.dtype is not _F32:
             raise TypeError("scales are float32")
         if k_scale.shape != (shape[0], scale_row(shape[2])) or v_scale.shape != k_scale.shape:
             raise ValueError("scales are [num_blocks, num_kv_heads rounded up to a multiple of 4]")
-    return shape[0], shape[1], shape[2], shape[3], kind
+    return *shape, kind
 
 
 def _block_scaled(k_cache, v_cache, k_scale, v_scale):
@@ -489,7 +488,7 @@ def decode_weights(out, weights, q, k_cache, v_cache, block_tables, context_lens
         raise ValueError("one query row per sequence")
     kind = _kind(q)
     wshape = weights.shape
-    if weights.dtype is not torch.float32 or len(wshape) != 3 or wshape[0] != B or wshape[1] != Hkv:
+    if weights.dtype is not _F32 or len(wshape) != 3 or wshape[0] != B or wshape[1] != Hkv:
         raise ValueError("weights is float32 [num_seqs, num_kv_heads, slots]")
     if workspace is None:
         workspace = _on_stream(alloc_weights_workspace(q, k_cache, block_tables, partition_size), stream)
@@ -520,10 +519,10 @@ def evict(k_cache, v_cache, block_tables, context_lens, kept_lens, seen_lens, we
     NB, bs, Hkv, D, kv = _pools(k_cache, v_cache, k_scale, v_scale)
     B, cols = _table(block_tables, context_lens)
     _int32(kept_lens, seen_lens, token_pos, new_lens, token_pos_out)
-    for t in (kept_lens, seen_lens, new_lens):
-        if t.dim() != 1 or t.size(0) != B:
-            raise ValueError("kept_lens, seen_lens and new_lens are [num_seqs]")
-    if weights.dtype is not torch.float32 or weights_out.dtype is not torch.float32:
+    lens = context_lens.shape
+    if kept_lens.shape != lens or seen_lens.shape != lens or new_lens.shape != lens:
+        raise ValueError("kept_lens, seen_lens and new_lens are [num_seqs]")
+    if weights.dtype is not _F32 or weights_out.dtype is not _F32:
         raise TypeError("weights are float32")
     shape = weights.shape
     if len(shape) != 3 or shape[0] != B or shape[1] != Hkv or not (
