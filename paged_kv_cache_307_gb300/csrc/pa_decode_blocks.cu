@@ -36,10 +36,10 @@ bool good_sizes(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int
 // Automatic split: the longest partition that still gives the GPU its CTAs at the
 // table's capacity (the lengths themselves are on the device).
 //  * tcgen05, one CTA per (partition, sequence, row of 128 codes): 2048, 1024 or 512
-//    tokens, two CTAs per SM.  A CTA's start and end weigh about as much as three of
-//    its 128-token tiles: 64 requests x 8 KV heads over U[1024, 16384] take 375, 251,
-//    204 and 194 us at 256, 512, 1024 and 2048 tokens; one request x 8 heads at 32768
-//    tokens 27.1, 25.1, 21.8 and 29.0, eight at up to 8192 32.2, 26.8, 23.8 and 29.8.
+//    tokens, two CTAs per SM.  A CTA's start and end weigh about as much as two of
+//    its 128-token tiles: 64 requests x 8 KV heads over U[1024, 16384] take 258, 204
+//    and 188 us at 512, 1024 and 2048 tokens; one request x 8 heads at 32768 tokens
+//    24.0, 20.7 and 29.2, eight at up to 8192 28.7, 23.8 and 28.6.
 //  * direct, one CTA per (partition, sequence, KV head, 4 query heads): 512 down to
 //    64 tokens, four CTAs per SM: 5 requests x 4 heads of up to 700 tokens (f32)
 //    take 12.5, 14.6, 22.8 and 39.2 us at 64, 128, 256 and 512 tokens; 32 x 8 heads

@@ -6,11 +6,11 @@
 //
 // What bounds decode over 8-bit pools is not the bytes but the instructions
 // that widen every code for 16-bit products (about 36 per token and KV head on
-// the mma.sync path: 281 us where this takes 197).  Here a tile of 128 tokens of
+// the mma.sync path: 281 us where this takes 188).  Here a tile of 128 tokens of
 // one KV head costs eight MMAs, and per token only its scores are touched by threads.
 // Bound by HBM but for the CTAs' starts and ends: 64 requests x 8 KV heads x 128,
-// 32 query heads, over U[1024, 16384] tokens take 192 us (1.14 GB, 5.9 TB/s, 87 % of
-// the copy rate) and 64 x 32 heads over U[128, 2048] 100 us (5.7 TB/s).
+// 32 query heads, over U[1024, 16384] tokens take 188 us (1.14 GB, 6.1 TB/s, 90 % of
+// the copy rate) and 64 x 32 heads over U[128, 2048] 97 us (5.9 TB/s).
 //
 // One CTA = (sequence, partition of P tokens, KV head, up to 16 query heads):
 //   S^T[128 tokens x N] = K[128 x 128] Q^T      A = K tile (K-major), B = Q rows
@@ -35,7 +35,9 @@
 //
 //  * warp 4 (TMA): block-table entries and scales by parallel lanes, K and V
 //    boxes {128 B, 1 head, bs rows} into 2-stage rings of 16 KB tiles; K's
-//    stage frees with its S, V's with its O.
+//    stage frees with its S, V's with its O.  The first two tiles are requested
+//    before the CTA's barrier, as soon as the length and their ids are there (by
+//    the loop, behind their scales, the first request left 2000 clocks later: 196 us).
 //  * warp 5: TMEM, and the MMAs: S_{j+1} before O += V_j P_j.
 //  * warps 0-3: one thread per token: scores from TMEM, scale, mask, p = 2^(s-m),
 //    the sum, P's two terms as bytes into the B tile.  The references (m and w of
@@ -44,7 +46,7 @@
 //    rescaled in TMEM.
 //  * 74 KB of shared memory for up to 8 heads: three CTAs per SM, so one CTA's
 //    softmax and its start and end overlap the others' copies.  (Three stages and
-//    two CTAs: 212 us; one V stage and four CTAs: 270.)
+//    two CTAs took 8 % more, one V stage and four CTAs 41 %.)
 //  * V rows past the context are zeroed in shared memory (0 * NaN).  Waits are
 //    bounded (2 s); after a timeout the softmax warps keep walking the tiles
 //    without waiting, so that their barriers stay matched.
@@ -121,6 +123,7 @@ __device__ __forceinline__ float warp_max(float x) {
   return x;
 }
 __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try_wait(smem_u32(bar), parity)) return true;
   if (*abort_flag) return false;
   if (mbar_wait(bar, parity)) return true;
   atomicOr(&g_status_decode, PA_DEV_TIMEOUT);
@@ -185,10 +188,10 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
   const int t0 = part * p.part_tokens;
   const int bsh = 31 - __clz(p.bs);
   // What does not depend on the context's length is requested with it: the
-  // queries, and the first three tiles' block-table entries (a lane each, inside
+  // queries, and the first five tiles' block-table entries (a lane each, inside
   // the row whatever the length is).
   __nv_bfloat16 qraw[GT];
-  int id[3] = {0, 0, 0};
+  int id[5] = {0, 0, 0, 0, 0};
   if (warp < 4) {
     const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q) + ((size_t)b * p.Hq + h0) * D;
 #pragma unroll
@@ -198,7 +201,7 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
     }
   } else if (warp == 4) {
 #pragma unroll
-    for (int j = 0; j < 3; ++j) {
+    for (int j = 0; j < 5; ++j) {
       const int i = ((t0 + j * kTcTile) >> bsh) + lane;
       if (lane < (kTcTile >> bsh) && i < p.max_blocks) id[j] = __ldg(&p.block_tables[(size_t)b * p.max_blocks + i]);
     }
@@ -211,21 +214,53 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
   const int t1 = min(L, t0 + p.part_tokens);
   const int nt = (t1 - t0 + kTcTile - 1) / kTcTile;
 
-  if (threadIdx.x == 160) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh->full_k[i], 1);
-      mbar_init(&sh->full_v[i], 1);
-      mbar_init(&sh->empty_k[i], 1);
-      mbar_init(&sh->empty_v[i], 1);
-      mbar_init(&sh->s[i], 1);
-      mbar_init(&sh->p[i], 128);
-      mbar_init(&sh->pv[i], 1);
+  // ---- TMA producer, its state and first requests: the ring is empty, so the first two tiles
+  // go out before the CTA has met at its barrier
+  const uint64_t pol = policy_evict_first();
+  const uint32_t box = (uint32_t)p.bs * 128u;
+  auto in_use = [&](int j) -> bool {
+    return j < nt && lane < (kTcTile >> bsh) && t0 + j * kTcTile + (lane << bsh) < t1;
+  };
+  auto boxes_of = [&](int j) -> int { return (min(kTcTile, t1 - t0 - j * kTcTile) + p.bs - 1) >> bsh; };
+  auto checked = [&](int id) -> int {
+    if ((unsigned)id < (unsigned)p.num_blocks) return id;
+    atomicOr(&g_status_decode, PA_DEV_BAD_BLOCK);
+    return 0;                                   // keep every copy inside the pool
+  };
+  auto request = [&](const CUtensorMap& map, uint64_t* full, uint32_t off, int j, int blk) {
+    const int nb = boxes_of(j);
+    if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)nb * box);
+    __syncwarp();
+    if (lane < nb) tma_load_4d(smem + off + (j & 1) * kTcStage + lane * box, &map, full, 0, rowh, 0, blk, pol);
+  };
+  const int first = min(nt, 2);
+  if (warp == 4) {
+    if (lane == 0) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&sh->full_k[i], 1);
+        mbar_init(&sh->full_v[i], 1);
+        mbar_init(&sh->empty_k[i], 1);
+        mbar_init(&sh->empty_v[i], 1);
+        mbar_init(&sh->s[i], 1);
+        mbar_init(&sh->p[i], 128);
+        mbar_init(&sh->pv[i], 1);
+      }
+      for (int i = 0; i < 4; ++i) mbar_init(&sh->scl_full[i], 1);
+      mbar_init(&sh->qf, 128);
+      mbar_init(&sh->drain, 1);
+      sh->abort = 0;
+      fence_mbar_init();
+      fence_proxy_async_smem();
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&sh->scl_full[i], 1);
-    mbar_init(&sh->qf, 128);
-    mbar_init(&sh->drain, 1);
-    sh->abort = 0;
-    fence_mbar_init();
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 2; ++j) id[j] = in_use(j) ? checked(id[j]) : 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (j < first) request(mapK, &sh->full_k[j], 0, j, id[j]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (j < first) request(mapV, &sh->full_v[j], kOffV, j, id[j]);
   }
   __syncwarp();
   if (warp == 5) {
@@ -240,25 +275,11 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
 
   if (warp == 4) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      prefetch_tensormap(&mapK);
-      prefetch_tensormap(&mapV);
-    }
-    const uint64_t pol = policy_evict_first();
     const int32_t* row = p.block_tables + (size_t)b * p.max_blocks;
-    const uint32_t box = (uint32_t)p.bs * 128u;
     // Lane i: block i of a tile (at most 16), its id and scales.  The scales hang
     // on the id and both come from memory: ids are read three tiles ahead and
     // scales two, so that neither latency is waited for (one tile ahead for
     // both held every tile up by two memory latencies, about 4000 clocks).
-    auto in_use = [&](int j) -> bool {
-      return j < nt && lane < (kTcTile >> bsh) && t0 + j * kTcTile + (lane << bsh) < t1;
-    };
-    auto checked = [&](int id) -> int {
-      if ((unsigned)id < (unsigned)p.num_blocks) return id;
-      atomicOr(&g_status_decode, PA_DEV_BAD_BLOCK);
-      return 0;                                 // keep every copy inside the pool
-    };
     struct Scales {
       float k[HP], v[HP];
     };
@@ -271,40 +292,36 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       }
       return x;
     };
-    int blk = in_use(0) ? checked(id[0]) : 0;
-    Scales sc = scales_of(blk);
-    int blk1 = in_use(1) ? checked(id[1]) : 0;
-    Scales sc1 = scales_of(blk1);
-    int blk2 = id[2];
-    int issued_k = 0, issued_v = 0;
-    for (int j = 0; j < nt; ++j) {
-      const int st = j & 1;
-      const uint32_t ph = ((uint32_t)(j >> 1) & 1u) ^ 1u;
-      const int nb = (min(kTcTile, t1 - t0 - j * kTcTile) + p.bs - 1) >> bsh;
-      bool ok = true;
-      if (lane == 0) ok = tc_wait(&sh->empty_k[st], ph, abort_flag);
-      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
-      if (lane == 0) mbar_arrive_expect_tx(&sh->full_k[st], (uint32_t)nb * box);
-      __syncwarp();
-      if (lane < nb)
-        tma_load_4d(smem + st * kTcStage + lane * box, &mapK, &sh->full_k[st], 0, rowh, 0, blk, pol);
-      issued_k = j + 1;
-      if (lane == 0) ok = tc_wait(&sh->empty_v[st], ph, abort_flag);
-      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
-      if (lane == 0) mbar_arrive_expect_tx(&sh->full_v[st], (uint32_t)nb * box);
-      __syncwarp();
-      if (lane < nb)
-        tma_load_4d(smem + kOffV + st * kTcStage + lane * box, &mapV, &sh->full_v[st], 0, rowh, 0, blk, pol);
-      issued_v = j + 1;
+    auto put_scales = [&](int j, const Scales& x) {
       if (lane < 16) {
 #pragma unroll
         for (int i = 0; i < HP; ++i) {
-          sh->scl[j & 3][0][lane * HP + i] = sc.k[i];
-          sh->scl[j & 3][1][lane * HP + i] = log2f(sc.v[i]);
+          sh->scl[j & 3][0][lane * HP + i] = x.k[i];
+          sh->scl[j & 3][1][lane * HP + i] = log2f(x.v[i]);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->scl_full[j & 3]);
+    };
+    const Scales sc_0 = scales_of(id[0]), sc_1 = scales_of(id[1]);
+    int blk = in_use(2) ? checked(id[2]) : 0;
+    Scales sc = scales_of(blk);
+    int blk1 = in_use(3) ? checked(id[3]) : 0;
+    Scales sc1 = scales_of(blk1);
+    int blk2 = id[4];
+    if (first > 0) put_scales(0, sc_0);
+    if (first > 1) put_scales(1, sc_1);
+    int issued_k = first, issued_v = first;
+    for (int j = 2; j < nt; ++j) {
+      const int st = j & 1;
+      const uint32_t ph = ((uint32_t)(j >> 1) & 1u) ^ 1u;
+      if (!__all_sync(0xffffffffu, tc_wait(&sh->empty_k[st], ph, abort_flag))) break;
+      request(mapK, &sh->full_k[st], 0, j, blk);
+      issued_k = j + 1;
+      if (!__all_sync(0xffffffffu, tc_wait(&sh->empty_v[st], ph, abort_flag))) break;
+      request(mapV, &sh->full_v[st], kOffV, j, blk);
+      issued_v = j + 1;
+      put_scales(j, sc);
       blk = blk1;
       sc = sc1;
       blk1 = in_use(j + 2) ? checked(blk2) : 0;
