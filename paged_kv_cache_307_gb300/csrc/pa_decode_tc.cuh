@@ -66,7 +66,7 @@ constexpr float kTcSlack = 3.f;            // log2 units a score may exceed the 
 constexpr float kTcPShift = 5.f;           // log2 of what P is scaled by: [0, 8] -> [0, 256]
 
 struct TcShared {
-  uint64_t full_k[2], full_v[2], empty_k[2], empty_v[2], s[2], p[2], pv[2], scl_full[4], qf, drain;
+  uint64_t full_k[2], full_v[2], empty_k[2], empty_v[2], s[2], p[2], pv[2], scl_full[4], drain;
   // scales (K's, log2 of V's) of the 128 / bs blocks of tile j, HP heads each, in slot j & 3:
   // tile j+2's and j+3's may be written while the softmax works on j, j+4's only
   // after P_j
@@ -118,9 +118,9 @@ __device__ __forceinline__ bool vote128(bool x) {
   return r != 0;
 }
 __device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-  return x;
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
 }
 __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   if (mbar_try_wait(smem_u32(bar), parity)) return true;
@@ -246,7 +246,6 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
         mbar_init(&sh->pv[i], 1);
       }
       for (int i = 0; i < 4; ++i) mbar_init(&sh->scl_full[i], 1);
-      mbar_init(&sh->qf, 128);
       mbar_init(&sh->drain, 1);
       sh->abort = 0;
       fence_mbar_init();
@@ -258,11 +257,36 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
 #pragma unroll
     for (int j = 0; j < 2; ++j)
       if (j < first) request(mapK, &sh->full_k[j], 0, j, id[j]);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (j < first) request(mapV, &sh->full_v[j], kOffV, j, id[j]);
+    if (first > 0) request(mapV, &sh->full_v[0], kOffV, 0, id[0]);
   }
   __syncwarp();
+  float qf[GT];                                  // scale * log2(e) * 2^e of every head
+  if (warp < 4) {
+    // ---- Q: two e4m3 rows per head, while the first tiles are on their way
+    float q[GT];
+#pragma unroll
+    for (int h = 0; h < GT; ++h) {
+      q[h] = __bfloat162float(qraw[h]);
+      const float m = warp_max(fabsf(q[h]));
+      if (lane == 0) sh->mx[warp][h] = m;
+    }
+    named_sync(1, 128);
+#pragma unroll
+    for (int h = 0; h < GT; ++h) {
+      const float m = fmaxf(fmaxf(sh->mx[0][h], sh->mx[1][h]), fmaxf(sh->mx[2][h], sh->mx[3][h]));
+      const int e = m > 0.f && m < INFINITY ? max(-110, min(110, ilogbf(m) - 7)) : 0;
+      // (an infinite query has no answer: NaN, as its scores would be)
+      const float x = m < INFINITY ? q[h] * __uint_as_float((uint32_t)(127 - e) << 23) : NAN;
+      qf[h] = p.qscale * __uint_as_float((uint32_t)(127 + e) << 23);
+      const uint32_t hi = e4m3x2(x, 0.f);
+      float back, none;
+      from_e4m3x2(hi, back, none);
+      const uint32_t lo = e4m3x2((x - back) * 16.f, 0.f);
+      sts_u8(sbase + kOffQ + swz_byte(h, (int)threadIdx.x), hi);
+      sts_u8(sbase + kOffQ + swz_byte(NH + h, (int)threadIdx.x), lo);
+    }
+    fence_proxy_async_smem();
+  }
   if (warp == 5) {
     tmem_alloc(&sh->tmem_base, kTmem);
     tmem_relinquish();
@@ -303,6 +327,7 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->scl_full[j & 3]);
     };
+    if (first > 1) request(mapV, &sh->full_v[1], kOffV, 1, id[1]);
     const Scales sc_0 = scales_of(id[0]), sc_1 = scales_of(id[1]);
     int blk = in_use(2) ? checked(id[2]) : 0;
     Scales sc = scales_of(blk);
@@ -348,7 +373,7 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
         umma_commit(&sh->s[j & 1]);
         umma_commit(&sh->empty_k[j & 1]);
       };
-      if (tc_wait(&sh->qf, 0, abort_flag) && tc_wait(&sh->full_k[0], 0, abort_flag)) {
+      if (tc_wait(&sh->full_k[0], 0, abort_flag)) {
         tc_fence_after();
         issue_s(0);
         for (int j = 0; j < nt; ++j) {
@@ -377,34 +402,6 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
     // ------------------------------------------------------------ softmax
     const int r = (int)threadIdx.x;              // token of the tile, head dim at either end; TMEM lane
     const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-    float qf[GT];                                // scale * log2(e) * 2^e of every head
-    {
-      float q[GT];
-#pragma unroll
-      for (int h = 0; h < GT; ++h) {
-        q[h] = __bfloat162float(qraw[h]);
-        const float m = warp_max(fabsf(q[h]));
-        if (lane == 0) sh->mx[warp][h] = m;
-      }
-      named_sync(1, 128);
-#pragma unroll
-      for (int h = 0; h < GT; ++h) {
-        const float m = fmaxf(fmaxf(sh->mx[0][h], sh->mx[1][h]), fmaxf(sh->mx[2][h], sh->mx[3][h]));
-        const int e = m > 0.f && m < INFINITY ? max(-110, min(110, ilogbf(m) - 7)) : 0;
-        // (an infinite query has no answer: NaN, as its scores would be)
-        const float x = m < INFINITY ? q[h] * __uint_as_float((uint32_t)(127 - e) << 23) : NAN;
-        qf[h] = p.qscale * __uint_as_float((uint32_t)(127 + e) << 23);
-        const uint32_t hi = e4m3x2(x, 0.f);
-        float back, none;
-        from_e4m3x2(hi, back, none);
-        const uint32_t lo = e4m3x2((x - back) * 16.f, 0.f);
-        sts_u8(sbase + kOffQ + swz_byte(h, r), hi);
-        sts_u8(sbase + kOffQ + swz_byte(NH + h, r), lo);
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(&sh->qf);
-      named_sync(1, 128);                        // mx is written again below
-    }
     float m[GT], l[GT], w[GT];
     int kvi[GT];
 #pragma unroll
