@@ -28,7 +28,10 @@
 // rows are requantised (the scales are powers of two: exact but for underflow).
 // One warp owns a destination block's head, so nothing is atomic.
 // Bound by latency and HBM: 8 bytes read per token and head, 8 written per slot,
-// and the moved rows.
+// and the moved rows.  4 prompts of 4096 to 16384 tokens x 8 heads (bf16) cut to 2048
+// take 37 us (45 with the cluster's bins added by one warp, a scan each for holes and
+// movers, and ties counted in any case); a step of 64 sequences x 8 heads from at most
+// 1040 tokens to 1024 (e4m3) 20.6 on the GPU.
 #include <limits.h>
 
 #include "pa_common.cuh"
@@ -569,7 +572,8 @@ extern "C" int pa_evict(void* k_cache, void* v_cache, float* k_scale, float* v_s
   const Layout l = layout(num_seqs, num_kv_heads, max_blocks_per_seq, block_size, budget);
   if (!workspace || workspace_bytes < l.total) return PA_ERR_WORKSPACE;
   // destination blocks per CTA of the second kernel: a warp has one while the
-  // (sequence, head) rows alone do not fill the SMs, four otherwise
+  // (sequence, head) rows alone do not fill the SMs, four otherwise (32 rows 37 us
+  // against 48 with four, 512 rows 28 with one against 22.5)
   const int rows = num_seqs * num_kv_heads;
   const int per = rows >= 2 * 152 ? 4 * kMoveWarps : kMoveWarps;
   const long long blocks = (long long)rows * ((l.nb + per - 1) / per);
@@ -607,15 +611,19 @@ extern "C" int pa_evict(void* k_cache, void* v_cache, float* k_scale, float* v_s
   p.dst = reinterpret_cast<int32_t*>(ws + l.dst);
   p.first = reinterpret_cast<int32_t*>(ws + l.first);
   p.ws_len = reinterpret_cast<int32_t*>(ws + l.len);
-  // Up to 4096 slots: one CTA of 256 threads, several (sequence, head) rows per SM;
-  // above: a cluster of four of 512.
-  const bool wide = max_ctx > 4096;
+  // A row of up to 2048 slots has one CTA of 256 threads (512 rows of 1040 slots: 22 us; clusters 93).  A
+  // longer one has 512 (32 rows of 4000 slots 21 us against 26, 512 rows 97 against 91; 128 rows of 16384
+  // 65 against 86), or a cluster of four of them while the rows leave SMs idle (64 rows of 16384 slots 36 us
+  // against 46, 32 of 6000 22 against 24; but 128 of 16384 73 against 65) and where a CTA's shared memory
+  // does not hold the keys.
+  const bool tall = max_ctx > 2048, wide = tall && (rows * kCluster <= 2 * 152 || max_ctx > kMaxSmemKeys);
   const int cs = wide ? kCluster : 1;
   const long long slots = wide ? ((max_ctx + cs - 1) / cs + 31) / 32 * 32 : max_ctx;    // of a CTA
   const bool in_smem = slots <= kMaxSmemKeys;
   int words = (int)((slots + 31) / 32);
   const size_t smem = (size_t)words * 4 + (in_smem ? (size_t)slots * 4 : 0);
-  const void* select = !wide     ? reinterpret_cast<const void*>(&select_kernel<256, 1, true>)
+  const void* select = !tall     ? reinterpret_cast<const void*>(&select_kernel<256, 1, true>)
+                       : !wide   ? reinterpret_cast<const void*>(&select_kernel<512, 1, true>)
                        : in_smem ? reinterpret_cast<const void*>(&select_kernel<512, kCluster, true>)
                                  : reinterpret_cast<const void*>(&select_kernel<512, kCluster, false>);
   if (smem > 32 * 1024) {
@@ -627,7 +635,7 @@ extern "C" int pa_evict(void* k_cache, void* v_cache, float* k_scale, float* v_s
   void* args[] = {&p, &words};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * cs));
-  cfg.blockDim = dim3(wide ? 512u : 256u);
+  cfg.blockDim = dim3(tall ? 512u : 256u);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute attr;

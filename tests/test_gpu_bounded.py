@@ -205,6 +205,14 @@ def test_evict_long_context(pa, L, in_place):
     assert _evict_both(pa, *args, 2048, 256, 4, in_place) == 0
 
 
+@pytest.mark.parametrize("ties", [False, True])
+@pytest.mark.parametrize("lens", [[2100, 2049, 300], [5000] * 2 + [1200] * 38])
+def test_evict_long_rows_few_and_many(pa, lens, ties):
+    """Six and eighty rows of more than 2048 slots: another split of the selection each."""
+    args = _evict_inputs("e4m3", lens, 2, 32, 32, 1024, seed=6, ties=ties)
+    assert _evict_both(pa, *args, 1024, 64, 4, ties) == 0
+
+
 def test_evict_lengths_out_of_range_are_clamped_and_flagged(pa):
     c, w, pos, kl, seen = _evict_inputs("bf16", [40, 40], 2, 64, 16, 16)
     c.lens[0] = -3
