@@ -27,8 +27,13 @@
 //    a query tile's MMAs each: P V of a step, then the S of the next but one, so that
 //    the step's successor has its scores already.  (Steps of 128 keys in one buffer
 //    make less of the tensor core wait for its A operand, 68 clocks an MMA against 48
-//    for half the work, but chain softmax, P V and S: 8 chunks of 512 queries took
-//    218 us and not 191.  One issuing warp for both tiles: 235, its waits in a row.)
+//    for half the work, but chain softmax, P V and S: 14 % slower on 8 chunks of 512
+//    queries.  One issuing warp for both tiles: 8 % more on top, its waits in a row.)
+//  * What bounds it: a step of a query tile is a chain of softmax, P V, S and the waits
+//    between them, and the MMAs' operands take most of the shared memory's bandwidth.
+//    8 chunks of 512 queries x 32 heads (8 KV heads) over U[1024, 4096] take 168 us
+//    (921 TFLOP/s, 48 % of the library's bf16 rate); a mixed round of 16 sequences with
+//    1 to 100 new tokens each 45.
 //  * Keys at or past the context length have P = 0, and in the V tile they are finite
 //    whatever the pool holds: a NaN code comes out finite, a block past the context with
 //    a scale of 0.  A NaN of a key in the context has to reach the rows at and past it
@@ -175,7 +180,8 @@ constexpr uint32_t kOffK = 65536;      // 3 stages of codes
 constexpr uint32_t kOffV = 114688;     // 2 stages x 2 halves of bf16
 constexpr uint32_t kOffRawV = 180224;  // 2 stages of codes
 constexpr uint32_t kOffBar = 212992;
-constexpr uint32_t kTileSmem = kOffBar + 2048 + 1024;   // + alignment slack
+constexpr uint32_t kTileSmem = kOffBar + 3072 + 1024;   // + alignment slack
+constexpr int kSorted = 128;           // batches up to which the longest contexts' pairs come first
 constexpr float kRescaleThreshold = 8.0f;               // log2 units
 constexpr uint32_t kTmemCols = 512;    // query tile h: S (and P) at columns 128 h, O at 256 + 128 h
 
@@ -189,12 +195,15 @@ struct Bars {
   // first key whose V is NaN, of every head dim, and whether there is any
   int nan_key[128];
   int any_nan;
+  // the batch's context lengths and pairs, and the sequence and pair of this CTA
+  int len[kSorted], pairs[kSorted], seq, pair;
   uint32_t tmem_base;
   int abort;
 };
-static_assert(sizeof(Bars) <= 2048 && offsetof(Bars, kscl) % 16 == 0, "barrier block");
+static_assert(sizeof(Bars) <= 3072 && offsetof(Bars, kscl) % 16 == 0, "barrier block");
 
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try_wait(smem_u32(bar), parity)) return true;
   if (*abort_flag) return false;
   if (mbar_wait(bar, parity)) return true;
   atomicOr(&g_status_prefill_fp8, PA_DEV_TIMEOUT);
@@ -356,7 +365,9 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
   volatile int* abort_flag = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // ---- work item: sequence b's pairs are units U_b = floor(query_start[b] / (2 QP)) + b
+  // ---- work item.  Up to kSorted sequences: the longest context first, so that what the SMs end
+  // with is short (8 chunks of 512: 193 us in the batch's order, 180 in this; a mixed round 54, 47).
+  // More, of which the SMs take many turns: sequence b's pairs are units U_b = floor(query_start[b] / (2 QP)) + b
   // and on; n rows make at most floor(n / (2 QP)) + 1 pairs, which never passes U_{b+1}
   const int kvh = (int)(blockIdx.x % p.Hkv);
   const int u = (int)(blockIdx.x / p.Hkv);
@@ -366,11 +377,38 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
       if (!good_rows(p, i) || Li < 0 || Li > p.max_blocks * p.bs) atomicOr(&g_status_prefill_fp8, PA_DEV_BAD_LEN);
     }
   }
-  const int b = find_unit(p.query_start, p.B, 2 * QP, 1, u);
-  if (!good_rows(p, b)) return;
+  int b, pi;
+  if (p.B <= kSorted) {
+    const int x = (int)threadIdx.x;
+    int mine = 0, len = 0;
+    if (x < p.B) {
+      len = __ldg(&p.context_lens[x]);
+      mine = good_rows(p, x) ? (__ldg(&p.query_start[x + 1]) - __ldg(&p.query_start[x]) + 2 * QP - 1) / (2 * QP) : 0;
+      bars->len[x] = len;
+      bars->pairs[x] = mine;
+    }
+    if (x == 0) bars->seq = -1;
+    __syncthreads();
+    if (x < p.B) {
+      int before = 0;                              // pairs of the longer contexts
+      for (int i = 0; i < p.B; ++i)
+        if (bars->len[i] > len || (bars->len[i] == len && i < x)) before += bars->pairs[i];
+      if (u >= before && u < before + mine) {
+        bars->seq = x;
+        bars->pair = u - before;
+      }
+    }
+    __syncthreads();
+    b = bars->seq;
+    if (b < 0) return;
+    pi = bars->pair;
+  } else {
+    b = find_unit(p.query_start, p.B, 2 * QP, 1, u);
+    if (!good_rows(p, b)) return;
+    pi = u - (__ldg(&p.query_start[b]) / (2 * QP) + b);
+  }
   const int qrow0 = __ldg(&p.query_start[b]);
   const int nq = __ldg(&p.query_start[b + 1]) - qrow0;
-  const int pi = u - (qrow0 / (2 * QP) + b);
   const int npairs = (nq + 2 * QP - 1) / (2 * QP);
   if (pi < 0 || pi >= npairs) return;              // nothing allocated yet
   int L = __ldg(&p.context_lens[b]);
