@@ -266,6 +266,22 @@ def test_prefill(pa, Hq, Hkv, D, bs):
     check(out, ref, tol)
 
 
+@pytest.mark.parametrize("B", [128, 129, 300])
+def test_prefill_many_sequences(pa, B):
+    """Batches on both sides of the size up to which the longest contexts come first."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(1, 150, B)
+    n = np.minimum(lens, rng.choice([0, 1, 1, 1, 2, 33, 70], B))
+    c = Case("e4m3", lens, 8, 2, 128, 16, seed=B, rows=int(n.sum()))
+    start = _start(n)
+    ref, tol = reference(c, start.numpy())
+    c.cuda()
+    out = torch.full_like(c.q, float("nan"))
+    pa.prefill_fp8_blocks(out, c.q, start.cuda(), c.k, c.v, c.ks, c.vs, c.tab, c.lens, c.scale)
+    assert pa.last_error() == 0
+    check(out, ref, tol)
+
+
 def test_prefill_rows_before_the_context_and_rows_past_the_last_sequence(pa):
     c = Case("e4m3", [40, 5], 8, 2, 128, 16, seed=9, rows=30)
     start = torch.tensor([0, 10, 22], dtype=torch.int32)      # 12 rows on a context of 5; rows 22..29 are nobody's
