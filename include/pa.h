@@ -370,11 +370,12 @@ int pa_append_fp8_blocks(const void* key, const void* value,
  *   other arguments as for pa_decode
  *
  * With block_size 8 to 32 and num_kv_heads * head_dim a multiple of 128 it runs
- * on the tcgen05 tensor cores, the codes as they are (e4m3 products, fp32
- * accumulation): Q, and the products of softmax weight and V scale, enter as two
- * e4m3 terms each, which carry bf16's 8 significant bits for products down to
- * 2^-11 of the head's largest and 2^-19 of that largest below.  Everything else
- * runs on CUDA cores in fp32.
+ * on the tcgen05 tensor cores, the codes as they are (8-bit products, fp32
+ * accumulation): Q enters as two e4m3 terms, off by at most 2^-21 of the head's
+ * largest element; the products of softmax weight and V scale as three e5m2 terms,
+ * which hold a product to 2^-9 of itself (bf16's precision) down to 2^-26 of the
+ * head's largest, and to 2^-35 of that largest below.  Everything else runs on CUDA
+ * cores in fp32.
  */
 int pa_decode_fp8_blocks(void* out, const void* query,
                          const void* k_cache, const void* v_cache,

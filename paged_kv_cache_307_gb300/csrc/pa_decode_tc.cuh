@@ -6,26 +6,34 @@
 //
 // What bounds decode over 8-bit pools is not the bytes but the instructions
 // that widen every code for 16-bit products (about 36 per token and KV head on
-// the mma.sync path: 281 us where this takes 188).  Here a tile of 128 tokens of
+// the mma.sync path: 281 us where this takes 192).  Here a tile of 128 tokens of
 // one KV head costs eight MMAs, and per token only its scores are touched by threads.
 // Bound by HBM but for the CTAs' starts and ends: 64 requests x 8 KV heads x 128,
-// 32 query heads, over U[1024, 16384] tokens take 188 us (1.14 GB, 6.1 TB/s, 90 % of
-// the copy rate) and 64 x 32 heads over U[128, 2048] 97 us (5.9 TB/s).
+// 32 query heads, over U[1024, 16384] tokens take 192 us (1.14 GB, 6.0 TB/s, 88 % of
+// the copy rate) and 64 x 32 heads over U[128, 2048] 96 us (6.0 TB/s).  P's third term
+// costs nothing that shows (193 and 94 us with two terms): the tensor pipe is idle
+// enough, and threads store three bytes for two.
 //
 // One CTA = (sequence, partition of P tokens, KV head, up to 16 query heads):
 //   S^T[128 tokens x N] = K[128 x 128] Q^T      A = K tile (K-major), B = Q rows
 //   O^T[128 dims x N]  += V^T[128 x 128] P^T    A = V tile (MN-major), B = P rows
-// N = 2 x (8 or 16) columns: every query head has two rows, because bf16 Q (8
-// significant bits) and P do not fit one e4m3 value (4 bits):
+// N: every query head has several rows, because bf16 Q (8 significant bits) and P
+// do not fit one 8-bit value.  Q has two e4m3 terms (N = 2 x 8 or 16):
 //   q 2^-e = hi + lo / 16, hi = e4m3(q 2^-e), lo = e4m3(16 (q 2^-e - hi)),
 // with 2^e per head so that max |q 2^-e| is in [128, 256).  The residual of hi
 // has at most 4 significant bits left, so the split is exact while
-// |q 2^-e| >= 2^-6, and off by at most 2^-14 (2^-21 of the largest) below.  P
-// likewise: a token enters O with 32 2^(z - w), z = score + log2 of its block's V
-// scale, w the head's running reference for z; so 8 bits for products of weight
-// and V scale down to 2^-11 of the head's largest, an absolute 2^-19 of it below,
-// however far the blocks' scales are apart.  The sum of the softmax has a reference m
-// of its own (a block may have the scale 0); the K scale multiplies the score in fp32.
+// |q 2^-e| >= 2^-6, and off by at most 2^-14 (2^-21 of the largest) below.
+// P has three e5m2 terms (N = 3 x 4, 8 or 16, rounded up to 16, 32, 48; the two
+// operands' formats are independent):
+//   x = 2^(z - w + 12) = t0 + t1 / 16 + t2 / 256, each term the rest's e5m2 value,
+// z = score + log2 of its block's V scale, w the head's running reference for z,
+// x <= 2^15.  Each term takes 3 bits, so x is held to 2^-9 of itself down to 2^-26 of
+// the reference and to 2^-35 of the reference below: bf16's precision, and next to
+// nothing lost of the many tokens of small weight that stand beside one that takes
+// nearly all of it (two e4m3 terms dropped what is below 2^-19 of the reference, which
+// was all of the output where the one had a value of zero), however far the blocks' scales are
+// apart.  The sum of the softmax has a reference m of its own (a block may have the
+// scale 0); the K scale multiplies the score in fp32.
 //
 // head_dim 64 and 32 (HP = 2 and 4): HP neighbouring KV heads make one row of 128
 // codes, so the pool is read as one of Hkv / HP heads of 128.  The query heads of
@@ -40,7 +48,7 @@
 //    the loop, behind their scales, the first request left 2000 clocks later: 196 us).
 //  * warp 5: TMEM, and the MMAs: S_{j+1} before O += V_j P_j.
 //  * warps 0-3: one thread per token: scores from TMEM, scale, mask, p = 2^(s-m),
-//    the sum, P's two terms as bytes into the B tile.  The references (m and w of
+//    the sum, P's three terms as bytes into the B tile.  The references (m and w of
 //    every head) are common to the 128 threads and move only when a score or a z
 //    exceeds its own by 3 (a factor 8): one barrier with a vote per tile; then O is
 //    rescaled in TMEM.
@@ -63,24 +71,36 @@ namespace {
 constexpr int kTcTile = 128;               // tokens per tile
 constexpr uint32_t kTcStage = 16384;       // 128 tokens x 128 codes
 constexpr float kTcSlack = 3.f;            // log2 units a score may exceed the reference by
-constexpr float kTcPShift = 5.f;           // log2 of what P is scaled by: [0, 8] -> [0, 256]
+constexpr float kTcPShift = 12.f;          // log2 of what P is scaled by: [0, 8] -> [0, 2^15], e5m2's top binade
 
+// Heads' rows of one term, for GT query heads: of Q (two terms), and of P (three).
+constexpr int tc_q_heads(int gt) { return gt <= 8 ? 8 : 16; }
+constexpr int tc_p_heads(int gt) { return gt <= 4 ? 4 : gt <= 8 ? 8 : 16; }
+// P's columns (a multiple of 16), and the bytes of one of its two buffers: whole 8-row
+// atoms of the rows that there are.  (The MMAs read 8 rows past the last of 24: of the
+// next buffer, or of Q behind it; their columns of O are never read.)
+constexpr int tc_p_cols(int gt) { return (3 * tc_p_heads(gt) + 15) / 16 * 16; }
+constexpr uint32_t tc_p_bytes(int gt) { return (3u * tc_p_heads(gt) + 7u) / 8u * 1024u; }
+
+template <int NH, int HP>
 struct TcShared {
-  uint64_t full_k[2], full_v[2], empty_k[2], empty_v[2], s[2], p[2], pv[2], scl_full[4], drain;
-  // scales (K's, log2 of V's) of the 128 / bs blocks of tile j, HP heads each, in slot j & 3:
-  // tile j+2's and j+3's may be written while the softmax works on j, j+4's only
-  // after P_j
-  alignas(16) float scl[4][2][64];
-  alignas(16) float mx[4][16];             // per warp: tile maximum of every head; at the end, sums
-  alignas(16) float wx[4][16];             // likewise of z
+  uint64_t full_k[2], full_v[2], empty_k[2], empty_v[2], s[2], p[2], pv[2], scl_full[2], drain;
+  // scales (K's, log2 of V's) of the 128 / bs <= 16 blocks of tile j, HP heads each, in
+  // slot j & 1: tile j+2's are written when its V stage is free, which is after P_j
+  alignas(16) float scl[2][2][16 * HP];
+  alignas(16) float mx[4][NH];             // per warp: tile maximum of every head; at the end, sums
+  alignas(16) float wx[4][NH];             // likewise of z
   uint32_t tmem_base;
   int abort;
 };
 
-template <int NH>
+template <int GT, int HP>
 constexpr uint32_t tc_smem_bytes() {
-  return 4 * kTcStage + 3u * (2u * NH * 128u) + (uint32_t)sizeof(TcShared) + 1024u;
+  return 4 * kTcStage + 2 * tc_p_bytes(GT) + 2u * tc_q_heads(GT) * 128u +
+         (uint32_t)sizeof(TcShared<tc_q_heads(GT), HP>) + 1024u;
 }
+// (three CTAs of up to 8 heads per SM: 228 KB less 1 KB a CTA that the system takes)
+static_assert(tc_smem_bytes<8, 1>() <= 75 * 1024 && tc_smem_bytes<8, 4>() <= 75 * 1024, "three CTAs per SM");
 
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                         uint32_t accumulate) {
@@ -90,9 +110,10 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
       ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
 }
-// kind::f8f6f4, e4m3 operands (format 0), fp32 accumulation.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn_major) {
-  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// kind::f8f6f4, A e4m3 (format 0), B e4m3 or e5m2 (format 1), fp32 accumulation.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn_major, bool b_e5m2) {
+  return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | ((a_mn_major ? 1u : 0u) << 15) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
 }
 // Two floats as e4m3 codes (a in the low byte), saturating, and back.
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
@@ -104,6 +125,15 @@ __device__ __forceinline__ void from_e4m3x2(uint32_t c, float& a, float& b) {
   uint32_t h;
   asm("{\n\t.reg .b16 x;\n\tcvt.u16.u32 x, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(h) : "r"(c));
   f16x2_to_float2(h, a, b);
+}
+// The same for e5m2 codes, which are the upper bytes of f16 values.
+__device__ __forceinline__ uint32_t e5m2x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ void from_e5m2x2(uint32_t c, float& a, float& b) {
+  f16x2_to_float2(__byte_perm(c, 0u, 0x1404), a, b);
 }
 __device__ __forceinline__ void sts_u8(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
@@ -159,14 +189,18 @@ __global__ void __launch_bounds__(kTcThreads, GT <= 8 ? 3 : 2)
 tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                  const DecodeParams p) {
   constexpr int D = 128 / HP;
-  constexpr int NH = GT <= 8 ? 8 : 16;          // heads' rows of one term
-  constexpr int N = 2 * NH;
-  constexpr uint32_t kTmem = N == 16 ? 64u : 128u;   // S_0, S_1, O: N columns each
-  constexpr uint32_t kOffV = 2 * kTcStage, kOffQ = 4 * kTcStage, kOffP = kOffQ + N * 128;
+  constexpr int NH = tc_q_heads(GT), N = 2 * NH;     // Q's rows and the columns of S
+  constexpr int NP = tc_p_heads(GT), NO = tc_p_cols(GT);
+  constexpr uint32_t kTmem = GT <= 8 ? 64u : 128u;   // S_0, S_1: N columns each, O: NO
+  static_assert(2 * N + NO <= (int)kTmem, "tensor memory");
+  constexpr uint32_t kPBytes = tc_p_bytes(GT);
+  constexpr uint32_t kOffV = 2 * kTcStage, kOffP = 4 * kTcStage, kOffQ = kOffP + 2 * kPBytes;
+  static_assert(NO * 128u - kPBytes <= N * 128u, "P's MMAs read inside the tiles");
+  using Shared = TcShared<NH, HP>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
-  TcShared* sh = reinterpret_cast<TcShared*>(smem + kOffP + 2 * N * 128);
+  Shared* sh = reinterpret_cast<Shared*>(smem + kOffQ + N * 128);
   volatile int* abort_flag = &sh->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;");
@@ -245,7 +279,7 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
         mbar_init(&sh->p[i], 128);
         mbar_init(&sh->pv[i], 1);
       }
-      for (int i = 0; i < 4; ++i) mbar_init(&sh->scl_full[i], 1);
+      for (int i = 0; i < 2; ++i) mbar_init(&sh->scl_full[i], 1);
       mbar_init(&sh->drain, 1);
       sh->abort = 0;
       fence_mbar_init();
@@ -320,12 +354,12 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       if (lane < 16) {
 #pragma unroll
         for (int i = 0; i < HP; ++i) {
-          sh->scl[j & 3][0][lane * HP + i] = x.k[i];
-          sh->scl[j & 3][1][lane * HP + i] = log2f(x.v[i]);
+          sh->scl[j & 1][0][lane * HP + i] = x.k[i];
+          sh->scl[j & 1][1][lane * HP + i] = log2f(x.v[i]);
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->scl_full[j & 3]);
+      if (lane == 0) mbar_arrive(&sh->scl_full[j & 1]);
     };
     if (first > 1) request(mapV, &sh->full_v[1], kOffV, 1, id[1]);
     const Scales sc_0 = scales_of(id[0]), sc_1 = scales_of(id[1]);
@@ -361,8 +395,8 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
   } else if (warp == 5) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0 && nt > 0) {
-      constexpr uint32_t idS = idesc_e4m3_f32(kTcTile, N, false);
-      constexpr uint32_t idO = idesc_e4m3_f32(128, N, true);
+      constexpr uint32_t idS = idesc_e4m3_f32(kTcTile, N, false, false);
+      constexpr uint32_t idO = idesc_e4m3_f32(128, NO, true, true);
       const uint64_t dk = sdesc_sw128(sbase, 16, 1024), dq = sdesc_sw128(sbase + kOffQ, 16, 1024);
       const uint64_t dv = sdesc_sw128(sbase + kOffV, kTcStage, 1024), dp = sdesc_sw128(sbase + kOffP, 16, 1024);
       auto issue_s = [&](int j) {
@@ -387,7 +421,7 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           if (!tc_wait(&sh->p[st], ph, abort_flag)) break;
           if (!tc_wait(&sh->full_v[st], ph, abort_flag)) break;
           tc_fence_after();
-          const uint64_t dvj = sdesc_at(dv, (uint32_t)st * kTcStage), dpj = sdesc_at(dp, (uint32_t)st * (N * 128));
+          const uint64_t dvj = sdesc_at(dv, (uint32_t)st * kTcStage), dpj = sdesc_at(dp, (uint32_t)st * kPBytes);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)         // 32 tokens each: four 8-token groups of 1024 bytes
             umma_f8(tO, sdesc_at(dvj, kk * 4096u), sdesc_at(dpj, kk * 32u), idO, (j > 0 || kk > 0) ? 1u : 0u);
@@ -423,12 +457,12 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       const uint32_t ph = (uint32_t)(j >> 1) & 1u;
       const int t = t0 + j * kTcTile + r;
       const bool ok = t < t1;
-      tc_wait(&sh->scl_full[j & 3], (uint32_t)(j >> 2) & 1u, abort_flag);
+      tc_wait(&sh->scl_full[st], ph, abort_flag);
       float ks[HP], lv[HP];
 #pragma unroll
       for (int i = 0; i < HP; ++i) {
-        ks[i] = sh->scl[j & 3][0][(r >> bsh) * HP + i];
-        lv[i] = ok ? sh->scl[j & 3][1][(r >> bsh) * HP + i] : -INFINITY;
+        ks[i] = sh->scl[st][0][(r >> bsh) * HP + i];
+        lv[i] = ok ? sh->scl[st][1][(r >> bsh) * HP + i] : -INFINITY;
       }
       __syncwarp();
       tc_wait(&sh->s[st], ph, abort_flag);
@@ -502,56 +536,44 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
           w[h] = wn;
         }
         if (j > 0) {
-          // O holds V_{j-1} P_{j-1}: this thread's head dim, every head's two columns
+          // O holds V_{j-1} P_{j-1}: this thread's head dim, every head's three columns
           tc_wait(&sh->pv[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u, abort_flag);
           __syncwarp();
           tc_fence_after();
-          if constexpr (NH == 8) {
-            uint32_t v[16];
-            tmem_ld16(tO + lane_off, v);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            uint32_t v[NP];
+            tmem_ld(tO + i * NP + lane_off, v);
             tmem_ld_wait();
 #pragma unroll
-            for (int h = 0; h < GT; ++h) {
-              v[h] = __float_as_uint(__uint_as_float(v[h]) * f[h]);
-              v[8 + h] = __float_as_uint(__uint_as_float(v[8 + h]) * f[h]);
-            }
-            tmem_st16(tO + lane_off, v);
-          } else {
-            uint32_t v[32];
-            tmem_ld32(tO + lane_off, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int h = 0; h < GT; ++h) {
-              v[h] = __float_as_uint(__uint_as_float(v[h]) * f[h]);
-              v[16 + h] = __float_as_uint(__uint_as_float(v[16 + h]) * f[h]);
-            }
-            tmem_st32(tO + lane_off, v);
+            for (int h = 0; h < GT; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) * f[h]);
+            tmem_st(tO + i * NP + lane_off, v);
           }
           tmem_st_wait();
         }
         named_sync(1, 128);                      // mx is free again
       }
-      // P: 32 2^(z - w) as two e4m3 terms, byte r of rows h and NH + h
-      const uint32_t pb = sbase + kOffP + (uint32_t)st * (N * 128);
+      // P: 2^(z - w + 12) as three e5m2 terms, byte r of rows h, NP + h and 2 NP + h
+      const uint32_t pb = sbase + kOffP + (uint32_t)st * kPBytes;
       auto weight = [&](int h) -> float {
         const float z = s[h] + pick(lv, kvi[h]);
         return z == -INFINITY ? 0.f : exp2f(z - w[h] + kTcPShift);
       };
 #pragma unroll
       for (int h = 0; h < GT; h += 2) {
-        const bool two = GT > 1;
         l[h] += s[h] == -INFINITY ? 0.f : exp2f(s[h] - m[h]);
         if constexpr (GT > 1) l[h + 1] += s[h + 1] == -INFINITY ? 0.f : exp2f(s[h + 1] - m[h + 1]);
         const float x0 = weight(h), x1 = GT > 1 ? weight(h + (GT > 1)) : 0.f;
-        const uint32_t hi = e4m3x2(x0, x1);
-        float y0, y1;
-        from_e4m3x2(hi, y0, y1);
-        const uint32_t lo = e4m3x2((x0 - y0) * 16.f, (x1 - y1) * 16.f);
-        sts_u8(pb + swz_byte(h, r), hi);
-        sts_u8(pb + swz_byte(NH + h, r), lo);
-        if (two) {
-          sts_u8(pb + swz_byte(h + 1, r), hi >> 8);
-          sts_u8(pb + swz_byte(NH + h + 1, r), lo >> 8);
+        float r0 = x0, r1 = x1;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const uint32_t c = e5m2x2(r0, r1);
+          sts_u8(pb + swz_byte(i * NP + h, r), c);
+          if constexpr (GT > 1) sts_u8(pb + swz_byte(i * NP + h + 1, r), c >> 8);
+          float y0, y1;
+          from_e5m2x2(c, y0, y1);
+          r0 = (r0 - y0) * 16.f;
+          r1 = (r1 - y1) * 16.f;
         }
       }
       if (!ok) {
@@ -585,19 +607,14 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       __syncwarp();
       tc_fence_after();
       auto up = [&](int h) -> float { return w[h] == -INFINITY ? 0.f : exp2f(w[h] - m[h] - kTcPShift); };
-      if constexpr (NH == 8) {
-        uint32_t v[16];
-        tmem_ld16(tO + lane_off, v);
-        tmem_ld_wait();
+      uint32_t v[3][NP];
 #pragma unroll
-        for (int h = 0; h < GT; ++h) o[h] = fmaf(__uint_as_float(v[8 + h]), 0.0625f, __uint_as_float(v[h])) * up(h);
-      } else {
-        uint32_t v[32];
-        tmem_ld32(tO + lane_off, v);
-        tmem_ld_wait();
+      for (int i = 0; i < 3; ++i) tmem_ld(tO + i * NP + lane_off, v[i]);
+      tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < GT; ++h) o[h] = fmaf(__uint_as_float(v[16 + h]), 0.0625f, __uint_as_float(v[h])) * up(h);
-      }
+      for (int h = 0; h < GT; ++h)
+        o[h] = fmaf(fmaf(__uint_as_float(v[2][h]), 0.0625f, __uint_as_float(v[1][h])), 0.0625f, __uint_as_float(v[0][h])) *
+               up(h);
     }
 #pragma unroll
     for (int h = 0; h < GT; ++h) {

@@ -20,7 +20,7 @@ Launch pick_direct(int gt) {
 // tcgen05 instances: gt query heads per CTA, 128 / head_dim KV heads per row of codes.
 template <int GT, int HP>
 Launch pick_tc(size_t* smem) {
-  *smem = tc_smem_bytes<(GT <= 8 ? 8 : 16)>();
+  *smem = tc_smem_bytes<GT, HP>();
   return {reinterpret_cast<const void*>(&tc_decode_kernel<GT, HP, true>),
           reinterpret_cast<const void*>(&weights_kernel<B16, 128 / HP>)};
 }
