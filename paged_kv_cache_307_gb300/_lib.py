@@ -129,6 +129,15 @@ def _check(code, what):
         raise PAError(code, what)
 
 
+def _own(alloc, stream, *sizes):
+    """A workspace of the call's own, out of the memory of the stream that the call runs on: what the current
+    stream has freed it may still be writing, and what `stream` frees it has used up in its own order."""
+    if stream is None:
+        return alloc(*sizes)
+    with torch.cuda.stream(stream):
+        return alloc(*sizes)
+
+
 def _contig(*ts):
     for t in ts:
         if not t.is_contiguous():
@@ -183,7 +192,7 @@ def decode(out, q, k_cache, v_cache, block_tables, context_lens, scale, partitio
     B, Hq, D = q.shape
     NB, bs, Hkv, _ = k_cache.shape
     if workspace is None:
-        workspace = alloc_workspace(q, k_cache, block_tables, partition_size)
+        workspace = _own(alloc_workspace, stream, q, k_cache, block_tables, partition_size)
     _check(lib.pa_decode(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                          block_tables.shape[1], _ptr(context_lens), B, Hq, Hkv, D, bs, NB,
                          ctypes.c_float(scale), partition_size, _ptr(workspace), workspace.numel(),
@@ -218,7 +227,7 @@ def decode_shared(out, q, k_cache, v_cache, block_tables, context_lens, group_st
     ng = shared_blocks.shape[0]
     assert group_start.shape[0] == ng + 1
     if workspace is None:
-        workspace = alloc_shared_workspace(q, k_cache, block_tables, ng, partition_size)
+        workspace = _own(alloc_shared_workspace, stream, q, k_cache, block_tables, ng, partition_size)
     _check(lib.pa_decode_shared(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                 block_tables.shape[1], _ptr(context_lens), B, _ptr(group_start),
                                 _ptr(shared_blocks), ng, Hq, Hkv, D, bs, NB, ctypes.c_float(scale), partition_size,
@@ -235,7 +244,7 @@ def decode_fp8(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context
     B, Hq, D = q.shape
     NB, bs, Hkv, _ = k_cache.shape
     if workspace is None:
-        workspace = alloc_workspace(q, k_cache, block_tables, partition_size)
+        workspace = _own(alloc_workspace, stream, q, k_cache, block_tables, partition_size)
     _check(lib.pa_decode_fp8(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
                              _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), B, Hq, Hkv, D, bs, NB,
                              ctypes.c_float(scale), partition_size, _ptr(workspace), workspace.numel(), _dtype(q),
@@ -320,13 +329,6 @@ def _on(stream, device):
     if stream is not None:
         return stream.cuda_stream
     return _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
-
-
-def _on_stream(workspace, stream):
-    """A workspace of the call's own, kept from other uses until `stream` is through with it."""
-    if stream is not None:
-        workspace.record_stream(stream)
-    return workspace
 
 
 def _ready(*ts):
@@ -441,7 +443,7 @@ def decode_fp8_blocks(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, 
         raise ValueError("one query row per sequence")
     kind = _kind(q)
     if workspace is None:
-        workspace = _on_stream(alloc_fp8_blocks_workspace(q, k_cache, block_tables, partition_size), stream)
+        workspace = _own(alloc_fp8_blocks_workspace, stream, q, k_cache, block_tables, partition_size)
     dev = _ready(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, workspace)
     _check(lib.pa_decode_fp8_blocks(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                                     k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(), cols,
@@ -491,7 +493,7 @@ def decode_weights(out, weights, q, k_cache, v_cache, block_tables, context_lens
     if weights.dtype is not _F32 or len(wshape) != 3 or wshape[0] != B or wshape[1] != Hkv:
         raise ValueError("weights is float32 [num_seqs, num_kv_heads, slots]")
     if workspace is None:
-        workspace = _on_stream(alloc_weights_workspace(q, k_cache, block_tables, partition_size), stream)
+        workspace = _own(alloc_weights_workspace, stream, q, k_cache, block_tables, partition_size)
     ks = vs = None
     if kv == PA_FP8_E4M3:
         _ready(k_scale, v_scale)
@@ -529,7 +531,7 @@ def evict(k_cache, v_cache, block_tables, context_lens, kept_lens, seen_lens, we
             token_pos.shape == shape and weights_out.shape == shape and token_pos_out.shape == shape):
         raise ValueError("weights and token_pos are [num_seqs, num_kv_heads, slots], in and out alike")
     if workspace is None:
-        workspace = _on_stream(alloc_evict_workspace(k_cache, block_tables, budget), stream)
+        workspace = _own(alloc_evict_workspace, stream, k_cache, block_tables, budget)
     ks = vs = None
     if kv == PA_FP8_E4M3:
         _ready(k_scale, v_scale)
