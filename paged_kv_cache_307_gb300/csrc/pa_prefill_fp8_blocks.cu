@@ -8,11 +8,13 @@
 // tile_kernel (head_dim 128, blocks of 8 and more): 5th-generation tensor cores.  One CTA per (pair of
 // query tiles, KV head), one CTA per SM: a tile is 128 rows = QP = 128 / G positions
 // x G query heads; keys in tiles of 128; scores and output in tensor memory.
-//  * S = Q K^T takes the codes of K as they are (kind::f8f6f4).  Q enters as two e4m3
-//    terms: q 2^-e = hi + lo with 2^e per row so that the row's largest value is in
-//    [128, 256); hi carries 4 significant bits, lo the other 4 of a bf16 value, exactly
-//    down to 2^-10 of the largest and within 2^-17 of it below.  K's scales stay apart,
-//    in the softmax.
+//  * S = Q K^T takes the codes of K as they are (kind::f8f6f4).  Q enters as two terms,
+//    hi in e4m3 and lo in e5m2: q 2^-e = hi + lo with 2^e per row so that the row's
+//    largest value is in [128, 256).  hi takes 4 significant bits of a bf16 value and
+//    leaves 4, at most 8 units of the value's last place, which e5m2's 3 bits hold
+//    exactly: the split is exact down to 2^-13 of the largest, and within 2^-20 of it below.
+//    (lo in e4m3 ends at 2^-9, so it dropped what is below 2^-17 of the largest.)  K's
+//    scales stay apart, in the softmax.
 //  * P V runs in bf16.  V's codes come by TMA into a stage of their own; warps 8-11
 //    widen them (codes_to_bf16), multiply their scale in (exact for a power of two;
 //    bf16 has the exponents for it, so a row that attends only to blocks of small scale
@@ -220,7 +222,7 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// D[tmem] (+)= A[smem] * B[smem], e4m3 operands.
+// D[tmem] (+)= A[smem] * B[smem], 8-bit operands of the descriptor's formats.
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                         uint32_t accumulate) {
   asm volatile(
@@ -229,11 +231,19 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
       ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
 }
-// Four floats as e4m3 codes (the first in the low byte), and back.
+// Four floats as e4m3 codes (the first in the low byte).
 __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
   uint32_t r;
   asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\t"
       "cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\tmov.b32 %0, {x, y};\n\t}"
+      : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+// The same as e5m2 codes.
+__device__ __forceinline__ uint32_t to_e5m2x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e5m2x2.f32 x, %2, %1;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f32 y, %4, %3;\n\tmov.b32 %0, {x, y};\n\t}"
       : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
   return r;
 }
@@ -538,7 +548,9 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
   } else if (warp >= 13) {
     // ---------------------------------------------------------- MMA issuers, one per query tile
     if (lane == 0 && nt > 0) {
-      constexpr uint32_t idS = (1u << 4) | ((uint32_t)(kStep >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);   // e4m3, fp32
+      // fp32 scores of e4m3 keys; of Q the e4m3 term, then the e5m2 one (format 1 of A)
+      constexpr uint32_t idHi = (1u << 4) | ((uint32_t)(kStep >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+      constexpr uint32_t idLo = idHi | (1u << 7);
       constexpr uint32_t idO = idesc_bf16_f32(kRows, 128, false, true);   // V MN-major
       const int h = warp - 13, ns = h ? ns1 : ns0;
       const uint64_t dq = sdesc_sw128(sbase + kOffQ + h * 2 * kQHalf, 16, 1024), dk = sdesc_sw128(sbase + kOffK, 16, 1024);
@@ -557,7 +569,7 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             umma_f8(tS + g * 64, sdesc_at(dq, (uint32_t)(kk >> 2) * kQHalf + (uint32_t)(kk & 3) * 32u),
-                    sdesc_at(dkj, (uint32_t)(kk & 3) * 32u), idS, kk > 0 ? 1u : 0u);
+                    sdesc_at(dkj, (uint32_t)(kk & 3) * 32u), kk < 4 ? idHi : idLo, kk > 0 ? 1u : 0u);
           umma_commit(&bars->s[h][g]);
         }
         if (g == 1) {
@@ -638,7 +650,7 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
           for (int k = 0; k < 4; ++k) x[k] *= down;
           hi[e] = to_e4m3x4(x[0], x[1], x[2], x[3]);
           from_e4m3x4(hi[e], y);
-          lo[e] = to_e4m3x4(x[0] - y[0], x[1] - y[1], x[2] - y[2], x[3] - y[3]);
+          lo[e] = to_e5m2x4(x[0] - y[0], x[1] - y[1], x[2] - y[2], x[3] - y[3]);
         }
         if (live) {
           *reinterpret_cast<uint4*>(qs + ((i ^ (r & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
