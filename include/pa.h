@@ -307,8 +307,7 @@ int pa_decode_fp8(void* out, const void* query,
  *
  * A dequantised element is e4m3_value(code) * scale.  The calls below write
  * powers of two; pa_decode_fp8_blocks, pa_decode_weights and
- * pa_prefill_fp8_blocks read any finite scale >= 0 (the last rounds a V scale
- * to bf16, which a power of two survives).  Blocks are copied and
+ * pa_prefill_fp8_blocks read any finite scale >= 0.  Blocks are copied and
  * swapped with pa_copy_blocks / pa_swap_blocks on the codes and again, with
  * the same pairs, on (k_scale, v_scale) as fp32 pools of block_size 4,
  * num_kv_heads = PA_SCALE_ROW(num_kv_heads) / 4 and head_dim 1.
@@ -408,6 +407,12 @@ int pa_decode_fp8_blocks_partition_size(int num_seqs, int num_heads, int num_kv_
  *
  * A NaN value makes NaN of its head dim in the rows at and past its token, a NaN
  * key of those rows whole; the rows before are not touched by either.
+ *
+ * With head_dim 128, block_size 8 to 32 and at most 128 query heads per KV head it
+ * runs on the tcgen05 tensor cores: a query row enters as an e4m3 and an e5m2 term,
+ * off by at most 2^-20 of the row's largest element (exact down to 2^-13 of it); the
+ * softmax weights and the dequantised values are rounded to bf16 once each (which a
+ * power of two as the scale leaves exact).  Everything else runs in fp32.
  */
 int pa_prefill_fp8_blocks(void* out, const void* query, const int32_t* query_start, int total_queries,
                           const void* k_cache, const void* v_cache,

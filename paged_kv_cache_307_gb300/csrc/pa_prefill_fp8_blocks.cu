@@ -16,9 +16,9 @@
 //    (lo in e4m3 ends at 2^-9, so it dropped what is below 2^-17 of the largest.)  K's
 //    scales stay apart, in the softmax.
 //  * P V runs in bf16.  V's codes come by TMA into a stage of their own; warps 8-11
-//    widen them (codes_to_bf16), multiply their scale in (exact for a power of two;
-//    bf16 has the exponents for it, so a row that attends only to blocks of small scale
-//    keeps its precision beside blocks of large scale) and write the 128-byte-swizzled
+//    widen them (codes_to_bf16), multiply their scale in (one rounding to bf16, none for a
+//    power of two; bf16 has the exponents for it, so a row that attends only to blocks of
+//    small scale keeps its precision beside blocks of large scale) and write the 128-byte-swizzled
 //    tile that both query tiles' MMAs read: widening a tile is as many instructions as
 //    its softmax, and the pair shares it.
 //  * One thread per row (warps 0-3 and 4-7, a query tile each): x = s * (K scale of
@@ -284,6 +284,25 @@ __device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t s, uint32_t& 
   b = mul_bf16x2(mul_bf16x2(__byte_perm(lo, hi, 0x7362), kUp), s);
 }
 
+// Sixteen codes times a scale that bf16 does not hold: the products in fp32, rounded once.
+struct Row16 {
+  uint4 a, b;
+};
+__device__ __noinline__ Row16 scaled_row(uint4 c, float s) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    codes_to_bf16(w[k], 0x3f803f80u, o[2 * k], o[2 * k + 1]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(bf16lo(o[2 * k + e]) * s, bf16hi(o[2 * k + e]) * s);
+      o[2 * k + e] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+  }
+  return {make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7])};
+}
+
 // V (four warps): the codes of each key tile as bf16 rows.  Thread x takes the
 // 16-code chunk x % 8 of rows x / 8, x / 8 + 16, ...
 __device__ __forceinline__ void convert_v(const Params& p, Bars* bars, unsigned char* smem, int b, int kvh, int kend,
@@ -305,10 +324,9 @@ __device__ __forceinline__ void convert_v(const Params& p, Bars* bars, unsigned 
     }
     return -1;
   };
-  // as a bf16 in both halves; 0 past the context, where codes may be anything and P is 0
+  // its bits; 0 past the context, where codes may be anything and P is 0
   auto scale_of = [&](int id) -> uint32_t {
-    const __nv_bfloat162 x = __float2bfloat162_rn(id >= 0 ? __ldg(&scales[(size_t)id * p.scale_row]) : 0.f);
-    return *reinterpret_cast<const uint32_t*>(&x);
+    return __float_as_uint(id >= 0 ? __ldg(&scales[(size_t)id * p.scale_row]) : 0.f);
   };
   // scales (a lane each) of the tile at hand and of the next, block ids of the one after
   int id2 = -1;
@@ -327,6 +345,8 @@ __device__ __forceinline__ void convert_v(const Params& p, Bars* bars, unsigned 
     if (!__all_sync(0xffffffffu, ok)) break;
     const unsigned char* from = smem + kOffRawV + st * kCodes + ch * 16;
     unsigned char* dst = tile + st * 2 * kVHalf;
+    // a scale is a bf16 as it stands (every power of two is) when its lower half is empty
+    const bool bf16_scales = !__any_sync(0xffffffffu, (sc0 & 0xffffu) != 0u);
     // four rows at a time, read before the first is written (the compiler keeps
     // shared-memory reads behind writes: one by one a row took a latency each)
 #pragma unroll 1
@@ -343,12 +363,22 @@ __device__ __forceinline__ void convert_v(const Params& p, Bars* bars, unsigned 
 #pragma unroll
         for (int i = 0; i < 4; ++i) note_nan(c[i], bars, ch * 16, t * kKT + rr + i * RS, kend);
       }
+      if (!bf16_scales) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = rr + i * RS;
+          const Row16 o = scaled_row(c[i], __uint_as_float(__shfl_sync(0xffffffffu, sc0, r >> bsh)));
+          *reinterpret_cast<uint4*>(dst + r * 128 + ((c0 ^ (r & 7)) << 4)) = o.a;
+          *reinterpret_cast<uint4*>(dst + r * 128 + (((c0 + 1) ^ (r & 7)) << 4)) = o.b;
+        }
+        continue;
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = rr + i * RS;
         const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
         uint32_t o[8];
-        const uint32_t s2 = __shfl_sync(0xffffffffu, sc0, r >> bsh);
+        const uint32_t s2 = __byte_perm(__shfl_sync(0xffffffffu, sc0, r >> bsh), 0u, 0x3232);
 #pragma unroll
         for (int k = 0; k < 4; ++k) codes_to_bf16(w[k], s2, o[2 * k], o[2 * k + 1]);
         *reinterpret_cast<uint4*>(dst + r * 128 + ((c0 ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
