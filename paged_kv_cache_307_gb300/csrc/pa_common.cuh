@@ -236,6 +236,16 @@ template <> struct Elem<fp8e4m3b> : Elem<fp8e4m3> {};
 // to whole 16-byte chunks, so that a row can be moved by bulk copies.
 __host__ __device__ __forceinline__ constexpr int scale_row(int num_kv_heads) { return (num_kv_heads + 3) & ~3; }
 
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// The exponent e by which a query row over e4m3 codes is brought to a common size, m its
+// largest magnitude: m 2^-e in [128, 256), where e4m3 holds it and no sum of products with
+// codes leaves fp32's range, whatever bf16 the query is made of.  (Below m = 2^-113 the
+// elements stay multiples of 2^-13, which the terms of the split still hold.)
+__device__ __forceinline__ int query_exponent(float m) {
+  return m > 0.f && m < INFINITY ? max(-120, min(120, ilogbf(m) - 7)) : 0;
+}
+
 // Warp-collective: the last sequence i < n whose first unit
 //   floor(start[i] / per) + mul * i
 // is not above u, 0 if there is none (start non-decreasing; any other array still

@@ -120,10 +120,25 @@ direct_decode_kernel(const DecodeParams p, const unsigned char* __restrict__ k_c
   if (part >= nparts) return;
   const int t1 = min(L, t0 + p.part_tokens);
   const int ns = (t1 - t0 + STEP - 1) / STEP;
+  // over codes the query's size goes with the block's scale: the products of the two alone may
+  // be past fp32's range where the keys' values bring them back
+  float qf[GT];
 #pragma unroll
-  for (int h = 0; h < GT; ++h)
+  for (int h = 0; h < GT; ++h) {
+    float f = p.qscale;
+    if constexpr (BLK) {
+      float mx = 0.f;
 #pragma unroll
-    for (int e = 0; e < KE; ++e) q[h][e] *= p.qscale;
+      for (int e = 0; e < KE; ++e) mx = fmaxf(mx, fabsf(q[h][e]));
+#pragma unroll
+      for (int off = LPT / 2; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      const int e = query_exponent(mx);
+      f = pow2i(-e);
+      qf[h] = p.qscale * pow2i(e);
+    }
+#pragma unroll
+    for (int e = 0; e < KE; ++e) q[h][e] *= f;
+  }
 
   float m[GT], l[GT], o[GT][KE];
 #pragma unroll
@@ -180,7 +195,8 @@ direct_decode_kernel(const DecodeParams p, const unsigned char* __restrict__ k_c
         }
 #pragma unroll
         for (int off = LPT / 2; off > 0; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
-        s[k][h] = ok[k] ? (BLK ? a * ks[k] : a) : -INFINITY;
+        if constexpr (BLK) a *= qf[h] * ks[k];
+        s[k][h] = ok[k] ? a : -INFINITY;
         if constexpr (W) {
           if (li == 0 && ok[k] && h < gh)
             p.ws_s[((size_t)b * p.Hq + h0 + h) * (size_t)Lmax + token(i, k)] = s[k][h];

@@ -172,13 +172,15 @@ __device__ __noinline__ float plain_score(const DecodeParams& p, int b, int t, i
   if ((unsigned)id >= (unsigned)p.num_blocks) id = 0;
   const uint8_t* k = p.k_codes + (((size_t)id * p.bs + t % p.bs) * p.Hkv + kvh) * D;
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + ((size_t)b * p.Hq + hq) * D;
-  float acc = 0.f;
+  float acc = 0.f, m = 0.f;
+  for (int d = 0; d < D; ++d) m = fmaxf(m, fabsf(__bfloat162float(q[d])));
+  const int e = query_exponent(m);
   for (int d = 0; d < D; ++d) {
     __nv_fp8_e4m3 c;
     c.__x = k[d];
-    acc = fmaf(__bfloat162float(q[d]), static_cast<float>(c), acc);
+    acc = fmaf(__bfloat162float(q[d]) * pow2i(-e), static_cast<float>(c), acc);
   }
-  return acc * (p.qscale * p.k_scale[(size_t)id * p.scale_row + kvh]);
+  return acc * (p.qscale * pow2i(e) * p.k_scale[(size_t)id * p.scale_row + kvh]);
 }
 
 // GT: query heads of the CTA, rounded up (1, 2, 4, 8, 16); HP: KV heads per row
@@ -308,10 +310,10 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
 #pragma unroll
     for (int h = 0; h < GT; ++h) {
       const float m = fmaxf(fmaxf(sh->mx[0][h], sh->mx[1][h]), fmaxf(sh->mx[2][h], sh->mx[3][h]));
-      const int e = m > 0.f && m < INFINITY ? max(-110, min(110, ilogbf(m) - 7)) : 0;
+      const int e = query_exponent(m);
       // (an infinite query has no answer: NaN, as its scores would be)
-      const float x = m < INFINITY ? q[h] * __uint_as_float((uint32_t)(127 - e) << 23) : NAN;
-      qf[h] = p.qscale * __uint_as_float((uint32_t)(127 + e) << 23);
+      const float x = m < INFINITY ? q[h] * pow2i(-e) : NAN;
+      qf[h] = p.qscale * pow2i(e);
       const uint32_t hi = e4m3x2(x, 0.f);
       float back, none;
       from_e4m3x2(hi, back, none);

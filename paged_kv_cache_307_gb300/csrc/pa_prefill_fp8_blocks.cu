@@ -104,7 +104,13 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const Params p) {
   const int pos = L - (r1 - r0) + (row - r0);
   const int h = hq / p.G;
   const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) + ((size_t)row * p.Hq + hq) * D;
-  for (int d = lane; d < D; d += 32) qs[warp][d] = __bfloat162float(qrow[d]) * p.qscale;
+  float qmax = 0.f;
+  for (int d = lane; d < D; d += 32) qmax = fmaxf(qmax, fabsf(__bfloat162float(qrow[d])));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, off));
+  const int qe = query_exponent(qmax);
+  const float rowf = p.qscale * pow2i(qe);
+  for (int d = lane; d < D; d += 32) qs[warp][d] = __bfloat162float(qrow[d]) * pow2i(-qe);
   __syncwarp();
   float m = -INFINITY, l = 0.f, o[DPL];
 #pragma unroll
@@ -130,7 +136,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const Params p) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc = fmaf(qs[warp][16 * c + e], f[e], acc);
       }
-      s = acc * __ldg(&p.k_scale[(size_t)blk * p.scale_row + h]);
+      s = acc * (rowf * __ldg(&p.k_scale[(size_t)blk * p.scale_row + h]));
       vs = __ldg(&p.v_scale[(size_t)blk * p.scale_row + h]);
     }
     float mx = s;
@@ -194,6 +200,7 @@ struct Bars {
   // t & 3: those of t+1 to t+3 may be written while the softmax reads t's, t+4's
   // only after P_t (its K stage waits for S_{t+1}, which is issued after P_t)
   alignas(16) float kscl[4][kKT / 4];
+  float kup[4];                          // what tile t's scales are to be multiplied by: 1, or 2^32
   // first key whose V is NaN, of every head dim, and whether there is any
   int nan_key[128];
   int any_nan;
@@ -544,8 +551,13 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
       __syncwarp();
       if (lane < nb) tma_load_4d(smem + kOffK + ks * kCodes + lane * box, &mapK, &bars->full_k[ks], 0, kvh, 0, id, pol);
       issued_k = t + 1;
-      // a scale of 0 as a tiny one: the scores are 0 all the same, and a masked -inf stays one
-      bars->kscl[t & 3][lane] = fmaxf(__shfl_sync(0xffffffffu, sc, (4 * lane) >> bsh), 1e-37f);
+      // a scale of 0 as the tiniest one: the scores are 0 all the same, and a masked -inf stays one;
+      // a tile with scales so large that their products with raw scores (up to 2^24) could be past
+      // fp32's range, where small queries bring them back, holds them times 2^-32
+      const bool big = __any_sync(0xffffffffu, sc > 0x1p96f);
+      const float ks4 = __shfl_sync(0xffffffffu, sc, (4 * lane) >> bsh) * (big ? 0x1p-32f : 1.f);
+      bars->kscl[t & 3][lane] = fmaxf(ks4, __uint_as_float(1u));
+      if (lane == 0) bars->kup[t & 3] = big ? 0x1p32f : 1.f;
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&bars->scl_full[t & 3]);
@@ -662,10 +674,10 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
 #pragma unroll
         for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(f[e]));
       }
-      const int qe = mx > 0.f && mx < INFINITY ? max(-110, min(110, ilogbf(mx) - 7)) : 0;
+      const int qe = query_exponent(mx);
       // (an infinite query has no answer: NaN, as its scores would be)
-      const float down = mx < INFINITY ? __uint_as_float((uint32_t)(127 - qe) << 23) : NAN;
-      rowf = fmaxf(p.qscale * __uint_as_float((uint32_t)(127 + qe) << 23), FLT_MIN);
+      const float down = mx < INFINITY ? pow2i(-qe) : NAN;
+      rowf = fmaxf(p.qscale * pow2i(qe), FLT_MIN);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {                // 16 head dims
         float f[16];
@@ -702,6 +714,7 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
       const float4* ks4 = reinterpret_cast<const float4*>(bars->kscl[t & 3]) + 4 * g;   // 16 keys' scales each
       const bool partial = k0 + kStep - 1 > pos;
       // maximum of the row's scaled scores, 32 keys at a time
+      const float rf = rowf * bars->kup[t & 3];
       float mx = -INFINITY;
       uint32_t buf[2][32];
       tmem_ld32(tP, buf[0]);
@@ -729,7 +742,7 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
           mx = fmax3(fmax3(mx, a[0], a[1]), a[2], a[3]);
         }
       }
-      mx *= rowf;
+      mx *= rf;
       const bool need = mx > m_ref + kRescaleThreshold;
       const float alpha = need ? exp2f(m_ref - mx) : 1.f;
       if (need) m_ref = mx;
@@ -764,7 +777,7 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
           const float4 k4 = ks4[2 * c + (i >> 3)];
           const int q = (i >> 1) & 3;
           // (above 0: a masked score is -inf, and -inf * 0 is NaN)
-          const float f = fmaxf(rowf * (q == 0 ? k4.x : q == 1 ? k4.y : q == 2 ? k4.z : k4.w), FLT_MIN);
+          const float f = fmaxf(rf * (q == 0 ? k4.x : q == 1 ? k4.y : q == 2 ? k4.z : k4.w), FLT_MIN);
           float x0, x1;
           f2unpack(ffma2(f2pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2pack(f, f), nm2), x0, x1);
           const float p0 = ex2_f32(x0), p1 = ex2_f32(x1);
