@@ -107,25 +107,42 @@ bool encode_map(CUtensorMap* map, const void* base, pa_dtype dt, int rank, const
 
 }  // namespace pa
 
+// Takes every unit's status word and leaves what they held in g_status_taken: one
+// kernel and one read, where a blocking read a unit took 108 us for twelve.
+constexpr int kUnits = 12;
+struct StatusWords {
+  unsigned* word[kUnits];
+};
+static __device__ unsigned g_status_taken;
+static __global__ void __launch_bounds__(32) take_status_kernel(const StatusWords w) {
+  unsigned v = threadIdx.x < kUnits ? atomicExch(w.word[threadIdx.x], 0u) : 0u;
+  v = __reduce_or_sync(0xffffffffu, v);
+  if (threadIdx.x == 0) g_status_taken = v;
+}
+
 extern "C" int pa_last_error(void) {
   if (cudaDeviceSynchronize() != cudaSuccess) return PA_ERR_CUDA;
-  const unsigned a = pa::fetch_status_cache_ops();
-  const unsigned b0 = pa::fetch_status_decode(), b1 = pa::fetch_status_decode_fp8(), b2 = pa::fetch_status_shared();
-  const unsigned b = (b0 == 0xffffffffu || b1 == 0xffffffffu || b2 == 0xffffffffu) ? 0xffffffffu : (b0 | b1 | b2);
-  const unsigned c = pa::fetch_status_prefill();
-  const unsigned d = pa::fetch_status_selftest();
-  if (a == 0xffffffffu || b == 0xffffffffu || c == 0xffffffffu || d == 0xffffffffu) return PA_ERR_CUDA;
-  unsigned all = a | b | c | d;
-  // the block-scaled e4m3 cache and the eviction units
-  unsigned (*const more[])() = {pa::fetch_status_fp8_blocks, pa::fetch_status_decode_fp8_blocks,
-                                pa::fetch_status_decode_weights, pa::fetch_status_decode_weights_fp8,
-                                pa::fetch_status_prefill_fp8_blocks, pa::fetch_status_evict};
-  for (auto fetch : more) {
-    const unsigned v = fetch();
-    if (v == 0xffffffffu) return PA_ERR_CUDA;
-    all |= v;
-  }
-  return (int)all;
+  const StatusWords w = {{
+      pa::status_word_cache_ops(),
+      pa::status_word_decode(),
+      pa::status_word_decode_fp8(),
+      pa::status_word_decode_fp8_blocks(),
+      pa::status_word_decode_weights(),
+      pa::status_word_decode_weights_fp8(),
+      pa::status_word_fp8_blocks(),
+      pa::status_word_prefill_fp8_blocks(),
+      pa::status_word_evict(),
+      pa::status_word_shared(),
+      pa::status_word_prefill(),
+      pa::status_word_selftest(),
+  }};
+  for (unsigned* p : w.word)
+    if (!p) return PA_ERR_CUDA;
+  take_status_kernel<<<1, 32>>>(w);
+  unsigned v = 0;
+  if (cudaGetLastError() != cudaSuccess || cudaMemcpyFromSymbol(&v, g_status_taken, sizeof(v)) != cudaSuccess)
+    return PA_ERR_CUDA;
+  return (int)v;
 }
 
 extern "C" const char* pa_strerror(int code) {

@@ -188,12 +188,7 @@ static bool copyable_block(int block_size, int heads, int dim, pa_dtype dt) {
   return bytes % 16 == 0 && bytes <= (1ll << 30);
 }
 
-unsigned fetch_status_cache_ops() {
-  unsigned v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_status_cache, sizeof(v)) != cudaSuccess) return 0xffffffffu;
-  if (v && cudaMemcpyToSymbol(g_status_cache, &zero, sizeof(zero)) != cudaSuccess) return 0xffffffffu;
-  return v;
-}
+unsigned* status_word_cache_ops() { return device_word(g_status_cache); }
 
 }  // namespace pa
 

@@ -4,7 +4,7 @@
 // TMA tensor loads (cp.async.bulk.tensor) completing on an mbarrier, and a
 // bounded wait that gives up after a wall-clock limit instead of spinning
 // forever.  Every translation unit keeps its own sticky status word and
-// exposes a host function that fetches and clears it.
+// exposes a host function that gives its address.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -309,18 +309,23 @@ bool raise_smem_limit(const void* kernel, int dev);
 // runtime does not accept the attribute.
 cudaError_t launch_after(const void* kernel, dim3 grid, dim3 block, void** args, cudaStream_t stream);
 
-// Per-translation-unit status fetch (returns the sticky word and clears it).
-unsigned fetch_status_cache_ops();
-unsigned fetch_status_decode();
-unsigned fetch_status_decode_fp8();
-unsigned fetch_status_decode_fp8_blocks();
-unsigned fetch_status_decode_weights();
-unsigned fetch_status_decode_weights_fp8();
-unsigned fetch_status_fp8_blocks();
-unsigned fetch_status_prefill_fp8_blocks();
-unsigned fetch_status_evict();
-unsigned fetch_status_shared();
-unsigned fetch_status_prefill();
-unsigned fetch_status_selftest();
+// Host: the current device's address of a translation unit's sticky status word, null on failure.
+template <typename T>
+inline unsigned* device_word(const T& symbol) {
+  void* p = nullptr;
+  return cudaGetSymbolAddress(&p, symbol) == cudaSuccess ? static_cast<unsigned*>(p) : nullptr;
+}
+unsigned* status_word_cache_ops();
+unsigned* status_word_decode();
+unsigned* status_word_decode_fp8();
+unsigned* status_word_decode_fp8_blocks();
+unsigned* status_word_decode_weights();
+unsigned* status_word_decode_weights_fp8();
+unsigned* status_word_fp8_blocks();
+unsigned* status_word_prefill_fp8_blocks();
+unsigned* status_word_evict();
+unsigned* status_word_shared();
+unsigned* status_word_prefill();
+unsigned* status_word_selftest();
 
 }  // namespace pa

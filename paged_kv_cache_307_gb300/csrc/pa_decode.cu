@@ -217,12 +217,7 @@ cudaError_t launch_dependent(const void* kernel, dim3 grid, dim3 block, void** a
   return cudaLaunchKernel(kernel, grid, block, args, smem, stream);
 }
 
-unsigned fetch_status_decode() {
-  unsigned v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_status_decode, sizeof(v)) != cudaSuccess) return 0xffffffffu;
-  if (v && cudaMemcpyToSymbol(g_status_decode, &zero, sizeof(zero)) != cudaSuccess) return 0xffffffffu;
-  return v;
-}
+unsigned* status_word_decode() { return device_word(g_status_decode); }
 
 }  // namespace pa
 

@@ -53,11 +53,6 @@ Launch pick_decode_fp8(int head_dim, int gt, int hg, bool mma) {
   return pick_gt<128>(gt, hg);
 }
 
-unsigned fetch_status_decode_fp8() {
-  unsigned v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_status_decode, sizeof(v)) != cudaSuccess) return 0xffffffffu;
-  if (v && cudaMemcpyToSymbol(g_status_decode, &zero, sizeof(zero)) != cudaSuccess) return 0xffffffffu;
-  return v;
-}
+unsigned* status_word_decode_fp8() { return device_word(g_status_decode); }
 
 }  // namespace pa

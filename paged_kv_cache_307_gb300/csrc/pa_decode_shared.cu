@@ -1185,12 +1185,7 @@ SharedPlan shared_plan(int num_seqs, int num_heads, int num_kv_heads, int head_d
 
 }  // namespace
 
-unsigned fetch_status_shared() {
-  unsigned v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_status_shared, sizeof(v)) != cudaSuccess) return 0xffffffffu;
-  if (v && cudaMemcpyToSymbol(g_status_shared, &zero, sizeof(zero)) != cudaSuccess) return 0xffffffffu;
-  return v;
-}
+unsigned* status_word_shared() { return device_word(g_status_shared); }
 
 }  // namespace pa
 

@@ -50,11 +50,6 @@ Launch pick_decode_weights(bool f32, int head_dim, int gt) {
   return f32 ? pick_d<float>(head_dim, gt) : pick_d<B16>(head_dim, gt);
 }
 
-unsigned fetch_status_decode_weights() {
-  unsigned v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_status_decode, sizeof(v)) != cudaSuccess) return 0xffffffffu;
-  if (v && cudaMemcpyToSymbol(g_status_decode, &zero, sizeof(zero)) != cudaSuccess) return 0xffffffffu;
-  return v;
-}
+unsigned* status_word_decode_weights() { return device_word(g_status_decode); }
 
 }  // namespace pa

@@ -50,11 +50,6 @@ Launch pick_decode_weights_fp8_tc(int head_dim, int gt, size_t* smem) {
   return pick_tc_gt<1>(gt, smem);
 }
 
-unsigned fetch_status_decode_weights_fp8() {
-  unsigned v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_status_decode, sizeof(v)) != cudaSuccess) return 0xffffffffu;
-  if (v && cudaMemcpyToSymbol(g_status_decode, &zero, sizeof(zero)) != cudaSuccess) return 0xffffffffu;
-  return v;
-}
+unsigned* status_word_decode_weights_fp8() { return device_word(g_status_decode); }
 
 }  // namespace pa

@@ -530,12 +530,7 @@ Layout layout(int B, int Hkv, int max_blocks, int bs, int budget) {
 
 }  // namespace
 
-unsigned fetch_status_evict() {
-  unsigned v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_status_evict, sizeof(v)) != cudaSuccess) return 0xffffffffu;
-  if (v && cudaMemcpyToSymbol(g_status_evict, &zero, sizeof(zero)) != cudaSuccess) return 0xffffffffu;
-  return v;
-}
+unsigned* status_word_evict() { return device_word(g_status_evict); }
 
 }  // namespace pa
 

@@ -233,12 +233,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(const AppendPara
 
 }  // namespace
 
-unsigned fetch_status_fp8_blocks() {
-  unsigned v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_status_fp8_blocks, sizeof(v)) != cudaSuccess) return 0xffffffffu;
-  if (v && cudaMemcpyToSymbol(g_status_fp8_blocks, &zero, sizeof(zero)) != cudaSuccess) return 0xffffffffu;
-  return v;
-}
+unsigned* status_word_fp8_blocks() { return device_word(g_status_fp8_blocks); }
 
 }  // namespace pa
 

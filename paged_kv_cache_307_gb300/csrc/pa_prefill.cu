@@ -539,12 +539,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__
 
 }  // namespace
 
-unsigned fetch_status_prefill() {
-  unsigned v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_status_prefill, sizeof(v)) != cudaSuccess) return 0xffffffffu;
-  if (v && cudaMemcpyToSymbol(g_status_prefill, &zero, sizeof(zero)) != cudaSuccess) return 0xffffffffu;
-  return v;
-}
+unsigned* status_word_prefill() { return device_word(g_status_prefill); }
 
 }  // namespace pa
 

@@ -861,12 +861,7 @@ tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CU
 
 }  // namespace
 
-unsigned fetch_status_prefill_fp8_blocks() {
-  unsigned v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_status_prefill_fp8, sizeof(v)) != cudaSuccess) return 0xffffffffu;
-  if (v && cudaMemcpyToSymbol(g_status_prefill_fp8, &zero, sizeof(zero)) != cudaSuccess) return 0xffffffffu;
-  return v;
-}
+unsigned* status_word_prefill_fp8_blocks() { return device_word(g_status_prefill_fp8); }
 
 }  // namespace pa
 

@@ -26,12 +26,7 @@ __global__ void __launch_bounds__(32) bounded_wait_kernel(unsigned long long lim
 
 }  // namespace
 
-unsigned fetch_status_selftest() {
-  unsigned v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_status_selftest, sizeof(v)) != cudaSuccess) return 0xffffffffu;
-  if (v && cudaMemcpyToSymbol(g_status_selftest, &zero, sizeof(zero)) != cudaSuccess) return 0xffffffffu;
-  return v;
-}
+unsigned* status_word_selftest() { return device_word(g_status_selftest); }
 
 }  // namespace pa
 
