@@ -332,7 +332,9 @@ int pa_decode_fp8(void* out, const void* query,
  *           become e4m3(value(code) * old_scale / s)
  *
  * Powers of two make x / s exact and a raised scale exact for every code whose
- * value stays a normal one, so the tokens' split into calls hardly shows.
+ * value stays a normal one, so the tokens' split into calls hardly shows.  (Under a
+ * scale of the caller's own that is no power of two, x / s is off by 2^-23 of itself
+ * before it is rounded to a code.)
  * A NaN gives a NaN code; an infinity gives +-448 codes, or NaN codes where the
  * block's head holds nothing that is finite and not zero.
  *

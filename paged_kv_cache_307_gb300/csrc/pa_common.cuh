@@ -277,6 +277,8 @@ constexpr long long kMaxRowTokens = 1ll << 30;
 inline bool supported_head_dim(int d) { return d == 32 || d == 64 || d == 128; }
 inline bool supported_block_size(int bs) { return bs == 4 || bs == 8 || bs == 16 || bs == 32; }
 
+// GB300's SMs, for the sizing functions that make no CUDA call.
+constexpr int kTunedSms = 152;
 // Host: number of SMs on the current device (cached per device).
 int device_sm_count();
 

@@ -59,7 +59,7 @@ int partition_of(Form form, int num_seqs, int num_heads, int num_kv_heads, int h
                                : (long long)num_seqs * num_kv_heads * ((G + 3) / 4);
     const int least = tc ? 512 : 64;
     P = tc ? 2048 : 512;
-    while (P > least && items * max_ctx < (tc ? 2ll : 4ll) * 152 * P) P /= 2;
+    while (P > least && items * max_ctx < (tc ? 2ll : 4ll) * kTunedSms * P) P /= 2;
   }
   return P >= max_ctx ? max_ctx : P;
 }
@@ -188,7 +188,7 @@ int launch_weights(const Launch& L, const DecodeParams& prm, const WeightsArgs& 
   const long long max_ctx = (long long)p.max_blocks * p.bs;
   // one wave of CTAs at the table's capacity (eight fit an SM) where the chunks allow it
   const long long all = (long long)p.B * p.Hkv * ((max_ctx + kWeightTokens - 1) / kWeightTokens);
-  int chunks = (int)(all / (8 * 152));
+  int chunks = (int)(all / (8 * device_sm_count()));
   chunks = chunks < 1 ? 1 : chunks > 8 ? 8 : chunks;
   const long long span = (long long)chunks * kWeightTokens;
   const long long ctas = merge_ctas + (long long)p.B * p.Hkv * ((max_ctx + span - 1) / span);

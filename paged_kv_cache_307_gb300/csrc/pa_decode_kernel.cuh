@@ -1724,7 +1724,8 @@ __global__ void __launch_bounds__(kFinishThreads) merge_wide_kernel(const Decode
 // of totals per KV head and token; of the 130 us that 64 e4m3 requests x 8 KV heads
 // (groups of 4) over U[1024, 8192] take with their weights, 16 are this.
 constexpr int kWeightTokens = 4 * kFinishThreads;
-// 2^x for x <= 0, what is below 2^-126 as 0.
+// 2^x, what is below 2^-126 as 0.  (x <= 3: M is the reference of a row's states, which may lag
+// its largest score by kTcSlack, and l is a sum over the same reference.)
 __device__ __forceinline__ float ex2_ftz(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

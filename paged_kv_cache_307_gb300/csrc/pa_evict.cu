@@ -569,8 +569,8 @@ extern "C" int pa_evict(void* k_cache, void* v_cache, float* k_scale, float* v_s
   // destination blocks per CTA of the second kernel: a warp has one while the
   // (sequence, head) rows alone do not fill the SMs, four otherwise (32 rows 37 us
   // against 48 with four, 512 rows 28 with one against 22.5)
-  const int rows = num_seqs * num_kv_heads;
-  const int per = rows >= 2 * 152 ? 4 * kMoveWarps : kMoveWarps;
+  const int rows = num_seqs * num_kv_heads, sms = device_sm_count();
+  const int per = rows >= 2 * sms ? 4 * kMoveWarps : kMoveWarps;
   const long long blocks = (long long)rows * ((l.nb + per - 1) / per);
   if (blocks > 0x7fffffffll) return PA_ERR_SHAPE;
   EvictParams p;
@@ -611,7 +611,7 @@ extern "C" int pa_evict(void* k_cache, void* v_cache, float* k_scale, float* v_s
   // 65 against 86), or a cluster of four of them while the rows leave SMs idle (64 rows of 16384 slots 36 us
   // against 46, 32 of 6000 22 against 24; but 128 of 16384 73 against 65) and where a CTA's shared memory
   // does not hold the keys.
-  const bool tall = max_ctx > 2048, wide = tall && (rows * kCluster <= 2 * 152 || max_ctx > kMaxSmemKeys);
+  const bool tall = max_ctx > 2048, wide = tall && (rows * kCluster <= 2 * sms || max_ctx > kMaxSmemKeys);
   const int cs = wide ? kCluster : 1;
   const long long slots = wide ? ((max_ctx + cs - 1) / cs + 31) / 32 * 32 : max_ctx;    // of a CTA
   const bool in_smem = slots <= kMaxSmemKeys;

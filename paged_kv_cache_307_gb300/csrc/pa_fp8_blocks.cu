@@ -14,10 +14,11 @@
 // what one filled at once holds, up to those.
 //
 // One warp per (touched block, head): the block's new rows of the head, K's and V's,
-// 16 bytes per lane, are read once and stay in registers from the maximum to the
-// codes (sixteen loads in flight per lane).  Blocks are owned by one warp each, so
-// nothing is atomic.  Which block a warp works on needs no scan over the
-// sequences: sequence b's units start at
+// 16 bytes per lane, stay in registers from the maximum to the codes as far as 16
+// chunks a lane reach (sixteen loads in flight: all of a bf16 block of 16 x 128); of
+// larger blocks (f32, or 32 tokens) the rest is read a second time, out of the caches.
+// Blocks are owned by one warp each, so nothing is atomic.  Which block a warp works on
+// needs no scan over the sequences: sequence b's units start at
 //   U_b = floor(query_start[b] / bs) + 2 b,
 // and n tokens touch at most floor((n - 1) / bs) + 2 blocks, which never passes
 // U_{b+1}; a search over query_start finds b, and surplus units leave.
