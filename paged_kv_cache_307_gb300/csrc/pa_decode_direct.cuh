@@ -80,7 +80,7 @@ direct_decode_kernel(const DecodeParams p, const unsigned char* __restrict__ k_c
   constexpr int STEP = kDirectWarps * kU * TPW;         // tokens of a CTA step
   constexpr bool BLK = std::is_same<KT, fp8e4m3b>::value;
   static_assert(LPT >= 4 && LPT <= 32, "lane split");
-  __shared__ float so[kDirectWarps][GT][D], sm[kDirectWarps][GT], sl[kDirectWarps][GT];
+  __shared__ float so[kDirectWarps][GT][D], sm[kDirectWarps][GT], sl[kDirectWarps][GT], up[kDirectWarps][GT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = lane / LPT, li = lane % LPT;
   asm volatile("griddepcontrol.launch_dependents;");
@@ -120,25 +120,36 @@ direct_decode_kernel(const DecodeParams p, const unsigned char* __restrict__ k_c
   if (part >= nparts) return;
   const int t1 = min(L, t0 + p.part_tokens);
   const int ns = (t1 - t0 + STEP - 1) / STEP;
-  // over codes the query's size goes with the block's scale: the products of the two alone may
-  // be past fp32's range where the keys' values bring them back
-  float qf[GT];
+  // Over codes, a query past 2^64 or below 2^-64 has its size go with the block's scale: its sums of
+  // products with codes may be past fp32's range where the scale brings them back.  (Every query:
+  // 3 % more, a product a token and head.)
+  bool far = false;
+  if constexpr (BLK) {
+    float mx[GT];
 #pragma unroll
-  for (int h = 0; h < GT; ++h) {
-    float f = p.qscale;
-    if constexpr (BLK) {
-      float mx = 0.f;
+    for (int h = 0; h < GT; ++h) {
+      mx[h] = 0.f;
 #pragma unroll
-      for (int e = 0; e < KE; ++e) mx = fmaxf(mx, fabsf(q[h][e]));
+      for (int e = 0; e < KE; ++e) mx[h] = fmaxf(mx[h], fabsf(q[h][e]));
 #pragma unroll
-      for (int off = LPT / 2; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-      const int e = query_exponent(mx);
-      f = pow2i(-e);
-      qf[h] = p.qscale * pow2i(e);
+      for (int off = LPT / 2; off > 0; off >>= 1) mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], off));
+      far = far || mx[h] > 0x1p64f || (mx[h] > 0.f && mx[h] < 0x1p-64f);
     }
+    if (far) {
 #pragma unroll
-    for (int e = 0; e < KE; ++e) q[h][e] *= f;
+      for (int h = 0; h < GT; ++h) {
+        const int x = query_exponent(mx[h]);
+#pragma unroll
+        for (int e = 0; e < KE; ++e) q[h][e] *= pow2i(-x);
+        if (lane == 0) up[warp][h] = pow2i(x);
+      }
+    }
+    __syncwarp();
   }
+#pragma unroll
+  for (int h = 0; h < GT; ++h)
+#pragma unroll
+    for (int e = 0; e < KE; ++e) q[h][e] *= p.qscale;
 
   float m[GT], l[GT], o[GT][KE];
 #pragma unroll
@@ -195,8 +206,25 @@ direct_decode_kernel(const DecodeParams p, const unsigned char* __restrict__ k_c
         }
 #pragma unroll
         for (int off = LPT / 2; off > 0; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
-        if constexpr (BLK) a *= qf[h] * ks[k];
-        s[k][h] = ok[k] ? a : -INFINITY;
+        s[k][h] = a;
+      }
+    }
+    if (BLK && far) {
+#pragma unroll
+      for (int k = 0; k < kU; ++k)
+#pragma unroll
+        for (int h = 0; h < GT; ++h) s[k][h] *= ks[k] * up[warp][h];
+    } else if constexpr (BLK) {
+#pragma unroll
+      for (int k = 0; k < kU; ++k)
+#pragma unroll
+        for (int h = 0; h < GT; ++h) s[k][h] *= ks[k];
+    }
+#pragma unroll
+    for (int k = 0; k < kU; ++k) {
+#pragma unroll
+      for (int h = 0; h < GT; ++h) {
+        s[k][h] = ok[k] ? s[k][h] : -INFINITY;
         if constexpr (W) {
           if (li == 0 && ok[k] && h < gh)
             p.ws_s[((size_t)b * p.Hq + h0 + h) * (size_t)Lmax + token(i, k)] = s[k][h];

@@ -15,7 +15,10 @@
 //    exactly: the split is exact down to 2^-13 of the largest, and within 2^-20 of it below.
 //    (lo in e4m3 ends at 2^-9, so it dropped what is below 2^-17 of the largest.)  K's
 //    scales stay apart, in the softmax.
-//  * P V runs in bf16.  V's codes come by TMA into a stage of their own; warps 8-11
+//  * P V runs in bf16: a weight is off by at most 2^-8 of itself, either way, so that the
+//    output's error against 64 bits is 0.0023 of it where the last rounding alone makes
+//    0.0017.  (bf16 has fp32's range: no weight is lost.  8-bit terms of P, as in
+//    decode, would be three products of the larger kind.)  V's codes come by TMA into a stage of their own; warps 8-11
 //    widen them (codes_to_bf16), multiply their scale in (one rounding to bf16, none for a
 //    power of two; bf16 has the exponents for it, so a row that attends only to blocks of
 //    small scale keeps its precision beside blocks of large scale) and write the 128-byte-swizzled
@@ -33,9 +36,9 @@
 //    queries.  One issuing warp for both tiles: 8 % more on top, its waits in a row.)
 //  * What bounds it: a step of a query tile is a chain of softmax, P V, S and the waits
 //    between them, and the MMAs' operands take most of the shared memory's bandwidth.
-//    8 chunks of 512 queries x 32 heads (8 KV heads) over U[1024, 4096] take 168 us
-//    (921 TFLOP/s, 48 % of the library's bf16 rate); a mixed round of 16 sequences with
-//    1 to 100 new tokens each 45.
+//    8 chunks of 512 queries x 32 heads (8 KV heads) over U[1024, 4096] take 170 us
+//    (910 TFLOP/s, 48 % of the library's bf16 rate); a mixed round of 16 sequences with
+//    1 to 100 new tokens each 43 to 45.  The softmax spills 136 bytes at 128 registers.
 //  * Keys at or past the context length have P = 0, and in the V tile they are finite
 //    whatever the pool holds: a NaN code comes out finite, a block past the context with
 //    a scale of 0.  A NaN of a key in the context has to reach the rows at and past it
