@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from _bounded import Case, check, reference
+from test_gpu_bounded import _totals
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +57,20 @@ def test_prefill(pa, Hq, Hkv, D, bs, power):
     pa.prefill_fp8_blocks(out, c.q, start.cuda(), c.k, c.v, c.ks, c.vs, c.tab, c.lens, c.scale)
     assert pa.last_error() == 0
     check(out, ref, tol)
+
+
+@pytest.mark.parametrize("power", [124, -120])
+@pytest.mark.parametrize("Hq,Hkv,D,bs", SHAPES + [(9, 3, 64, 16)])
+def test_heads_of_one_group_far_apart(pa, Hq, Hkv, D, bs, power):
+    """Every other query head at an ordinary size: its scores go to nothing, or far apart, beside the others'."""
+    c = _case(Hq, Hkv, D, bs, [200, 33], power)
+    c.q[:, 1::2] *= 2.0 ** (-power if power > 0 else 0)
+    ref, tol = reference(c)
+    start = torch.zeros(2, Hkv, c.tab.shape[1] * bs)
+    wref, wtol = _totals(c, start)
+    c.cuda()
+    out, w = torch.full_like(c.q, float("nan")), start.cuda()
+    pa.decode_weights(out, w, c.q, c.k, c.v, c.tab, c.lens, c.scale, k_scale=c.ks, v_scale=c.vs)
+    assert pa.last_error() == 0
+    check(out, ref, tol)
+    check(w, wref, wtol)
