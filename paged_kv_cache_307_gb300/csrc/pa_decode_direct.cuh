@@ -16,8 +16,12 @@
 // 5 requests x 4 KV heads of head_dim 64 (f32, groups of 3) of up to 700 tokens take
 // 10 us on the GPU with their weights, 41 through the TMA ring of decode_kernel, whose
 // fill such contexts never repay; 32 x 8 heads of 128 over U[128, 4096]: bf16 in
-// groups of 7 163 us against 140, so at large batches the ring is 15 % ahead: what is
-// bound there is the issue of the CUDA-core products.
+// groups of 7 163 us against 140, so at large batches the ring is 15 % ahead.
+// What bounds large calls: over e4m3, instruction issue (35 requests x 21 heads of 64 in
+// groups of 3, 106 us: 0.67 a cycle and scheduler, widening and shuffles beside the
+// products); over f32 in large groups the latency of loads (18 requests x 4 heads of 128
+// in groups of 16, 622 to 632 us: issue 0.38, waiting for memory the top stall, DRAM 7 %
+// busy: the four CTAs of a group each read K and V, three of them from L2).
 #pragma once
 
 #include "pa_decode_kernel.cuh"
