@@ -138,9 +138,14 @@ extern "C" int pa_last_error(void) {
   }};
   for (unsigned* p : w.word)
     if (!p) return PA_ERR_CUDA;
-  take_status_kernel<<<1, 32>>>(w);
+  // one caller at a time between the kernel and the read: another's kernel would write over the word
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lk(mu);
+  void* args[] = {const_cast<StatusWords*>(&w)};
   unsigned v = 0;
-  if (cudaGetLastError() != cudaSuccess || cudaMemcpyFromSymbol(&v, g_status_taken, sizeof(v)) != cudaSuccess)
+  if (cudaLaunchKernel(reinterpret_cast<const void*>(&take_status_kernel), dim3(1), dim3(32), args, 0, nullptr) !=
+          cudaSuccess ||
+      cudaMemcpyFromSymbol(&v, g_status_taken, sizeof(v)) != cudaSuccess)
     return PA_ERR_CUDA;
   return (int)v;
 }

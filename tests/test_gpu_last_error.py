@@ -89,3 +89,17 @@ def test_looking_costs_one_read_of_the_device(pa):
     torch.cuda.synchronize()
     pa.last_error()
     assert _median_us(pa.last_error) < 5 * _median_us(x.item)
+
+
+def test_two_threads_looking_at_once_lose_no_condition(pa):
+    from concurrent.futures import ThreadPoolExecutor
+    c = Case("bf16", [40, 40], 8, 2, 128, 16).cuda()
+    bad = c.tab.clone()
+    bad[1, 1] = -5
+    out = torch.empty_like(c.q)
+    with ThreadPoolExecutor(2) as two:
+        for _ in range(300):
+            pa.decode(out, c.q, c.k, c.v, bad, c.lens, c.scale)
+            torch.cuda.synchronize()
+            a, b = two.submit(pa.last_error), two.submit(pa.last_error)
+            assert a.result() | b.result() == pa.DEV_BAD_BLOCK
