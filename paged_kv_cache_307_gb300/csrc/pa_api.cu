@@ -16,6 +16,7 @@ void note_host_error(const char* what) { snprintf(g_host_msg, sizeof(g_host_msg)
 
 bool ck(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return true;
+  (void)cudaGetLastError();        // reported here: a later call's launch check is not to find it again
   snprintf(g_host_msg, sizeof(g_host_msg), "%s: %s", what, cudaGetErrorString(e));
   return false;
 }
@@ -121,7 +122,7 @@ static __global__ void __launch_bounds__(32) take_status_kernel(const StatusWord
 }
 
 extern "C" int pa_last_error(void) {
-  if (cudaDeviceSynchronize() != cudaSuccess) return PA_ERR_CUDA;
+  if (!pa::ck(cudaDeviceSynchronize(), "cudaDeviceSynchronize")) return PA_ERR_CUDA;
   const StatusWords w = {{
       pa::status_word_cache_ops(),
       pa::status_word_decode(),
@@ -143,9 +144,9 @@ extern "C" int pa_last_error(void) {
   std::lock_guard<std::mutex> lk(mu);
   void* args[] = {const_cast<StatusWords*>(&w)};
   unsigned v = 0;
-  if (cudaLaunchKernel(reinterpret_cast<const void*>(&take_status_kernel), dim3(1), dim3(32), args, 0, nullptr) !=
-          cudaSuccess ||
-      cudaMemcpyFromSymbol(&v, g_status_taken, sizeof(v)) != cudaSuccess)
+  if (!pa::ck(cudaLaunchKernel(reinterpret_cast<const void*>(&take_status_kernel), dim3(1), dim3(32), args, 0, nullptr),
+              "cudaLaunchKernel(take_status_kernel)") ||
+      !pa::ck(cudaMemcpyFromSymbol(&v, g_status_taken, sizeof(v)), "cudaMemcpyFromSymbol"))
     return PA_ERR_CUDA;
   return (int)v;
 }

@@ -297,7 +297,8 @@ bool pool_map(CUtensorMap* out, const void* base, pa_dtype dt, int nb, int bs, i
 // Host: record the text of the last host-side failure (per thread); read
 // back through pa_last_host_error().
 void note_host_error(const char* what);
-// Host: true if `e` is cudaSuccess, otherwise records "<what>: <error>".
+// Host: true if `e` is cudaSuccess, otherwise records "<what>: <error>" and clears the
+// runtime's last error.
 bool ck(cudaError_t e, const char* what);
 // Host: raise `kernel`'s dynamic shared-memory limit to the device opt-in
 // maximum (once per kernel and device).
@@ -315,7 +316,7 @@ cudaError_t launch_after(const void* kernel, dim3 grid, dim3 block, void** args,
 template <typename T>
 inline unsigned* device_word(const T& symbol) {
   void* p = nullptr;
-  return cudaGetSymbolAddress(&p, symbol) == cudaSuccess ? static_cast<unsigned*>(p) : nullptr;
+  return ck(cudaGetSymbolAddress(&p, symbol), "cudaGetSymbolAddress") ? static_cast<unsigned*>(p) : nullptr;
 }
 unsigned* status_word_cache_ops();
 unsigned* status_word_decode();

@@ -103,3 +103,18 @@ def test_two_threads_looking_at_once_lose_no_condition(pa):
             torch.cuda.synchronize()
             a, b = two.submit(pa.last_error), two.submit(pa.last_error)
             assert a.result() | b.result() == pa.DEV_BAD_BLOCK
+
+
+def test_an_error_is_reported_once(pa):
+    """A call that fails in CUDA (here: waiting for the device inside a capture, which ends the capture) leaves no
+    error behind for the calls after it."""
+    e = Case("e4m3", [40, 40], 8, 2, 128, 16).cuda()
+    new = torch.zeros(2, 2, 128, dtype=torch.bfloat16, device="cuda")
+    st = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    with pytest.raises(Exception):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            with pytest.raises(pa.PAError):
+                pa.last_error()
+    pa.append_fp8_blocks(new, new, st, e.tab, e.lens, e.k, e.v, e.ks, e.vs)
+    assert pa.last_error() == 0
