@@ -13,8 +13,7 @@
 // the copy rate) and 64 x 32 heads over U[128, 2048] 96 us (6.0 TB/s).  P's third term
 // costs nothing that shows there (193 and 94 us with two terms): the tensor pipe is idle
 // enough, and threads store three bytes for two.  Where the threads' work bounds the
-// call it does: 64 x 8 heads over U[1024, 8192], 16 query heads a CTA of head_dim 64
-// 137 us (132), of head_dim 32 117 (106).
+// call it is 1 %: 64 x 8 heads over U[1024, 8192] in groups of 8 121 us (120).
 //
 // One CTA = (sequence, partition of P tokens, KV head, up to 16 query heads):
 //   S^T[128 tokens x N] = K[128 x 128] Q^T      A = K tile (K-major), B = Q rows
@@ -513,15 +512,26 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
             if (h < gh) sp[(size_t)h * Lmax] = s[h];
         }
       }
+      // z is kept where a head's scale has to be picked from several (64 x 8 heads in groups of 4 over
+      // U[1024, 8192]: head_dim 64 79 -> 77 us, 32 117 -> 104); with one scale an addition is
+      // cheaper than the register (groups of 8 over head_dim 128: 121 against 123)
       bool need = false;
+      float z[GT];
 #pragma unroll
-      for (int h = 0; h < GT; ++h) need = need || s[h] > m[h] + kTcSlack || s[h] + pick(lv, kvi[h]) > w[h] + kTcSlack;
+      for (int h = 0; h < GT; ++h) {
+        if constexpr (HP > 1) {
+          z[h] = s[h] + pick(lv, kvi[h]);
+          need = need || s[h] > m[h] + kTcSlack || z[h] > w[h] + kTcSlack;
+        } else {
+          need = need || s[h] > m[h] + kTcSlack || s[h] + lv[0] > w[h] + kTcSlack;
+        }
+      }
       __syncwarp();
       if (vote128(need)) {
         // new references: the tile's maxima where they are above
 #pragma unroll
         for (int h = 0; h < GT; ++h) {
-          const float x = warp_max(s[h]), y = warp_max(s[h] + pick(lv, kvi[h]));
+          const float x = warp_max(s[h]), y = warp_max(HP > 1 ? z[h] : s[h] + lv[0]);
           if (lane == 0) {
             sh->mx[warp][h] = x;
             sh->wx[warp][h] = y;
@@ -560,8 +570,8 @@ tc_decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant
       // P: 2^(z - w + 12) as three e5m2 terms, byte r of rows h, NP + h and 2 NP + h
       const uint32_t pb = sbase + kOffP + (uint32_t)st * kPBytes;
       auto weight = [&](int h) -> float {
-        const float z = s[h] + pick(lv, kvi[h]);
-        return z == -INFINITY ? 0.f : exp2f(z - w[h] + kTcPShift);
+        const float x = HP > 1 ? z[h] : s[h] + lv[0];
+        return x == -INFINITY ? 0.f : exp2f(x - w[h] + kTcPShift);
       };
 #pragma unroll
       for (int h = 0; h < GT; h += 2) {
