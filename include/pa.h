@@ -668,6 +668,188 @@ int pa_prefill_varlen(void* out, const void* query, const int32_t* query_start, 
                       int block_size, int num_blocks, float scale,
                       pa_dtype dtype, void* stream);
 
+/*
+ * Rotary positions.  Pair i of a head at position p is turned by the angle
+ * p * f_i and multiplied by an amplitude A:
+ *
+ *   (x, y) -> A (x cos(p f_i) - y sin(p f_i), y cos(p f_i) + x sin(p f_i))
+ *
+ * for the first rotary_dim elements of the head; the rest stays as it is.
+ *
+ *   PA_ROPE_HALF         pair i is elements i and i + rotary_dim / 2
+ *   PA_ROPE_INTERLEAVED  pair i is elements 2 i and 2 i + 1
+ *
+ * The frequencies come as a table of steps: steps[i] = round(2^64 f_i / 2 pi),
+ * the fraction of a turn that one position makes, so that p * steps[i] modulo
+ * 2^64 is the turn's fraction with no angle to reduce: exact to 2^-33 of a turn
+ * for every int32 position.  pa_rope_steps fills a HOST table of rotary_dim / 2
+ * entries (to be copied to the device) and *amplitude:
+ *
+ *   PA_ROPE_PLAIN   f_i = base^(-2 i / rotary_dim), A = 1; the other arguments
+ *                   are not looked at
+ *   PA_ROPE_LINEAR  f_i / factor (positions interpolated)
+ *   PA_ROPE_NTK     the base times factor^(rotary_dim / (rotary_dim - 2))
+ *   PA_ROPE_YARN    f_i ((1 - r_i) + r_i / factor), r_i rising from 0 to 1
+ *                   between the pairs that make beta_fast and beta_slow turns
+ *                   over original_len positions, A = 0.1 ln(factor) + 1
+ *
+ * rotary_dim is a multiple of 16 up to 512, base > 1, factor >= 1,
+ * 0 < beta_slow <= beta_fast.  Pure host arithmetic; no CUDA call.
+ */
+typedef enum { PA_ROPE_HALF = 0, PA_ROPE_INTERLEAVED = 1 } pa_rope_layout;
+typedef enum { PA_ROPE_PLAIN = 0, PA_ROPE_LINEAR = 1, PA_ROPE_NTK = 2, PA_ROPE_YARN = 3 } pa_rope_scaling;
+int pa_rope_steps(uint64_t* steps, float* amplitude, int rotary_dim, double base, pa_rope_scaling scaling,
+                  double factor, double original_len, double beta_fast, double beta_slow);
+
+/*
+ * Rotate queries and keys.  Both are strided [num_tokens, heads, head_dim]
+ * tensors (strides in elements, the innermost 1; a view into a fused
+ * projection's output will do).  An output may be its input (same pointer and
+ * strides: the elements past rotary_dim are then not touched) and must not
+ * overlap it otherwise, nor itself.  A part of a head other than its first
+ * elements is rotated through a pointer to it, with head_dim = rotary_dim.
+ *
+ *   positions    [num_tokens] int32, any value
+ *   num_heads, num_kv_heads  0 to 2^20: 0 leaves that side out
+ *   head_dim     a multiple of 16 up to 512; rotary_dim <= head_dim likewise
+ *   steps        device copy of the table of pa_rope_steps
+ *   dtype        PA_F32 or PA_BF16; products in fp32, rounded once
+ *
+ * Pointers and strides are multiples of 16 bytes (PA_ERR_ALIGN).
+ */
+int pa_rope(void* q_out, long long q_out_token_stride, long long q_out_head_stride,
+            const void* q, long long q_token_stride, long long q_head_stride, int num_heads,
+            void* k_out, long long k_out_token_stride, long long k_out_head_stride,
+            const void* k, long long k_token_stride, long long k_head_stride, int num_kv_heads,
+            const int32_t* positions, int num_tokens, int head_dim, int rotary_dim,
+            pa_rope_layout layout, const uint64_t* steps, float amplitude,
+            pa_dtype dtype, void* stream);
+
+/*
+ * pa_rope and pa_reshape_and_cache in one launch: the queries rotated, the
+ * keys rotated into their slots of k_cache, the values copied into v_cache.
+ * Strides, positions, steps as for pa_rope; slots, pools and their conditions
+ * as for pa_reshape_and_cache (a token without a slot has its queries rotated
+ * all the same).  num_heads 0 leaves the queries out.
+ */
+int pa_rope_and_cache(void* q_out, long long q_out_token_stride, long long q_out_head_stride,
+                      const void* q, long long q_token_stride, long long q_head_stride, int num_heads,
+                      const void* key, long long key_token_stride, long long key_head_stride,
+                      const void* value, long long value_token_stride, long long value_head_stride,
+                      int num_kv_heads, const int32_t* positions, const int64_t* slot_mapping, int num_tokens,
+                      void* k_cache, void* v_cache, int num_blocks, int block_size, int head_dim, int rotary_dim,
+                      pa_rope_layout layout, const uint64_t* steps, float amplitude,
+                      pa_dtype dtype, void* stream);
+
+/*
+ * The latent cache: one vector a token for all heads.
+ *
+ *   cache  [num_blocks, block_size, latent_dim + rope_dim], row-major: the
+ *          token's latent vector, then its rotated key
+ *
+ * latent_dim in {128, 256, 384, 512}, rope_dim in {16, 32, 48, 64}, block_size
+ * in {8, 16, 32}.  Blocks are copied and swapped with pa_copy_blocks /
+ * pa_swap_blocks, num_kv_heads = 1 and head_dim = latent_dim + rope_dim, two
+ * layers' pools a call (or one pool as both).
+ *
+ * Append: row t of latent goes to slot slot_mapping[t] as it is, row t of
+ * key_rope rotated behind it, and the rotary part of the token's queries
+ * (strided [num_tokens, num_heads, rope_dim]) is rotated into query_out in the
+ * same launch (num_heads 0 leaves it out).  Row strides in elements; alignment,
+ * positions, steps and layouts as for pa_rope, slots as for
+ * pa_reshape_and_cache.
+ */
+int pa_latent_append(const void* latent, long long latent_stride, const void* key_rope, long long key_rope_stride,
+                     void* query_out, long long query_out_token_stride, long long query_out_head_stride,
+                     const void* query, long long query_token_stride, long long query_head_stride, int num_heads,
+                     const int32_t* positions, const int64_t* slot_mapping, int num_tokens,
+                     void* cache, int num_blocks, int block_size, int latent_dim, int rope_dim,
+                     pa_rope_layout layout, const uint64_t* steps, float amplitude,
+                     pa_dtype dtype, void* stream);
+
+/*
+ * Attention over a latent cache in its absorbed form: every head's queries
+ * meet the cached rows themselves, and the rows' latent part is the values.
+ * With c_t row t of the context and q of latent_dim + rope_dim elements (the
+ * query times the key's up-projection, then its rotated part),
+ *
+ *   out[r,h,:] = sum_t softmax_t(scale * <q[r,h,:], c_t>) c_t[:latent_dim]
+ *
+ * (to be multiplied by the value's up-projection).  Rows and positions are
+ * pa_prefill_varlen's: sequence b's rows are query_start[b] ..
+ * query_start[b+1]-1, the last of its context, and see it causally; rows at
+ * negative positions are zeros, rows of no sequence are left as they were.
+ *
+ *   out            [total_queries, num_heads, latent_dim] (written)
+ *   query          [total_queries, num_heads, latent_dim + rope_dim]
+ *   query_start    [num_seqs + 1] int32, non-decreasing from 0 to
+ *                  total_queries, or NULL: one row a sequence (total_queries =
+ *                  num_seqs).  A bad pair sets PA_DEV_BAD_LEN, and that
+ *                  sequence writes nothing.
+ *   scale          > 0
+ *   partition_size as for pa_decode; pa_latent_decode_partition_size returns
+ *                  the size used
+ *   workspace      at least pa_latent_decode_workspace_bytes() with the same
+ *                  sizes, 16-byte aligned (may be NULL when that is 0);
+ *                  contents on entry do not matter, calls that share one must
+ *                  be ordered
+ *   dtype          PA_BF16
+ *
+ * A context length outside its table row is clamped and sets PA_DEV_BAD_LEN, a
+ * block id outside the pool is read as block 0 and sets PA_DEV_BAD_BLOCK.  A
+ * table row holds at most 2^30 tokens, total_queries * num_heads < 2^31.
+ * Accumulation is fp32; the softmax weights are rounded to bf16 for their
+ * product with the values.
+ */
+int pa_latent_decode(void* out, const void* query, const int32_t* query_start, int total_queries,
+                     const void* cache, const int32_t* block_tables, int max_blocks_per_seq,
+                     const int32_t* context_lens, int num_seqs, int num_heads, int latent_dim, int rope_dim,
+                     int block_size, int num_blocks, float scale, int partition_size,
+                     void* workspace, size_t workspace_bytes, pa_dtype dtype, void* stream);
+
+/* Bytes of workspace pa_latent_decode needs for these sizes, and the partition
+ * size (tokens) it uses.  Pure host arithmetic; no CUDA call. */
+size_t pa_latent_decode_workspace_bytes(int total_queries, int num_seqs, int num_heads, int latent_dim,
+                                        int max_blocks_per_seq, int block_size, int partition_size);
+int pa_latent_decode_partition_size(int total_queries, int num_seqs, int num_heads, int latent_dim,
+                                    int max_blocks_per_seq, int block_size, int partition_size);
+
+/*
+ * Attention over latent vectors in their expanded form (prompts): keys and
+ * values of every head, as the up-projection writes them, and one rotated key
+ * shared by all heads.  With k[t,h,:] = (kv[t,h,:key_dim], key_rope[t,:]) and
+ * v[t,h,:] = kv[t,h,key_dim:],
+ *
+ *   out[r,h,:] = sum_t softmax_t(scale * <q[r,h,:], k[t,h,:]>) v[t,h,:]
+ *
+ * over ragged sequences: sequence b's context is rows kv_start[b] ..
+ * kv_start[b+1]-1 of kv and key_rope, its queries rows query_start[b] ..
+ * query_start[b+1]-1, the last tokens of that context, causal.  (A chunk that
+ * continues a cached context takes the cached rows back first: they are rows
+ * of the latent pool, to be multiplied by the up-projection again.)
+ *
+ *   out             [total_queries, num_heads, value_dim] (written)
+ *   query           [total_queries, num_heads, key_dim + rope_dim]
+ *   kv              [total_kv, num_heads, key_dim + value_dim]
+ *   key_rope        [total_kv, rope_dim], rows key_rope_stride elements apart
+ *                   (a multiple of 16 bytes)
+ *   query_start, kv_start  [num_seqs + 1] int32, non-decreasing from 0 to
+ *                   total_queries / total_kv.  A bad pair sets PA_DEV_BAD_LEN,
+ *                   and that sequence writes nothing.  Rows at negative
+ *                   positions (more rows than context) are zeros; rows of no
+ *                   sequence are left as they were.
+ *   key_dim, value_dim  32, 64 or 128; rope_dim 16, 32, 48 or 64
+ *   scale           > 0
+ *   dtype           PA_BF16; accumulation fp32, softmax weights rounded to
+ *                   bf16 for their product with the values
+ *
+ * num_seqs <= 2048.
+ */
+int pa_latent_prefill(void* out, const void* query, const int32_t* query_start, int total_queries,
+                      const void* kv, const void* key_rope, long long key_rope_stride, const int32_t* kv_start,
+                      int total_kv, int num_seqs, int num_heads, int key_dim, int rope_dim, int value_dim,
+                      float scale, pa_dtype dtype, void* stream);
+
 /* Return the sticky device-detected condition bits (PA_DEV_*) and clear
  * them.  Synchronises the current device; 0 means nothing was detected.
  * Returns PA_ERR_CUDA if the device cannot be read. */

@@ -61,4 +61,10 @@ from .bounded import (  # noqa: F401
     attention_weights,
     evict,
 )
+from .latent import (  # noqa: F401
+    rope_frequencies,
+    rope,
+    latent_decode,
+    latent_prefill,
+)
 from .block_manager import BlockPool, BlockTable, BlockExhausted  # noqa: F401

@@ -78,6 +78,27 @@ lib.pa_evict.argtypes = [_p, _p, _p, _p, _i32p, _i, _i32p, _i32p, _i32p, _i, _p,
 lib.pa_evict.restype = _i
 lib.pa_evict_workspace_bytes.argtypes = [_i, _i, _i, _i, _i]
 lib.pa_evict_workspace_bytes.restype = _sz
+_ll, _d = ctypes.c_longlong, ctypes.c_double
+_rows3 = [_p, _ll, _ll]                                  # a strided [tokens, heads, dim] tensor
+lib.pa_rope_steps.argtypes = [_p, _p, _i, _d, _i, _d, _d, _d, _d]
+lib.pa_rope_steps.restype = _i
+lib.pa_rope.argtypes = [*_rows3, *_rows3, _i, *_rows3, *_rows3, _i, _i32p, _i, _i, _i, _i, _p, _f, _i, _p]
+lib.pa_rope.restype = _i
+lib.pa_rope_and_cache.argtypes = [*_rows3, *_rows3, _i, *_rows3, *_rows3, _i, _i32p, _i64p, _i, _p, _p, _i, _i, _i, _i,
+                                  _i, _p, _f, _i, _p]
+lib.pa_rope_and_cache.restype = _i
+lib.pa_latent_append.argtypes = [_p, _ll, _p, _ll, *_rows3, *_rows3, _i, _i32p, _i64p, _i, _p, _i, _i, _i, _i, _i, _p,
+                                 _f, _i, _p]
+lib.pa_latent_append.restype = _i
+lib.pa_latent_decode.argtypes = [_p, _p, _i32p, _i, _p, _i32p, _i, _i32p, _i, _i, _i, _i, _i, _i, _f, _i, _p, _sz, _i,
+                                 _p]
+lib.pa_latent_decode.restype = _i
+lib.pa_latent_decode_workspace_bytes.argtypes = [_i, _i, _i, _i, _i, _i, _i]
+lib.pa_latent_decode_workspace_bytes.restype = _sz
+lib.pa_latent_decode_partition_size.argtypes = [_i, _i, _i, _i, _i, _i, _i]
+lib.pa_latent_decode_partition_size.restype = _i
+lib.pa_latent_prefill.argtypes = [_p, _p, _i32p, _i, _p, _p, _ll, _i32p, _i, _i, _i, _i, _i, _i, _f, _i, _p]
+lib.pa_latent_prefill.restype = _i
 lib.pa_last_error.argtypes = []
 lib.pa_last_error.restype = _i
 lib.pa_strerror.argtypes = [_i]
@@ -544,6 +565,218 @@ def evict(k_cache, v_cache, block_tables, context_lens, kept_lens, seen_lens, we
                         token_pos_out.data_ptr(), shape[2], NB, bs, Hkv, D, workspace.data_ptr(), workspace.nbytes,
                         kv, _on(stream, dev)), "pa_evict")
     return new_lens
+
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def rope_steps(rotary_dim, base=10000.0, scaling="none", factor=1.0, original_len=4096.0, beta_fast=32.0,
+               beta_slow=1.0, device=None):
+    """(steps, amplitude): the table of turns per position of rotary_dim / 2 pairs, 64-bit fractions in an int64
+    tensor on `device`, and the factor of the rotated pairs.  scaling: none, linear, ntk or yarn."""
+    steps = torch.empty(max(rotary_dim, 0) // 2, dtype=torch.int64)
+    amplitude = _f()
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError("scaling is one of %s" % ", ".join(ROPE_SCALINGS))
+    _check(lib.pa_rope_steps(steps.data_ptr() if steps.numel() else None, ctypes.byref(amplitude), rotary_dim, base,
+                             ROPE_SCALINGS[scaling], factor, original_len, beta_fast, beta_slow), "pa_rope_steps")
+    return (steps if device is None else steps.to(device)), amplitude.value
+
+
+def _on_device(*ts):
+    """The current device, which every tensor has to be on (whatever its strides)."""
+    d = torch.cuda.current_device() if ts[0].is_cuda else -2
+    for t in ts:
+        if t.get_device() != d:
+            raise ValueError("tensors must be on the current CUDA device")
+    return d
+
+
+def _rows(t, what):
+    """(pointer, token stride, head stride) of a [tokens, heads, dim] view whose innermost stride is 1."""
+    s = t.stride()
+    if len(s) != 3 or (s[2] != 1 and t.size(2) > 1):
+        raise ValueError("%s is [tokens, heads, dim], its elements next to each other" % what)
+    return t.data_ptr(), s[0] if t.size(0) > 1 else 0, s[1] if t.size(1) > 1 else 0
+
+
+def _distinct_rows(t, what):
+    """No element of the output `t` lies in two places of it."""
+    n, h, d = t.shape
+    s0, s1, _ = t.stride()
+    if n * h * d and not ((h == 1 or s1 >= d) and (n == 1 or s0 >= s1 * (h - 1) + d) or
+                          (n == 1 or s0 >= d) and (h == 1 or s1 >= s0 * (n - 1) + d)):
+        raise ValueError("the rows of %s overlap" % what)
+
+
+def _turn(x, out, dtype, n, what):
+    """Checks and marshals a rotated tensor and where it goes: (out rows, x rows, heads); None leaves it out."""
+    if x is None:
+        if out is not None:
+            raise ValueError("%s_out without %s" % (what, what))
+        return 0, 0, 0, 0, 0, 0, 0
+    out = x if out is None else out
+    if x.dim() != 3 or x.size(0) != n or out.shape != x.shape or x.dtype is not dtype or out.dtype is not dtype:
+        raise ValueError("%s and its output are [tokens, heads, head_dim] of one type" % what)
+    _distinct_rows(out, what if out is x else what + "_out")
+    return (*_rows(out, what), *_rows(x, what), x.size(1))
+
+
+def _angles(positions, steps, layout, n):
+    _int32(positions)
+    if positions.dim() != 1 or positions.size(0) != n:
+        raise ValueError("positions is [tokens]")
+    if steps.dtype is not torch.int64 or steps.dim() != 1:
+        raise TypeError("steps is the int64 table of rope_steps")
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError("layout is half or interleaved")
+    return ROPE_LAYOUTS[layout], 2 * steps.size(0)
+
+
+def _slots(slot_mapping, n):
+    if slot_mapping.dtype is not torch.int64 or slot_mapping.dim() != 1 or slot_mapping.size(0) != n:
+        raise ValueError("slot_mapping is int64 [tokens]")
+
+
+def _float_kind(t):
+    if t.dtype is not _F32 and t.dtype is not torch.bfloat16:
+        raise TypeError("unsupported dtype %s" % t.dtype)
+    return _KIND[t.dtype]
+
+
+def rope(q, k, positions, steps, amplitude=1.0, layout="half", q_out=None, k_out=None, stream=None):
+    """Rotate the first 2 * len(steps) elements of every head of q [T, Hq, D] and k [T, Hkv, D] (either may be None;
+    strided views will do) by the tokens' positions: in place, or into q_out / k_out.  Returns what it wrote."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k")
+    if x.dim() != 3 or (k is not None and k.dim() == 3 and k.size(2) != x.size(2)):
+        raise ValueError("q and k are [tokens, heads, head_dim]")
+    n, kind = x.size(0), _float_kind(x)
+    lay, rot = _angles(positions, steps, layout, n)
+    qa, ka = _turn(q, q_out, x.dtype, n, "q"), _turn(k, k_out, x.dtype, n, "k")
+    _ready(positions, steps)
+    dev = _on_device(*(t for t in (q, k, q_out, k_out, positions) if t is not None))
+    _check(lib.pa_rope(*qa, *ka, positions.data_ptr(), n, x.size(2), rot, lay, steps.data_ptr(), amplitude, kind,
+                       _on(stream, dev)), "pa_rope")
+    return (q if q_out is None else q_out), (k if k_out is None else k_out)
+
+
+def rope_and_cache(q, key, value, positions, slot_mapping, k_cache, v_cache, steps, amplitude=1.0, layout="half",
+                   q_out=None, stream=None):
+    """Rotate q [T, Hq, D] (in place, or into q_out; None leaves it out) and append the rotated key and the value
+    [T, Hkv, D] to the pool slots named by slot_mapping.  q, key and value may be strided views."""
+    NB, bs, H, D, kind = _pools(k_cache, v_cache)
+    if kind == PA_FP8_E4M3:
+        raise TypeError("rotate first, then append to an e4m3 pool")
+    n = key.size(0)
+    for t in (key, value):
+        if t.dim() != 3 or t.size(0) != n or t.size(1) != H or t.size(2) != D or t.dtype is not k_cache.dtype:
+            raise ValueError("key and value are [tokens, num_kv_heads, head_dim] of the pools' type")
+    if q is not None and q.dim() == 3 and q.size(2) != D:
+        raise ValueError("q is [tokens, num_heads, head_dim]")
+    lay, rot = _angles(positions, steps, layout, n)
+    _slots(slot_mapping, n)
+    qa = _turn(q, q_out, k_cache.dtype, n, "q")
+    _ready(positions, slot_mapping, k_cache, v_cache, steps)
+    dev = _on_device(*(t for t in (key, value, q, q_out) if t is not None))
+    _check(lib.pa_rope_and_cache(*qa, *_rows(key, "key"), *_rows(value, "value"), H, positions.data_ptr(),
+                                 slot_mapping.data_ptr(), n, k_cache.data_ptr(), v_cache.data_ptr(), NB, bs, D, rot,
+                                 lay, steps.data_ptr(), amplitude, kind, _on(stream, dev)), "pa_rope_and_cache")
+    return q if q_out is None else q_out
+
+
+def _latent_pool(cache):
+    if cache.dim() != 3:
+        raise ValueError("cache is [num_blocks, block_size, latent_dim + rope_dim]")
+    return cache.shape
+
+
+def latent_append(latent, key_rope, positions, slot_mapping, cache, steps, amplitude=1.0, layout="half", query=None,
+                  query_out=None, stream=None):
+    """Append latent [T, R] and the rotated key_rope [T, P] to the slots of a latent cache [NB, bs, R + P]; query
+    [T, H, P], the rotary part of the tokens' queries, is rotated along (in place, or into query_out).  Rows may be
+    strided."""
+    NB, bs, width = _latent_pool(cache)
+    n, kind = latent.size(0), _float_kind(cache)
+    for t in (latent, key_rope):
+        if t.dim() != 2 or t.size(0) != n or t.dtype is not cache.dtype or (t.stride(1) != 1 and t.size(1) > 1):
+            raise ValueError("latent and key_rope are [tokens, dim] of the cache's type, elements next to each other")
+    R, P = latent.size(1), key_rope.size(1)
+    lay, rot = _angles(positions, steps, layout, n)
+    if R + P != width or rot != P or (query is not None and query.dim() == 3 and query.size(2) != P):
+        raise ValueError("cache rows are latent_dim + rope_dim, and steps and queries have rope_dim")
+    _slots(slot_mapping, n)
+    qa = _turn(query, query_out, cache.dtype, n, "query")
+    _ready(positions, slot_mapping, cache, steps)
+    dev = _on_device(*(t for t in (latent, key_rope, query, query_out) if t is not None))
+    _check(lib.pa_latent_append(latent.data_ptr(), latent.stride(0), key_rope.data_ptr(), key_rope.stride(0), *qa,
+                                positions.data_ptr(), slot_mapping.data_ptr(), n, cache.data_ptr(), NB, bs, R, P, lay,
+                                steps.data_ptr(), amplitude, kind, _on(stream, dev)), "pa_latent_append")
+    return query if query_out is None else query_out
+
+
+def alloc_latent_workspace(q, cache, block_tables, partition_size=0):
+    """Workspace for latent_decode with these sizes."""
+    rows, H, width = q.shape
+    R = (width - 16) // 128 * 128            # the one latent_dim of rows of this width
+    n = lib.pa_latent_decode_workspace_bytes(rows, block_tables.shape[0], H, R, block_tables.shape[1], cache.shape[1],
+                                             partition_size)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+
+
+def latent_decode(out, q, cache, block_tables, context_lens, scale, query_start=None, partition_size=0,
+                  workspace=None, stream=None):
+    """out[rows, H, R] = attention of q[rows, H, R + P] over a latent cache [NB, bs, R + P], whose rows' first R
+    elements are the values too.  One row a sequence, or sequence b's rows are query_start[b]..query_start[b+1]-1,
+    the last tokens of its context, causal."""
+    NB, bs, width = _latent_pool(cache)
+    B, cols = _table(block_tables, context_lens)
+    if q.dim() != 3 or out.dim() != 3 or q.size(2) != width or out.shape[:2] != q.shape[:2] or not (
+            q.dtype is cache.dtype and out.dtype is cache.dtype):
+        raise ValueError("q is [rows, num_heads, latent_dim + rope_dim], out [rows, num_heads, latent_dim], of the "
+                         "cache's type")
+    rows, H, R = out.shape
+    kind = _float_kind(q)
+    start = None
+    if query_start is not None:
+        _starts(query_start, B)
+        _ready(query_start)
+        start = query_start.data_ptr()
+    elif rows != B:
+        raise ValueError("one query row per sequence")
+    if workspace is None:
+        workspace = _own(alloc_latent_workspace, stream, q, cache, block_tables, partition_size)
+    dev = _ready(out, q, cache, block_tables, context_lens, workspace)
+    _check(lib.pa_latent_decode(out.data_ptr(), q.data_ptr(), start, rows, cache.data_ptr(), block_tables.data_ptr(),
+                                cols, context_lens.data_ptr(), B, H, R, width - R, bs, NB, scale, partition_size,
+                                workspace.data_ptr(), workspace.nbytes, kind, _on(stream, dev)), "pa_latent_decode")
+    return out
+
+
+def latent_prefill(out, q, query_start, kv, key_rope, kv_start, scale, stream=None):
+    """Ragged causal attention over expanded latent vectors: q [rows, H, Dk + P], kv [T, H, Dk + Dv] (keys, then
+    values, of every head), key_rope [T, P] shared by the heads (rows may be strided), out [rows, H, Dv].  Sequence
+    b's context is rows kv_start[b]..kv_start[b+1]-1, its queries query_start[b]..query_start[b+1]-1, the last of it."""
+    if not (q.dim() == kv.dim() == out.dim() == 3 and key_rope.dim() == 2) or not (
+            q.dtype is kv.dtype and out.dtype is kv.dtype and key_rope.dtype is kv.dtype):
+        raise ValueError("q, kv and out are [rows, num_heads, dim], key_rope [rows, rope_dim], of one type")
+    rows, H, Dv = out.shape
+    T, P = key_rope.shape
+    Dk = q.size(2) - P
+    if q.shape[:2] != out.shape[:2] or kv.shape != (T, H, Dk + Dv) or (key_rope.stride(1) != 1 and P > 1):
+        raise ValueError("q is [rows, H, Dk + P], kv [T, H, Dk + Dv], key_rope [T, P], out [rows, H, Dv]")
+    B = query_start.size(0) - 1
+    _starts(query_start, B)
+    _starts(kv_start, B)
+    kind = _float_kind(q)
+    _on_device(q, key_rope)
+    dev = _ready(out, q, kv, query_start, kv_start)
+    _check(lib.pa_latent_prefill(out.data_ptr(), q.data_ptr(), query_start.data_ptr(), rows, kv.data_ptr(),
+                                 key_rope.data_ptr(), key_rope.stride(0) if T > 1 else P, kv_start.data_ptr(), T, B, H, Dk, P,
+                                 Dv, scale, kind, _on(stream, dev)), "pa_latent_prefill")
+    return out
 
 
 def selftest_bounded_wait(limit_ns, stream=None):

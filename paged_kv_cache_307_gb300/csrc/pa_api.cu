@@ -110,7 +110,7 @@ bool encode_map(CUtensorMap* map, const void* base, pa_dtype dt, int rank, const
 
 // Takes every unit's status word and leaves what they held in g_status_taken: one
 // kernel and one read, where a blocking read a unit took 108 us for twelve.
-constexpr int kUnits = 12;
+constexpr int kUnits = 15;
 struct StatusWords {
   unsigned* word[kUnits];
 };
@@ -135,6 +135,9 @@ extern "C" int pa_last_error(void) {
       pa::status_word_evict(),
       pa::status_word_shared(),
       pa::status_word_prefill(),
+      pa::status_word_rope(),
+      pa::status_word_latent_decode(),
+      pa::status_word_latent_prefill(),
       pa::status_word_selftest(),
   }};
   for (unsigned* p : w.word)
@@ -169,6 +172,6 @@ extern "C" const char* pa_strerror(int code) {
   }
 }
 
-extern "C" int pa_version(void) { return 101; }
+extern "C" int pa_version(void) { return 102; }
 
 extern "C" const char* pa_last_host_error(void) { return pa::g_host_msg; }

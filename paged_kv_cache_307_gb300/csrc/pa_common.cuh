@@ -277,6 +277,13 @@ constexpr long long kMaxRowTokens = 1ll << 30;
 inline bool supported_head_dim(int d) { return d == 32 || d == 64 || d == 128; }
 inline bool supported_block_size(int bs) { return bs == 4 || bs == 8 || bs == 16 || bs == 32; }
 
+// A latent cache: whole 128-row products over the latent vector, the rotary part at most one
+// swizzled row span, blocks of whole swizzle atoms.
+inline bool latent_shape(int latent_dim, int rope_dim, int block_size) {
+  return latent_dim > 0 && latent_dim <= 512 && latent_dim % 128 == 0 && rope_dim > 0 && rope_dim <= 64 &&
+         rope_dim % 16 == 0 && (block_size == 8 || block_size == 16 || block_size == 32);
+}
+
 // GB300's SMs, for the sizing functions that make no CUDA call.
 constexpr int kTunedSms = 152;
 // Host: number of SMs on the current device (cached per device).
@@ -329,6 +336,9 @@ unsigned* status_word_prefill_fp8_blocks();
 unsigned* status_word_evict();
 unsigned* status_word_shared();
 unsigned* status_word_prefill();
+unsigned* status_word_rope();
+unsigned* status_word_latent_decode();
+unsigned* status_word_latent_prefill();
 unsigned* status_word_selftest();
 
 }  // namespace pa

@@ -1,0 +1,395 @@
+// pa_rope.cu — rotary positions: queries and keys rotated, the keys on their way into a
+// paged cache (pa_rope, pa_rope_and_cache) or, as the one key that all heads share, into a
+// latent cache (pa_latent_append).
+//
+// Pair i of a head at position p turns by the angle p f_i:
+//   (x, y) -> A (x cos - y sin, y cos + x sin)
+// The angle is never formed.  The caller's table holds f_i / 2 pi as a 64-bit fraction of a
+// turn, and p times that, modulo 2^64, is the turn's fraction exactly: the integer product
+// wraps where an angle would have to be reduced.  (An fp32 angle is off by 2^-24 of itself,
+// 0.06 at a position of a million.)  The fraction as a float goes to sincospif.
+//
+// Data movement bound by HBM: every element is read and written once, in 16-byte chunks.
+// A CTA takes p.tpb tokens; their cosines and sines are made once, in shared memory, for
+// all heads.  A work unit is what one pass over registers needs: in the half layout two
+// chunks, half the rotated part apart; else one chunk.  Each thread has four units' loads in flight.
+#include "pa_common.cuh"
+#include "pa_mma.cuh"
+
+#include <math.h>
+
+namespace pa {
+namespace {
+
+__device__ unsigned g_status_rope;
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 4;                // units in flight per thread
+constexpr int kTableEntries = 2048;      // (cos, sin) pairs in shared memory
+
+// One tensor of rows: bytes from token to token and head to head.
+struct Part {
+  const char* src;
+  char* dst;
+  long long src_token, src_head, dst_token, dst_head;
+  int units;                             // of a head
+  int all;                               // of a token
+};
+
+struct RopeParams {
+  Part q, k, c;                          // rotated; rotated (by slot where slots is given); copied by slot
+  const int32_t* positions;
+  const int64_t* slots;
+  const uint64_t* steps;
+  long long num_slots;
+  float amplitude;
+  int n, tpb, items;                     // tokens, tokens a CTA, units a token
+  int pairs;                             // rotated pairs of a head
+};
+
+struct Unit {
+  const char* s;                         // null: nothing to do
+  char* d;
+  int table;                             // first entry of the cosines, -1: copied as it is
+};
+
+__device__ __forceinline__ uint4 ld_v4(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float* f) {
+  if constexpr (sizeof(T) == 4)
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  else
+    return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+}
+
+// HALF: pair i is elements i and pairs + i of a head; else 2i and 2i + 1.
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+  using E = Elem<T>;
+  constexpr int EPC = E::kPerChunk;
+  constexpr int kPairs = HALF ? EPC : EPC / 2;             // pairs of a unit
+  __shared__ __align__(16) float2 table[kTableEntries];
+  const int tok0 = blockIdx.x * p.tpb;
+  const int nt = min(p.tpb, p.n - tok0);
+  const unsigned total = (unsigned)nt * p.items;
+  const int turned = p.pairs / kPairs;                     // units of a head that are rotated
+  const int hop = p.pairs * E::kBytes;                     // HALF: from a pair's first element to its second
+
+  auto unit_of = [&](unsigned i) -> Unit {
+    Unit u{nullptr, nullptr, -1};
+    if (i >= total) return u;
+    const unsigned t = i / (unsigned)p.items;
+    unsigned r = i - t * p.items;
+    const long long tok = tok0 + (int)t;
+    const bool is_q = r < (unsigned)p.q.all;
+    if (!is_q) r -= p.q.all;
+    const bool is_c = !is_q && r >= (unsigned)p.k.all;
+    if (is_c) r -= p.k.all;
+    const Part& a = is_q ? p.q : is_c ? p.c : p.k;
+    long long row = tok;
+    if (!is_q && p.slots) {
+      row = __ldg(reinterpret_cast<const long long*>(p.slots) + tok);
+      if (row < 0) return u;                               // padding
+      if (row >= p.num_slots) {
+        if (!is_c && r == 0) atomicOr(&g_status_rope, PA_DEV_BAD_SLOT);
+        return u;
+      }
+    }
+    const unsigned h = r / (unsigned)a.units, x = r - h * a.units;
+    int off = (int)x * 16;
+    if (!is_c && x < (unsigned)turned)
+      u.table = (int)t * p.pairs + (int)x * kPairs;
+    else if (HALF && !is_c)
+      off += turned * 16;                                  // (each rotated unit was two chunks)
+    u.s = a.src + tok * a.src_token + h * a.src_head + off;
+    u.d = a.dst + row * a.dst_token + h * a.dst_head + off;
+    return u;
+  };
+
+  Unit u[kBatch];
+  uint4 lo[kBatch], hi[kBatch];
+  auto load = [&](unsigned i) {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      u[b] = unit_of(i + b * kThreads);
+      if (u[b].s) {
+        lo[b] = ld_v4(u[b].s);
+        if (HALF && u[b].table >= 0) hi[b] = ld_v4(u[b].s + hop);
+      }
+    }
+  };
+  auto finish = [&]() {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (!u[b].s) continue;
+      if (u[b].table < 0) {
+        st_v4(u[b].d, lo[b]);
+        continue;
+      }
+      const float4* cs = reinterpret_cast<const float4*>(table + u[b].table);
+      float x[EPC], y[EPC];
+      E::unpack(lo[b], x);
+      if constexpr (HALF) {
+        E::unpack(hi[b], y);
+#pragma unroll
+        for (int e = 0; e < EPC; e += 2) {
+          const float4 a = cs[e / 2];                      // cos, sin of two pairs
+          const float x0 = x[e], x1 = x[e + 1];
+          x[e] = fmaf(x0, a.x, -y[e] * a.y);
+          y[e] = fmaf(y[e], a.x, x0 * a.y);
+          x[e + 1] = fmaf(x1, a.z, -y[e + 1] * a.w);
+          y[e + 1] = fmaf(y[e + 1], a.z, x1 * a.w);
+        }
+        st_v4(u[b].d + hop, pack<T>(y));
+      } else {
+#pragma unroll
+        for (int e = 0; e < EPC; e += 4) {
+          const float4 a = cs[e / 4];
+          y[e] = fmaf(x[e], a.x, -x[e + 1] * a.y);
+          y[e + 1] = fmaf(x[e + 1], a.x, x[e] * a.y);
+          y[e + 2] = fmaf(x[e + 2], a.z, -x[e + 3] * a.w);
+          y[e + 3] = fmaf(x[e + 3], a.z, x[e + 2] * a.w);
+        }
+#pragma unroll
+        for (int e = 0; e < EPC; ++e) x[e] = y[e];
+      }
+      st_v4(u[b].d, pack<T>(x));
+    }
+  };
+
+  load(threadIdx.x);                                       // (on its way while the table is made)
+  for (int i = threadIdx.x; i < nt * p.pairs; i += kThreads) {
+    const int t = i / p.pairs;
+    const uint64_t turn = (uint64_t)(int64_t)__ldg(&p.positions[tok0 + t]) * __ldg(&p.steps[i - t * p.pairs]);
+    // the turn's fraction in [-1/2, 1/2), in half turns
+    float s, c;
+    sincospif(__ll2float_rn((long long)turn) * 0x1p-63f, &s, &c);
+    table[i] = make_float2(c * p.amplitude, s * p.amplitude);
+  }
+  __syncthreads();
+  for (unsigned i = threadIdx.x;;) {
+    finish();
+    i += kBatch * kThreads;
+    if (i >= total) break;
+    load(i);
+  }
+}
+
+// ---------------------------------------------------------------------------- host
+struct Rows {                            // a strided [tokens, heads, dim] tensor, strides in elements
+  const void* data;
+  long long token, head;
+};
+
+bool aligned_rows(const Rows& r, int e) {
+  return aligned16(r.data) && (r.token * e) % 16 == 0 && (r.head * e) % 16 == 0;
+}
+
+// A rotated part; what lies behind the rotated elements moves along unless it is in place already.
+Part turned_part(const Rows& dst, const Rows& src, int heads, int dim, int rot, int e, bool half, bool by_slot) {
+  Part a = {};
+  a.src = static_cast<const char*>(src.data);
+  a.dst = static_cast<char*>(const_cast<void*>(dst.data));
+  a.src_token = src.token * e;
+  a.src_head = src.head * e;
+  a.dst_token = dst.token * e;
+  a.dst_head = dst.head * e;
+  const bool in_place = !by_slot && dst.data == src.data && dst.token == src.token && dst.head == src.head;
+  a.units = rot * e / (half ? 32 : 16) + (in_place ? 0 : (dim - rot) * e / 16);
+  a.all = heads * a.units;
+  return a;
+}
+
+Part copied_part(void* dst, long long dst_row, const Rows& src, int heads, int dim, int e) {
+  Part a = {};
+  a.src = static_cast<const char*>(src.data);
+  a.dst = static_cast<char*>(dst);
+  a.src_token = src.token * e;
+  a.src_head = src.head * e;
+  a.dst_token = dst_row * e;
+  a.dst_head = (long long)dim * e;
+  a.units = dim * e / 16;
+  a.all = heads * a.units;
+  return a;
+}
+
+// (a token's units then fit 32 bits)
+bool heads_in_range(int n) { return n >= 0 && n <= 1 << 20; }
+
+bool rotary_shape(int dim, int rot) { return rot > 0 && rot <= dim && rot % 16 == 0 && dim % 16 == 0 && dim <= 512; }
+
+int launch(RopeParams& p, pa_dtype dtype, bool half, void* stream) {
+  const long long items = (long long)p.q.all + p.k.all + p.c.all;
+  if (items > 1 << 24) return PA_ERR_SHAPE;
+  if (items == 0) return PA_OK;
+  p.items = (int)items;
+  for (Part* a : {&p.q, &p.k, &p.c})
+    if (a->units == 0) a->units = 1;
+  // Tokens a CTA: one batch of units for its threads, as far as shared memory holds their
+  // cosines and two CTAs an SM are left.
+  long long tpb = (long long)kBatch * kThreads / items;
+  tpb = tpb < kTableEntries / p.pairs ? tpb : kTableEntries / p.pairs;
+  const long long spread = p.n / (2 * kTunedSms);
+  tpb = tpb < spread ? tpb : spread;
+  p.tpb = (int)(tpb < 1 ? 1 : tpb);
+  const unsigned grid = (unsigned)((p.n + (long long)p.tpb - 1) / p.tpb);
+  auto kernel = dtype == PA_F32 ? (half ? &rope_kernel<float, true> : &rope_kernel<float, false>)
+                                : (half ? &rope_kernel<__nv_bfloat16, true> : &rope_kernel<__nv_bfloat16, false>);
+  void* args[] = {&p};
+  return ck(cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(grid), dim3(kThreads), args, 0,
+                             (cudaStream_t)stream),
+            "cudaLaunchKernel(rope_kernel)")
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+unsigned* status_word_rope() { return device_word(g_status_rope); }
+
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" int pa_rope_steps(uint64_t* steps, float* amplitude, int rotary_dim, double base, pa_rope_scaling scaling,
+                             double factor, double original_len, double beta_fast, double beta_slow) {
+  constexpr double kPi = 3.14159265358979323846;
+  if (rotary_dim <= 0 || rotary_dim % 16 || rotary_dim > 512 || !(base > 1.0) || !(base < 1e300)) return PA_ERR_SHAPE;
+  if (scaling < PA_ROPE_PLAIN || scaling > PA_ROPE_YARN) return PA_ERR_SHAPE;
+  if (scaling != PA_ROPE_PLAIN && !(factor >= 1.0 && factor < 1e30)) return PA_ERR_SHAPE;
+  if (scaling == PA_ROPE_YARN && !(original_len > 0.0 && original_len < 1e30 && beta_slow > 0.0 && beta_fast >= beta_slow && beta_fast < 1e30))
+    return PA_ERR_SHAPE;
+  if (!steps || !amplitude) return PA_ERR_NULL;
+  const double d = rotary_dim;
+  if (scaling == PA_ROPE_NTK) base *= pow(factor, d / (d - 2.0));
+  double lo = 0.0, hi = 0.0;
+  if (scaling == PA_ROPE_YARN) {
+    auto pair = [&](double turns) { return d * log(original_len / (turns * 2.0 * kPi)) / (2.0 * log(base)); };
+    lo = fmax(0.0, floor(pair(beta_fast)));
+    hi = fmin(d - 1.0, ceil(pair(beta_slow)));
+  }
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    double f = pow(base, -2.0 * i / d);
+    if (scaling == PA_ROPE_LINEAR) f /= factor;
+    if (scaling == PA_ROPE_YARN) {
+      const double part = fmin(1.0, fmax(0.0, (i - lo) / fmax(hi - lo, 1e-3)));
+      f = f * (part / factor + 1.0 - part);
+    }
+    steps[i] = (uint64_t)(ldexp(f / (2.0 * kPi), 64) + 0.5);
+  }
+  *amplitude = scaling == PA_ROPE_YARN ? (float)(0.1 * log(factor) + 1.0) : 1.f;
+  return PA_OK;
+}
+
+extern "C" int pa_rope(void* q_out, long long q_out_token_stride, long long q_out_head_stride, const void* q,
+                       long long q_token_stride, long long q_head_stride, int num_heads, void* k_out,
+                       long long k_out_token_stride, long long k_out_head_stride, const void* k,
+                       long long k_token_stride, long long k_head_stride, int num_kv_heads,
+                       const int32_t* positions, int num_tokens, int head_dim, int rotary_dim, pa_rope_layout layout,
+                       const uint64_t* steps, float amplitude, pa_dtype dtype, void* stream) {
+  if (dtype != PA_F32 && dtype != PA_BF16) return PA_ERR_DTYPE;
+  if (num_tokens < 0 || !heads_in_range(num_heads) || !heads_in_range(num_kv_heads) || !rotary_shape(head_dim, rotary_dim) ||
+      (layout != PA_ROPE_HALF && layout != PA_ROPE_INTERLEAVED))
+    return PA_ERR_SHAPE;
+  if (num_tokens == 0 || (num_heads == 0 && num_kv_heads == 0)) return PA_OK;
+  if ((num_heads && (!q || !q_out)) || (num_kv_heads && (!k || !k_out)) || !positions || !steps) return PA_ERR_NULL;
+  const int e = elem_bytes(dtype);
+  const Rows qs{q, q_token_stride, q_head_stride}, qd{q_out, q_out_token_stride, q_out_head_stride};
+  const Rows ks{k, k_token_stride, k_head_stride}, kd{k_out, k_out_token_stride, k_out_head_stride};
+  if ((num_heads && (!aligned_rows(qs, e) || !aligned_rows(qd, e))) ||
+      (num_kv_heads && (!aligned_rows(ks, e) || !aligned_rows(kd, e))))
+    return PA_ERR_ALIGN;
+  const bool half = layout == PA_ROPE_HALF;
+  RopeParams p = {};
+  if (num_heads) p.q = turned_part(qd, qs, num_heads, head_dim, rotary_dim, e, half, false);
+  if (num_kv_heads) p.k = turned_part(kd, ks, num_kv_heads, head_dim, rotary_dim, e, half, false);
+  p.positions = positions;
+  p.steps = steps;
+  p.amplitude = amplitude;
+  p.n = num_tokens;
+  p.pairs = rotary_dim / 2;
+  return launch(p, dtype, half, stream);
+}
+
+extern "C" int pa_rope_and_cache(void* q_out, long long q_out_token_stride, long long q_out_head_stride,
+                                 const void* q, long long q_token_stride, long long q_head_stride, int num_heads,
+                                 const void* key, long long key_token_stride, long long key_head_stride,
+                                 const void* value, long long value_token_stride, long long value_head_stride,
+                                 int num_kv_heads, const int32_t* positions, const int64_t* slot_mapping,
+                                 int num_tokens, void* k_cache, void* v_cache, int num_blocks, int block_size,
+                                 int head_dim, int rotary_dim, pa_rope_layout layout, const uint64_t* steps,
+                                 float amplitude, pa_dtype dtype, void* stream) {
+  if (dtype != PA_F32 && dtype != PA_BF16) return PA_ERR_DTYPE;
+  if (num_tokens < 0 || !heads_in_range(num_heads) || !heads_in_range(num_kv_heads) || num_kv_heads == 0 || num_blocks <= 0 || !supported_head_dim(head_dim) ||
+      !supported_block_size(block_size) || !rotary_shape(head_dim, rotary_dim) ||
+      (layout != PA_ROPE_HALF && layout != PA_ROPE_INTERLEAVED))
+    return PA_ERR_SHAPE;
+  if (num_tokens == 0) return PA_OK;
+  if ((num_heads && (!q || !q_out)) || !key || !value || !positions || !slot_mapping || !k_cache || !v_cache || !steps)
+    return PA_ERR_NULL;
+  const int e = elem_bytes(dtype);
+  const Rows qs{q, q_token_stride, q_head_stride}, qd{q_out, q_out_token_stride, q_out_head_stride};
+  const Rows ks{key, key_token_stride, key_head_stride}, vs{value, value_token_stride, value_head_stride};
+  const long long row = (long long)num_kv_heads * head_dim;
+  const Rows kd{k_cache, row, head_dim};
+  if ((num_heads && (!aligned_rows(qs, e) || !aligned_rows(qd, e))) || !aligned_rows(ks, e) || !aligned_rows(vs, e) ||
+      !aligned16(k_cache) || !aligned16(v_cache))
+    return PA_ERR_ALIGN;
+  const bool half = layout == PA_ROPE_HALF;
+  RopeParams p = {};
+  if (num_heads) p.q = turned_part(qd, qs, num_heads, head_dim, rotary_dim, e, half, false);
+  p.k = turned_part(kd, ks, num_kv_heads, head_dim, rotary_dim, e, half, true);
+  p.c = copied_part(v_cache, row, vs, num_kv_heads, head_dim, e);
+  p.positions = positions;
+  p.slots = slot_mapping;
+  p.num_slots = (long long)num_blocks * block_size;
+  p.steps = steps;
+  p.amplitude = amplitude;
+  p.n = num_tokens;
+  p.pairs = rotary_dim / 2;
+  return launch(p, dtype, half, stream);
+}
+
+extern "C" int pa_latent_append(const void* latent, long long latent_stride, const void* key_rope,
+                                long long key_rope_stride, void* query_out, long long query_out_token_stride,
+                                long long query_out_head_stride, const void* query, long long query_token_stride,
+                                long long query_head_stride, int num_heads, const int32_t* positions,
+                                const int64_t* slot_mapping, int num_tokens, void* cache, int num_blocks,
+                                int block_size, int latent_dim, int rope_dim, pa_rope_layout layout,
+                                const uint64_t* steps, float amplitude, pa_dtype dtype, void* stream) {
+  if (dtype != PA_F32 && dtype != PA_BF16) return PA_ERR_DTYPE;
+  if (num_tokens < 0 || !heads_in_range(num_heads) || num_blocks <= 0 || !latent_shape(latent_dim, rope_dim, block_size) ||
+      (layout != PA_ROPE_HALF && layout != PA_ROPE_INTERLEAVED))
+    return PA_ERR_SHAPE;
+  if (num_tokens == 0) return PA_OK;
+  if (!latent || !key_rope || (num_heads && (!query || !query_out)) || !positions || !slot_mapping || !cache || !steps)
+    return PA_ERR_NULL;
+  const int e = elem_bytes(dtype);
+  const long long row = latent_dim + rope_dim;
+  const Rows ls{latent, latent_stride, 0}, ks{key_rope, key_rope_stride, 0};
+  const Rows qs{query, query_token_stride, query_head_stride};
+  const Rows qd{query_out, query_out_token_stride, query_out_head_stride};
+  if (!aligned_rows(ls, e) || !aligned_rows(ks, e) || !aligned16(cache) ||
+      (num_heads && (!aligned_rows(qs, e) || !aligned_rows(qd, e))))
+    return PA_ERR_ALIGN;
+  const bool half = layout == PA_ROPE_HALF;
+  RopeParams p = {};
+  if (num_heads) p.q = turned_part(qd, qs, num_heads, rope_dim, rope_dim, e, half, false);
+  const Rows kd{static_cast<char*>(cache) + (size_t)latent_dim * e, row, 0};
+  p.k = turned_part(kd, ks, 1, rope_dim, rope_dim, e, half, true);
+  p.c = copied_part(cache, row, ls, 1, latent_dim, e);
+  p.positions = positions;
+  p.slots = slot_mapping;
+  p.num_slots = (long long)num_blocks * block_size;
+  p.steps = steps;
+  p.amplitude = amplitude;
+  p.n = num_tokens;
+  p.pairs = rope_dim / 2;
+  return launch(p, dtype, half, stream);
+}
