@@ -787,32 +787,32 @@ int pa_latent_append(const void* latent, long long latent_stride, const void* ke
  *                  num_seqs).  A bad pair sets PA_DEV_BAD_LEN, and that
  *                  sequence writes nothing.
  *   scale          > 0
- *   partition_size as for pa_decode; pa_latent_decode_partition_size returns
- *                  the size used
  *   workspace      at least pa_latent_decode_workspace_bytes() with the same
- *                  sizes, 16-byte aligned (may be NULL when that is 0);
- *                  contents on entry do not matter, calls that share one must
- *                  be ordered
+ *                  sizes, 16-byte aligned; contents on entry do not matter,
+ *                  calls that share one must be ordered
  *   dtype          PA_BF16
  *
  * A context length outside its table row is clamped and sets PA_DEV_BAD_LEN, a
  * block id outside the pool is read as block 0 and sets PA_DEV_BAD_BLOCK.  A
  * table row holds at most 2^30 tokens, total_queries * num_heads < 2^31.
  * Accumulation is fp32; the softmax weights are rounded to bf16 for their
- * product with the values.
+ * product with the values.  A cached row that holds a NaN makes NaN of the rows
+ * that see it, whole; the rows before it are not touched.
+ *
+ * The batch's tokens are divided evenly among the SMs by the lengths on the
+ * device, and what a cut divides is joined by a second kernel (outside stream
+ * capture its launch is a programmatic dependent of the first's): the same call
+ * gives the same bits, another batch around a sequence may round it otherwise.
  */
 int pa_latent_decode(void* out, const void* query, const int32_t* query_start, int total_queries,
                      const void* cache, const int32_t* block_tables, int max_blocks_per_seq,
                      const int32_t* context_lens, int num_seqs, int num_heads, int latent_dim, int rope_dim,
-                     int block_size, int num_blocks, float scale, int partition_size,
+                     int block_size, int num_blocks, float scale,
                      void* workspace, size_t workspace_bytes, pa_dtype dtype, void* stream);
 
-/* Bytes of workspace pa_latent_decode needs for these sizes, and the partition
- * size (tokens) it uses.  Pure host arithmetic; no CUDA call. */
-size_t pa_latent_decode_workspace_bytes(int total_queries, int num_seqs, int num_heads, int latent_dim,
-                                        int max_blocks_per_seq, int block_size, int partition_size);
-int pa_latent_decode_partition_size(int total_queries, int num_seqs, int num_heads, int latent_dim,
-                                    int max_blocks_per_seq, int block_size, int partition_size);
+/* Bytes of workspace pa_latent_decode needs for these sizes (whatever the
+ * table's).  Pure host arithmetic; no CUDA call. */
+size_t pa_latent_decode_workspace_bytes(int total_queries, int num_seqs, int num_heads, int latent_dim);
 
 /*
  * Attention over latent vectors in their expanded form (prompts): keys and

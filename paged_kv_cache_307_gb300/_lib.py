@@ -90,13 +90,10 @@ lib.pa_rope_and_cache.restype = _i
 lib.pa_latent_append.argtypes = [_p, _ll, _p, _ll, *_rows3, *_rows3, _i, _i32p, _i64p, _i, _p, _i, _i, _i, _i, _i, _p,
                                  _f, _i, _p]
 lib.pa_latent_append.restype = _i
-lib.pa_latent_decode.argtypes = [_p, _p, _i32p, _i, _p, _i32p, _i, _i32p, _i, _i, _i, _i, _i, _i, _f, _i, _p, _sz, _i,
-                                 _p]
+lib.pa_latent_decode.argtypes = [_p, _p, _i32p, _i, _p, _i32p, _i, _i32p, _i, _i, _i, _i, _i, _i, _f, _p, _sz, _i, _p]
 lib.pa_latent_decode.restype = _i
-lib.pa_latent_decode_workspace_bytes.argtypes = [_i, _i, _i, _i, _i, _i, _i]
+lib.pa_latent_decode_workspace_bytes.argtypes = [_i, _i, _i, _i]
 lib.pa_latent_decode_workspace_bytes.restype = _sz
-lib.pa_latent_decode_partition_size.argtypes = [_i, _i, _i, _i, _i, _i, _i]
-lib.pa_latent_decode_partition_size.restype = _i
 lib.pa_latent_prefill.argtypes = [_p, _p, _i32p, _i, _p, _p, _ll, _i32p, _i, _i, _i, _i, _i, _i, _f, _i, _p]
 lib.pa_latent_prefill.restype = _i
 lib.pa_last_error.argtypes = []
@@ -717,17 +714,15 @@ def latent_append(latent, key_rope, positions, slot_mapping, cache, steps, ampli
     return query if query_out is None else query_out
 
 
-def alloc_latent_workspace(q, cache, block_tables, partition_size=0):
+def alloc_latent_workspace(q, cache, block_tables):
     """Workspace for latent_decode with these sizes."""
     rows, H, width = q.shape
     R = (width - 16) // 128 * 128            # the one latent_dim of rows of this width
-    n = lib.pa_latent_decode_workspace_bytes(rows, block_tables.shape[0], H, R, block_tables.shape[1], cache.shape[1],
-                                             partition_size)
+    n = lib.pa_latent_decode_workspace_bytes(rows, block_tables.shape[0], H, R)
     return torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
 
 
-def latent_decode(out, q, cache, block_tables, context_lens, scale, query_start=None, partition_size=0,
-                  workspace=None, stream=None):
+def latent_decode(out, q, cache, block_tables, context_lens, scale, query_start=None, workspace=None, stream=None):
     """out[rows, H, R] = attention of q[rows, H, R + P] over a latent cache [NB, bs, R + P], whose rows' first R
     elements are the values too.  One row a sequence, or sequence b's rows are query_start[b]..query_start[b+1]-1,
     the last tokens of its context, causal."""
@@ -747,10 +742,10 @@ def latent_decode(out, q, cache, block_tables, context_lens, scale, query_start=
     elif rows != B:
         raise ValueError("one query row per sequence")
     if workspace is None:
-        workspace = _own(alloc_latent_workspace, stream, q, cache, block_tables, partition_size)
+        workspace = _own(alloc_latent_workspace, stream, q, cache, block_tables)
     dev = _ready(out, q, cache, block_tables, context_lens, workspace)
     _check(lib.pa_latent_decode(out.data_ptr(), q.data_ptr(), start, rows, cache.data_ptr(), block_tables.data_ptr(),
-                                cols, context_lens.data_ptr(), B, H, R, width - R, bs, NB, scale, partition_size,
+                                cols, context_lens.data_ptr(), B, H, R, width - R, bs, NB, scale,
                                 workspace.data_ptr(), workspace.nbytes, kind, _on(stream, dev)), "pa_latent_decode")
     return out
 

@@ -1,113 +1,764 @@
 // pa_latent_decode.cu — attention over a paged cache of one latent vector a token, in the
-// absorbed form (pa_latent_decode): the rows are the keys, and their latent part the values.
+// absorbed form (pa_latent_decode), on the 5th-generation tensor cores: the cached rows are
+// the keys, and their latent part the values.
 //
-// One CTA per (query row, head): scores of 64 tokens at a time by the warps, a running maximum
-// and sum, and a thread per two latent elements for the values.
-#include "pa_common.cuh"
+// Rows of a sequence are (query position, head) pairs.  A CTA takes NR = 16, 32 or 64 of them
+// against tiles of 128 tokens, tokens in the accumulators' lanes:
+//   S^T[128 tokens x NR] = C[128 x (R + P)] Q^T     A = the tile (K-major), B = Q rows
+//   O^T[R dims x NR]    += C^T[R x 128] P^T         A = the same bytes (MN-major), B = P
+// so a tile is read into shared memory once for both products, and few heads cost few
+// columns and not padded rows.
+#include <stddef.h>
+
+#include "pa_mma.cuh"
+#include "pa_tc.cuh"
 
 namespace pa {
 namespace {
 
 __device__ unsigned g_status_latent;
 
-constexpr int kThreads = 256;
-constexpr int kTile = 64;
+constexpr int kTile = 128;                   // tokens per tile
+constexpr int kThreads = 192;                // warps 0-3 softmax, 4 TMA, 5 MMA
+constexpr uint32_t kChunk = 16384;           // 128 tokens x 64 elements
+constexpr uint32_t kPair = 2 * kChunk;       // 128 elements: one M = 128 product of O^T
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.f;                // log2 units a score may exceed its reference by
+constexpr uint32_t kSmemMax = 232448;        // 227 KB
+constexpr int kMaxSlots = 6;
 
 struct LatentParams {
   __nv_bfloat16* out;
-  const __nv_bfloat16* q;
-  const __nv_bfloat16* cache;
-  const int32_t* query_start;
+  const int32_t* query_start;                // null: one row a sequence
   const int32_t* block_tables;
   const int32_t* context_lens;
+  float* ws_o;                               // [2 * CTAs, NR, R] partial sums
+  float* ws_ml;                              // [2 * CTAs, NR, 2] their maximum and sum
+  long long* ws_base;                        // [B + 1] units before each sequence
+  int32_t* ws_group;                         // [B + 1] row groups before each sequence
   int B, H, R, P, rows, max_blocks, bs, num_blocks;
+  int cl;                                    // CTAs that take neighbouring row groups over the same tokens
   float qscale;
 };
 
-__global__ void __launch_bounds__(kThreads) latent_decode_kernel(const LatentParams p) {
-  __shared__ float qs[576], sc[kTile];
-  __shared__ const __nv_bfloat16* at[kTile];
-  const int row = blockIdx.x / p.H, h = blockIdx.x % p.H;
-  int b = row, i = 0, n = 1;
-  if (p.query_start) {
-    int a = 0, e = 0;
-    bool found = false, bad = false;
-    for (int s = 0; s < p.B; ++s) {
-      const int x = p.query_start[s], y = p.query_start[s + 1];
-      const bool ok = x >= 0 && y >= x && y <= p.rows;
-      bad |= !ok;
-      if (ok && row >= x && row < y) {
-        b = s;
-        a = x;
-        e = y;
-        found = true;
-      }
-    }
-    if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_status_latent, PA_DEV_BAD_LEN);
-    if (!found) return;
-    i = row - a;
-    n = e - a;
-    if (i < 0 || i >= n) return;
-  }
-  const int Lmax = p.max_blocks * p.bs;
-  int L = p.context_lens[b];
-  if (L < 0 || L > Lmax) {
-    if (threadIdx.x == 0) atomicOr(&g_status_latent, PA_DEV_BAD_LEN);
-    L = L < 0 ? 0 : Lmax;
-  }
-  const int end = L - n + i + 1;               // tokens that the row sees
-  const int W = p.R + p.P;
-  const size_t r = (size_t)row * p.H + h;
-  for (int d = threadIdx.x; d < W; d += kThreads) qs[d] = __bfloat162float(p.q[r * W + d]);
-  float m = -INFINITY, l = 0.f, o[2] = {0.f, 0.f};
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int t0 = 0; t0 < end; t0 += kTile) {
-    __syncthreads();
-    const int nt = min(kTile, end - t0);
-    for (int t = warp; t < nt; t += kThreads / 32) {
-      int id = p.block_tables[(size_t)b * p.max_blocks + (t0 + t) / p.bs];
-      if ((unsigned)id >= (unsigned)p.num_blocks) {
-        if (lane == 0) atomicOr(&g_status_latent, PA_DEV_BAD_BLOCK);
-        id = 0;
-      }
-      const __nv_bfloat16* c = p.cache + ((size_t)id * p.bs + (t0 + t) % p.bs) * W;
-      float s = 0.f;
-      for (int d = lane; d < W; d += 32) s = fmaf(qs[d], __bfloat162float(c[d]), s);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      if (lane == 0) {
-        sc[t] = s * p.qscale;
-        at[t] = c;
-      }
-    }
-    __syncthreads();
-    float mx = m;
-    for (int t = 0; t < nt; ++t) mx = fmaxf(mx, sc[t]);
-    const float f = m == -INFINITY ? 0.f : exp2f(m - mx);
-    l *= f;
-    o[0] *= f;
-    o[1] *= f;
-    m = mx;
-    for (int t = 0; t < nt; ++t) {
-      const float w = mx == -INFINITY ? 0.f : exp2f(sc[t] - mx);
-      l += w;
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (threadIdx.x + k * kThreads < p.R) o[k] = fmaf(w, __bfloat162float(at[t][threadIdx.x + k * kThreads]), o[k]);
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    if (threadIdx.x + k * kThreads < p.R)
-      p.out[r * p.R + threadIdx.x + k * kThreads] = __float2bfloat16_rn(l != 0.f ? o[k] / l : 0.f);
+template <int NR>
+struct Shared {
+  uint64_t full[kMaxSlots], empty[kMaxSlots], full_r[2], empty_r[2];
+  uint64_t q_full, q_empty, s[2], p, pv, o_free, drain;
+  alignas(16) float neg_m[NR];               // minus the reference of every row
+  alignas(16) float f[NR];
+  alignas(16) float red[4][NR];              // per warp: maxima, at the end sums
+  long long scan[8];
+  long long first_off;
+  int first_b;
+  uint32_t tmem_base;
+  int abort;
+};
+
+// Shared memory: Q [NC chunks][NR rows][128 B], a ring of SLOTS pairs, the rotated keys' chunk
+// (P behind it where two of them and P's own 16 KB leave no room for a second tile's first pair).
+template <int NR, int RC>
+struct Layout {
+  static constexpr int NC = RC + 1, NP = RC / 2;
+  static constexpr bool kAlias = RC >= 6;
+  static constexpr uint32_t kQ = NC * NR * 128u;
+  static constexpr uint32_t kFixed = kQ + (kAlias ? kChunk : 3 * kChunk) + (uint32_t)sizeof(Shared<NR>) + 1024u;
+  static constexpr int kFit = (int)((kSmemMax - kFixed) / kPair);
+  static constexpr int kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
+  static constexpr uint32_t kOffRing = kQ, kOffRope = kOffRing + kSlots * kPair;
+  static constexpr uint32_t kOffP = kAlias ? kOffRope : kOffRope + 2 * kChunk;
+  static constexpr uint32_t kOffShared = kOffP + kChunk;
+  static constexpr uint32_t kBytes = kOffShared + (uint32_t)sizeof(Shared<NR>) + 1024u;
+  static constexpr uint32_t kCols = 2 * NR + NP * NR;
+  static constexpr uint32_t kTmem = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+  static_assert(kSlots >= NP && kBytes <= kSmemMax, "shared memory");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Barrier 2 of the 128 softmax threads, true for all if true for any.
+__device__ __forceinline__ bool vote128(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r) : "r"(x ? 1u : 0u) : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try_wait(smem_u32(bar), parity)) return true;
+  if (*abort_flag) return false;
+  if (mbar_wait(bar, parity)) return true;
+  atomicOr(&g_status_latent, PA_DEV_TIMEOUT);
+  *abort_flag = 1;
+  return false;
 }
 
-bool good_sizes(int total, int num_seqs, int num_heads, int latent_dim, int max_blocks, int bs, int partition_size) {
-  return total >= 0 && num_seqs >= 0 && num_heads > 0 && latent_shape(latent_dim, 16, bs) && max_blocks > 0 &&
-         (long long)max_blocks * bs <= kMaxRowTokens && !(partition_size > 0 && partition_size % bs) &&
-         (long long)total * num_heads <= 0x7fffffffll;
+// A sequence: its first row, rows, context, and tiles (one at least, which writes the zeros).
+struct Seq {
+  int q0, n, L, tiles;
+};
+__device__ __forceinline__ Seq seq_of(const LatentParams& p, int b, bool flag) {
+  Seq s{b, 1, 0, 1};
+  if (p.query_start) {
+    s.q0 = __ldg(&p.query_start[b]);
+    const int e = __ldg(&p.query_start[b + 1]);
+    s.n = s.q0 >= 0 && e >= s.q0 && e <= p.rows ? e - s.q0 : -1;
+  }
+  const int L = __ldg(&p.context_lens[b]), most = p.max_blocks * p.bs;
+  s.L = L < 0 ? 0 : min(L, most);
+  if (flag && (s.n < 0 || s.L != L)) atomicOr(&g_status_latent, PA_DEV_BAD_LEN);
+  if (s.n < 0) s.n = 0;
+  s.tiles = max(1, (s.L + kTile - 1) / kTile);
+  return s;
 }
+__device__ __forceinline__ int groups_of(const LatentParams& p, const Seq& s, int nr) { return (s.n * p.H + nr - 1) / nr; }
+
+// A CTA's work: consecutive units of the line of all (sequence, cl row groups, tile).  The
+// line is cut into equal parts, so that every CTA has as many tiles whatever the lengths are;
+// what a cut leaves in two CTAs is joined by the second kernel.
+struct Item {
+  int b, r0, rows;                           // row group: first row of the sequence's, rows of it
+  int tile, nt;                              // first tile, tiles with something to see
+  int end, L, n, q0;                         // tokens that any of its rows sees
+  bool whole;
+  int slot;
+};
+template <int NR>
+struct Walk {
+  int b, half, part;
+  long long off, left;
+  bool first;
+  __device__ __forceinline__ bool next(const LatentParams& p, Item& it) {
+    while (left > 0) {
+      const Seq s = seq_of(p, b, false);
+      const int supers = (groups_of(p, s, NR) + p.cl - 1) / p.cl;
+      if (off >= (long long)supers * s.tiles) {
+        ++b;
+        off = 0;
+        continue;
+      }
+      const int sg = (int)(off / s.tiles);
+      const int t = (int)(off - (long long)sg * s.tiles);
+      const int cnt = (int)min((long long)(s.tiles - t), left);
+      off += cnt;
+      left -= cnt;
+      const bool was_first = first;
+      first = false;
+      it.b = b;
+      it.r0 = (sg * p.cl + half) * NR;
+      it.rows = min(NR, s.n * p.H - it.r0);
+      if (it.rows <= 0) continue;
+      it.end = min(s.L, max(0, s.L - s.n + (it.r0 + it.rows - 1) / p.H + 1));
+      it.tile = t;
+      it.nt = max(0, min(t + cnt, (it.end + kTile - 1) / kTile) - t);
+      it.L = s.L;
+      it.n = s.n;
+      it.q0 = s.q0;
+      it.whole = cnt == s.tiles;
+      it.slot = (part * p.cl + half) * 2 + (was_first ? 0 : 1);
+      return true;
+    }
+    return false;
+  }
+};
+
+// Sum of every x[i] over the warp: lane's x[0] is column col(lane)'s, NR / 32 more behind it.
+template <int N>
+__device__ __forceinline__ void warp_sums(float (&x)[N], int lane) {
+  int n = N;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    if (n > 1) {
+      n /= 2;
+      const bool up = lane & off;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        if (i < n) {
+          const float keep = up ? x[i + n] : x[i], give = up ? x[i] : x[i + n];
+          x[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+        }
+      }
+    } else {
+      x[0] += __shfl_xor_sync(0xffffffffu, x[0], off);
+    }
+  }
+}
+
+template <int NR, int RC>
+__global__ void __launch_bounds__(kThreads, 1)
+latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_constant__ CUtensorMap mapQ,
+                     const LatentParams p) {
+  using Lay = Layout<NR, RC>;
+  constexpr int NC = Lay::NC, NP = Lay::NP, SLOTS = Lay::kSlots;
+  constexpr bool kAlias = Lay::kAlias;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  Shared<NR>* sh = reinterpret_cast<Shared<NR>*>(smem + Lay::kOffShared);
+  volatile int* abort_flag = &sh->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < SLOTS; ++i) {
+      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->full_r[i], 1);
+      mbar_init(&sh->empty_r[i], 1);
+      mbar_init(&sh->s[i], 1);
+    }
+    mbar_init(&sh->q_full, 1);
+    mbar_init(&sh->q_empty, 1);
+    mbar_init(&sh->p, 128);
+    mbar_init(&sh->pv, 1);
+    mbar_init(&sh->o_free, 128);
+    mbar_init(&sh->drain, 1);
+    sh->abort = 0;
+    sh->first_b = p.B;
+    fence_mbar_init();
+    prefetch_tensormap(&mapC);
+    prefetch_tensormap(&mapQ);
+  }
+  if (warp == 5) {
+    tmem_alloc(&sh->tmem_base, Lay::kTmem);
+    tmem_relinquish();
+  }
+
+  // ---- this CTA's part of the line
+  const int parts = gridDim.x / p.cl, part = blockIdx.x / p.cl;
+  Walk<NR> walk;
+  {
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
+    const bool note = blockIdx.x == 0;
+    long long sum = 0;
+    int groups = 0;
+    for (int b = b0; b < b1; ++b) {
+      const Seq s = seq_of(p, b, note);
+      const int g = groups_of(p, s, NR);
+      sum += (long long)((g + p.cl - 1) / p.cl) * s.tiles;
+      groups += g;
+    }
+    long long incl = sum;
+    int gincl = groups;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+      const int z = __shfl_up_sync(0xffffffffu, gincl, off);
+      if (lane >= off) {
+        incl += y;
+        gincl += z;
+      }
+    }
+    if (lane == 31) {
+      sh->scan[warp] = incl;
+      sh->red[0][warp] = __int_as_float(gincl);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    long long total = 0, before = incl - sum;
+    int gbefore = gincl - groups;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      total += sh->scan[w];
+      if (w < warp) {
+        before += sh->scan[w];
+        gbefore += __float_as_int(sh->red[0][w]);
+      }
+    }
+    // (no empty parts: a line shorter than the grid leaves its last CTAs without work)
+    const long long cuts = min((long long)parts, total);
+    const long long u0 = part < cuts ? total * part / cuts : total, u1 = part < cuts ? total * (part + 1) / cuts : total;
+    if (u0 >= before && u0 < before + sum) {     // (one thread, where there is anything)
+      long long at = before;
+      for (int b = b0; b < b1; ++b) {
+        const Seq s = seq_of(p, b, false);
+        const long long u = (long long)((groups_of(p, s, NR) + p.cl - 1) / p.cl) * s.tiles;
+        if (u0 < at + u) {
+          sh->first_b = b;
+          sh->first_off = u0 - at;
+          break;
+        }
+        at += u;
+      }
+    }
+    if (note && p.ws_base) {
+      for (int b = b0; b < b1; ++b) {
+        const Seq s = seq_of(p, b, false);
+        const int g = groups_of(p, s, NR);
+        p.ws_base[b] = before;
+        p.ws_group[b] = gbefore;
+        before += (long long)((g + p.cl - 1) / p.cl) * s.tiles;
+        gbefore += g;
+      }
+      if (b0 < b1 && b1 == p.B) {
+        p.ws_base[p.B] = before;
+        p.ws_group[p.B] = gbefore;
+      }
+    }
+    __syncthreads();
+    walk.b = sh->first_b;
+    walk.off = sh->first_off;
+    walk.left = walk.b < p.B ? u1 - u0 : 0;
+    walk.half = blockIdx.x % p.cl;
+    walk.part = part;
+    walk.first = true;
+  }
+  const uint32_t tmem = sh->tmem_base;
+  const uint32_t tO = tmem + 2 * NR;
+  Item it;
+
+  if (warp == 4) {
+    // ------------------------------------------------------------ TMA producer
+    const uint64_t pol = policy_evict_first(), pol_q = policy_evict_first();
+    const int bsh = 31 - __clz(p.bs);
+    const uint32_t box = (uint32_t)p.bs * 128u;
+    int kp = 0, kr = 0, kq = 0;              // pairs, rotated chunks and query groups requested
+    bool ok = true;
+    while (ok && walk.next(p, it)) {
+      if (it.nt == 0) continue;
+      const int32_t* row = p.block_tables + (size_t)it.b * p.max_blocks;
+      auto id_of = [&](int j) -> int {
+        const int t = (it.tile + j) * kTile + (lane << bsh);
+        return j < it.nt && lane < (kTile >> bsh) && t < it.end ? __ldg(&row[t >> bsh]) : 0;
+      };
+      int blk = id_of(0);
+      ok = __all_sync(0xffffffffu, wait(&sh->q_empty, (uint32_t)(kq & 1) ^ 1u, abort_flag));
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&sh->q_full, (uint32_t)NC * NR * 128u);
+      __syncwarp();
+      if (lane < NC)
+        tma_load_4d(smem + lane * NR * 128, &mapQ, &sh->q_full, lane * 64, it.q0 * p.H + it.r0, 0, 0, pol_q);
+      ++kq;
+      for (int j = 0; j < it.nt; ++j) {
+        const int next = id_of(j + 1);
+        const int nb = (min(kTile, it.end - (it.tile + j) * kTile) + p.bs - 1) >> bsh;
+        if (lane < nb && (unsigned)blk >= (unsigned)p.num_blocks) {
+          atomicOr(&g_status_latent, PA_DEV_BAD_BLOCK);
+          blk = 0;                           // keep every copy inside the pool
+        }
+        for (int i = 0; i < NP; ++i, ++kp) {
+          const int sl = kp % SLOTS;
+          ok = __all_sync(0xffffffffu, wait(&sh->empty[sl], ((uint32_t)(kp / SLOTS) & 1u) ^ 1u, abort_flag));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&sh->full[sl], 2u * nb * box);
+          __syncwarp();
+          if (lane < nb) {
+            unsigned char* dst = smem + Lay::kOffRing + sl * kPair + lane * box;
+            tma_load_4d(dst, &mapC, &sh->full[sl], i * 128, 0, blk, 0, pol);
+            tma_load_4d(dst + kChunk, &mapC, &sh->full[sl], i * 128 + 64, 0, blk, 0, pol);
+          }
+        }
+        if (!ok) break;
+        const int sr = kAlias ? 0 : kr & 1;
+        const uint32_t use = kAlias ? (uint32_t)kr : (uint32_t)kr >> 1;
+        ok = __all_sync(0xffffffffu, wait(&sh->empty_r[sr], (use & 1u) ^ 1u, abort_flag));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&sh->full_r[sr], (uint32_t)nb * box);
+        __syncwarp();
+        if (lane < nb)
+          tma_load_4d(smem + Lay::kOffRope + sr * kChunk + lane * box, &mapC, &sh->full_r[sr], RC * 64, 0, blk, 0, pol);
+        ++kr;
+        blk = next;
+      }
+    }
+    // no TMA write may land after the CTA has left
+    if (lane == 0) {
+      for (int k = max(0, kp - SLOTS); k < kp; ++k) mbar_wait(&sh->full[k % SLOTS], (uint32_t)(k / SLOTS) & 1u);
+      for (int k = max(0, kr - (kAlias ? 1 : 2)); k < kr; ++k)
+        mbar_wait(&sh->full_r[kAlias ? 0 : k & 1], (uint32_t)(kAlias ? k : k >> 1) & 1u);
+      if (kq > 0) mbar_wait(&sh->q_full, (uint32_t)(kq - 1) & 1u);
+    }
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_bf16_f32(kTile, NR, false, false);
+      constexpr uint32_t idO = idesc_bf16_f32(kTile, NR, true, true);
+      const uint64_t dk = sdesc_sw128(sbase + Lay::kOffRing, 16, 1024);            // the tile as K
+      const uint64_t dv = sdesc_sw128(sbase + Lay::kOffRing, kChunk, 1024);        // the tile as V^T
+      const uint64_t dr = sdesc_sw128(sbase + Lay::kOffRope, 16, 1024);
+      const uint64_t dq = sdesc_sw128(sbase, 16, 1024);
+      const uint64_t dp = sdesc_sw128(sbase + Lay::kOffP, kChunk, 1024);
+      constexpr int kEarly = SLOTS - NP < NP ? SLOTS - NP : NP;   // pairs of the next tile that a tile leaves room for
+      constexpr bool kAllEarly = kEarly == NP && !kAlias;
+      const int rope_steps = p.P / 16;
+      int kt = 0, kq = 0;                    // tiles, query groups
+      // pairs [a, b) of tile k's scores
+      auto scores = [&](int k, int a, int b) -> bool {
+        for (int i = a; i < b; ++i) {
+          const int u = k * NP + i, sl = u % SLOTS;
+          if (!wait(&sh->full[sl], (uint32_t)(u / SLOTS) & 1u, abort_flag)) return false;
+          tc_fence_after();
+          const uint64_t da = sdesc_at(dk, sl * kPair), db = sdesc_at(dq, i * 2 * NR * 128);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_bf16(tmem + (k & 1) * NR, sdesc_at(da, (kk >> 2) * kChunk + (kk & 3) * 32),
+                      sdesc_at(db, (kk >> 2) * NR * 128 + (kk & 3) * 32), idS, i > 0 || kk > 0 ? 1u : 0u);
+        }
+        return true;
+      };
+      auto scores_end = [&](int k, bool last) -> bool {
+        const int sr = kAlias ? 0 : k & 1;
+        if (!wait(&sh->full_r[sr], (uint32_t)(kAlias ? k : k >> 1) & 1u, abort_flag)) return false;
+        tc_fence_after();
+        const uint64_t da = sdesc_at(dr, sr * kChunk), db = sdesc_at(dq, RC * NR * 128);
+        for (int kk = 0; kk < rope_steps; ++kk)
+          umma_bf16(tmem + (k & 1) * NR, sdesc_at(da, kk * 32), sdesc_at(db, kk * 32), idS, 1u);
+        umma_commit(&sh->s[k & 1]);
+        if (!kAlias) umma_commit(&sh->empty_r[sr]);
+        if (last) umma_commit(&sh->q_empty);
+        return true;
+      };
+      bool ok = true;
+      while (ok && walk.next(p, it)) {
+        if (it.nt == 0) continue;
+        ok = wait(&sh->q_full, (uint32_t)kq & 1u, abort_flag) && scores(kt, 0, NP) && scores_end(kt, it.nt == 1);
+        for (int j = 0; ok && j < it.nt; ++j, ++kt) {
+          const bool more = j + 1 < it.nt;
+          if (more && kEarly > 0) {
+            if (!(ok = scores(kt + 1, 0, kEarly))) break;
+            if (kAllEarly && !(ok = scores_end(kt + 1, j + 2 == it.nt))) break;
+          }
+          if (!(ok = wait(&sh->p, (uint32_t)kt & 1u, abort_flag))) break;
+          if (j == 0 && !(ok = wait(&sh->o_free, ((uint32_t)kq & 1u) ^ 1u, abort_flag))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            const int sl = (kt * NP + i) % SLOTS;
+            const uint64_t da = sdesc_at(dv, sl * kPair);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)   // 16 tokens each
+              umma_bf16(tO + i * NR, sdesc_at(da, kk * 2048), sdesc_at(dp, kk * 2048), idO, j > 0 || kk > 0 ? 1u : 0u);
+            umma_commit(&sh->empty[sl]);
+          }
+          umma_commit(&sh->pv);
+          if (kAlias) umma_commit(&sh->empty_r[0]);
+          if (more && !kAllEarly) {
+            if (!(ok = scores(kt + 1, kEarly, NP))) break;
+            if (!(ok = scores_end(kt + 1, j + 2 == it.nt))) break;
+          }
+        }
+        ++kq;
+      }
+      umma_commit(&sh->drain);               // every MMA has completed before TMEM is freed
+      mbar_wait(&sh->drain, 0);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int r = (int)threadIdx.x;          // token of the tile, latent dim at the end; TMEM lane
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    int kt = 0;
+    float l[NR];
+    while (walk.next(p, it)) {
+      const int past = it.L - it.n;          // position of the sequence's first row
+#pragma unroll
+      for (int c = 0; c < NR; ++c) l[c] = 0.f;
+      for (int j = 0; j < it.nt; ++j, ++kt) {
+        const int st = kt & 1;
+        const int t = (it.tile + j) * kTile + r;
+        wait(&sh->s[st], (uint32_t)(kt >> 1) & 1u, abort_flag);
+        __syncwarp();
+        tc_fence_after();
+        float s[NR];
+        {
+          uint32_t v[NR];
+#pragma unroll
+          for (int c = 0; c < NR; c += 16) tmem_ld16(tmem + st * NR + c + lane_off, reinterpret_cast<uint32_t(&)[16]>(v[c]));
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < NR; ++c) s[c] = __uint_as_float(v[c]);
+        }
+        // rows (t - past) H and on of the sequence see token t
+        const int hide = t >= it.end ? NR : (int)max(-1ll, min((long long)NR, (long long)(t - past) * p.H - it.r0));
+        if (__any_sync(0xffffffffu, hide > 0)) {
+#pragma unroll
+          for (int c = 0; c < NR; ++c)
+            if (c < hide) s[c] = -INFINITY;
+        }
+        // exponents, against the references as they are
+        bool need = j == 0;
+        if (j > 0) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < NR; c += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(&sh->neg_m[c]);
+            top = fmax3(top, fmaf(s[c], p.qscale, m.x), fmaf(s[c + 1], p.qscale, m.y));
+            top = fmax3(top, fmaf(s[c + 2], p.qscale, m.z), fmaf(s[c + 3], p.qscale, m.w));
+          }
+          need = top > kSlack;
+        }
+        need = vote128(need);
+        // P, and with it the rotated keys' chunk, is free; O holds the tile before
+        if (kt > 0) wait(&sh->pv, (uint32_t)(kt - 1) & 1u, abort_flag);
+        __syncwarp();
+        if (need) {
+          // new references: the tile's maxima where they are above
+#pragma unroll
+          for (int c = 0; c < NR; ++c) {
+            const float x = warp_max(s[c]);
+            if (lane == 0) sh->red[warp][c] = x;
+          }
+          named_sync(1, 128);
+          if (r < NR) {
+            const float x = fmaxf(fmaxf(sh->red[0][r], sh->red[1][r]), fmaxf(sh->red[2][r], sh->red[3][r])) * p.qscale;
+            const float old = j > 0 ? -sh->neg_m[r] : -INFINITY;
+            const float m = fmaxf(old, x);
+            sh->f[r] = old == -INFINITY ? 0.f : exp2f(old - m);
+            // (a row that sees nothing of its first tile sees nothing of the later ones)
+            sh->neg_m[r] = m == -INFINITY ? 0.f : -m;
+          }
+          named_sync(1, 128);
+          if (j > 0) {
+#pragma unroll
+            for (int c = 0; c < NR; ++c) l[c] *= sh->f[c];
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < NP * NR; c += 16) {
+              uint32_t v[16];
+              tmem_ld16(tO + c + lane_off, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * sh->f[c % NR + i]);
+              tmem_st16(tO + c + lane_off, v);
+            }
+            tmem_st_wait();
+          }
+        }
+        // P: row r of an MN-major tile, 8 columns a 16-byte piece
+        unsigned char* prow = smem + Lay::kOffP + r * 128;
+#pragma unroll
+        for (int c = 0; c < NR; c += 8) {
+          const float4 m0 = *reinterpret_cast<const float4*>(&sh->neg_m[c]);
+          const float4 m1 = *reinterpret_cast<const float4*>(&sh->neg_m[c + 4]);
+          const float nm[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+          float e[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            e[i] = ex2(fmaf(s[c + i], p.qscale, nm[i]));
+            l[c + i] += e[i];
+          }
+          *reinterpret_cast<uint4*>(prow + (((c >> 3) ^ (r & 7)) << 4)) =
+              make_uint4(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7]));
+        }
+        if (t >= it.end || t > past) {
+          // A slot that no row sees may hold anything, and 0 * NaN would reach O: its values are
+          // zeroed.  Of a token that some rows see and others do not, what is not finite: the
+          // rows that see it have the NaN from their score.
+          const bool drop = t >= it.end;
+#pragma unroll 1
+          for (int i = 0; i < NP; ++i) {
+            unsigned char* at = smem + Lay::kOffRing + ((kt * NP + i) % SLOTS) * kPair + r * 128;
+#pragma unroll 1
+            for (int x = 0; x < 16; ++x) {
+              uint4* w = reinterpret_cast<uint4*>(at + (x >> 3) * kChunk + (x & 7) * 16);
+              if (drop) {
+                *w = make_uint4(0u, 0u, 0u, 0u);
+              } else {
+                uint4 v = *w;
+                auto clean = [](uint32_t y) {
+                  if ((y & 0x7f80u) == 0x7f80u) y &= 0xffff0000u;
+                  if ((y & 0x7f800000u) == 0x7f800000u) y &= 0xffffu;
+                  return y;
+                };
+                *w = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+              }
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(&sh->p);
+      }
+
+      // ---------------------------------------------------------- output of the row group
+      warp_sums(l, lane);
+      __syncwarp();
+      named_sync(1, 128);
+      {
+        // which columns the halvings left in this lane
+        constexpr int kLeft = NR / 32 > 0 ? NR / 32 : 1;
+        int col = 0;
+#pragma unroll
+        for (int off = 16, n = NR / 2; n > 0 && off > 0; off >>= 1, n /= 2)
+          if (lane & off) col += n;
+        if (NR >= 32 || (lane & (32 / NR - 1)) == 0) {
+#pragma unroll
+          for (int i = 0; i < kLeft; ++i) sh->red[warp][col + i] = l[i];
+        }
+      }
+      named_sync(1, 128);
+      if (r < NR) {
+        const float sum = (sh->red[0][r] + sh->red[1][r]) + (sh->red[2][r] + sh->red[3][r]);
+        if (it.whole) {
+          sh->f[r] = it.nt > 0 && sum != 0.f ? 1.f / sum : 0.f;
+        } else {
+          float* ml = p.ws_ml + ((size_t)it.slot * NR + r) * 2;
+          ml[0] = it.nt > 0 && sum != 0.f ? -sh->neg_m[r] : -INFINITY;
+          ml[1] = it.nt > 0 ? sum : 0.f;
+        }
+      }
+      named_sync(1, 128);
+      const int R = RC * 64;
+      if (it.nt > 0) {
+        wait(&sh->pv, (uint32_t)(kt - 1) & 1u, abort_flag);
+        __syncwarp();
+        tc_fence_after();
+      }
+#pragma unroll 1
+      for (int i = 0; i < NP; ++i) {
+#pragma unroll 1
+        for (int c = 0; c < NR; c += 16) {
+          uint32_t v[16];
+          if (it.nt > 0) {
+            tmem_ld16(tO + i * NR + c + lane_off, v);
+            tmem_ld_wait();
+          }
+          const int d = i * 128 + r;
+          if (it.whole) {
+            __nv_bfloat16* o = p.out + ((size_t)it.q0 * p.H + it.r0 + c) * R + d;
+#pragma unroll
+            for (int x = 0; x < 16; ++x)
+              if (c + x < it.rows)
+                o[(size_t)x * R] = __float2bfloat16_rn(it.nt > 0 ? __uint_as_float(v[x]) * sh->f[c + x] : 0.f);
+          } else if (it.nt > 0) {
+            float* o = p.ws_o + ((size_t)it.slot * NR + c) * R + d;
+#pragma unroll
+            for (int x = 0; x < 16; ++x)
+              if (c + x < it.rows) o[(size_t)x * R] = __uint_as_float(v[x]);
+          }
+        }
+      }
+      if (it.nt > 0) {
+        tc_fence_before();
+        mbar_arrive(&sh->o_free);
+      }
+      named_sync(1, 128);                    // f and red are free again
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 5) tmem_dealloc(tmem, Lay::kTmem);
+}
+
+// Joins the row groups that a cut left in several CTAs.  grid (row groups, NR / 8): a warp per row.
+template <int NR, int RC>
+__global__ void __launch_bounds__(256) latent_join_kernel(const LatentParams p, int all_parts) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int R = RC * 64, kPer = R / 128;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int u = blockIdx.x;
+  if (u >= p.ws_group[p.B]) return;
+  int lo = 0, hi = p.B - 1;                  // the sequence holding group u
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.ws_group[mid] <= u) lo = mid;
+    else hi = mid - 1;
+  }
+  const Seq s = seq_of(p, lo, false);
+  const int g = u - p.ws_group[lo];
+  const int c = blockIdx.y * 8 + warp, row = g * NR + c;
+  if (row >= s.n * p.H) return;
+  const long long total = p.ws_base[p.B];
+  const long long u0 = p.ws_base[lo] + (long long)(g / p.cl) * s.tiles;
+  const long long parts = min((long long)all_parts, total);
+  // the part that holds unit x: the last that begins at or before it
+  auto part_of = [&](long long x) -> int { return (int)(((x + 1) * parts + total - 1) / total) - 1; };
+  const int p0 = part_of(u0), p1 = part_of(u0 + s.tiles - 1);
+  if (p0 == p1) return;                      // one CTA had it whole
+  auto slot_of = [&](int q) -> size_t {
+    const bool first = q > p0 || total * q / parts == u0;
+    return (size_t)((q * p.cl + g % p.cl) * 2 + (first ? 0 : 1)) * NR + c;
+  };
+  float m = -INFINITY;
+  for (int q = p0 + lane; q <= p1; q += 32) m = fmaxf(m, p.ws_ml[slot_of(q) * 2]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  float l = 0.f;
+  float4 o[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int q = p0; q <= p1; ++q) {
+    const size_t at = slot_of(q);
+    const float mq = p.ws_ml[at * 2], lq = p.ws_ml[at * 2 + 1];
+    if (mq == -INFINITY) continue;
+    const float w = exp2f(mq - m);
+    l = fmaf(lq, w, l);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(p.ws_o + at * R + i * 128 + lane * 4);
+      o[i].x = fmaf(x.x, w, o[i].x);
+      o[i].y = fmaf(x.y, w, o[i].y);
+      o[i].z = fmaf(x.z, w, o[i].z);
+      o[i].w = fmaf(x.w, w, o[i].w);
+    }
+  }
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  __nv_bfloat16* out = p.out + ((size_t)s.q0 * p.H + row) * R;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    *reinterpret_cast<uint2*>(out + i * 128 + lane * 4) =
+        make_uint2(pack_bf16(o[i].x * inv, o[i].y * inv), pack_bf16(o[i].z * inv, o[i].w * inv));
+}
+
+bool good_sizes(int total, int num_seqs, int num_heads, int latent_dim, int max_blocks, int bs) {
+  return total >= 0 && num_seqs >= 0 && num_heads > 0 && latent_shape(latent_dim, 16, bs) && max_blocks > 0 &&
+         (long long)max_blocks * bs <= kMaxRowTokens && (long long)total * num_heads <= 0x7fffffffll;
+}
+
+// How the rows are taken: NR rows a CTA (what most sequences have, as far as it is known here),
+// and two CTAs side by side over the same tokens where that is less than a sequence's rows.
+struct Plan {
+  int nr, cl, parts;
+  long long groups;                          // row groups at most
+  size_t o, ml, base, group, bytes;          // workspace offsets
+};
+Plan plan_of(int total, int num_seqs, int num_heads, int latent_dim) {
+  Plan w = {};
+  const long long rows = ((long long)total + num_seqs - 1) / num_seqs * num_heads;
+  w.nr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  w.cl = rows > w.nr ? 2 : 1;
+  w.parts = kTunedSms / w.cl;
+  w.groups = (long long)total * num_heads / w.nr + num_seqs;
+  const size_t slots = 2 * (size_t)w.parts * w.cl * w.nr;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  w.ml = up(slots * latent_dim * 4);
+  w.base = w.ml + up(slots * 8);
+  w.group = w.base + up(((size_t)num_seqs + 1) * 8);
+  w.bytes = w.group + up(((size_t)num_seqs + 1) * 4);
+  return w;
+}
+
+struct Pick {
+  const void *kernel, *join;
+  size_t smem;
+};
+template <int NR, int RC>
+Pick pick1() {
+  return {reinterpret_cast<const void*>(&latent_decode_kernel<NR, RC>),
+          reinterpret_cast<const void*>(&latent_join_kernel<NR, RC>), Layout<NR, RC>::kBytes};
+}
+template <int NR>
+Pick pick2(int rc) {
+  return rc == 2 ? pick1<NR, 2>() : rc == 4 ? pick1<NR, 4>() : rc == 6 ? pick1<NR, 6>() : pick1<NR, 8>();
+}
+Pick pick(int nr, int rc) { return nr == 16 ? pick2<16>(rc) : nr == 32 ? pick2<32>(rc) : pick2<64>(rc); }
 
 }  // namespace
 
@@ -120,23 +771,53 @@ using namespace pa;
 extern "C" int pa_latent_decode(void* out, const void* query, const int32_t* query_start, int total_queries,
                                 const void* cache, const int32_t* block_tables, int max_blocks_per_seq,
                                 const int32_t* context_lens, int num_seqs, int num_heads, int latent_dim,
-                                int rope_dim, int block_size, int num_blocks, float scale, int partition_size,
-                                void* workspace, size_t workspace_bytes, pa_dtype dtype, void* stream) {
+                                int rope_dim, int block_size, int num_blocks, float scale, void* workspace,
+                                size_t workspace_bytes, pa_dtype dtype, void* stream) {
   if (dtype != PA_BF16) return PA_ERR_DTYPE;
-  if (!good_sizes(total_queries, num_seqs, num_heads, latent_dim, max_blocks_per_seq, block_size, partition_size) ||
+  if (!good_sizes(total_queries, num_seqs, num_heads, latent_dim, max_blocks_per_seq, block_size) ||
       !latent_shape(latent_dim, rope_dim, block_size) || num_blocks <= 0 || !(scale > 0.f) ||
       (!query_start && total_queries != num_seqs))
     return PA_ERR_SHAPE;
   if (num_seqs == 0 || total_queries == 0) return PA_OK;
   if (!out || !query || !cache || !block_tables || !context_lens) return PA_ERR_NULL;
-  if (!aligned16(out) || !aligned16(query) || !aligned16(cache)) return PA_ERR_ALIGN;
+  if (!aligned16(out) || !aligned16(query) || !aligned16(cache) || !aligned16(workspace)) return PA_ERR_ALIGN;
+  const Plan w = plan_of(total_queries, num_seqs, num_heads, latent_dim);
+  if (!workspace || workspace_bytes < w.bytes) return PA_ERR_WORKSPACE;
+  CUtensorMap mapC, mapQ;
+  const uint64_t width = (uint64_t)latent_dim + rope_dim;
+  {
+    const uint64_t dims[4] = {width, (uint64_t)block_size, (uint64_t)num_blocks, 1};
+    const uint64_t str[3] = {width * 2, width * 2 * block_size, width * 2 * block_size * num_blocks};
+    const uint32_t box[4] = {64, (uint32_t)block_size, 1, 1};
+    if (!encode_map(&mapC, cache, PA_BF16, 4, dims, str, box, true)) {
+      note_host_error("cuTensorMapEncodeTiled failed for the latent pool");
+      return PA_ERR_CUDA;
+    }
+  }
+  {
+    const uint64_t rows = (uint64_t)total_queries * num_heads;
+    const uint64_t dims[4] = {width, rows, 1, 1};
+    const uint64_t str[3] = {width * 2, width * 2 * rows, width * 2 * rows};
+    const uint32_t box[4] = {64, (uint32_t)w.nr, 1, 1};
+    if (!encode_map(&mapQ, query, PA_BF16, 4, dims, str, box, true)) {
+      note_host_error("cuTensorMapEncodeTiled failed for the queries");
+      return PA_ERR_CUDA;
+    }
+  }
+  int dev = 0;
+  if (!ck(cudaGetDevice(&dev), "cudaGetDevice")) return PA_ERR_CUDA;
+  const Pick k = pick(w.nr, latent_dim / 64);
+  if (!raise_smem_limit(k.kernel, dev)) return PA_ERR_CUDA;
+  char* ws = static_cast<char*>(workspace);
   LatentParams p = {};
   p.out = static_cast<__nv_bfloat16*>(out);
-  p.q = static_cast<const __nv_bfloat16*>(query);
-  p.cache = static_cast<const __nv_bfloat16*>(cache);
   p.query_start = query_start;
   p.block_tables = block_tables;
   p.context_lens = context_lens;
+  p.ws_o = reinterpret_cast<float*>(ws);
+  p.ws_ml = reinterpret_cast<float*>(ws + w.ml);
+  p.ws_base = reinterpret_cast<long long*>(ws + w.base);
+  p.ws_group = reinterpret_cast<int32_t*>(ws + w.group);
   p.B = num_seqs;
   p.H = num_heads;
   p.R = latent_dim;
@@ -145,23 +826,21 @@ extern "C" int pa_latent_decode(void* out, const void* query, const int32_t* que
   p.max_blocks = max_blocks_per_seq;
   p.bs = block_size;
   p.num_blocks = num_blocks;
+  p.cl = w.cl;
   p.qscale = scale * kLog2e;
-  void* args[] = {&p};
-  return ck(cudaLaunchKernel(reinterpret_cast<const void*>(&latent_decode_kernel),
-                             dim3((unsigned)total_queries * num_heads), dim3(kThreads), args, 0, (cudaStream_t)stream),
-            "cudaLaunchKernel(latent_decode_kernel)")
+  int parts = w.parts;
+  void* args[] = {&mapC, &mapQ, &p};
+  if (!ck(cudaLaunchKernel(k.kernel, dim3((unsigned)(parts * w.cl)), dim3(kThreads), args, k.smem, (cudaStream_t)stream),
+          "cudaLaunchKernel(latent_decode_kernel)"))
+    return PA_ERR_CUDA;
+  void* join[] = {&p, &parts};
+  return ck(launch_after(k.join, dim3((unsigned)w.groups, (unsigned)w.nr / 8), dim3(256), join, (cudaStream_t)stream),
+            "cudaLaunchKernel(latent_join_kernel)")
              ? PA_OK
              : PA_ERR_CUDA;
 }
 
-extern "C" size_t pa_latent_decode_workspace_bytes(int total_queries, int num_seqs, int num_heads, int latent_dim,
-                                                   int max_blocks_per_seq, int block_size, int partition_size) {
-  return 0;
-}
-
-extern "C" int pa_latent_decode_partition_size(int total_queries, int num_seqs, int num_heads, int latent_dim,
-                                               int max_blocks_per_seq, int block_size, int partition_size) {
-  if (!good_sizes(total_queries, num_seqs, num_heads, latent_dim, max_blocks_per_seq, block_size, partition_size))
-    return PA_ERR_SHAPE;
-  return max_blocks_per_seq * block_size;
+extern "C" size_t pa_latent_decode_workspace_bytes(int total_queries, int num_seqs, int num_heads, int latent_dim) {
+  if (!good_sizes(total_queries, num_seqs, num_heads, latent_dim, 1, 8) || num_seqs == 0 || total_queries == 0) return 0;
+  return plan_of(total_queries, num_seqs, num_heads, latent_dim).bytes;
 }

@@ -37,10 +37,6 @@ def test_one_row_a_sequence(pa, R, P, H, bs, lens):
     want = c.oracle(q, scale)
     check(_run(pa, c, q, scale), *want)
     assert pa.last_error() == 0
-    # every split gives the same up to rounding; a partition per two blocks, none at all
-    for part in (128, -1):
-        check(_run(pa, c, q, scale, partition_size=part), *want)
-    assert pa.last_error() == 0
 
 
 @pytest.mark.parametrize("R,P,H,bs,lens,new", [
@@ -52,8 +48,7 @@ def test_several_rows_causal(pa, R, P, H, bs, lens, new):
     q = randn(R, int(start[-1]), H, R + P)
     scale = 2.0 * (R + P) ** -0.5
     want = c.oracle(q, scale, start)
-    for part in (0, 64, -1):
-        check(_run(pa, c, q, scale, start, partition_size=part), *want)
+    check(_run(pa, c, q, scale, start), *want)
     assert pa.last_error() == 0
 
 
@@ -64,8 +59,7 @@ def test_rows_with_nothing_to_see(pa):
     q = randn(1, 11, 16, 576)
     want = c.oracle(q, 0.1, start)
     assert not want[0][:4].any()
-    for part in (0, -1, 16):
-        check(_run(pa, c, q, 0.1, start, partition_size=part), *want)
+    check(_run(pa, c, q, 0.1, start), *want)
     assert pa.last_error() == 0
     c = Cache([0, 40], 256, 32, 8)
     q = randn(1, 2, 4, 288)
@@ -99,6 +93,30 @@ def test_nan_stays_with_the_rows_that_see_it(pa):
     assert torch.isnan(out[5:10]).all()                   # positions 95..99
     keep = [0, 1, 2, 3, 4, 10, 11]
     check(out[keep], *(x[keep] for x in want))
+
+
+def test_nan_values_stay_with_the_rows_that_see_them(pa):
+    """The same in the latent part, whose elements are the values too."""
+    for H, R in ((8, 256), (16, 512)):
+        c = Cache([100, 60], R, 32, 16)
+        c.cache[int(c.table[0, 95 // 16]), 95 % 16, 70] = float("nan")
+        start = [0, 10, 12]
+        q = randn(3, 12, H, R + 32)
+        out = _run(pa, c, q, 0.1, start)
+        want = c.oracle(q, 0.1, start)
+        assert torch.isnan(out[5:10]).all()
+        keep = [0, 1, 2, 3, 4, 10, 11]
+        check(out[keep], *(x[keep] for x in want))
+    assert pa.last_error() == 0
+
+
+@pytest.mark.parametrize("H,lens", [(16, [20000]), (128, [9000, 30]), (40, [5000, 128, 0, 129, 7777])])
+def test_long_sequences_cut_among_many(pa, H, lens):
+    """Many CTAs a sequence, cuts at and inside tiles."""
+    c = Cache(lens, 256, 32, 32, scale=0.5)
+    q = randn(H, len(lens), H, 288)
+    check(_run(pa, c, q, 0.2), *c.oracle(q, 0.2))
+    assert pa.last_error() == 0
 
 
 def test_bad_tables_and_lengths(pa):

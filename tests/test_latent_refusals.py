@@ -43,9 +43,9 @@ def _append(pa, lat=FAKE, ls=512, key=FAKE, ks=64, q=FAKE, qh=64, H=4, slots=FAK
                                    FAKE, 1.0, dt, NULL)
 
 
-def _decode(pa, q=FAKE, start=NULL, rows=2, cache=FAKE, mb=4, B=2, H=16, R=512, P=64, bs=16, NB=10, scale=1.0, ps=0,
+def _decode(pa, q=FAKE, start=NULL, rows=2, cache=FAKE, mb=4, B=2, H=16, R=512, P=64, bs=16, NB=10, scale=1.0,
             ws=FAKE, n=1 << 40, dt=1):
-    return pa.lib.pa_latent_decode(FAKE, q, start, rows, cache, FAKE, mb, FAKE, B, H, R, P, bs, NB, scale, ps, ws, n, dt,
+    return pa.lib.pa_latent_decode(FAKE, q, start, rows, cache, FAKE, mb, FAKE, B, H, R, P, bs, NB, scale, ws, n, dt,
                                    NULL)
 
 
@@ -93,11 +93,20 @@ def test_latent_append(pa, kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(dt=0), -3), (dict(dt=2), -3), (dict(R=192), -2), (dict(R=640), -2), (dict(P=72), -2), (dict(P=0), -2), (dict(bs=4), -2), (dict(bs=64), -2),
     (dict(H=0), -2), (dict(rows=3), -2), (dict(rows=-1, start=FAKE), -2), (dict(NB=0), -2), (dict(mb=0), -2), (dict(mb=(1 << 25) + 1, bs=32), -2),
-    (dict(ps=24), -2), (dict(scale=0.0), -2), (dict(scale=float("nan")), -2), (dict(rows=1 << 28, B=1 << 28, H=16), -2),
-    (dict(q=NULL), -1), (dict(cache=NULL), -1), (dict(q=ODD), -4), (dict(cache=ODD), -4), (dict(B=0, rows=0), 0),
+    (dict(scale=0.0), -2), (dict(scale=float("nan")), -2), (dict(rows=1 << 28, B=1 << 28, H=16), -2),
+    (dict(q=NULL), -1), (dict(cache=NULL), -1), (dict(q=ODD), -4), (dict(cache=ODD), -4), (dict(ws=ODD), -4), (dict(ws=NULL), -5),
+    (dict(n=100), -5), (dict(B=0, rows=0), 0),
     (dict(rows=0, start=FAKE, q=NULL), 0)])
 def test_latent_decode(pa, kw, code):
     assert _decode(pa, **kw) == code
+
+
+def test_workspace_arithmetic(pa):
+    need = pa.lib.pa_latent_decode_workspace_bytes
+    # two slots a CTA of 152: 16 rows of 512 sums, their maxima and sums, two prefixes of B + 1
+    assert need(4, 4, 16, 512) == 2 * 152 * 16 * (512 * 4 + 8) + 2 * 256
+    assert need(4, 4, 128, 512) == 2 * 152 * 64 * (512 * 4 + 8) + 2 * 256
+    assert need(0, 4, 16, 512) == need(4, 0, 16, 512) == need(4, 4, 16, 500) == need(-1, 4, 16, 512) == 0
 
 
 @pytest.mark.parametrize("kw,code", [
