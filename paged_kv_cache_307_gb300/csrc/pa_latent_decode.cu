@@ -19,16 +19,18 @@ namespace {
 __device__ unsigned g_status_latent;
 
 constexpr int kTile = 128;                   // tokens per tile
-constexpr int kThreads = 192;                // warps 0-3 softmax, 4 TMA, 5 MMA
+constexpr int kThreads = 416;                // warps 0-7 softmax, 8-11 TMA, 12 MMA
 constexpr uint32_t kChunk = 16384;           // 128 tokens x 64 elements
 constexpr uint32_t kPair = 2 * kChunk;       // 128 elements: one M = 128 product of O^T
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;                // log2 units a score may exceed its reference by
 constexpr uint32_t kSmemMax = 232448;        // 227 KB
 constexpr int kMaxSlots = 6;
+constexpr bool kPrefetch = false;
 
 struct LatentParams {
   __nv_bfloat16* out;
+  const __nv_bfloat16* cache;
   const int32_t* query_start;                // null: one row a sequence
   const int32_t* block_tables;
   const int32_t* context_lens;
@@ -48,7 +50,8 @@ struct Shared {
   alignas(16) float neg_m[NR];               // minus the reference of every row
   alignas(16) float f[NR];
   alignas(16) float red[4][NR];              // per warp: maxima, at the end sums
-  long long scan[8];
+  long long scan[kThreads / 32];
+  int gscan[kThreads / 32];
   long long first_off;
   int first_b;
   uint32_t tmem_base;
@@ -89,12 +92,12 @@ __device__ __forceinline__ float warp_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
 }
-// Barrier 2 of the 128 softmax threads, true for all if true for any.
-__device__ __forceinline__ bool vote128(bool x) {
+// Barrier 2 of the 256 softmax threads, true for all if true for any.
+__device__ __forceinline__ bool vote256(bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "bar.red.or.pred q, 2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r) : "r"(x ? 1u : 0u) : "memory");
   return r != 0;
 }
@@ -176,7 +179,8 @@ struct Walk {
   }
 };
 
-// Sum of every x[i] over the warp: lane's x[0] is column col(lane)'s, NR / 32 more behind it.
+// Sum of every x[i] over the warp, N <= 32: x[0] is that of the column whose bits the lane's
+// upper bits spell.
 template <int N>
 __device__ __forceinline__ void warp_sums(float (&x)[N], int lane) {
   int n = N;
@@ -197,6 +201,9 @@ __device__ __forceinline__ void warp_sums(float (&x)[N], int lane) {
     }
   }
 }
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[8]) { tmem_ld(taddr, r); }
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
 
 template <int NR, int RC>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -225,9 +232,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
     }
     mbar_init(&sh->q_full, 1);
     mbar_init(&sh->q_empty, 1);
-    mbar_init(&sh->p, 128);
+    mbar_init(&sh->p, 8);
     mbar_init(&sh->pv, 1);
-    mbar_init(&sh->o_free, 128);
+    mbar_init(&sh->o_free, 8);
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
     sh->first_b = p.B;
@@ -235,7 +242,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
     prefetch_tensormap(&mapC);
     prefetch_tensormap(&mapQ);
   }
-  if (warp == 5) {
+  if (warp == 12) {
     tmem_alloc(&sh->tmem_base, Lay::kTmem);
     tmem_relinquish();
   }
@@ -268,7 +275,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
     }
     if (lane == 31) {
       sh->scan[warp] = incl;
-      sh->red[0][warp] = __int_as_float(gincl);
+      sh->gscan[warp] = gincl;
     }
     tc_fence_before();
     __syncthreads();
@@ -279,7 +286,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
       total += sh->scan[w];
       if (w < warp) {
         before += sh->scan[w];
-        gbefore += __float_as_int(sh->red[0][w]);
+        gbefore += sh->gscan[w];
       }
     }
     // (no empty parts: a line shorter than the grid leaves its last CTAs without work)
@@ -324,32 +331,51 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
   const uint32_t tO = tmem + 2 * NR;
   Item it;
 
-  if (warp == 4) {
-    // ------------------------------------------------------------ TMA producer
-    const uint64_t pol = policy_evict_first(), pol_q = policy_evict_first();
+  if (warp >= 8 && warp < 12) {
+    // ------------------------------------------------------------ TMA producers
+    // A warp gets a copy out in about 60 clocks, whatever its size, and a tile is 72 of 2 KB:
+    // four warps share them (chunk w >> 1 of a pair, half w & 1 of the tile's blocks).
+    const uint64_t pol = policy_evict_first();
+    const int w = warp - 8;
     const int bsh = 31 - __clz(p.bs);
     const uint32_t box = (uint32_t)p.bs * 128u;
+    const int lanes = kTile >> (bsh + 1);
+    const int mine = (w & 1) * lanes + lane;     // the lane's block of a tile
     int kp = 0, kr = 0, kq = 0;              // pairs, rotated chunks and query groups requested
     bool ok = true;
     while (ok && walk.next(p, it)) {
       if (it.nt == 0) continue;
       const int32_t* row = p.block_tables + (size_t)it.b * p.max_blocks;
       auto id_of = [&](int j) -> int {
-        const int t = (it.tile + j) * kTile + (lane << bsh);
-        return j < it.nt && lane < (kTile >> bsh) && t < it.end ? __ldg(&row[t >> bsh]) : 0;
+        const int t = (it.tile + j) * kTile + (mine << bsh);
+        return j < it.nt && lane < lanes && t < it.end ? __ldg(&row[t >> bsh]) : 0;
       };
-      int blk = id_of(0);
+      // The ring holds little more than a tile, which does not cover HBM's latency: blocks are asked
+      // into L2 two tiles ahead (a block is one span of memory), by one CTA of the two that read them.
+      const uint32_t span = (uint32_t)p.bs * (uint32_t)(p.R + p.P) * 2u;
+      auto ahead = [&](int j, int id) {
+        const int t = (it.tile + j) * kTile + (mine << bsh);
+        if (kPrefetch && w < 2 && j < it.nt && lane < lanes && t < it.end && (unsigned)id < (unsigned)p.num_blocks &&
+            (p.cl == 1 || (j & 1) == walk.half))
+          bulk_prefetch(p.cache + (size_t)id * p.bs * (p.R + p.P), span);
+      };
+      int blk = id_of(0), next = id_of(1), after = id_of(2);
+      ahead(1, next);
       ok = __all_sync(0xffffffffu, wait(&sh->q_empty, (uint32_t)(kq & 1) ^ 1u, abort_flag));
       if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(&sh->q_full, (uint32_t)NC * NR * 128u);
-      __syncwarp();
-      if (lane < NC)
-        tma_load_4d(smem + lane * NR * 128, &mapQ, &sh->q_full, lane * 64, it.q0 * p.H + it.r0, 0, 0, pol_q);
+      if (w == 0) {
+        if (lane == 0) mbar_arrive_expect_tx(&sh->q_full, (uint32_t)NC * NR * 128u);
+        __syncwarp();
+        if (lane < NC)
+          tma_load_4d(smem + lane * NR * 128, &mapQ, &sh->q_full, lane * 64, it.q0 * p.H + it.r0, 0, 0, pol);
+      }
       ++kq;
       for (int j = 0; j < it.nt; ++j) {
-        const int next = id_of(j + 1);
+        const int later = id_of(j + 3);
+        ahead(j + 2, after);
         const int nb = (min(kTile, it.end - (it.tile + j) * kTile) + p.bs - 1) >> bsh;
-        if (lane < nb && (unsigned)blk >= (unsigned)p.num_blocks) {
+        const bool has = lane < lanes && mine < nb;
+        if (has && (unsigned)blk >= (unsigned)p.num_blocks) {
           atomicOr(&g_status_latent, PA_DEV_BAD_BLOCK);
           blk = 0;                           // keep every copy inside the pool
         }
@@ -357,25 +383,26 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
           const int sl = kp % SLOTS;
           ok = __all_sync(0xffffffffu, wait(&sh->empty[sl], ((uint32_t)(kp / SLOTS) & 1u) ^ 1u, abort_flag));
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&sh->full[sl], 2u * nb * box);
+          // (a warp may be ahead of the one that names the bytes: the phase waits for that one)
+          if (w == 0 && lane == 0) mbar_arrive_expect_tx(&sh->full[sl], 2u * nb * box);
           __syncwarp();
-          if (lane < nb) {
-            unsigned char* dst = smem + Lay::kOffRing + sl * kPair + lane * box;
-            tma_load_4d(dst, &mapC, &sh->full[sl], i * 128, 0, blk, 0, pol);
-            tma_load_4d(dst + kChunk, &mapC, &sh->full[sl], i * 128 + 64, 0, blk, 0, pol);
-          }
+          if (has)
+            tma_load_4d(smem + Lay::kOffRing + sl * kPair + (w >> 1) * kChunk + mine * box, &mapC, &sh->full[sl],
+                        i * 128 + (w >> 1) * 64, 0, blk, 0, pol);
         }
         if (!ok) break;
         const int sr = kAlias ? 0 : kr & 1;
         const uint32_t use = kAlias ? (uint32_t)kr : (uint32_t)kr >> 1;
         ok = __all_sync(0xffffffffu, wait(&sh->empty_r[sr], (use & 1u) ^ 1u, abort_flag));
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&sh->full_r[sr], (uint32_t)nb * box);
+        if (w == 0 && lane == 0) mbar_arrive_expect_tx(&sh->full_r[sr], (uint32_t)nb * box);
         __syncwarp();
-        if (lane < nb)
-          tma_load_4d(smem + Lay::kOffRope + sr * kChunk + lane * box, &mapC, &sh->full_r[sr], RC * 64, 0, blk, 0, pol);
+        if (w < 2 && has)
+          tma_load_4d(smem + Lay::kOffRope + sr * kChunk + mine * box, &mapC, &sh->full_r[sr], RC * 64, 0, blk, 0, pol);
         ++kr;
         blk = next;
+        next = after;
+        after = later;
       }
     }
     // no TMA write may land after the CTA has left
@@ -385,175 +412,217 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
         mbar_wait(&sh->full_r[kAlias ? 0 : k & 1], (uint32_t)(kAlias ? k : k >> 1) & 1u);
       if (kq > 0) mbar_wait(&sh->q_full, (uint32_t)(kq - 1) & 1u);
     }
-  } else if (warp == 5) {
+  } else if (warp == 12) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idS = idesc_bf16_f32(kTile, NR, false, false);
-      constexpr uint32_t idO = idesc_bf16_f32(kTile, NR, true, true);
-      const uint64_t dk = sdesc_sw128(sbase + Lay::kOffRing, 16, 1024);            // the tile as K
-      const uint64_t dv = sdesc_sw128(sbase + Lay::kOffRing, kChunk, 1024);        // the tile as V^T
-      const uint64_t dr = sdesc_sw128(sbase + Lay::kOffRope, 16, 1024);
-      const uint64_t dq = sdesc_sw128(sbase, 16, 1024);
-      const uint64_t dp = sdesc_sw128(sbase + Lay::kOffP, kChunk, 1024);
-      constexpr int kEarly = SLOTS - NP < NP ? SLOTS - NP : NP;   // pairs of the next tile that a tile leaves room for
-      constexpr bool kAllEarly = kEarly == NP && !kAlias;
-      const int rope_steps = p.P / 16;
-      int kt = 0, kq = 0;                    // tiles, query groups
-      // pairs [a, b) of tile k's scores
-      auto scores = [&](int k, int a, int b) -> bool {
-        for (int i = a; i < b; ++i) {
-          const int u = k * NP + i, sl = u % SLOTS;
-          if (!wait(&sh->full[sl], (uint32_t)(u / SLOTS) & 1u, abort_flag)) return false;
-          tc_fence_after();
+    // The whole warp walks, with values that are the same in all lanes, and one lane issues: the
+    // descriptors then stay in uniform registers (moved there for every MMA, 57 clocks an MMA and not 47).
+    constexpr uint32_t idS = idesc_bf16_f32(kTile, NR, false, false);
+    constexpr uint32_t idO = idesc_bf16_f32(kTile, NR, true, true);
+    const bool lead = elect_one();
+    const uint32_t t0 = __shfl_sync(0xffffffffu, tmem, 0), tO0 = t0 + 2 * NR;
+    const uint32_t sb = __shfl_sync(0xffffffffu, sbase, 0);
+    const uint64_t dk = sdesc_sw128(sb + Lay::kOffRing, 16, 1024);               // the tile as K
+    const uint64_t dv = sdesc_sw128(sb + Lay::kOffRing, kChunk, 1024);           // the tile as V^T
+    const uint64_t dr = sdesc_sw128(sb + Lay::kOffRope, 16, 1024);
+    const uint64_t dq = sdesc_sw128(sb, 16, 1024);
+    const uint64_t dp = sdesc_sw128(sb + Lay::kOffP, kChunk, 1024);
+    constexpr int kEarly = SLOTS - NP < NP ? SLOTS - NP : NP;     // pairs of the next tile that a tile leaves room for
+    constexpr bool kAllEarly = kEarly == NP && !kAlias;
+    const int rope_steps = p.P / 16;
+    int kt = 0, kq = 0;                      // tiles, query groups
+    int u0 = 0;                              // slot of tile kt's first pair, and how often the ring has turned
+    uint32_t turn = 0;
+    // pairs [a, b) of tile k's scores, its pairs from slot `at` on in turn `tn`
+    auto scores = [&](int k, int at, uint32_t tn, int a, int b) -> bool {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        if (i < a || i >= b) continue;
+        const bool over = at + i >= SLOTS;
+        const int sl = over ? at + i - SLOTS : at + i;
+        if (!wait(&sh->full[sl], (tn + (over ? 1u : 0u)) & 1u, abort_flag)) return false;
+        tc_fence_after();
+        if (lead) {
           const uint64_t da = sdesc_at(dk, sl * kPair), db = sdesc_at(dq, i * 2 * NR * 128);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            umma_bf16(tmem + (k & 1) * NR, sdesc_at(da, (kk >> 2) * kChunk + (kk & 3) * 32),
+            umma_bf16(t0 + (k & 1) * NR, sdesc_at(da, (kk >> 2) * kChunk + (kk & 3) * 32),
                       sdesc_at(db, (kk >> 2) * NR * 128 + (kk & 3) * 32), idS, i > 0 || kk > 0 ? 1u : 0u);
         }
-        return true;
-      };
-      auto scores_end = [&](int k, bool last) -> bool {
-        const int sr = kAlias ? 0 : k & 1;
-        if (!wait(&sh->full_r[sr], (uint32_t)(kAlias ? k : k >> 1) & 1u, abort_flag)) return false;
-        tc_fence_after();
+        __syncwarp();
+      }
+      return true;
+    };
+    auto scores_end = [&](int k, bool last) -> bool {
+      const int sr = kAlias ? 0 : k & 1;
+      if (!wait(&sh->full_r[sr], (uint32_t)(kAlias ? k : k >> 1) & 1u, abort_flag)) return false;
+      tc_fence_after();
+      if (lead) {
         const uint64_t da = sdesc_at(dr, sr * kChunk), db = sdesc_at(dq, RC * NR * 128);
-        for (int kk = 0; kk < rope_steps; ++kk)
-          umma_bf16(tmem + (k & 1) * NR, sdesc_at(da, kk * 32), sdesc_at(db, kk * 32), idS, 1u);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          if (kk < rope_steps) umma_bf16(t0 + (k & 1) * NR, sdesc_at(da, kk * 32), sdesc_at(db, kk * 32), idS, 1u);
         umma_commit(&sh->s[k & 1]);
         if (!kAlias) umma_commit(&sh->empty_r[sr]);
         if (last) umma_commit(&sh->q_empty);
-        return true;
-      };
-      bool ok = true;
-      while (ok && walk.next(p, it)) {
-        if (it.nt == 0) continue;
-        ok = wait(&sh->q_full, (uint32_t)kq & 1u, abort_flag) && scores(kt, 0, NP) && scores_end(kt, it.nt == 1);
-        for (int j = 0; ok && j < it.nt; ++j, ++kt) {
-          const bool more = j + 1 < it.nt;
-          if (more && kEarly > 0) {
-            if (!(ok = scores(kt + 1, 0, kEarly))) break;
-            if (kAllEarly && !(ok = scores_end(kt + 1, j + 2 == it.nt))) break;
-          }
-          if (!(ok = wait(&sh->p, (uint32_t)kt & 1u, abort_flag))) break;
-          if (j == 0 && !(ok = wait(&sh->o_free, ((uint32_t)kq & 1u) ^ 1u, abort_flag))) break;
-          tc_fence_after();
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = true;
+    while (ok && walk.next(p, it)) {
+      const int nt = __shfl_sync(0xffffffffu, it.nt, 0);
+      if (nt == 0) continue;
+      ok = wait(&sh->q_full, (uint32_t)kq & 1u, abort_flag) && scores(kt, u0, turn, 0, NP) && scores_end(kt, nt == 1);
+      for (int j = 0; ok && j < nt; ++j, ++kt) {
+        const bool more = j + 1 < nt;
+        const bool over = u0 + NP >= SLOTS;
+        const int u1 = over ? u0 + NP - SLOTS : u0 + NP;
+        const uint32_t turn1 = turn + (over ? 1u : 0u);
+        if (more && kEarly > 0) {
+          if (!(ok = scores(kt + 1, u1, turn1, 0, kEarly))) break;
+          if (kAllEarly && !(ok = scores_end(kt + 1, j + 2 == nt))) break;
+        }
+        if (!(ok = wait(&sh->p, (uint32_t)kt & 1u, abort_flag))) break;
+        if (j == 0 && !(ok = wait(&sh->o_free, ((uint32_t)kq & 1u) ^ 1u, abort_flag))) break;
+        tc_fence_after();
 #pragma unroll
-          for (int i = 0; i < NP; ++i) {
-            const int sl = (kt * NP + i) % SLOTS;
+        for (int i = 0; i < NP; ++i) {
+          const int sl = u0 + i >= SLOTS ? u0 + i - SLOTS : u0 + i;
+          if (lead) {
             const uint64_t da = sdesc_at(dv, sl * kPair);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)   // 16 tokens each
-              umma_bf16(tO + i * NR, sdesc_at(da, kk * 2048), sdesc_at(dp, kk * 2048), idO, j > 0 || kk > 0 ? 1u : 0u);
+              umma_bf16(tO0 + i * NR, sdesc_at(da, kk * 2048), sdesc_at(dp, kk * 2048), idO, j > 0 || kk > 0 ? 1u : 0u);
             umma_commit(&sh->empty[sl]);
+            if (i == NP - 1) {
+              umma_commit(&sh->pv);
+              if (kAlias) umma_commit(&sh->empty_r[0]);
+            }
           }
-          umma_commit(&sh->pv);
-          if (kAlias) umma_commit(&sh->empty_r[0]);
-          if (more && !kAllEarly) {
-            if (!(ok = scores(kt + 1, kEarly, NP))) break;
-            if (!(ok = scores_end(kt + 1, j + 2 == it.nt))) break;
-          }
+          __syncwarp();
         }
-        ++kq;
+        if (more && !kAllEarly) {
+          if (!(ok = scores(kt + 1, u1, turn1, kEarly, NP))) break;
+          if (!(ok = scores_end(kt + 1, j + 2 == nt))) break;
+        }
+        u0 = u1;
+        turn = turn1;
       }
-      umma_commit(&sh->drain);               // every MMA has completed before TMEM is freed
-      mbar_wait(&sh->drain, 0);
+      ++kq;
     }
+    if (lead) umma_commit(&sh->drain);       // every MMA has completed before TMEM is freed
+    mbar_wait(&sh->drain, 0);
   } else {
     // ------------------------------------------------------------ softmax
-    const int r = (int)threadIdx.x;          // token of the tile, latent dim at the end; TMEM lane
-    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    // Thread = token; the tile's columns are divided between two warps a lane quarter.
+    constexpr int CW = NR / 2;
+    const int r = (int)threadIdx.x & 127;    // token of the tile, latent dim at the end; TMEM lane
+    const int half = warp >> 2, c0 = half * CW;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     int kt = 0;
-    float l[NR];
+    float l[CW];
     while (walk.next(p, it)) {
       const int past = it.L - it.n;          // position of the sequence's first row
 #pragma unroll
-      for (int c = 0; c < NR; ++c) l[c] = 0.f;
+      for (int c = 0; c < CW; ++c) l[c] = 0.f;
       for (int j = 0; j < it.nt; ++j, ++kt) {
         const int st = kt & 1;
         const int t = (it.tile + j) * kTile + r;
         wait(&sh->s[st], (uint32_t)(kt >> 1) & 1u, abort_flag);
         __syncwarp();
         tc_fence_after();
-        float s[NR];
-        {
-          uint32_t v[NR];
-#pragma unroll
-          for (int c = 0; c < NR; c += 16) tmem_ld16(tmem + st * NR + c + lane_off, reinterpret_cast<uint32_t(&)[16]>(v[c]));
-          tmem_ld_wait();
-#pragma unroll
-          for (int c = 0; c < NR; ++c) s[c] = __uint_as_float(v[c]);
-        }
         // rows (t - past) H and on of the sequence see token t
         const int hide = t >= it.end ? NR : (int)max(-1ll, min((long long)NR, (long long)(t - past) * p.H - it.r0));
-        if (__any_sync(0xffffffffu, hide > 0)) {
+        const bool any_hidden = __any_sync(0xffffffffu, hide > c0);
+        float x[CW];
+        auto scores = [&]() {
+          uint32_t v[CW];
+          tmem_load(tmem + st * NR + c0 + lane_off, v);
+          tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < NR; ++c)
-            if (c < hide) s[c] = -INFINITY;
-        }
+          for (int c = 0; c < CW; ++c) x[c] = __uint_as_float(v[c]);
+          if (any_hidden) {
+#pragma unroll
+            for (int c = 0; c < CW; ++c)
+              if (c0 + c < hide) x[c] = -INFINITY;
+          }
+        };
         // exponents, against the references as they are
+        auto exponents = [&]() {
+#pragma unroll
+          for (int c = 0; c < CW; c += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(&sh->neg_m[c0 + c]);
+            x[c] = fmaf(x[c], p.qscale, m.x);
+            x[c + 1] = fmaf(x[c + 1], p.qscale, m.y);
+            x[c + 2] = fmaf(x[c + 2], p.qscale, m.z);
+            x[c + 3] = fmaf(x[c + 3], p.qscale, m.w);
+          }
+        };
         bool need = j == 0;
         if (j > 0) {
-          float top = -INFINITY;
+          scores();
+          exponents();
+          float top[4];
 #pragma unroll
-          for (int c = 0; c < NR; c += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(&sh->neg_m[c]);
-            top = fmax3(top, fmaf(s[c], p.qscale, m.x), fmaf(s[c + 1], p.qscale, m.y));
-            top = fmax3(top, fmaf(s[c + 2], p.qscale, m.z), fmaf(s[c + 3], p.qscale, m.w));
-          }
-          need = top > kSlack;
+          for (int i = 0; i < 4; ++i) top[i] = fmaxf(x[2 * i], x[2 * i + 1]);
+#pragma unroll
+          for (int c = 8; c < CW; c += 2) top[(c >> 1) & 3] = fmax3(top[(c >> 1) & 3], x[c], x[c + 1]);
+          need = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kSlack;
         }
-        need = vote128(need);
+        need = vote256(need);
+        if (need) {
+          // new references: the tile's maxima where they are above
+          scores();
+#pragma unroll
+          for (int c = 0; c < CW; ++c) {
+            const float y = warp_max(x[c]);
+            if (lane == 0) sh->red[warp & 3][c0 + c] = y;
+          }
+          named_sync(1, 256);
+          if (threadIdx.x < NR) {
+            const int c = (int)threadIdx.x;
+            const float y = fmaxf(fmaxf(sh->red[0][c], sh->red[1][c]), fmaxf(sh->red[2][c], sh->red[3][c])) * p.qscale;
+            const float old = j > 0 ? -sh->neg_m[c] : -INFINITY;
+            const float m = fmaxf(old, y);
+            sh->f[c] = old == -INFINITY ? 0.f : exp2f(old - m);
+            // (a row that sees nothing of its first tile sees nothing of the later ones)
+            sh->neg_m[c] = m == -INFINITY ? 0.f : -m;
+          }
+          named_sync(1, 256);
+          exponents();
+        }
         // P, and with it the rotated keys' chunk, is free; O holds the tile before
         if (kt > 0) wait(&sh->pv, (uint32_t)(kt - 1) & 1u, abort_flag);
         __syncwarp();
-        if (need) {
-          // new references: the tile's maxima where they are above
+        if (need && j > 0) {
 #pragma unroll
-          for (int c = 0; c < NR; ++c) {
-            const float x = warp_max(s[c]);
-            if (lane == 0) sh->red[warp][c] = x;
-          }
-          named_sync(1, 128);
-          if (r < NR) {
-            const float x = fmaxf(fmaxf(sh->red[0][r], sh->red[1][r]), fmaxf(sh->red[2][r], sh->red[3][r])) * p.qscale;
-            const float old = j > 0 ? -sh->neg_m[r] : -INFINITY;
-            const float m = fmaxf(old, x);
-            sh->f[r] = old == -INFINITY ? 0.f : exp2f(old - m);
-            // (a row that sees nothing of its first tile sees nothing of the later ones)
-            sh->neg_m[r] = m == -INFINITY ? 0.f : -m;
-          }
-          named_sync(1, 128);
-          if (j > 0) {
-#pragma unroll
-            for (int c = 0; c < NR; ++c) l[c] *= sh->f[c];
-            tc_fence_after();
+          for (int c = 0; c < CW; ++c) l[c] *= sh->f[c0 + c];
+          tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < NP * NR; c += 16) {
-              uint32_t v[16];
-              tmem_ld16(tO + c + lane_off, v);
+          for (int i = 0; i < NP; ++i) {
+#pragma unroll 1
+            for (int c = c0; c < c0 + CW; c += 8) {
+              uint32_t v[8];
+              tmem_ld(tO + i * NR + c + lane_off, v);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * sh->f[c % NR + i]);
-              tmem_st16(tO + c + lane_off, v);
+              for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * sh->f[c + k]);
+              tmem_st(tO + i * NR + c + lane_off, v);
             }
-            tmem_st_wait();
           }
+          tmem_st_wait();
         }
         // P: row r of an MN-major tile, 8 columns a 16-byte piece
         unsigned char* prow = smem + Lay::kOffP + r * 128;
 #pragma unroll
-        for (int c = 0; c < NR; c += 8) {
-          const float4 m0 = *reinterpret_cast<const float4*>(&sh->neg_m[c]);
-          const float4 m1 = *reinterpret_cast<const float4*>(&sh->neg_m[c + 4]);
-          const float nm[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+        for (int c = 0; c < CW; c += 8) {
           float e[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            e[i] = ex2(fmaf(s[c + i], p.qscale, nm[i]));
+            e[i] = ex2(x[c + i]);
             l[c + i] += e[i];
           }
-          *reinterpret_cast<uint4*>(prow + (((c >> 3) ^ (r & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(prow + ((((c0 + c) >> 3) ^ (r & 7)) << 4)) =
               make_uint4(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7]));
         }
         if (t >= it.end || t > past) {
@@ -563,57 +632,57 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
           const bool drop = t >= it.end;
 #pragma unroll 1
           for (int i = 0; i < NP; ++i) {
-            unsigned char* at = smem + Lay::kOffRing + ((kt * NP + i) % SLOTS) * kPair + r * 128;
+            unsigned char* at = smem + Lay::kOffRing + ((kt * NP + i) % SLOTS) * kPair + half * kChunk + r * 128;
 #pragma unroll 1
-            for (int x = 0; x < 16; ++x) {
-              uint4* w = reinterpret_cast<uint4*>(at + (x >> 3) * kChunk + (x & 7) * 16);
+            for (int k = 0; k < 8; ++k) {
+              uint4* q = reinterpret_cast<uint4*>(at + k * 16);
               if (drop) {
-                *w = make_uint4(0u, 0u, 0u, 0u);
+                *q = make_uint4(0u, 0u, 0u, 0u);
               } else {
-                uint4 v = *w;
+                const uint4 v = *q;
                 auto clean = [](uint32_t y) {
                   if ((y & 0x7f80u) == 0x7f80u) y &= 0xffff0000u;
                   if ((y & 0x7f800000u) == 0x7f800000u) y &= 0xffffu;
                   return y;
                 };
-                *w = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+                *q = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
               }
             }
           }
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(&sh->p);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->p);
       }
 
       // ---------------------------------------------------------- output of the row group
       warp_sums(l, lane);
       __syncwarp();
-      named_sync(1, 128);
+      named_sync(1, 256);
       {
-        // which columns the halvings left in this lane
-        constexpr int kLeft = NR / 32 > 0 ? NR / 32 : 1;
-        int col = 0;
+        // the column that the halvings left in this lane
+        int col = 0, spare = 31;
 #pragma unroll
-        for (int off = 16, n = NR / 2; n > 0 && off > 0; off >>= 1, n /= 2)
+        for (int off = 16, n = CW / 2; n > 0; off >>= 1, n /= 2) {
           if (lane & off) col += n;
-        if (NR >= 32 || (lane & (32 / NR - 1)) == 0) {
-#pragma unroll
-          for (int i = 0; i < kLeft; ++i) sh->red[warp][col + i] = l[i];
+          spare &= ~off;
         }
+        if ((lane & spare) == 0) sh->red[warp & 3][c0 + col] = l[0];
       }
-      named_sync(1, 128);
-      if (r < NR) {
-        const float sum = (sh->red[0][r] + sh->red[1][r]) + (sh->red[2][r] + sh->red[3][r]);
+      named_sync(1, 256);
+      if (threadIdx.x < NR) {
+        const int c = (int)threadIdx.x;
+        const float sum = (sh->red[0][c] + sh->red[1][c]) + (sh->red[2][c] + sh->red[3][c]);
         if (it.whole) {
-          sh->f[r] = it.nt > 0 && sum != 0.f ? 1.f / sum : 0.f;
+          sh->f[c] = it.nt > 0 && sum != 0.f ? 1.f / sum : 0.f;
         } else {
-          float* ml = p.ws_ml + ((size_t)it.slot * NR + r) * 2;
-          ml[0] = it.nt > 0 && sum != 0.f ? -sh->neg_m[r] : -INFINITY;
+          float* ml = p.ws_ml + ((size_t)it.slot * NR + c) * 2;
+          ml[0] = it.nt > 0 && sum != 0.f ? -sh->neg_m[c] : -INFINITY;
           ml[1] = it.nt > 0 ? sum : 0.f;
         }
       }
-      named_sync(1, 128);
+      named_sync(1, 256);
       const int R = RC * 64;
       if (it.nt > 0) {
         wait(&sh->pv, (uint32_t)(kt - 1) & 1u, abort_flag);
@@ -622,39 +691,37 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
       }
 #pragma unroll 1
       for (int i = 0; i < NP; ++i) {
-#pragma unroll 1
-        for (int c = 0; c < NR; c += 16) {
-          uint32_t v[16];
-          if (it.nt > 0) {
-            tmem_ld16(tO + i * NR + c + lane_off, v);
-            tmem_ld_wait();
-          }
-          const int d = i * 128 + r;
-          if (it.whole) {
-            __nv_bfloat16* o = p.out + ((size_t)it.q0 * p.H + it.r0 + c) * R + d;
+        uint32_t v[CW];
+        if (it.nt > 0) {
+          tmem_load(tO + i * NR + c0 + lane_off, v);
+          tmem_ld_wait();
+        }
+        const int d = i * 128 + r;
+        if (it.whole) {
+          __nv_bfloat16* o = p.out + ((size_t)it.q0 * p.H + it.r0 + c0) * R + d;
 #pragma unroll
-            for (int x = 0; x < 16; ++x)
-              if (c + x < it.rows)
-                o[(size_t)x * R] = __float2bfloat16_rn(it.nt > 0 ? __uint_as_float(v[x]) * sh->f[c + x] : 0.f);
-          } else if (it.nt > 0) {
-            float* o = p.ws_o + ((size_t)it.slot * NR + c) * R + d;
+          for (int c = 0; c < CW; ++c)
+            if (c0 + c < it.rows)
+              o[(size_t)c * R] = __float2bfloat16_rn(it.nt > 0 ? __uint_as_float(v[c]) * sh->f[c0 + c] : 0.f);
+        } else if (it.nt > 0) {
+          float* o = p.ws_o + ((size_t)it.slot * NR + c0) * R + d;
 #pragma unroll
-            for (int x = 0; x < 16; ++x)
-              if (c + x < it.rows) o[(size_t)x * R] = __uint_as_float(v[x]);
-          }
+          for (int c = 0; c < CW; ++c)
+            if (c0 + c < it.rows) o[(size_t)c * R] = __uint_as_float(v[c]);
         }
       }
       if (it.nt > 0) {
         tc_fence_before();
-        mbar_arrive(&sh->o_free);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->o_free);
       }
-      named_sync(1, 128);                    // f and red are free again
+      named_sync(1, 256);                    // f and red are free again
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 5) tmem_dealloc(tmem, Lay::kTmem);
+  if (warp == 12) tmem_dealloc(tmem, Lay::kTmem);
 }
 
 // Joins the row groups that a cut left in several CTAs.  grid (row groups, NR / 8): a warp per row.
@@ -811,6 +878,7 @@ extern "C" int pa_latent_decode(void* out, const void* query, const int32_t* que
   char* ws = static_cast<char*>(workspace);
   LatentParams p = {};
   p.out = static_cast<__nv_bfloat16*>(out);
+  p.cache = static_cast<const __nv_bfloat16*>(cache);
   p.query_start = query_start;
   p.block_tables = block_tables;
   p.context_lens = context_lens;
