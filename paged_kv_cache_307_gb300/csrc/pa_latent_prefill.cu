@@ -211,11 +211,16 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
       for (int i = max(0, nv - 2); i < nv; ++i) mbar_wait(&sh->full_v[i & 1], (uint32_t)(i >> 1) & 1u);
     }
     // ------------------------------------------------------------ MMA issuer
-    if (warp == 9 && lane == 0 && most > 0) {
+    // The whole warp walks, with values that are the same in all lanes, and one lane issues: the
+    // descriptors then stay in uniform registers.
+    if (warp == 9 && most > 0) {
+      const bool lead = elect_one();
+      const uint32_t sb = __shfl_sync(0xffffffffu, sbase, 0), t0 = __shfl_sync(0xffffffffu, tmem, 0);
+      const int n0 = __shfl_sync(0xffffffffu, nt[0], 0), n1 = __shfl_sync(0xffffffffu, nt[1], 0);
       const uint32_t idS = idesc_bf16_f32(kRows, kKT, false, false);
       const uint32_t idO = idesc_bf16_f32(kRows, p.Dv, false, true);
-      const uint64_t dq = sdesc_sw128(sbase, 16, 1024), dk = sdesc_sw128(sbase + kOffK, 16, 1024);
-      const uint64_t dv = sdesc_sw128(sbase + kOffV, kChunk / 2, 1024);
+      const uint64_t dq = sdesc_sw128(sb, 16, 1024), dk = sdesc_sw128(sb + kOffK, 16, 1024);
+      const uint64_t dv = sdesc_sw128(sb + kOffV, kChunk / 2, 1024);
       const int own_steps = p.Dk / 16, rope_steps = p.P / 16;
       bool ok = true;
       auto scores = [&](int x, int j) {
@@ -223,17 +228,24 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
         ok = ok && wait(&sh->full_k[j & 1], (uint32_t)(j >> 1) & 1u, abort_flag);
         if (!ok) return;
         tc_fence_after();
-        const uint64_t da = sdesc_at(dq, x * 3 * kChunk), db = sdesc_at(dk, (j & 1) * 3 * kChunk);
-        const uint32_t d = tmem + x * 128;
-        for (int kk = 0; kk < own_steps; ++kk) {
-          const uint32_t off = (kk >> 2) * kChunk + (kk & 3) * 32;
-          umma_bf16(d, sdesc_at(da, off), sdesc_at(db, off), idS, kk > 0 ? 1u : 0u);
+        if (lead) {
+          const uint64_t da = sdesc_at(dq, x * 3 * kChunk), db = sdesc_at(dk, (j & 1) * 3 * kChunk);
+          const uint32_t d = t0 + x * 128;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            if (kk >= own_steps) break;
+            umma_bf16(d, sdesc_at(da, (kk >> 2) * kChunk + (kk & 3) * 32), sdesc_at(db, (kk >> 2) * kChunk + (kk & 3) * 32), idS,
+                      kk > 0 ? 1u : 0u);
+          }
+          const uint64_t ra = sdesc_at(da, ncd * kChunk), rb = sdesc_at(db, ncd * kChunk);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk >= rope_steps) break;
+            umma_bf16(d, sdesc_at(ra, kk * 32), sdesc_at(rb, kk * 32), idS, 1u);
+          }
+          umma_commit(&sh->s[x]);
         }
-        for (int kk = 0; kk < rope_steps; ++kk) {
-          const uint32_t off = ncd * kChunk + kk * 32;
-          umma_bf16(d, sdesc_at(da, off), sdesc_at(db, off), idS, 1u);
-        }
-        umma_commit(&sh->s[x]);
+        __syncwarp();
       };
       auto values = [&](int x, int j, bool frees) {
         ok = ok && wait(&sh->p[x], (uint32_t)j & 1u, abort_flag);
@@ -241,27 +253,31 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
           ok = ok && wait(&sh->full_v[v], (uint32_t)j & 1u, abort_flag);
           if (!ok) return;
           tc_fence_after();
-          const uint64_t db = sdesc_at(dv, v * kChunk);
+          if (lead) {
+            const uint64_t db = sdesc_at(dv, v * kChunk);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_bf16_ts(tmem + kColO + x * 128, tmem + x * 128 + v * 32 + kk * 8, sdesc_at(db, kk * 2048), idO,
-                         j > 0 || v > 0 || kk > 0 ? 1u : 0u);
-          if (frees) umma_commit(&sh->empty_v[v]);
+            for (int kk = 0; kk < 4; ++kk)
+              umma_bf16_ts(t0 + kColO + x * 128, t0 + x * 128 + v * 32 + kk * 8, sdesc_at(db, kk * 2048), idO,
+                           j > 0 || v > 0 || kk > 0 ? 1u : 0u);
+            if (frees) umma_commit(&sh->empty_v[v]);
+            if (v == 1) umma_commit(&sh->pv[x]);
+          }
+          __syncwarp();
         }
-        umma_commit(&sh->pv[x]);
       };
       // (the row tile that sees a key tile last frees it)
-      if (nt[0] > 0) scores(0, 0);
-      if (nt[1] > 0) scores(1, 0);
-      if (ok) umma_commit(&sh->empty_k[0]);
-      for (int j = 0; ok && j < most; ++j) {
-        if (j < nt[0]) values(0, j, j >= nt[1]);
-        if (j + 1 < nt[0]) scores(0, j + 1);
-        if (j < nt[1]) values(1, j, true);
-        if (j + 1 < nt[1]) scores(1, j + 1);
-        if (ok && j + 1 < most) umma_commit(&sh->empty_k[(j + 1) & 1]);
+      if (n0 > 0) scores(0, 0);
+      if (n1 > 0) scores(1, 0);
+      if (ok && lead) umma_commit(&sh->empty_k[0]);
+      for (int j = 0; ok && j < max(n0, n1); ++j) {
+        if (j < n0) values(0, j, j >= n1);
+        if (j + 1 < n0) scores(0, j + 1);
+        if (j < n1) values(1, j, true);
+        if (j + 1 < n1) scores(1, j + 1);
+        if (ok && lead && j + 1 < max(n0, n1)) umma_commit(&sh->empty_k[(j + 1) & 1]);
+        __syncwarp();
       }
-      umma_commit(&sh->drain);               // every MMA has completed before TMEM is freed
+      if (lead) umma_commit(&sh->drain);     // every MMA has completed before TMEM is freed
       mbar_wait(&sh->drain, 0);
     }
   } else {
