@@ -33,19 +33,17 @@ static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "
 
 struct PrefillParams {
   __nv_bfloat16* out;
+  const __nv_bfloat16 *q, *kv, *key;         // for single rows; the tiles go by tensor maps
+  long long key_stride;
   const int32_t *query_start, *kv_start;
   int B, H, Dk, P, Dv, rows, kv_rows;
   float qscale;
 };
 
 struct Shared {
-  uint64_t q[2], full_k[2], empty_k[2], full_v[2], empty_v[2], s[2], p[2], pv[2], drain;
-  int bad_from[128];                         // per value element: first key that is not finite, of the masked ones
-  int any_bad;
+  uint64_t q[2], q_empty[2], full_k[2], empty_k[2], full_v[2], empty_v[2], s[2], p[2][2], pv[2], o_free[2], drain;
   uint32_t tmem_base;
   int abort;
-  int scan[kThreads / 32];
-  int unit[3];                               // sequence, tile of it, units in all
 };
 constexpr uint32_t kSmemBytes = kOffBar + (uint32_t)sizeof(Shared) + 1024u;
 static_assert(kSmemBytes <= 232448, "shared memory");
@@ -76,6 +74,90 @@ __device__ __forceinline__ int rows_of(const PrefillParams& p, int b) {
   return a >= 0 && e >= a && e <= p.rows && u >= 0 && v >= u && v <= p.kv_rows ? e - a : -1;
 }
 
+// The work: (unit, head) pairs, heads innermost, a unit being 256 rows of a sequence; the units
+// of all sequences in order, every sequence's last, and longest, unit first.  The CTAs take
+// them in rounds, forth and back, so that no CTA has the longer ones of every round; a warp walks
+// its CTA's by itself, 32 sequences a step.
+struct Item {
+  int h, q0, n, k0, L, first, past;          // head; rows; keys; the item's first row of the sequence's, its position
+  int nt[2];                                 // key tiles that each row tile sees
+};
+struct Walk {
+  int round, b, base;                        // next round; a sequence at or before its unit's, units before that
+  __device__ __forceinline__ bool next(const PrefillParams& p, int lane, Item& it) {
+    const int item = round * (int)gridDim.x + (int)((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    ++round;
+    const int unit = item / p.H;
+    it.h = item - unit * p.H;
+    for (; b < p.B; b += 32) {
+      const int k = b + lane < p.B ? (max(rows_of(p, b + lane), 0) + 2 * kRows - 1) / (2 * kRows) : 0;
+      int incl = k;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += y;
+      }
+      const uint32_t beyond = __ballot_sync(0xffffffffu, base + incl > unit);
+      if (beyond) {
+        const int at = __ffs(beyond) - 1;
+        base += __shfl_sync(0xffffffffu, incl - k, at);
+        const int units = __shfl_sync(0xffffffffu, k, at);
+        b += at;
+        it.q0 = __ldg(&p.query_start[b]);
+        it.n = __ldg(&p.query_start[b + 1]) - it.q0;
+        it.k0 = __ldg(&p.kv_start[b]);
+        it.L = __ldg(&p.kv_start[b + 1]) - it.k0;
+        it.first = (base + units - 1 - unit) * 2 * kRows;
+        it.past = it.L - it.n + it.first;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int r = min(it.n - it.first - x * kRows, kRows);
+          const int end = r > 0 ? min(it.L, max(0, it.past + x * kRows + r)) : 0;
+          it.nt[x] = (end + kKT - 1) / kKT;
+        }
+        return true;
+      }
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return false;
+  }
+};
+
+// One output row by a warp: query row `row` of head h over the first n keys from k0 on, a key a
+// lane for the scores, then elements a lane for the values.
+__device__ __noinline__ void plain_row(const PrefillParams& p, int row, int h, int k0, int n, int lane) {
+  const __nv_bfloat16* q = p.q + ((size_t)row * p.H + h) * (p.Dk + p.P);
+  auto score = [&](int t) -> float {
+    if (t >= n) return -INFINITY;
+    const __nv_bfloat16* k = p.kv + ((size_t)(k0 + t) * p.H + h) * (p.Dk + p.Dv);
+    const __nv_bfloat16* kr = p.key + (k0 + t) * p.key_stride;
+    float s = 0.f;
+    for (int d = 0; d < p.Dk; ++d) s = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), s);
+    for (int d = 0; d < p.P; ++d) s = fmaf(__bfloat162float(q[p.Dk + d]), __bfloat162float(kr[d]), s);
+    return s * p.qscale;
+  };
+  float m = -INFINITY;
+  for (int t = 0; t < n; t += 32) m = fmaxf(m, score(t + lane));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < n; t += 32) {
+    const float w = exp2f(score(t + lane) - m);
+    l += w;
+    for (int i = 0; i < min(32, n - t); ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const __nv_bfloat16* v = p.kv + ((size_t)(k0 + t + i) * p.H + h) * (p.Dk + p.Dv) + p.Dk;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e * 32 < p.Dv) o[e] = fmaf(wi, __bfloat162float(v[e * 32 + lane]), o[e]);
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+  for (int e = 0; e * 32 < p.Dv; ++e)
+    p.out[((size_t)row * p.H + h) * p.Dv + e * 32 + lane] = __float2bfloat16_rn(o[e] / l);
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
 latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapQr,
                       const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapKr,
@@ -87,149 +169,119 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
   volatile int* abort_flag = &sh->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // ---- work item: the units (256 rows) of all sequences in order, every sequence's last, and
-  // longest, unit first; heads innermost
-  const int unit = (int)(blockIdx.x / p.H), h = (int)(blockIdx.x % p.H);
-  {
-    const int per = (p.B + kThreads - 1) / kThreads;
-    const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
-    int sum = 0;
-    for (int b = b0; b < b1; ++b) {
-      const int n = rows_of(p, b);
-      if (n < 0 && blockIdx.x == 0) atomicOr(&g_status_latent, PA_DEV_BAD_LEN);
-      sum += (max(n, 0) + 2 * kRows - 1) / (2 * kRows);
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < p.B; b += kThreads)
+      if (rows_of(p, b) < 0) atomicOr(&g_status_latent, PA_DEV_BAD_LEN);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->q[i], 1);
+      mbar_init(&sh->q_empty[i], 1);
+      mbar_init(&sh->full_k[i], 1);
+      mbar_init(&sh->empty_k[i], 1);
+      mbar_init(&sh->full_v[i], 1);
+      mbar_init(&sh->empty_v[i], 1);
+      mbar_init(&sh->s[i], 1);
+      mbar_init(&sh->p[i][0], 4);
+      mbar_init(&sh->p[i][1], 4);
+      mbar_init(&sh->pv[i], 1);
+      mbar_init(&sh->o_free[i], 4);
     }
-    int incl = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += y;
-    }
-    if (lane == 31) sh->scan[warp] = incl;
-    __syncthreads();
-    int before = incl - sum, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += sh->scan[w];
-      total += sh->scan[w];
-    }
-    if (unit >= total) return;               // nothing allocated yet
-    if (unit >= before && unit < before + sum) {
-      for (int b = b0; b < b1; ++b) {
-        const int k = (max(rows_of(p, b), 0) + 2 * kRows - 1) / (2 * kRows);
-        if (unit < before + k) {
-          sh->unit[0] = b;
-          sh->unit[1] = before + k - 1 - unit;
-          break;
-        }
-        before += k;
-      }
-    }
-    if (threadIdx.x < 128) sh->bad_from[threadIdx.x] = 0x7fffffff;
-    if (threadIdx.x == 0) {
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&sh->q[i], 1);
-        mbar_init(&sh->full_k[i], 1);
-        mbar_init(&sh->empty_k[i], 1);
-        mbar_init(&sh->full_v[i], 1);
-        mbar_init(&sh->empty_v[i], 1);
-        mbar_init(&sh->s[i], 1);
-        mbar_init(&sh->p[i], 128);
-        mbar_init(&sh->pv[i], 1);
-      }
-      mbar_init(&sh->drain, 1);
-      sh->abort = 0;
-      sh->any_bad = 0;
-      fence_mbar_init();
-    }
-    if (warp == 9) {
-      tmem_alloc(&sh->tmem_base, 512);
-      tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
+    mbar_init(&sh->drain, 1);
+    sh->abort = 0;
+    fence_mbar_init();
   }
-  const int b = sh->unit[0];
-  const int q0 = __ldg(&p.query_start[b]), n = __ldg(&p.query_start[b + 1]) - q0;
-  const int k0 = __ldg(&p.kv_start[b]), L = __ldg(&p.kv_start[b + 1]) - k0;
-  const int first = sh->unit[1] * 2 * kRows;   // first row of the sequence's
-  const int past = L - n + first;              // its position
-  // tiles of keys that each row tile sees
-  int nt[2];
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int r = min(n - first - x * kRows, kRows);           // rows of the tile
-    const int end = r > 0 ? min(L, max(0, past + x * kRows + r)) : 0;
-    nt[x] = (end + kKT - 1) / kKT;
+  if (warp == 9) {
+    tmem_alloc(&sh->tmem_base, 512);
+    tmem_relinquish();
   }
-  const int most = max(nt[0], nt[1]);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
   const int ncd = (p.Dk + 63) / 64, ncv = (p.Dv + 63) / 64;    // chunks of the keys' own part, of the values
+  Walk walk{0, 0, 0};
+  Item it = {};
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     // ------------------------------------------------------------ TMA producer
-    if (warp == 8 && lane == 0 && most > 0) {
+    if (warp == 8) {
       const uint64_t once = policy_evict_first(), keep = policy_evict_last();   // (K, V: other row tiles read them too)
+      int nk = 0, nv = 0, nq[2] = {0, 0};    // key tiles, value halves, row tiles requested
+      bool ok = true;
       auto load_q = [&](int x) {
-        if (nt[x] == 0) return;
+        if (it.nt[x] == 0) return;
+        ok = ok && wait(&sh->q_empty[x], ((uint32_t)nq[x] & 1u) ^ 1u, abort_flag);
+        if (!ok) return;
         mbar_arrive_expect_tx(&sh->q[x], (uint32_t)(ncd + 1) * kChunk);
-        for (int c = 0; c < ncd; ++c)
-          tma_load_4d(smem + (x * 3 + c) * kChunk, &mapQ, &sh->q[x], c * 64, h, q0 + first + x * kRows, 0, once);
-        tma_load_4d(smem + (x * 3 + ncd) * kChunk, &mapQr, &sh->q[x], 0, h, q0 + first + x * kRows, 0, once);
+        const int row = it.q0 + it.first + x * kRows;
+        for (int c = 0; c < ncd; ++c) tma_load_4d(smem + (x * 3 + c) * kChunk, &mapQ, &sh->q[x], c * 64, it.h, row, 0, once);
+        tma_load_4d(smem + (x * 3 + ncd) * kChunk, &mapQr, &sh->q[x], 0, it.h, row, 0, once);
+        ++nq[x];
       };
-      int nk = 0, nv = 0;
-      auto load_k = [&](int j) -> bool {
-        const int st = j & 1;
-        if (!wait(&sh->empty_k[st], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag)) return false;
+      auto load_k = [&](int j) {
+        const int st = nk & 1;
+        ok = ok && wait(&sh->empty_k[st], ((uint32_t)(nk >> 1) & 1u) ^ 1u, abort_flag);
+        if (!ok) return;
         mbar_arrive_expect_tx(&sh->full_k[st], (uint32_t)(ncd + 1) * kChunk);
         unsigned char* dst = smem + kOffK + st * 3 * kChunk;
         for (int c = 0; c < ncd; ++c)
-          tma_load_4d(dst + c * kChunk, &mapK, &sh->full_k[st], c * 64, h, k0 + j * kKT, 0, keep);
-        tma_load_4d(dst + ncd * kChunk, &mapKr, &sh->full_k[st], 0, k0 + j * kKT, 0, 0, keep);
-        nk = j + 1;
-        return true;
+          tma_load_4d(dst + c * kChunk, &mapK, &sh->full_k[st], c * 64, it.h, it.k0 + j * kKT, 0, keep);
+        tma_load_4d(dst + ncd * kChunk, &mapKr, &sh->full_k[st], 0, it.k0 + j * kKT, 0, 0, keep);
+        ++nk;
       };
-      load_q(0);
-      bool ok = load_k(0);
-      load_q(1);
-      for (int j = 0; ok && j < most; ++j) {
-        if (j + 1 < most && !(ok = load_k(j + 1))) break;
-        for (int v = 0; v < 2; ++v) {
-          if (!(ok = wait(&sh->empty_v[v], ((uint32_t)j & 1u) ^ 1u, abort_flag))) break;
-          mbar_arrive_expect_tx(&sh->full_v[v], (uint32_t)ncv * kChunk / 2);
-          for (int c = 0; c < ncv; ++c)
-            tma_load_4d(smem + kOffV + v * kChunk + c * (kChunk / 2), &mapV, &sh->full_v[v], c * 64, h,
-                        k0 + j * kKT + v * 64, 0, keep);
-          nv = 2 * j + v + 1;
+      while (ok && walk.next(p, lane, it)) {
+        const int most = max(it.nt[0], it.nt[1]);
+        if (lane == 0 && most > 0) {
+          load_q(0);
+          load_k(0);
+          load_q(1);
+          for (int j = 0; ok && j < most; ++j) {
+            if (j + 1 < most) load_k(j + 1);
+            for (int v = 0; v < 2; ++v) {
+              ok = ok && wait(&sh->empty_v[v], ((uint32_t)(nv >> 1) & 1u) ^ 1u, abort_flag);
+              if (!ok) break;
+              mbar_arrive_expect_tx(&sh->full_v[v], (uint32_t)ncv * kChunk / 2);
+              for (int c = 0; c < ncv; ++c)
+                tma_load_4d(smem + kOffV + v * kChunk + c * (kChunk / 2), &mapV, &sh->full_v[v], c * 64, it.h,
+                            it.k0 + j * kKT + v * 64, 0, keep);
+              ++nv;
+            }
+          }
         }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
       // no TMA write may land after the CTA has left
-      for (int x = 0; x < 2; ++x)
-        if (nt[x] > 0) mbar_wait(&sh->q[x], 0);
-      for (int j = max(0, nk - 2); j < nk; ++j) mbar_wait(&sh->full_k[j & 1], (uint32_t)(j >> 1) & 1u);
-      for (int i = max(0, nv - 2); i < nv; ++i) mbar_wait(&sh->full_v[i & 1], (uint32_t)(i >> 1) & 1u);
+      if (lane == 0) {
+        for (int x = 0; x < 2; ++x)
+          if (nq[x] > 0) mbar_wait(&sh->q[x], (uint32_t)(nq[x] - 1) & 1u);
+        for (int j = max(0, nk - 2); j < nk; ++j) mbar_wait(&sh->full_k[j & 1], (uint32_t)(j >> 1) & 1u);
+        for (int i = max(0, nv - 2); i < nv; ++i) mbar_wait(&sh->full_v[i & 1], (uint32_t)(i >> 1) & 1u);
+      }
+      __syncwarp();
     }
     // ------------------------------------------------------------ MMA issuer
     // The whole warp walks, with values that are the same in all lanes, and one lane issues: the
     // descriptors then stay in uniform registers.
-    if (warp == 9 && most > 0) {
+    if (warp == 9) {
       const bool lead = elect_one();
       const uint32_t sb = __shfl_sync(0xffffffffu, sbase, 0), t0 = __shfl_sync(0xffffffffu, tmem, 0);
-      const int n0 = __shfl_sync(0xffffffffu, nt[0], 0), n1 = __shfl_sync(0xffffffffu, nt[1], 0);
       const uint32_t idS = idesc_bf16_f32(kRows, kKT, false, false);
       const uint32_t idO = idesc_bf16_f32(kRows, p.Dv, false, true);
       const uint64_t dq = sdesc_sw128(sb, 16, 1024), dk = sdesc_sw128(sb + kOffK, 16, 1024);
       const uint64_t dv = sdesc_sw128(sb + kOffV, kChunk / 2, 1024);
       const int own_steps = p.Dk / 16, rope_steps = p.P / 16;
       bool ok = true;
-      auto scores = [&](int x, int j) {
-        if (j == 0) ok = ok && wait(&sh->q[x], 0, abort_flag);
-        ok = ok && wait(&sh->full_k[j & 1], (uint32_t)(j >> 1) & 1u, abort_flag);
+      int kc = 0, nq[2] = {0, 0}, np[2] = {0, 0};              // key tiles, row tiles, P tiles before this item
+      // S_x against key tile j of the item
+      auto scores = [&](int x, int j, bool last) {
+        if (j == 0) ok = ok && wait(&sh->q[x], (uint32_t)nq[x] & 1u, abort_flag);
+        const int k = kc + j;
+        ok = ok && wait(&sh->full_k[k & 1], (uint32_t)(k >> 1) & 1u, abort_flag);
         if (!ok) return;
         tc_fence_after();
         if (lead) {
-          const uint64_t da = sdesc_at(dq, x * 3 * kChunk), db = sdesc_at(dk, (j & 1) * 3 * kChunk);
+          const uint64_t da = sdesc_at(dq, x * 3 * kChunk), db = sdesc_at(dk, (k & 1) * 3 * kChunk);
           const uint32_t d = t0 + x * 128;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
@@ -244,13 +296,16 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
             umma_bf16(d, sdesc_at(ra, kk * 32), sdesc_at(rb, kk * 32), idS, 1u);
           }
           umma_commit(&sh->s[x]);
+          if (last) umma_commit(&sh->q_empty[x]);
         }
         __syncwarp();
       };
+      // O_x += P_x V of key tile j, half a tile of keys at a time
       auto values = [&](int x, int j, bool frees) {
-        ok = ok && wait(&sh->p[x], (uint32_t)j & 1u, abort_flag);
+#pragma unroll
         for (int v = 0; v < 2; ++v) {
-          ok = ok && wait(&sh->full_v[v], (uint32_t)j & 1u, abort_flag);
+          ok = ok && wait(&sh->p[x][v], (uint32_t)(np[x] + j) & 1u, abort_flag);
+          ok = ok && wait(&sh->full_v[v], (uint32_t)(kc + j) & 1u, abort_flag);
           if (!ok) return;
           tc_fence_after();
           if (lead) {
@@ -265,17 +320,28 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
           __syncwarp();
         }
       };
-      // (the row tile that sees a key tile last frees it)
-      if (n0 > 0) scores(0, 0);
-      if (n1 > 0) scores(1, 0);
-      if (ok && lead) umma_commit(&sh->empty_k[0]);
-      for (int j = 0; ok && j < max(n0, n1); ++j) {
-        if (j < n0) values(0, j, j >= n1);
-        if (j + 1 < n0) scores(0, j + 1);
-        if (j < n1) values(1, j, true);
-        if (j + 1 < n1) scores(1, j + 1);
-        if (ok && lead && j + 1 < max(n0, n1)) umma_commit(&sh->empty_k[(j + 1) & 1]);
-        __syncwarp();
+      while (ok && walk.next(p, lane, it)) {
+        const int n0 = __shfl_sync(0xffffffffu, it.nt[0], 0), n1 = __shfl_sync(0xffffffffu, it.nt[1], 0);
+        const int most = max(n0, n1);
+        if (n0 > 0) scores(0, 0, n0 == 1);
+        if (n1 > 0) scores(1, 0, n1 == 1);
+        if (ok && lead && most > 0) umma_commit(&sh->empty_k[kc & 1]);
+        // the last outputs of both row tiles have been read
+        for (int x = 0; x < 2; ++x) ok = ok && wait(&sh->o_free[x], ((uint32_t)nq[x] & 1u) ^ 1u, abort_flag);
+        for (int j = 0; ok && j < most; ++j) {
+          if (j < n0) values(0, j, j >= n1);
+          if (j + 1 < n0) scores(0, j + 1, j + 2 == n0);
+          if (j < n1) values(1, j, true);
+          if (j + 1 < n1) scores(1, j + 1, j + 2 == n1);
+          // (the row tile that sees a key tile last frees it)
+          if (ok && lead && j + 1 < most) umma_commit(&sh->empty_k[(kc + j + 1) & 1]);
+          __syncwarp();
+        }
+        kc += most;
+        nq[0] += n0 > 0;
+        nq[1] += n1 > 0;
+        np[0] += n0;
+        np[1] += n1;
       }
       if (lead) umma_commit(&sh->drain);     // every MMA has completed before TMEM is freed
       mbar_wait(&sh->drain, 0);
@@ -287,146 +353,137 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
     const int r = (int)threadIdx.x & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + x * 128 + lane_off, tO = tmem + kColO + x * 128 + lane_off;
-    const int row = first + x * kRows + r;   // of the sequence
-    const int pos = past + x * kRows + r;
-    const int mine = x == 0 ? nt[0] : nt[1];
-    float m_ref = -INFINITY, lsum = 0.f;
-    for (int j = 0; j < mine; ++j) {
-      wait(&sh->s[x], (uint32_t)j & 1u, abort_flag);
-      __syncwarp();
-      tc_fence_after();
-      uint32_t v[4][32];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld32(tS + i * 32, v[i]);
-      tmem_ld_wait();
-      const int seen = min(pos, L - 1) - j * kKT;              // last key of the tile that the row sees
-      if (__any_sync(0xffffffffu, seen < kKT - 1)) {
-#pragma unroll
-        for (int c = 0; c < kKT; ++c)
-          if (c > seen) v[c >> 5][c & 31] = __float_as_uint(-INFINITY);
-      }
-      float mx8[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) mx8[i] = __uint_as_float(v[0][i]);
-#pragma unroll
-      for (int c = 8; c < kKT; c += 2)
-        mx8[(c >> 1) & 7] = fmax3(mx8[(c >> 1) & 7], __uint_as_float(v[c >> 5][c & 31]), __uint_as_float(v[c >> 5][(c + 1) & 31]));
-      float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])) * p.qscale;
-      const bool need = mx > m_ref + kSlack;
-      const float alpha = need ? exp2f(m_ref - mx) : 1.f;      // (m_ref = -inf gives 0)
-      if (need) m_ref = mx;
-      if (j > 0 && __any_sync(0xffffffffu, need)) {
-        // O holds P V of the tile before
-        wait(&sh->pv[x], (uint32_t)(j - 1) & 1u, abort_flag);
+    int kc = 0, np = 0;                      // key tiles, tiles of P before this item
+    while (walk.next(p, lane, it)) {
+      const int row = it.first + x * kRows + r;                // of the sequence
+      const int pos = it.past + x * kRows + r;
+      const int mine = x == 0 ? it.nt[0] : it.nt[1];
+      float m_ref = -INFINITY, lsum = 0.f;
+      for (int j = 0; j < mine; ++j) {
+        wait(&sh->s[x], (uint32_t)(np + j) & 1u, abort_flag);
         __syncwarp();
         tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < p.Dv; c += 16) {
-          uint32_t w[16];
-          tmem_ld16(tO + c, w);
-          tmem_ld_wait();
+        uint32_t v[4][32];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
-          tmem_st16(tO + c, w);
-        }
-        tmem_st_wait();
-      }
-      lsum *= alpha;
-      const float negm = m_ref == -INFINITY ? 0.f : -m_ref;
-      const uint64_t qs2 = f2pack(p.qscale, p.qscale), nm2 = f2pack(negm, negm);
-      uint64_t ls2[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ls2[i] = f2pack(0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t pw[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          float x0, x1;
-          f2unpack(ffma2(f2pack(__uint_as_float(v[i][2 * c]), __uint_as_float(v[i][2 * c + 1])), qs2, nm2), x0, x1);
-          const float p0 = ex2(x0), p1 = ex2(x1);
-          ls2[c & 3] = fadd2(ls2[c & 3], f2pack(p0, p1));
-          pw[c] = pack_bf16(p0, p1);
-        }
-        tmem_st16(tS + i * 16, pw);
-      }
-      float ls[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f2unpack(ls2[i], ls[2 * i], ls[2 * i + 1]);
-      lsum += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
-      // Values that not every row of the CTA sees: rows behind the context may hold anything, and
-      // 0 * NaN would reach O, so they are zeroed; of the others what is not finite, and the rows
-      // that do see it are told so at the end.  The row tile whose P V comes first does it.
-      if ((x == 0 || j >= nt[0]) && j * kKT + kKT - 1 > past) {
-        const int key = j * kKT + r;
-        wait(&sh->full_v[r >> 6], (uint32_t)j & 1u, abort_flag);
-        if (key > past) {
-          unsigned char* vrow = smem + kOffV + (r >> 6) * kChunk + (r & 63) * 128;
-          for (int c = 0; c < ncv * 8; ++c) {
-            uint4* w = reinterpret_cast<uint4*>(vrow + (c >> 3) * (kChunk / 2) + (c & 7) * 16);
-            if (key >= L) {
-              *w = make_uint4(0u, 0u, 0u, 0u);
-              continue;
-            }
-            uint32_t y[4] = {w->x, w->y, w->z, w->w};
-            bool bad = false;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              bad = bad || (y[i] & 0x7f80u) == 0x7f80u || (y[i] & 0x7f800000u) == 0x7f800000u;
-            if (bad) {
-              const int d = (c >> 3) * 64 + (((c & 7) ^ (r & 7)) << 3);     // first element of the piece
-              sh->any_bad = 1;
-              for (int i = 0; i < 4; ++i) {
-                if ((y[i] & 0x7f80u) == 0x7f80u) {
-                  atomicMin(&sh->bad_from[d + 2 * i], key);
-                  y[i] &= 0xffff0000u;
-                }
-                if ((y[i] & 0x7f800000u) == 0x7f800000u) {
-                  atomicMin(&sh->bad_from[d + 2 * i + 1], key);
-                  y[i] &= 0xffffu;
-                }
-              }
-              *w = make_uint4(y[0], y[1], y[2], y[3]);
-            }
-          }
-          fence_proxy_async_smem();
-        }
-        __syncwarp();
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&sh->p[x]);
-    }
-
-    // ---- O / l as bf16 rows
-    if (mine > 0) {
-      wait(&sh->pv[x], (uint32_t)(mine - 1) & 1u, abort_flag);
-      __syncwarp();
-      tc_fence_after();
-    }
-    const float inv = lsum != 0.f ? 1.f / lsum : 0.f;
-    const bool bad = *static_cast<volatile int*>(&sh->any_bad) != 0;   // (written before the last P this tile used)
-    __nv_bfloat16* o = p.out + ((size_t)(q0 + row) * p.H + h) * p.Dv;
-    for (int c = 0; c < p.Dv; c += 32) {
-      uint32_t w[32];
-      if (mine > 0) {
-        tmem_ld32(tO + c, w);
+        for (int i = 0; i < 4; ++i) tmem_ld32(tS + i * 32, v[i]);
         tmem_ld_wait();
-      }
-      if (row >= n) continue;
-      if (bad) {
+        const int seen = min(pos, it.L - 1) - j * kKT;         // last key of the tile that the row sees
+        if (__any_sync(0xffffffffu, seen < kKT - 1)) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (pos >= sh->bad_from[c + i]) w[i] = 0x7fc00000u;
-      }
+          for (int c = 0; c < kKT; ++c)
+            if (c > seen) v[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+        }
+        float mx8[8];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        uint32_t y[4];
+        for (int i = 0; i < 8; ++i) mx8[i] = __uint_as_float(v[0][i]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          y[i] = mine > 0 ? pack_bf16(__uint_as_float(w[g * 8 + 2 * i]) * inv, __uint_as_float(w[g * 8 + 2 * i + 1]) * inv) : 0u;
-        st_v4(o + c + g * 8, make_uint4(y[0], y[1], y[2], y[3]));
+        for (int c = 8; c < kKT; c += 2)
+          mx8[(c >> 1) & 7] = fmax3(mx8[(c >> 1) & 7], __uint_as_float(v[c >> 5][c & 31]), __uint_as_float(v[c >> 5][(c + 1) & 31]));
+        float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])) * p.qscale;
+        const bool need = mx > m_ref + kSlack;
+        const float alpha = need ? exp2f(m_ref - mx) : 1.f;    // (m_ref = -inf gives 0)
+        if (need) m_ref = mx;
+        if (j > 0 && __any_sync(0xffffffffu, need)) {
+          // O holds P V of the tile before
+          wait(&sh->pv[x], (uint32_t)(np + j - 1) & 1u, abort_flag);
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < p.Dv; c += 16) {
+            uint32_t w[16];
+            tmem_ld16(tO + c, w);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+            tmem_st16(tO + c, w);
+          }
+          tmem_st_wait();
+        }
+        lsum *= alpha;
+        const float negm = m_ref == -INFINITY ? 0.f : -m_ref;
+        const uint64_t qs2 = f2pack(p.qscale, p.qscale), nm2 = f2pack(negm, negm);
+        uint64_t ls2[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ls2[i] = f2pack(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t pw[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            float x0, x1;
+            f2unpack(ffma2(f2pack(__uint_as_float(v[i][2 * c]), __uint_as_float(v[i][2 * c + 1])), qs2, nm2), x0, x1);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            ls2[c & 3] = fadd2(ls2[c & 3], f2pack(p0, p1));
+            pw[c] = pack_bf16(p0, p1);
+          }
+          tmem_st16(tS + i * 16, pw);
+          if (i == 1 && (x == 0 || j >= it.nt[0]) && (j + 1) * kKT > it.L) {
+            // Rows behind the context may hold anything, and 0 * NaN would reach O: zeros, from the
+            // row tile whose P V comes first, before any of its P is handed over.
+            wait(&sh->full_v[r >> 6], (uint32_t)(kc + j) & 1u, abort_flag);
+            if (j * kKT + r >= it.L) {
+              unsigned char* vrow = smem + kOffV + (r >> 6) * kChunk + (r & 63) * 128;
+              for (int c = 0; c < ncv * 8; ++c)  // (each row in another order: the banks are all in use)
+                *reinterpret_cast<uint4*>(vrow + (c >> 3) * (kChunk / 2) + (((c + r) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+              fence_proxy_async_smem();
+            }
+            __syncwarp();
+          }
+          if (i & 1) {
+            // half a tile of P: its product may begin
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->p[x][i >> 1]);
+          }
+        }
+        float ls[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f2unpack(ls2[i], ls[2 * i], ls[2 * i + 1]);
+        lsum += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
       }
+
+      // ---- O / l as bf16 rows
+      if (mine > 0) {
+        wait(&sh->pv[x], (uint32_t)(np + mine - 1) & 1u, abort_flag);
+        __syncwarp();
+        tc_fence_after();
+      }
+      const float inv = lsum != 0.f ? 1.f / lsum : 0.f;
+      __nv_bfloat16* o = p.out + ((size_t)(it.q0 + row) * p.H + it.h) * p.Dv;
+      uint32_t full = 0;                     // carries of exponents that are all ones
+      for (int c = 0; c < p.Dv; c += 32) {
+        uint32_t w[32];
+        if (mine > 0) {
+          tmem_ld32(tO + c, w);
+          tmem_ld_wait();
+        }
+        if (row >= it.n) continue;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          uint32_t y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            y[i] = mine > 0 ? pack_bf16(__uint_as_float(w[g * 8 + 2 * i]) * inv, __uint_as_float(w[g * 8 + 2 * i + 1]) * inv) : 0u;
+          full |= ((y[0] & 0x7f807f80u) + 0x00800080u) | ((y[1] & 0x7f807f80u) + 0x00800080u) |
+                  ((y[2] & 0x7f807f80u) + 0x00800080u) | ((y[3] & 0x7f807f80u) + 0x00800080u);
+          st_v4(o + c + g * 8, make_uint4(y[0], y[1], y[2], y[3]));
+        }
+      }
+      if (mine > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->o_free[x]);
+      }
+      // A value that is not finite reaches every row of the tile, the ones that do not see it by
+      // 0 * NaN.  Rows with finite weights and an output that is not are done again by themselves.
+      const bool redo = (full & 0x80008000u) && lsum - lsum == 0.f;
+      for (uint32_t todo = __ballot_sync(0xffffffffu, redo); todo; todo &= todo - 1) {
+        const int who = __ffs(todo) - 1;
+        plain_row(p, it.q0 + __shfl_sync(0xffffffffu, row, who), it.h, it.k0, __shfl_sync(0xffffffffu, pos, who) + 1, lane);
+      }
+      kc += max(it.nt[0], it.nt[1]);
+      np += mine;
     }
   }
   tc_fence_before();
@@ -455,7 +512,7 @@ extern "C" int pa_latent_prefill(void* out, const void* query, const int32_t* qu
       !(scale > 0.f) || (long long)total_queries * num_heads > 0x7fffffffll)
     return PA_ERR_SHAPE;
   const long long units = (long long)total_queries / (2 * kRows) + num_seqs;
-  if (units * num_heads > 0x7fffffffll) return PA_ERR_SHAPE;
+  if (units * num_heads > 0x7fff0000ll) return PA_ERR_SHAPE;
   if (num_seqs == 0 || total_queries == 0) return PA_OK;
   if (!out || !query || !query_start || !kv_start || (total_kv && (!kv || !key_rope))) return PA_ERR_NULL;
   if (!aligned16(out) || !aligned16(query) || !aligned16(kv) || !aligned16(key_rope) || key_rope_stride % 8)
@@ -488,6 +545,10 @@ extern "C" int pa_latent_prefill(void* out, const void* query, const int32_t* qu
   if (!raise_smem_limit(reinterpret_cast<const void*>(&latent_prefill_kernel), dev)) return PA_ERR_CUDA;
   PrefillParams p = {};
   p.out = static_cast<__nv_bfloat16*>(out);
+  p.q = static_cast<const __nv_bfloat16*>(query);
+  p.kv = static_cast<const __nv_bfloat16*>(kv);
+  p.key = static_cast<const __nv_bfloat16*>(key_rope);
+  p.key_stride = key_rope_stride;
   p.query_start = query_start;
   p.kv_start = kv_start;
   p.B = num_seqs;
@@ -498,8 +559,9 @@ extern "C" int pa_latent_prefill(void* out, const void* query, const int32_t* qu
   p.rows = total_queries;
   p.kv_rows = total_kv;
   p.qscale = scale * kLog2e;
+  const int sms = device_sm_count();
   void* args[] = {&mapQ, &mapQr, &mapK, &mapKr, &mapV, &p};
-  return ck(cudaLaunchKernel(reinterpret_cast<const void*>(&latent_prefill_kernel), dim3((unsigned)(units * num_heads)),
+  return ck(cudaLaunchKernel(reinterpret_cast<const void*>(&latent_prefill_kernel), dim3((unsigned)(units * num_heads < sms ? units * num_heads : sms)),
                              dim3(kThreads), args, kSmemBytes, (cudaStream_t)stream),
             "cudaLaunchKernel(latent_prefill_kernel)")
              ? PA_OK
