@@ -27,8 +27,8 @@ constexpr uint32_t kColO = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;                // log2 units a score may exceed its reference by
 constexpr int kMaxSeqs = 2048;
-// Registers: 384 x 168 at launch, then 2 x 128 x 200 for the softmax and 128 x 104 for the rest.
-constexpr int kLaunchRegs = 168, kSoftmaxRegs = 200, kOtherRegs = 104;
+// Registers: 384 x 168 at launch, then 2 x 128 x 208 for the softmax and 128 x 88 for the rest.
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
 
 struct PrefillParams {
@@ -156,6 +156,57 @@ __device__ __noinline__ void plain_row(const PrefillParams& p, int row, int h, i
   for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
   for (int e = 0; e * 32 < p.Dv; ++e)
     p.out[((size_t)row * p.H + h) * p.Dv + e * 32 + lane] = __float2bfloat16_rn(o[e] / l);
+}
+
+// O / l of a warp's 32 rows as bf16 (zeros if there is no O); returns the carries of exponents
+// that are all ones.
+__device__ __forceinline__ uint32_t write_rows(const PrefillParams& p, uint32_t tO, bool have, float inv, int q0, int row,
+                                            int n, int h, int lane) {
+  uint32_t full = 0;
+  auto packed = [&](const uint32_t* w) -> uint4 {
+    uint32_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[i] = have ? pack_bf16(__uint_as_float(w[2 * i]) * inv, __uint_as_float(w[2 * i + 1]) * inv) : 0u;
+      full |= (y[i] & 0x7f807f80u) + 0x00800080u;
+    }
+    return make_uint4(y[0], y[1], y[2], y[3]);
+  };
+  // 32 elements of 4 rows change places among 4 lanes, which then write 64 bytes of a row together
+  const int row4 = row - (lane & 3);                         // the lanes' first row
+  __nv_bfloat16* o = p.out + ((size_t)(q0 + row4) * p.H + h) * p.Dv + (lane & 3) * 8;
+#pragma unroll 1
+  for (int c = 0; c < p.Dv; c += 32) {
+    uint4 y[4];
+    {
+      uint32_t w[32];
+      if (have) {
+        tmem_ld32(tO + c, w);
+        tmem_ld_wait();
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] = packed(w + k * 8);
+    }
+#pragma unroll
+    for (int s = 1; s < 4; s *= 2) {
+      const bool up = lane & s;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k & s) continue;
+        uint4 give = up ? y[k] : y[k | s];
+        give.x = __shfl_xor_sync(0xffffffffu, give.x, s);
+        give.y = __shfl_xor_sync(0xffffffffu, give.y, s);
+        give.z = __shfl_xor_sync(0xffffffffu, give.z, s);
+        give.w = __shfl_xor_sync(0xffffffffu, give.w, s);
+        if (up) y[k] = give;
+        else y[k | s] = give;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (row4 + k < n) st_v4(o + (size_t)k * p.H * p.Dv + c, y[k]);
+  }
+  return full;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -320,12 +371,14 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
           __syncwarp();
         }
       };
-      while (ok && walk.next(p, lane, it)) {
+      bool more = walk.next(p, lane, it);
+      while (ok && more) {
         const int n0 = __shfl_sync(0xffffffffu, it.nt[0], 0), n1 = __shfl_sync(0xffffffffu, it.nt[1], 0);
         const int most = max(n0, n1);
         if (n0 > 0) scores(0, 0, n0 == 1);
         if (n1 > 0) scores(1, 0, n1 == 1);
         if (ok && lead && most > 0) umma_commit(&sh->empty_k[kc & 1]);
+        more = walk.next(p, lane, it);       // (while the softmax has work)
         // the last outputs of both row tiles have been read
         for (int x = 0; x < 2; ++x) ok = ok && wait(&sh->o_free[x], ((uint32_t)nq[x] & 1u) ^ 1u, abort_flag);
         for (int j = 0; ok && j < most; ++j) {
@@ -354,7 +407,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + x * 128 + lane_off, tO = tmem + kColO + x * 128 + lane_off;
     int kc = 0, np = 0;                      // key tiles, tiles of P before this item
-    while (walk.next(p, lane, it)) {
+    bool more = walk.next(p, lane, it);
+    while (more) {
       const int row = it.first + x * kRows + r;                // of the sequence
       const int pos = it.past + x * kRows + r;
       const int mine = x == 0 ? it.nt[0] : it.nt[1];
@@ -444,32 +498,15 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
       }
 
       // ---- O / l as bf16 rows
+      const int q0 = it.q0, n = it.n, k0 = it.k0, h = it.h, tiles = max(it.nt[0], it.nt[1]);
+      more = walk.next(p, lane, it);         // (its loads run beside the last product)
       if (mine > 0) {
         wait(&sh->pv[x], (uint32_t)(np + mine - 1) & 1u, abort_flag);
         __syncwarp();
         tc_fence_after();
       }
       const float inv = lsum != 0.f ? 1.f / lsum : 0.f;
-      __nv_bfloat16* o = p.out + ((size_t)(it.q0 + row) * p.H + it.h) * p.Dv;
-      uint32_t full = 0;                     // carries of exponents that are all ones
-      for (int c = 0; c < p.Dv; c += 32) {
-        uint32_t w[32];
-        if (mine > 0) {
-          tmem_ld32(tO + c, w);
-          tmem_ld_wait();
-        }
-        if (row >= it.n) continue;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          uint32_t y[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            y[i] = mine > 0 ? pack_bf16(__uint_as_float(w[g * 8 + 2 * i]) * inv, __uint_as_float(w[g * 8 + 2 * i + 1]) * inv) : 0u;
-          full |= ((y[0] & 0x7f807f80u) + 0x00800080u) | ((y[1] & 0x7f807f80u) + 0x00800080u) |
-                  ((y[2] & 0x7f807f80u) + 0x00800080u) | ((y[3] & 0x7f807f80u) + 0x00800080u);
-          st_v4(o + c + g * 8, make_uint4(y[0], y[1], y[2], y[3]));
-        }
-      }
+      const uint32_t full = write_rows(p, tO, mine > 0, inv, q0, row, n, h, lane);
       if (mine > 0) {
         tc_fence_before();
         __syncwarp();
@@ -477,12 +514,12 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
       }
       // A value that is not finite reaches every row of the tile, the ones that do not see it by
       // 0 * NaN.  Rows with finite weights and an output that is not are done again by themselves.
-      const bool redo = (full & 0x80008000u) && lsum - lsum == 0.f;
+      const bool redo = (full & 0x80008000u) && lsum - lsum == 0.f && row < n;
       for (uint32_t todo = __ballot_sync(0xffffffffu, redo); todo; todo &= todo - 1) {
         const int who = __ffs(todo) - 1;
-        plain_row(p, it.q0 + __shfl_sync(0xffffffffu, row, who), it.h, it.k0, __shfl_sync(0xffffffffu, pos, who) + 1, lane);
+        plain_row(p, q0 + __shfl_sync(0xffffffffu, row, who), h, k0, __shfl_sync(0xffffffffu, pos, who) + 1, lane);
       }
-      kc += max(it.nt[0], it.nt[1]);
+      kc += tiles;
       np += mine;
     }
   }
