@@ -16,13 +16,17 @@ namespace {
 
 __device__ unsigned g_status_latent;
 
-constexpr int kThreads = 384;                // warps 0-3 and 4-7: softmax of a tile each; 8 TMA, 9 MMA, 10-11 none
+constexpr int kThreads = 384;                // warps 0-3 and 4-7: softmax of a tile each; 8 TMA, 9 and 10 MMA of a tile each
 constexpr int kRows = 128;                   // query rows of a tile
 constexpr int kKT = 128;                     // keys per tile
 constexpr uint32_t kChunk = 16384;           // 128 rows x 64 elements
-constexpr uint32_t kOffK = 6 * kChunk;       // Q: 2 tiles x 3 chunks; K: 2 stages x 3 chunks
-constexpr uint32_t kOffV = kOffK + 6 * kChunk;   // V: 2 halves of 64 keys x 2 chunks of 8 KB
-constexpr uint32_t kOffBar = kOffV + 2 * kChunk;
+// Q: 2 tiles x 3 chunks; then a ring of 16 KB slots, which a key tile after the other takes for its
+// K chunks (128 keys x 64 elements) and its two halves of V (64 keys x up to 128 elements).  One
+// ring: a tile's last K then has the place of the V before it (a ring of two K and one V held
+// every tile up by its V, about 1000 clocks).
+constexpr int kSlots = 8;
+constexpr uint32_t kOffRing = 6 * kChunk;
+constexpr uint32_t kOffBar = kOffRing + kSlots * kChunk;
 constexpr uint32_t kColO = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;                // log2 units a score may exceed its reference by
@@ -41,9 +45,10 @@ struct PrefillParams {
 };
 
 struct Shared {
-  uint64_t q[2], q_empty[2], full_k[2], empty_k[2], full_v[2], empty_v[2], s[2], p[2][2], pv[2], o_free[2], drain;
+  uint64_t empty[kSlots], full_k[2], full_v[2], q[2], q_empty[2], s[2], p[2][2], pv[2], o_free[2], drain[2];
   uint32_t tmem_base;
   int abort;
+  int turn;                                  // 1 while one row tile's products go out
 };
 constexpr uint32_t kSmemBytes = kOffBar + (uint32_t)sizeof(Shared) + 1024u;
 static_assert(kSmemBytes <= 232448, "shared memory");
@@ -65,6 +70,13 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   atomicOr(&g_status_latent, PA_DEV_TIMEOUT);
   *abort_flag = 1;
   return false;
+}
+
+// One row tile's products go out together: let in among each other, both tiles' scores would be
+// ready at the same time, and the tensor cores idle while both softmaxes run.  (Only the order is
+// at stake: a turn that does not come is taken after a while.)
+__device__ __forceinline__ void take_turn(int* turn) {
+  for (int i = 0; i < 4096 && atomicCAS(turn, 0, 1) != 0; ++i) {}
 }
 
 // Query rows of sequence b, -1 for an inconsistent one.
@@ -227,18 +239,18 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->q[i], 1);
       mbar_init(&sh->q_empty[i], 1);
-      mbar_init(&sh->full_k[i], 1);
-      mbar_init(&sh->empty_k[i], 1);
-      mbar_init(&sh->full_v[i], 1);
-      mbar_init(&sh->empty_v[i], 1);
       mbar_init(&sh->s[i], 1);
       mbar_init(&sh->p[i][0], 4);
       mbar_init(&sh->p[i][1], 4);
       mbar_init(&sh->pv[i], 1);
       mbar_init(&sh->o_free[i], 4);
+      mbar_init(&sh->full_k[i], 1);
+      mbar_init(&sh->full_v[i], 1);
+      mbar_init(&sh->drain[i], 1);
     }
-    mbar_init(&sh->drain, 1);
+    for (int i = 0; i < kSlots; ++i) mbar_init(&sh->empty[i], 2);    // both row tiles
     sh->abort = 0;
+    sh->turn = 0;
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -250,6 +262,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
   const int ncd = (p.Dk + 63) / 64, ncv = (p.Dv + 63) / 64;    // chunks of the keys' own part, of the values
+  const int per = ncd + 3;                   // slots of a key tile: ncd + 1 of K, 2 of V
   Walk walk{0, 0, 0};
   Item it = {};
 
@@ -258,7 +271,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
     // ------------------------------------------------------------ TMA producer
     if (warp == 8) {
       const uint64_t once = policy_evict_first(), keep = policy_evict_last();   // (K, V: other row tiles read them too)
-      int nk = 0, nv = 0, nq[2] = {0, 0};    // key tiles, value halves, row tiles requested
+      int u = 0, k = 0, nq[2] = {0, 0};      // slots, key tiles, row tiles requested
       bool ok = true;
       auto load_q = [&](int x) {
         if (it.nt[x] == 0) return;
@@ -270,134 +283,142 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
         tma_load_4d(smem + (x * 3 + ncd) * kChunk, &mapQr, &sh->q[x], 0, it.h, row, 0, once);
         ++nq[x];
       };
-      auto load_k = [&](int j) {
-        const int st = nk & 1;
-        ok = ok && wait(&sh->empty_k[st], ((uint32_t)(nk >> 1) & 1u) ^ 1u, abort_flag);
-        if (!ok) return;
-        mbar_arrive_expect_tx(&sh->full_k[st], (uint32_t)(ncd + 1) * kChunk);
-        unsigned char* dst = smem + kOffK + st * 3 * kChunk;
-        for (int c = 0; c < ncd; ++c)
-          tma_load_4d(dst + c * kChunk, &mapK, &sh->full_k[st], c * 64, it.h, it.k0 + j * kKT, 0, keep);
-        tma_load_4d(dst + ncd * kChunk, &mapKr, &sh->full_k[st], 0, it.k0 + j * kKT, 0, 0, keep);
-        ++nk;
+      // the next slot, once it is free
+      auto slot = [&]() -> unsigned char* {
+        const int sl = u & (kSlots - 1);
+        ok = ok && wait(&sh->empty[sl], ((uint32_t)(u / kSlots) & 1u) ^ 1u, abort_flag);
+        ++u;
+        return smem + kOffRing + sl * kChunk;
       };
       while (ok && walk.next(p, lane, it)) {
         const int most = max(it.nt[0], it.nt[1]);
         if (lane == 0 && most > 0) {
           load_q(0);
-          load_k(0);
-          load_q(1);
-          for (int j = 0; ok && j < most; ++j) {
-            if (j + 1 < most) load_k(j + 1);
-            for (int v = 0; v < 2; ++v) {
-              ok = ok && wait(&sh->empty_v[v], ((uint32_t)(nv >> 1) & 1u) ^ 1u, abort_flag);
+          for (int j = 0; ok && j < most; ++j, ++k) {
+            const int row = it.k0 + j * kKT;
+            uint64_t* full = &sh->full_k[k & 1];
+            mbar_arrive_expect_tx(full, (uint32_t)(ncd + 1) * kChunk);
+            for (int c = 0; c <= ncd; ++c) {
+              unsigned char* dst = slot();
               if (!ok) break;
-              mbar_arrive_expect_tx(&sh->full_v[v], (uint32_t)ncv * kChunk / 2);
-              for (int c = 0; c < ncv; ++c)
-                tma_load_4d(smem + kOffV + v * kChunk + c * (kChunk / 2), &mapV, &sh->full_v[v], c * 64, it.h,
-                            it.k0 + j * kKT + v * 64, 0, keep);
-              ++nv;
+              if (c < ncd) tma_load_4d(dst, &mapK, full, c * 64, it.h, row, 0, keep);
+              else tma_load_4d(dst, &mapKr, full, 0, row, 0, 0, keep);
+            }
+            if (!ok) break;
+            if (j == 0) load_q(1);
+            full = &sh->full_v[k & 1];
+            mbar_arrive_expect_tx(full, (uint32_t)ncv * kChunk);
+            for (int v = 0; v < 2; ++v) {
+              unsigned char* dst = slot();
+              for (int c = 0; ok && c < ncv; ++c)
+                tma_load_4d(dst + c * (kChunk / 2), &mapV, full, c * 64, it.h, row + v * 64, 0, keep);
             }
           }
         }
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
       // no TMA write may land after the CTA has left
-      if (lane == 0) {
+      if (lane == 0 && ok) {
         for (int x = 0; x < 2; ++x)
           if (nq[x] > 0) mbar_wait(&sh->q[x], (uint32_t)(nq[x] - 1) & 1u);
-        for (int j = max(0, nk - 2); j < nk; ++j) mbar_wait(&sh->full_k[j & 1], (uint32_t)(j >> 1) & 1u);
-        for (int i = max(0, nv - 2); i < nv; ++i) mbar_wait(&sh->full_v[i & 1], (uint32_t)(i >> 1) & 1u);
+        for (int i = max(0, k - 2); i < k; ++i) {
+          mbar_wait(&sh->full_k[i & 1], (uint32_t)(i >> 1) & 1u);
+          mbar_wait(&sh->full_v[i & 1], (uint32_t)(i >> 1) & 1u);
+        }
       }
+      // (given up: a millisecond for what is still on its way)
+      if (lane == 0 && !ok)
+        for (const unsigned long long t = globaltimer_ns(); globaltimer_ns() - t < 1000000ull;) {}
       __syncwarp();
     }
-    // ------------------------------------------------------------ MMA issuer
-    // The whole warp walks, with values that are the same in all lanes, and one lane issues: the
-    // descriptors then stay in uniform registers.
-    if (warp == 9) {
+    // ------------------------------------------------------------ MMA issuers
+    // A warp for each row tile x: P_x V of a key tile, then S_x of the next.  (One warp for both
+    // was busy for longer than the products: a wait costs it about 190 clocks, an MMA 50.)  A whole
+    // warp walks, with values that are the same in all lanes, and one lane issues: the descriptors
+    // then stay in uniform registers.
+    if (warp == 9 || warp == 10) {
+      const int x = __shfl_sync(0xffffffffu, warp - 9, 0);
       const bool lead = elect_one();
       const uint32_t sb = __shfl_sync(0xffffffffu, sbase, 0), t0 = __shfl_sync(0xffffffffu, tmem, 0);
       const uint32_t idS = idesc_bf16_f32(kRows, kKT, false, false);
       const uint32_t idO = idesc_bf16_f32(kRows, p.Dv, false, true);
-      const uint64_t dq = sdesc_sw128(sb, 16, 1024), dk = sdesc_sw128(sb + kOffK, 16, 1024);
-      const uint64_t dv = sdesc_sw128(sb + kOffV, kChunk / 2, 1024);
+      const uint64_t da = sdesc_sw128(sb + x * 3 * kChunk, 16, 1024), dk = sdesc_sw128(sb + kOffRing, 16, 1024);
+      const uint64_t dv = sdesc_sw128(sb + kOffRing, kChunk / 2, 1024);
+      const uint32_t tS = t0 + x * 128, tO = t0 + kColO + x * 128;
       const int own_steps = p.Dk / 16, rope_steps = p.P / 16;
       bool ok = true;
-      int kc = 0, nq[2] = {0, 0}, np[2] = {0, 0};              // key tiles, row tiles, P tiles before this item
-      // S_x against key tile j of the item
-      auto scores = [&](int x, int j, bool last) {
-        if (j == 0) ok = ok && wait(&sh->q[x], (uint32_t)nq[x] & 1u, abort_flag);
-        const int k = kc + j;
-        ok = ok && wait(&sh->full_k[k & 1], (uint32_t)(k >> 1) & 1u, abort_flag);
+      int k = 0, u = 0, nq = 0, np = 0;      // key tiles, their slots; row tiles, P tiles of x
+      // S_x against key tile k, whose slots begin at v
+      auto scores = [&](int k, int v, bool last) {
         if (!ok) return;
-        tc_fence_after();
         if (lead) {
-          const uint64_t da = sdesc_at(dq, x * 3 * kChunk), db = sdesc_at(dk, (k & 1) * 3 * kChunk);
-          const uint32_t d = t0 + x * 128;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            if (kk >= own_steps) break;
-            umma_bf16(d, sdesc_at(da, (kk >> 2) * kChunk + (kk & 3) * 32), sdesc_at(db, (kk >> 2) * kChunk + (kk & 3) * 32), idS,
-                      kk > 0 ? 1u : 0u);
-          }
-          const uint64_t ra = sdesc_at(da, ncd * kChunk), rb = sdesc_at(db, ncd * kChunk);
+          for (int c = 0; c < 3; ++c) {
+            if (c > ncd) break;
+            const int sl = (v + c) & (kSlots - 1);
+            const int steps = c == ncd ? rope_steps : min(4, own_steps - c * 4);
+            const uint64_t a = sdesc_at(da, c * kChunk), b = sdesc_at(dk, sl * kChunk);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            if (kk >= rope_steps) break;
-            umma_bf16(d, sdesc_at(ra, kk * 32), sdesc_at(rb, kk * 32), idS, 1u);
+            for (int kk = 0; kk < 4; ++kk)
+              if (kk < steps) umma_bf16(tS, sdesc_at(a, kk * 32), sdesc_at(b, kk * 32), idS, c > 0 || kk > 0 ? 1u : 0u);
+            umma_commit(&sh->empty[sl]);
           }
           umma_commit(&sh->s[x]);
           if (last) umma_commit(&sh->q_empty[x]);
         }
         __syncwarp();
       };
-      // O_x += P_x V of key tile j, half a tile of keys at a time
-      auto values = [&](int x, int j, bool frees) {
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          ok = ok && wait(&sh->p[x][v], (uint32_t)(np[x] + j) & 1u, abort_flag);
-          ok = ok && wait(&sh->full_v[v], (uint32_t)(kc + j) & 1u, abort_flag);
-          if (!ok) return;
-          tc_fence_after();
-          if (lead) {
-            const uint64_t db = sdesc_at(dv, v * kChunk);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_bf16_ts(t0 + kColO + x * 128, t0 + x * 128 + v * 32 + kk * 8, sdesc_at(db, kk * 2048), idO,
-                           j > 0 || v > 0 || kk > 0 ? 1u : 0u);
-            if (frees) umma_commit(&sh->empty_v[v]);
-            if (v == 1) umma_commit(&sh->pv[x]);
-          }
-          __syncwarp();
-        }
-      };
       bool more = walk.next(p, lane, it);
       while (ok && more) {
-        const int n0 = __shfl_sync(0xffffffffu, it.nt[0], 0), n1 = __shfl_sync(0xffffffffu, it.nt[1], 0);
-        const int most = max(n0, n1);
-        if (n0 > 0) scores(0, 0, n0 == 1);
-        if (n1 > 0) scores(1, 0, n1 == 1);
-        if (ok && lead && most > 0) umma_commit(&sh->empty_k[kc & 1]);
-        more = walk.next(p, lane, it);       // (while the softmax has work)
-        // the last outputs of both row tiles have been read
-        for (int x = 0; x < 2; ++x) ok = ok && wait(&sh->o_free[x], ((uint32_t)nq[x] & 1u) ^ 1u, abort_flag);
-        for (int j = 0; ok && j < most; ++j) {
-          if (j < n0) values(0, j, j >= n1);
-          if (j + 1 < n0) scores(0, j + 1, j + 2 == n0);
-          if (j < n1) values(1, j, true);
-          if (j + 1 < n1) scores(1, j + 1, j + 2 == n1);
-          // (the row tile that sees a key tile last frees it)
-          if (ok && lead && j + 1 < most) umma_commit(&sh->empty_k[(kc + j + 1) & 1]);
-          __syncwarp();
+        const int n = __shfl_sync(0xffffffffu, it.nt[x], 0);
+        const int most = __shfl_sync(0xffffffffu, max(it.nt[0], it.nt[1]), 0);
+        if (n > 0) {
+          ok = ok && wait(&sh->q[x], (uint32_t)nq & 1u, abort_flag) &&
+               wait(&sh->full_k[k & 1], (uint32_t)(k >> 1) & 1u, abort_flag);
+          tc_fence_after();
+          scores(k, u, n == 1);
         }
-        kc += most;
-        nq[0] += n0 > 0;
-        nq[1] += n1 > 0;
-        np[0] += n0;
-        np[1] += n1;
+        more = walk.next(p, lane, it);       // (while the softmax has work)
+        // the last output of the row tile has been read
+        ok = ok && wait(&sh->o_free[x], ((uint32_t)nq & 1u) ^ 1u, abort_flag);
+        for (int j = 0; ok && j < most; ++j, ++k, u += per) {
+          if (j >= n) {
+            // a key tile that only the other row tile sees
+            ok = wait(&sh->full_k[k & 1], (uint32_t)(k >> 1) & 1u, abort_flag) &&
+                 wait(&sh->full_v[k & 1], (uint32_t)(k >> 1) & 1u, abort_flag);
+            if (lead && ok)
+              for (int c = 0; c < per; ++c) mbar_arrive(&sh->empty[(u + c) & (kSlots - 1)]);
+            __syncwarp();
+            continue;
+          }
+          // O_x += P_x V, half a tile of keys at a time
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const int sl = (u + ncd + 1 + v) & (kSlots - 1);
+            ok = ok && wait(&sh->p[x][v], (uint32_t)(np + j) & 1u, abort_flag);
+            if (v == 0) ok = ok && wait(&sh->full_v[k & 1], (uint32_t)(k >> 1) & 1u, abort_flag);
+            if (v == 1 && j + 1 < n) ok = ok && wait(&sh->full_k[(k + 1) & 1], (uint32_t)((k + 1) >> 1) & 1u, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            if (v == 1 && lead) take_turn(&sh->turn);
+            if (lead) {
+              const uint64_t db = sdesc_at(dv, sl * kChunk);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_bf16_ts(tO, tS + v * 32 + kk * 8, sdesc_at(db, kk * 2048), idO, j > 0 || v > 0 || kk > 0 ? 1u : 0u);
+              umma_commit(&sh->empty[sl]);
+              if (v == 1) umma_commit(&sh->pv[x]);
+            }
+            __syncwarp();
+          }
+          if (j + 1 < n) scores(k + 1, u + per, j + 2 == n);
+          if (lead) *static_cast<volatile int*>(&sh->turn) = 0;
+        }
+        nq += n > 0;
+        np += n;
       }
-      if (lead) umma_commit(&sh->drain);     // every MMA has completed before TMEM is freed
-      mbar_wait(&sh->drain, 0);
+      if (lead) umma_commit(&sh->drain[x]);  // every MMA has completed before TMEM is freed
+      mbar_wait(&sh->drain[x], 0);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -471,12 +492,13 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
             pw[c] = pack_bf16(p0, p1);
           }
           tmem_st16(tS + i * 16, pw);
-          if (i == 1 && (x == 0 || j >= it.nt[0]) && (j + 1) * kKT > it.L) {
-            // Rows behind the context may hold anything, and 0 * NaN would reach O: zeros, from the
-            // row tile whose P V comes first, before any of its P is handed over.
-            wait(&sh->full_v[r >> 6], (uint32_t)(kc + j) & 1u, abort_flag);
+          if (i == 1 && (j + 1) * kKT > it.L) {
+            // Rows behind the context may hold anything, and 0 * NaN would reach O: zeros, before
+            // any of P is handed over (from both row tiles: either's P V may come first).
+            const int u = (kc + j) * per + ncd + 1 + (r >> 6);
+            wait(&sh->full_v[(kc + j) & 1], (uint32_t)((kc + j) >> 1) & 1u, abort_flag);
             if (j * kKT + r >= it.L) {
-              unsigned char* vrow = smem + kOffV + (r >> 6) * kChunk + (r & 63) * 128;
+              unsigned char* vrow = smem + kOffRing + (u & (kSlots - 1)) * kChunk + (r & 63) * 128;
               for (int c = 0; c < ncv * 8; ++c)  // (each row in another order: the banks are all in use)
                 *reinterpret_cast<uint4*>(vrow + (c >> 3) * (kChunk / 2) + (((c + r) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
               fence_proxy_async_smem();
