@@ -19,25 +19,22 @@ namespace {
 __device__ unsigned g_status_latent;
 
 constexpr int kTile = 128;                   // tokens per tile
-constexpr int kThreads = 416;                // warps 0-7 softmax, 8-11 TMA, 12 MMA
+constexpr int kThreads = 384;                // warps 0-7 softmax, 8-10 TMA, 11 MMA
 constexpr uint32_t kChunk = 16384;           // 128 tokens x 64 elements
 constexpr uint32_t kPair = 2 * kChunk;       // 128 elements: one M = 128 product of O^T
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;                // log2 units a score may exceed its reference by
 constexpr uint32_t kSmemMax = 232448;        // 227 KB
 constexpr int kMaxSlots = 6;
-constexpr bool kPrefetch = false;
 
 struct LatentParams {
   __nv_bfloat16* out;
-  const __nv_bfloat16* cache;
   const int32_t* query_start;                // null: one row a sequence
   const int32_t* block_tables;
   const int32_t* context_lens;
   float* ws_o;                               // [2 * CTAs, NR, R] partial sums
   float* ws_ml;                              // [2 * CTAs, NR, 2] their maximum and sum
-  long long* ws_base;                        // [B + 1] units before each sequence
-  int32_t* ws_group;                         // [B + 1] row groups before each sequence
+  int4* ws_join;                             // [2 * CTAs] what the slot begins: first row, rows, slots that go on with it
   int B, H, R, P, rows, max_blocks, bs, num_blocks;
   int cl;                                    // CTAs that take neighbouring row groups over the same tokens
   float qscale;
@@ -51,7 +48,6 @@ struct Shared {
   alignas(16) float f[NR];
   alignas(16) float red[4][NR];              // per warp: maxima, at the end sums
   long long scan[kThreads / 32];
-  int gscan[kThreads / 32];
   long long first_off;
   int first_b;
   uint32_t tmem_base;
@@ -135,7 +131,8 @@ __device__ __forceinline__ int groups_of(const LatentParams& p, const Seq& s, in
 // what a cut leaves in two CTAs is joined by the second kernel.
 struct Item {
   int b, r0, rows;                           // row group: first row of the sequence's, rows of it
-  int tile, nt;                              // first tile, tiles with something to see
+  int tile, nt, tiles;                       // first tile, tiles with something to see, tiles of the whole group
+  long long unit;                            // the first tile's place in the line
   int end, L, n, q0;                         // tokens that any of its rows sees
   bool whole;
   int slot;
@@ -143,7 +140,7 @@ struct Item {
 template <int NR>
 struct Walk {
   int b, half, part;
-  long long off, left;
+  long long off, left, at, total;
   bool first;
   __device__ __forceinline__ bool next(const LatentParams& p, Item& it) {
     while (left > 0) {
@@ -157,8 +154,10 @@ struct Walk {
       const int sg = (int)(off / s.tiles);
       const int t = (int)(off - (long long)sg * s.tiles);
       const int cnt = (int)min((long long)(s.tiles - t), left);
+      it.unit = at;
       off += cnt;
       left -= cnt;
+      at += cnt;
       const bool was_first = first;
       first = false;
       it.b = b;
@@ -167,6 +166,7 @@ struct Walk {
       if (it.rows <= 0) continue;
       it.end = min(s.L, max(0, s.L - s.n + (it.r0 + it.rows - 1) / p.H + 1));
       it.tile = t;
+      it.tiles = s.tiles;
       it.nt = max(0, min(t + cnt, (it.end + kTile - 1) / kTile) - t);
       it.L = s.L;
       it.n = s.n;
@@ -242,7 +242,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
     prefetch_tensormap(&mapC);
     prefetch_tensormap(&mapQ);
   }
-  if (warp == 12) {
+  if (warp == 11) {
     tmem_alloc(&sh->tmem_base, Lay::kTmem);
     tmem_relinquish();
   }
@@ -255,39 +255,24 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
     const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
     const bool note = blockIdx.x == 0;
     long long sum = 0;
-    int groups = 0;
     for (int b = b0; b < b1; ++b) {
       const Seq s = seq_of(p, b, note);
-      const int g = groups_of(p, s, NR);
-      sum += (long long)((g + p.cl - 1) / p.cl) * s.tiles;
-      groups += g;
+      sum += (long long)((groups_of(p, s, NR) + p.cl - 1) / p.cl) * s.tiles;
     }
     long long incl = sum;
-    int gincl = groups;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, incl, off);
-      const int z = __shfl_up_sync(0xffffffffu, gincl, off);
-      if (lane >= off) {
-        incl += y;
-        gincl += z;
-      }
+      if (lane >= off) incl += y;
     }
-    if (lane == 31) {
-      sh->scan[warp] = incl;
-      sh->gscan[warp] = gincl;
-    }
+    if (lane == 31) sh->scan[warp] = incl;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     long long total = 0, before = incl - sum;
-    int gbefore = gincl - groups;
     for (int w = 0; w < kThreads / 32; ++w) {
       total += sh->scan[w];
-      if (w < warp) {
-        before += sh->scan[w];
-        gbefore += sh->gscan[w];
-      }
+      if (w < warp) before += sh->scan[w];
     }
     // (no empty parts: a line shorter than the grid leaves its last CTAs without work)
     const long long cuts = min((long long)parts, total);
@@ -305,42 +290,35 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
         at += u;
       }
     }
-    if (note && p.ws_base) {
-      for (int b = b0; b < b1; ++b) {
-        const Seq s = seq_of(p, b, false);
-        const int g = groups_of(p, s, NR);
-        p.ws_base[b] = before;
-        p.ws_group[b] = gbefore;
-        before += (long long)((g + p.cl - 1) / p.cl) * s.tiles;
-        gbefore += g;
-      }
-      if (b0 < b1 && b1 == p.B) {
-        p.ws_base[p.B] = before;
-        p.ws_group[p.B] = gbefore;
-      }
-    }
     __syncthreads();
     walk.b = sh->first_b;
     walk.off = sh->first_off;
     walk.left = walk.b < p.B ? u1 - u0 : 0;
     walk.half = blockIdx.x % p.cl;
     walk.part = part;
+    walk.at = u0;
+    walk.total = total;
     walk.first = true;
+    // what neither of the CTA's slots begins stays at 0
+    if (threadIdx.x < 2) p.ws_join[blockIdx.x * 2 + threadIdx.x] = make_int4(0, 0, 0, 0);
   }
   const uint32_t tmem = sh->tmem_base;
   const uint32_t tO = tmem + 2 * NR;
+  const long long cuts = min((long long)parts, walk.total);
   Item it;
 
-  if (warp >= 8 && warp < 12) {
+  if (warp >= 8 && warp < 11) {
     // ------------------------------------------------------------ TMA producers
     // A warp gets a copy out in about 60 clocks, whatever its size, and a tile is 72 of 2 KB:
-    // four warps share them (chunk w >> 1 of a pair, half w & 1 of the tile's blocks).
+    // three warps share them, every third copy of a pair each.
     const uint64_t pol = policy_evict_first();
     const int w = warp - 8;
     const int bsh = 31 - __clz(p.bs);
     const uint32_t box = (uint32_t)p.bs * 128u;
-    const int lanes = kTile >> (bsh + 1);
-    const int mine = (w & 1) * lanes + lane;     // the lane's block of a tile
+    const int blocks = kTile >> bsh;
+    const int copy = lane * 3 + w;           // the lane's copy of a pair: a chunk of a block
+    const int chunk = copy >= blocks ? 1 : 0, mine = copy - chunk * blocks;
+    const bool used = copy < 2 * blocks;
     int kp = 0, kr = 0, kq = 0;              // pairs, rotated chunks and query groups requested
     bool ok = true;
     while (ok && walk.next(p, it)) {
@@ -348,19 +326,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
       const int32_t* row = p.block_tables + (size_t)it.b * p.max_blocks;
       auto id_of = [&](int j) -> int {
         const int t = (it.tile + j) * kTile + (mine << bsh);
-        return j < it.nt && lane < lanes && t < it.end ? __ldg(&row[t >> bsh]) : 0;
+        return j < it.nt && used && t < it.end ? __ldg(&row[t >> bsh]) : 0;
       };
-      // The ring holds little more than a tile, which does not cover HBM's latency: blocks are asked
-      // into L2 two tiles ahead (a block is one span of memory), by one CTA of the two that read them.
-      const uint32_t span = (uint32_t)p.bs * (uint32_t)(p.R + p.P) * 2u;
-      auto ahead = [&](int j, int id) {
-        const int t = (it.tile + j) * kTile + (mine << bsh);
-        if (kPrefetch && w < 2 && j < it.nt && lane < lanes && t < it.end && (unsigned)id < (unsigned)p.num_blocks &&
-            (p.cl == 1 || (j & 1) == walk.half))
-          bulk_prefetch(p.cache + (size_t)id * p.bs * (p.R + p.P), span);
-      };
-      int blk = id_of(0), next = id_of(1), after = id_of(2);
-      ahead(1, next);
+      int blk = id_of(0);
       ok = __all_sync(0xffffffffu, wait(&sh->q_empty, (uint32_t)(kq & 1) ^ 1u, abort_flag));
       if (!ok) break;
       if (w == 0) {
@@ -371,10 +339,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
       }
       ++kq;
       for (int j = 0; j < it.nt; ++j) {
-        const int later = id_of(j + 3);
-        ahead(j + 2, after);
+        const int next = id_of(j + 1);
         const int nb = (min(kTile, it.end - (it.tile + j) * kTile) + p.bs - 1) >> bsh;
-        const bool has = lane < lanes && mine < nb;
+        const bool has = used && mine < nb;
         if (has && (unsigned)blk >= (unsigned)p.num_blocks) {
           atomicOr(&g_status_latent, PA_DEV_BAD_BLOCK);
           blk = 0;                           // keep every copy inside the pool
@@ -387,8 +354,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
           if (w == 0 && lane == 0) mbar_arrive_expect_tx(&sh->full[sl], 2u * nb * box);
           __syncwarp();
           if (has)
-            tma_load_4d(smem + Lay::kOffRing + sl * kPair + (w >> 1) * kChunk + mine * box, &mapC, &sh->full[sl],
-                        i * 128 + (w >> 1) * 64, 0, blk, 0, pol);
+            tma_load_4d(smem + Lay::kOffRing + sl * kPair + chunk * kChunk + mine * box, &mapC, &sh->full[sl],
+                        i * 128 + chunk * 64, 0, blk, 0, pol);
         }
         if (!ok) break;
         const int sr = kAlias ? 0 : kr & 1;
@@ -397,12 +364,10 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
         if (!ok) break;
         if (w == 0 && lane == 0) mbar_arrive_expect_tx(&sh->full_r[sr], (uint32_t)nb * box);
         __syncwarp();
-        if (w < 2 && has)
+        if (chunk == 0 && has)
           tma_load_4d(smem + Lay::kOffRope + sr * kChunk + mine * box, &mapC, &sh->full_r[sr], RC * 64, 0, blk, 0, pol);
         ++kr;
         blk = next;
-        next = after;
-        after = later;
       }
     }
     // no TMA write may land after the CTA has left
@@ -412,7 +377,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
         mbar_wait(&sh->full_r[kAlias ? 0 : k & 1], (uint32_t)(kAlias ? k : k >> 1) & 1u);
       if (kq > 0) mbar_wait(&sh->q_full, (uint32_t)(kq - 1) & 1u);
     }
-  } else if (warp == 12) {
+  } else if (warp == 11) {
     // ------------------------------------------------------------ MMA issuer
     // The whole warp walks, with values that are the same in all lanes, and one lane issues: the
     // descriptors then stay in uniform registers (moved there for every MMA, 57 clocks an MMA and not 47).
@@ -635,7 +600,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
             unsigned char* at = smem + Lay::kOffRing + ((kt * NP + i) % SLOTS) * kPair + half * kChunk + r * 128;
 #pragma unroll 1
             for (int k = 0; k < 8; ++k) {
-              uint4* q = reinterpret_cast<uint4*>(at + k * 16);
+              uint4* q = reinterpret_cast<uint4*>(at + (((k + r) & 7) << 4));   // (another piece in each row of eight)
               if (drop) {
                 *q = make_uint4(0u, 0u, 0u, 0u);
               } else {
@@ -671,6 +636,13 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
         if ((lane & spare) == 0) sh->red[warp & 3][c0 + col] = l[0];
       }
       named_sync(1, 256);
+      if (!it.whole && it.tile == 0 && threadIdx.x == 0) {
+        // the CTAs after this one, as far as the group goes: the part that holds its last unit is
+        // the last that begins at or before it
+        const long long last = it.unit + it.tiles - 1;
+        const int part_of = (int)(((last + 1) * cuts + walk.total - 1) / walk.total) - 1;
+        p.ws_join[it.slot] = make_int4(it.q0 * p.H + it.r0, it.rows, part_of - part, 0);
+      }
       if (threadIdx.x < NR) {
         const int c = (int)threadIdx.x;
         const float sum = (sh->red[0][c] + sh->red[1][c]) + (sh->red[2][c] + sh->red[3][c]);
@@ -721,63 +693,51 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, Lay::kTmem);
+  if (warp == 11) tmem_dealloc(tmem, Lay::kTmem);
 }
 
-// Joins the row groups that a cut left in several CTAs.  grid (row groups, NR / 8): a warp per row.
+// Joins the row groups that a cut left in several CTAs.  grid (slots, NR / 8): a warp per row of the
+// group that the slot begins, if it begins one.
 template <int NR, int RC>
-__global__ void __launch_bounds__(256) latent_join_kernel(const LatentParams p, int all_parts) {
+__global__ void __launch_bounds__(256) latent_join_kernel(const LatentParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int R = RC * 64, kPer = R / 128;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int u = blockIdx.x;
-  if (u >= p.ws_group[p.B]) return;
-  int lo = 0, hi = p.B - 1;                  // the sequence holding group u
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.ws_group[mid] <= u) lo = mid;
-    else hi = mid - 1;
-  }
-  const Seq s = seq_of(p, lo, false);
-  const int g = u - p.ws_group[lo];
-  const int c = blockIdx.y * 8 + warp, row = g * NR + c;
-  if (row >= s.n * p.H) return;
-  const long long total = p.ws_base[p.B];
-  const long long u0 = p.ws_base[lo] + (long long)(g / p.cl) * s.tiles;
-  const long long parts = min((long long)all_parts, total);
-  // the part that holds unit x: the last that begins at or before it
-  auto part_of = [&](long long x) -> int { return (int)(((x + 1) * parts + total - 1) / total) - 1; };
-  const int p0 = part_of(u0), p1 = part_of(u0 + s.tiles - 1);
-  if (p0 == p1) return;                      // one CTA had it whole
+  const int4 j = p.ws_join[blockIdx.x];
+  const int c = blockIdx.y * 8 + warp;
+  if (c >= j.y) return;
+  const int more = j.z;                      // the group goes on in the first slots of so many CTAs of its kind
+  const int cta = blockIdx.x >> 1;
   auto slot_of = [&](int q) -> size_t {
-    const bool first = q > p0 || total * q / parts == u0;
-    return (size_t)((q * p.cl + g % p.cl) * 2 + (first ? 0 : 1)) * NR + c;
+    return (size_t)(q == 0 ? (int)blockIdx.x : (cta + q * p.cl) * 2) * NR + c;
   };
   float m = -INFINITY;
-  for (int q = p0 + lane; q <= p1; q += 32) m = fmaxf(m, p.ws_ml[slot_of(q) * 2]);
+  for (int q = lane; q <= more; q += 32) m = fmaxf(m, p.ws_ml[slot_of(q) * 2]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   float l = 0.f;
   float4 o[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int q = p0; q <= p1; ++q) {
+  for (int q = 0; q <= more; ++q) {
     const size_t at = slot_of(q);
     const float mq = p.ws_ml[at * 2], lq = p.ws_ml[at * 2 + 1];
     if (mq == -INFINITY) continue;
+    float4 x[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i] = *reinterpret_cast<const float4*>(p.ws_o + at * R + i * 128 + lane * 4);
     const float w = exp2f(mq - m);
     l = fmaf(lq, w, l);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const float4 x = *reinterpret_cast<const float4*>(p.ws_o + at * R + i * 128 + lane * 4);
-      o[i].x = fmaf(x.x, w, o[i].x);
-      o[i].y = fmaf(x.y, w, o[i].y);
-      o[i].z = fmaf(x.z, w, o[i].z);
-      o[i].w = fmaf(x.w, w, o[i].w);
+      o[i].x = fmaf(x[i].x, w, o[i].x);
+      o[i].y = fmaf(x[i].y, w, o[i].y);
+      o[i].z = fmaf(x[i].z, w, o[i].z);
+      o[i].w = fmaf(x[i].w, w, o[i].w);
     }
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;
-  __nv_bfloat16* out = p.out + ((size_t)s.q0 * p.H + row) * R;
+  __nv_bfloat16* out = p.out + ((size_t)j.x + c) * R;
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
     *reinterpret_cast<uint2*>(out + i * 128 + lane * 4) =
@@ -793,8 +753,7 @@ bool good_sizes(int total, int num_seqs, int num_heads, int latent_dim, int max_
 // and two CTAs side by side over the same tokens where that is less than a sequence's rows.
 struct Plan {
   int nr, cl, parts;
-  long long groups;                          // row groups at most
-  size_t o, ml, base, group, bytes;          // workspace offsets
+  size_t ml, join, bytes;                    // workspace offsets
 };
 Plan plan_of(int total, int num_seqs, int num_heads, int latent_dim) {
   Plan w = {};
@@ -802,13 +761,11 @@ Plan plan_of(int total, int num_seqs, int num_heads, int latent_dim) {
   w.nr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   w.cl = rows > w.nr ? 2 : 1;
   w.parts = kTunedSms / w.cl;
-  w.groups = (long long)total * num_heads / w.nr + num_seqs;
-  const size_t slots = 2 * (size_t)w.parts * w.cl * w.nr;
+  const size_t slots = 2 * (size_t)w.parts * w.cl;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  w.ml = up(slots * latent_dim * 4);
-  w.base = w.ml + up(slots * 8);
-  w.group = w.base + up(((size_t)num_seqs + 1) * 8);
-  w.bytes = w.group + up(((size_t)num_seqs + 1) * 4);
+  w.ml = up(slots * w.nr * latent_dim * 4);
+  w.join = w.ml + up(slots * w.nr * 8);
+  w.bytes = w.join + up(slots * 16);
   return w;
 }
 
@@ -878,14 +835,12 @@ extern "C" int pa_latent_decode(void* out, const void* query, const int32_t* que
   char* ws = static_cast<char*>(workspace);
   LatentParams p = {};
   p.out = static_cast<__nv_bfloat16*>(out);
-  p.cache = static_cast<const __nv_bfloat16*>(cache);
   p.query_start = query_start;
   p.block_tables = block_tables;
   p.context_lens = context_lens;
   p.ws_o = reinterpret_cast<float*>(ws);
   p.ws_ml = reinterpret_cast<float*>(ws + w.ml);
-  p.ws_base = reinterpret_cast<long long*>(ws + w.base);
-  p.ws_group = reinterpret_cast<int32_t*>(ws + w.group);
+  p.ws_join = reinterpret_cast<int4*>(ws + w.join);
   p.B = num_seqs;
   p.H = num_heads;
   p.R = latent_dim;
@@ -896,13 +851,13 @@ extern "C" int pa_latent_decode(void* out, const void* query, const int32_t* que
   p.num_blocks = num_blocks;
   p.cl = w.cl;
   p.qscale = scale * kLog2e;
-  int parts = w.parts;
+  const unsigned ctas = (unsigned)(w.parts * w.cl);
   void* args[] = {&mapC, &mapQ, &p};
-  if (!ck(cudaLaunchKernel(k.kernel, dim3((unsigned)(parts * w.cl)), dim3(kThreads), args, k.smem, (cudaStream_t)stream),
+  if (!ck(cudaLaunchKernel(k.kernel, dim3(ctas), dim3(kThreads), args, k.smem, (cudaStream_t)stream),
           "cudaLaunchKernel(latent_decode_kernel)"))
     return PA_ERR_CUDA;
-  void* join[] = {&p, &parts};
-  return ck(launch_after(k.join, dim3((unsigned)w.groups, (unsigned)w.nr / 8), dim3(256), join, (cudaStream_t)stream),
+  void* join[] = {&p};
+  return ck(launch_after(k.join, dim3(2 * ctas, (unsigned)w.nr / 8), dim3(256), join, (cudaStream_t)stream),
             "cudaLaunchKernel(latent_join_kernel)")
              ? PA_OK
              : PA_ERR_CUDA;

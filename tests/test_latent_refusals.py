@@ -103,9 +103,9 @@ def test_latent_decode(pa, kw, code):
 
 def test_workspace_arithmetic(pa):
     need = pa.lib.pa_latent_decode_workspace_bytes
-    # two slots a CTA of 152: 16 rows of 512 sums, their maxima and sums, two prefixes of B + 1
-    assert need(4, 4, 16, 512) == 2 * 152 * 16 * (512 * 4 + 8) + 2 * 256
-    assert need(4, 4, 128, 512) == 2 * 152 * 64 * (512 * 4 + 8) + 2 * 256
+    # two slots a CTA of 152: 16 or 64 rows of 512 sums, their maxima and sums, 16 bytes a slot
+    assert need(4, 4, 16, 512) == 2 * 152 * (16 * (512 * 4 + 8) + 16)
+    assert need(4, 4, 128, 512) == 2 * 152 * (64 * (512 * 4 + 8) + 16)
     assert need(0, 4, 16, 512) == need(4, 0, 16, 512) == need(4, 4, 16, 500) == need(-1, 4, 16, 512) == 0
 
 
