@@ -581,82 +581,91 @@ def rope_steps(rotary_dim, base=10000.0, scaling="none", factor=1.0, original_le
     return (steps if device is None else steps.to(device)), amplitude.value
 
 
-def _on_device(*ts):
-    """The current device, which every tensor has to be on (whatever its strides)."""
-    d = torch.cuda.current_device() if ts[0].is_cuda else -2
-    for t in ts:
-        if t.get_device() != d:
-            raise ValueError("tensors must be on the current CUDA device")
+def _here(t):
+    """The current device, which `t` has to be on."""
+    d = t.get_device()
+    if d < 0 or d != torch._C._cuda_getDevice():
+        raise ValueError("tensors must be on the current CUDA device")
     return d
 
 
-def _rows(t, what):
-    """(pointer, token stride, head stride) of a [tokens, heads, dim] view whose innermost stride is 1."""
-    s = t.stride()
-    if len(s) != 3 or (s[2] != 1 and t.size(2) > 1):
-        raise ValueError("%s is [tokens, heads, dim], its elements next to each other" % what)
-    return t.data_ptr(), s[0] if t.size(0) > 1 else 0, s[1] if t.size(1) > 1 else 0
+def _strided(t, n, dim, dtype, dev, what):
+    """(pointer, token stride, head stride, heads) of a [n, heads, dim] view whose innermost stride is 1."""
+    shape, s = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != n or shape[2] != dim or t.dtype is not dtype or (s[2] != 1 and dim > 1):
+        raise ValueError("%s is [tokens, heads, head_dim] of one type, its elements next to each other" % what)
+    if t.get_device() != dev:
+        raise ValueError("tensors must be on the current CUDA device")
+    h = shape[1]
+    return t.data_ptr(), (s[0] if n > 1 else 0), (s[1] if h > 1 else 0), h
 
 
-def _distinct_rows(t, what):
-    """No element of the output `t` lies in two places of it."""
-    n, h, d = t.shape
-    s0, s1, _ = t.stride()
-    if n * h * d and not ((h == 1 or s1 >= d) and (n == 1 or s0 >= s1 * (h - 1) + d) or
-                          (n == 1 or s0 >= d) and (h == 1 or s1 >= s0 * (n - 1) + d)):
+def _turn(x, out, n, dim, dtype, dev, what):
+    """Checks and marshals a rotated tensor and where it goes: (out rows, x rows, heads)."""
+    src = _strided(x, n, dim, dtype, dev, what)
+    dst = src if out is None else _strided(out, n, dim, dtype, dev, what + "_out")
+    p, s0, s1, h = dst
+    if h != src[3]:
+        raise ValueError("%s and %s_out have the same heads" % (what, what))
+    # no element of the output lies in two places of it
+    if n and h and not ((h == 1 or s1 >= dim) and (n == 1 or s0 >= s1 * (h - 1) + dim) or
+                        (n == 1 or s0 >= dim) and (h == 1 or s1 >= s0 * (n - 1) + dim)):
         raise ValueError("the rows of %s overlap" % what)
+    return p, s0, s1, src[0], src[1], src[2], h
 
 
-def _turn(x, out, dtype, n, what):
-    """Checks and marshals a rotated tensor and where it goes: (out rows, x rows, heads); None leaves it out."""
-    if x is None:
-        if out is not None:
-            raise ValueError("%s_out without %s" % (what, what))
-        return 0, 0, 0, 0, 0, 0, 0
-    out = x if out is None else out
-    if x.dim() != 3 or x.size(0) != n or out.shape != x.shape or x.dtype is not dtype or out.dtype is not dtype:
-        raise ValueError("%s and its output are [tokens, heads, head_dim] of one type" % what)
-    _distinct_rows(out, what if out is x else what + "_out")
-    return (*_rows(out, what), *_rows(x, what), x.size(1))
+_NO_TURN = (None, 0, 0, None, 0, 0, 0)
 
 
-def _angles(positions, steps, layout, n):
-    _int32(positions)
-    if positions.dim() != 1 or positions.size(0) != n:
-        raise ValueError("positions is [tokens]")
+def _angles(positions, steps, n, dev):
+    """(pointer of the positions, pointer of the steps, rotary_dim)"""
+    if positions.dtype is not _I32 or positions.shape != (n,):
+        raise TypeError("positions is int32 [tokens]")
     if steps.dtype is not torch.int64 or steps.dim() != 1:
         raise TypeError("steps is the int64 table of rope_steps")
-    if layout not in ROPE_LAYOUTS:
-        raise ValueError("layout is half or interleaved")
-    return ROPE_LAYOUTS[layout], 2 * steps.size(0)
+    if positions.get_device() != dev or steps.get_device() != dev:
+        raise ValueError("tensors must be on the current CUDA device")
+    if not (positions.is_contiguous() and steps.is_contiguous()):
+        raise ValueError("tensors must be contiguous")
+    return positions.data_ptr(), steps.data_ptr(), 2 * len(steps)
 
 
-def _slots(slot_mapping, n):
-    if slot_mapping.dtype is not torch.int64 or slot_mapping.dim() != 1 or slot_mapping.size(0) != n:
-        raise ValueError("slot_mapping is int64 [tokens]")
+def _slots(slot_mapping, n, dev):
+    if slot_mapping.dtype is not torch.int64 or slot_mapping.shape != (n,):
+        raise TypeError("slot_mapping is int64 [tokens]")
+    if slot_mapping.get_device() != dev or not slot_mapping.is_contiguous():
+        raise ValueError("slot_mapping must be contiguous and on the current CUDA device")
+    return slot_mapping.data_ptr()
 
 
 def _float_kind(t):
-    if t.dtype is not _F32 and t.dtype is not torch.bfloat16:
+    k = _KIND.get(t.dtype)
+    if k is None or k == PA_FP8_E4M3:
         raise TypeError("unsupported dtype %s" % t.dtype)
-    return _KIND[t.dtype]
+    return k
+
+
+def _layout(layout):
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError("layout is half or interleaved")
+    return ROPE_LAYOUTS[layout]
 
 
 def rope(q, k, positions, steps, amplitude=1.0, layout="half", q_out=None, k_out=None, stream=None):
     """Rotate the first 2 * len(steps) elements of every head of q [T, Hq, D] and k [T, Hkv, D] (either may be None;
     strided views will do) by the tokens' positions: in place, or into q_out / k_out.  Returns what it wrote."""
     x = q if q is not None else k
-    if x is None:
-        raise ValueError("q or k")
-    if x.dim() != 3 or (k is not None and k.dim() == 3 and k.size(2) != x.size(2)):
+    if x is None or (q is None and q_out is not None) or (k is None and k_out is not None):
+        raise ValueError("q or k, and outputs for what is given")
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != 3:
         raise ValueError("q and k are [tokens, heads, head_dim]")
-    n, kind = x.size(0), _float_kind(x)
-    lay, rot = _angles(positions, steps, layout, n)
-    qa, ka = _turn(q, q_out, x.dtype, n, "q"), _turn(k, k_out, x.dtype, n, "k")
-    _ready(positions, steps)
-    dev = _on_device(*(t for t in (q, k, q_out, k_out, positions) if t is not None))
-    _check(lib.pa_rope(*qa, *ka, positions.data_ptr(), n, x.size(2), rot, lay, steps.data_ptr(), amplitude, kind,
-                       _on(stream, dev)), "pa_rope")
+    n, _, dim = shape
+    kind, dev = _float_kind(x), _here(x)
+    pos, table, rot = _angles(positions, steps, n, dev)
+    qa = _NO_TURN if q is None else _turn(q, q_out, n, dim, dtype, dev, "q")
+    ka = _NO_TURN if k is None else _turn(k, k_out, n, dim, dtype, dev, "k")
+    _check(lib.pa_rope(*qa, *ka, pos, n, dim, rot, _layout(layout), table, amplitude, kind, _on(stream, dev)), "pa_rope")
     return (q if q_out is None else q_out), (k if k_out is None else k_out)
 
 
@@ -667,20 +676,21 @@ def rope_and_cache(q, key, value, positions, slot_mapping, k_cache, v_cache, ste
     NB, bs, H, D, kind = _pools(k_cache, v_cache)
     if kind == PA_FP8_E4M3:
         raise TypeError("rotate first, then append to an e4m3 pool")
-    n = key.size(0)
-    for t in (key, value):
-        if t.dim() != 3 or t.size(0) != n or t.size(1) != H or t.size(2) != D or t.dtype is not k_cache.dtype:
-            raise ValueError("key and value are [tokens, num_kv_heads, head_dim] of the pools' type")
-    if q is not None and q.dim() == 3 and q.size(2) != D:
-        raise ValueError("q is [tokens, num_heads, head_dim]")
-    lay, rot = _angles(positions, steps, layout, n)
-    _slots(slot_mapping, n)
-    qa = _turn(q, q_out, k_cache.dtype, n, "q")
-    _ready(positions, slot_mapping, k_cache, v_cache, steps)
-    dev = _on_device(*(t for t in (key, value, q, q_out) if t is not None))
-    _check(lib.pa_rope_and_cache(*qa, *_rows(key, "key"), *_rows(value, "value"), H, positions.data_ptr(),
-                                 slot_mapping.data_ptr(), n, k_cache.data_ptr(), v_cache.data_ptr(), NB, bs, D, rot,
-                                 lay, steps.data_ptr(), amplitude, kind, _on(stream, dev)), "pa_rope_and_cache")
+    if q is None and q_out is not None:
+        raise ValueError("q_out without q")
+    n, dtype, dev = key.size(0), k_cache.dtype, _here(key)
+    if k_cache.get_device() != dev or v_cache.get_device() != dev or not (
+            k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("the pools must be contiguous and on the current CUDA device")
+    pos, table, rot = _angles(positions, steps, n, dev)
+    qa = _NO_TURN if q is None else _turn(q, q_out, n, D, dtype, dev, "q")
+    *ka, kh = _strided(key, n, D, dtype, dev, "key")
+    *va, vh = _strided(value, n, D, dtype, dev, "value")
+    if kh != H or vh != H:
+        raise ValueError("key and value are [tokens, num_kv_heads, head_dim]")
+    _check(lib.pa_rope_and_cache(*qa, *ka, *va, H, pos, _slots(slot_mapping, n, dev), n, k_cache.data_ptr(),
+                                 v_cache.data_ptr(), NB, bs, D, rot, _layout(layout), table, amplitude, kind,
+                                 _on(stream, dev)), "pa_rope_and_cache")
     return q if q_out is None else q_out
 
 
@@ -696,21 +706,23 @@ def latent_append(latent, key_rope, positions, slot_mapping, cache, steps, ampli
     [T, H, P], the rotary part of the tokens' queries, is rotated along (in place, or into query_out).  Rows may be
     strided."""
     NB, bs, width = _latent_pool(cache)
-    n, kind = latent.size(0), _float_kind(cache)
-    for t in (latent, key_rope):
-        if t.dim() != 2 or t.size(0) != n or t.dtype is not cache.dtype or (t.stride(1) != 1 and t.size(1) > 1):
-            raise ValueError("latent and key_rope are [tokens, dim] of the cache's type, elements next to each other")
-    R, P = latent.size(1), key_rope.size(1)
-    lay, rot = _angles(positions, steps, layout, n)
-    if R + P != width or rot != P or (query is not None and query.dim() == 3 and query.size(2) != P):
-        raise ValueError("cache rows are latent_dim + rope_dim, and steps and queries have rope_dim")
-    _slots(slot_mapping, n)
-    qa = _turn(query, query_out, cache.dtype, n, "query")
-    _ready(positions, slot_mapping, cache, steps)
-    dev = _on_device(*(t for t in (latent, key_rope, query, query_out) if t is not None))
-    _check(lib.pa_latent_append(latent.data_ptr(), latent.stride(0), key_rope.data_ptr(), key_rope.stride(0), *qa,
-                                positions.data_ptr(), slot_mapping.data_ptr(), n, cache.data_ptr(), NB, bs, R, P, lay,
-                                steps.data_ptr(), amplitude, kind, _on(stream, dev)), "pa_latent_append")
+    lshape, kshape, ls, ks = latent.shape, key_rope.shape, latent.stride(), key_rope.stride()
+    n, dtype, kind, dev = lshape[0], cache.dtype, _float_kind(cache), _here(cache)
+    if len(lshape) != 2 or len(kshape) != 2 or kshape[0] != n or latent.dtype is not dtype or (
+            key_rope.dtype is not dtype) or ls[1] != 1 or ks[1] != 1:
+        raise ValueError("latent and key_rope are [tokens, dim] of the cache's type, elements next to each other")
+    if latent.get_device() != dev or key_rope.get_device() != dev or not cache.is_contiguous():
+        raise ValueError("tensors must be on the current CUDA device, and the cache contiguous")
+    if query is None and query_out is not None:
+        raise ValueError("query_out without query")
+    R, P = lshape[1], kshape[1]
+    pos, table, rot = _angles(positions, steps, n, dev)
+    if R + P != width or rot != P:
+        raise ValueError("cache rows are latent_dim + rope_dim, and steps has rope_dim / 2 entries")
+    qa = _NO_TURN if query is None else _turn(query, query_out, n, P, dtype, dev, "query")
+    _check(lib.pa_latent_append(latent.data_ptr(), ls[0] if n > 1 else 0, key_rope.data_ptr(), ks[0] if n > 1 else 0,
+                                *qa, pos, _slots(slot_mapping, n, dev), n, cache.data_ptr(), NB, bs, R, P,
+                                _layout(layout), table, amplitude, kind, _on(stream, dev)), "pa_latent_append")
     return query if query_out is None else query_out
 
 
@@ -766,8 +778,9 @@ def latent_prefill(out, q, query_start, kv, key_rope, kv_start, scale, stream=No
     _starts(query_start, B)
     _starts(kv_start, B)
     kind = _float_kind(q)
-    _on_device(q, key_rope)
     dev = _ready(out, q, kv, query_start, kv_start)
+    if key_rope.get_device() != dev:
+        raise ValueError("tensors must be on the current CUDA device")
     _check(lib.pa_latent_prefill(out.data_ptr(), q.data_ptr(), query_start.data_ptr(), rows, kv.data_ptr(),
                                  key_rope.data_ptr(), key_rope.stride(0) if T > 1 else P, kv_start.data_ptr(), T, B, H, Dk, P,
                                  Dv, scale, kind, _on(stream, dev)), "pa_latent_prefill")

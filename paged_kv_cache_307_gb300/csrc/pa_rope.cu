@@ -12,7 +12,10 @@
 // Data movement bound by HBM: every element is read and written once, in 16-byte chunks.
 // A CTA takes p.tpb tokens; their cosines and sines are made once, in shared memory, for
 // all heads.  A work unit is what one pass over registers needs: in the half layout two
-// chunks, half the rotated part apart; else one chunk.  Each thread has four units' loads in flight.
+// chunks, half the rotated part apart; else one chunk.  A thread keeps its unit of a token
+// and walks the tokens: what the unit is costs it two divisions in all (found anew for every
+// token, they took 8192 tokens of 40 heads x 128 from 31 to 38 us, 64 tokens of a step from 2.9
+// to 4.2).
 #include "pa_common.cuh"
 #include "pa_mma.cuh"
 
@@ -24,7 +27,12 @@ namespace {
 __device__ unsigned g_status_rope;
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;                // units in flight per thread
+// Tokens in flight per thread, CTAs an SM, and batches of tokens a CTA takes: 2, 6 and 2 move
+// 8192 tokens of 40 heads x 128 in 31 us (5.3 TB/s); four tokens and four CTAs take 36, one token
+// and eight CTAs 38, a batch a CTA 35.
+constexpr int kBatch = 2;
+constexpr int kMinCtas = 6;
+constexpr int kRounds = 2;
 constexpr int kTableEntries = 2048;      // (cos, sin) pairs in shared memory
 
 // One tensor of rows: bytes from token to token and head to head.
@@ -47,12 +55,6 @@ struct RopeParams {
   int pairs;                             // rotated pairs of a head
 };
 
-struct Unit {
-  const char* s;                         // null: nothing to do
-  char* d;
-  int table;                             // first entry of the cosines, -1: copied as it is
-};
-
 __device__ __forceinline__ uint4 ld_v4(const void* p) {
   uint4 r;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -70,114 +72,110 @@ __device__ __forceinline__ uint4 pack(const float* f) {
 
 // HALF: pair i is elements i and pairs + i of a head; else 2i and 2i + 1.
 template <typename T, bool HALF>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, kMinCtas) rope_kernel(const RopeParams p) {
   using E = Elem<T>;
   constexpr int EPC = E::kPerChunk;
   constexpr int kPairs = HALF ? EPC : EPC / 2;             // pairs of a unit
   __shared__ __align__(16) float2 table[kTableEntries];
   const int tok0 = blockIdx.x * p.tpb;
   const int nt = min(p.tpb, p.n - tok0);
-  const unsigned total = (unsigned)nt * p.items;
-  const int turned = p.pairs / kPairs;                     // units of a head that are rotated
   const int hop = p.pairs * E::kBytes;                     // HALF: from a pair's first element to its second
 
-  auto unit_of = [&](unsigned i) -> Unit {
-    Unit u{nullptr, nullptr, -1};
-    if (i >= total) return u;
-    const unsigned t = i / (unsigned)p.items;
-    unsigned r = i - t * p.items;
-    const long long tok = tok0 + (int)t;
-    const bool is_q = r < (unsigned)p.q.all;
-    if (!is_q) r -= p.q.all;
-    const bool is_c = !is_q && r >= (unsigned)p.k.all;
-    if (is_c) r -= p.k.all;
-    const Part& a = is_q ? p.q : is_c ? p.c : p.k;
-    long long row = tok;
-    if (!is_q && p.slots) {
-      row = __ldg(reinterpret_cast<const long long*>(p.slots) + tok);
-      if (row < 0) return u;                               // padding
-      if (row >= p.num_slots) {
-        if (!is_c && r == 0) atomicOr(&g_status_rope, PA_DEV_BAD_SLOT);
-        return u;
-      }
-    }
-    const unsigned h = r / (unsigned)a.units, x = r - h * a.units;
-    int off = (int)x * 16;
-    if (!is_c && x < (unsigned)turned)
-      u.table = (int)t * p.pairs + (int)x * kPairs;
-    else if (HALF && !is_c)
-      off += turned * 16;                                  // (each rotated unit was two chunks)
-    u.s = a.src + tok * a.src_token + h * a.src_head + off;
-    u.d = a.dst + row * a.dst_token + h * a.dst_head + off;
-    return u;
-  };
+  // ---- the thread's unit: tokens with few units share the CTA, of many each takes several CTAs
+  const int side = p.items < kThreads ? kThreads / p.items : 1;     // tokens side by side
+  int sub = 0, r = (int)(blockIdx.y * kThreads + threadIdx.x);
+  if (side > 1) {
+    sub = (int)threadIdx.x / p.items;
+    r = (int)threadIdx.x - sub * p.items;
+  }
+  const bool active = sub < side && r < p.items;
+  const bool is_q = r < p.q.all, is_c = !is_q && r >= p.q.all + p.k.all;
+  const Part& a = is_q ? p.q : is_c ? p.c : p.k;
+  r -= is_q ? 0 : is_c ? p.q.all + p.k.all : p.q.all;
+  const int h = r / a.units, x = r - h * a.units;
+  const int turned = is_c ? 0 : p.pairs / kPairs;          // units of the head that are rotated
+  const bool turn = x < turned;
+  const int off = x * 16 + (HALF && !turn ? turned * 16 : 0);       // (each rotated unit was two chunks)
+  const char* src = a.src + tok0 * a.src_token + h * a.src_head + off;
+  char* dst = a.dst + h * a.dst_head + off;
+  const bool by_slot = !is_q && p.slots;
 
-  Unit u[kBatch];
+  const char* s[kBatch];
+  char* d[kBatch];
   uint4 lo[kBatch], hi[kBatch];
-  auto load = [&](unsigned i) {
+  auto load = [&](int t) {
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      u[b] = unit_of(i + b * kThreads);
-      if (u[b].s) {
-        lo[b] = ld_v4(u[b].s);
-        if (HALF && u[b].table >= 0) hi[b] = ld_v4(u[b].s + hop);
+    for (int b = 0; b < kBatch; ++b, t += side) {
+      s[b] = nullptr;
+      if (!active || t >= nt) continue;
+      long long row = tok0 + t;
+      if (by_slot) {
+        row = __ldg(reinterpret_cast<const long long*>(p.slots) + row);
+        if (row < 0) continue;                             // padding
+        if (row >= p.num_slots) {
+          if (!is_c && r == 0) atomicOr(&g_status_rope, PA_DEV_BAD_SLOT);
+          continue;
+        }
       }
+      s[b] = src + t * a.src_token;
+      d[b] = dst + row * a.dst_token;
+      lo[b] = ld_v4(s[b]);
+      if (HALF && turn) hi[b] = ld_v4(s[b] + hop);
     }
   };
-  auto finish = [&]() {
+  auto finish = [&](int t) {
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      if (!u[b].s) continue;
-      if (u[b].table < 0) {
-        st_v4(u[b].d, lo[b]);
+    for (int b = 0; b < kBatch; ++b, t += side) {
+      if (!s[b]) continue;
+      if (!turn) {
+        st_v4(d[b], lo[b]);
         continue;
       }
-      const float4* cs = reinterpret_cast<const float4*>(table + u[b].table);
-      float x[EPC], y[EPC];
-      E::unpack(lo[b], x);
+      const float4* cs = reinterpret_cast<const float4*>(table + t * p.pairs + x * kPairs);
+      float v[EPC], w[EPC];
+      E::unpack(lo[b], v);
       if constexpr (HALF) {
-        E::unpack(hi[b], y);
+        E::unpack(hi[b], w);
 #pragma unroll
         for (int e = 0; e < EPC; e += 2) {
-          const float4 a = cs[e / 2];                      // cos, sin of two pairs
-          const float x0 = x[e], x1 = x[e + 1];
-          x[e] = fmaf(x0, a.x, -y[e] * a.y);
-          y[e] = fmaf(y[e], a.x, x0 * a.y);
-          x[e + 1] = fmaf(x1, a.z, -y[e + 1] * a.w);
-          y[e + 1] = fmaf(y[e + 1], a.z, x1 * a.w);
+          const float4 f = cs[e / 2];                      // cos, sin of two pairs
+          const float v0 = v[e], v1 = v[e + 1];
+          v[e] = fmaf(v0, f.x, -w[e] * f.y);
+          w[e] = fmaf(w[e], f.x, v0 * f.y);
+          v[e + 1] = fmaf(v1, f.z, -w[e + 1] * f.w);
+          w[e + 1] = fmaf(w[e + 1], f.z, v1 * f.w);
         }
-        st_v4(u[b].d + hop, pack<T>(y));
+        st_v4(d[b] + hop, pack<T>(w));
+        st_v4(d[b], pack<T>(v));
       } else {
 #pragma unroll
         for (int e = 0; e < EPC; e += 4) {
-          const float4 a = cs[e / 4];
-          y[e] = fmaf(x[e], a.x, -x[e + 1] * a.y);
-          y[e + 1] = fmaf(x[e + 1], a.x, x[e] * a.y);
-          y[e + 2] = fmaf(x[e + 2], a.z, -x[e + 3] * a.w);
-          y[e + 3] = fmaf(x[e + 3], a.z, x[e + 2] * a.w);
+          const float4 f = cs[e / 4];
+          w[e] = fmaf(v[e], f.x, -v[e + 1] * f.y);
+          w[e + 1] = fmaf(v[e + 1], f.x, v[e] * f.y);
+          w[e + 2] = fmaf(v[e + 2], f.z, -v[e + 3] * f.w);
+          w[e + 3] = fmaf(v[e + 3], f.z, v[e + 2] * f.w);
         }
-#pragma unroll
-        for (int e = 0; e < EPC; ++e) x[e] = y[e];
+        st_v4(d[b], pack<T>(w));
       }
-      st_v4(u[b].d, pack<T>(x));
     }
   };
 
-  load(threadIdx.x);                                       // (on its way while the table is made)
+  load(sub);                                               // (on its way while the table is made)
   for (int i = threadIdx.x; i < nt * p.pairs; i += kThreads) {
     const int t = i / p.pairs;
-    const uint64_t turn = (uint64_t)(int64_t)__ldg(&p.positions[tok0 + t]) * __ldg(&p.steps[i - t * p.pairs]);
+    const uint64_t phase = (uint64_t)(int64_t)__ldg(&p.positions[tok0 + t]) * __ldg(&p.steps[i - t * p.pairs]);
     // the turn's fraction in [-1/2, 1/2), in half turns
-    float s, c;
-    sincospif(__ll2float_rn((long long)turn) * 0x1p-63f, &s, &c);
-    table[i] = make_float2(c * p.amplitude, s * p.amplitude);
+    float sn, cn;
+    sincospif(__ll2float_rn((long long)phase) * 0x1p-63f, &sn, &cn);
+    table[i] = make_float2(cn * p.amplitude, sn * p.amplitude);
   }
   __syncthreads();
-  for (unsigned i = threadIdx.x;;) {
-    finish();
-    i += kBatch * kThreads;
-    if (i >= total) break;
-    load(i);
+  for (int t = sub;;) {
+    finish(t);
+    t += kBatch * side;
+    if (t >= nt) break;
+    load(t);
   }
 }
 
@@ -231,18 +229,22 @@ int launch(RopeParams& p, pa_dtype dtype, bool half, void* stream) {
   p.items = (int)items;
   for (Part* a : {&p.q, &p.k, &p.c})
     if (a->units == 0) a->units = 1;
-  // Tokens a CTA: one batch of units for its threads, as far as shared memory holds their
-  // cosines and two CTAs an SM are left.
-  long long tpb = (long long)kBatch * kThreads / items;
-  tpb = tpb < kTableEntries / p.pairs ? tpb : kTableEntries / p.pairs;
-  const long long spread = p.n / (2 * kTunedSms);
-  tpb = tpb < spread ? tpb : spread;
+  // Tokens a CTA: kRounds batches, as far as shared memory holds their cosines and the GPU gets
+  // four CTAs an SM.
+  const unsigned groups = (unsigned)((items + kThreads - 1) / kThreads);
+  const int side = items < kThreads ? (int)(kThreads / items) : 1;
+  const int most = kTableEntries / p.pairs;
+  const long long spread = (long long)p.n * groups / (4 * kTunedSms);
+  long long tpb = spread < most ? spread : most;
+  tpb = tpb < kRounds * kBatch * side ? tpb : kRounds * kBatch * side;
+  if (tpb > kBatch * side) tpb -= tpb % (kBatch * side);
   p.tpb = (int)(tpb < 1 ? 1 : tpb);
   const unsigned grid = (unsigned)((p.n + (long long)p.tpb - 1) / p.tpb);
+  if (groups > 65535) return PA_ERR_SHAPE;
   auto kernel = dtype == PA_F32 ? (half ? &rope_kernel<float, true> : &rope_kernel<float, false>)
                                 : (half ? &rope_kernel<__nv_bfloat16, true> : &rope_kernel<__nv_bfloat16, false>);
   void* args[] = {&p};
-  return ck(cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(grid), dim3(kThreads), args, 0,
+  return ck(cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(grid, groups), dim3(kThreads), args, 0,
                              (cudaStream_t)stream),
             "cudaLaunchKernel(rope_kernel)")
              ? PA_OK
