@@ -45,7 +45,8 @@ struct PrefillParams {
 };
 
 struct Shared {
-  uint64_t empty[kSlots], full_k[2], full_v[2], q[2], q_empty[2], s[2], p[2][2], pv[2], o_free[2], drain[2];
+  uint64_t empty[kSlots], full_k[2], full_v[2], q[2], q_empty[2], s[2], p[2][2], pv[2], o_free[2], drain[2], ml_full;
+  float ml[128][2];                          // SPLIT: maximum and sum of the second half's rows
   uint32_t tmem_base;
   int abort;
   int turn;                                  // 1 while one row tile's products go out
@@ -86,15 +87,21 @@ __device__ __forceinline__ int rows_of(const PrefillParams& p, int b) {
   return a >= 0 && e >= a && e <= p.rows && u >= 0 && v >= u && v <= p.kv_rows ? e - a : -1;
 }
 
-// The work: (unit, head) pairs, heads innermost, a unit being 256 rows of a sequence; the units
+// Two chains of softmax and products run side by side in a CTA.  They are two row tiles over the
+// same keys or, SPLIT, the even and the odd key tiles of one row tile, joined at the end: half the
+// time for an item, where the rows are too few to give every CTA 256 of them.
+//
+// The work: (unit, head) pairs, heads innermost, a unit being 256 (128) rows of a sequence; the units
 // of all sequences in order, every sequence's last, and longest, unit first.  The CTAs take
 // them in rounds, forth and back, so that no CTA has the longer ones of every round; a warp walks
 // its CTA's by itself, 32 sequences a step.
 struct Item {
   int h, q0, n, k0, L, first, past;          // head; rows; keys; the item's first row of the sequence's, its position
-  int nt[2];                                 // key tiles that each row tile sees
+  int nt[2], most;                           // key tiles of each chain, of the item
 };
+template <bool SPLIT>
 struct Walk {
+  static constexpr int kUnit = SPLIT ? kRows : 2 * kRows;      // rows of a unit
   int round, b, base;                        // next round; a sequence at or before its unit's, units before that
   __device__ __forceinline__ bool next(const PrefillParams& p, int lane, Item& it) {
     const int item = round * (int)gridDim.x + (int)((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
@@ -102,7 +109,7 @@ struct Walk {
     const int unit = item / p.H;
     it.h = item - unit * p.H;
     for (; b < p.B; b += 32) {
-      const int k = b + lane < p.B ? (max(rows_of(p, b + lane), 0) + 2 * kRows - 1) / (2 * kRows) : 0;
+      const int k = b + lane < p.B ? (max(rows_of(p, b + lane), 0) + kUnit - 1) / kUnit : 0;
       int incl = k;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -119,13 +126,22 @@ struct Walk {
         it.n = __ldg(&p.query_start[b + 1]) - it.q0;
         it.k0 = __ldg(&p.kv_start[b]);
         it.L = __ldg(&p.kv_start[b + 1]) - it.k0;
-        it.first = (base + units - 1 - unit) * 2 * kRows;
+        it.first = (base + units - 1 - unit) * kUnit;
         it.past = it.L - it.n + it.first;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        auto tiles = [&](int x) -> int {
           const int r = min(it.n - it.first - x * kRows, kRows);
           const int end = r > 0 ? min(it.L, max(0, it.past + x * kRows + r)) : 0;
-          it.nt[x] = (end + kKT - 1) / kKT;
+          return (end + kKT - 1) / kKT;
+        };
+        if constexpr (SPLIT) {
+          const int all = tiles(0);
+          it.nt[0] = (all + 1) / 2;
+          it.nt[1] = all / 2;
+          it.most = all;
+        } else {
+          it.nt[0] = tiles(0);
+          it.nt[1] = tiles(1);
+          it.most = max(it.nt[0], it.nt[1]);
         }
         return true;
       }
@@ -170,16 +186,16 @@ __device__ __noinline__ void plain_row(const PrefillParams& p, int row, int h, i
     p.out[((size_t)row * p.H + h) * p.Dv + e * 32 + lane] = __float2bfloat16_rn(o[e] / l);
 }
 
-// O / l of a warp's 32 rows as bf16 (zeros if there is no O); returns the carries of exponents
-// that are all ones.
-__device__ __forceinline__ uint32_t write_rows(const PrefillParams& p, uint32_t tO, bool have, float inv, int q0, int row,
-                                            int n, int h, int lane) {
+// f0 O of a warp's 32 rows, and f1 of the next chain's if there are two, as bf16 (zeros if there is
+// none); returns the carries of exponents that are all ones.
+__device__ __forceinline__ uint32_t write_rows(const PrefillParams& p, uint32_t tO, bool have, float f0, bool two,
+                                               float f1, int q0, int row, int n, int h, int lane) {
   uint32_t full = 0;
   auto packed = [&](const uint32_t* w) -> uint4 {
     uint32_t y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      y[i] = have ? pack_bf16(__uint_as_float(w[2 * i]) * inv, __uint_as_float(w[2 * i + 1]) * inv) : 0u;
+      y[i] = have ? pack_bf16(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])) : 0u;
       full |= (y[i] & 0x7f807f80u) + 0x00800080u;
     }
     return make_uint4(y[0], y[1], y[2], y[3]);
@@ -195,6 +211,15 @@ __device__ __forceinline__ uint32_t write_rows(const PrefillParams& p, uint32_t 
       if (have) {
         tmem_ld32(tO + c, w);
         tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f0);
+      }
+      if (two) {
+        uint32_t z[32];
+        tmem_ld32(tO + 128 + c, z);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(fmaf(__uint_as_float(z[i]), f1, __uint_as_float(w[i])));
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) y[k] = packed(w + k * 8);
@@ -221,6 +246,7 @@ __device__ __forceinline__ uint32_t write_rows(const PrefillParams& p, uint32_t 
   return full;
 }
 
+template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapQr,
                       const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapKr,
@@ -238,7 +264,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->q[i], 1);
-      mbar_init(&sh->q_empty[i], 1);
+      mbar_init(&sh->q_empty[i], SPLIT ? 2 : 1);
       mbar_init(&sh->s[i], 1);
       mbar_init(&sh->p[i][0], 4);
       mbar_init(&sh->p[i][1], 4);
@@ -248,7 +274,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
       mbar_init(&sh->full_v[i], 1);
       mbar_init(&sh->drain[i], 1);
     }
-    for (int i = 0; i < kSlots; ++i) mbar_init(&sh->empty[i], 2);    // both row tiles
+    for (int i = 0; i < kSlots; ++i) mbar_init(&sh->empty[i], SPLIT ? 1 : 2);    // chains that use a key tile
+    mbar_init(&sh->ml_full, 4);
     sh->abort = 0;
     sh->turn = 0;
     fence_mbar_init();
@@ -263,7 +290,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
   const uint32_t tmem = sh->tmem_base;
   const int ncd = (p.Dk + 63) / 64, ncv = (p.Dv + 63) / 64;    // chunks of the keys' own part, of the values
   const int per = ncd + 3;                   // slots of a key tile: ncd + 1 of K, 2 of V
-  Walk walk{0, 0, 0};
+  Walk<SPLIT> walk{0, 0, 0};
   Item it = {};
 
   if (warp >= 8) {
@@ -291,7 +318,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
         return smem + kOffRing + sl * kChunk;
       };
       while (ok && walk.next(p, lane, it)) {
-        const int most = max(it.nt[0], it.nt[1]);
+        const int most = it.most;
         if (lane == 0 && most > 0) {
           load_q(0);
           for (int j = 0; ok && j < most; ++j, ++k) {
@@ -305,7 +332,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
               else tma_load_4d(dst, &mapKr, full, 0, row, 0, 0, keep);
             }
             if (!ok) break;
-            if (j == 0) load_q(1);
+            if (!SPLIT && j == 0) load_q(1);
             full = &sh->full_v[k & 1];
             mbar_arrive_expect_tx(full, (uint32_t)ncv * kChunk);
             for (int v = 0; v < 2; ++v) {
@@ -342,15 +369,17 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
       const uint32_t sb = __shfl_sync(0xffffffffu, sbase, 0), t0 = __shfl_sync(0xffffffffu, tmem, 0);
       const uint32_t idS = idesc_bf16_f32(kRows, kKT, false, false);
       const uint32_t idO = idesc_bf16_f32(kRows, p.Dv, false, true);
-      const uint64_t da = sdesc_sw128(sb + x * 3 * kChunk, 16, 1024), dk = sdesc_sw128(sb + kOffRing, 16, 1024);
+      const int qx = SPLIT ? 0 : x;          // whose Q
+      const uint64_t da = sdesc_sw128(sb + qx * 3 * kChunk, 16, 1024), dk = sdesc_sw128(sb + kOffRing, 16, 1024);
       const uint64_t dv = sdesc_sw128(sb + kOffRing, kChunk / 2, 1024);
       const uint32_t tS = t0 + x * 128, tO = t0 + kColO + x * 128;
       const int own_steps = p.Dk / 16, rope_steps = p.P / 16;
       bool ok = true;
-      int k = 0, u = 0, nq = 0, np = 0;      // key tiles, their slots; row tiles, P tiles of x
-      // S_x against key tile k, whose slots begin at v
-      auto scores = [&](int k, int v, bool last) {
+      int k = 0, nq = 0, no = 0, np = 0;     // key tiles; Q tiles, outputs and P tiles of x
+      // S_x against key tile k
+      auto scores = [&](int k, bool last) {
         if (!ok) return;
+        const int v = k * per;
         if (lead) {
 #pragma unroll
           for (int c = 0; c < 3; ++c) {
@@ -364,57 +393,72 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
             umma_commit(&sh->empty[sl]);
           }
           umma_commit(&sh->s[x]);
-          if (last) umma_commit(&sh->q_empty[x]);
+          if (last) umma_commit(&sh->q_empty[qx]);
         }
         __syncwarp();
       };
       bool more = walk.next(p, lane, it);
       while (ok && more) {
         const int n = __shfl_sync(0xffffffffu, it.nt[x], 0);
-        const int most = __shfl_sync(0xffffffffu, max(it.nt[0], it.nt[1]), 0);
+        const int most = __shfl_sync(0xffffffffu, it.most, 0);
+        constexpr int kStep = SPLIT ? 2 : 1;
+        int kk = SPLIT ? k + x : k;          // the chain's key tile
+        if (n > 0 || (SPLIT && most > 0)) ok = ok && wait(&sh->q[qx], (uint32_t)nq & 1u, abort_flag);
         if (n > 0) {
-          ok = ok && wait(&sh->q[x], (uint32_t)nq & 1u, abort_flag) &&
-               wait(&sh->full_k[k & 1], (uint32_t)(k >> 1) & 1u, abort_flag);
+          ok = ok && wait(&sh->full_k[kk & 1], (uint32_t)(kk >> 1) & 1u, abort_flag);
           tc_fence_after();
-          scores(k, u, n == 1);
+          scores(kk, n == 1);
+        } else if (SPLIT && most > 0 && lead && ok) {
+          mbar_arrive(&sh->q_empty[0]);      // (no key tile for this chain)
         }
         more = walk.next(p, lane, it);       // (while the softmax has work)
-        // the last output of the row tile has been read
-        ok = ok && wait(&sh->o_free[x], ((uint32_t)nq & 1u) ^ 1u, abort_flag);
-        for (int j = 0; ok && j < most; ++j, ++k, u += per) {
-          if (j >= n) {
-            // a key tile that only the other row tile sees
-            ok = wait(&sh->full_k[k & 1], (uint32_t)(k >> 1) & 1u, abort_flag) &&
-                 wait(&sh->full_v[k & 1], (uint32_t)(k >> 1) & 1u, abort_flag);
-            if (lead && ok)
-              for (int c = 0; c < per; ++c) mbar_arrive(&sh->empty[(u + c) & (kSlots - 1)]);
-            __syncwarp();
-            continue;
-          }
+        // the last output of the chain has been read
+        if (n > 0) ok = ok && wait(&sh->o_free[x], ((uint32_t)no & 1u) ^ 1u, abort_flag);
+        for (int j = 0; ok && j < n; ++j, kk += kStep) {
           // O_x += P_x V, half a tile of keys at a time
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
-            const int sl = (u + ncd + 1 + v) & (kSlots - 1);
+            const int sl = (kk * per + ncd + 1 + v) & (kSlots - 1), kn = kk + kStep;
             ok = ok && wait(&sh->p[x][v], (uint32_t)(np + j) & 1u, abort_flag);
-            if (v == 0) ok = ok && wait(&sh->full_v[k & 1], (uint32_t)(k >> 1) & 1u, abort_flag);
-            if (v == 1 && j + 1 < n) ok = ok && wait(&sh->full_k[(k + 1) & 1], (uint32_t)((k + 1) >> 1) & 1u, abort_flag);
+            if (v == 0) ok = ok && wait(&sh->full_v[kk & 1], (uint32_t)(kk >> 1) & 1u, abort_flag);
+            if (!SPLIT && v == 1 && j + 1 < n) ok = ok && wait(&sh->full_k[kn & 1], (uint32_t)(kn >> 1) & 1u, abort_flag);
             if (!ok) break;
             tc_fence_after();
             if (v == 1 && lead) take_turn(&sh->turn);
             if (lead) {
               const uint64_t db = sdesc_at(dv, sl * kChunk);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_bf16_ts(tO, tS + v * 32 + kk * 8, sdesc_at(db, kk * 2048), idO, j > 0 || v > 0 || kk > 0 ? 1u : 0u);
+              for (int i = 0; i < 4; ++i)
+                umma_bf16_ts(tO, tS + v * 32 + i * 8, sdesc_at(db, i * 2048), idO, j > 0 || v > 0 || i > 0 ? 1u : 0u);
               umma_commit(&sh->empty[sl]);
               if (v == 1) umma_commit(&sh->pv[x]);
             }
             __syncwarp();
           }
-          if (j + 1 < n) scores(k + 1, u + per, j + 2 == n);
+          if (SPLIT && j + 1 < n) {
+            // (the chain's next keys may need the place of the values that just went out)
+            const int kn = kk + kStep;
+            if (lead) *static_cast<volatile int*>(&sh->turn) = 0;
+            ok = ok && wait(&sh->full_k[kn & 1], (uint32_t)(kn >> 1) & 1u, abort_flag);
+            tc_fence_after();
+            if (lead) take_turn(&sh->turn);
+          }
+          if (j + 1 < n) scores(kk + kStep, j + 2 == n);
           if (lead) *static_cast<volatile int*>(&sh->turn) = 0;
         }
-        nq += n > 0;
+        if constexpr (!SPLIT) {
+          // key tiles that only the other row tile sees
+          for (int j = n; ok && j < most; ++j) {
+            ok = wait(&sh->full_k[(k + j) & 1], (uint32_t)((k + j) >> 1) & 1u, abort_flag) &&
+                 wait(&sh->full_v[(k + j) & 1], (uint32_t)((k + j) >> 1) & 1u, abort_flag);
+            if (lead && ok)
+              for (int c = 0; c < per; ++c) mbar_arrive(&sh->empty[((k + j) * per + c) & (kSlots - 1)]);
+            __syncwarp();
+          }
+        }
+        k += most;
+        nq += SPLIT ? most > 0 : n > 0;
+        no += n > 0;
         np += n;
       }
       if (lead) umma_commit(&sh->drain[x]);  // every MMA has completed before TMEM is freed
@@ -427,12 +471,12 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
     const int r = (int)threadIdx.x & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + x * 128 + lane_off, tO = tmem + kColO + x * 128 + lane_off;
-    int kc = 0, np = 0;                      // key tiles, tiles of P before this item
+    int kc = 0, np = 0, np1 = 0, joins = 0;  // key tiles, tiles of P (of the second chain's, items that have any) before this item
     bool more = walk.next(p, lane, it);
     while (more) {
-      const int row = it.first + x * kRows + r;                // of the sequence
-      const int pos = it.past + x * kRows + r;
-      const int mine = x == 0 ? it.nt[0] : it.nt[1];
+      const int row = it.first + (SPLIT ? 0 : x * kRows) + r;  // of the sequence
+      const int pos = it.past + (SPLIT ? 0 : x * kRows) + r;
+      const int mine = x == 0 ? it.nt[0] : it.nt[1], other = SPLIT && x == 0 ? it.nt[1] : 0;
       float m_ref = -INFINITY, lsum = 0.f;
       for (int j = 0; j < mine; ++j) {
         wait(&sh->s[x], (uint32_t)(np + j) & 1u, abort_flag);
@@ -442,7 +486,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32(tS + i * 32, v[i]);
         tmem_ld_wait();
-        const int seen = min(pos, it.L - 1) - j * kKT;         // last key of the tile that the row sees
+        const int jt = SPLIT ? 2 * j + x : j;                  // key tile of the item
+        const int seen = min(pos, it.L - 1) - jt * kKT;        // last key of the tile that the row sees
         if (__any_sync(0xffffffffu, seen < kKT - 1)) {
 #pragma unroll
           for (int c = 0; c < kKT; ++c)
@@ -492,12 +537,12 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
             pw[c] = pack_bf16(p0, p1);
           }
           tmem_st16(tS + i * 16, pw);
-          if (i == 1 && (j + 1) * kKT > it.L) {
+          if (i == 1 && (jt + 1) * kKT > it.L) {
             // Rows behind the context may hold anything, and 0 * NaN would reach O: zeros, before
-            // any of P is handed over (from both row tiles: either's P V may come first).
-            const int u = (kc + j) * per + ncd + 1 + (r >> 6);
-            wait(&sh->full_v[(kc + j) & 1], (uint32_t)((kc + j) >> 1) & 1u, abort_flag);
-            if (j * kKT + r >= it.L) {
+            // any of P is handed over (by every chain that uses them: either's P V may come first).
+            const int u = (kc + jt) * per + ncd + 1 + (r >> 6);
+            wait(&sh->full_v[(kc + jt) & 1], (uint32_t)((kc + jt) >> 1) & 1u, abort_flag);
+            if (jt * kKT + r >= it.L) {
               unsigned char* vrow = smem + kOffRing + (u & (kSlots - 1)) * kChunk + (r & 63) * 128;
               for (int c = 0; c < ncv * 8; ++c)  // (each row in another order: the banks are all in use)
                 *reinterpret_cast<uint4*>(vrow + (c >> 3) * (kChunk / 2) + (((c + r) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
@@ -520,19 +565,49 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
       }
 
       // ---- O / l as bf16 rows
-      const int q0 = it.q0, n = it.n, k0 = it.k0, h = it.h, tiles = max(it.nt[0], it.nt[1]);
+      const int q0 = it.q0, n = it.n, k0 = it.k0, h = it.h;
+      kc += it.most;
       more = walk.next(p, lane, it);         // (its loads run beside the last product)
+      if (SPLIT && x == 1) {
+        if (mine > 0) {
+          // (its last product waited for the item before to be read)
+          wait(&sh->pv[1], (uint32_t)(np + mine - 1) & 1u, abort_flag);
+          __syncwarp();
+          sh->ml[r][0] = m_ref;
+          sh->ml[r][1] = lsum;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->ml_full);
+        }
+        np += mine;
+        continue;
+      }
       if (mine > 0) {
         wait(&sh->pv[x], (uint32_t)(np + mine - 1) & 1u, abort_flag);
         __syncwarp();
         tc_fence_after();
       }
+      float f0 = 1.f, f1 = 0.f;              // of O_x, and of the other half's
+      if (other > 0) {
+        wait(&sh->ml_full, (uint32_t)joins & 1u, abort_flag);
+        wait(&sh->pv[1], (uint32_t)(np1 + other - 1) & 1u, abort_flag);
+        __syncwarp();
+        tc_fence_after();
+        const float m1 = sh->ml[r][0], l1 = sh->ml[r][1], m = fmaxf(m_ref, m1);
+        f0 = m_ref == -INFINITY ? 0.f : exp2f(m_ref - m);
+        f1 = m1 == -INFINITY ? 0.f : exp2f(m1 - m);
+        lsum = fmaf(lsum, f0, l1 * f1);
+        if (l1 != l1) lsum = l1;             // (a row of NaN scores has no maximum)
+        ++joins;
+      }
       const float inv = lsum != 0.f ? 1.f / lsum : 0.f;
-      const uint32_t full = write_rows(p, tO, mine > 0, inv, q0, row, n, h, lane);
+      const uint32_t full = write_rows(p, tO, mine > 0, inv * f0, SPLIT && other > 0, inv * f1, q0, row, n, h, lane);
       if (mine > 0) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->o_free[x]);
+        if (lane == 0) {
+          mbar_arrive(&sh->o_free[x]);
+          if (other > 0) mbar_arrive(&sh->o_free[1]);
+        }
       }
       // A value that is not finite reaches every row of the tile, the ones that do not see it by
       // 0 * NaN.  Rows with finite weights and an output that is not are done again by themselves.
@@ -541,8 +616,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
         const int who = __ffs(todo) - 1;
         plain_row(p, q0 + __shfl_sync(0xffffffffu, row, who), h, k0, __shfl_sync(0xffffffffu, pos, who) + 1, lane);
       }
-      kc += tiles;
       np += mine;
+      np1 += other;
     }
   }
   tc_fence_before();
@@ -570,8 +645,10 @@ extern "C" int pa_latent_prefill(void* out, const void* query, const int32_t* qu
       !dim_ok(value_dim) || rope_dim <= 0 || rope_dim > 64 || rope_dim % 16 || key_rope_stride < rope_dim ||
       !(scale > 0.f) || (long long)total_queries * num_heads > 0x7fffffffll)
     return PA_ERR_SHAPE;
-  const long long units = (long long)total_queries / (2 * kRows) + num_seqs;
-  if (units * num_heads > 0x7fff0000ll) return PA_ERR_SHAPE;
+  // units of 256 rows at most, and of 128
+  const long long units2 = (long long)total_queries / (2 * kRows) + num_seqs;
+  const long long units1 = (long long)total_queries / kRows + num_seqs;
+  if (units1 * num_heads > 0x7fff0000ll) return PA_ERR_SHAPE;
   if (num_seqs == 0 || total_queries == 0) return PA_OK;
   if (!out || !query || !query_start || !kv_start || (total_kv && (!kv || !key_rope))) return PA_ERR_NULL;
   if (!aligned16(out) || !aligned16(query) || !aligned16(kv) || !aligned16(key_rope) || key_rope_stride % 8)
@@ -601,7 +678,14 @@ extern "C" int pa_latent_prefill(void* out, const void* query, const int32_t* qu
   }
   int dev = 0;
   if (!ck(cudaGetDevice(&dev), "cudaGetDevice")) return PA_ERR_CUDA;
-  if (!raise_smem_limit(reinterpret_cast<const void*>(&latent_prefill_kernel), dev)) return PA_ERR_CUDA;
+  const int sms = device_sm_count();
+  // The chains of a CTA divide one row tile's keys where the sequences have no second row tile, or
+  // where 256 rows a CTA would leave SMs without work.
+  const bool split = total_queries <= (long long)kRows * num_seqs || units2 * num_heads <= 2ll * sms;
+  const long long items = (split ? units1 : units2) * num_heads;
+  const void* kernel = split ? reinterpret_cast<const void*>(&latent_prefill_kernel<true>)
+                             : reinterpret_cast<const void*>(&latent_prefill_kernel<false>);
+  if (!raise_smem_limit(kernel, dev)) return PA_ERR_CUDA;
   PrefillParams p = {};
   p.out = static_cast<__nv_bfloat16*>(out);
   p.q = static_cast<const __nv_bfloat16*>(query);
@@ -618,10 +702,9 @@ extern "C" int pa_latent_prefill(void* out, const void* query, const int32_t* qu
   p.rows = total_queries;
   p.kv_rows = total_kv;
   p.qscale = scale * kLog2e;
-  const int sms = device_sm_count();
   void* args[] = {&mapQ, &mapQr, &mapK, &mapKr, &mapV, &p};
-  return ck(cudaLaunchKernel(reinterpret_cast<const void*>(&latent_prefill_kernel), dim3((unsigned)(units * num_heads < sms ? units * num_heads : sms)),
-                             dim3(kThreads), args, kSmemBytes, (cudaStream_t)stream),
+  return ck(cudaLaunchKernel(kernel, dim3((unsigned)(items < sms ? items : sms)), dim3(kThreads), args, kSmemBytes,
+                             (cudaStream_t)stream),
             "cudaLaunchKernel(latent_prefill_kernel)")
              ? PA_OK
              : PA_ERR_CUDA;
