@@ -59,14 +59,24 @@ def rope(x, positions, frequencies, amplitude=1.0, layout="half"):
 def _attend(q, K, V, scale, at):
     """q [n, d], K [L, d], V [L, e], row i seeing 0..at[i]: output, sum w |v|, max sum |q k|."""
     out, mass, size = np.zeros((len(q), V.shape[1])), np.zeros((len(q), V.shape[1])), np.zeros(len(q))
-    for i, p in enumerate(at):
-        if p < 0:
-            continue
-        s = scale * (K[:p + 1] @ q[i])
+    live = [i for i, p in enumerate(at) if p >= 0]
+    if not live:
+        return out, mass, size
+    if np.isfinite(K).all() and np.isfinite(V).all():
+        late = np.arange(len(K))[None] > np.asarray(at)[live][:, None]
+        s = np.where(late, -np.inf, scale * (q[live] @ K.T))
+        w = np.exp(s - s.max(1, keepdims=True))
+        w /= w.sum(1, keepdims=True)
+        out[live], mass[live] = w @ V, w @ np.abs(V)
+        size[live] = scale * np.where(late, 0, np.abs(q[live]) @ np.abs(K).T).max(1)
+        return out, mass, size
+    for i in live:                       # (a product with 0 would carry a NaN into rows that do not see it)
+        n = at[i] + 1
+        s = scale * (K[:n] @ q[i])
         w = np.exp(s - s.max())
         w /= w.sum()
-        out[i], mass[i] = w @ V[:p + 1], w @ np.abs(V[:p + 1])
-        size[i] = scale * (np.abs(K[:p + 1]) @ np.abs(q[i])).max()
+        out[i], mass[i] = w @ V[:n], w @ np.abs(V[:n])
+        size[i] = scale * (np.abs(K[:n]) @ np.abs(q[i])).max()
     return out, mass, size
 
 

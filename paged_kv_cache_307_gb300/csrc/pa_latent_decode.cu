@@ -856,6 +856,7 @@ extern "C" int pa_latent_decode(void* out, const void* query, const int32_t* que
   if (!ck(cudaLaunchKernel(k.kernel, dim3(ctas), dim3(kThreads), args, k.smem, (cudaStream_t)stream),
           "cudaLaunchKernel(latent_decode_kernel)"))
     return PA_ERR_CUDA;
+  if ((long long)max_blocks_per_seq * block_size <= kTile) return PA_OK;    // a tile a row group: nothing is cut
   void* join[] = {&p};
   return ck(launch_after(k.join, dim3(2 * ctas, (unsigned)w.nr / 8), dim3(256), join, (cudaStream_t)stream),
             "cudaLaunchKernel(latent_join_kernel)")

@@ -45,7 +45,7 @@ struct PrefillParams {
 };
 
 struct Shared {
-  uint64_t empty[kSlots], full_k[2], full_v[2], q[2], q_empty[2], s[2], p[2][2], pv[2], o_free[2], drain[2], ml_full;
+  uint64_t empty[kSlots], full_k[4], full_v[4], q[2], q_empty[2], s[2], p[2][2], pv[2], o_free[2], drain[2], ml_full;
   float ml[128][2];                          // SPLIT: maximum and sum of the second half's rows
   uint32_t tmem_base;
   int abort;
@@ -270,11 +270,13 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
       mbar_init(&sh->p[i][1], 4);
       mbar_init(&sh->pv[i], 1);
       mbar_init(&sh->o_free[i], 4);
-      mbar_init(&sh->full_k[i], 1);
-      mbar_init(&sh->full_v[i], 1);
       mbar_init(&sh->drain[i], 1);
     }
     for (int i = 0; i < kSlots; ++i) mbar_init(&sh->empty[i], SPLIT ? 1 : 2);    // chains that use a key tile
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sh->full_k[i], 1);
+      mbar_init(&sh->full_v[i], 1);
+    }
     mbar_init(&sh->ml_full, 4);
     sh->abort = 0;
     sh->turn = 0;
@@ -323,20 +325,23 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
           load_q(0);
           for (int j = 0; ok && j < most; ++j, ++k) {
             const int row = it.k0 + j * kKT;
-            uint64_t* full = &sh->full_k[k & 1];
-            mbar_arrive_expect_tx(full, (uint32_t)(ncd + 1) * kChunk);
+            // Key tile k uses full_k[k & 3] and full_v[k & 3].  Each is armed once the first slot is
+            // free, and not before: the slot's last user, or one after it, has waited for what the
+            // barrier announced four tiles ago.
+            uint64_t* full = &sh->full_k[k & 3];
             for (int c = 0; c <= ncd; ++c) {
               unsigned char* dst = slot();
               if (!ok) break;
+              if (c == 0) mbar_arrive_expect_tx(full, (uint32_t)(ncd + 1) * kChunk);
               if (c < ncd) tma_load_4d(dst, &mapK, full, c * 64, it.h, row, 0, keep);
               else tma_load_4d(dst, &mapKr, full, 0, row, 0, 0, keep);
             }
             if (!ok) break;
             if (!SPLIT && j == 0) load_q(1);
-            full = &sh->full_v[k & 1];
-            mbar_arrive_expect_tx(full, (uint32_t)ncv * kChunk);
+            full = &sh->full_v[k & 3];
             for (int v = 0; v < 2; ++v) {
               unsigned char* dst = slot();
+              if (ok && v == 0) mbar_arrive_expect_tx(full, (uint32_t)ncv * kChunk);
               for (int c = 0; ok && c < ncv; ++c)
                 tma_load_4d(dst + c * (kChunk / 2), &mapV, full, c * 64, it.h, row + v * 64, 0, keep);
             }
@@ -348,9 +353,9 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
       if (lane == 0 && ok) {
         for (int x = 0; x < 2; ++x)
           if (nq[x] > 0) mbar_wait(&sh->q[x], (uint32_t)(nq[x] - 1) & 1u);
-        for (int i = max(0, k - 2); i < k; ++i) {
-          mbar_wait(&sh->full_k[i & 1], (uint32_t)(i >> 1) & 1u);
-          mbar_wait(&sh->full_v[i & 1], (uint32_t)(i >> 1) & 1u);
+        for (int i = max(0, k - 4); i < k; ++i) {
+          mbar_wait(&sh->full_k[i & 3], (uint32_t)(i >> 2) & 1u);
+          mbar_wait(&sh->full_v[i & 3], (uint32_t)(i >> 2) & 1u);
         }
       }
       // (given up: a millisecond for what is still on its way)
@@ -405,7 +410,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
         int kk = SPLIT ? k + x : k;          // the chain's key tile
         if (n > 0 || (SPLIT && most > 0)) ok = ok && wait(&sh->q[qx], (uint32_t)nq & 1u, abort_flag);
         if (n > 0) {
-          ok = ok && wait(&sh->full_k[kk & 1], (uint32_t)(kk >> 1) & 1u, abort_flag);
+          ok = ok && wait(&sh->full_k[kk & 3], (uint32_t)(kk >> 2) & 1u, abort_flag);
           tc_fence_after();
           scores(kk, n == 1);
         } else if (SPLIT && most > 0 && lead && ok) {
@@ -420,8 +425,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
           for (int v = 0; v < 2; ++v) {
             const int sl = (kk * per + ncd + 1 + v) & (kSlots - 1), kn = kk + kStep;
             ok = ok && wait(&sh->p[x][v], (uint32_t)(np + j) & 1u, abort_flag);
-            if (v == 0) ok = ok && wait(&sh->full_v[kk & 1], (uint32_t)(kk >> 1) & 1u, abort_flag);
-            if (!SPLIT && v == 1 && j + 1 < n) ok = ok && wait(&sh->full_k[kn & 1], (uint32_t)(kn >> 1) & 1u, abort_flag);
+            if (v == 0) ok = ok && wait(&sh->full_v[kk & 3], (uint32_t)(kk >> 2) & 1u, abort_flag);
+            if (!SPLIT && v == 1 && j + 1 < n) ok = ok && wait(&sh->full_k[kn & 3], (uint32_t)(kn >> 2) & 1u, abort_flag);
             if (!ok) break;
             tc_fence_after();
             if (v == 1 && lead) take_turn(&sh->turn);
@@ -439,7 +444,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
             // (the chain's next keys may need the place of the values that just went out)
             const int kn = kk + kStep;
             if (lead) *static_cast<volatile int*>(&sh->turn) = 0;
-            ok = ok && wait(&sh->full_k[kn & 1], (uint32_t)(kn >> 1) & 1u, abort_flag);
+            ok = ok && wait(&sh->full_k[kn & 3], (uint32_t)(kn >> 2) & 1u, abort_flag);
             tc_fence_after();
             if (lead) take_turn(&sh->turn);
           }
@@ -449,8 +454,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
         if constexpr (!SPLIT) {
           // key tiles that only the other row tile sees
           for (int j = n; ok && j < most; ++j) {
-            ok = wait(&sh->full_k[(k + j) & 1], (uint32_t)((k + j) >> 1) & 1u, abort_flag) &&
-                 wait(&sh->full_v[(k + j) & 1], (uint32_t)((k + j) >> 1) & 1u, abort_flag);
+            ok = wait(&sh->full_k[(k + j) & 3], (uint32_t)((k + j) >> 2) & 1u, abort_flag) &&
+                 wait(&sh->full_v[(k + j) & 3], (uint32_t)((k + j) >> 2) & 1u, abort_flag);
             if (lead && ok)
               for (int c = 0; c < per; ++c) mbar_arrive(&sh->empty[((k + j) * per + c) & (kSlots - 1)]);
             __syncwarp();
@@ -541,7 +546,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
             // Rows behind the context may hold anything, and 0 * NaN would reach O: zeros, before
             // any of P is handed over (by every chain that uses them: either's P V may come first).
             const int u = (kc + jt) * per + ncd + 1 + (r >> 6);
-            wait(&sh->full_v[(kc + jt) & 1], (uint32_t)((kc + jt) >> 1) & 1u, abort_flag);
+            wait(&sh->full_v[(kc + jt) & 3], (uint32_t)((kc + jt) >> 2) & 1u, abort_flag);
             if (jt * kKT + r >= it.L) {
               unsigned char* vrow = smem + kOffRing + (u & (kSlots - 1)) * kChunk + (r & 63) * 128;
               for (int c = 0; c < ncv * 8; ++c)  // (each row in another order: the banks are all in use)

@@ -211,6 +211,29 @@ def test_same_bits_again_on_another_stream_and_in_graphs(pa):
     assert pa.last_error() == 0
 
 
+def test_two_calls_at_once(pa):
+    """Calls on two streams, each with a workspace of its own."""
+    c, d = Cache([700, 300, 5], 512, 64, 16, seed=1), Cache([2500], 256, 32, 8, seed=2)
+    q, r = randn(1, 3, 40, 576), randn(2, 1, 16, 288)
+    one, two = _run(pa, c, q, 0.08), _run(pa, d, r, 0.1)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    for st in (s, t):
+        st.wait_stream(torch.cuda.current_stream())
+    outs = [(_run(pa, c, q, 0.08, stream=s), _run(pa, d, r, 0.1, stream=t)) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, one) and torch.equal(y, two) for x, y in outs) and pa.last_error() == 0
+
+
+def test_shared_blocks(pa):
+    """Sequences whose tables share blocks, and one that names a block twice."""
+    c = Cache([64, 64], 512, 64, 16, seed=3)
+    c.table[1] = c.table[0]
+    c.table[1, 2] = c.table[0, 1]
+    q = randn(1, 2, 16, 576)
+    check(_run(pa, c, q, 0.1), *c.oracle(q, 0.1))
+    assert pa.last_error() == 0
+
+
 def test_a_run_of_steps(pa):
     """Prompts appended, then tokens one step at a time: rotate and append, attend; the cache rebuilt by hand."""
     import oracle

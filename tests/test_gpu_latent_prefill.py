@@ -51,6 +51,20 @@ def test_ragged(pa, Dk, P, Dv, H, lens, new):
     assert pa.last_error() == 0
 
 
+@pytest.mark.parametrize("Dk,P,Dv", [(128, 64, 128), (64, 32, 32), (32, 48, 64)])
+def test_many_heads(pa, Dk, P, Dv):
+    """More (256 rows, head) pairs than the GPU takes at a time: two row tiles a CTA, several items each."""
+    a = _case([300, 129, 520, 7, 0, 260], [257, 129, 400, 9, 0, 4], 90, Dk, P, Dv, seed=3)
+    check(_run(pa, *a, Dv), *_want(*a))
+    assert pa.last_error() == 0
+
+
+def test_whole_prompt_of_many_tiles(pa):
+    a = _case([1500, 1100], [1500, 1100], 34, 128, 64, 128, seed=5)
+    check(_run(pa, *a, 128), *_want(*a))
+    assert pa.last_error() == 0
+
+
 def test_many_short_sequences(pa):
     lens = [(7 * i) % 31 + 1 for i in range(150)]
     new = [(5 * i) % (L + 1) for i, L in enumerate(lens)]
@@ -67,8 +81,9 @@ def test_strided_shared_keys(pa):
 
 
 @pytest.mark.parametrize("factor", [8.0, 60.0])
-def test_scores_far_apart(pa, factor):
-    q, start, kv, key, kv_start, scale = _case([700], [700], 2, 128, 64, 128, seed=4)
+@pytest.mark.parametrize("H", [2, 120])
+def test_scores_far_apart(pa, factor, H):
+    q, start, kv, key, kv_start, scale = _case([700], [700], H, 128, 64, 128, seed=4)
     for j in range(0, 700, 64):                               # growing keys: the maximum moves in every tile
         kv[j:j + 64, :, :128] *= 1.0 + j / 64
     a = (q, start, kv, key, kv_start, scale * factor)
@@ -79,7 +94,11 @@ def test_scores_far_apart(pa, factor):
 
 def test_rows_with_nothing_to_see(pa):
     """More rows than context, a context of zero, rows behind the last sequence, sequences without rows."""
-    H = 3
+    for H in (3, 70):
+        _nothing_to_see(pa, H)
+
+
+def _nothing_to_see(pa, H):
     q, kv, key = randn(1, 200, H, 192), randn(2, 170, H, 256), randn(3, 170, 64)
     start, kv_start = np.array([0, 140, 143, 143, 150]), np.array([0, 10, 10, 150, 160])
     want = oracle.latent_prefill(f64(q), start, f64(kv), f64(key), kv_start, 0.07)
@@ -89,8 +108,9 @@ def test_rows_with_nothing_to_see(pa):
     assert pa.last_error() == 0
 
 
-def test_nan_stays_with_the_rows_that_see_it(pa):
-    q, start, kv, key, kv_start, scale = _case([200, 90], [200, 90], 2, 128, 64, 128)
+@pytest.mark.parametrize("H", [2, 160])                     # a row tile a CTA, and two
+def test_nan_stays_with_the_rows_that_see_it(pa, H):
+    q, start, kv, key, kv_start, scale = _case([200, 90], [200, 90], H, 128, 64, 128)
     want = _want(q, start, kv, key, kv_start, scale)
     kv[150, 1, 200] = float("nan")                            # a value: its element from row 150 on
     key[180] = float("nan")                                   # a shared key: every head from row 180 on
@@ -104,6 +124,20 @@ def test_nan_stays_with_the_rows_that_see_it(pa):
     got, (w, m, s) = out[mid], (x[mid] for x in want)
     w[:, 1, 72] = np.nan
     check(got, w, m, s)
+
+
+def test_two_calls_at_once(pa):
+    """Calls on two streams share nothing."""
+    a, b = _case([600, 90], [600, 40], 12, 128, 64, 128, seed=1), _case([333], [333], 40, 64, 32, 64, seed=2)
+    one, two = _run(pa, *a, 128), _run(pa, *b, 64)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    for st in (s, t):
+        st.wait_stream(torch.cuda.current_stream())
+    for _ in range(4):
+        outs.append((_run(pa, *a, 128, stream=s), _run(pa, *b, 64, stream=t)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, one) and torch.equal(y, two) for x, y in outs) and pa.last_error() == 0
 
 
 def test_bad_starts(pa):
