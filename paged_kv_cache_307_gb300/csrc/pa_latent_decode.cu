@@ -19,7 +19,10 @@ namespace {
 __device__ unsigned g_status_latent;
 
 constexpr int kTile = 128;                   // tokens per tile
-constexpr int kThreads = 384;                // warps 0-7 softmax, 8-10 TMA, 11 MMA
+// Warps: softmax, SUB for each quarter of the accumulators' lanes (the columns divided among them),
+// then three of TMA and one of MMA.
+constexpr int subs(int nr) { return nr == 64 ? 4 : 2; }
+constexpr int threads(int nr) { return 128 * subs(nr) + 128; }
 constexpr uint32_t kChunk = 16384;           // 128 tokens x 64 elements
 constexpr uint32_t kPair = 2 * kChunk;       // 128 elements: one M = 128 product of O^T
 constexpr float kLog2e = 1.4426950408889634f;
@@ -47,7 +50,7 @@ struct Shared {
   alignas(16) float neg_m[NR];               // minus the reference of every row
   alignas(16) float f[NR];
   alignas(16) float red[4][NR];              // per warp: maxima, at the end sums
-  long long scan[kThreads / 32];
+  long long scan[threads(NR) / 32];
   long long first_off;
   int first_b;
   uint32_t tmem_base;
@@ -88,13 +91,14 @@ __device__ __forceinline__ float warp_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
 }
-// Barrier 2 of the 256 softmax threads, true for all if true for any.
-__device__ __forceinline__ bool vote256(bool x) {
+// Barrier 2 of the N softmax threads, true for all if true for any.
+template <int N>
+__device__ __forceinline__ bool vote(bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, 2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r) : "r"(x ? 1u : 0u) : "memory");
+      "bar.red.or.pred q, 2, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r) : "r"(x ? 1u : 0u), "n"(N) : "memory");
   return r != 0;
 }
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
@@ -126,6 +130,29 @@ __device__ __forceinline__ Seq seq_of(const LatentParams& p, int b, bool flag) {
 }
 __device__ __forceinline__ int groups_of(const LatentParams& p, const Seq& s, int nr) { return (s.n * p.H + nr - 1) / nr; }
 
+// x / y for what mostly fits 32 bits.
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  if (((x | y) >> 31) == 0) return (long long)((unsigned)x / (unsigned)y);
+  return x / y;
+}
+// The line of `total` units in at most `parts` parts, none of them empty: the first `longer` of
+// `len` + 1 units, the rest of `len`.
+struct Cuts {
+  long long len, longer;
+  int n;
+  Cuts() = default;
+  __device__ __forceinline__ Cuts(long long total, int parts) {
+    n = (int)min((long long)parts, total);
+    len = n > 0 ? quotient(total, n) : 0;
+    longer = total - len * n;
+  }
+  __device__ __forceinline__ long long begin(int part) const { return len * min(part, n) + min((long long)min(part, n), longer); }
+  __device__ __forceinline__ int part_of(long long unit) const {
+    const long long first = longer * (len + 1);
+    return (int)(unit < first ? quotient(unit, len + 1) : longer + quotient(unit - first, len));
+  }
+};
+
 // A CTA's work: consecutive units of the line of all (sequence, cl row groups, tile).  The
 // line is cut into equal parts, so that every CTA has as many tiles whatever the lengths are;
 // what a cut leaves in two CTAs is joined by the second kernel.
@@ -140,7 +167,8 @@ struct Item {
 template <int NR>
 struct Walk {
   int b, half, part;
-  long long off, left, at, total;
+  long long off, left, at;
+  Cuts cuts;
   bool first;
   __device__ __forceinline__ bool next(const LatentParams& p, Item& it) {
     while (left > 0) {
@@ -151,7 +179,7 @@ struct Walk {
         off = 0;
         continue;
       }
-      const int sg = (int)(off / s.tiles);
+      const int sg = (int)quotient(off, s.tiles);
       const int t = (int)(off - (long long)sg * s.tiles);
       const int cnt = (int)min((long long)(s.tiles - t), left);
       it.unit = at;
@@ -206,12 +234,13 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[16]) { t
 __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
 
 template <int NR, int RC>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads(NR), 1)
 latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_constant__ CUtensorMap mapQ,
                      const LatentParams p) {
   using Lay = Layout<NR, RC>;
   constexpr int NC = Lay::NC, NP = Lay::NP, SLOTS = Lay::kSlots;
   constexpr bool kAlias = Lay::kAlias;
+  constexpr int kThreads = threads(NR), SUB = subs(NR), kSoft = 128 * SUB, kTma = 4 * SUB, kMma = kTma + 3;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
@@ -232,9 +261,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
     }
     mbar_init(&sh->q_full, 1);
     mbar_init(&sh->q_empty, 1);
-    mbar_init(&sh->p, 8);
+    mbar_init(&sh->p, 4 * SUB);
     mbar_init(&sh->pv, 1);
-    mbar_init(&sh->o_free, 8);
+    mbar_init(&sh->o_free, 4 * SUB);
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
     sh->first_b = p.B;
@@ -242,7 +271,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
     prefetch_tensormap(&mapC);
     prefetch_tensormap(&mapQ);
   }
-  if (warp == 11) {
+  if (warp == kMma) {
     tmem_alloc(&sh->tmem_base, Lay::kTmem);
     tmem_relinquish();
   }
@@ -275,11 +304,14 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
       if (w < warp) before += sh->scan[w];
     }
     // (no empty parts: a line shorter than the grid leaves its last CTAs without work)
-    const long long cuts = min((long long)parts, total);
-    const long long u0 = part < cuts ? total * part / cuts : total, u1 = part < cuts ? total * (part + 1) / cuts : total;
+    const Cuts cuts(total, parts);
+    const long long u0 = cuts.begin(part), u1 = cuts.begin(part + 1);
     if (u0 >= before && u0 < before + sum) {     // (one thread, where there is anything)
       long long at = before;
-      for (int b = b0; b < b1; ++b) {
+      if (b1 - b0 == 1) {
+        sh->first_b = b0;
+        sh->first_off = u0 - before;
+      } else for (int b = b0; b < b1; ++b) {
         const Seq s = seq_of(p, b, false);
         const long long u = (long long)((groups_of(p, s, NR) + p.cl - 1) / p.cl) * s.tiles;
         if (u0 < at + u) {
@@ -297,22 +329,21 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
     walk.half = blockIdx.x % p.cl;
     walk.part = part;
     walk.at = u0;
-    walk.total = total;
+    walk.cuts = cuts;
     walk.first = true;
     // what neither of the CTA's slots begins stays at 0
     if (threadIdx.x < 2) p.ws_join[blockIdx.x * 2 + threadIdx.x] = make_int4(0, 0, 0, 0);
   }
   const uint32_t tmem = sh->tmem_base;
   const uint32_t tO = tmem + 2 * NR;
-  const long long cuts = min((long long)parts, walk.total);
   Item it;
 
-  if (warp >= 8 && warp < 11) {
+  if (warp >= kTma && warp < kMma) {
     // ------------------------------------------------------------ TMA producers
     // A warp gets a copy out in about 60 clocks, whatever its size, and a tile is 72 of 2 KB:
     // three warps share them, every third copy of a pair each.
     const uint64_t pol = policy_evict_first();
-    const int w = warp - 8;
+    const int w = warp - kTma;
     const int bsh = 31 - __clz(p.bs);
     const uint32_t box = (uint32_t)p.bs * 128u;
     const int blocks = kTile >> bsh;
@@ -377,7 +408,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
         mbar_wait(&sh->full_r[kAlias ? 0 : k & 1], (uint32_t)(kAlias ? k : k >> 1) & 1u);
       if (kq > 0) mbar_wait(&sh->q_full, (uint32_t)(kq - 1) & 1u);
     }
-  } else if (warp == 11) {
+  } else if (warp == kMma) {
     // ------------------------------------------------------------ MMA issuer
     // The whole warp walks, with values that are the same in all lanes, and one lane issues: the
     // descriptors then stay in uniform registers (moved there for every MMA, 57 clocks an MMA and not 47).
@@ -479,10 +510,10 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
     mbar_wait(&sh->drain, 0);
   } else {
     // ------------------------------------------------------------ softmax
-    // Thread = token; the tile's columns are divided between two warps a lane quarter.
-    constexpr int CW = NR / 2;
+    // Thread = token; the tile's columns are divided among SUB warps a lane quarter.
+    constexpr int CW = NR / SUB;
     const int r = (int)threadIdx.x & 127;    // token of the tile, latent dim at the end; TMEM lane
-    const int half = warp >> 2, c0 = half * CW;
+    const int sub = warp >> 2, c0 = sub * CW;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     int kt = 0;
     float l[CW];
@@ -534,7 +565,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
           for (int c = 8; c < CW; c += 2) top[(c >> 1) & 3] = fmax3(top[(c >> 1) & 3], x[c], x[c + 1]);
           need = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kSlack;
         }
-        need = vote256(need);
+        need = vote<kSoft>(need);
         if (need) {
           // new references: the tile's maxima where they are above
           scores();
@@ -543,7 +574,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
             const float y = warp_max(x[c]);
             if (lane == 0) sh->red[warp & 3][c0 + c] = y;
           }
-          named_sync(1, 256);
+          named_sync(1, kSoft);
           if (threadIdx.x < NR) {
             const int c = (int)threadIdx.x;
             const float y = fmaxf(fmaxf(sh->red[0][c], sh->red[1][c]), fmaxf(sh->red[2][c], sh->red[3][c])) * p.qscale;
@@ -553,7 +584,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
             // (a row that sees nothing of its first tile sees nothing of the later ones)
             sh->neg_m[c] = m == -INFINITY ? 0.f : -m;
           }
-          named_sync(1, 256);
+          named_sync(1, kSoft);
           exponents();
         }
         // P, and with it the rotated keys' chunk, is free; O holds the tile before
@@ -597,10 +628,10 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
           const bool drop = t >= it.end;
 #pragma unroll 1
           for (int i = 0; i < NP; ++i) {
-            unsigned char* at = smem + Lay::kOffRing + ((kt * NP + i) % SLOTS) * kPair + half * kChunk + r * 128;
+            unsigned char* at = smem + Lay::kOffRing + ((kt * NP + i) % SLOTS) * kPair + r * 128;
 #pragma unroll 1
-            for (int k = 0; k < 8; ++k) {
-              uint4* q = reinterpret_cast<uint4*>(at + (((k + r) & 7) << 4));   // (another piece in each row of eight)
+            for (int k = sub * (16 / SUB); k < (sub + 1) * (16 / SUB); ++k) {
+              uint4* q = reinterpret_cast<uint4*>(at + (k >> 3) * kChunk + (((k + r) & 7) << 4));   // (another piece in each row of eight)
               if (drop) {
                 *q = make_uint4(0u, 0u, 0u, 0u);
               } else {
@@ -624,7 +655,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
       // ---------------------------------------------------------- output of the row group
       warp_sums(l, lane);
       __syncwarp();
-      named_sync(1, 256);
+      named_sync(1, kSoft);
       {
         // the column that the halvings left in this lane
         int col = 0, spare = 31;
@@ -635,13 +666,10 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
         }
         if ((lane & spare) == 0) sh->red[warp & 3][c0 + col] = l[0];
       }
-      named_sync(1, 256);
+      named_sync(1, kSoft);
       if (!it.whole && it.tile == 0 && threadIdx.x == 0) {
-        // the CTAs after this one, as far as the group goes: the part that holds its last unit is
-        // the last that begins at or before it
-        const long long last = it.unit + it.tiles - 1;
-        const int part_of = (int)(((last + 1) * cuts + walk.total - 1) / walk.total) - 1;
-        p.ws_join[it.slot] = make_int4(it.q0 * p.H + it.r0, it.rows, part_of - part, 0);
+        // the CTAs after this one, as far as the group goes
+        p.ws_join[it.slot] = make_int4(it.q0 * p.H + it.r0, it.rows, walk.cuts.part_of(it.unit + it.tiles - 1) - part, 0);
       }
       if (threadIdx.x < NR) {
         const int c = (int)threadIdx.x;
@@ -654,7 +682,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
           ml[1] = it.nt > 0 ? sum : 0.f;
         }
       }
-      named_sync(1, 256);
+      named_sync(1, kSoft);
       const int R = RC * 64;
       if (it.nt > 0) {
         wait(&sh->pv, (uint32_t)(kt - 1) & 1u, abort_flag);
@@ -687,13 +715,13 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->o_free);
       }
-      named_sync(1, 256);                    // f and red are free again
+      named_sync(1, kSoft);                    // f and red are free again
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 11) tmem_dealloc(tmem, Lay::kTmem);
+  if (warp == kMma) tmem_dealloc(tmem, Lay::kTmem);
 }
 
 // Joins the row groups that a cut left in several CTAs.  grid (slots, NR / 8): a warp per row of the
@@ -772,11 +800,12 @@ Plan plan_of(int total, int num_seqs, int num_heads, int latent_dim) {
 struct Pick {
   const void *kernel, *join;
   size_t smem;
+  int threads;
 };
 template <int NR, int RC>
 Pick pick1() {
   return {reinterpret_cast<const void*>(&latent_decode_kernel<NR, RC>),
-          reinterpret_cast<const void*>(&latent_join_kernel<NR, RC>), Layout<NR, RC>::kBytes};
+          reinterpret_cast<const void*>(&latent_join_kernel<NR, RC>), Layout<NR, RC>::kBytes, threads(NR)};
 }
 template <int NR>
 Pick pick2(int rc) {
@@ -853,7 +882,7 @@ extern "C" int pa_latent_decode(void* out, const void* query, const int32_t* que
   p.qscale = scale * kLog2e;
   const unsigned ctas = (unsigned)(w.parts * w.cl);
   void* args[] = {&mapC, &mapQ, &p};
-  if (!ck(cudaLaunchKernel(k.kernel, dim3(ctas), dim3(kThreads), args, k.smem, (cudaStream_t)stream),
+  if (!ck(cudaLaunchKernel(k.kernel, dim3(ctas), dim3(k.threads), args, k.smem, (cudaStream_t)stream),
           "cudaLaunchKernel(latent_decode_kernel)"))
     return PA_ERR_CUDA;
   if ((long long)max_blocks_per_seq * block_size <= kTile) return PA_OK;    // a tile a row group: nothing is cut
