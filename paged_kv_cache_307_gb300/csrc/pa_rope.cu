@@ -15,7 +15,7 @@
 // chunks, half the rotated part apart; else one chunk.  A thread keeps its unit of a token
 // and walks the tokens: what the unit is costs it two divisions in all (found anew for every
 // token, they took 8192 tokens of 40 heads x 128 from 31 to 38 us, 64 tokens of a step from 2.9
-// to 4.2).
+// to 4.2; what is left bounds it still: the issue slots are 0.7 full).
 #include "pa_common.cuh"
 #include "pa_mma.cuh"
 
@@ -27,12 +27,12 @@ namespace {
 __device__ unsigned g_status_rope;
 
 constexpr int kThreads = 256;
-// Tokens in flight per thread, CTAs an SM, and batches of tokens a CTA takes: 2, 6 and 2 move
-// 8192 tokens of 40 heads x 128 in 31 us (5.3 TB/s); four tokens and four CTAs take 36, one token
-// and eight CTAs 38, a batch a CTA 35.
-constexpr int kBatch = 2;
-constexpr int kMinCtas = 6;
-constexpr int kRounds = 2;
+// Tokens a CTA takes side by side with as many as its threads have in flight: four, or two twice in
+// the half layout, whose units are twice as large; and CTAs an SM.  8192 tokens of 40 heads x 128,
+// interleaved, take 28.7 us (5.8 TB/s); two in flight 36, six CTAs 33, four 40.  5000 tokens of 20
+// heads x 64 in f32, half layout, take 8.9 us (5.8 TB/s); four in flight 13, six CTAs 9.7.
+constexpr int kTokens = 4;
+constexpr int kMinCtas = 5;
 constexpr int kTableEntries = 2048;      // (cos, sin) pairs in shared memory
 
 // One tensor of rows: bytes from token to token and head to head.
@@ -42,6 +42,7 @@ struct Part {
   long long src_token, src_head, dst_token, dst_head;
   int units;                             // of a head
   int all;                               // of a token
+  uint32_t per;                          // 2^32 / units, rounded up: r / units is the upper word of r * per
 };
 
 struct RopeParams {
@@ -53,6 +54,7 @@ struct RopeParams {
   float amplitude;
   int n, tpb, items;                     // tokens, tokens a CTA, units a token
   int pairs;                             // rotated pairs of a head
+  uint32_t per_pairs;                    // likewise
 };
 
 __device__ __forceinline__ uint4 ld_v4(const void* p) {
@@ -76,57 +78,70 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) rope_kernel(const RopePara
   using E = Elem<T>;
   constexpr int EPC = E::kPerChunk;
   constexpr int kPairs = HALF ? EPC : EPC / 2;             // pairs of a unit
+  constexpr int kBatch = HALF ? kTokens / 2 : kTokens;     // tokens in flight per thread
   __shared__ __align__(16) float2 table[kTableEntries];
   const int tok0 = blockIdx.x * p.tpb;
   const int nt = min(p.tpb, p.n - tok0);
   const int hop = p.pairs * E::kBytes;                     // HALF: from a pair's first element to its second
 
-  // ---- the thread's unit: tokens with few units share the CTA, of many each takes several CTAs
-  const int side = p.items < kThreads ? kThreads / p.items : 1;     // tokens side by side
-  int sub = 0, r = (int)(blockIdx.y * kThreads + threadIdx.x);
+  // ---- the thread's units: tokens with few units share the CTA side by side
+  const int side = p.items < kThreads ? kThreads / p.items : 1;
+  int sub = 0, r0 = (int)(blockIdx.y * kThreads + threadIdx.x);
   if (side > 1) {
     sub = (int)threadIdx.x / p.items;
-    r = (int)threadIdx.x - sub * p.items;
+    r0 = sub < side ? (int)threadIdx.x - sub * p.items : p.items;
   }
-  const bool active = sub < side && r < p.items;
-  const bool is_q = r < p.q.all, is_c = !is_q && r >= p.q.all + p.k.all;
-  const Part& a = is_q ? p.q : is_c ? p.c : p.k;
-  r -= is_q ? 0 : is_c ? p.q.all + p.k.all : p.q.all;
-  const int h = r / a.units, x = r - h * a.units;
-  const int turned = is_c ? 0 : p.pairs / kPairs;          // units of the head that are rotated
-  const bool turn = x < turned;
-  const int off = x * 16 + (HALF && !turn ? turned * 16 : 0);       // (each rotated unit was two chunks)
-  const char* src = a.src + tok0 * a.src_token + h * a.src_head + off;
-  char* dst = a.dst + h * a.dst_head + off;
-  const bool by_slot = !is_q && p.slots;
+  const int turned = p.pairs / kPairs;                     // units of a head that are rotated
 
-  const char* s[kBatch];
-  char* d[kBatch];
+  const char* src = nullptr;                               // the unit's bytes of token tok0
+  char* dst = nullptr;
+  long long src_token = 0, dst_token = 0;
+  int x = 0;
+  bool turn = false, by_slot = false, first = false;
+  auto unit = [&](int r) {
+    const bool is_q = r < p.q.all, is_c = !is_q && r >= p.q.all + p.k.all;
+    r -= is_q ? 0 : is_c ? p.q.all + p.k.all : p.q.all;
+    const uint32_t per = is_q ? p.q.per : is_c ? p.c.per : p.k.per;
+    const int units = is_q ? p.q.units : is_c ? p.c.units : p.k.units;
+    const int h = units > 1 ? (int)__umulhi((uint32_t)r, per) : r;
+    x = r - h * units;
+    turn = !is_c && x < turned;
+    by_slot = !is_q && p.slots;
+    first = !is_c && r == 0;
+    const int off = x * 16 + (HALF && !is_c && !turn ? turned * 16 : 0);    // (each rotated unit was two chunks)
+    src_token = is_q ? p.q.src_token : is_c ? p.c.src_token : p.k.src_token;
+    dst_token = is_q ? p.q.dst_token : is_c ? p.c.dst_token : p.k.dst_token;
+    src = (is_q ? p.q.src : is_c ? p.c.src : p.k.src) + tok0 * src_token +
+          h * (is_q ? p.q.src_head : is_c ? p.c.src_head : p.k.src_head) + off;
+    dst = (is_q ? p.q.dst : is_c ? p.c.dst : p.k.dst) + h * (is_q ? p.q.dst_head : is_c ? p.c.dst_head : p.k.dst_head) + off;
+  };
+
+  char* d[kBatch];                                         // null: nothing to do
   uint4 lo[kBatch], hi[kBatch];
   auto load = [&](int t) {
 #pragma unroll
     for (int b = 0; b < kBatch; ++b, t += side) {
-      s[b] = nullptr;
-      if (!active || t >= nt) continue;
+      d[b] = nullptr;
+      if (t >= nt) continue;
       long long row = tok0 + t;
       if (by_slot) {
         row = __ldg(reinterpret_cast<const long long*>(p.slots) + row);
         if (row < 0) continue;                             // padding
         if (row >= p.num_slots) {
-          if (!is_c && r == 0) atomicOr(&g_status_rope, PA_DEV_BAD_SLOT);
+          if (first) atomicOr(&g_status_rope, PA_DEV_BAD_SLOT);
           continue;
         }
       }
-      s[b] = src + t * a.src_token;
-      d[b] = dst + row * a.dst_token;
-      lo[b] = ld_v4(s[b]);
-      if (HALF && turn) hi[b] = ld_v4(s[b] + hop);
+      const char* s = src + t * src_token;
+      d[b] = dst + row * dst_token;
+      lo[b] = ld_v4(s);
+      if (HALF && turn) hi[b] = ld_v4(s + hop);
     }
   };
   auto finish = [&](int t) {
 #pragma unroll
     for (int b = 0; b < kBatch; ++b, t += side) {
-      if (!s[b]) continue;
+      if (!d[b]) continue;
       if (!turn) {
         st_v4(d[b], lo[b]);
         continue;
@@ -161,21 +176,30 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) rope_kernel(const RopePara
     }
   };
 
-  load(sub);                                               // (on its way while the table is made)
+  if (r0 < p.items) {                                      // (on its way while the table is made)
+    unit(r0);
+    load(sub);
+  }
   for (int i = threadIdx.x; i < nt * p.pairs; i += kThreads) {
-    const int t = i / p.pairs;
+    const int t = (int)__umulhi((uint32_t)i, p.per_pairs);
     const uint64_t phase = (uint64_t)(int64_t)__ldg(&p.positions[tok0 + t]) * __ldg(&p.steps[i - t * p.pairs]);
-    // the turn's fraction in [-1/2, 1/2), in half turns
+    // the turn's fraction in [-1/2, 1/2), in half turns (its upper word: 2^-33 of a turn)
     float sn, cn;
-    sincospif(__ll2float_rn((long long)phase) * 0x1p-63f, &sn, &cn);
+    sincospif((float)(int)(phase >> 32) * 0x1p-31f, &sn, &cn);
     table[i] = make_float2(cn * p.amplitude, sn * p.amplitude);
   }
   __syncthreads();
-  for (int t = sub;;) {
-    finish(t);
-    t += kBatch * side;
-    if (t >= nt) break;
-    load(t);
+  for (int r = r0; r < p.items;) {
+    for (int t = sub;;) {
+      finish(t);
+      t += kBatch * side;
+      if (t >= nt) break;
+      load(t);
+    }
+    r += (int)gridDim.y * kThreads;
+    if (side > 1 || r >= p.items) break;
+    unit(r);
+    load(sub);
   }
 }
 
@@ -227,20 +251,23 @@ int launch(RopeParams& p, pa_dtype dtype, bool half, void* stream) {
   if (items > 1 << 24) return PA_ERR_SHAPE;
   if (items == 0) return PA_OK;
   p.items = (int)items;
-  for (Part* a : {&p.q, &p.k, &p.c})
+  auto per = [](int n) { return n > 1 ? (uint32_t)(((1ull << 32) + n - 1) / n) : 0u; };
+  for (Part* a : {&p.q, &p.k, &p.c}) {
     if (a->units == 0) a->units = 1;
-  // Tokens a CTA: kRounds batches, as far as shared memory holds their cosines and the GPU gets
-  // four CTAs an SM.
-  const unsigned groups = (unsigned)((items + kThreads - 1) / kThreads);
+    a->per = per(a->units);
+  }
+  p.per_pairs = per(p.pairs);
+  // Tokens a CTA, as far as shared memory holds their cosines and the GPU gets four CTAs an SM; the
+  // units of few tokens are divided among CTAs as well.
   const int side = items < kThreads ? (int)(kThreads / items) : 1;
   const int most = kTableEntries / p.pairs;
-  const long long spread = (long long)p.n * groups / (4 * kTunedSms);
+  const long long spread = (long long)p.n / (4 * kTunedSms);
   long long tpb = spread < most ? spread : most;
-  tpb = tpb < kRounds * kBatch * side ? tpb : kRounds * kBatch * side;
-  if (tpb > kBatch * side) tpb -= tpb % (kBatch * side);
+  tpb = tpb < kTokens * side ? tpb : kTokens * side;
   p.tpb = (int)(tpb < 1 ? 1 : tpb);
   const unsigned grid = (unsigned)((p.n + (long long)p.tpb - 1) / p.tpb);
-  if (groups > 65535) return PA_ERR_SHAPE;
+  const long long all = (items + kThreads - 1) / kThreads, room = 8ll * kTunedSms / grid;
+  const unsigned groups = (unsigned)(all < room ? all : room < 1 ? 1 : room < 65535 ? room : 65535);
   auto kernel = dtype == PA_F32 ? (half ? &rope_kernel<float, true> : &rope_kernel<float, false>)
                                 : (half ? &rope_kernel<__nv_bfloat16, true> : &rope_kernel<__nv_bfloat16, false>);
   void* args[] = {&p};
