@@ -28,8 +28,9 @@
  *    Accumulation is fp32 whatever the storage type (the tensor-core forms
  *    round their product operands as each call's description states); bf16
  *    results are rounded to nearest even.
- *  - Supported sizes: head_dim in {32, 64, 128}; block_size in {4, 8, 16,
- *    32}; num_heads a multiple of num_kv_heads.  Query head h reads KV head
+ *  - Supported sizes (the latent cache and the rotary calls state their own):
+ *    head_dim in {32, 64, 128}; block_size in {4, 8, 16, 32}; num_heads a
+ *    multiple of num_kv_heads.  Query head h reads KV head
  *    h / (num_heads / num_kv_heads) (grouped-query attention).
  *  - Every pointer argument is a DEVICE pointer unless stated otherwise; the
  *    caller owns all memory and the library allocates nothing per call.
@@ -843,7 +844,9 @@ size_t pa_latent_decode_workspace_bytes(int total_queries, int num_seqs, int num
  *   dtype           PA_BF16; accumulation fp32, softmax weights rounded to
  *                   bf16 for their product with the values
  *
- * num_seqs <= 2048.
+ * num_seqs <= 2048.  A NaN value makes NaN of its element in the rows that see
+ * it, a NaN key of those rows whole; the rows before it are not touched by
+ * either.  (Rows next to a value that is not finite are computed one by one.)
  */
 int pa_latent_prefill(void* out, const void* query, const int32_t* query_start, int total_queries,
                       const void* kv, const void* key_rope, long long key_rope_stride, const int32_t* kv_start,

@@ -7,7 +7,31 @@
 //   S^T[128 tokens x NR] = C[128 x (R + P)] Q^T     A = the tile (K-major), B = Q rows
 //   O^T[R dims x NR]    += C^T[R x 128] P^T         A = the same bytes (MN-major), B = P
 // so a tile is read into shared memory once for both products, and few heads cost few
-// columns and not padded rows.
+// columns and not padded rows.  R = 512 with 64 rows: O^T takes 256 columns of tensor
+// memory, S^T two buffers of 64.
+//
+// Bound by HBM up to 64 rows a sequence: 64 requests x 16 heads over U[1024, 16384] take
+// 112 us (644 MB; 6.5 TB/s, 96 % of the copy rate, while all CTAs have tiles; 5.7 with the
+// start, the last tiles and the join).  With 128 heads two CTAs read the same tiles (DRAM traffic
+// is that of one: 340 MB) and the chain of a tile bounds them: 64 requests over U[1024, 8192]
+// take 131 us (629 TFLOP/s), about 6500 clocks a tile, of which the 68 MMAs are 3700 (an MMA of
+// M = 128 costs 48 clocks whatever is below 64 columns: its A operand's way out of shared
+// memory), the softmax between them 1500, waits for the copies into the slots that the second
+// product leaves 900.  Shared memory (Q 72 KB, a tile 144 KB) holds no second tile to fill those.
+//
+//  * The batch is a line of (sequence, row groups, tile) units, cut into equal parts for one
+//    CTA an SM (Walk): no tail of long contexts, at most two partial results a CTA, and a
+//    second kernel joins what a cut divides.
+//  * Copies: a warp gets a TMA copy out in about 60 clocks whatever its size, and a tile is 72 boxes
+//    of 2 KB (its chunks are apart in shared memory, so that the scores may begin with the first
+//    pair of chunks): three warps share them (one warp: 153 us where 117 came of four).
+//  * A slot of the ring is the 128 latent elements of one M = 128 product of O^T: it is free
+//    again when that product is done, while the other products still run.
+//  * The MMA warp keeps its descriptors in uniform registers (99 clocks an MMA where 49 do).
+//  * The references of the softmax are common to the 128 threads of a column and move only when a
+//    score exceeds one by 2^8: a barrier with a vote a tile; then O^T is scaled in tensor memory.
+//  * P lies over the rotated keys' chunk, which the scores are done with, where a tile is large.
+//  * Every wait is bounded (2 s); a timeout sets PA_DEV_TIMEOUT, and the roles wind down.
 #include <stddef.h>
 
 #include "pa_mma.cuh"

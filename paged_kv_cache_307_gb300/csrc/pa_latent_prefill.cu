@@ -2,12 +2,27 @@
 // (pa_latent_prefill) on the 5th-generation tensor cores: keys of key_dim elements a head,
 // one rotated key for all heads, values of value_dim.
 //
-// One CTA per (256 queries of a sequence, head), as two tiles of 128 rows:
+// Two chains in a CTA, each with 128 query rows of a head, a softmax warpgroup and an issuing warp:
 //   S_x = Q_x [K | K_rope]^T   M = 128, N = 128 keys, K = key_dim + rope_dim (12 MMAs of 192)
 //   O_x += P_x V               M = 128, N = value_dim, K = 128 keys, P from tensor memory
 // Tensor memory holds S_0, S_1 (128 columns each, P_x over the first half of its S_x) and
-// O_0, O_1.  The products of one tile run while the other's softmax does:
-//   ... P_0 V, S_0', P_1 V, S_1', P_0' V, ...
+// O_0, O_1: all 512 columns.  The products of one chain run while the other's softmax does.
+//
+// Bound by the chain of a tile and the tensor pipe: 4 prompts of 4096 tokens x 32 heads of 128 + 64
+// take 465 to 475 us (1450 TFLOP/s, 76 % of the burst GEMM rate; tensor pipe 66 % active).  A step
+// of both chains takes 3600 clocks, of which the 40 MMAs are 2600 (65 each at N = 128: operands of
+// 8 KB for a score's, at 128 bytes a clock), a chain's softmax 1500 and its products' way through
+// the pipe, with the waits around them, 1900.  What was tried and lost: 2^x by a polynomial for some
+// elements (the issue slots, not the special functions, bound the softmax), P in quarters, loading S
+// in two parts.  K and V are kept in L2 for the other row tiles (5 % slower without).
+//
+//  * One CTA an SM walks the items, so the next one's Q and K arrive during the last tiles.
+//  * K chunks and V halves share one ring of 16 KB slots, in the order in which they are needed.
+//  * P is handed over by halves; the second half and the next scores go out in one turn.
+//  * The softmax reference moves only when a maximum exceeds it by 2^8.
+//  * Values that are not finite are not looked for: an output row that is not, though its weights
+//    are, is computed again by itself (0 * NaN in a key that the row does not see).
+//  * Every wait is bounded (2 s); a timeout sets PA_DEV_TIMEOUT, and the roles wind down.
 #include "pa_mma.cuh"
 #include "pa_tc.cuh"
 

@@ -234,6 +234,25 @@ def test_shared_blocks(pa):
     assert pa.last_error() == 0
 
 
+def test_blocks_copied_and_swapped(pa):
+    """Copy-on-write and swap of a latent pool's blocks: two layers a call, or one pool as both."""
+    a, b = randn(1, 8, 16, 576), randn(2, 8, 16, 576)
+    pairs = torch.tensor([[1, 5], [3, 0]], device="cuda")
+    want_a, want_b = a.clone(), b.clone()
+    for src, dst in pairs.tolist():
+        want_a[dst], want_b[dst] = a[src], b[src]
+    view = lambda x: x.view(8, 16, 1, 576)                 # noqa: E731
+    pa.copy_blocks(view(a), view(b), pairs)
+    assert torch.equal(a, want_a) and torch.equal(b, want_b)
+    c, d = randn(3, 8, 16, 576), torch.zeros(8, 16, 576, dtype=torch.bfloat16, device="cuda")
+    want = c.clone()
+    want[5], want[0] = c[1], c[3]
+    pa.copy_blocks(view(c), view(c), pairs)
+    assert torch.equal(c, want)
+    pa.swap_blocks(view(d), view(d), view(c), view(c), pairs)
+    assert torch.equal(d[5], c[1]) and torch.equal(d[0], c[3]) and not d[1:5].any() and pa.last_error() == 0
+
+
 def test_a_run_of_steps(pa):
     """Prompts appended, then tokens one step at a time: rotate and append, attend; the cache rebuilt by hand."""
     import oracle
@@ -263,6 +282,14 @@ def test_a_run_of_steps(pa):
         turned = oracle.rope(f64(q[:, :, 128:]), at, freq, 1.0, "interleaved")
         assert np.abs(f64(full[:, :, R:]) - turned).max() <= np.abs(turned).max() * 2.0 ** -8 + 2.0 ** -18
         start = np.concatenate([[0], np.cumsum(new)])
+        if turn == 0:
+            # the prompts in the expanded form, their shared keys taken back from the cache
+            up = randn(99, R, H * 256, scale=R ** -0.5)
+            kv = (down[:, :R] @ up).view(n, H, 256)
+            key = cache.view(-1, R + P)[torch.tensor(where, device="cuda")][:, R:]
+            st = torch.tensor(start, dtype=torch.int32, device="cuda")
+            got = pa.latent_prefill(torch.empty(n, H, 128, dtype=q.dtype, device="cuda"), q, st, kv, key, st, 0.08)
+            check(got, *oracle.latent_prefill(f64(q), start, f64(kv), f64(key), start, 0.08))
         ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
         out = torch.empty(n, H, R, dtype=q.dtype, device="cuda")
         pa.latent_decode(out, full, cache, table, ln, 0.1, query_start=torch.tensor(start, dtype=torch.int32, device="cuda"))
