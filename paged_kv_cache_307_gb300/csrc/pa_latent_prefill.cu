@@ -198,7 +198,7 @@ __device__ __noinline__ void plain_row(const PrefillParams& p, int row, int h, i
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
   for (int e = 0; e * 32 < p.Dv; ++e)
-    p.out[((size_t)row * p.H + h) * p.Dv + e * 32 + lane] = __float2bfloat16_rn(o[e] / l);
+    p.out[((size_t)row * p.H + h) * p.Dv + e * 32 + lane] = __float2bfloat16_rn(l != 0.f ? o[e] / l : 0.f);
 }
 
 // f0 O of a warp's 32 rows, and f1 of the next chain's if there are two, as bf16 (zeros if there is

@@ -126,6 +126,20 @@ def test_nan_stays_with_the_rows_that_see_it(pa, H):
     check(got, w, m, s)
 
 
+@pytest.mark.parametrize("H", [2, 160])
+def test_rows_before_the_context_beside_a_nan(pa, H):
+    """More rows than context: the rows that see nothing are zeros, whatever the values hold."""
+    q, kv, key = randn(1, 140, H, 192), randn(2, 20, H, 256), randn(3, 20, 64)
+    kv[0, :, 130] = float("nan")
+    start, kv_start = [0, 140], [0, 20]
+    out = _run(pa, q, start, kv, key, kv_start, 0.07, 128)
+    assert not out[:120].any() and torch.isnan(out[120:, :, 2]).all()
+    w, m, s = oracle.latent_prefill(f64(q), start, f64(kv), f64(key), kv_start, 0.07)
+    keep = [d for d in range(128) if d != 2]
+    check(out[..., keep], w[..., keep], m[..., keep], s)
+    assert pa.last_error() == 0
+
+
 def test_two_calls_at_once(pa):
     """Calls on two streams share nothing."""
     a, b = _case([600, 90], [600, 40], 12, 128, 64, 128, seed=1), _case([333], [333], 40, 64, 32, 64, seed=2)
