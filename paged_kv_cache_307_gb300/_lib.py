@@ -619,7 +619,7 @@ _NO_TURN = (None, 0, 0, None, 0, 0, 0)
 
 def _angles(positions, steps, n, dev):
     """(pointer of the positions, pointer of the steps, rotary_dim)"""
-    if positions.dtype is not _I32 or positions.shape != (n,):
+    if positions.dtype is not _I32 or positions.dim() != 1 or positions.numel() != n:
         raise TypeError("positions is int32 [tokens]")
     if steps.dtype is not torch.int64 or steps.dim() != 1:
         raise TypeError("steps is the int64 table of rope_steps")
@@ -627,11 +627,11 @@ def _angles(positions, steps, n, dev):
         raise ValueError("tensors must be on the current CUDA device")
     if not (positions.is_contiguous() and steps.is_contiguous()):
         raise ValueError("tensors must be contiguous")
-    return positions.data_ptr(), steps.data_ptr(), 2 * len(steps)
+    return positions.data_ptr(), steps.data_ptr(), 2 * steps.numel()
 
 
 def _slots(slot_mapping, n, dev):
-    if slot_mapping.dtype is not torch.int64 or slot_mapping.shape != (n,):
+    if slot_mapping.dtype is not torch.int64 or slot_mapping.dim() != 1 or slot_mapping.numel() != n:
         raise TypeError("slot_mapping is int64 [tokens]")
     if slot_mapping.get_device() != dev or not slot_mapping.is_contiguous():
         raise ValueError("slot_mapping must be contiguous and on the current CUDA device")
@@ -695,9 +695,10 @@ def rope_and_cache(q, key, value, positions, slot_mapping, k_cache, v_cache, ste
 
 
 def _latent_pool(cache):
-    if cache.dim() != 3:
+    shape = cache.shape
+    if len(shape) != 3:
         raise ValueError("cache is [num_blocks, block_size, latent_dim + rope_dim]")
-    return cache.shape
+    return shape
 
 
 def latent_append(latent, key_rope, positions, slot_mapping, cache, steps, amplitude=1.0, layout="half", query=None,
@@ -740,11 +741,12 @@ def latent_decode(out, q, cache, block_tables, context_lens, scale, query_start=
     the last tokens of its context, causal."""
     NB, bs, width = _latent_pool(cache)
     B, cols = _table(block_tables, context_lens)
-    if q.dim() != 3 or out.dim() != 3 or q.size(2) != width or out.shape[:2] != q.shape[:2] or not (
-            q.dtype is cache.dtype and out.dtype is cache.dtype):
+    qs, shape, dtype = q.shape, out.shape, cache.dtype
+    if len(qs) != 3 or len(shape) != 3 or qs[2] != width or shape[0] != qs[0] or shape[1] != qs[1] or not (
+            q.dtype is dtype and out.dtype is dtype):
         raise ValueError("q is [rows, num_heads, latent_dim + rope_dim], out [rows, num_heads, latent_dim], of the "
                          "cache's type")
-    rows, H, R = out.shape
+    rows, H, R = shape
     kind = _float_kind(q)
     start = None
     if query_start is not None:
