@@ -273,6 +273,13 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
   volatile int* abort_flag = &sh->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  if (warp == 8 && lane == 0) {
+    prefetch_tensormap(&mapQ);
+    prefetch_tensormap(&mapQr);
+    prefetch_tensormap(&mapK);
+    prefetch_tensormap(&mapKr);
+    prefetch_tensormap(&mapV);
+  }
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < p.B; b += kThreads)
       if (rows_of(p, b) < 0) atomicOr(&g_status_latent, PA_DEV_BAD_LEN);
