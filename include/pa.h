@@ -716,7 +716,8 @@ int pa_rope_steps(uint64_t* steps, float* amplitude, int rotary_dim, double base
  *   steps        device copy of the table of pa_rope_steps
  *   dtype        PA_F32 or PA_BF16; products in fp32, rounded once
  *
- * Pointers and strides are multiples of 16 bytes (PA_ERR_ALIGN).
+ * Pointers and strides are multiples of 16 bytes (PA_ERR_ALIGN); a token has at
+ * most 2^28 bytes to move (PA_ERR_SHAPE).
  */
 int pa_rope(void* q_out, long long q_out_token_stride, long long q_out_head_stride,
             const void* q, long long q_token_stride, long long q_head_stride, int num_heads,

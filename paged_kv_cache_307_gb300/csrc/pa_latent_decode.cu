@@ -51,6 +51,7 @@ constexpr uint32_t kChunk = 16384;           // 128 tokens x 64 elements
 constexpr uint32_t kPair = 2 * kChunk;       // 128 elements: one M = 128 product of O^T
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;                // log2 units a score may exceed its reference by
+constexpr float kUnset = 3e38f;              // minus a reference that is not there yet
 constexpr uint32_t kSmemMax = 232448;        // 227 KB
 constexpr int kMaxSlots = 6;
 
@@ -605,8 +606,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
             const float old = j > 0 ? -sh->neg_m[c] : -INFINITY;
             const float m = fmaxf(old, y);
             sh->f[c] = old == -INFINITY ? 0.f : exp2f(old - m);
-            // (a row that sees nothing of its first tile sees nothing of the later ones)
-            sh->neg_m[c] = m == -INFINITY ? 0.f : -m;
+            // No reference yet (nothing seen, or scores of -inf alone): one that every finite score exceeds.
+            sh->neg_m[c] = m == -INFINITY ? kUnset : -m;
           }
           named_sync(1, kSoft);
           exponents();

@@ -110,6 +110,25 @@ def test_nan_values_stay_with_the_rows_that_see_them(pa):
     assert pa.last_error() == 0
 
 
+@pytest.mark.parametrize("H", [16, 128])
+def test_tokens_of_no_weight_before_low_scores(pa, H):
+    """Scores of -inf in whole tiles at the start, then scores far below zero: as if the context began there."""
+    B = 200                                               # (of one context: several tiles for every CTA)
+    for L, hidden in ((300, 128), (700, 384), (150, 144)):
+        c = Cache([L], 256, 32, 16, scale=0.5)
+        q = randn(H, 1, H, 288)
+        q[:, :, 280], q[:, :, 281] = 8.0, 1.0
+        ids = c.table[0].long()
+        c.cache[ids, :, 280] = -50.0                      # every score 400 lower
+        c.cache[ids[:hidden // 16], :, 281] = -float("inf")
+        rest = Cache([1], 256, 32, 16)
+        rest.cache, rest.table, rest.lens = c.cache, c.table[:, hidden // 16:], c.lens - hidden
+        want = rest.oracle(q, 1.0)
+        c.table, c.lens = c.table.repeat(B, 1), c.lens.repeat(B)
+        check(_run(pa, c, q.repeat(B, 1, 1), 1.0), *(x.repeat(B, 0) for x in want))
+    assert pa.last_error() == 0
+
+
 @pytest.mark.parametrize("H,lens", [(16, [20000]), (128, [9000, 30]), (40, [5000, 128, 0, 129, 7777])])
 def test_long_sequences_cut_among_many(pa, H, lens):
     """Many CTAs a sequence, cuts at and inside tiles."""

@@ -140,6 +140,18 @@ def test_rows_before_the_context_beside_a_nan(pa, H):
     assert pa.last_error() == 0
 
 
+@pytest.mark.parametrize("H", [2, 160])
+def test_tokens_of_no_weight_before_low_scores(pa, H):
+    """Scores of -inf in whole tiles at the start, then scores far below zero: as if the context began there."""
+    for L, hidden, n in ((300, 128, 140), (700, 384, 260), (150, 140, 5)):
+        q, start, kv, key, kv_start, _ = _case([L], [n], H, 128, 32, 64, seed=L)
+        q[:, :, 150], q[:, :, 151] = 8.0, 1.0
+        key[:, 22], key[:hidden, 23] = -50.0, -float("inf")   # every score 400 lower
+        want = _want(q, start, kv[hidden:], key[hidden:], [0, L - hidden], 0.5)
+        check(_run(pa, q, start, kv, key, kv_start, 0.5, 64), *want)
+    assert pa.last_error() == 0
+
+
 def test_two_calls_at_once(pa):
     """Calls on two streams share nothing."""
     a, b = _case([600, 90], [600, 40], 12, 128, 64, 128, seed=1), _case([333], [333], 40, 64, 32, 64, seed=2)
