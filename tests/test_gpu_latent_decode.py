@@ -110,6 +110,23 @@ def test_nan_values_stay_with_the_rows_that_see_them(pa):
     assert pa.last_error() == 0
 
 
+@pytest.mark.parametrize("R,P", [(512, 64), (384, 16), (256, 48), (128, 32)])
+@pytest.mark.parametrize("H,n,L", [(16, 1, 1500), (24, 1, 900), (64, 1, 1100), (128, 1, 700), (5, 3, 1000), (40, 4, 770)])
+def test_many_tiles_a_cta(pa, R, P, H, n, L):
+    """160 sequences over one context, whose maxima move in every tile: each is done by a CTA or two."""
+    B = 160
+    c = Cache([L], R, P, 16, seed=n)
+    for j in range(-(-L // 16)):
+        c.cache[int(c.table[0, j])] *= 1.0 + j / 16
+    q = randn(H, n, H, R + P)
+    scale = 0.5 * (R + P) ** -0.5
+    want = c.oracle(q, scale, [0, n])
+    c.table, c.lens = c.table.repeat(B, 1), c.lens.repeat(B)
+    start = None if n == 1 else np.arange(B + 1) * n
+    check(_run(pa, c, q.repeat(B, 1, 1), scale, start), *(np.tile(x, (B,) + (1,) * (x.ndim - 1)) for x in want))
+    assert pa.last_error() == 0
+
+
 @pytest.mark.parametrize("H", [16, 128])
 def test_tokens_of_no_weight_before_low_scores(pa, H):
     """Scores of -inf in whole tiles at the start, then scores far below zero: as if the context began there."""
