@@ -60,9 +60,9 @@ struct LatentParams {
   const int32_t* query_start;                // null: one row a sequence
   const int32_t* block_tables;
   const int32_t* context_lens;
-  float* ws_o;                               // [2 * CTAs, NR, R] partial sums
+  float* ws_o;                               // [2 * CTAs, R / 128, NR / 4, 128, 4] partial sums
   float* ws_ml;                              // [2 * CTAs, NR, 2] their maximum and sum
-  int4* ws_join;                             // [2 * CTAs] what the slot begins: first row, rows, slots that go on with it
+  int4* ws_join;                             // [CTAs] what the CTA begins and others go on with: first row, rows, those others, its slot
   int B, H, R, P, rows, max_blocks, bs, num_blocks;
   int cl;                                    // CTAs that take neighbouring row groups over the same tokens
   float qscale;
@@ -356,8 +356,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
     walk.at = u0;
     walk.cuts = cuts;
     walk.first = true;
-    // what neither of the CTA's slots begins stays at 0
-    if (threadIdx.x < 2) p.ws_join[blockIdx.x * 2 + threadIdx.x] = make_int4(0, 0, 0, 0);
+    // (what stays where the CTA begins nothing that goes on)
+    if (threadIdx.x == 0) p.ws_join[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
   const uint32_t tmem = sh->tmem_base;
   const uint32_t tO = tmem + 2 * NR;
@@ -654,19 +654,23 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
 #pragma unroll 1
           for (int i = 0; i < NP; ++i) {
             unsigned char* at = smem + Lay::kOffRing + ((kt * NP + i) % SLOTS) * kPair + r * 128;
+            auto piece = [&](int k) {        // (another one in each row of eight)
+              k += sub * (16 / SUB);
+              return reinterpret_cast<uint4*>(at + (k >> 3) * kChunk + (((k + r) & 7) << 4));
+            };
+            if (drop) {
+#pragma unroll
+              for (int k = 0; k < 16 / SUB; ++k) *piece(k) = make_uint4(0u, 0u, 0u, 0u);
+            } else {
 #pragma unroll 1
-            for (int k = sub * (16 / SUB); k < (sub + 1) * (16 / SUB); ++k) {
-              uint4* q = reinterpret_cast<uint4*>(at + (k >> 3) * kChunk + (((k + r) & 7) << 4));   // (another piece in each row of eight)
-              if (drop) {
-                *q = make_uint4(0u, 0u, 0u, 0u);
-              } else {
-                const uint4 v = *q;
+              for (int k = 0; k < 16 / SUB; ++k) {
+                const uint4 v = *piece(k);
                 auto clean = [](uint32_t y) {
                   if ((y & 0x7f80u) == 0x7f80u) y &= 0xffff0000u;
                   if ((y & 0x7f800000u) == 0x7f800000u) y &= 0xffffu;
                   return y;
                 };
-                *q = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+                *piece(k) = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
               }
             }
           }
@@ -693,8 +697,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
       }
       named_sync(1, kSoft);
       if (!it.whole && it.tile == 0 && threadIdx.x == 0) {
-        // the CTAs after this one, as far as the group goes
-        p.ws_join[it.slot] = make_int4(it.q0 * p.H + it.r0, it.rows, walk.cuts.part_of(it.unit + it.tiles - 1) - part, 0);
+        // the CTAs after this one, as far as the group goes (it is the CTA's last: there is one at most)
+        p.ws_join[blockIdx.x] = make_int4(it.q0 * p.H + it.r0, it.rows, walk.cuts.part_of(it.unit + it.tiles - 1) - part, it.slot & 1);
       }
       if (threadIdx.x < NR) {
         const int c = (int)threadIdx.x;
@@ -721,18 +725,49 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
           tmem_load(tO + i * NR + c0 + lane_off, v);
           tmem_ld_wait();
         }
-        const int d = i * 128 + r;
         if (it.whole) {
-          __nv_bfloat16* o = p.out + ((size_t)it.q0 * p.H + it.r0 + c0) * R + d;
+          // 8 columns of 8 lanes' dims change places, and a lane writes 8 dims of a column
+          const bool up1 = lane & 1, up2 = lane & 2, up4 = lane & 4;
+          const int col = c0 + (up1 ? 4 : 0) + (up2 ? 2 : 0) + (up4 ? 1 : 0);
+          __nv_bfloat16* o = p.out + ((size_t)it.q0 * p.H + it.r0 + col) * R + i * 128 + (r & ~7);
 #pragma unroll
-          for (int c = 0; c < CW; ++c)
-            if (c0 + c < it.rows)
-              o[(size_t)c * R] = __float2bfloat16_rn(it.nt > 0 ? __uint_as_float(v[c]) * sh->f[c0 + c] : 0.f);
+          for (int g = 0; g < CW; g += 8) {
+            uint32_t w[4], x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 fk = *reinterpret_cast<const float2*>(&sh->f[c0 + g + 2 * k]);
+              w[k] = it.nt > 0 ? pack_bf16(__uint_as_float(v[g + 2 * k]) * fk.x, __uint_as_float(v[g + 2 * k + 1]) * fk.y) : 0u;
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {      // two dims of columns 2k, 2k + 1
+              const uint32_t mine = up1 ? w[2 + k] : w[k];
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, up1 ? w[k] : w[2 + k], 1);
+              const uint32_t lo = up1 ? got : mine, hi = up1 ? mine : got;
+              x[2 * k] = __byte_perm(lo, hi, 0x5410);
+              x[2 * k + 1] = __byte_perm(lo, hi, 0x7632);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {      // four dims of column k
+              const uint32_t mine = up2 ? x[2 + k] : x[k];
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, up2 ? x[k] : x[2 + k], 2);
+              w[2 * k] = up2 ? got : mine;
+              w[2 * k + 1] = up2 ? mine : got;
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {      // eight
+              const uint32_t mine = up4 ? w[2 + k] : w[k];
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, up4 ? w[k] : w[2 + k], 4);
+              x[k] = up4 ? got : mine;
+              x[2 + k] = up4 ? mine : got;
+            }
+            if (col + g < it.rows) st_v4(o + (size_t)g * R, make_uint4(x[0], x[1], x[2], x[3]));
+          }
         } else if (it.nt > 0) {
-          float* o = p.ws_o + ((size_t)it.slot * NR + c0) * R + d;
+          // four columns of a dim side by side, as the join takes them
+          uint4* o = reinterpret_cast<uint4*>(p.ws_o) + (((size_t)it.slot * NP + i) * (NR / 4) + c0 / 4) * 128 + r;
 #pragma unroll
-          for (int c = 0; c < CW; ++c)
-            if (c0 + c < it.rows) o[(size_t)c * R] = __uint_as_float(v[c]);
+          for (int c = 0; c < CW; c += 4)
+            if (c0 + c < it.rows) o[(c / 4) * 128] = make_uint4(v[c], v[c + 1], v[c + 2], v[c + 3]);
         }
       }
       if (it.nt > 0) {
@@ -749,52 +784,78 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
   if (warp == kMma) tmem_dealloc(tmem, Lay::kTmem);
 }
 
-// Joins the row groups that a cut left in several CTAs.  grid (slots, NR / 8): a warp per row of the
-// group that the slot begins, if it begins one.
+// Joins the row groups that a cut left in several CTAs.  grid (CTAs, blocks of 8 warps): a warp takes
+// four rows x 128 dims of the group that the CTA begins, if it begins one.  Bound by latency: what the
+// CTA began, then maxima and sums together, four parts ahead (two: 11 drafts of 32 heads 25.5 us for
+// 23.9 with the kernel before; a row a warp, one part after the other: 2 short contexts 12.7 for 10.9).
 template <int NR, int RC>
 __global__ void __launch_bounds__(256) latent_join_kernel(const LatentParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int R = RC * 64, kPer = R / 128;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int R = RC * 64, NP = RC / 2;
+  const int lane = threadIdx.x & 31;
   const int4 j = p.ws_join[blockIdx.x];
-  const int c = blockIdx.y * 8 + warp;
+  const int u = blockIdx.y * 8 + (threadIdx.x >> 5), c = u / NP * 4, piece = u % NP;
   if (c >= j.y) return;
-  const int more = j.z;                      // the group goes on in the first slots of so many CTAs of its kind
-  const int cta = blockIdx.x >> 1;
-  auto slot_of = [&](int q) -> size_t {
-    return (size_t)(q == 0 ? (int)blockIdx.x : (cta + q * p.cl) * 2) * NR + c;
+  const int parts = j.z + 1;                 // the CTA's slot, and the first slots of so many CTAs of its kind
+  auto slot_of = [&](int q) -> size_t { return (size_t)(q == 0 ? (int)blockIdx.x * 2 + j.w : ((int)blockIdx.x + q * p.cl) * 2); };
+  const float4* src = reinterpret_cast<const float4*>(p.ws_o) + ((size_t)piece * (NR / 4) + c / 4) * 128 + lane * 2;
+  // (a part whose rows saw nothing has no sums: they are read and not used)
+  float4 x[4][4];
+  auto fetch = [&](int q0) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (q0 + q >= parts) break;
+      const float4* s = src + slot_of(q0 + q) * (NP * (NR / 4) * 128);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) x[q][d] = s[(d >> 1) * 64 + (d & 1)];
+    }
   };
+  fetch(0);
+  // maxima and sums: lane = (part, row)
+  const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + c + (lane & 3);
   float m = -INFINITY;
-  for (int q = lane; q <= more; q += 32) m = fmaxf(m, p.ws_ml[slot_of(q) * 2]);
+  for (int q = lane >> 2; q < parts; q += 8) m = fmaxf(m, ml[slot_of(q) * NR].x);
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  float l = 0.f;
-  float4 o[kPer];
+  for (int off = 16; off > 2; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  float l = 0.f, w = 0.f, o[4][4] = {};
+  uint32_t live = 0;
+  for (int q0 = 0; q0 < parts; q0 += 4) {
+    if ((q0 & 7) == 0) {
+      const int mine = q0 + (lane >> 2);
+      float2 y = make_float2(-INFINITY, 0.f);
+      if (mine < parts) y = ml[slot_of(mine) * NR];
+      live = __ballot_sync(0xffffffffu, y.x != -INFINITY);
+      w = y.x != -INFINITY ? exp2f(y.x - m) : 0.f;
+      if (y.x != -INFINITY) l = fmaf(y.y, w, l);
+    }
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int q = 0; q <= more; ++q) {
-    const size_t at = slot_of(q);
-    const float mq = p.ws_ml[at * 2], lq = p.ws_ml[at * 2 + 1];
-    if (mq == -INFINITY) continue;
-    float4 x[kPer];
+    for (int q = 0; q < 4; ++q) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) x[i] = *reinterpret_cast<const float4*>(p.ws_o + at * R + i * 128 + lane * 4);
-    const float w = exp2f(mq - m);
-    l = fmaf(lq, w, l);
+      for (int k = 0; k < 4; ++k) {
+        const int from = ((q0 & 7) + q) * 4 + k;
+        const float wk = __shfl_sync(0xffffffffu, w, from);
+        if (!((live >> from) & 1u)) continue;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      o[i].x = fmaf(x[i].x, w, o[i].x);
-      o[i].y = fmaf(x[i].y, w, o[i].y);
-      o[i].z = fmaf(x[i].z, w, o[i].z);
-      o[i].w = fmaf(x[i].w, w, o[i].w);
+        for (int d = 0; d < 4; ++d) {
+          const float4 y = x[q][d];
+          o[d][k] = fmaf(k == 0 ? y.x : k == 1 ? y.y : k == 2 ? y.z : y.w, wk, o[d][k]);
+        }
+      }
+    }
+    fetch(q0 + 4);
+  }
+#pragma unroll
+  for (int off = 16; off > 2; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  __nv_bfloat16* out = p.out + ((size_t)j.x + c) * R + piece * 128 + lane * 2;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float f = __shfl_sync(0xffffffffu, inv, k);
+    if (c + k < j.y) {
+      *reinterpret_cast<uint32_t*>(out + k * R) = pack_bf16(o[0][k] * f, o[1][k] * f);
+      *reinterpret_cast<uint32_t*>(out + k * R + 64) = pack_bf16(o[2][k] * f, o[3][k] * f);
     }
   }
-  const float inv = l != 0.f ? 1.f / l : 0.f;
-  __nv_bfloat16* out = p.out + ((size_t)j.x + c) * R;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    *reinterpret_cast<uint2*>(out + i * 128 + lane * 4) =
-        make_uint2(pack_bf16(o[i].x * inv, o[i].y * inv), pack_bf16(o[i].z * inv, o[i].w * inv));
 }
 
 bool good_sizes(int total, int num_seqs, int num_heads, int latent_dim, int max_blocks, int bs) {
@@ -818,7 +879,7 @@ Plan plan_of(int total, int num_seqs, int num_heads, int latent_dim) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   w.ml = up(slots * w.nr * latent_dim * 4);
   w.join = w.ml + up(slots * w.nr * 8);
-  w.bytes = w.join + up(slots * 16);
+  w.bytes = w.join + up((size_t)w.parts * w.cl * 16);
   return w;
 }
 
@@ -912,7 +973,7 @@ extern "C" int pa_latent_decode(void* out, const void* query, const int32_t* que
     return PA_ERR_CUDA;
   if ((long long)max_blocks_per_seq * block_size <= kTile) return PA_OK;    // a tile a row group: nothing is cut
   void* join[] = {&p};
-  return ck(launch_after(k.join, dim3(2 * ctas, (unsigned)w.nr / 8), dim3(256), join, (cudaStream_t)stream),
+  return ck(launch_after(k.join, dim3(ctas, (unsigned)(w.nr / 4 * latent_dim / 128 + 7) / 8), dim3(256), join, (cudaStream_t)stream),
             "cudaLaunchKernel(latent_join_kernel)")
              ? PA_OK
              : PA_ERR_CUDA;
