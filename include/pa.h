@@ -796,7 +796,9 @@ int pa_latent_append(const void* latent, long long latent_stride, const void* ke
  *
  * A context length outside its table row is clamped and sets PA_DEV_BAD_LEN, a
  * block id outside the pool is read as block 0 and sets PA_DEV_BAD_BLOCK.  A
- * table row holds at most 2^30 tokens, total_queries * num_heads < 2^31.
+ * table row holds at most 2^30 tokens, total_queries * num_heads < 2^31, and
+ * (total_queries * num_heads / 16 + num_seqs) * (a table row's tiles of 128
+ * tokens) < 2^31 (PA_ERR_SHAPE).
  * Accumulation is fp32; the softmax weights are rounded to bf16 for their
  * product with the values.  A cached row that holds a NaN makes NaN of the rows
  * that see it, whole; the rows before it are not touched.

@@ -75,8 +75,9 @@ struct Shared {
   alignas(16) float neg_m[NR];               // minus the reference of every row
   alignas(16) float f[NR];
   alignas(16) float red[4][NR];              // per warp: maxima, at the end sums
-  long long scan[threads(NR) / 32];
-  long long first_off;
+  alignas(16) uint4 turn[4 * subs(NR)][32];  // per warp: 8 columns of 32 dims on their way out
+  int scan[threads(NR) / 32];
+  unsigned first_off;
   int first_b;
   uint32_t tmem_base;
   int abort;
@@ -153,28 +154,24 @@ __device__ __forceinline__ Seq seq_of(const LatentParams& p, int b, bool flag) {
   s.tiles = max(1, (s.L + kTile - 1) / kTile);
   return s;
 }
-__device__ __forceinline__ int groups_of(const LatentParams& p, const Seq& s, int nr) { return (s.n * p.H + nr - 1) / nr; }
-
-// x / y for what mostly fits 32 bits.
-__device__ __forceinline__ long long quotient(long long x, long long y) {
-  if (((x | y) >> 31) == 0) return (long long)((unsigned)x / (unsigned)y);
-  return x / y;
+__device__ __forceinline__ int supers_of(const LatentParams& p, const Seq& s, int nr) {
+  return ((s.n * p.H + nr - 1) / nr + p.cl - 1) >> (p.cl - 1);               // (cl is 1 or 2)
 }
+
 // The line of `total` units in at most `parts` parts, none of them empty: the first `longer` of
-// `len` + 1 units, the rest of `len`.
+// `len` + 1 units, the rest of `len`.  (The host refuses what could be 2^31 units.)
 struct Cuts {
-  long long len, longer;
-  int n;
+  unsigned len, longer, n;
   Cuts() = default;
-  __device__ __forceinline__ Cuts(long long total, int parts) {
-    n = (int)min((long long)parts, total);
-    len = n > 0 ? quotient(total, n) : 0;
+  __device__ __forceinline__ Cuts(unsigned total, unsigned parts) {
+    n = min(parts, total);
+    len = n > 0 ? total / n : 0;
     longer = total - len * n;
   }
-  __device__ __forceinline__ long long begin(int part) const { return len * min(part, n) + min((long long)min(part, n), longer); }
-  __device__ __forceinline__ int part_of(long long unit) const {
-    const long long first = longer * (len + 1);
-    return (int)(unit < first ? quotient(unit, len + 1) : longer + quotient(unit - first, len));
+  __device__ __forceinline__ unsigned begin(unsigned part) const { return len * min(part, n) + min(min(part, n), longer); }
+  __device__ __forceinline__ int part_of(unsigned unit) const {
+    const unsigned first = longer * (len + 1);
+    return (int)(unit < first ? unit / (len + 1) : longer + (unit - first) / len);
   }
 };
 
@@ -184,7 +181,7 @@ struct Cuts {
 struct Item {
   int b, r0, rows;                           // row group: first row of the sequence's, rows of it
   int tile, nt, tiles;                       // first tile, tiles with something to see, tiles of the whole group
-  long long unit;                            // the first tile's place in the line
+  unsigned unit;                             // the first tile's place in the line
   int end, L, n, q0;                         // tokens that any of its rows sees
   bool whole;
   int slot;
@@ -192,21 +189,21 @@ struct Item {
 template <int NR>
 struct Walk {
   int b, half, part;
-  long long off, left, at;
+  unsigned off, left, at;
   Cuts cuts;
   bool first;
   __device__ __forceinline__ bool next(const LatentParams& p, Item& it) {
-    while (left > 0) {
+    while (left > 0 && b < p.B) {            // (starts that go back and forth may name more than 2^31 units)
       const Seq s = seq_of(p, b, false);
-      const int supers = (groups_of(p, s, NR) + p.cl - 1) / p.cl;
-      if (off >= (long long)supers * s.tiles) {
+      const unsigned supers = supers_of(p, s, NR);
+      if (off >= supers * s.tiles) {
         ++b;
         off = 0;
         continue;
       }
-      const int sg = (int)quotient(off, s.tiles);
-      const int t = (int)(off - (long long)sg * s.tiles);
-      const int cnt = (int)min((long long)(s.tiles - t), left);
+      const unsigned sg = off < (unsigned)s.tiles ? 0u : off / (unsigned)s.tiles;
+      const int t = (int)(off - sg * s.tiles);
+      const int cnt = (int)min((unsigned)(s.tiles - t), left);
       it.unit = at;
       off += cnt;
       left -= cnt;
@@ -214,10 +211,10 @@ struct Walk {
       const bool was_first = first;
       first = false;
       it.b = b;
-      it.r0 = (sg * p.cl + half) * NR;
+      it.r0 = ((int)sg * p.cl + half) * NR;
       it.rows = min(NR, s.n * p.H - it.r0);
       if (it.rows <= 0) continue;
-      it.end = min(s.L, max(0, s.L - s.n + (it.r0 + it.rows - 1) / p.H + 1));
+      it.end = s.n == 1 ? s.L : min(s.L, max(0, s.L - s.n + (int)((unsigned)(it.r0 + it.rows - 1) / (unsigned)p.H) + 1));
       it.tile = t;
       it.tiles = s.tiles;
       it.nt = max(0, min(t + cnt, (it.end + kTile - 1) / kTile) - t);
@@ -302,56 +299,50 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
   }
 
   // ---- this CTA's part of the line
-  const int parts = gridDim.x / p.cl, part = blockIdx.x / p.cl;
+  const int parts = gridDim.x >> (p.cl - 1), part = blockIdx.x >> (p.cl - 1);
   Walk<NR> walk;
   {
-    const int per = (p.B + kThreads - 1) / kThreads;
+    const int per = p.B <= kThreads ? 1 : (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
     const bool note = blockIdx.x == 0;
-    long long sum = 0;
+    int sum = 0;
     for (int b = b0; b < b1; ++b) {
       const Seq s = seq_of(p, b, note);
-      sum += (long long)((groups_of(p, s, NR) + p.cl - 1) / p.cl) * s.tiles;
+      sum += supers_of(p, s, NR) * s.tiles;
     }
-    long long incl = sum;
+    int incl = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+      const int y = __shfl_up_sync(0xffffffffu, incl, off);
       if (lane >= off) incl += y;
     }
     if (lane == 31) sh->scan[warp] = incl;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    long long total = 0, before = incl - sum;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      total += sh->scan[w];
-      if (w < warp) before += sh->scan[w];
-    }
+    const int mine = lane < kThreads / 32 ? sh->scan[lane] : 0;
+    const int total = __reduce_add_sync(0xffffffffu, mine);
+    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0) + incl - sum;
     // (no empty parts: a line shorter than the grid leaves its last CTAs without work)
     const Cuts cuts(total, parts);
-    const long long u0 = cuts.begin(part), u1 = cuts.begin(part + 1);
-    if (u0 >= before && u0 < before + sum) {     // (one thread, where there is anything)
-      long long at = before;
-      if (b1 - b0 == 1) {
-        sh->first_b = b0;
-        sh->first_off = u0 - before;
-      } else for (int b = b0; b < b1; ++b) {
+    const unsigned u0 = cuts.begin(part), u1 = cuts.begin(part + 1);
+    if (u0 - (unsigned)before < (unsigned)sum) {     // (one thread, where there is anything)
+      unsigned off = u0 - (unsigned)before;
+      int b = b0;
+      for (; b + 1 < b1; ++b) {
         const Seq s = seq_of(p, b, false);
-        const long long u = (long long)((groups_of(p, s, NR) + p.cl - 1) / p.cl) * s.tiles;
-        if (u0 < at + u) {
-          sh->first_b = b;
-          sh->first_off = u0 - at;
-          break;
-        }
-        at += u;
+        const unsigned u = (unsigned)(supers_of(p, s, NR) * s.tiles);
+        if (off < u) break;
+        off -= u;
       }
+      sh->first_b = b;
+      sh->first_off = off;
     }
     __syncthreads();
     walk.b = sh->first_b;
     walk.off = sh->first_off;
     walk.left = walk.b < p.B ? u1 - u0 : 0;
-    walk.half = blockIdx.x % p.cl;
+    walk.half = blockIdx.x & (p.cl - 1);
     walk.part = part;
     walk.at = u0;
     walk.cuts = cuts;
@@ -387,12 +378,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
       int blk = id_of(0);
       ok = __all_sync(0xffffffffu, wait(&sh->q_empty, (uint32_t)(kq & 1) ^ 1u, abort_flag));
       if (!ok) break;
-      if (w == 0) {
-        if (lane == 0) mbar_arrive_expect_tx(&sh->q_full, (uint32_t)NC * NR * 128u);
-        __syncwarp();
-        if (lane < NC)
-          tma_load_4d(smem + lane * NR * 128, &mapQ, &sh->q_full, lane * 64, it.q0 * p.H + it.r0, 0, 0, pol);
-      }
+      if (w == 0 && lane == 0) mbar_arrive_expect_tx(&sh->q_full, (uint32_t)NC * NR * 128u);
+      __syncwarp();
+      if (copy < NC) tma_load_4d(smem + copy * NR * 128, &mapQ, &sh->q_full, copy * 64, it.q0 * p.H + it.r0, 0, 0, pol);
       ++kq;
       for (int j = 0; j < it.nt; ++j) {
         const int next = id_of(j + 1);
@@ -698,7 +686,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
       named_sync(1, kSoft);
       if (!it.whole && it.tile == 0 && threadIdx.x == 0) {
         // the CTAs after this one, as far as the group goes (it is the CTA's last: there is one at most)
-        p.ws_join[blockIdx.x] = make_int4(it.q0 * p.H + it.r0, it.rows, walk.cuts.part_of(it.unit + it.tiles - 1) - part, it.slot & 1);
+        p.ws_join[blockIdx.x] = make_int4(it.q0 * p.H + it.r0, it.rows, max(0, min(walk.cuts.part_of(it.unit + it.tiles - 1), parts - 1) - part),
+                                          it.slot & 1);
       }
       if (threadIdx.x < NR) {
         const int c = (int)threadIdx.x;
@@ -713,54 +702,40 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
       }
       named_sync(1, kSoft);
       const int R = RC * 64;
-      if (it.nt > 0) {
-        wait(&sh->pv, (uint32_t)(kt - 1) & 1u, abort_flag);
-        __syncwarp();
-        tc_fence_after();
-      }
 #pragma unroll 1
       for (int i = 0; i < NP; ++i) {
         uint32_t v[CW];
         if (it.nt > 0) {
+          // the last tile's values have left their slot: these dims are done
+          const int u = (kt - 1) * NP + i;
+          wait(&sh->empty[u % SLOTS], (uint32_t)(u / SLOTS) & 1u, abort_flag);
+          __syncwarp();
+          tc_fence_after();
           tmem_load(tO + i * NR + c0 + lane_off, v);
           tmem_ld_wait();
         }
         if (it.whole) {
-          // 8 columns of 8 lanes' dims change places, and a lane writes 8 dims of a column
-          const bool up1 = lane & 1, up2 = lane & 2, up4 = lane & 4;
-          const int col = c0 + (up1 ? 4 : 0) + (up2 ? 2 : 0) + (up4 ? 1 : 0);
-          __nv_bfloat16* o = p.out + ((size_t)it.q0 * p.H + it.r0 + col) * R + i * 128 + (r & ~7);
+          // Lanes hold a dim of 8 columns and write 8 dims of one: matrix k of the transposition is dims
+          // 8 x + 2 k + {0, 1} of every x.  (By shuffles the row group took 5700 clocks and not ...)
+          const int dim = ((lane & 6) << 2) + ((lane >> 3) << 1) + (lane & 1);
+          const int col = c0 + (lane >> 2);
+          __nv_bfloat16* o = p.out + ((size_t)it.q0 * p.H + it.r0 + col) * R + i * 128 + (warp & 3) * 32 + (lane & 3) * 8;
 #pragma unroll
           for (int g = 0; g < CW; g += 8) {
-            uint32_t w[4], x[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 fk = *reinterpret_cast<const float2*>(&sh->f[c0 + g + 2 * k]);
-              w[k] = it.nt > 0 ? pack_bf16(__uint_as_float(v[g + 2 * k]) * fk.x, __uint_as_float(v[g + 2 * k + 1]) * fk.y) : 0u;
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {      // two dims of columns 2k, 2k + 1
-              const uint32_t mine = up1 ? w[2 + k] : w[k];
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, up1 ? w[k] : w[2 + k], 1);
-              const uint32_t lo = up1 ? got : mine, hi = up1 ? mine : got;
-              x[2 * k] = __byte_perm(lo, hi, 0x5410);
-              x[2 * k + 1] = __byte_perm(lo, hi, 0x7632);
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {      // four dims of column k
-              const uint32_t mine = up2 ? x[2 + k] : x[k];
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, up2 ? x[k] : x[2 + k], 2);
-              w[2 * k] = up2 ? got : mine;
-              w[2 * k + 1] = up2 ? mine : got;
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {      // eight
-              const uint32_t mine = up4 ? w[2 + k] : w[k];
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, up4 ? w[k] : w[2 + k], 4);
-              x[k] = up4 ? got : mine;
-              x[2 + k] = up4 ? mine : got;
-            }
-            if (col + g < it.rows) st_v4(o + (size_t)g * R, make_uint4(x[0], x[1], x[2], x[3]));
+            const float4 f0 = *reinterpret_cast<const float4*>(&sh->f[c0 + g]);
+            const float4 f1 = *reinterpret_cast<const float4*>(&sh->f[c0 + g + 4]);
+            uint4 y = make_uint4(0u, 0u, 0u, 0u);
+            if (it.nt > 0)
+              y = make_uint4(pack_bf16(__uint_as_float(v[g]) * f0.x, __uint_as_float(v[g + 1]) * f0.y),
+                             pack_bf16(__uint_as_float(v[g + 2]) * f0.z, __uint_as_float(v[g + 3]) * f0.w),
+                             pack_bf16(__uint_as_float(v[g + 4]) * f1.x, __uint_as_float(v[g + 5]) * f1.y),
+                             pack_bf16(__uint_as_float(v[g + 6]) * f1.z, __uint_as_float(v[g + 7]) * f1.w));
+            sh->turn[warp][lane] = y;
+            __syncwarp();
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "r"(smem_u32(&sh->turn[warp][dim])) : "memory");
+            __syncwarp();
+            if (col + g < it.rows) st_v4(o + (size_t)g * R, y);
           }
         } else if (it.nt > 0) {
           // four columns of a dim side by side, as the join takes them
@@ -879,7 +854,7 @@ Plan plan_of(int total, int num_seqs, int num_heads, int latent_dim) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   w.ml = up(slots * w.nr * latent_dim * 4);
   w.join = w.ml + up(slots * w.nr * 8);
-  w.bytes = w.join + up((size_t)w.parts * w.cl * 16);
+  w.bytes = w.join + up(slots * 16);
   return w;
 }
 
@@ -921,6 +896,9 @@ extern "C" int pa_latent_decode(void* out, const void* query, const int32_t* que
   if (!out || !query || !cache || !block_tables || !context_lens) return PA_ERR_NULL;
   if (!aligned16(out) || !aligned16(query) || !aligned16(cache) || !aligned16(workspace)) return PA_ERR_ALIGN;
   const Plan w = plan_of(total_queries, num_seqs, num_heads, latent_dim);
+  // units of (row groups, tile): 31 bits
+  if (((long long)total_queries * num_heads / w.nr + num_seqs) * (((long long)max_blocks_per_seq * block_size + kTile - 1) / kTile) > 0x7fffffffll)
+    return PA_ERR_SHAPE;
   if (!workspace || workspace_bytes < w.bytes) return PA_ERR_WORKSPACE;
   CUtensorMap mapC, mapQ;
   const uint64_t width = (uint64_t)latent_dim + rope_dim;
