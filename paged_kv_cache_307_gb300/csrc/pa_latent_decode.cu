@@ -10,14 +10,17 @@
 // columns and not padded rows.  R = 512 with 64 rows: O^T takes 256 columns of tensor
 // memory, S^T two buffers of 64.
 //
-// Bound by HBM up to 64 rows a sequence: 64 requests x 16 heads over U[1024, 16384] take
-// 112 us (644 MB; 6.5 TB/s, 96 % of the copy rate, while all CTAs have tiles; 5.7 with the
+// Bound by HBM up to 64 rows a sequence: 64 requests x 16 heads over U[1024, 16384] take 108 to
+// 111 us (644 MB; 6.5 TB/s, 96 % of the copy rate, while all CTAs have tiles; 5.9 with the
 // start, the last tiles and the join).  With 128 heads two CTAs read the same tiles (DRAM traffic
 // is that of one: 340 MB) and the chain of a tile bounds them: 64 requests over U[1024, 8192]
-// take 131 us (629 TFLOP/s), about 6500 clocks a tile, of which the 68 MMAs are 3700 (an MMA of
+// take 126 us (654 TFLOP/s), about 6500 clocks a tile, of which the 68 MMAs are 3700 (an MMA of
 // M = 128 costs 48 clocks whatever is below 64 columns: its A operand's way out of shared
 // memory), the softmax between them 1500, waits for the copies into the slots that the second
 // product leaves 900.  Shared memory (Q 72 KB, a tile 144 KB) holds no second tile to fill those.
+// A short call (2 contexts of up to 300 tokens, 9.6 us) is latency: of a CTA's 11000 clocks 3000 go
+// until the first copy (lengths, cuts; mostly code met for the first time), 3500 until the first
+// scores, 2500 in softmax and values, 1500 to 2000 until the rows are out; the join takes 2 us.
 //
 //  * The batch is a line of (sequence, row groups, tile) units, cut into equal parts for one
 //    CTA an SM (Walk): no tail of long contexts, at most two partial results a CTA, and a
@@ -716,7 +719,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
         }
         if (it.whole) {
           // Lanes hold a dim of 8 columns and write 8 dims of one: matrix k of the transposition is dims
-          // 8 x + 2 k + {0, 1} of every x.  (By shuffles the row group took 5700 clocks and not ...)
+          // 8 x + 2 k + {0, 1} of every x.  (A row group of 16 takes 2000 clocks; elements of 2 bytes 3000,
+          // by shuffles 2300, by 256 bytes a row, which four warps put together, 3200.)
           const int dim = ((lane & 6) << 2) + ((lane >> 3) << 1) + (lane & 1);
           const int col = c0 + (lane >> 2);
           __nv_bfloat16* o = p.out + ((size_t)it.q0 * p.H + it.r0 + col) * R + i * 128 + (warp & 3) * 32 + (lane & 3) * 8;

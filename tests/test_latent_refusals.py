@@ -101,6 +101,13 @@ def test_latent_decode(pa, kw, code):
     assert _decode(pa, **kw) == code
 
 
+def test_latent_decode_of_too_many_tiles(pa):
+    """Row groups and tiles are counted in 31 bits: (rows / 16 + sequences) x tiles of a table row."""
+    assert _decode(pa, mb=1 << 26, bs=16, rows=128, B=128) == -2
+    assert _decode(pa, mb=1 << 26, bs=16, rows=127, B=127, n=0) == -5      # (in range: the workspace is looked at next)
+    assert _decode(pa, mb=1 << 20, bs=16, rows=1 << 14, B=1 << 14) == -2
+
+
 def test_workspace_arithmetic(pa):
     need = pa.lib.pa_latent_decode_workspace_bytes
     # two slots a CTA of 152: 16 or 64 rows of 512 sums, their maxima and sums, 16 bytes a slot
