@@ -848,8 +848,12 @@ size_t pa_latent_decode_workspace_bytes(int total_queries, int num_seqs, int num
  *                   bf16 for their product with the values
  *
  * num_seqs <= 2048.  A NaN value makes NaN of its element in the rows that see
- * it, a NaN key of those rows whole; the rows before it are not touched by
- * either.  (Rows next to a value that is not finite are computed one by one.)
+ * it, an infinite one makes it infinite (NaN beside one of the other sign, or
+ * where its token's weight has underflowed: either), a NaN key makes NaN of those
+ * rows whole; the rows before it are not touched by any.  Rows next to a value
+ * that is not finite are computed a second time, with the (256 rows, head) pair
+ * or less that they belong to.  Sums of weights (1 at most) times values are
+ * fp32 and divided at the end: values whose sum passes 3.4e38 overflow.
  */
 int pa_latent_prefill(void* out, const void* query, const int32_t* query_start, int total_queries,
                       const void* kv, const void* key_rope, long long key_rope_stride, const int32_t* kv_start,

@@ -20,8 +20,13 @@
 //  * K chunks and V halves share one ring of 16 KB slots, in the order in which they are needed.
 //  * P is handed over by halves; the second half and the next scores go out in one turn.
 //  * The softmax reference moves only when a maximum exceeds it by 2^8.
-//  * Values that are not finite are not looked for: an output row that is not, though its weights
-//    are, is computed again by itself (0 * NaN in a key that the row does not see).
+//  * Values that are not finite are not looked for, though one reaches the rows of a tile that do not see
+//    it, as 0 * NaN.  An item with a row that is not finite while its weights are is noted, and
+//    done once more when the CTA's line is through: a warp of its own then takes such values out of
+//    the key tiles that some row does not see whole, and the rows that see them get them back as
+//    they are written.  That costs an item's time again, whatever the values are, and nobody waits
+//    for it (rows done by themselves, key by key and among the items, held the other warps' waits up
+//    for seconds in a long context).
 //  * Every wait is bounded (2 s); a timeout sets PA_DEV_TIMEOUT, and the roles wind down.
 #include "pa_mma.cuh"
 #include "pa_tc.cuh"
@@ -31,7 +36,7 @@ namespace {
 
 __device__ unsigned g_status_latent;
 
-constexpr int kThreads = 384;                // warps 0-3 and 4-7: softmax of a tile each; 8 TMA, 9 and 10 MMA of a tile each
+constexpr int kThreads = 384;                // warps 0-3 and 4-7: softmax of a tile each; 8 TMA, 9 and 10 MMA of a tile each, 11 values
 constexpr int kRows = 128;                   // query rows of a tile
 constexpr int kKT = 128;                     // keys per tile
 constexpr uint32_t kChunk = 16384;           // 128 rows x 64 elements
@@ -52,19 +57,21 @@ static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "
 
 struct PrefillParams {
   __nv_bfloat16* out;
-  const __nv_bfloat16 *q, *kv, *key;         // for single rows; the tiles go by tensor maps
-  long long key_stride;
+  const __nv_bfloat16* kv;                   // for values that are not finite; the tiles go by tensor maps
   const int32_t *query_start, *kv_start;
   int B, H, Dk, P, Dv, rows, kv_rows;
   float qscale;
 };
 
+constexpr int kNoted = 1024;                 // rounds that are told apart where items are done again (others go along)
 struct Shared {
-  uint64_t empty[kSlots], full_k[4], full_v[4], q[2], q_empty[2], s[2], p[2][2], pv[2], o_free[2], drain[2], ml_full;
+  uint64_t empty[kSlots], full_k[4], full_v[4], raw_v[4], q[2], q_empty[2], s[2], p[2][2], pv[2], o_free[2], drain[2], ml_full;
   float ml[128][2];                          // SPLIT: maximum and sum of the second half's rows
   uint32_t tmem_base;
   int abort;
   int turn;                                  // 1 while one row tile's products go out
+  int redo;                                  // rounds up to the last one whose item is to be done again
+  uint32_t noted[kNoted / 32];               // those rounds, modulo kNoted
 };
 constexpr uint32_t kSmemBytes = kOffBar + (uint32_t)sizeof(Shared) + 1024u;
 static_assert(kSmemBytes <= 232448, "shared memory");
@@ -113,12 +120,19 @@ __device__ __forceinline__ int rows_of(const PrefillParams& p, int b) {
 struct Item {
   int h, q0, n, k0, L, first, past;          // head; rows; keys; the item's first row of the sequence's, its position
   int nt[2], most;                           // key tiles of each chain, of the item
+  // key tiles that all its rows see whole
+  __device__ __forceinline__ int whole() const { return max(0, past + 1) / kKT; }
 };
 template <bool SPLIT>
 struct Walk {
   static constexpr int kUnit = SPLIT ? kRows : 2 * kRows;      // rows of a unit
   int round, b, base;                        // next round; a sequence at or before its unit's, units before that
-  __device__ __forceinline__ bool next(const PrefillParams& p, int lane, Item& it) {
+  int last;                                  // the second time: rounds up to the last noted one
+  __device__ __forceinline__ bool next(const PrefillParams& p, const Shared* sh, int lane, Item& it) {
+    if (last > 0) {
+      while (round < last && !((sh->noted[(round / 32) & (kNoted / 32 - 1)] >> (round & 31)) & 1u)) ++round;
+      if (round >= last) return false;
+    }
     const int item = round * (int)gridDim.x + (int)((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     ++round;
     const int unit = item / p.H;
@@ -166,39 +180,31 @@ struct Walk {
   }
 };
 
-// One output row by a warp: query row `row` of head h over the first n keys from k0 on, a key a
-// lane for the scores, then elements a lane for the values.
-__device__ __noinline__ void plain_row(const PrefillParams& p, int row, int h, int k0, int n, int lane) {
-  const __nv_bfloat16* q = p.q + ((size_t)row * p.H + h) * (p.Dk + p.P);
-  auto score = [&](int t) -> float {
-    if (t >= n) return -INFINITY;
-    const __nv_bfloat16* k = p.kv + ((size_t)(k0 + t) * p.H + h) * (p.Dk + p.Dv);
-    const __nv_bfloat16* kr = p.key + (k0 + t) * p.key_stride;
-    float s = 0.f;
-    for (int d = 0; d < p.Dk; ++d) s = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), s);
-    for (int d = 0; d < p.P; ++d) s = fmaf(__bfloat162float(q[p.Dk + d]), __bfloat162float(kr[d]), s);
-    return s * p.qscale;
-  };
-  float m = -INFINITY;
-  for (int t = 0; t < n; t += 32) m = fmaxf(m, score(t + lane));
+// The values that are not finite, of the tokens after `past`, for a warp's rows from `row` on (at
+// position `pos`) of the sequence whose rows begin at q0 and whose keys begin at k0: added to what the
+// rows that see them hold (infinities of both signs make a NaN, as in the sum that they belong to).
+// 255 tokens and 32 rows at most.
+__device__ __noinline__ void put_back(const PrefillParams& p, int q0, int n, int k0, int h, int past, int row, int pos,
+                                      int lane) {
+  const int each = p.Dv / 32;                // a lane's elements, next to each other: 1, 2 or 4
+  const __nv_bfloat16* v = p.kv + ((size_t)k0 * p.H + h) * (p.Dk + p.Dv) + p.Dk + lane * each;
+  const size_t step = (size_t)p.H * (p.Dk + p.Dv);
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  int t = max(0, past + 1);
+  for (int r = 0; r < 32 && row + r < n; ++r) {
+#pragma unroll 4
+    for (; t <= pos + r; ++t) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int t = 0; t < n; t += 32) {
-    const float w = exp2f(score(t + lane) - m);
-    l += w;
-    for (int i = 0; i < min(32, n - t); ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      const __nv_bfloat16* v = p.kv + ((size_t)(k0 + t + i) * p.H + h) * (p.Dk + p.Dv) + p.Dk;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (e * 32 < p.Dv) o[e] = fmaf(wi, __bfloat162float(v[e * 32 + lane]), o[e]);
+      for (int e = 0; e < 4; ++e) {
+        const float x = e < each ? __bfloat162float(v[t * step + e]) : 0.f;
+        if (x - x != 0.f) sum[e] += x;       // (NaN, not 0, for what is not finite)
+      }
     }
-  }
+    __nv_bfloat16* o = p.out + ((size_t)(q0 + row + r) * p.H + h) * p.Dv + lane * each;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-  for (int e = 0; e * 32 < p.Dv; ++e)
-    p.out[((size_t)row * p.H + h) * p.Dv + e * 32 + lane] = __float2bfloat16_rn(l != 0.f ? o[e] / l : 0.f);
+    for (int e = 0; e < 4; ++e)
+      if (e < each && sum[e] != 0.f) o[e] = __float2bfloat16_rn(__bfloat162float(o[e]) + sum[e]);
+  }
 }
 
 // f0 O of a warp's 32 rows, and f1 of the next chain's if there are two, as bf16 (zeros if there is
@@ -298,12 +304,15 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sh->full_k[i], 1);
       mbar_init(&sh->full_v[i], 1);
+      mbar_init(&sh->raw_v[i], 1);
     }
     mbar_init(&sh->ml_full, 4);
     sh->abort = 0;
     sh->turn = 0;
+    sh->redo = 0;
     fence_mbar_init();
   }
+  if (threadIdx.x < kNoted / 32) sh->noted[threadIdx.x] = 0u;
   if (warp == 9) {
     tmem_alloc(&sh->tmem_base, 512);
     tmem_relinquish();
@@ -314,15 +323,26 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
   const uint32_t tmem = sh->tmem_base;
   const int ncd = (p.Dk + 63) / 64, ncv = (p.Dv + 63) / 64;    // chunks of the keys' own part, of the values
   const int per = ncd + 3;                   // slots of a key tile: ncd + 1 of K, 2 of V
-  Walk<SPLIT> walk{0, 0, 0};
+  Walk<SPLIT> walk{0, 0, 0, 0};
   Item it = {};
+  // When a role has walked the line: true where all of them walk it again, for the noted items.  (All
+  // twelve warps come here once, whatever has become of their waits.)
+  auto once_more = [&]() -> bool {
+    if (walk.last > 0) return false;
+    __syncwarp();
+    named_sync(1, kThreads);
+    const int redo = *static_cast<volatile int*>(&sh->redo);
+    if (redo == 0 || *abort_flag) return false;
+    walk = Walk<SPLIT>{0, 0, 0, redo};
+    return true;
+  };
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     // ------------------------------------------------------------ TMA producer
     if (warp == 8) {
       const uint64_t once = policy_evict_first(), keep = policy_evict_last();   // (K, V: other row tiles read them too)
-      int u = 0, k = 0, nq[2] = {0, 0};      // slots, key tiles, row tiles requested
+      int u = 0, k = 0, m = 0, nq[2] = {0, 0};  // slots, key tiles, those to be looked through, row tiles requested
       bool ok = true;
       auto load_q = [&](int x) {
         if (it.nt[x] == 0) return;
@@ -341,49 +361,91 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
         ++u;
         return smem + kOffRing + sl * kChunk;
       };
-      while (ok && walk.next(p, lane, it)) {
-        const int most = it.most;
-        if (lane == 0 && most > 0) {
-          load_q(0);
-          for (int j = 0; ok && j < most; ++j, ++k) {
-            const int row = it.k0 + j * kKT;
-            // Key tile k uses full_k[k & 3] and full_v[k & 3].  Each is armed once the first slot is
-            // free, and not before: the slot's last user, or one after it, has waited for what the
-            // barrier announced four tiles ago.
-            uint64_t* full = &sh->full_k[k & 3];
-            for (int c = 0; c <= ncd; ++c) {
-              unsigned char* dst = slot();
+      do {
+        while (ok && walk.next(p, sh, lane, it)) {
+          const int most = it.most, whole = walk.last > 0 ? it.whole() : most;
+          if (lane == 0 && most > 0) {
+            load_q(0);
+            for (int j = 0; ok && j < most; ++j, ++k) {
+              const int row = it.k0 + j * kKT;
+              // Key tile k uses full_k[k & 3] and full_v[k & 3].  Each is armed once the first slot is
+              // free, and not before: the slot's last user, or one after it, has waited for what the
+              // barrier announced four tiles ago (a tile takes 4 or 5 of the 8 slots, so that every slot
+              // of tile k - 4 has been free since).  Values to be looked through are announced to the
+              // warp that does so, which arrives on full_v in the copy's place.
+              uint64_t* full = &sh->full_k[k & 3];
+              for (int c = 0; c <= ncd; ++c) {
+                unsigned char* dst = slot();
+                if (!ok) break;
+                if (c == 0) mbar_arrive_expect_tx(full, (uint32_t)(ncd + 1) * kChunk);
+                if (c < ncd) tma_load_4d(dst, &mapK, full, c * 64, it.h, row, 0, keep);
+                else tma_load_4d(dst, &mapKr, full, 0, row, 0, 0, keep);
+              }
               if (!ok) break;
-              if (c == 0) mbar_arrive_expect_tx(full, (uint32_t)(ncd + 1) * kChunk);
-              if (c < ncd) tma_load_4d(dst, &mapK, full, c * 64, it.h, row, 0, keep);
-              else tma_load_4d(dst, &mapKr, full, 0, row, 0, 0, keep);
-            }
-            if (!ok) break;
-            if (!SPLIT && j == 0) load_q(1);
-            full = &sh->full_v[k & 3];
-            for (int v = 0; v < 2; ++v) {
-              unsigned char* dst = slot();
-              if (ok && v == 0) mbar_arrive_expect_tx(full, (uint32_t)ncv * kChunk);
-              for (int c = 0; ok && c < ncv; ++c)
-                tma_load_4d(dst + c * (kChunk / 2), &mapV, full, c * 64, it.h, row + v * 64, 0, keep);
+              if (!SPLIT && j == 0) load_q(1);
+              full = j < whole ? &sh->full_v[k & 3] : &sh->raw_v[m++ & 3];
+              for (int v = 0; v < 2; ++v) {
+                unsigned char* dst = slot();
+                if (ok && v == 0) mbar_arrive_expect_tx(full, (uint32_t)ncv * kChunk);
+                for (int c = 0; ok && c < ncv; ++c)
+                  tma_load_4d(dst + c * (kChunk / 2), &mapV, full, c * 64, it.h, row + v * 64, 0, keep);
+              }
             }
           }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      }
-      // no TMA write may land after the CTA has left
-      if (lane == 0 && ok) {
-        for (int x = 0; x < 2; ++x)
-          if (nq[x] > 0) mbar_wait(&sh->q[x], (uint32_t)(nq[x] - 1) & 1u);
-        for (int i = max(0, k - 4); i < k; ++i) {
-          mbar_wait(&sh->full_k[i & 3], (uint32_t)(i >> 2) & 1u);
-          mbar_wait(&sh->full_v[i & 3], (uint32_t)(i >> 2) & 1u);
+        // no TMA write may land after the CTA has left
+        if (lane == 0 && ok) {
+          for (int x = 0; x < 2; ++x)
+            if (nq[x] > 0) mbar_wait(&sh->q[x], (uint32_t)(nq[x] - 1) & 1u);
+          for (int i = max(0, k - 4); i < k; ++i) {
+            mbar_wait(&sh->full_k[i & 3], (uint32_t)(i >> 2) & 1u);
+            mbar_wait(&sh->full_v[i & 3], (uint32_t)(i >> 2) & 1u);
+          }
         }
-      }
-      // (given up: a millisecond for what is still on its way)
-      if (lane == 0 && !ok)
-        for (const unsigned long long t = globaltimer_ns(); globaltimer_ns() - t < 1000000ull;) {}
-      __syncwarp();
+        // (given up: a millisecond for what is still on its way)
+        if (lane == 0 && !ok)
+          for (const unsigned long long t = globaltimer_ns(); globaltimer_ns() - t < 1000000ull;) {}
+        __syncwarp();
+      } while (once_more());
+    }
+    // ------------------------------------------------------------ values that are not finite
+    // In items done again: zeros in their place, in the tokens that some row of the item does not see.
+    if (warp == 11) {
+      int k = 0, m = 0;                      // key tiles, those looked through
+      bool ok = true;
+      do {
+        while (ok && walk.next(p, sh, lane, it)) {
+          const int whole = walk.last > 0 ? it.whole() : it.most;
+          for (int j = whole; ok && j < it.most; ++j, ++m) {
+            ok = __all_sync(0xffffffffu, wait(&sh->raw_v[m & 3], (uint32_t)(m >> 2) & 1u, abort_flag));
+            if (!ok) break;
+            const int lo = it.past + 1 - j * kKT, hi = it.L - j * kKT;   // rows to look at: lo <= row < hi
+            for (int part = 0; part < 4; ++part) {                       // 64 rows x 64 elements, 4 rows at a time
+              const int v = part >> 1, c = part & 1;
+              if (c >= ncv) continue;
+              unsigned char* at = smem + kOffRing + (((k + j) * per + ncd + 1 + v) & (kSlots - 1)) * kChunk + c * (kChunk / 2) + lane * 16;
+#pragma unroll 4
+              for (int i = 0; i < 16; ++i) {
+                const int row = v * 64 + i * 4 + (lane >> 3);
+                if (row < lo || row >= hi) continue;
+                auto clean = [](uint32_t x) {
+                  if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+                  if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+                  return x;
+                };
+                uint4* y = reinterpret_cast<uint4*>(at + i * 512);
+                const uint4 x = *y;
+                *y = make_uint4(clean(x.x), clean(x.y), clean(x.z), clean(x.w));
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->full_v[(k + j) & 3]);
+          }
+          k += it.most;
+        }
+      } while (once_more());
     }
     // ------------------------------------------------------------ MMA issuers
     // A warp for each row tile x: P_x V of a key tile, then S_x of the next.  (One warp for both
@@ -424,72 +486,75 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
         }
         __syncwarp();
       };
-      bool more = walk.next(p, lane, it);
-      while (ok && more) {
-        const int n = __shfl_sync(0xffffffffu, it.nt[x], 0);
-        const int most = __shfl_sync(0xffffffffu, it.most, 0);
-        constexpr int kStep = SPLIT ? 2 : 1;
-        int kk = SPLIT ? k + x : k;          // the chain's key tile
-        if (n > 0 || (SPLIT && most > 0)) ok = ok && wait(&sh->q[qx], (uint32_t)nq & 1u, abort_flag);
-        if (n > 0) {
-          ok = ok && wait(&sh->full_k[kk & 3], (uint32_t)(kk >> 2) & 1u, abort_flag);
-          tc_fence_after();
-          scores(kk, n == 1);
-        } else if (SPLIT && most > 0 && lead && ok) {
-          mbar_arrive(&sh->q_empty[0]);      // (no key tile for this chain)
-        }
-        more = walk.next(p, lane, it);       // (while the softmax has work)
-        // the last output of the chain has been read
-        if (n > 0) ok = ok && wait(&sh->o_free[x], ((uint32_t)no & 1u) ^ 1u, abort_flag);
-        for (int j = 0; ok && j < n; ++j, kk += kStep) {
-          // O_x += P_x V, half a tile of keys at a time
-#pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            const int sl = (kk * per + ncd + 1 + v) & (kSlots - 1), kn = kk + kStep;
-            ok = ok && wait(&sh->p[x][v], (uint32_t)(np + j) & 1u, abort_flag);
-            if (v == 0) ok = ok && wait(&sh->full_v[kk & 3], (uint32_t)(kk >> 2) & 1u, abort_flag);
-            if (!SPLIT && v == 1 && j + 1 < n) ok = ok && wait(&sh->full_k[kn & 3], (uint32_t)(kn >> 2) & 1u, abort_flag);
-            if (!ok) break;
+      do {
+        bool more = walk.next(p, sh, lane, it);
+        while (ok && more) {
+          const int n = __shfl_sync(0xffffffffu, it.nt[x], 0);
+          const int most = __shfl_sync(0xffffffffu, it.most, 0);
+          constexpr int kStep = SPLIT ? 2 : 1;
+          int kk = SPLIT ? k + x : k;          // the chain's key tile
+          if (n > 0 || (SPLIT && most > 0)) ok = ok && wait(&sh->q[qx], (uint32_t)nq & 1u, abort_flag);
+          if (n > 0) {
+            ok = ok && wait(&sh->full_k[kk & 3], (uint32_t)(kk >> 2) & 1u, abort_flag);
             tc_fence_after();
-            if (v == 1 && lead) take_turn(&sh->turn);
-            if (lead) {
-              const uint64_t db = sdesc_at(dv, sl * kChunk);
+            scores(kk, n == 1);
+          } else if (SPLIT && most > 0 && lead && ok) {
+            mbar_arrive(&sh->q_empty[0]);      // (no key tile for this chain)
+          }
+          more = walk.next(p, sh, lane, it);   // (while the softmax has work)
+          // the last output of the chain has been read
+          if (n > 0) ok = ok && wait(&sh->o_free[x], ((uint32_t)no & 1u) ^ 1u, abort_flag);
+          for (int j = 0; ok && j < n; ++j, kk += kStep) {
+            // O_x += P_x V, half a tile of keys at a time
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                umma_bf16_ts(tO, tS + v * 32 + i * 8, sdesc_at(db, i * 2048), idO, j > 0 || v > 0 || i > 0 ? 1u : 0u);
-              umma_commit(&sh->empty[sl]);
-              if (v == 1) umma_commit(&sh->pv[x]);
+            for (int v = 0; v < 2; ++v) {
+              const int sl = (kk * per + ncd + 1 + v) & (kSlots - 1), kn = kk + kStep;
+              ok = ok && wait(&sh->p[x][v], (uint32_t)(np + j) & 1u, abort_flag);
+              if (v == 0) ok = ok && wait(&sh->full_v[kk & 3], (uint32_t)(kk >> 2) & 1u, abort_flag);
+              if (!SPLIT && v == 1 && j + 1 < n) ok = ok && wait(&sh->full_k[kn & 3], (uint32_t)(kn >> 2) & 1u, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              if (v == 1 && lead) take_turn(&sh->turn);
+              if (lead) {
+                const uint64_t db = sdesc_at(dv, sl * kChunk);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  umma_bf16_ts(tO, tS + v * 32 + i * 8, sdesc_at(db, i * 2048), idO, j > 0 || v > 0 || i > 0 ? 1u : 0u);
+                umma_commit(&sh->empty[sl]);
+                if (v == 1) umma_commit(&sh->pv[x]);
+              }
+              __syncwarp();
             }
-            __syncwarp();
-          }
-          if (SPLIT && j + 1 < n) {
-            // (the chain's next keys may need the place of the values that just went out)
-            const int kn = kk + kStep;
+            if (SPLIT && j + 1 < n) {
+              // (the chain's next keys may need the place of the values that just went out)
+              const int kn = kk + kStep;
+              if (lead) *static_cast<volatile int*>(&sh->turn) = 0;
+              ok = ok && wait(&sh->full_k[kn & 3], (uint32_t)(kn >> 2) & 1u, abort_flag);
+              tc_fence_after();
+              if (lead) take_turn(&sh->turn);
+            }
+            if (j + 1 < n) scores(kk + kStep, j + 2 == n);
             if (lead) *static_cast<volatile int*>(&sh->turn) = 0;
-            ok = ok && wait(&sh->full_k[kn & 3], (uint32_t)(kn >> 2) & 1u, abort_flag);
-            tc_fence_after();
-            if (lead) take_turn(&sh->turn);
           }
-          if (j + 1 < n) scores(kk + kStep, j + 2 == n);
-          if (lead) *static_cast<volatile int*>(&sh->turn) = 0;
-        }
-        if constexpr (!SPLIT) {
-          // key tiles that only the other row tile sees
-          for (int j = n; ok && j < most; ++j) {
-            ok = wait(&sh->full_k[(k + j) & 3], (uint32_t)((k + j) >> 2) & 1u, abort_flag) &&
-                 wait(&sh->full_v[(k + j) & 3], (uint32_t)((k + j) >> 2) & 1u, abort_flag);
-            if (lead && ok)
-              for (int c = 0; c < per; ++c) mbar_arrive(&sh->empty[((k + j) * per + c) & (kSlots - 1)]);
-            __syncwarp();
+          if constexpr (!SPLIT) {
+            // key tiles that only the other row tile sees
+            for (int j = n; ok && j < most; ++j) {
+              ok = wait(&sh->full_k[(k + j) & 3], (uint32_t)((k + j) >> 2) & 1u, abort_flag) &&
+                   wait(&sh->full_v[(k + j) & 3], (uint32_t)((k + j) >> 2) & 1u, abort_flag);
+              if (lead && ok)
+                for (int c = 0; c < per; ++c) mbar_arrive(&sh->empty[((k + j) * per + c) & (kSlots - 1)]);
+              __syncwarp();
+            }
           }
+          k += most;
+          nq += SPLIT ? most > 0 : n > 0;
+          no += n > 0;
+          np += n;
         }
-        k += most;
-        nq += SPLIT ? most > 0 : n > 0;
-        no += n > 0;
-        np += n;
-      }
-      if (lead) umma_commit(&sh->drain[x]);  // every MMA has completed before TMEM is freed
-      mbar_wait(&sh->drain[x], 0);
+        if (lead) umma_commit(&sh->drain[x]);  // every MMA has completed before TMEM is freed
+        mbar_wait(&sh->drain[x], walk.last > 0 ? 1u : 0u);
+        __syncwarp();
+      } while (once_more());
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -499,153 +564,158 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_con
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + x * 128 + lane_off, tO = tmem + kColO + x * 128 + lane_off;
     int kc = 0, np = 0, np1 = 0, joins = 0;  // key tiles, tiles of P (of the second chain's, items that have any) before this item
-    bool more = walk.next(p, lane, it);
-    while (more) {
-      const int row = it.first + (SPLIT ? 0 : x * kRows) + r;  // of the sequence
-      const int pos = it.past + (SPLIT ? 0 : x * kRows) + r;
-      const int mine = x == 0 ? it.nt[0] : it.nt[1], other = SPLIT && x == 0 ? it.nt[1] : 0;
-      float m_ref = -INFINITY, lsum = 0.f;
-      for (int j = 0; j < mine; ++j) {
-        wait(&sh->s[x], (uint32_t)(np + j) & 1u, abort_flag);
-        __syncwarp();
-        tc_fence_after();
-        uint32_t v[4][32];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(tS + i * 32, v[i]);
-        tmem_ld_wait();
-        const int jt = SPLIT ? 2 * j + x : j;                  // key tile of the item
-        const int seen = min(pos, it.L - 1) - jt * kKT;        // last key of the tile that the row sees
-        if (__any_sync(0xffffffffu, seen < kKT - 1)) {
-#pragma unroll
-          for (int c = 0; c < kKT; ++c)
-            if (c > seen) v[c >> 5][c & 31] = __float_as_uint(-INFINITY);
-        }
-        float mx8[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mx8[i] = __uint_as_float(v[0][i]);
-#pragma unroll
-        for (int c = 8; c < kKT; c += 2)
-          mx8[(c >> 1) & 7] = fmax3(mx8[(c >> 1) & 7], __uint_as_float(v[c >> 5][c & 31]), __uint_as_float(v[c >> 5][(c + 1) & 31]));
-        float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])) * p.qscale;
-        const bool need = mx > m_ref + kSlack;
-        const float alpha = need ? exp2f(m_ref - mx) : 1.f;    // (m_ref = -inf gives 0)
-        if (need) m_ref = mx;
-        if (j > 0 && __any_sync(0xffffffffu, need)) {
-          // O holds P V of the tile before
-          wait(&sh->pv[x], (uint32_t)(np + j - 1) & 1u, abort_flag);
+    do {
+      bool more = walk.next(p, sh, lane, it);
+      while (more) {
+        const int row = it.first + (SPLIT ? 0 : x * kRows) + r;  // of the sequence
+        const int pos = it.past + (SPLIT ? 0 : x * kRows) + r;
+        const int mine = x == 0 ? it.nt[0] : it.nt[1], other = SPLIT && x == 0 ? it.nt[1] : 0;
+        float m_ref = -INFINITY, lsum = 0.f;
+        for (int j = 0; j < mine; ++j) {
+          wait(&sh->s[x], (uint32_t)(np + j) & 1u, abort_flag);
           __syncwarp();
           tc_fence_after();
+          uint32_t v[4][32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(tS + i * 32, v[i]);
+          tmem_ld_wait();
+          const int jt = SPLIT ? 2 * j + x : j;                  // key tile of the item
+          const int seen = min(pos, it.L - 1) - jt * kKT;        // last key of the tile that the row sees
+          if (__any_sync(0xffffffffu, seen < kKT - 1)) {
+#pragma unroll
+            for (int c = 0; c < kKT; ++c)
+              if (c > seen) v[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+          }
+          float mx8[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mx8[i] = __uint_as_float(v[0][i]);
+#pragma unroll
+          for (int c = 8; c < kKT; c += 2)
+            mx8[(c >> 1) & 7] = fmax3(mx8[(c >> 1) & 7], __uint_as_float(v[c >> 5][c & 31]), __uint_as_float(v[c >> 5][(c + 1) & 31]));
+          float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])) * p.qscale;
+          const bool need = mx > m_ref + kSlack;
+          const float alpha = need ? exp2f(m_ref - mx) : 1.f;    // (m_ref = -inf gives 0)
+          if (need) m_ref = mx;
+          if (j > 0 && __any_sync(0xffffffffu, need)) {
+            // O holds P V of the tile before
+            wait(&sh->pv[x], (uint32_t)(np + j - 1) & 1u, abort_flag);
+            __syncwarp();
+            tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < p.Dv; c += 16) {
-            uint32_t w[16];
-            tmem_ld16(tO + c, w);
-            tmem_ld_wait();
+            for (int c = 0; c < p.Dv; c += 16) {
+              uint32_t w[16];
+              tmem_ld16(tO + c, w);
+              tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
-            tmem_st16(tO + c, w);
-          }
-          tmem_st_wait();
-        }
-        lsum *= alpha;
-        const float negm = m_ref == -INFINITY ? 0.f : -m_ref;
-        const uint64_t qs2 = f2pack(p.qscale, p.qscale), nm2 = f2pack(negm, negm);
-        uint64_t ls2[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ls2[i] = f2pack(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t pw[16];
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            float x0, x1;
-            f2unpack(ffma2(f2pack(__uint_as_float(v[i][2 * c]), __uint_as_float(v[i][2 * c + 1])), qs2, nm2), x0, x1);
-            const float p0 = ex2(x0), p1 = ex2(x1);
-            ls2[c & 3] = fadd2(ls2[c & 3], f2pack(p0, p1));
-            pw[c] = pack_bf16(p0, p1);
-          }
-          tmem_st16(tS + i * 16, pw);
-          if (i == 1 && (jt + 1) * kKT > it.L) {
-            // Rows behind the context may hold anything, and 0 * NaN would reach O: zeros, before
-            // any of P is handed over (by every chain that uses them: either's P V may come first).
-            const int u = (kc + jt) * per + ncd + 1 + (r >> 6);
-            wait(&sh->full_v[(kc + jt) & 3], (uint32_t)((kc + jt) >> 2) & 1u, abort_flag);
-            if (jt * kKT + r >= it.L) {
-              unsigned char* vrow = smem + kOffRing + (u & (kSlots - 1)) * kChunk + (r & 63) * 128;
-              for (int c = 0; c < ncv * 8; ++c)  // (each row in another order: the banks are all in use)
-                *reinterpret_cast<uint4*>(vrow + (c >> 3) * (kChunk / 2) + (((c + r) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-              fence_proxy_async_smem();
+              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+              tmem_st16(tO + c, w);
             }
-            __syncwarp();
-          }
-          if (i & 1) {
-            // half a tile of P: its product may begin
             tmem_st_wait();
-            tc_fence_before();
+          }
+          lsum *= alpha;
+          // (weights of 2^-8 where the reference is, so that none is above 1, and sums of large values stay finite)
+          const float negm = m_ref == -INFINITY ? 0.f : -m_ref - kSlack;
+          const uint64_t qs2 = f2pack(p.qscale, p.qscale), nm2 = f2pack(negm, negm);
+          uint64_t ls2[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ls2[i] = f2pack(0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t pw[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              float x0, x1;
+              f2unpack(ffma2(f2pack(__uint_as_float(v[i][2 * c]), __uint_as_float(v[i][2 * c + 1])), qs2, nm2), x0, x1);
+              const float p0 = ex2(x0), p1 = ex2(x1);
+              ls2[c & 3] = fadd2(ls2[c & 3], f2pack(p0, p1));
+              pw[c] = pack_bf16(p0, p1);
+            }
+            tmem_st16(tS + i * 16, pw);
+            if (i == 1 && (jt + 1) * kKT > it.L) {
+              // Rows behind the context may hold anything, and 0 * NaN would reach O: zeros, before
+              // any of P is handed over (by every chain that uses them: either's P V may come first).
+              const int u = (kc + jt) * per + ncd + 1 + (r >> 6);
+              wait(&sh->full_v[(kc + jt) & 3], (uint32_t)((kc + jt) >> 2) & 1u, abort_flag);
+              if (jt * kKT + r >= it.L) {
+                unsigned char* vrow = smem + kOffRing + (u & (kSlots - 1)) * kChunk + (r & 63) * 128;
+                for (int c = 0; c < ncv * 8; ++c)  // (each row in another order: the banks are all in use)
+                  *reinterpret_cast<uint4*>(vrow + (c >> 3) * (kChunk / 2) + (((c + r) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+              }
+              __syncwarp();
+            }
+            if (i & 1) {
+              // half a tile of P: its product may begin
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh->p[x][i >> 1]);
+            }
+          }
+          float ls[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f2unpack(ls2[i], ls[2 * i], ls[2 * i + 1]);
+          lsum += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
+        }
+
+        // ---- O / l as bf16 rows
+        const int q0 = it.q0, n = it.n, k0 = it.k0, h = it.h;
+        kc += it.most;
+        more = walk.next(p, sh, lane, it);     // (its loads run beside the last product)
+        if (SPLIT && x == 1) {
+          if (mine > 0) {
+            // (its last product waited for the item before to be read)
+            wait(&sh->pv[1], (uint32_t)(np + mine - 1) & 1u, abort_flag);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->p[x][i >> 1]);
+            sh->ml[r][0] = m_ref;
+            sh->ml[r][1] = lsum;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->ml_full);
+          }
+          np += mine;
+          continue;
+        }
+        if (mine > 0) {
+          wait(&sh->pv[x], (uint32_t)(np + mine - 1) & 1u, abort_flag);
+          __syncwarp();
+          tc_fence_after();
+        }
+        float f0 = 1.f, f1 = 0.f;              // of O_x, and of the other half's
+        if (other > 0) {
+          wait(&sh->ml_full, (uint32_t)joins & 1u, abort_flag);
+          wait(&sh->pv[1], (uint32_t)(np1 + other - 1) & 1u, abort_flag);
+          __syncwarp();
+          tc_fence_after();
+          const float m1 = sh->ml[r][0], l1 = sh->ml[r][1], m = fmaxf(m_ref, m1);
+          f0 = m_ref == -INFINITY ? 0.f : exp2f(m_ref - m);
+          f1 = m1 == -INFINITY ? 0.f : exp2f(m1 - m);
+          lsum = fmaf(lsum, f0, l1 * f1);
+          if (l1 != l1) lsum = l1;             // (a row of NaN scores has no maximum)
+          ++joins;
+        }
+        const float inv = lsum != 0.f ? 1.f / lsum : 0.f;
+        const uint32_t full = write_rows(p, tO, mine > 0, inv * f0, SPLIT && other > 0, inv * f1, q0, row, n, h, lane);
+        if (mine > 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sh->o_free[x]);
+            if (other > 0) mbar_arrive(&sh->o_free[1]);
           }
         }
-        float ls[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f2unpack(ls2[i], ls[2 * i], ls[2 * i + 1]);
-        lsum += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
-      }
-
-      // ---- O / l as bf16 rows
-      const int q0 = it.q0, n = it.n, k0 = it.k0, h = it.h;
-      kc += it.most;
-      more = walk.next(p, lane, it);         // (its loads run beside the last product)
-      if (SPLIT && x == 1) {
-        if (mine > 0) {
-          // (its last product waited for the item before to be read)
-          wait(&sh->pv[1], (uint32_t)(np + mine - 1) & 1u, abort_flag);
+        if (walk.last > 0) {
+          // (all of the warp's rows are written)
           __syncwarp();
-          sh->ml[r][0] = m_ref;
-          sh->ml[r][1] = lsum;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh->ml_full);
+          put_back(p, q0, n, k0, h, pos - r - (SPLIT ? 0 : x * kRows), row - lane, pos - lane, lane);
+        } else if (__builtin_expect((full & 0x80008000u) && lsum - lsum == 0.f && row < n, 0)) {
+          const int round = walk.round - 2;    // (the next item's has been looked up)
+          atomicOr(&sh->noted[(round / 32) & (kNoted / 32 - 1)], 1u << (round & 31));
+          atomicMax(&sh->redo, round + 1);
         }
         np += mine;
-        continue;
+        np1 += other;
       }
-      if (mine > 0) {
-        wait(&sh->pv[x], (uint32_t)(np + mine - 1) & 1u, abort_flag);
-        __syncwarp();
-        tc_fence_after();
-      }
-      float f0 = 1.f, f1 = 0.f;              // of O_x, and of the other half's
-      if (other > 0) {
-        wait(&sh->ml_full, (uint32_t)joins & 1u, abort_flag);
-        wait(&sh->pv[1], (uint32_t)(np1 + other - 1) & 1u, abort_flag);
-        __syncwarp();
-        tc_fence_after();
-        const float m1 = sh->ml[r][0], l1 = sh->ml[r][1], m = fmaxf(m_ref, m1);
-        f0 = m_ref == -INFINITY ? 0.f : exp2f(m_ref - m);
-        f1 = m1 == -INFINITY ? 0.f : exp2f(m1 - m);
-        lsum = fmaf(lsum, f0, l1 * f1);
-        if (l1 != l1) lsum = l1;             // (a row of NaN scores has no maximum)
-        ++joins;
-      }
-      const float inv = lsum != 0.f ? 1.f / lsum : 0.f;
-      const uint32_t full = write_rows(p, tO, mine > 0, inv * f0, SPLIT && other > 0, inv * f1, q0, row, n, h, lane);
-      if (mine > 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sh->o_free[x]);
-          if (other > 0) mbar_arrive(&sh->o_free[1]);
-        }
-      }
-      // A value that is not finite reaches every row of the tile, the ones that do not see it by
-      // 0 * NaN.  Rows with finite weights and an output that is not are done again by themselves.
-      const bool redo = (full & 0x80008000u) && lsum - lsum == 0.f && row < n;
-      for (uint32_t todo = __ballot_sync(0xffffffffu, redo); todo; todo &= todo - 1) {
-        const int who = __ffs(todo) - 1;
-        plain_row(p, q0 + __shfl_sync(0xffffffffu, row, who), h, k0, __shfl_sync(0xffffffffu, pos, who) + 1, lane);
-      }
-      np += mine;
-      np1 += other;
-    }
+    } while (once_more());
   }
   tc_fence_before();
   __syncthreads();
@@ -715,10 +785,7 @@ extern "C" int pa_latent_prefill(void* out, const void* query, const int32_t* qu
   if (!raise_smem_limit(kernel, dev)) return PA_ERR_CUDA;
   PrefillParams p = {};
   p.out = static_cast<__nv_bfloat16*>(out);
-  p.q = static_cast<const __nv_bfloat16*>(query);
   p.kv = static_cast<const __nv_bfloat16*>(kv);
-  p.key = static_cast<const __nv_bfloat16*>(key_rope);
-  p.key_stride = key_rope_stride;
   p.query_start = query_start;
   p.kv_start = kv_start;
   p.B = num_seqs;

@@ -1,0 +1,131 @@
+"""Latent attention on the GPU where values or scores are not finite, against the oracle: who sees them, what the others
+keep, and that neither the context's length nor the number of such values holds a call up."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from _helpers import f64
+from _latent import check, randn
+
+pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore:.*encountered in.*:RuntimeWarning")]
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def pa():
+    from paged_kv_cache_307_gb300 import build
+    build.build()
+    from paged_kv_cache_307_gb300 import _lib
+    assert torch.cuda.is_available()
+    _lib.last_error()
+    return _lib
+
+
+def _check(got, want, mass, size):
+    """What is not finite has to be the same, the rest within its bound."""
+    g = f64(got)
+    odd = ~np.isfinite(want)
+    assert np.array_equal(g[odd], want[odd], equal_nan=True), "%d of %d are not what they should be, first %s" % (
+        (~((g[odd] == want[odd]) | (np.isnan(g[odd]) & np.isnan(want[odd])))).sum(), odd.sum(), np.argwhere(odd)[0])
+    want = np.where(odd, np.nan, want)
+    check(torch.from_numpy(np.where(odd, np.nan, g)), want, mass, size)
+
+
+def _prefill(pa, q, start, kv, key, kv_start, scale):
+    Dv = kv.shape[2] - (q.shape[2] - key.shape[1])
+    out = torch.full((q.shape[0], q.shape[1], Dv), 7.0, dtype=q.dtype, device="cuda")
+    st, ks = (torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda") for x in (start, kv_start))
+    return pa.latent_prefill(out, q, st, kv, key, ks, scale)
+
+
+def _prefill_check(pa, *a):
+    q, start, kv, key, kv_start, scale = a
+    _check(_prefill(pa, *a), *oracle.latent_prefill(f64(q), start, f64(kv), f64(key), kv_start, scale))
+    assert pa.last_error() == 0
+
+
+# ------------------------------------------------------------------ expanded
+
+@pytest.mark.parametrize("Dk,P,Dv", [(32, 16, 32), (128, 64, 128), (64, 32, 64)])
+@pytest.mark.parametrize("H", [2, 160])                     # a row tile a CTA, and two
+def test_values_that_are_not_finite(pa, H, Dk, P, Dv):
+    """Infinities and NaN in tokens that no new row, some or all new rows see, several in one element."""
+    lens, new = [300, 60, 131], [290, 3, 131]
+    start, kv_start = np.concatenate([[0], np.cumsum(new)]), np.concatenate([[0], np.cumsum(lens)])
+    q, kv, key = randn(1, start[-1], H, Dk + P), randn(2, kv_start[-1], H, Dk + Dv), randn(3, kv_start[-1], P)
+    for t, d, x in ((0, 0, INF), (5, 1, NAN), (9, 2, -INF), (15, 3, INF), (137, 3, -INF), (137, 4, INF), (138, 5, -INF),
+                    (200, 4, INF), (255, 6, NAN), (256, 7, INF), (265, 8, -INF), (298, 9, INF), (299, 10, NAN),
+                    (300, 11, INF), (357, 12, -INF), (358, 13, NAN), (360, 14, INF), (488, 15, INF), (490, 16, NAN)):
+        kv[t, H // 2, Dk + d] = x
+    kv[[20, 280], 0, Dk + 20:] = INF
+    kv[400, 1] = NAN                                        # keys too: its rows from there on whole
+    _prefill_check(pa, q, start, kv, key, kv_start, (Dk + P) ** -0.5)
+
+
+@pytest.mark.parametrize("H", [3, 48])
+def test_many_short_sequences_with_values_that_are_not_finite(pa, H):
+    """More items a CTA than are under way at a time, every other one with such a value."""
+    lens = [(29 * i) % 150 + 1 for i in range(90)]
+    new = [max(1, L // (1 + i % 3)) for i, L in enumerate(lens)]
+    start, kv_start = np.concatenate([[0], np.cumsum(new)]), np.concatenate([[0], np.cumsum(lens)])
+    q, kv, key = randn(4, start[-1], H, 48), randn(5, kv_start[-1], H, 64), randn(6, kv_start[-1], 16)
+    rng = np.random.default_rng(0)
+    for b in range(0, 90, 2):
+        for _ in range(3):
+            kv[kv_start[b] + rng.integers(lens[b]), rng.integers(H), 32 + rng.integers(32)] = rng.choice([INF, -INF, NAN])
+    _prefill_check(pa, q, start, kv, key, kv_start, 0.15)
+
+
+def test_long_contexts_beside_values_that_are_not_finite(pa):
+    """A NaN among the newest of 100 000 tokens and an infinity in the first, other sequences and heads beside them:
+    nothing waits for rows that are done one by one."""
+    lens, new = [100000, 900, 40000], [260, 300, 5]
+    H, Dk, P, Dv = 4, 32, 16, 32
+    start, kv_start = np.concatenate([[0], np.cumsum(new)]), np.concatenate([[0], np.cumsum(lens)])
+    q, kv, key = randn(1, start[-1], H, Dk + P), randn(2, kv_start[-1], H, Dk + Dv), randn(3, kv_start[-1], P)
+    scale = 2.0 * (Dk + P) ** -0.5
+    out0 = _prefill(pa, q, start, kv, key, kv_start, scale)
+    kv[100000 - 30, :, Dk + 3] = NAN
+    kv[0, 1, Dk + 5] = INF
+    kv[100900, 2, Dk + 6] = INF
+    out = _prefill(pa, q, start, kv, key, kv_start, scale)
+    assert pa.last_error() == 0
+    want = out0.clone()
+    want[230:260, :, 3] = NAN
+    want[:260, 1, 5] = INF
+    want[560:, 2, 6] = INF
+    same = (out == want) | (torch.isnan(out) & torch.isnan(want))
+    assert same.all(), torch.argwhere(~same)[:5].tolist()
+    kv = randn(2, kv_start[-1], H, Dk + Dv)                  # some rows of the finite call against the oracle
+    for r in (0, 100, 229, 230, 259, 400, 560, 564):
+        b = int(np.searchsorted(start, r, "right")) - 1
+        n = int(lens[b] - (start[b + 1] - r) + 1)
+        k0 = int(kv_start[b])
+        _check(out0[r:r + 1], *oracle.latent_prefill(f64(q[r:r + 1]), [0, 1], f64(kv[k0:k0 + n]), f64(key[k0:k0 + n]), [0, n], scale))
+
+
+def test_every_value_of_a_head_not_finite(pa):
+    """One head all NaN, another all infinite: theirs alone."""
+    H = 160
+    start = kv_start = [0, 700, 760]
+    q, kv, key = randn(1, 760, H, 48), randn(2, 760, H, 64), randn(3, 760, 16)
+    out0 = _prefill(pa, q, start, kv, key, kv_start, 0.2)
+    kv[:, 3, 32:], kv[:700, 7, 32:] = NAN, -INF
+    out = _prefill(pa, q, start, kv, key, kv_start, 0.2)
+    want = out0.clone()
+    want[:, 3], want[:700, 7] = NAN, -INF
+    assert ((out == want) | (torch.isnan(out) & torch.isnan(want))).all() and pa.last_error() == 0
+
+
+@pytest.mark.parametrize("H", [2, 160])
+def test_sums_of_large_values(pa, H):
+    """Values up to 1e36 under weights that grow from tile to tile: their sums before the division stay finite."""
+    L = 300
+    q, kv, key = randn(1, L, H, 48), randn(2, L, H, 64), randn(3, L, 16, scale=0.0)
+    q[:, :, :48], kv[:, :, 32:] = 0, kv[:, :, 32:].sign() * 1e36
+    q[:, :, 47] = 1.0
+    key[128:, 15], key[256:, 15] = 5.0, 10.0                # scores of 0, 7.2 and 14.4 in powers of 2
+    _prefill_check(pa, q, [0, L], kv, key, [0, L], 1.0)
