@@ -271,7 +271,7 @@ template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_prefill_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapQr,
                       const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapKr,
-                      const __grid_constant__ CUtensorMap mapV, const PrefillParams p) {
+                      const __grid_constant__ CUtensorMap mapV, const __grid_constant__ PrefillParams p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
