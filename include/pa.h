@@ -801,7 +801,8 @@ int pa_latent_append(const void* latent, long long latent_stride, const void* ke
  * tokens) < 2^31 (PA_ERR_SHAPE).
  * Accumulation is fp32; the softmax weights are rounded to bf16 for their
  * product with the values.  A cached row that holds a NaN makes NaN of the rows
- * that see it, whole; the rows before it are not touched.
+ * that see it, whole, and one that holds an infinity likewise or, for a row whose
+ * score it makes -inf, of its elements; the rows before it are not touched.
  *
  * The batch's tokens are divided evenly among the SMs by the lengths on the
  * device, and what a cut divides is joined by a second kernel (outside stream

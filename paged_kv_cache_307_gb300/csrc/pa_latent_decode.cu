@@ -60,6 +60,7 @@ constexpr int kMaxSlots = 6;
 
 struct LatentParams {
   __nv_bfloat16* out;
+  const __nv_bfloat16* cache;                // for values that are not finite; the tiles go by the tensor map
   const int32_t* query_start;                // null: one row a sequence
   const int32_t* block_tables;
   const int32_t* context_lens;
@@ -84,6 +85,7 @@ struct Shared {
   int first_b;
   uint32_t tmem_base;
   int abort;
+  unsigned odd;                              // the row group that values were taken out for: its first unit's place + 1
 };
 
 // Shared memory: Q [NC chunks][NR rows][128 B], a ring of SLOTS pairs, the rotated keys' chunk
@@ -232,6 +234,30 @@ struct Walk {
   }
 };
 
+// NaN in the elements of the calling softmax thread (dims r of every 128, its columns) that see a value
+// which is not finite, among the part's tokens that some row of the group does not see: NR / H + 1 at
+// most.  The rows of the output, or the partial sums, have been written.
+template <int NR, int RC>
+__device__ __noinline__ void put_nans(const LatentParams& p, const Item it) {
+  constexpr int SUB = subs(NR), CW = NR / SUB, R = RC * 64, NP = RC / 2;
+  const int r = (int)threadIdx.x & 127, c0 = (int)(threadIdx.x >> 7) * CW;
+  const int past = it.L - it.n, cols = min(CW, it.rows - c0);
+  const int first = max(it.tile * kTile, past + it.r0 / p.H + 1), stop = min(it.end, (it.tile + it.nt) * kTile);
+  for (int i = 0; i < NP; ++i) {
+    long long seen = cols;                   // rows from here on
+    for (int t = first; t < stop; ++t) {
+      int block = __ldg(&p.block_tables[(size_t)it.b * p.max_blocks + t / p.bs]);
+      if ((unsigned)block >= (unsigned)p.num_blocks) block = 0;      // (as it was copied)
+      const float x = __bfloat162float(p.cache[((size_t)block * p.bs + t % p.bs) * (R + p.P) + i * 128 + r]);
+      if (x - x != 0.f) seen = min(seen, max(0ll, (long long)(t - past) * p.H - it.r0 - c0));
+    }
+    for (int c = (int)seen; c < cols; ++c) {
+      if (it.whole) p.out[((size_t)it.q0 * p.H + it.r0 + c0 + c) * R + i * 128 + r] = __float2bfloat16_rn(NAN);
+      else p.ws_o[((((size_t)it.slot * NP + i) * (NR / 4) + (c0 + c) / 4) * 128 + r) * 4 + (c & 3)] = NAN;
+    }
+  }
+}
+
 // Sum of every x[i] over the warp, N <= 32: x[0] is that of the column whose bits the lane's
 // upper bits spell.
 template <int N>
@@ -261,7 +287,7 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32]) { t
 template <int NR, int RC>
 __global__ void __launch_bounds__(threads(NR), 1)
 latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_constant__ CUtensorMap mapQ,
-                     const LatentParams p) {
+                     const __grid_constant__ LatentParams p) {
   using Lay = Layout<NR, RC>;
   constexpr int NC = Lay::NC, NP = Lay::NP, SLOTS = Lay::kSlots;
   constexpr bool kAlias = Lay::kAlias;
@@ -291,6 +317,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
     mbar_init(&sh->o_free, 4 * SUB);
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
+    sh->odd = 0;
     sh->first_b = p.B;
     fence_mbar_init();
     prefetch_tensormap(&mapC);
@@ -637,11 +664,13 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
           *reinterpret_cast<uint4*>(prow + ((((c0 + c) >> 3) ^ (r & 7)) << 4)) =
               make_uint4(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7]));
         }
-        if (t >= it.end || t > past) {
+        if (t >= it.end || hide > 0) {
           // A slot that no row sees may hold anything, and 0 * NaN would reach O: its values are
-          // zeroed.  Of a token that some rows see and others do not, what is not finite: the
-          // rows that see it have the NaN from their score.
+          // zeroed.  Of a token that some rows see and others do not, what is not finite: most
+          // rows that see it have a NaN from their score, and one whose score is -inf gets its NaN
+          // in those elements when they are written.
           const bool drop = t >= it.end;
+          bool odd = false;
 #pragma unroll 1
           for (int i = 0; i < NP; ++i) {
             unsigned char* at = smem + Lay::kOffRing + ((kt * NP + i) % SLOTS) * kPair + r * 128;
@@ -661,10 +690,13 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
                   if ((y & 0x7f800000u) == 0x7f800000u) y &= 0xffffu;
                   return y;
                 };
-                *piece(k) = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+                const uint4 w = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+                odd |= w.x != v.x || w.y != v.y || w.z != v.z || w.w != v.w;
+                *piece(k) = w;
               }
             }
           }
+          if (odd) *static_cast<volatile unsigned*>(&sh->odd) = it.unit + 1;
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -699,8 +731,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
           sh->f[c] = it.nt > 0 && sum != 0.f ? 1.f / sum : 0.f;
         } else {
           float* ml = p.ws_ml + ((size_t)it.slot * NR + c) * 2;
+          // (a part whose scores are all -inf has a sum of 0, marked by a maximum of -inf, and elements to be joined)
           ml[0] = it.nt > 0 && sum != 0.f ? -sh->neg_m[c] : -INFINITY;
-          ml[1] = it.nt > 0 ? sum : 0.f;
+          ml[1] = it.nt == 0 ? 0.f : sum != 0.f ? sum : 1.f;
         }
       }
       named_sync(1, kSoft);
@@ -753,6 +786,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->o_free);
+        if (*static_cast<volatile unsigned*>(&sh->odd) == it.unit + 1) put_nans<NR, RC>(p, it);
       }
       named_sync(1, kSoft);                    // f and red are free again
     }
@@ -803,7 +837,7 @@ __global__ void __launch_bounds__(256) latent_join_kernel(const LatentParams p) 
       const int mine = q0 + (lane >> 2);
       float2 y = make_float2(-INFINITY, 0.f);
       if (mine < parts) y = ml[slot_of(mine) * NR];
-      live = __ballot_sync(0xffffffffu, y.x != -INFINITY);
+      live = __ballot_sync(0xffffffffu, y.y != 0.f);
       w = y.x != -INFINITY ? exp2f(y.x - m) : 0.f;
       if (y.x != -INFINITY) l = fmaf(y.y, w, l);
     }
@@ -932,6 +966,7 @@ extern "C" int pa_latent_decode(void* out, const void* query, const int32_t* que
   char* ws = static_cast<char*>(workspace);
   LatentParams p = {};
   p.out = static_cast<__nv_bfloat16*>(out);
+  p.cache = static_cast<const __nv_bfloat16*>(cache);
   p.query_start = query_start;
   p.block_tables = block_tables;
   p.context_lens = context_lens;

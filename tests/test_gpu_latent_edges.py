@@ -7,7 +7,7 @@ import torch
 
 import oracle
 from _helpers import f64
-from _latent import check, randn
+from _latent import Cache, check, randn
 
 pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore:.*encountered in.*:RuntimeWarning")]
 
@@ -129,3 +129,38 @@ def test_sums_of_large_values(pa, H):
     q[:, :, 47] = 1.0
     key[128:, 15], key[256:, 15] = 5.0, 10.0                # scores of 0, 7.2 and 14.4 in powers of 2
     _prefill_check(pa, q, [0, L], kv, key, [0, L], 1.0)
+
+
+# ------------------------------------------------------------------ absorbed
+
+def _decode(pa, c, q, scale, start=None):
+    out = torch.full((*q.shape[:2], c.R), 7.0, dtype=q.dtype, device="cuda")
+    st = None if start is None else torch.tensor(np.asarray(start), dtype=torch.int32, device="cuda")
+    return pa.latent_decode(out, q, c.cache, c.table, c.lens, scale, query_start=st)
+
+
+def _put(c, b, t, d, x):
+    c.cache[int(c.table[b, t // c.bs]), t % c.bs, d] = x
+
+
+@pytest.mark.parametrize("R,P", [(256, 32), (512, 64)])
+@pytest.mark.parametrize("H,lens,new", [(8, [100, 60], [10, 2]), (40, [300, 129, 50], [4, 4, 1]), (128, [400, 140], [2, 3]),
+                                        (16, [128 * 23 + 2, 70], [3, 1]), (1, [700], [150]), (64, [128 * 5 + 1, 128 * 2 + 1], [1, 1])])
+def test_infinite_values_under_scores_of_minus_infinity(pa, R, P, H, lens, new):
+    """An infinity whose score is -inf: a weight of zero, and NaN in its element, for newest tokens (which some rows do
+    not see) as for older ones, and where it is all that a CTA has of a row."""
+    c = Cache(lens, R, P, 16, seed=H)
+    start = np.concatenate([[0], np.cumsum(new)])
+    q = randn(H, int(start[-1]), H, R + P)
+    scale = 2.0 * (R + P) ** -0.5
+    size = c.oracle(q, scale, start)[2]
+    for b, (L, n) in enumerate(zip(lens, new)):
+        _put(c, b, L - 1, 70, -INF)                       # for rows of a positive q: -inf, of a negative one: NaN whole
+        if n > 1:
+            _put(c, b, L - n // 2 - 1, 100, INF)
+    q[:, :, 70], q[:, :, 100] = q[:, :, 70].abs(), -q[:, :, 100].abs()
+    q[:, H // 2, 70] *= -1
+    want, mass, _ = c.oracle(q, scale, start)
+    assert np.isnan(want).any() and not np.isnan(want).all(2).all()
+    _check(_decode(pa, c, q, scale, None if max(new) == 1 else start), want, mass, size * 1.5)
+    assert pa.last_error() == 0
