@@ -306,7 +306,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
       mbar_init(&sh->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh->full_r[i], 1);
+      mbar_init(&sh->full_r[i], 3);          // the TMA warps, with copies to do or without
       mbar_init(&sh->empty_r[i], 1);
       mbar_init(&sh->s[i], 1);
     }
@@ -408,7 +408,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
       int blk = id_of(0);
       ok = __all_sync(0xffffffffu, wait(&sh->q_empty, (uint32_t)(kq & 1) ^ 1u, abort_flag));
       if (!ok) break;
-      if (w == 0 && lane == 0) mbar_arrive_expect_tx(&sh->q_full, (uint32_t)NC * NR * 128u);
+      if (w == 0 && lane == 0) mbar_arrive_expect_tx(&sh->q_full, (uint32_t)NC * NR * 128u);   // (every warp has a chunk)
       __syncwarp();
       if (copy < NC) tma_load_4d(smem + copy * NR * 128, &mapQ, &sh->q_full, copy * 64, it.q0 * p.H + it.r0, 0, 0, pol);
       ++kq;
@@ -436,7 +436,13 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
         const uint32_t use = kAlias ? (uint32_t)kr : (uint32_t)kr >> 1;
         ok = __all_sync(0xffffffffu, wait(&sh->empty_r[sr], (use & 1u) ^ 1u, abort_flag));
         if (!ok) break;
-        if (w == 0 && lane == 0) mbar_arrive_expect_tx(&sh->full_r[sr], (uint32_t)nb * box);
+        // All three arrive, once a tile: one without anything to copy would else be free to look at a
+        // slot a turn late, when its parity has come round.  (A tile's slots are not used up before
+        // its scores are done, and those wait for this.  An arrival for every pair took 2 %.)
+        if (lane == 0) {
+          if (w == 0) mbar_arrive_expect_tx(&sh->full_r[sr], (uint32_t)nb * box);
+          else mbar_arrive(&sh->full_r[sr]);
+        }
         __syncwarp();
         if (chunk == 0 && has)
           tma_load_4d(smem + Lay::kOffRope + sr * kChunk + mine * box, &mapC, &sh->full_r[sr], RC * 64, 0, blk, 0, pol);

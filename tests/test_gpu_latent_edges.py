@@ -164,3 +164,22 @@ def test_infinite_values_under_scores_of_minus_infinity(pa, R, P, H, lens, new):
     assert np.isnan(want).any() and not np.isnan(want).all(2).all()
     _check(_decode(pa, c, q, scale, None if max(new) == 1 else start), want, mass, size * 1.5)
     assert pa.last_error() == 0
+
+
+@pytest.mark.parametrize("H,R,bs", [(16, 512, 16), (64, 512, 16), (16, 256, 8), (40, 128, 32)])
+def test_last_tiles_of_one_block(pa, H, R, bs):
+    """Tiles in which not every copying warp has something to copy, dozens of them a CTA, one after the other and
+    between whole ones."""
+    B = 2500
+    lens = [1 + (7 * b) % bs + (128 if b % 3 == 0 else 0) for b in range(B)]
+    c = Cache([256], R, 32, bs)
+    q = randn(H, 1, H, R + 32)
+    scale = (R + 32) ** -0.5
+    want = {}
+    for L in set(lens):
+        one = Cache([1], R, 32, bs)
+        one.cache, one.table, one.lens = c.cache, c.table, torch.tensor([L], dtype=torch.int32, device="cuda")
+        want[L] = one.oracle(q, scale)
+    c.table, c.lens = c.table.repeat(B, 1), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    check(_decode(pa, c, q.repeat(B, 1, 1), scale), *(np.concatenate([want[L][i] for L in lens]) for i in range(3)))
+    assert pa.last_error() == 0
