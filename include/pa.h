@@ -803,6 +803,8 @@ int pa_latent_append(const void* latent, long long latent_stride, const void* ke
  * product with the values.  A cached row that holds a NaN makes NaN of the rows
  * that see it, whole, and one that holds an infinity likewise or, for a row whose
  * score it makes -inf, of its elements; the rows before it are not touched.
+ * Sums of weights (1 at most) times values are fp32 and divided at the end:
+ * values whose sum passes 3.4e38 overflow.
  *
  * The batch's tokens are divided evenly among the SMs by the lengths on the
  * device, and what a cut divides is joined by a second kernel (outside stream

@@ -31,8 +31,9 @@
 //  * A slot of the ring is the 128 latent elements of one M = 128 product of O^T: it is free
 //    again when that product is done, while the other products still run.
 //  * The MMA warp keeps its descriptors in uniform registers (99 clocks an MMA where 49 do).
-//  * The references of the softmax are common to the 128 threads of a column and move only when a
-//    score exceeds one by 2^8: a barrier with a vote a tile; then O^T is scaled in tensor memory.
+//  * The references of the softmax are common to the 128 threads of a column, 2^8 above the maximum that
+//    set them, and move only when a score exceeds one: a barrier with a vote a tile; then O^T is scaled
+//    in tensor memory.
 //  * P lies over the rotated keys' chunk, which the scores are done with, where a tile is large.
 //  * Every wait is bounded (2 s); a timeout sets PA_DEV_TIMEOUT, and the roles wind down.
 #include <stddef.h>
@@ -53,7 +54,7 @@ constexpr int threads(int nr) { return 128 * subs(nr) + 128; }
 constexpr uint32_t kChunk = 16384;           // 128 tokens x 64 elements
 constexpr uint32_t kPair = 2 * kChunk;       // 128 elements: one M = 128 product of O^T
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 8.f;                // log2 units a score may exceed its reference by
+constexpr float kSlack = 8.f;                // log2 units that a new reference is above its score
 constexpr float kUnset = 3e38f;              // minus a reference that is not there yet
 constexpr uint32_t kSmemMax = 232448;        // 227 KB
 constexpr int kMaxSlots = 6;
@@ -612,11 +613,12 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
           for (int i = 0; i < 4; ++i) top[i] = fmaxf(x[2 * i], x[2 * i + 1]);
 #pragma unroll
           for (int c = 8; c < CW; c += 2) top[(c >> 1) & 3] = fmax3(top[(c >> 1) & 3], x[c], x[c + 1]);
-          need = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kSlack;
+          need = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > 0.f;
         }
         need = vote<kSoft>(need);
         if (need) {
-          // new references: the tile's maxima where they are above
+          // new references: 2^8 above the tile's maxima, where those are above the references there are.
+          // (No weight is above 1 then, and sums of large values stay finite.)
           scores();
 #pragma unroll
           for (int c = 0; c < CW; ++c) {
@@ -628,7 +630,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap mapC, const __grid_cons
             const int c = (int)threadIdx.x;
             const float y = fmaxf(fmaxf(sh->red[0][c], sh->red[1][c]), fmaxf(sh->red[2][c], sh->red[3][c])) * p.qscale;
             const float old = j > 0 ? -sh->neg_m[c] : -INFINITY;
-            const float m = fmaxf(old, y);
+            const float m = y > old ? y + kSlack : old;
             sh->f[c] = old == -INFINITY ? 0.f : exp2f(old - m);
             // No reference yet (nothing seen, or scores of -inf alone): one that every finite score exceeds.
             sh->neg_m[c] = m == -INFINITY ? kUnset : -m;

@@ -183,3 +183,21 @@ def test_last_tiles_of_one_block(pa, H, R, bs):
     c.table, c.lens = c.table.repeat(B, 1), torch.tensor(lens, dtype=torch.int32, device="cuda")
     check(_decode(pa, c, q.repeat(B, 1, 1), scale), *(np.concatenate([want[L][i] for L in lens]) for i in range(3)))
     assert pa.last_error() == 0
+
+
+@pytest.mark.parametrize("H", [16, 64])
+def test_sums_of_large_latent_values(pa, H):
+    """Values of 1e36 under weights that grow from tile to tile: their sums before the division stay finite."""
+    c = Cache([500], 256, 32, 16)
+    ids, sign = c.table[0].long(), c.cache[c.table[0].long(), :, :256].float().nan_to_num().sign()
+    c.cache[ids, :, :256] = sign.to(c.cache.dtype) * 1e36
+    c.cache[ids, :, 256:] = 0.0
+    for j in range(1, 4):                                   # scores of 0, 7.2, 14.4 and 21.6 in powers of 2
+        c.cache[ids[8 * j:8 * j + 8], :, 287] = 5.0 * j
+    q = torch.zeros(1, H, 288, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 287] = 1.0
+    want = c.oracle(q, 1.0)
+    B = 160
+    c.table, c.lens = c.table.repeat(B, 1), c.lens.repeat(B)
+    check(_decode(pa, c, q.repeat(B, 1, 1), 1.0), *(x.repeat(B, 0) for x in want))
+    assert pa.last_error() == 0
