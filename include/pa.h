@@ -682,8 +682,9 @@ int pa_prefill_varlen(void* out, const void* query, const int32_t* query_start, 
  *
  * The frequencies come as a table of steps: steps[i] = round(2^64 f_i / 2 pi),
  * the fraction of a turn that one position makes, so that p * steps[i] modulo
- * 2^64 is the turn's fraction with no angle to reduce: exact to 2^-33 of a turn
- * for every int32 position.  pa_rope_steps fills a HOST table of rotary_dim / 2
+ * 2^64 is the turn's fraction with no angle to reduce: right to 2^-33 of a turn
+ * for every int32 position.  (The kernels take it as a float, off by 2^-25 of a
+ * turn at most.)  pa_rope_steps fills a HOST table of rotary_dim / 2
  * entries (to be copied to the device) and *amplitude:
  *
  *   PA_ROPE_PLAIN   f_i = base^(-2 i / rotary_dim), A = 1; the other arguments
