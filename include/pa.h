@@ -798,8 +798,10 @@ int pa_latent_append(const void* latent, long long latent_stride, const void* ke
  * A context length outside its table row is clamped and sets PA_DEV_BAD_LEN, a
  * block id outside the pool is read as block 0 and sets PA_DEV_BAD_BLOCK.  A
  * table row holds at most 2^30 tokens, total_queries * num_heads < 2^31, and
- * (total_queries * num_heads / 16 + num_seqs) * (a table row's tiles of 128
- * tokens) < 2^31 (PA_ERR_SHAPE).
+ * (total_queries * num_heads / G + num_seqs) * (a table row's tiles of 128
+ * tokens) < 2^31 (PA_ERR_SHAPE), where G is 16 up to 16 (query, head) rows a
+ * sequence, 32 up to 32, else 64 (total_queries / num_seqs, rounded up, times
+ * num_heads).
  * Accumulation is fp32; the softmax weights are rounded to bf16 for their
  * product with the values.  A cached row that holds a NaN makes NaN of the rows
  * that see it, whole, and one that holds an infinity likewise or, for a row whose

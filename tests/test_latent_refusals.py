@@ -108,6 +108,18 @@ def test_latent_decode_of_too_many_tiles(pa):
     assert _decode(pa, mb=1 << 20, bs=16, rows=1 << 14, B=1 << 14) == -2
 
 
+def test_latent_decode_of_too_many_tiles_for_wider_groups(pa):
+    """The same by groups of 32 and 64 rows: 2^14 and 2^15 tiles a table row, on each side of the limit (the
+    workspace is looked at next)."""
+    assert _decode(pa, mb=1 << 17, H=32, rows=1 << 16, B=1 << 16, n=0) == -2              # (2^16 + 2^16) x 2^14
+    assert _decode(pa, mb=1 << 17, H=32, rows=(1 << 16) - 1, B=(1 << 16) - 1, n=0) == -5
+    # 64 rows a sequence or more: rows x 128 heads / 64 and the sequences
+    assert _decode(pa, mb=1 << 18, H=128, rows=3 * 21846, start=FAKE, B=3, n=0) == -2     # 131079 groups
+    assert _decode(pa, mb=1 << 17, H=128, rows=65534, start=FAKE, B=3, n=0) == -5         # 131071 x 2^14
+    assert _decode(pa, mb=1 << 17, H=64, rows=65536, start=FAKE, B=65536, n=0) == -2      # 131072 x 2^14
+    assert _decode(pa, mb=1 << 17, H=64, rows=65535, start=FAKE, B=65535, n=0) == -5
+
+
 def test_workspace_arithmetic(pa):
     need = pa.lib.pa_latent_decode_workspace_bytes
     # two slots a CTA of 152: 16 or 64 rows of 512 sums, their maxima and sums, 16 bytes a slot
