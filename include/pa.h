@@ -807,7 +807,8 @@ int pa_latent_append(const void* latent, long long latent_stride, const void* ke
  * that see it, whole, and one that holds an infinity likewise or, for a row whose
  * score it makes -inf, of its elements; the rows before it are not touched.
  * Sums of weights (1 at most) times values are fp32 and divided at the end:
- * values whose sum passes 3.4e38 overflow.
+ * values whose sum passes 3.4e38 overflow.  A score of -inf is a weight of zero,
+ * and a row of such scores alone is zeros, as in the other attention calls.
  *
  * The batch's tokens are divided evenly among the SMs by the lengths on the
  * device, and what a cut divides is joined by a second kernel (outside stream
@@ -858,8 +859,8 @@ size_t pa_latent_decode_workspace_bytes(int total_queries, int num_seqs, int num
  * where its token's weight has underflowed: either), a NaN key makes NaN of those
  * rows whole; the rows before it are not touched by any.  Rows next to a value
  * that is not finite are computed a second time, with the (256 rows, head) pair
- * or less that they belong to.  Sums of weights (1 at most) times values are
- * fp32 and divided at the end: values whose sum passes 3.4e38 overflow.
+ * or less that they belong to.  Scores of -inf and sums of large values as for
+ * pa_latent_decode.
  */
 int pa_latent_prefill(void* out, const void* query, const int32_t* query_start, int total_queries,
                       const void* kv, const void* key_rope, long long key_rope_stride, const int32_t* kv_start,

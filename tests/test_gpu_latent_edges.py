@@ -201,3 +201,23 @@ def test_sums_of_large_latent_values(pa, H):
     c.table, c.lens = c.table.repeat(B, 1), c.lens.repeat(B)
     check(_decode(pa, c, q.repeat(B, 1, 1), 1.0), *(x.repeat(B, 0) for x in want))
     assert pa.last_error() == 0
+
+
+@pytest.mark.parametrize("L", [100, 3000])
+def test_rows_of_no_weight_at_all(pa, L):
+    """Every score -inf: zeros, whole or cut among CTAs, and nothing of it in other rows."""
+    c = Cache([L, 50], 256, 32, 16)
+    q = randn(1, 2, 16, 288)
+    q[:, :, 281] = 1.0
+    want, mass, size = c.oracle(q, 0.1)
+    c.cache[c.table[0, :-(-L // 16)].long(), :, 281] = -INF
+    want[0], mass[0] = 0, 0
+    check(_decode(pa, c, q, 0.1), want, mass, size)
+    q, kv, key = randn(1, 210, 2, 192), randn(2, 210, 2, 256), randn(3, 210, 64)
+    q[:, :, 191] = 1.0
+    st = [0, 150, 210]
+    want, mass, size = oracle.latent_prefill(f64(q), st, f64(kv), f64(key), st, 0.07)
+    key[:150, 63] = -INF
+    want[:150], mass[:150] = 0, 0
+    check(_prefill(pa, q, st, kv, key, st, 0.07), want, mass, size)
+    assert pa.last_error() == 0
