@@ -221,3 +221,17 @@ def test_rows_of_no_weight_at_all(pa, L):
     want[:150], mass[:150] = 0, 0
     check(_prefill(pa, q, st, kv, key, st, 0.07), want, mass, size)
     assert pa.last_error() == 0
+
+
+@pytest.mark.parametrize("B", [385, 700, 1500])
+@pytest.mark.parametrize("H,new", [(16, False), (3, False), (64, False), (40, True), (128, True)])
+def test_more_sequences_than_threads(pa, B, H, new):
+    """Several sequences a thread where the batch is cut: empty contexts and sequences without rows among them, cuts at
+    any of them."""
+    lens = [0 if b % 7 == 3 else (37 * b) % 300 + 1 for b in range(B)]
+    rows = [(0, 2, 1, 3, 0)[b % 5] if new else 1 for b in range(B)]
+    c = Cache(lens, 128, 16, 16, seed=B)
+    start = np.concatenate([[0], np.cumsum(rows)])
+    q = randn(H, int(start[-1]), H, 144)
+    check(_decode(pa, c, q, 0.15, start if new else None), *c.oracle(q, 0.15, start))
+    assert pa.last_error() == 0
