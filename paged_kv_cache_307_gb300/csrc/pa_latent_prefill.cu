@@ -51,6 +51,7 @@ constexpr uint32_t kColO = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;                // log2 units a score may exceed its reference by
 constexpr int kMaxSeqs = 2048;
+constexpr int kMostItems = 0x7fff0000;       // (and a round of every CTA more fits 31 bits)
 // Registers: 384 x 168 at launch, then 2 x 128 x 208 for the softmax and 128 x 88 for the rest.
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
@@ -135,6 +136,7 @@ struct Walk {
     }
     const int item = round * (int)gridDim.x + (int)((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     ++round;
+    if (item >= kMostItems) return false;    // (starts that go back and forth may name more than the host allows)
     const int unit = item / p.H;
     it.h = item - unit * p.H;
     for (; b < p.B; b += 32) {
@@ -145,7 +147,7 @@ struct Walk {
         const int y = __shfl_up_sync(0xffffffffu, incl, off);
         if (lane >= off) incl += y;
       }
-      const uint32_t beyond = __ballot_sync(0xffffffffu, base + incl > unit);
+      const uint32_t beyond = __ballot_sync(0xffffffffu, (unsigned)base + (unsigned)incl > (unsigned)unit);
       if (beyond) {
         const int at = __ffs(beyond) - 1;
         base += __shfl_sync(0xffffffffu, incl - k, at);
@@ -745,7 +747,7 @@ extern "C" int pa_latent_prefill(void* out, const void* query, const int32_t* qu
   // units of 256 rows at most, and of 128
   const long long units2 = (long long)total_queries / (2 * kRows) + num_seqs;
   const long long units1 = (long long)total_queries / kRows + num_seqs;
-  if (units1 * num_heads > 0x7fff0000ll) return PA_ERR_SHAPE;
+  if (units1 * num_heads > kMostItems) return PA_ERR_SHAPE;
   if (num_seqs == 0 || total_queries == 0) return PA_OK;
   if (!out || !query || !query_start || !kv_start || (total_kv && (!kv || !key_rope))) return PA_ERR_NULL;
   if (!aligned16(out) || !aligned16(query) || !aligned16(kv) || !aligned16(key_rope) || key_rope_stride % 8)
