@@ -11,8 +11,8 @@
 // memory, S^T two buffers of 64.
 //
 // Bound by HBM up to 64 rows a sequence: 64 requests x 16 heads over U[1024, 16384] take 108 to
-// 111 us (644 MB; 6.5 TB/s, 96 % of the copy rate, while all CTAs have tiles; 5.9 with the
-// start, the last tiles and the join).  With 128 heads two CTAs read the same tiles (DRAM traffic
+// 112 us in a replayed graph (644 MB; 6.5 TB/s, 96 % of the copy rate, while all CTAs have tiles; 5.8
+// with the start, the last tiles and the join), 116 through the call with inputs that change.  With 128 heads two CTAs read the same tiles (DRAM traffic
 // is that of one: 340 MB) and the chain of a tile bounds them: 64 requests over U[1024, 8192]
 // take 126 us (654 TFLOP/s), about 6500 clocks a tile, of which the 68 MMAs are 3700 (an MMA of
 // M = 128 costs 48 clocks whatever is below 64 columns: its A operand's way out of shared
@@ -34,7 +34,9 @@
 //  * The references of the softmax are common to the 128 threads of a column, 2^8 above the maximum that
 //    set them, and move only when a score exceeds one: a barrier with a vote a tile; then O^T is scaled
 //    in tensor memory.
-//  * P lies over the rotated keys' chunk, which the scores are done with, where a tile is large.
+//  * P lies over the rotated keys' chunk, which the scores are done with, where a tile is large.  It is
+//    bf16, as the cached rows are that it meets (both operands have one type), 2^-9 of a weight on
+//    average beside the output's own 2^-9; the sum that divides keeps the weights in 32 bits.
 //  * Every wait is bounded (2 s); a timeout sets PA_DEV_TIMEOUT, and the roles wind down.
 #include <stddef.h>
 

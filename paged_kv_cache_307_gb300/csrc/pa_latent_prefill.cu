@@ -9,7 +9,8 @@
 // O_0, O_1: all 512 columns.  The products of one chain run while the other's softmax does.
 //
 // Bound by the chain of a tile and the tensor pipe: 4 prompts of 4096 tokens x 32 heads of 128 + 64
-// take 465 to 475 us (1450 TFLOP/s, 76 % of the burst GEMM rate; tensor pipe 66 % active).  A step
+// take 465 to 475 us in a replayed graph (1460 TFLOP/s, 76 % of the burst GEMM rate; tensor pipe 66 %
+// active) and 505 through the call with inputs that change (1360 TFLOP/s, 71 %).  A step
 // of both chains takes 3600 clocks, of which the 40 MMAs are 2600 (65 each at N = 128: operands of
 // 8 KB for a score's, at 128 bytes a clock), a chain's softmax 1500 and its products' way through
 // the pipe, with the waits around them, 1900.  What was tried and lost: 2^x by a polynomial for some
@@ -18,7 +19,10 @@
 //
 //  * One CTA an SM walks the items, so the next one's Q and K arrive during the last tiles.
 //  * K chunks and V halves share one ring of 16 KB slots, in the order in which they are needed.
-//  * P is handed over by halves; the second half and the next scores go out in one turn.
+//  * P is handed over by halves; the second half and the next scores go out in one turn.  It is bf16, as
+//    the values are that it meets (both operands have one type): 2^-9 of a weight on average, beside
+//    the output's own 2^-9; the sum that divides keeps the weights in 32 bits.  The call's error against
+//    64 bits is 0.0020 to 0.0022 of the output's size, 0.0017 of it the output's rounding.
 //  * The softmax reference moves only when a maximum exceeds it by 2^8.
 //  * Values that are not finite are not looked for, though one reaches the rows of a tile that do not see
 //    it, as 0 * NaN.  An item with a row that is not finite while its weights are is noted, and
