@@ -845,8 +845,9 @@ size_t pa_latent_decode_workspace_bytes(int total_queries, int num_seqs, int num
  *   key_rope        [total_kv, rope_dim], rows key_rope_stride elements apart
  *                   (a multiple of 16 bytes)
  *   query_start, kv_start  [num_seqs + 1] int32, non-decreasing from 0 to
- *                   total_queries / total_kv.  A bad pair sets PA_DEV_BAD_LEN,
- *                   and that sequence writes nothing.  Rows at negative
+ *                   total_queries / total_kv.  A bad pair, or a context of
+ *                   more than 2^26 tokens, sets PA_DEV_BAD_LEN, and that
+ *                   sequence writes nothing.  Rows at negative
  *                   positions (more rows than context) are zeros; rows of no
  *                   sequence are left as they were.
  *   key_dim, value_dim  32, 64 or 128; rope_dim 16, 32, 48 or 64

@@ -55,6 +55,8 @@ constexpr uint32_t kColO = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.f;                // log2 units a score may exceed its reference by
 constexpr int kMaxSeqs = 2048;
+// A chain without keys in an item waits for the other's (some 2 us for 128 keys): 1.3 s at most.
+constexpr int kMaxContext = 1 << 26;
 constexpr int kMostItems = 0x7fff0000;       // (and a round of every CTA more fits 31 bits)
 // Registers: 384 x 168 at launch, then 2 x 128 x 208 for the softmax and 128 x 88 for the rest.
 constexpr int kLaunchRegs = 168, kSoftmaxRegs = 208, kOtherRegs = 88;
@@ -111,7 +113,7 @@ __device__ __forceinline__ void take_turn(int* turn) {
 __device__ __forceinline__ int rows_of(const PrefillParams& p, int b) {
   const int a = __ldg(&p.query_start[b]), e = __ldg(&p.query_start[b + 1]);
   const int u = __ldg(&p.kv_start[b]), v = __ldg(&p.kv_start[b + 1]);
-  return a >= 0 && e >= a && e <= p.rows && u >= 0 && v >= u && v <= p.kv_rows ? e - a : -1;
+  return a >= 0 && e >= a && e <= p.rows && u >= 0 && v >= u && v <= p.kv_rows && v - u <= kMaxContext ? e - a : -1;
 }
 
 // Two chains of softmax and products run side by side in a CTA.  They are two row tiles over the

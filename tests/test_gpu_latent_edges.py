@@ -131,6 +131,30 @@ def test_sums_of_large_values(pa, H):
     _prefill_check(pa, q, [0, L], kv, key, [0, L], 1.0)
 
 
+def test_more_rounds_than_are_told_apart(pa):
+    """More than 1024 items a CTA, some of them with a value that is not finite, which the first row of two does not
+    see."""
+    B, H = 1300, 128
+    start = np.arange(B + 1) * 2
+    q, kv, key = randn(1, 2 * B, H, 48), randn(2, 2 * B, H, 64), randn(3, 2 * B, 16)
+    want = _prefill(pa, q, start, kv, key, start, 0.2)
+    rng = np.random.default_rng(1)
+    for b, h, d in zip(rng.integers(0, B, 60).tolist(), rng.integers(0, H, 60).tolist(), rng.integers(0, 32, 60).tolist()):
+        kv[2 * b + 1, h, 32 + d] = want[2 * b + 1, h, d] = INF
+    assert torch.equal(_prefill(pa, q, start, kv, key, start, 0.2), want) and pa.last_error() == 0
+
+
+def test_contexts_longer_than_the_limit(pa):
+    """A context of more than 2^26 tokens writes nothing and is not walked; the one beside it is as ever."""
+    L = (1 << 26) + 1
+    kv, key = torch.empty(L + 40, 1, 64, dtype=torch.bfloat16, device="cuda"), torch.empty(L + 40, 16, dtype=torch.bfloat16, device="cuda")
+    kv[L:], key[L:] = randn(1, 40, 1, 64), randn(2, 40, 16)
+    q = randn(3, 10, 1, 48)
+    out = _prefill(pa, q, [0, 4, 10], kv, key, [0, L, L + 40], 0.2)
+    assert pa.last_error() == pa.DEV_BAD_LEN and (out[:4] == 7.0).all()
+    _check(out[4:], *oracle.latent_prefill(f64(q[4:]), [0, 6], f64(kv[L:]), f64(key[L:]), [0, 40], 0.2))
+
+
 # ------------------------------------------------------------------ absorbed
 
 def _decode(pa, c, q, scale, start=None):
