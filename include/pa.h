@@ -708,8 +708,9 @@ int pa_rope_steps(uint64_t* steps, float* amplitude, int rotary_dim, double base
  * tensors (strides in elements, the innermost 1; a view into a fused
  * projection's output will do).  An output may be its input (same pointer and
  * strides: the elements past rotary_dim are then not touched) and must not
- * overlap it otherwise, nor itself, nor the other side.  A part of a head other than its first
- * elements is rotated through a pointer to it, with head_dim = rotary_dim.
+ * overlap it otherwise, nor itself, nor the other side.  A part of a head other
+ * than its first elements is rotated through a pointer to it, with head_dim =
+ * rotary_dim.
  *
  *   positions    [num_tokens] int32, any value
  *   num_heads, num_kv_heads  0 to 2^20: 0 leaves that side out
